@@ -26,49 +26,49 @@ _DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 def listed():
     return [
         # a few decoded tokens of a vision-language model: pure latency
-        {"name": "rope, 7 tokens", "op": "rope", "T": 7, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128, "axes": "16/24/24",
+        {"name": "rope 7 tokens", "op": "rope", "T": 7, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128, "axes": "16/24/24",
          "weave": False, "adjacent": False, "fused": False, "inverse": False, "dtype": "bf16", "far": 4096},
         # a packed training batch, queries and keys read out of the fused projection's output
-        {"name": "rope, packed batch, fused qkv", "op": "rope", "T": 14632, "Hq": 16, "Hkv": 16, "D": 128, "rot": 128,
+        {"name": "rope packed fused qkv", "op": "rope", "T": 14632, "Hq": 16, "Hkv": 16, "D": 128, "rot": 128,
          "axes": "24/20/20", "weave": True, "adjacent": False, "fused": True, "inverse": False, "dtype": "bf16",
          "far": 16384},
         # the gradient of a long video's queries and keys
-        {"name": "rope backward, 131072 tokens", "op": "rope", "T": 131072, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128,
+        {"name": "rope backward 131072 tokens", "op": "rope", "T": 131072, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128,
          "axes": "16/24/24", "weave": False, "adjacent": False, "fused": False, "inverse": True, "dtype": "bf16",
          "far": 1000000},
         # an image encoder: two axes, half of the head rotated, adjacent pairs, fp32, an odd number of rows
-        {"name": "rope, fp32, half the head", "op": "rope", "T": 9001, "Hq": 16, "Hkv": 4, "D": 64, "rot": 32,
+        {"name": "rope fp32 half the head", "op": "rope", "T": 9001, "Hq": 16, "Hkv": 4, "D": 64, "rot": 32,
          "axes": "8/8", "weave": False, "adjacent": True, "fused": False, "inverse": False, "dtype": "fp32",
          "far": 512},
         # two short sequences, capped scores: pure latency
-        {"name": "score, tiny, capped", "op": "score", "train": False, "seqs": 2, "lo": 64, "hi": 128, "more": 0,
+        {"name": "score tiny capped", "op": "score", "train": False, "seqs": 2, "lo": 64, "hi": 128, "more": 0,
          "pad": 0, "cp": 2, "Hq": 2, "Hkv": 2, "D": 64, "causal": 1, "cap": 50.0, "bias": False, "docs": 0,
          "prefix": 0, "mix": 1},
         # a packed batch of ordinary lengths, capped scores
-        {"name": "score, packed batch, capped", "op": "score", "train": False, "seqs": 8, "lo": 256, "hi": 4096,
+        {"name": "score packed capped", "op": "score", "train": False, "seqs": 8, "lo": 256, "hi": 4096,
          "more": 0, "pad": 0, "cp": 4, "Hq": 16, "Hkv": 16, "D": 128, "causal": 1, "cap": 50.0, "bias": False,
          "docs": 0, "prefix": 0, "mix": 2},
         # padded sequences, shared key heads, bias by distance, a training step
-        {"name": "score train, padded, distance bias", "op": "score", "train": True, "seqs": 12, "lo": 128,
+        {"name": "score train padded bias", "op": "score", "train": True, "seqs": 12, "lo": 128,
          "hi": 1600, "more": 0, "pad": 64, "cp": 4, "Hq": 32, "Hkv": 8, "D": 128, "causal": 1, "cap": 0.0,
          "bias": True, "docs": 0, "prefix": 0, "mix": 3},
         # one long sequence, capped scores, a training step: the tensor cores' case
-        {"name": "score train, 32768 tokens, capped", "op": "score", "train": True, "seqs": 1, "lo": 32768,
+        {"name": "score train 32768 capped", "op": "score", "train": True, "seqs": 1, "lo": 32768,
          "hi": 32768, "more": 0, "pad": 0, "cp": 4, "Hq": 4, "Hkv": 1, "D": 128, "causal": 1, "cap": 30.0,
          "bias": False, "docs": 0, "prefix": 0, "mix": 4},
         # documents packed into one long sequence that is split over the ranks as a whole, a prefix seen by all of
         # its document, bias by distance and a cap: everything at once, a training step
-        {"name": "score train, documents", "op": "score", "train": True, "seqs": 1, "lo": 16384, "hi": 16384,
+        {"name": "score train documents", "op": "score", "train": True, "seqs": 1, "lo": 16384, "hi": 16384,
          "more": 0, "pad": 0, "cp": 8, "Hq": 8, "Hkv": 2, "D": 64, "causal": 1, "cap": 50.0, "bias": True,
          "docs": 2000, "prefix": 700, "mix": 5},
         # the residual of a small model's short batch: pure latency
-        {"name": "dropout, 192 x 128", "op": "dropout", "T": 192, "C": 128, "p": 0.1, "residual": True, "ids": False,
+        {"name": "dropout 192 x 128", "op": "dropout", "T": 192, "C": 128, "p": 0.1, "residual": True, "ids": False,
          "dtype": "bf16"},
         # a rank's rows of a packed batch: the mask goes by the rows' global numbers
-        {"name": "dropout, 41888 x 4096, rows of a rank", "op": "dropout", "T": 41888, "C": 4096, "p": 0.1,
+        {"name": "dropout 41888 x 4096 rank", "op": "dropout", "T": 41888, "C": 4096, "p": 0.1,
          "residual": True, "ids": True, "dtype": "bf16"},
         # the gradient, in fp32, with an odd number of columns (rows that start off every alignment)
-        {"name": "dropout backward, fp32, 9001 x 1111", "op": "dropout", "T": 9001, "C": 1111, "p": 0.25,
+        {"name": "dropout backward fp32", "op": "dropout", "T": 9001, "C": 1111, "p": 0.25,
          "residual": False, "ids": False, "dtype": "fp32"},
     ]
 
