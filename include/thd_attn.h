@@ -91,11 +91,17 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_KERNEL_TAIL_ZERO 7
 #define THD_KERNEL_PARTITION 8
 #define THD_KERNEL_A2A 9
+#define THD_KERNEL_ROPE 10
+#define THD_KERNEL_DROPOUT 11
 
 /* mask modes (the `causal` argument of the attention entry points) */
 #define THD_CAUSAL_NONE 0
 #define THD_CAUSAL_TOP_LEFT 1
 #define THD_CAUSAL_BOTTOM_RIGHT 2
+
+/* element types of the row-wise operators */
+#define THD_DTYPE_BF16 0
+#define THD_DTYPE_FP32 1
 
 /* thd_cp_a2a directions */
 #define THD_A2A_TO_GROUPS 0 /* shards -> per-member head groups (the all-to-all in front of attention) */
@@ -393,6 +399,67 @@ THD_API int thd_attn_bwd_a2a(const void* q, const void* k, const void* v, const 
                              const int32_t* cu_seqlens_padded, int B, int64_t T, int Hq, int Hkv, int D, int causal,
                              float softmax_scale, int cp_size, int a2a_size, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, thd_stream_t stream);
+
+/*
+ * ---- operators on the rows around attention: rotary positions, dropout ----
+ * They act on every one of the T rows they are given (a rank's shard, the
+ * global buffer, or a part of either) and need no cu_seqlens, no workspace
+ * and no device status: what can be wrong is seen on the host.
+ */
+
+/*
+ * thd_rope -- rotary positions with several axes (for example time, height
+ * and width) on queries and keys, one launch.  With f_i = inv_freq[i] and
+ * a_i = axis_of[i] for i < rot_dim / 2, per row t and head the pair i,
+ *     elements (i, i + rot_dim / 2)   (adjacent = 0)
+ *     elements (2 i, 2 i + 1)         (adjacent = 1),
+ * is turned by angle = positions[a_i][t] * f_i:
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * Elements past rot_dim are copied.  inverse = 1 turns by -angle: the
+ * gradient of the inputs from the gradient of the outputs.  Angles are exact
+ * to 2^-24 turns at any 32-bit position; products and sums are fp32, rounded
+ * once.
+ *   q_in, q_out: rows of [Hq, D]; k_in, k_out: rows of [Hkv, D] (NULL with
+ *     Hkv = 0: queries alone).  `..._stride`: elements between rows, at least
+ *     H * D (larger for a slice of a fused projection's output, as input or
+ *     as output).  In place (out == in) needs equal strides; otherwise inputs
+ *     and outputs must not overlap.  Aligned to the element size; 16-byte
+ *     aligned rows with D a multiple of 8 and rot_dim of 16 (8 if adjacent)
+ *     take 16-byte accesses.
+ *   T rows, 0 <= T < 2^31; 1 <= D <= 1024; rot_dim even, 2 <= rot_dim <=
+ *     min(D, 256).
+ *   positions: device int32 [n_axes][T], any values; n_axes 1..16.
+ *   inv_freq: HOST double [rot_dim / 2], finite; axis_of: HOST uint8
+ *     [rot_dim / 2], each < n_axes.  Both are read before the call returns.
+ *   dtype: THD_DTYPE_BF16 or THD_DTYPE_FP32 (inputs and outputs alike).
+ */
+THD_API int thd_rope(const void* q_in, const void* k_in, void* q_out, void* k_out, int64_t q_in_stride,
+                     int64_t k_in_stride, int64_t q_out_stride, int64_t k_out_stride, int64_t T, int Hq, int Hkv,
+                     int D, int rot_dim, const int32_t* positions, int n_axes, const double* inv_freq,
+                     const uint8_t* axis_of, int adjacent, int inverse, int dtype, thd_stream_t stream);
+
+/*
+ * thd_dropout_add -- out = residual + keep(row, column) * x / (1 - p) on
+ * [T, C] rows, the mask drawn from a counter-based generator and never
+ * stored.  The gradient with respect to x is the same call on the output's
+ * gradient, without a residual (that of the residual is the output's).
+ *   Mask: Philox 4x32-10, key = rng[0], counter = (column / 8, id, rng[1]),
+ *     16 bits an element (column 8 g + 2 w + h takes half h of word w); kept
+ *     when they are >= round(65536 p), and scaled by 65536 / (65536 -
+ *     round(65536 p)).  id is row_ids[row] when given, else the row's index:
+ *     with a rank's token map as row_ids (thd_cp_partition), a shard draws
+ *     what the unsplit buffer draws.
+ *   x, out: [T, C], residual: [T, C] or NULL; out may be x or residual, else
+ *     they must not overlap.  Aligned to the element size; 16-byte aligned
+ *     tensors with C a multiple of 8 take 16-byte accesses.
+ *   0 <= T < 2^31, 0 <= C < 2^31; 0 <= p, round(65536 p) < 65536.
+ *   rng: DEVICE uint64 [2] = {seed, offset}, 8-byte aligned, read by the
+ *     kernel: a captured graph draws a new mask when its owner changes them
+ *     between replays.
+ *   A dropped element gives the residual (or 0) whatever x holds.
+ */
+THD_API int thd_dropout_add(const void* x, const void* residual, void* out, int64_t T, int64_t C,
+                            const int32_t* row_ids, double p, const uint64_t* rng, int dtype, thd_stream_t stream);
 
 /*
  * Profiling hook (not needed for normal use): while enabled for `kernel_id`

@@ -11,6 +11,8 @@
 
 #include "a2a.cuh"
 #include "common.cuh"
+#include "dropout.cuh"
+#include "rope.cuh"
 
 namespace thd {
 
@@ -651,6 +653,82 @@ int thd_attn_bwd_a2a(const void* q, const void* k, const void* v, const void* o,
   out.job[2] = a2a_job(dv, w + L.buf[7], Hkv, 1);
   out.njobs = 3;
   return cuda_status(launch_a2a(out, false, st));
+}
+
+// One operand of thd_rope: pointers aligned to the element, rows wide enough,
+// in place only with equal strides.
+static bool rope_operand_ok(const void* in, const void* out, int64_t in_stride, int64_t out_stride, int H, int D,
+                            int esize) {
+  if (H == 0) return true;
+  if (!in || !out || !aligned(in, esize) || !aligned(out, esize)) return false;
+  if (in_stride < (int64_t)H * D || out_stride < (int64_t)H * D) return false;
+  return in != out || in_stride == out_stride;
+}
+
+int thd_rope(const void* q_in, const void* k_in, void* q_out, void* k_out, int64_t q_in_stride, int64_t k_in_stride,
+             int64_t q_out_stride, int64_t k_out_stride, int64_t T, int Hq, int Hkv, int D, int rot_dim,
+             const int32_t* positions, int n_axes, const double* inv_freq, const uint8_t* axis_of, int adjacent,
+             int inverse, int dtype, thd_stream_t stream) {
+  if (dtype != THD_DTYPE_BF16 && dtype != THD_DTYPE_FP32) return THD_ERR_UNSUPPORTED;
+  if (T < 0 || T >= ((int64_t)1 << 31) || Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv < 1 || Hq > (1 << 20) ||
+      Hkv > (1 << 20))
+    return THD_ERR_INVALID_ARG;
+  if (D < 1 || D > 1024) return THD_ERR_UNSUPPORTED;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > D) return THD_ERR_INVALID_ARG;
+  if (rot_dim / 2 > kRopeMaxPairs || n_axes > kRopeMaxAxes) return THD_ERR_UNSUPPORTED;
+  if (n_axes < 1 || !inv_freq || !axis_of) return THD_ERR_INVALID_ARG;
+  if (T == 0) return THD_OK;
+  if (!positions || !aligned(positions, 4)) return THD_ERR_INVALID_ARG;
+  const int esize = dtype == THD_DTYPE_BF16 ? 2 : 4;
+  if (!rope_operand_ok(q_in, q_out, q_in_stride, q_out_stride, Hq, D, esize) ||
+      !rope_operand_ok(k_in, k_out, k_in_stride, k_out_stride, Hkv, D, esize))
+    return THD_ERR_INVALID_ARG;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    if (!std::isfinite(inv_freq[i]) || axis_of[i] >= n_axes) return THD_ERR_INVALID_ARG;
+    // turns per position: whole turns drop out at whole positions
+    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double frac = turns - std::floor(turns);              // in [0, 1]
+    p.turn[i] = (uint64_t)std::ldexp(frac, 63) << 1;            // 2^64 wraps to 0
+    p.axis[i] = axis_of[i];
+  }
+  p.x[0] = RopeTensor{q_in, q_out, q_in_stride, q_out_stride, Hq};
+  p.x[1] = RopeTensor{k_in, k_out, k_in_stride, k_out_stride, Hkv};
+  p.pos = positions;
+  p.T = T;
+  p.D = D;
+  p.rot = rot_dim;
+  p.n_axes = n_axes;
+  p.inverse = inverse != 0;
+  return cuda_status(launch_rope(p, dtype, adjacent != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int thd_dropout_add(const void* x, const void* residual, void* out, int64_t T, int64_t C, const int32_t* row_ids,
+                    double p, const uint64_t* rng, int dtype, thd_stream_t stream) {
+  if (dtype != THD_DTYPE_BF16 && dtype != THD_DTYPE_FP32) return THD_ERR_UNSUPPORTED;
+  const int esize = dtype == THD_DTYPE_BF16 ? 2 : 4;
+  if (!(p >= 0.0) || !(p < 1.0)) return THD_ERR_INVALID_ARG;
+  const double drop = std::nearbyint(65536.0 * p);
+  if (drop >= 65536.0) return THD_ERR_INVALID_ARG;
+  if (T < 0 || C < 0 || T >= ((int64_t)1 << 31) || C >= ((int64_t)1 << 31)) return THD_ERR_INVALID_ARG;
+  if (T == 0 || C == 0) return THD_OK;
+  if (!x || !out || !rng) return THD_ERR_INVALID_ARG;
+  if (!aligned(x, esize) || !aligned(out, esize) || !aligned(residual, esize) || !aligned(row_ids, 4) ||
+      !aligned(rng, 8))
+    return THD_ERR_INVALID_ARG;
+  DropoutParams d;
+  std::memset(&d, 0, sizeof(d));
+  d.x = x;
+  d.residual = residual;
+  d.out = out;
+  d.row_ids = row_ids;
+  d.rng = rng;
+  d.T = T;
+  d.C = C;
+  d.drop = (uint32_t)drop;
+  d.scale = (float)(65536.0 / (65536.0 - drop));
+  return cuda_status(launch_dropout(d, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int thd_profile_enable(int kernel_id, int max_records) {

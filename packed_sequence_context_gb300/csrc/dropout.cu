@@ -1,0 +1,209 @@
+// Dropout from a counter-based generator, plus the residual, on packed rows
+// (see thd_dropout_add in the header): out = residual + keep(row, column) *
+// x / (1 - p).  The mask is a function of (seed, offset, row number, column):
+// it is computed where it is used, forward and backward, and never stored, and
+// a rank's shard draws what the unsplit tensor draws for the same rows.
+//
+// Generator: Philox 4x32 with ten rounds (Salmon, Moraes, Dror and Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", SC 2011).  One call gives
+// eight columns of a row 16 bits each: counter (column / 8, row, offset),
+// key = seed; column 8 g + 2 w + h takes half h of word w.  Sixteen bits set
+// the drop probability in steps of 2^-16 (the scale goes by the rounded
+// probability, so the mean is exact) at half the generator's work of 32: a
+// call is about 90 instructions, and at 32 bits an element the bf16 backward
+// (4 bytes an element) would be bound by them instead of by HBM.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "dropout.cuh"
+
+namespace thd {
+
+constexpr int kDropThreads = 256;
+constexpr int kDropBatch = 4;  // groups of eight columns a thread has in flight
+
+// Bit e of the result: column 8 g + e of the row is kept.
+__device__ inline uint32_t keep_mask(uint32_t g, uint32_t row, uint64_t offset, uint64_t seed, uint32_t drop) {
+  uint32_t c0 = g, c1 = row, c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const uint32_t w[4] = {c0, c1, c2, c3};
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m |= ((w[k] & 0xffffu) >= drop ? 1u : 0u) << (2 * k);
+    m |= ((w[k] >> 16) >= drop ? 1u : 0u) << (2 * k + 1);
+  }
+  return m;
+}
+
+template <typename E>
+struct Vec8;  // eight elements in 16-byte pieces
+template <>
+struct Vec8<uint16_t> {
+  uint4 v;
+  __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+  __device__ void set(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// C a multiple of 8 and 16-byte aligned tensors: a thread moves groups of
+// eight columns with 16-byte accesses, kDropBatch of them in flight.
+template <typename E, bool kResidual>
+__global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const DropoutParams p) {
+  const uint64_t seed = p.rng[0], offset = p.rng[1];
+  const uint32_t G = (uint32_t)(p.C / 8);
+  const int64_t total = p.T * (int64_t)G;
+  const int64_t base = (int64_t)blockIdx.x * (kDropThreads * kDropBatch);
+  const int64_t row0 = base / G;
+  const uint32_t rem0 = (uint32_t)(base - row0 * G);
+  Vec8<E> x[kDropBatch], r[kDropBatch];
+  uint32_t keep[kDropBatch];
+#pragma unroll
+  for (int k = 0; k < kDropBatch; ++k) {
+    const uint32_t i = k * kDropThreads + threadIdx.x;
+    if (base + i < total) {
+      x[k].load(static_cast<const E*>(p.x) + 8 * (base + i));
+      if (kResidual) r[k].load(static_cast<const E*>(p.residual) + 8 * (base + i));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kDropBatch; ++k) {
+    const uint32_t i = k * kDropThreads + threadIdx.x;
+    if (base + i < total) {
+      const uint32_t at = rem0 + i, dr = at / G;
+      const int64_t row = row0 + dr;
+      const uint32_t id = p.row_ids ? (uint32_t)p.row_ids[row] : (uint32_t)row;
+      keep[k] = keep_mask(at - dr * G, id, offset, seed, p.drop);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kDropBatch; ++k) {
+    const uint32_t i = k * kDropThreads + threadIdx.x;
+    if (base + i < total) {
+      float f[8], g[8];
+      x[k].get(f);
+      if (kResidual) r[k].get(g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        f[e] = (keep[k] >> e) & 1u ? f[e] * p.scale : 0.f;
+        if (kResidual) f[e] += g[e];
+      }
+      x[k].set(f);
+      x[k].store(static_cast<E*>(p.out) + 8 * (base + i));
+    }
+  }
+}
+
+// Any C and alignment: a warp takes 256 columns of a row; each lane draws the
+// mask of one group of eight, and the elements move one to a lane (coalesced
+// whatever the row's alignment), their mask byte fetched from the lane that
+// drew it.
+__device__ inline float to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ inline float to_f32(float v) { return v; }
+__device__ inline void put(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+__device__ inline void put(float* p, float v) { *p = v; }
+
+template <typename E, bool kResidual>
+__global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const DropoutParams p) {
+  const uint64_t seed = p.rng[0], offset = p.rng[1];
+  const int lane = threadIdx.x & 31;
+  const int64_t blocks_per_row = (p.C + 255) / 256;
+  const int64_t w = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) >> 5;  // this warp's (row, 256 columns)
+  if (w >= p.T * blocks_per_row) return;  // the whole warp
+  const int64_t row = w / blocks_per_row, c0 = (w - row * blocks_per_row) * 256;
+  const int64_t at = row * p.C + c0;
+  const int n = (int)(p.C - c0 < 256 ? p.C - c0 : 256);
+  E x[8], r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (32 * k + lane < n) {
+      x[k] = static_cast<const E*>(p.x)[at + 32 * k + lane];
+      if (kResidual) r[k] = static_cast<const E*>(p.residual)[at + 32 * k + lane];
+    }
+  }
+  const uint32_t id = p.row_ids ? (uint32_t)p.row_ids[row] : (uint32_t)row;
+  const uint32_t mine = keep_mask((uint32_t)(c0 / 8) + lane, id, offset, seed, p.drop);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t m = __shfl_sync(0xffffffffu, mine, 4 * k + (lane >> 3));
+    if (32 * k + lane < n) {
+      float f = (m >> (lane & 7)) & 1u ? to_f32(x[k]) * p.scale : 0.f;
+      if (kResidual) f += to_f32(r[k]);
+      put(static_cast<E*>(p.out) + at + 32 * k + lane, f);
+    }
+  }
+}
+
+template <typename E, bool kResidual>
+static cudaError_t launch_dropout_t(const DropoutParams& p, cudaStream_t st) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out) |
+                      reinterpret_cast<uintptr_t>(p.residual);
+  const bool vec = p.C % 8 == 0 && (a & 15u) == 0;
+  const int64_t work = vec ? p.T * (p.C / 8) : p.T * ((p.C + 255) / 256) * 32;  // threads' worth
+  const int per_block = vec ? kDropThreads * kDropBatch : kDropThreads;
+  const int64_t grid = (work + per_block - 1) / per_block;
+  if (grid >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  prof_before(THD_KERNEL_DROPOUT, st);
+  if (vec)
+    dropout_vec_kernel<E, kResidual><<<(unsigned)grid, kDropThreads, 0, st>>>(p);
+  else
+    dropout_any_kernel<E, kResidual><<<(unsigned)grid, kDropThreads, 0, st>>>(p);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  prof_after(THD_KERNEL_DROPOUT, st);
+  return e;
+}
+
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, cudaStream_t st) {
+  if (p.T == 0 || p.C == 0) return cudaSuccess;
+  if (dtype == THD_DTYPE_BF16)
+    return p.residual ? launch_dropout_t<uint16_t, true>(p, st) : launch_dropout_t<uint16_t, false>(p, st);
+  return p.residual ? launch_dropout_t<float, true>(p, st) : launch_dropout_t<float, false>(p, st);
+}
+
+}  // namespace thd

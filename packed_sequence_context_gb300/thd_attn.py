@@ -43,6 +43,8 @@ THD_KERNEL_LSE_MERGE = 6
 THD_KERNEL_TAIL_ZERO = 7
 THD_KERNEL_PARTITION = 8
 THD_KERNEL_A2A = 9
+THD_KERNEL_ROPE = 10
+THD_KERNEL_DROPOUT = 11
 
 THD_FWD_KERNEL_SINGLE = 1
 THD_FWD_KERNEL_DUAL = 2
@@ -51,6 +53,9 @@ THD_CAUSAL_NONE = 0
 THD_CAUSAL_TOP_LEFT = 1
 THD_CAUSAL_BOTTOM_RIGHT = 2
 
+THD_DTYPE_BF16 = 0
+THD_DTYPE_FP32 = 1
+
 THD_A2A_TO_GROUPS = 0
 THD_A2A_TO_SHARDS = 1
 
@@ -58,6 +63,7 @@ _vp = ctypes.c_void_p
 _i32 = ctypes.c_int
 _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 _sz = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/thd_attn.h
@@ -85,6 +91,9 @@ SIGNATURES = {
                                 _i32, _vp, _sz, _vp, _vp]),
     "thd_attn_bwd_a2a": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32,
                                 _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "thd_rope": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
+                        _vp, _i32, _i32, _i32, _vp]),
+    "thd_dropout_add": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _f64, _vp, _i32, _vp]),
     "thd_profile_enable": (_i32, [_i32, _i32]),
     "thd_profile_read": (_i32, [_vp, _i32, _vp]),
     "thd_launch_count": (ctypes.c_uint64, []),
@@ -117,6 +126,13 @@ def _p(x):
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _h(a):
+    """Host address of a contiguous numpy array (or pass an int / None through)."""
+    if a is None or isinstance(a, int):
+        return a
+    return a.ctypes.data
 
 
 def _s(stream):
@@ -230,6 +246,17 @@ def thd_attn_bwd_a2a(q, k, v, o, lse, dout, dq, dk, dv, cu_seqlens, cu_seqlens_p
                                   cp_size, a2a_size, _p(workspace), workspace_bytes, _p(dev_status), _s(stream))
 
 
+def thd_rope(q_in, k_in, q_out, k_out, q_in_stride, k_in_stride, q_out_stride, k_out_stride, T, Hq, Hkv, D, rot_dim,
+             positions, n_axes, inv_freq, axis_of, adjacent, inverse, dtype, stream=None) -> int:
+    return lib().thd_rope(_p(q_in), _p(k_in), _p(q_out), _p(k_out), q_in_stride, k_in_stride, q_out_stride,
+                          k_out_stride, T, Hq, Hkv, D, rot_dim, _p(positions), n_axes, _h(inv_freq), _h(axis_of),
+                          adjacent, inverse, dtype, _s(stream))
+
+
+def thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dtype, stream=None) -> int:
+    return lib().thd_dropout_add(_p(x), _p(residual), _p(out), T, C, _p(row_ids), p, _p(rng), dtype, _s(stream))
+
+
 def thd_profile_enable(kernel_id: int, max_records: int) -> int:
     return lib().thd_profile_enable(kernel_id, max_records)
 
@@ -273,6 +300,29 @@ def check_status(dev_status) -> int:
     if code != 0:
         raise ThdError("device", code)
     return code
+
+
+def _need(where: str, ok: bool):
+    """Refuse a call whose tensors the library could not tell from right ones
+    (it sees pointers): wrong type, shape, device or layout."""
+    if not ok:
+        raise ThdError(where, THD_ERR_INVALID_ARG)
+
+
+def _dtype(where: str, t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return THD_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return THD_DTYPE_FP32
+    raise ThdError(where, THD_ERR_UNSUPPORTED)
+
+
+def _current(where: str, t):
+    """The tensor must be on the current CUDA device: that is where the
+    library launches."""
+    import torch
+    _need(where, t.is_cuda and t.device.index == torch.cuda.current_device())
 
 
 def _workspace(nbytes, device):
@@ -472,3 +522,74 @@ def attn_bwd_a2a(q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_padded, *, cp_siz
                                                 T, Hq, Hkv, D, int(causal), scale, cp_size, a2a_size, ws, ws.numel(),
                                                 st, stream))
     return dq, dk, dv, st
+
+
+def _rope_rows(t, H, D):
+    """Rows of [H, D] whose heads are contiguous: their stride in elements, or
+    None.  A dimension of size 1 may carry any stride."""
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        return None
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), H * D)
+
+
+def rope(q, k, positions, inv_freq, axis_of=None, *, adjacent=False, inverse=False, q_out=None, k_out=None,
+         stream=None):
+    """Rotary positions on q [T, Hq, D] and k [T, Hkv, D] (k may be None).
+    positions int32 [n_axes, T] (or [T]); inv_freq numpy float64
+    [rot_dim / 2] and axis_of numpy uint8 [rot_dim / 2] on the host (None: all
+    axis 0).  q and k may be slices of a fused projection (heads contiguous,
+    any row stride); outputs are new contiguous tensors unless given (q_out=q:
+    in place).  inverse=True: the gradients of the inputs.  Returns (q_out,
+    k_out)."""
+    import numpy as np
+    import torch
+    w = "thd_rope"
+    T, Hq, D = q.shape
+    _current(w, q)
+    dt = _dtype(w, q)
+    inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    axis = np.zeros(inv.size, np.uint8) if axis_of is None else np.ascontiguousarray(axis_of, dtype=np.uint8)
+    n_axes = positions.shape[0] if positions.dim() == 2 else 1
+    _need(w, inv.ndim == 1 and axis.shape == inv.shape and positions.dtype == torch.int32 and
+          positions.is_contiguous() and positions.shape[-1] == T and positions.device == q.device)
+    qo = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    Hkv, ko = 0, None
+    if k is not None:
+        _need(w, k.dim() == 3 and k.shape[0] == T and k.shape[2] == D)
+        Hkv = k.shape[1]
+        ko = torch.empty((T, Hkv, D), dtype=k.dtype, device=k.device) if k_out is None else k_out
+    strides = []
+    for t, H in ((q, Hq), (k, Hkv), (qo, Hq), (ko, Hkv)):
+        s = 0
+        if t is not None:
+            _need(w, t.shape == (T, H, D) and t.dtype == q.dtype and t.device == q.device)
+            s = _rope_rows(t, H, D)
+            _need(w, s is not None)
+        strides.append(s)
+    _check(w, thd_rope(q, k, qo, ko, *strides, T, Hq, Hkv, D, 2 * inv.size, positions, n_axes, inv, axis,
+                       int(adjacent), int(inverse), dt, stream))
+    return qo, ko
+
+
+def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None):
+    """residual + dropout(x) on contiguous rows [..., C] (the rows are the
+    flattened leading dimensions), the mask drawn from rng (device int64 or
+    uint64 [2]: seed, offset) and each row's number (row_ids int32 [rows], or
+    its index).  On the output's gradient without a residual: the gradient of
+    x.  out may be x or residual.  Returns out."""
+    import torch
+    w = "thd_dropout_add"
+    _current(w, x)
+    dt = _dtype(w, x)
+    C = x.shape[-1]
+    T = x.numel() // C if C else 0
+    o = torch.empty_like(x) if out is None else out
+    for t in (x, residual, o):
+        _need(w, t is None or (t.shape == x.shape and t.dtype == x.dtype and t.device == x.device and
+                               t.is_contiguous()))
+    _need(w, rng.device == x.device and rng.numel() == 2 and rng.is_contiguous() and
+          rng.dtype in (torch.int64, torch.uint64))
+    _need(w, row_ids is None or (row_ids.dtype == torch.int32 and row_ids.numel() == T and row_ids.is_contiguous()
+                                 and row_ids.device == x.device))
+    _check(w, thd_dropout_add(x, residual, o, T, C, row_ids, p, rng, dt, stream))
+    return o
