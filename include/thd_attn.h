@@ -80,6 +80,7 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_DEV_ERR_EXCEEDS_BUF 105    /* pad[B] larger than the buffer rows */
 #define THD_DEV_ERR_CAUSAL_LENGTHS 106 /* top-left causal with q and kv lengths differing */
 #define THD_DEV_ERR_CAPACITY 107       /* internal schedule capacity exceeded */
+#define THD_DEV_ERR_DOC_ORDER 108      /* document numbers decrease inside a sequence */
 
 /* Kernel identifiers for the profiling hook. */
 #define THD_KERNEL_PLAN 1
@@ -93,6 +94,7 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_KERNEL_A2A 9
 #define THD_KERNEL_ROPE 10
 #define THD_KERNEL_DROPOUT 11
+#define THD_KERNEL_DOCS 12
 
 /* mask modes (the `causal` argument of the attention entry points) */
 #define THD_CAUSAL_NONE 0
@@ -281,6 +283,68 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
                  const int32_t* cu_seqlens_kv_padded, int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D,
                  int causal, float softmax_scale, int cp_size, int pad_between_seqs, void* workspace,
                  size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream);
+
+/*
+ * thd_attn_score_fwd -- thd_attn_fwd with a score function and more masks:
+ *     x_ij = softmax_scale q_i . k_j
+ *     y_ij = softcap tanh(x_ij / softcap)            (softcap > 0; else x_ij)
+ *     y_ij -= dist_slopes[h] |i + koff - j|          (dist_slopes given)
+ *     O = softmax(y + mask) v,  lse = logsumexp(y + mask),
+ * with koff = L_kv - L_q under THD_CAUSAL_BOTTOM_RIGHT and 0 otherwise (the
+ * distance is between positions of the sequence).  Masks, all of which must
+ * let a pair through:
+ *   causal: as in thd_attn_fwd, except that with prefix_len the first
+ *     prefix_len[b] keys of sequence b are visible to all of its queries
+ *     (values below 0 count as 0, above L_kv as L_kv; without a causal mask
+ *     it changes nothing);
+ *   documents: query and key have the same number, doc_q[row] == doc_kv[row].
+ * A query that sees no key gets o = 0, lse = -inf (and zero gradients).
+ *   softcap: >= 0, finite; 0: no cap.
+ *   dist_slopes: device fp32 [Hq] or NULL, finite (constants: no gradient).
+ *   doc_q [T_q], doc_kv [T_kv]: device int32 document number of every row, or
+ *     both NULL.  They may be one array.  Inside a sequence the numbers of
+ *     its valid rows must not decrease (else THD_DEV_ERR_DOC_ORDER); rows
+ *     without a valid token are not looked at.
+ *   prefix_len: device int32 [B] or NULL.
+ * Key tiles that no query of a tile sees are skipped, whatever mask hides
+ * them.  With none of the four given the call is thd_attn_fwd.  Every row
+ * with a valid token must hold finite q, k, v: a masked key's score counts
+ * nothing, but its row of v is multiplied by 0.
+ * Other arguments as thd_attn_fwd; the workspace is larger:
+ * thd_score_workspace_size(.., has_docs = doc_q != NULL, 0).
+ * Launches: planner and forward; with documents two more (checks, extents).
+ */
+THD_API int thd_attn_score_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                               const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded, int B,
+                               int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int causal, float softmax_scale,
+                               int cp_size, int pad_between_seqs, float softcap, const float* dist_slopes,
+                               const int32_t* doc_q, const int32_t* doc_kv, const int32_t* prefix_len,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream);
+
+/*
+ * thd_attn_score_bwd -- gradients of thd_attn_score_fwd w.r.t. q, k, v; with
+ * P = exp(y - lse), dP = dO v^T, Delta = rowsum(dO * O):
+ *     dx = P (dP - Delta) (1 - tanh^2(x / softcap)).
+ * Arguments as thd_attn_bwd, with the modifications the forward was given;
+ * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible.
+ */
+THD_API int thd_attn_score_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                               const void* dout, void* dq, void* dk, void* dv, int64_t dq_rows, int64_t dkv_rows,
+                               const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                               const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded, int B,
+                               int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int causal, float softmax_scale,
+                               int cp_size, int pad_between_seqs, float softcap, const float* dist_slopes,
+                               const int32_t* doc_q, const int32_t* doc_kv, const int32_t* prefix_len,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream);
+
+/*
+ * Bytes of workspace thd_attn_score_fwd (for_bwd = 0) or thd_attn_score_bwd
+ * (for_bwd = 1) needs; has_docs: document numbers are given.  Returns 0 for
+ * invalid sizes.
+ */
+THD_API size_t thd_score_workspace_size(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp_size,
+                                        int has_docs, int for_bwd);
 
 /*
  * thd_lse_merge -- in place: (o_acc, lse_acc) <- merge((o_acc, lse_acc),

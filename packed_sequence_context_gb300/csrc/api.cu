@@ -170,10 +170,63 @@ static int locality_group(int Hkv, size_t bytes_per_kv_head, bool grouped) {
   return best;
 }
 
+// What the scored entry points add to the plain ones (see thd_attn_score_fwd).
+struct ScoreArgs {
+  float softcap;
+  const float* slopes;
+  const int32_t* doc_q;
+  const int32_t* doc_kv;
+  const int32_t* prefix;
+  bool any() const { return softcap > 0.f || slopes || doc_q || prefix; }
+  int mod() const { return kScored | (softcap > 0.f ? kModCap : 0) | (slopes ? kModDist : 0); }
+};
+
+constexpr double kLog2e = 1.4426950408889634;
+
+static int check_score(const ScoreArgs& a, float scale) {
+  if (!(a.softcap >= 0.f) || !std::isfinite(a.softcap)) return THD_ERR_INVALID_ARG;
+  // 2 log2(e) scale / softcap has to be a finite float
+  if (a.softcap > 0.f && !std::isfinite((float)(2.0 * kLog2e * scale / a.softcap))) return THD_ERR_INVALID_ARG;
+  if ((a.doc_q == nullptr) != (a.doc_kv == nullptr)) return THD_ERR_INVALID_ARG;
+  if (!aligned(a.slopes, 4) || !aligned(a.doc_q, 4) || !aligned(a.doc_kv, 4) || !aligned(a.prefix, 4))
+    return THD_ERR_INVALID_ARG;
+  return THD_OK;
+}
+
+static ScoreMods score_mods(const ScoreArgs& a, float scale, int causal, char* ws, const WsLayout& L, bool bwd) {
+  ScoreMods m;
+  std::memset(&m, 0, sizeof(m));
+  if (a.softcap > 0.f) {
+    m.cap_a = (float)(kLog2e * a.softcap);
+    m.cap_c = (float)(2.0 * kLog2e * scale / a.softcap);
+  }
+  m.slopes = a.slopes;
+  if (a.doc_q) {
+    m.rows_q = reinterpret_cast<const int2*>(ws + L.rows_q);
+    if (bwd) m.rows_kv = reinterpret_cast<const int2*>(ws + L.rows_kv);
+  }
+  m.prefix = causal == kCausalNone ? nullptr : a.prefix;  // without a causal mask every key is visible already
+  return m;
+}
+
+// With documents: a validating planner run, then each row's document extent
+// (the schedule, planned next, is made from them).
+static int plan_docs(const PlanParams& pp, const ScoreArgs& a, int64_t T_q, int64_t T_kv, char* ws, const WsLayout& L,
+                     bool bwd, cudaStream_t st) {
+  PlanParams check = pp;
+  check.mode = 0;
+  int rc = cuda_status(launch_plan(check, st));
+  if (rc) return rc;
+  return cuda_status(launch_docs(a.doc_q, a.doc_kv, pp.eff, pp.B, T_q, T_kv, reinterpret_cast<int2*>(ws + L.rows_q),
+                                 bwd ? reinterpret_cast<int2*>(ws + L.rows_kv) : nullptr, pp.doc_err, pp.dev_status,
+                                 st));
+}
+
 static int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
                       const int32_t* cu_kv, const int32_t* pad_q, const int32_t* pad_kv, int B, int64_t T_q,
                       int64_t T_kv, int Hq, int Hkv, int D, int causal, float scale, int cp, int pad_mode,
-                      int step, bool part_fp32, void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t st) {
+                      int step, bool part_fp32, const ScoreArgs* score, void* ws, size_t ws_bytes,
+                      int32_t* dev_status, cudaStream_t st) {
   int rc = check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp, pad_mode);
   if (rc) return rc;
   if (!q || !k || !v || !o || !lse || !cu_q || !cu_kv || !dev_status) return THD_ERR_INVALID_ARG;
@@ -182,7 +235,12 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   if (!(scale > 0.f) || !std::isfinite(scale) || causal < kCausalNone || causal > kCausalBottomRight)
     return THD_ERR_INVALID_ARG;
   if (step >= cp) return THD_ERR_INVALID_ARG;
-  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp, false);
+  if (score) {
+    rc = check_score(*score, scale);
+    if (rc) return rc;
+    if (!score->any()) score = nullptr;
+  }
+  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp, false, score != nullptr, score && score->doc_q);
   rc = check_ws(ws, ws_bytes, L.total);
   if (rc) return rc;
   char* w = static_cast<char*>(ws);
@@ -190,6 +248,19 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   if (step >= 0) {
     pp.step_lo = step;
     pp.step_hi = step + 1;
+  }
+  ScoreMods mods;
+  std::memset(&mods, 0, sizeof(mods));
+  if (score) {
+    mods = score_mods(*score, scale, causal, w, L, false);
+    pp.mods = mods;
+    pp.ranges = reinterpret_cast<int2*>(w + L.ranges);
+    mods.ranges = pp.ranges;
+    if (score->doc_q) {
+      pp.doc_err = reinterpret_cast<int32_t*>(w + L.doc_err);
+      rc = plan_docs(pp, *score, T_q, T_kv, w, L, false, st);
+      if (rc) return rc;
+    }
   }
   rc = cuda_status(launch_plan(pp, st));
   if (rc) return rc;
@@ -231,8 +302,134 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   // O is written in bf16 (the fused forward, or one step's partial in bf16)
   // or, for a step partial requested in fp32, in fp32
   const bool part32 = step >= 0 && part_fp32;
+  if (score) {
+    fp.mods = mods;
+    return cuda_status(single ? launch_score_fwd(fp, tk, tv, D, score->mod(), grid, st)
+                              : launch_score_fwd_dual(fp, tk, tv, D, score->mod(), grid, st));
+  }
   return cuda_status(single ? launch_fwd(fp, tk, tv, D, part32, grouped, grid, st)
                             : launch_fwd_dual(fp, tk, tv, D, part32, grid, st));
+}
+
+static int bwd_common(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                      void* dq, void* dk, void* dv, int64_t dq_rows, int64_t dkv_rows, const int32_t* cu_seqlens_q,
+                      const int32_t* cu_seqlens_kv, const int32_t* cu_seqlens_q_padded,
+                      const int32_t* cu_seqlens_kv_padded, int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D,
+                      int causal, float softmax_scale, int cp_size, int pad_between_seqs, const ScoreArgs* score,
+                      void* workspace, size_t workspace_bytes, int32_t* dev_status, cudaStream_t st) {
+  int rc = check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp_size, pad_between_seqs);
+  if (rc) return rc;
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !cu_seqlens_q || !cu_seqlens_kv || !dev_status)
+    return THD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4))
+    return THD_ERR_INVALID_ARG;
+  if (dq_rows < T_q || dkv_rows < T_kv || dq_rows >= ((int64_t)1 << 31) || dkv_rows >= ((int64_t)1 << 31))
+    return THD_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || causal < kCausalNone || causal > kCausalBottomRight)
+    return THD_ERR_INVALID_ARG;
+  if (score) {
+    rc = check_score(*score, softmax_scale);
+    if (rc) return rc;
+    if (!score->any()) score = nullptr;
+  }
+  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp_size, true, score != nullptr, score && score->doc_q);
+  rc = check_ws(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  char* w = static_cast<char*>(workspace);
+  // one planner launch, two schedules: key tiles for the dK/dV pass, query
+  // tiles for the dQ pass
+  PlanParams pp = plan_params(cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, cp_size,
+                              causal, pad_between_seqs, T_q, T_kv, 3, w, L, dev_status);
+  pp.tile_off_q = reinterpret_cast<int32_t*>(w + L.tile_off_q);
+  pp.counters_q = reinterpret_cast<int32_t*>(w + L.counters_q);
+  pp.items_q = reinterpret_cast<int4*>(w + L.items_q);
+  pp.item_cap_q = L.item_cap_q;
+  if (score) {
+    pp.mods = score_mods(*score, softmax_scale, causal, w, L, true);
+    pp.ranges = reinterpret_cast<int2*>(w + L.ranges);
+    pp.ranges_q = reinterpret_cast<int2*>(w + L.ranges_q);
+    if (score->doc_q) {
+      pp.doc_err = reinterpret_cast<int32_t*>(w + L.doc_err);
+      rc = plan_docs(pp, *score, T_q, T_kv, w, L, true, st);
+      if (rc) return rc;
+    }
+  }
+  rc = cuda_status(launch_plan(pp, st));
+  if (rc) return rc;
+  float* delta = reinterpret_cast<float*>(w + L.delta);
+  float* lse2 = reinterpret_cast<float*>(w + L.lse2);
+  rc = cuda_status(launch_bwd_prep(static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(dout), lse, delta,
+                                   lse2, pp.eff, B, T_q, Hq, D, dev_status, st));
+  if (rc) return rc;
+  CUtensorMap tq, tdo, tk, tv;
+  if (!make_thd_map(&tq, q, T_q, Hq, D) || !make_thd_map(&tdo, dout, T_q, Hq, D) ||
+      !make_thd_map(&tk, k, T_kv, Hkv, D) || !make_thd_map(&tv, v, T_kv, Hkv, D))
+    return THD_ERR_CUDA;
+  DqParams dp;
+  std::memset(&dp, 0, sizeof(dp));
+  dp.q = static_cast<const uint16_t*>(q);
+  dp.dout = static_cast<const uint16_t*>(dout);
+  dp.lse2 = lse2;
+  dp.delta = delta;
+  dp.dq = static_cast<uint16_t*>(dq);
+  dp.eff = pp.eff;
+  dp.items = pp.items_q;
+  dp.counters = pp.counters_q;
+  dp.claim = pp.counters_q + 1;
+  const bool grouped_q = long_sequences(B, T_kv);
+  dp.group_kv = locality_group(Hkv, (size_t)T_kv * D * 2 * 2, grouped_q);
+  dp.dev_status = dev_status;
+  dp.B = B;
+  dp.Hq = Hq;
+  dp.Hkv = Hkv;
+  dp.cp = cp_size;
+  dp.causal = causal;
+  dp.T_q = T_q;
+  dp.dq_rows = dq_rows;
+  dp.scale = softmax_scale;
+  dp.scale_log2 = softmax_scale * 1.4426950408889634f;
+  dp.step_lo = 0;
+  dp.step_hi = cp_size;
+  dp.test_stall = take_test_stall(THD_KERNEL_BWD_DQ) ? 1 : 0;
+  const int64_t bound_q = (int64_t)L.item_cap_q * Hq;
+  const int grid_q = (int)(bound_q < num_sms() ? (bound_q > 0 ? bound_q : 1) : num_sms());
+  dp.mods = pp.mods;
+  dp.mods.ranges = pp.ranges_q;
+  rc = cuda_status(score ? launch_score_dq(dp, tk, tv, D, grouped_q, score->mod(), grid_q, st)
+                         : launch_dq(dp, tk, tv, D, grouped_q, grid_q, st));
+  if (rc) return rc;
+  BwdParams bp;
+  std::memset(&bp, 0, sizeof(bp));
+  bp.q = static_cast<const uint16_t*>(q);
+  bp.dout = static_cast<const uint16_t*>(dout);
+  bp.lse2 = lse2;
+  bp.delta = delta;
+  bp.dk = static_cast<uint16_t*>(dk);
+  bp.dv = static_cast<uint16_t*>(dv);
+  bp.eff = pp.eff;
+  bp.items = pp.items;
+  bp.counters = pp.counters;
+  bp.claim = pp.counters + 1;
+  const bool grouped_kv = long_sequences(B, T_q);
+  bp.group_kv = locality_group(Hkv, (size_t)T_q * (Hq / Hkv) * (D * 2 * 2 + 8), grouped_kv);
+  bp.dev_status = dev_status;
+  bp.B = B;
+  bp.Hq = Hq;
+  bp.Hkv = Hkv;
+  bp.cp = cp_size;
+  bp.causal = causal;
+  bp.T_q = T_q;
+  bp.dkv_rows = dkv_rows;
+  bp.scale = softmax_scale;
+  bp.scale_log2 = softmax_scale * 1.4426950408889634f;
+  bp.test_stall = take_test_stall(THD_KERNEL_BWD) ? 1 : 0;
+  const int64_t bound = (int64_t)L.item_cap * Hkv;
+  const int grid = (int)(bound < num_sms() ? (bound > 0 ? bound : 1) : num_sms());
+  bp.mods = pp.mods;
+  bp.mods.ranges = pp.ranges;
+  return cuda_status(score ? launch_score_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, score->mod(), grid, st)
+                           : launch_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, grid, st));
 }
 
 // ------------------------------------------------------------------ A2A / hierarchical
@@ -335,6 +532,7 @@ const char* thd_status_string(int s) {
     case THD_DEV_ERR_NOT_DIVISIBLE: return "padded length not divisible by 2*cp_size";
     case THD_DEV_ERR_EXCEEDS_BUF: return "sequences exceed the buffer rows";
     case THD_DEV_ERR_CAUSAL_LENGTHS: return "top-left causal attention needs equal q/kv lengths per sequence";
+    case THD_DEV_ERR_DOC_ORDER: return "document numbers decrease inside a sequence";
     case THD_DEV_ERR_CAPACITY: return "internal schedule capacity exceeded";
     default: return "unknown status";
   }
@@ -382,7 +580,7 @@ int thd_attn_fwd(const void* q, const void* k, const void* v, void* o, float* ls
                  int causal, float softmax_scale, int cp_size, int pad_between_seqs, void* workspace,
                  size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream) {
   return fwd_common(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q,
-                    T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size, pad_between_seqs, -1, false, workspace,
+                    T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size, pad_between_seqs, -1, false, nullptr, workspace,
                     workspace_bytes, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -394,7 +592,7 @@ int thd_attn_fwd_step(const void* q, const void* k, const void* v, float* o_part
   if (step < 0) return THD_ERR_INVALID_ARG;
   return fwd_common(q, k, v, o_part, lse_part, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
                     cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size,
-                    pad_between_seqs, step, true, workspace, workspace_bytes, dev_status,
+                    pad_between_seqs, step, true, nullptr, workspace, workspace_bytes, dev_status,
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -407,7 +605,7 @@ int thd_attn_fwd_step_bf16(const void* q, const void* k, const void* v, void* o_
   if (step < 0) return THD_ERR_INVALID_ARG;
   return fwd_common(q, k, v, o_part, lse_part, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
                     cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size,
-                    pad_between_seqs, step, false, workspace, workspace_bytes, dev_status,
+                    pad_between_seqs, step, false, nullptr, workspace, workspace_bytes, dev_status,
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -417,99 +615,44 @@ int thd_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
                  const int32_t* cu_seqlens_kv_padded, int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D,
                  int causal, float softmax_scale, int cp_size, int pad_between_seqs, void* workspace,
                  size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int rc = check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp_size, pad_between_seqs);
-  if (rc) return rc;
-  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !cu_seqlens_q || !cu_seqlens_kv || !dev_status)
-    return THD_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
-      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4))
-    return THD_ERR_INVALID_ARG;
-  if (dq_rows < T_q || dkv_rows < T_kv || dq_rows >= ((int64_t)1 << 31) || dkv_rows >= ((int64_t)1 << 31))
-    return THD_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || causal < kCausalNone || causal > kCausalBottomRight)
-    return THD_ERR_INVALID_ARG;
-  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp_size, true);
-  rc = check_ws(workspace, workspace_bytes, L.total);
-  if (rc) return rc;
-  char* w = static_cast<char*>(workspace);
-  // one planner launch, two schedules: key tiles for the dK/dV pass, query
-  // tiles for the dQ pass
-  PlanParams pp = plan_params(cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, cp_size,
-                              causal, pad_between_seqs, T_q, T_kv, 3, w, L, dev_status);
-  pp.tile_off_q = reinterpret_cast<int32_t*>(w + L.tile_off_q);
-  pp.counters_q = reinterpret_cast<int32_t*>(w + L.counters_q);
-  pp.items_q = reinterpret_cast<int4*>(w + L.items_q);
-  pp.item_cap_q = L.item_cap_q;
-  rc = cuda_status(launch_plan(pp, st));
-  if (rc) return rc;
-  float* delta = reinterpret_cast<float*>(w + L.delta);
-  float* lse2 = reinterpret_cast<float*>(w + L.lse2);
-  rc = cuda_status(launch_bwd_prep(static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(dout), lse, delta,
-                                   lse2, pp.eff, B, T_q, Hq, D, dev_status, st));
-  if (rc) return rc;
-  CUtensorMap tq, tdo, tk, tv;
-  if (!make_thd_map(&tq, q, T_q, Hq, D) || !make_thd_map(&tdo, dout, T_q, Hq, D) ||
-      !make_thd_map(&tk, k, T_kv, Hkv, D) || !make_thd_map(&tv, v, T_kv, Hkv, D))
-    return THD_ERR_CUDA;
-  DqParams dp;
-  std::memset(&dp, 0, sizeof(dp));
-  dp.q = static_cast<const uint16_t*>(q);
-  dp.dout = static_cast<const uint16_t*>(dout);
-  dp.lse2 = lse2;
-  dp.delta = delta;
-  dp.dq = static_cast<uint16_t*>(dq);
-  dp.eff = pp.eff;
-  dp.items = pp.items_q;
-  dp.counters = pp.counters_q;
-  dp.claim = pp.counters_q + 1;
-  const bool grouped_q = long_sequences(B, T_kv);
-  dp.group_kv = locality_group(Hkv, (size_t)T_kv * D * 2 * 2, grouped_q);
-  dp.dev_status = dev_status;
-  dp.B = B;
-  dp.Hq = Hq;
-  dp.Hkv = Hkv;
-  dp.cp = cp_size;
-  dp.causal = causal;
-  dp.T_q = T_q;
-  dp.dq_rows = dq_rows;
-  dp.scale = softmax_scale;
-  dp.scale_log2 = softmax_scale * 1.4426950408889634f;
-  dp.step_lo = 0;
-  dp.step_hi = cp_size;
-  dp.test_stall = take_test_stall(THD_KERNEL_BWD_DQ) ? 1 : 0;
-  const int64_t bound_q = (int64_t)L.item_cap_q * Hq;
-  const int grid_q = (int)(bound_q < num_sms() ? (bound_q > 0 ? bound_q : 1) : num_sms());
-  rc = cuda_status(launch_dq(dp, tk, tv, D, grouped_q, grid_q, st));
-  if (rc) return rc;
-  BwdParams bp;
-  std::memset(&bp, 0, sizeof(bp));
-  bp.q = static_cast<const uint16_t*>(q);
-  bp.dout = static_cast<const uint16_t*>(dout);
-  bp.lse2 = lse2;
-  bp.delta = delta;
-  bp.dk = static_cast<uint16_t*>(dk);
-  bp.dv = static_cast<uint16_t*>(dv);
-  bp.eff = pp.eff;
-  bp.items = pp.items;
-  bp.counters = pp.counters;
-  bp.claim = pp.counters + 1;
-  const bool grouped_kv = long_sequences(B, T_q);
-  bp.group_kv = locality_group(Hkv, (size_t)T_q * (Hq / Hkv) * (D * 2 * 2 + 8), grouped_kv);
-  bp.dev_status = dev_status;
-  bp.B = B;
-  bp.Hq = Hq;
-  bp.Hkv = Hkv;
-  bp.cp = cp_size;
-  bp.causal = causal;
-  bp.T_q = T_q;
-  bp.dkv_rows = dkv_rows;
-  bp.scale = softmax_scale;
-  bp.scale_log2 = softmax_scale * 1.4426950408889634f;
-  bp.test_stall = take_test_stall(THD_KERNEL_BWD) ? 1 : 0;
-  const int64_t bound = (int64_t)L.item_cap * Hkv;
-  const int grid = (int)(bound < num_sms() ? (bound > 0 ? bound : 1) : num_sms());
-  return cuda_status(launch_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, grid, st));
+  return bwd_common(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q, cu_seqlens_kv,
+                    cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale,
+                    cp_size, pad_between_seqs, nullptr, workspace, workspace_bytes, dev_status,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t thd_score_workspace_size(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp_size, int has_docs,
+                                int for_bwd) {
+  if (check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp_size, -1) != THD_OK) return 0;
+  return ws_layout(B, T_q, T_kv, Hq, D, cp_size, for_bwd != 0, true, has_docs != 0).total;
+}
+
+int thd_attn_score_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,
+                       const int32_t* cu_seqlens_kv, const int32_t* cu_seqlens_q_padded,
+                       const int32_t* cu_seqlens_kv_padded, int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D,
+                       int causal, float softmax_scale, int cp_size, int pad_between_seqs, float softcap,
+                       const float* dist_slopes, const int32_t* doc_q, const int32_t* doc_kv,
+                       const int32_t* prefix_len, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                       thd_stream_t stream) {
+  const ScoreArgs a{softcap, dist_slopes, doc_q, doc_kv, prefix_len};
+  return fwd_common(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q,
+                    T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size, pad_between_seqs, -1, false, &a, workspace,
+                    workspace_bytes, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int thd_attn_score_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                       void* dq, void* dk, void* dv, int64_t dq_rows, int64_t dkv_rows, const int32_t* cu_seqlens_q,
+                       const int32_t* cu_seqlens_kv, const int32_t* cu_seqlens_q_padded,
+                       const int32_t* cu_seqlens_kv_padded, int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D,
+                       int causal, float softmax_scale, int cp_size, int pad_between_seqs, float softcap,
+                       const float* dist_slopes, const int32_t* doc_q, const int32_t* doc_kv,
+                       const int32_t* prefix_len, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                       thd_stream_t stream) {
+  const ScoreArgs a{softcap, dist_slopes, doc_q, doc_kv, prefix_len};
+  return bwd_common(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q, cu_seqlens_kv,
+                    cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale,
+                    cp_size, pad_between_seqs, &a, workspace, workspace_bytes, dev_status,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 int thd_lse_merge(float* o_acc, float* lse_acc, const float* o_part, const float* lse_part, int64_t T, int H, int D,
@@ -608,7 +751,7 @@ int thd_attn_fwd_a2a(const void* q, const void* k, const void* v, void* o, float
   if (rc) return rc;
   rc = fwd_common(w + L.buf[0], w + L.buf[1], w + L.buf[2], w + L.buf[3], lse, cu_seqlens, cu_seqlens,
                   cu_seqlens_padded, cu_seqlens_padded, B, T, T, Hq, Hkv, D, causal, softmax_scale, p2p, -1, -1,
-                  false, w + L.attn, workspace_bytes - L.attn, dev_status, st);
+                  false, nullptr, w + L.attn, workspace_bytes - L.attn, dev_status, st);
   if (rc) return rc;
   A2aParams out = a2a_params(cu_seqlens_padded, B, T, D, cp_size, 1, dev_status);
   out.job[0] = a2a_job(o, w + L.buf[3], Hq, 1);

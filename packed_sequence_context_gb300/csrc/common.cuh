@@ -20,6 +20,24 @@ __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; 
 __host__ __device__ inline int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 
+// ---------------------------------------------------------------- score modifications
+// What thd_attn_score_* adds to plain attention.  A kernel instantiation is
+// told which of it costs work per score by its kMod: 0 is plain attention;
+// with kScored set, each query sees the keys of one interval (causal, prefix
+// and document masks together); kModCap and kModDist add the tanh cap and the
+// distance bias.
+constexpr int kScored = 1, kModCap = 2, kModDist = 4;
+
+struct ScoreMods {
+  float cap_a;            // softcap * log2(e)
+  float cap_c;            // 2 log2(e) softmax_scale / softcap: 2^(cap_c s) = e^(2 scale s / softcap)
+  const float* slopes;    // [Hq], or null
+  const int2* rows_q;     // per query row: the keys [x, y) of its document, or null
+  const int2* rows_kv;    // per key row: the queries [x, y) of its document, or null
+  const int32_t* prefix;  // [B], or null
+  const int2* ranges;     // per schedule entry: the keys (queries) [x, y) its queries (keys) may see
+};
+
 // ---------------------------------------------------------------- workspace
 // Effective metadata written by the planner (after the pad decision):
 //   eff[0][*] = cu_q, eff[1][*] = pad_q, eff[2][*] = cu_kv, eff[3][*] = pad_kv
@@ -35,6 +53,12 @@ struct WsLayout {
   size_t items_q = 0;     // int4 [item_cap_q]
   size_t delta = 0;       // fp32 [Hq][T_q]
   size_t lse2 = 0;        // fp32 [Hq][T_q], lse * log2(e)
+  // scored attention only: the schedules' ranges and the documents' extents
+  size_t ranges = 0;    // int2 [item_cap]
+  size_t ranges_q = 0;  // int2 [item_cap_q], backward
+  size_t doc_err = 0;   // int32
+  size_t rows_q = 0;    // int2 [T_q], with documents
+  size_t rows_kv = 0;   // int2 [T_kv], with documents, backward
   size_t total = 0;
   int item_cap = 0;
   int item_cap_q = 0;
@@ -42,7 +66,8 @@ struct WsLayout {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int D, int cp, bool bwd) {
+inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int D, int cp, bool bwd, bool scored = false,
+                          bool docs = false) {
   WsLayout w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -66,6 +91,15 @@ inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int D, int c
     w.items_q = take(sizeof(int32_t) * 4 * (size_t)cap_q);
     w.delta = take(sizeof(float) * (size_t)Hq * (size_t)T_q);
     w.lse2 = take(sizeof(float) * (size_t)Hq * (size_t)T_q);
+  }
+  if (scored) {
+    w.ranges = take(sizeof(int32_t) * 2 * (size_t)w.item_cap);
+    if (bwd) w.ranges_q = take(sizeof(int32_t) * 2 * (size_t)w.item_cap_q);
+  }
+  if (docs) {
+    w.doc_err = take(sizeof(int32_t));
+    w.rows_q = take(sizeof(int32_t) * 2 * (size_t)T_q);
+    if (bwd) w.rows_kv = take(sizeof(int32_t) * 2 * (size_t)T_kv);
   }
   (void)D;
   w.total = off;
@@ -106,6 +140,13 @@ __device__ inline SeqGeom seq_geom(const int32_t* eff, int B, int b, int cp, int
 // rows [0, cb) are chunk r, rows [cb, 2cb) chunk 2cp-1-r.
 __host__ __device__ inline int local_to_pos(int p, int r, int cb, int cp) {
   return p < cb ? r * cb + p : (2 * cp - 1 - r) * cb + (p - cb);
+}
+
+// Smallest valid query position of the same tile (only for tiles that hold
+// one): its first row, or, when that row lies past the valid length, none
+// before it does not either.
+__host__ __device__ inline int fwd_tile_qmin(const SeqGeom& g, int r, int t, int cp) {
+  return local_to_pos(t * kTile, r, g.cbq, cp);
 }
 
 // Largest valid query position among rank-local rows [128 t, 128 t + 128)
@@ -157,11 +198,54 @@ __host__ __device__ inline int fwd_item_tiles(const SeqGeom& g, int r, int t, in
   return n;
 }
 
+// ---- scored attention: the keys one query sees, and the queries that see one
+// key, are intervals of positions inside the sequence:
+//   query i: keys [lo, hi), hi = Lkv, under a causal mask min(Lkv, i + koff + 1)
+//     or the prefix length if that is more; then cut to the keys [x, y) of its
+//     document;
+//   key j: queries [lo, hi), lo = 0, under a causal mask j - koff unless j is
+//     in the prefix, hi = Lq; then cut to the queries of its document.
+// Document numbers do not decrease inside a sequence, so lo and hi do not
+// decrease with the position either (empty intervals included: hi >= lo), and
+// a tile's interval runs from the lo of its first row to the hi of its last.
+template <class P>
+__host__ __device__ inline int2 query_sees(const P& p, const ScoreMods& mods, const SeqGeom& g, int b, int pos) {
+  int lo = 0, hi = g.Lkv;
+  if (p.causal) {
+    hi = imin(hi, imax(pos + g.koff + 1, 0));
+    if (mods.prefix) hi = imax(hi, imin(mods.prefix[b], g.Lkv));
+  }
+  if (mods.rows_q) {
+    const int2 d = mods.rows_q[(int64_t)g.q_off + pos];
+    lo = d.x;
+    hi = imax(imin(hi, d.y), lo);
+  }
+  return make_int2(lo, hi);
+}
+template <class P>
+__host__ __device__ inline int2 key_seen_by(const P& p, const ScoreMods& mods, const SeqGeom& g, int b, int pos) {
+  int lo = 0, hi = g.Lq;
+  if (p.causal && !(mods.prefix && pos < mods.prefix[b])) lo = imin(imax(pos - g.koff, 0), g.Lq);
+  if (mods.rows_kv) {
+    const int2 d = mods.rows_kv[(int64_t)g.kv_off + pos];
+    lo = imax(lo, d.x);
+    hi = imin(hi, d.y);
+  }
+  return make_int2(lo, imax(lo, hi));
+}
+
+// 128-row tiles [x, y) of chunk c (cb rows) that hold a position of [lo, hi).
+__host__ __device__ inline int2 chunk_tiles_in(int c, int cb, int lo, int hi) {
+  const int a = imax(lo - c * cb, 0), z = imin(hi - c * cb, cb);
+  return a < z ? make_int2(a / kTile, ceil_div(z, kTile)) : make_int2(0, 0);
+}
+
 // ---- one query tile's walk (forward and the dQ pass).  P is any params
 // struct with items, eff, B, Hq, Hkv, cp, causal, step_lo, step_hi.
 struct QItem {
   SeqGeom g;
   int b, r, t, h, kvh, qmax;
+  int k_lo, k_hi;  // scored: the keys the tile's queries may see
 };
 
 // Work item w -> (schedule entry, query head).  Items are ordered by groups
@@ -173,40 +257,52 @@ struct QItem {
 // length.
 // kGrouped is a compile-time choice: a runtime branch between the two maps
 // here measured 8% slower in the forward kernel.
-template <bool kGrouped, class P>
+template <bool kGrouped, int kMod, class P>
 __device__ inline QItem q_item(const P& p, int n_entries, int w) {
   QItem it;
-  int4 e;
+  int x;  // schedule entry
   if constexpr (kGrouped) {
     const int hg = p.group_kv * (p.Hq / p.Hkv);  // query heads per group
     const int per = n_entries * hg;               // items per group
     const int grp = w / per, rem = w - grp * per;
-    e = p.items[rem / hg];
+    x = rem / hg;
     it.h = grp * hg + rem % hg;
   } else {  // one group: entry-major, heads innermost
     (void)n_entries;
-    e = p.items[w / p.Hq];
+    x = w / p.Hq;
     it.h = w % p.Hq;
   }
+  const int4 e = p.items[x];
   it.b = e.x;
   it.r = e.y;
   it.t = e.z;
   it.kvh = it.h / (p.Hq / p.Hkv);
   it.g = seq_geom(p.eff, p.B, it.b, p.cp, p.causal);
-  it.qmax = fwd_tile_qmax(it.g, it.r, it.t, p.cp);
+  if constexpr (kMod != 0) {
+    const int2 k = p.mods.ranges[x];
+    it.k_lo = k.x;
+    it.k_hi = k.y;
+  } else {
+    it.qmax = fwd_tile_qmax(it.g, it.r, it.t, p.cp);
+  }
   return it;
 }
 
 // Calls f(c, j) for every key tile the item visits, in ring order: step i
 // holds the KV of rank s = (r - i) mod cp, chunks s then 2cp-1-s.
-template <class P, typename F>
+template <int kMod, class P, typename F>
 __device__ inline void for_each_kv_tile(const QItem& it, const P& p, F&& f) {
   for (int i = p.step_lo; i < p.step_hi; ++i) {
     const int s = ring_src(it.r, i, p.cp);
     for (int e = 0; e < 2; ++e) {
       const int c = ring_chunk(s, e, p.cp);
-      const int n = fwd_chunk_tiles(it.g, c, it.qmax, p.causal != 0);
-      for (int j = 0; j < n; ++j) f(c, j);
+      if constexpr (kMod != 0) {
+        const int2 n = chunk_tiles_in(c, it.g.cbkv, it.k_lo, it.k_hi);
+        for (int j = n.x; j < n.y; ++j) f(c, j);
+      } else {
+        const int n = fwd_chunk_tiles(it.g, c, it.qmax, p.causal != 0);
+        for (int j = 0; j < n; ++j) f(c, j);
+      }
     }
   }
 }
@@ -214,11 +310,16 @@ __device__ inline void for_each_kv_tile(const QItem& it, const P& p, F&& f) {
 // Columns (keys) of tile (c, j) any query of the item may see, rounded up to
 // the MMA granularity of 16: the N of the item's S product and the K of the
 // product that contracts over keys.
-template <class P>
+template <int kMod, class P>
 __device__ inline int q_tile_ncols(const QItem& it, const P& p, int c, int j) {
   const int j0 = c * it.g.cbkv + j * kTile;
-  int n = imin(kTile, imin((c + 1) * it.g.cbkv - j0, it.g.Lkv - j0));
-  if (p.causal) n = imin(n, it.qmax + it.g.koff - j0 + 1);
+  int n;
+  if constexpr (kMod != 0) {
+    n = imin(kTile, imin((c + 1) * it.g.cbkv, it.k_hi) - j0);
+  } else {
+    n = imin(kTile, imin((c + 1) * it.g.cbkv - j0, it.g.Lkv - j0));
+    if (p.causal) n = imin(n, it.qmax + it.g.koff - j0 + 1);
+  }
   return 16 * ceil_div(imax(n, 1), 16);
 }
 
@@ -284,6 +385,11 @@ struct PlanParams {
   int32_t* counters_q;
   int4* items_q;
   int item_cap_q;
+  // scored attention: the schedules take each entry's range from the masks
+  int2* ranges;
+  int2* ranges_q;
+  ScoreMods mods;
+  int32_t* doc_err;  // set by the document kernel; cleared by a mode 0 run
   int32_t* dev_status;
 };
 
@@ -303,6 +409,7 @@ struct FwdParams {
   float scale_log2;  // softmax_scale * log2(e)
   int step_lo, step_hi;
   int test_stall;  // test hook: every thread waits for a barrier nothing completes
+  ScoreMods mods;  // scored attention
 };
 
 struct BwdParams {
@@ -322,6 +429,7 @@ struct BwdParams {
   int64_t T_q, dkv_rows;
   float scale, scale_log2;
   int test_stall;  // test hook: every thread waits for a barrier nothing completes
+  ScoreMods mods;  // scored attention
 };
 
 struct DqParams {
@@ -341,6 +449,7 @@ struct DqParams {
   float scale, scale_log2;
   int step_lo, step_hi;  // always the whole ring
   int test_stall;  // test hook: every thread waits for a barrier nothing completes
+  ScoreMods mods;  // scored attention
 };
 
 // host launchers (each returns a cudaError_t)
@@ -353,6 +462,18 @@ cudaError_t launch_bwd(const BwdParams& p, const CUtensorMap& tq, const CUtensor
                        const CUtensorMap& tv, int D, bool grouped, int grid, cudaStream_t st);
 cudaError_t launch_dq(const DqParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D, bool grouped,
                       int grid, cudaStream_t st);
+// scored attention: the same kernels with the score modifications `mod`
+cudaError_t launch_score_fwd(const FwdParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D, int mod,
+                             int grid, cudaStream_t st);
+cudaError_t launch_score_fwd_dual(const FwdParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D, int mod,
+                                  int grid, cudaStream_t st);
+cudaError_t launch_score_bwd(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
+                             const CUtensorMap& tv, int D, bool grouped, int mod, int grid, cudaStream_t st);
+cudaError_t launch_score_dq(const DqParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D, bool grouped,
+                            int mod, int grid, cudaStream_t st);
+cudaError_t launch_docs(const int32_t* doc_q, const int32_t* doc_kv, const int32_t* eff, int B, int64_t T_q,
+                        int64_t T_kv, int2* rows_q, int2* rows_kv, int32_t* doc_err, const int32_t* dev_status,
+                        cudaStream_t st);
 cudaError_t launch_lse_merge(float* o_acc, float* lse_acc, const float* o_part, const float* lse_part, int64_t T,
                              int H, int D, cudaStream_t st);
 cudaError_t launch_lse_merge_bf16(float* o_acc, float* lse_acc, const uint16_t* o_part, const float* lse_part,

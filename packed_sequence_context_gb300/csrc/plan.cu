@@ -69,7 +69,8 @@ constexpr int kPlanSmemSeqs = 1024;
 // offsets (shared memory when they fit); `tile_off` receives the offsets in
 // the workspace.  Returns false when the schedule exceeds its capacity.
 __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* toff, int mode, int32_t* tile_off,
-                              int32_t* counters, int4* items, int item_cap, int* s_warp, int* s_hist) {
+                              int32_t* counters, int4* items, int2* ranges, int item_cap, int* s_warp,
+                              int* s_hist) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int B = p.B, cp = p.cp;
 
@@ -100,7 +101,9 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   }
   for (int i = tid; i < kCostBins; i += nt) s_hist[i] = 0;
   __syncthreads();
-  auto entry = [&](int w, int& b, int& x, int& y, int& cost) {
+  // a scored schedule also leaves each entry's range of keys (queries), and
+  // its cost is the number of tiles in it
+  auto entry = [&](int w, int& b, int& x, int& y, int& cost, int2& range) {
     b = upper_index(toff, B, w);
     // skip empty sequences that share the same offset
     while (b < B && toff[b + 1] <= w) ++b;
@@ -110,17 +113,45 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
       const int per_r = ceil_div(2 * g.cbq, kTile);
       x = rem / per_r;
       y = rem % per_r;
-      cost = fwd_item_tiles(g, x, y, cp, p.causal != 0, p.step_lo, p.step_hi);
+      if (ranges) {
+        const int qmax = fwd_tile_qmax(g, x, y, cp);
+        cost = 0;
+        if (qmax >= 0) {
+          range.x = query_sees(p, p.mods, g, b, fwd_tile_qmin(g, x, y, cp)).x;
+          range.y = query_sees(p, p.mods, g, b, qmax).y;
+          for (int c = 0; c < 2 * cp; ++c) {
+            const int2 n = chunk_tiles_in(c, g.cbkv, range.x, range.y);
+            cost += n.y - n.x;
+          }
+        }
+      } else {
+        cost = fwd_item_tiles(g, x, y, cp, p.causal != 0, p.step_lo, p.step_hi);
+      }
     } else {
       const int per_c = ceil_div(g.cbkv, kTile);
       x = rem / per_c;
       y = rem % per_c;
-      cost = bwd_item_qtiles(g, x, y, cp, p.causal != 0);
+      if (ranges) {
+        int kf, kl;
+        bwd_kv_range(g, x, y, kf, kl);
+        cost = 0;
+        if (kf <= kl) {
+          range.x = key_seen_by(p, p.mods, g, b, kf).x;
+          range.y = key_seen_by(p, p.mods, g, b, kl).y;
+          for (int c = 0; c < 2 * cp; ++c) {
+            const int2 n = chunk_tiles_in(c, g.cbq, range.x, range.y);
+            cost += n.y - n.x;
+          }
+        }
+      } else {
+        cost = bwd_item_qtiles(g, x, y, cp, p.causal != 0);
+      }
     }
   };
   for (int w = tid; w < total; w += nt) {
     int b, x, y, cost;
-    entry(w, b, x, y, cost);
+    int2 range;
+    entry(w, b, x, y, cost, range);
     atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
   }
   __syncthreads();
@@ -145,9 +176,11 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   __syncthreads();
   for (int w = tid; w < total; w += nt) {
     int b, x, y, cost;
-    entry(w, b, x, y, cost);
+    int2 range = make_int2(0, 0);
+    entry(w, b, x, y, cost, range);
     const int pos = atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
     items[pos] = make_int4(b, x, y, cost);
+    if (ranges) ranges[pos] = range;
   }
   if (tid == 0) {
     counters[0] = total;
@@ -212,6 +245,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
       if (p.token_map && (int64_t)pq > p.token_map_cap) set_err(&s_err, THD_DEV_ERR_EXCEEDS_BUF);
     }
   }
+  if (p.doc_err && tid == 0) {
+    if (p.mode == 0) *p.doc_err = 0;  // the document kernel runs next
+    else if (*p.doc_err) set_err(&s_err, THD_DEV_ERR_DOC_ORDER);
+  }
   __syncthreads();
   const int err = s_err == INT_MAX ? 0 : s_err;
   if (err) {
@@ -263,12 +300,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   if (p.mode == 0) return;
   const int32_t* effr = meta_in_smem ? s_meta : eff;
   if (!plan_schedule(p, effr, meta_in_smem ? s_meta + 4 * (B + 1) : p.tile_off, p.mode == 3 ? 2 : p.mode,
-                     p.tile_off, p.counters, p.items, p.item_cap, s_warp, s_hist))
+                     p.tile_off, p.counters, p.items, p.ranges, p.item_cap, s_warp, s_hist))
     return;
   if (p.mode == 3) {
     __syncthreads();  // s_hist and the staged tile offsets are reused
     plan_schedule(p, effr, meta_in_smem ? s_meta + 4 * (B + 1) : p.tile_off_q, 1, p.tile_off_q, p.counters_q,
-                  p.items_q, p.item_cap_q, s_warp, s_hist);
+                  p.items_q, p.ranges_q, p.item_cap_q, s_warp, s_hist);
   }
 }
 
@@ -278,6 +315,73 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t st) {
   count_launch();
   cudaError_t e = cudaGetLastError();
   prof_after(p.mode == 0 ? THD_KERNEL_PARTITION : THD_KERNEL_PLAN, st);
+  return e;
+}
+
+// ------------------------------------------------------------------ documents
+// Scored attention with documents: each query row's keys of the same document
+// number, and each key row's queries, as intervals of positions (see
+// query_sees).  Numbers do not decrease inside a sequence, so both ends are
+// binary searches over the other side's numbers; a decrease is reported.
+// One thread per row; bound by the latency of about 2 log2(L) dependent
+// loads that hit in L2 (131,072 rows: 34 loads, 0.5 MB of numbers).
+__device__ inline int first_not_below(const int32_t* a, int n, int x) {  // first i with a[i] >= x
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] < x) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ inline int first_above(const int32_t* a, int n, int x) {  // first i with a[i] > x
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(256) docs_kernel(const int32_t* __restrict__ doc_q,
+                                                   const int32_t* __restrict__ doc_kv,
+                                                   const int32_t* __restrict__ eff, int B, int2* rows_q,
+                                                   int2* rows_kv, int32_t* doc_err, const int32_t* dev_status) {
+  if (*dev_status != 0) return;
+  const int32_t* cu_q = eff;
+  const int32_t* pad_q = eff + (B + 1);
+  const int32_t* cu_kv = eff + 2 * (B + 1);
+  const int32_t* pad_kv = eff + 3 * (B + 1);
+  const int nq = pad_q[B], nkv = pad_kv[B];  // both at most the buffers' rows (checked)
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)nq + nkv; i += (int64_t)gridDim.x * 256) {
+    const bool query = i < nq;
+    const int t = (int)(query ? i : i - nq);
+    const int32_t* pad = query ? pad_q : pad_kv;
+    const int32_t* cu = query ? cu_q : cu_kv;
+    const int32_t* own = query ? doc_q : doc_kv;
+    int b = upper_index(pad, B, t);
+    if (b >= B || t - pad[b] >= cu[b + 1] - cu[b]) continue;  // no valid token
+    const int id = own[t];
+    if (t > pad[b] && own[t - 1] > id) atomicExch(doc_err, 1);
+    int2* rows = query ? rows_q : rows_kv;
+    if (!rows) continue;
+    const int32_t* other = query ? doc_kv + pad_kv[b] : doc_q + pad_q[b];
+    const int n = query ? cu_kv[b + 1] - cu_kv[b] : cu_q[b + 1] - cu_q[b];
+    rows[t] = make_int2(first_not_below(other, n, id), first_above(other, n, id));
+  }
+}
+
+cudaError_t launch_docs(const int32_t* doc_q, const int32_t* doc_kv, const int32_t* eff, int B, int64_t T_q,
+                        int64_t T_kv, int2* rows_q, int2* rows_kv, int32_t* doc_err, const int32_t* dev_status,
+                        cudaStream_t st) {
+  const int64_t want = (T_q + T_kv + 255) / 256;
+  const int grid = (int)(want < 1 ? 1 : (want < 8LL * num_sms() ? want : 8LL * num_sms()));
+  prof_before(THD_KERNEL_DOCS, st);
+  docs_kernel<<<grid, 256, 0, st>>>(doc_q, doc_kv, eff, B, rows_q, rows_kv, doc_err, dev_status);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  prof_after(THD_KERNEL_DOCS, st);
   return e;
 }
 

@@ -33,6 +33,7 @@ THD_DEV_ERR_NOT_DIVISIBLE = 104
 THD_DEV_ERR_EXCEEDS_BUF = 105
 THD_DEV_ERR_CAUSAL_LENGTHS = 106
 THD_DEV_ERR_CAPACITY = 107
+THD_DEV_ERR_DOC_ORDER = 108
 
 THD_KERNEL_PLAN = 1
 THD_KERNEL_FWD = 2
@@ -45,6 +46,7 @@ THD_KERNEL_PARTITION = 8
 THD_KERNEL_A2A = 9
 THD_KERNEL_ROPE = 10
 THD_KERNEL_DROPOUT = 11
+THD_KERNEL_DOCS = 12
 
 THD_FWD_KERNEL_SINGLE = 1
 THD_FWD_KERNEL_DUAL = 2
@@ -82,6 +84,12 @@ SIGNATURES = {
                                     _i32, _i32, _f32, _i32, _i32, _vp, _vp]),
     "thd_attn_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32,
                             _i64, _i64, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "thd_attn_score_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _i32, _i32,
+                                  _i32, _f32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "thd_attn_score_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32,
+                                  _i64, _i64, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
+                                  _vp, _sz, _vp, _vp]),
+    "thd_score_workspace_size": (_sz, [_i32, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32]),
     "thd_lse_merge": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp]),
     "thd_lse_merge_bf16": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp]),
     "thd_grad_tail_zero": (_i32, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp]),
@@ -206,6 +214,31 @@ def thd_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlen
                               dkv_rows, _p(cu_seqlens_q), _p(cu_seqlens_kv), _p(cu_seqlens_q_padded),
                               _p(cu_seqlens_kv_padded), B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size,
                               pad_between_seqs, _p(workspace), workspace_bytes, _p(dev_status), _s(stream))
+
+
+def thd_attn_score_fwd(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B,
+                       T_q, T_kv, Hq, Hkv, D, causal, softmax_scale, cp_size, pad_between_seqs, softcap, dist_slopes,
+                       doc_q, doc_kv, prefix_len, workspace, workspace_bytes, dev_status, stream=None) -> int:
+    return lib().thd_attn_score_fwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens_q), _p(cu_seqlens_kv),
+                                    _p(cu_seqlens_q_padded), _p(cu_seqlens_kv_padded), B, T_q, T_kv, Hq, Hkv, D,
+                                    causal, softmax_scale, cp_size, pad_between_seqs, softcap, _p(dist_slopes),
+                                    _p(doc_q), _p(doc_kv), _p(prefix_len), _p(workspace), workspace_bytes,
+                                    _p(dev_status), _s(stream))
+
+
+def thd_attn_score_bwd(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q, cu_seqlens_kv,
+                       cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale,
+                       cp_size, pad_between_seqs, softcap, dist_slopes, doc_q, doc_kv, prefix_len, workspace,
+                       workspace_bytes, dev_status, stream=None) -> int:
+    return lib().thd_attn_score_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(dout), _p(dq), _p(dk), _p(dv), dq_rows,
+                                    dkv_rows, _p(cu_seqlens_q), _p(cu_seqlens_kv), _p(cu_seqlens_q_padded),
+                                    _p(cu_seqlens_kv_padded), B, T_q, T_kv, Hq, Hkv, D, causal, softmax_scale,
+                                    cp_size, pad_between_seqs, softcap, _p(dist_slopes), _p(doc_q), _p(doc_kv),
+                                    _p(prefix_len), _p(workspace), workspace_bytes, _p(dev_status), _s(stream))
+
+
+def thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, has_docs, for_bwd) -> int:
+    return lib().thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, has_docs, for_bwd)
 
 
 def thd_lse_merge(o_acc, lse_acc, o_part, lse_part, T, H, D, stream=None) -> int:
@@ -414,6 +447,85 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_pa
                                         cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq,
                                         Hkv, D, int(causal), scale, cp_size, pad_between_seqs, ws, ws.numel(), st,
                                         stream))
+    return dq, dk, dv, st
+
+
+def _score_checks(w, q, k, v, more, offsets, dist_slopes, doc_q, doc_kv, prefix_len):
+    """What the library cannot see of a scored call: types, shapes, layout and
+    device of its tensors.  `more`: (tensor, shape, dtype) triples."""
+    import torch
+    _current(w, q)
+    _need(w, q.dim() == 3 and k.dim() == 3)
+    (T_q, Hq, D), (T_kv, Hkv, _) = q.shape, k.shape
+    B = offsets[0].numel() - 1
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    triples = [(q, (T_q, Hq, D), bf16), (k, (T_kv, Hkv, D), bf16), (v, (T_kv, Hkv, D), bf16),
+               (dist_slopes, (Hq,), f32), (doc_q, (T_q,), i32), (doc_kv, (T_kv,), i32), (prefix_len, (B,), i32)]
+    triples += [(c, (B + 1,), i32) for c in offsets] + more
+    dev = q.device
+    for t, shape, dtype in triples:
+        if t is not None:
+            _need(w, t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous())
+    return B, T_q, T_kv, Hq, Hkv, D
+
+
+def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None, cu_seqlens_kv_padded=None, *,
+                   softcap=0.0, dist_slopes=None, doc_q=None, doc_kv=None, prefix_len=None, cp_size=1, causal=True,
+                   softmax_scale=None, pad_between_seqs=-1, out=None, lse=None, dev_status=None, workspace=None,
+                   stream=None):
+    """attn_fwd with capped scores (softcap), a bias by distance (dist_slopes
+    fp32 [Hq]), documents (doc_q int32 [T_q], doc_kv [T_kv]) and prefixes
+    (prefix_len int32 [B]).  Returns (o, lse, dev_status)."""
+    import torch
+    w = "thd_attn_score_fwd"
+    more = [(out, q.shape, torch.bfloat16), (lse, (q.shape[1], q.shape[0]), torch.float32),
+            (dev_status, (1,), torch.int32)]
+    B, T_q, T_kv, Hq, Hkv, D = _score_checks(
+        w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
+        doc_q, doc_kv, prefix_len)
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    o = torch.empty_like(q) if out is None else out
+    l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
+    st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+    if workspace is None:
+        workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, int(doc_q is not None), 0),
+                               q.device)
+    _check(w, thd_attn_score_fwd(q, k, v, o, l, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+                                 cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal), scale, cp_size,
+                                 pad_between_seqs, softcap, dist_slopes, doc_q, doc_kv, prefix_len, workspace,
+                                 workspace.numel(), st, stream))
+    return o, l, st
+
+
+def attn_score_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
+                   cu_seqlens_kv_padded=None, *, softcap=0.0, dist_slopes=None, doc_q=None, doc_kv=None,
+                   prefix_len=None, cp_size=1, causal=True, softmax_scale=None, pad_between_seqs=-1, dq_rows=None,
+                   dkv_rows=None, dq=None, dk=None, dv=None, dev_status=None, workspace=None, stream=None):
+    """Gradients of attn_score_fwd (same modifications), with optional slack
+    rows as in attn_bwd.  Returns (dq, dk, dv, dev_status)."""
+    import torch
+    w = "thd_attn_score_bwd"
+    bf16 = torch.bfloat16
+    dq_rows = q.shape[0] if dq_rows is None else dq_rows
+    dkv_rows = k.shape[0] if dkv_rows is None else dkv_rows
+    qs, ks = (dq_rows, *q.shape[1:]), (dkv_rows, *k.shape[1:])
+    more = [(o, q.shape, bf16), (dout, q.shape, bf16), (lse, (q.shape[1], q.shape[0]), torch.float32),
+            (dq, qs, bf16), (dk, ks, bf16), (dv, ks, bf16), (dev_status, (1,), torch.int32)]
+    B, T_q, T_kv, Hq, Hkv, D = _score_checks(
+        w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
+        doc_q, doc_kv, prefix_len)
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    dq = torch.empty(qs, dtype=bf16, device=q.device) if dq is None else dq
+    dk = torch.empty(ks, dtype=bf16, device=q.device) if dk is None else dk
+    dv = torch.empty(ks, dtype=bf16, device=q.device) if dv is None else dv
+    st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+    if workspace is None:
+        workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, int(doc_q is not None), 1),
+                               q.device)
+    _check(w, thd_attn_score_bwd(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q, cu_seqlens_kv,
+                                 cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal),
+                                 scale, cp_size, pad_between_seqs, softcap, dist_slopes, doc_q, doc_kv, prefix_len,
+                                 workspace, workspace.numel(), st, stream))
     return dq, dk, dv, st
 
 
