@@ -170,6 +170,8 @@ static int locality_group(int Hkv, size_t bytes_per_kv_head, bool grouped) {
   return best;
 }
 
+constexpr double kLog2e = 1.4426950408889634;
+
 // What the scored entry points add to the plain ones (see thd_attn_score_fwd).
 struct ScoreArgs {
   float softcap;
@@ -179,9 +181,8 @@ struct ScoreArgs {
   const int32_t* prefix;
   bool any() const { return softcap > 0.f || slopes || doc_q || prefix; }
   int mod() const { return kScored | (softcap > 0.f ? kModCap : 0) | (slopes ? kModDist : 0); }
+  int fwd_mod() const { return mod() | (softcap > 0.f && !slopes && kLog2e * softcap <= kBoundedCap ? kModBounded : 0); }
 };
-
-constexpr double kLog2e = 1.4426950408889634;
 
 static int check_score(const ScoreArgs& a, float scale) {
   if (!(a.softcap >= 0.f) || !std::isfinite(a.softcap)) return THD_ERR_INVALID_ARG;
@@ -193,12 +194,34 @@ static int check_score(const ScoreArgs& a, float scale) {
   return THD_OK;
 }
 
+// Coefficients of tanh(c s) = s (b0 + b1 s^2 + ..) from those in u = c s, and
+// the largest |s| they hold for: 0 when a power of c, alone or times the cap,
+// is no normal float.
+static float cap_polynomial(const double* ck, int n, double u_max, double c, double softcap, float* b) {
+  double pw = c;
+  bool ok = true;
+  for (int i = 0; i < n; ++i, pw *= c * c) {
+    const double v = std::fabs(ck[i] * pw), a = v * kLog2e * softcap;
+    b[i] = (float)(ck[i] * pw);
+    ok = ok && v > 1e-37 && v < 1e37 && a > 1e-37 && a < 1e37;
+  }
+  const double lim = u_max / c;
+  return ok && lim * lim > 1e-37 && lim * lim < 1e37 ? (float)lim : 0.f;
+}
+
 static ScoreMods score_mods(const ScoreArgs& a, float scale, int causal, char* ws, const WsLayout& L, bool bwd) {
   ScoreMods m;
   std::memset(&m, 0, sizeof(m));
   if (a.softcap > 0.f) {
     m.cap_a = (float)(kLog2e * a.softcap);
     m.cap_c = (float)(2.0 * kLog2e * scale / a.softcap);
+    // tanh(u) / u = sum c_k u^(2k), to 4.0e-7 of its value on |u| <= 0.25 and
+    // to 5.7e-7 on |u| <= 0.75, in s = u / c
+    constexpr double near_c[3] = {0.999999604345, -0.333219082252, 0.128416134328};
+    constexpr double far_c[5] = {0.999999434924, -0.33328251533, 0.132589832236, -0.0500563027154, 0.0129296324108};
+    const double c = (double)scale / a.softcap;
+    m.cap_near = cap_polynomial(near_c, 3, 0.25, c, a.softcap, m.cap_n);
+    m.cap_far = cap_polynomial(far_c, 5, 0.75, c, a.softcap, m.cap_f);
   }
   m.slopes = a.slopes;
   if (a.doc_q) {
@@ -304,8 +327,8 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   const bool part32 = step >= 0 && part_fp32;
   if (score) {
     fp.mods = mods;
-    return cuda_status(single ? launch_score_fwd(fp, tk, tv, D, score->mod(), grid, st)
-                              : launch_score_fwd_dual(fp, tk, tv, D, score->mod(), grid, st));
+    return cuda_status(single ? launch_score_fwd(fp, tk, tv, D, score->fwd_mod(), grid, st)
+                              : launch_score_fwd_dual(fp, tk, tv, D, score->fwd_mod(), grid, st));
   }
   return cuda_status(single ? launch_fwd(fp, tk, tv, D, part32, grouped, grid, st)
                             : launch_fwd_dual(fp, tk, tv, D, part32, grid, st));

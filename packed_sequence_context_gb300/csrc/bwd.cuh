@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
         const int d0 = q0 + it.g.koff - j_pos;
         const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, n_lo < n_hi && d0 + n_lo < 0);
         ScoreConsts sc;
-        if constexpr (kMod != 0) sc = score_consts<kMod>(p, h);
+        if constexpr (kMod != 0) sc = score_consts<kMod, false>(p, h);
         // the cp.async writes of lse/Delta are visible to the threads that
         // observe the stage barrier's phase, so observe it here (it cannot have
         // moved on: the stage is refilled only after this step's p_ready)
@@ -545,31 +545,48 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
             if constexpr (kMod != 0) {
               // P in place over the scores and, for dS, P (1 - tanh^2); then 0
               // in the columns that do not see this key, whatever stood there
+              constexpr bool kCap = (kMod & kModCap) != 0;
               float(&y)[32] = reinterpret_cast<float(&)[32]>(sr);
-              score_run<kMod, true, 32, 1>(y, pv[i], sc, (float)(d0 + 32 * kk), abs_needed);
-#pragma unroll
-              for (int q4 = 0; q4 < 8; ++q4) {
-                const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
-                const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                  const int n = 4 * q4 + e;
-                  float x0, x1;
-                  fadd2(x0, x1, y[n], y[n + 1], -l[e], -l[e + 1]);
-                  y[n] = ex2(x0);
-                  y[n + 1] = ex2(x1);
-                  if constexpr ((kMod & kModCap) != 0)
-                    fmul2(pv[i][n], pv[i][n + 1], pv[i][n], pv[i][n + 1], y[n], y[n + 1]);
-                  else
-                    pv[i][n] = y[n], pv[i][n + 1] = y[n + 1];
-                }
+              if constexpr (kCap) {
+                if (cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+                tanh_run(y, sc);
               }
-              if (cut) {
+              const float a = kCap ? sc.cap_a : sl2;
+              auto write_p = [&](auto bias) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int n = 32 * kk + e;
-                  if (n < n_lo || n >= n_hi) y[e] = pv[i][e] = 0.f;
+                for (int q4 = 0; q4 < 8; ++q4) {
+                  const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
+                  const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                  for (int e = 0; e < 4; e += 2) {
+                    const int n = 4 * q4 + e;
+                    float x0, x1, b0 = -l[e], b1 = -l[e + 1];
+                    if constexpr ((kMod & kModDist) != 0) {
+                      float c0, c1;
+                      bias.at(n, c0, c1);
+                      fadd2(b0, b1, b0, b1, c0, c1);
+                    }
+                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                    x0 = ex2(x0);
+                    x1 = ex2(x1);
+                    if constexpr (kCap) {
+                      float w0, w1;
+                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                      fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
+                    } else {
+                      pv[i][n] = x0, pv[i][n + 1] = x1;
+                    }
+                    y[n] = x0, y[n + 1] = x1;
+                  }
                 }
+              };
+              if ((kMod & kModDist) != 0 && abs_needed)
+                write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
+              else
+                write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
+              if (cut) {
+                score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+                score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
               }
 #pragma unroll
               for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);

@@ -26,11 +26,18 @@ __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 // with kScored set, each query sees the keys of one interval (causal, prefix
 // and document masks together); kModCap and kModDist add the tanh cap and the
 // distance bias.
-constexpr int kScored = 1, kModCap = 2, kModDist = 4;
+// kModBounded (forward, with the cap alone): |y| <= softcap, small enough that
+// 2^y needs no running maximum.
+constexpr int kScored = 1, kModCap = 2, kModDist = 4, kModBounded = 8;
+constexpr float kBoundedCap = 80.f;  // softcap log2(e) at most this: 2^-80 <= P <= 2^80
 
 struct ScoreMods {
   float cap_a;            // softcap * log2(e)
   float cap_c;            // 2 log2(e) softmax_scale / softcap: 2^(cap_c s) = e^(2 scale s / softcap)
+  // tanh(scale s / softcap) as s times a polynomial in s^2: three terms while
+  // |s| <= cap_near, five while |s| <= cap_far (0: never)
+  float cap_n[3], cap_near;
+  float cap_f[5], cap_far;
   const float* slopes;    // [Hq], or null
   const int2* rows_q;     // per query row: the keys [x, y) of its document, or null
   const int2* rows_kv;    // per key row: the queries [x, y) of its document, or null

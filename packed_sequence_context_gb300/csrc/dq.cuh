@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(384, 1)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
-        sc = score_consts<kMod>(p, it.h);
+        sc = score_consts<kMod, false>(p, it.h);
       }
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
@@ -470,22 +470,35 @@ __global__ void __launch_bounds__(384, 1)
             if constexpr (kMod != 0) {
               // dS = P (dP - Delta) (1 - tanh^2), in place over the scores; then
               // 0 on the keys this row may not see, whatever stood there
-              float w[32];
+              constexpr bool kCap = (kMod & kModCap) != 0;
               float(&y)[32] = reinterpret_cast<float(&)[32]>(sr);
-              score_run<kMod, true, 32, -1>(y, w, sc, (float)(ahead - 1 - 32 * ch), abs_needed);
-#pragma unroll
-              for (int n = 0; n < 32; n += 2) {
-                float x0, x1, t0, t1;
-                fadd2(x0, x1, y[n], y[n + 1], -lse2, -lse2);
-                fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
-                if constexpr ((kMod & kModCap) != 0) fmul2(t0, t1, t0, t1, w[n], w[n + 1]);
-                fmul2(y[n], y[n + 1], ex2(x0), ex2(x1), t0, t1);
+              const bool cut = __any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch);
+              if constexpr (kCap) {
+                if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+                tanh_run(y, sc);
               }
-              if (__any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch)) {
+              const float a = kCap ? sc.cap_a : sl2;
+              auto write_ds = [&](auto bias) {
 #pragma unroll
-                for (int n = 0; n < 32; ++n)
-                  if (32 * ch + n >= cnt || 32 * ch + n < from) y[n] = 0.f;
-              }
+                for (int n = 0; n < 32; n += 2) {
+                  float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
+                  if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
+                  ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                  fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
+                  if constexpr (kCap) {
+                    float w0, w1;
+                    ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                    fmul2(t0, t1, t0, t1, w0, w1);
+                  }
+                  fmul2(y[n], y[n + 1], ex2(x0), ex2(x1), t0, t1);
+                }
+              };
+              const float d0 = (float)(ahead - 1 - 32 * ch);
+              if ((kMod & kModDist) != 0 && abs_needed)
+                write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
+              else
+                write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
+              if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
 #pragma unroll
               for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
               tmem_st16(scol + 64 * (ch >> 1) + 16 * (ch & 1), pk);

@@ -380,10 +380,10 @@ __global__ void __launch_bounds__(384, 1)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
-        sc = score_consts<kMod>(p, it.h);
+        sc = score_consts<kMod, true>(p, it.h);
       }
       // ---- key tiles
-      float m = -INFINITY, l = 0.f;  // running max (log2 units, shared value) and this half's sum
+      float m = (kMod & kModBounded) != 0 ? 0.f : -INFINITY, l = 0.f;  // running max (log2 units, shared value) and this half's sum
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
         if (!ok) return;
@@ -421,19 +421,33 @@ __global__ void __launch_bounds__(384, 1)
         // fully visible rows (every tile off the causal diagonal) skip the selects
         const int nvalid = (k0 + 1 < nch) ? 64 : (k0 < nch ? 32 : 0);  // this thread's loaded columns
         if constexpr (kMod != 0) {
+          const bool cut = __any_sync(0xffffffffu, cnt - 32 * k0 < nvalid || from > 32 * k0);
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
-          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          if constexpr (kMod != kScored) {
+            const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+            int form = kCapNear;
+            if constexpr ((kMod & kModCap) != 0) {
+              if (cut) {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            if (k0 + kk < nch)
-              score_run<kMod, false, 32, -1>(reinterpret_cast<float(&)[32]>(sr[kk]), nullptr, sc,
-                                             (float)(ahead - 1 - 32 * (k0 + kk)), abs_needed);
-          if (__any_sync(0xffffffffu, cnt - 32 * k0 < nvalid || from > 32 * k0)) {
+                for (int kk = 0; kk < 2; ++kk)
+                  score_fill(reinterpret_cast<float(&)[32]>(sr[kk]), from - 32 * (k0 + kk), cnt - 32 * (k0 + kk), 0.f);
+              }
+              float am = 0.f;
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+                if (k0 + kk < nch) am = fmaxf(am, score_abs_max(reinterpret_cast<float(&)[32]>(sr[kk])));
+              form = cap_form(am, sc);
+            }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
+              if (k0 + kk < nch)
+                score_run<kMod, -1>(reinterpret_cast<float(&)[32]>(sr[kk]), sc, form,
+                                    (float)(ahead - 1 - 32 * (k0 + kk)), abs_needed);
+          }
+          if (cut) {
 #pragma unroll
-              for (int n = 0; n < 32; ++n)
-                if (32 * (k0 + kk) + n >= cnt || 32 * (k0 + kk) + n < from) sr[kk][n] = __float_as_uint(-INFINITY);
+            for (int kk = 0; kk < 2; ++kk)
+              score_fill(reinterpret_cast<float(&)[32]>(sr[kk]), from - 32 * (k0 + kk), cnt - 32 * (k0 + kk), -INFINITY);
           }
         } else if (__any_sync(0xffffffffu, cnt - 32 * k0 < nvalid)) {
 #pragma unroll
@@ -450,52 +464,56 @@ __global__ void __launch_bounds__(384, 1)
             for (int n = 0; n < 32; ++n) sr[0][n] = __float_as_uint(-INFINITY);
           }
         }
-        // tree maximum: eight independent partial maxima of 8 values each
-        float pm[8];
+        if constexpr ((kMod & kModBounded) == 0) {  // bounded scores take a maximum of 0 throughout
+          // tree maximum: eight independent partial maxima of 8 values each
+          float pm[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t* v = &sr[i >> 2][8 * (i & 3)];
-          float a = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-          a = fmax3(a, __uint_as_float(v[3]), __uint_as_float(v[4]));
-          a = fmax3(a, __uint_as_float(v[5]), __uint_as_float(v[6]));
-          pm[i] = fmaxf(a, __uint_as_float(v[7]));
-        }
-        const float mloc = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-        s_mx[g & 1u][half][row] = mloc;
-        named_bar_sync(pair_bar, 64);
-        const float mt = fmaxf(mloc, s_mx[g & 1u][half ^ 1][row]) * (kMod != 0 ? 1.f : sl2);
-        // lazy rescale: move the running max only when it grows by > 8 (log2 units)
-        const bool upd = mt > m + 8.0f;
-        const float alpha = upd ? ex2(m - mt) : 1.0f;
-        const bool need_o = upd && (m != -INFINITY) && (jl > 0);
-        if (upd) {
-          l *= alpha;
-          m = mt;
-        }
-        if (__any_sync(0xffffffffu, need_o)) {
-          // O must hold the previous tile's PV before it is rescaled.  Its
-          // buffer's s_free barrier is at most one phase behind (the PV before
-          // it on that buffer completed before this item's QK reused it), so a
-          // parity wait is exact there; a single barrier for all PVs is not.
-          if (!mbar_wait(&bar_s_free[(g - 1) % C::kSBufs], ((g - 1) / C::kSBufs) & 1u, &s_abort)) {
-            ok = false;
-            return;
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t* v = &sr[i >> 2][8 * (i & 3)];
+            float a = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            a = fmax3(a, __uint_as_float(v[3]), __uint_as_float(v[4]));
+            a = fmax3(a, __uint_as_float(v[5]), __uint_as_float(v[6]));
+            pm[i] = fmaxf(a, __uint_as_float(v[7]));
           }
-          tc_fence_after();
-          const float f = need_o ? alpha : 1.0f;
+          const float mloc = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+          s_mx[g & 1u][half][row] = mloc;
+          named_bar_sync(pair_bar, 64);
+          // scored: in log2 units already, except under masks alone
+          const float mt = fmaxf(mloc, s_mx[g & 1u][half ^ 1][row]) * (kMod == 0 || kMod == kScored ? sl2 : 1.f);
+          // lazy rescale: move the running max only when it grows by > 8 (log2 units)
+          const bool upd = mt > m + 8.0f;
+          const float alpha = upd ? ex2(m - mt) : 1.0f;
+          const bool need_o = upd && (m != -INFINITY) && (jl > 0);
+          if (upd) {
+            l *= alpha;
+            m = mt;
+          }
+          if (__any_sync(0xffffffffu, need_o)) {
+            // O must hold the previous tile's PV before it is rescaled.  Its
+            // buffer's s_free barrier is at most one phase behind (the PV before
+            // it on that buffer completed before this item's QK reused it), so a
+            // parity wait is exact there; a single barrier for all PVs is not.
+            if (!mbar_wait(&bar_s_free[(g - 1) % C::kSBufs], ((g - 1) / C::kSBufs) & 1u, &s_abort)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after();
+            const float f = need_o ? alpha : 1.0f;
 #pragma unroll 1
-          for (int k = 0; k < DH / 32; ++k) {
-            uint32_t o[32];
-            const uint32_t oc = tmem + lane_base + C::kColO + half * DH + 32 * k;
-            tmem_ld32(oc, o);
-            tmem_ld_wait(o);
+            for (int k = 0; k < DH / 32; ++k) {
+              uint32_t o[32];
+              const uint32_t oc = tmem + lane_base + C::kColO + half * DH + 32 * k;
+              tmem_ld32(oc, o);
+              tmem_ld_wait(o);
 #pragma unroll
-            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-            tmem_st32(oc, o);
+              for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+              tmem_st32(oc, o);
+            }
           }
         }
-        const float mm = (m == -INFINITY) ? 0.f : m;
-        // P = 2^(S scale_log2 - m): the scale-and-shift as packed pair FMAs,
+        const float mm = (kMod & kModBounded) != 0 || m == -INFINITY ? 0.f : m;
+        // P = 2^(S scale_log2 - m): the scale-and-shift as packed pair FMAs
+        // (scored: in log2 units already, except under masks alone),
         // the row sum in four packed accumulators (short dependency chains)
         float sa[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -504,11 +522,12 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-              float x0, x1;
-              if constexpr (kMod != 0)  // already in log2 units
-                fadd2(x0, x1, __uint_as_float(sr[kk][2 * n]), __uint_as_float(sr[kk][2 * n + 1]), -mm, -mm);
-              else
-                ffma2(x0, x1, __uint_as_float(sr[kk][2 * n]), __uint_as_float(sr[kk][2 * n + 1]), sl2, sl2, -mm, -mm);
+              const float s0 = __uint_as_float(sr[kk][2 * n]), s1 = __uint_as_float(sr[kk][2 * n + 1]);
+              float x0 = s0, x1 = s1;
+              if constexpr (kMod == 0 || kMod == kScored)
+                ffma2(x0, x1, s0, s1, sl2, sl2, -mm, -mm);
+              else if constexpr ((kMod & kModBounded) == 0)
+                fadd2(x0, x1, s0, s1, -mm, -mm);
               const float p0 = ex2(x0), p1 = ex2(x1);
               const int a = 2 * (n & 3);
               fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);

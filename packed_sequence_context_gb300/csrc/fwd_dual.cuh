@@ -374,10 +374,10 @@ __global__ void __launch_bounds__(384, 1)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
-        sc = score_consts<kMod>(p, it.h);
+        sc = score_consts<kMod, true>(p, it.h);
       }
       // ---- key tiles
-      float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
+      float m = (kMod & kModBounded) != 0 ? 0.f : -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
         if (!ok) return;
@@ -411,19 +411,33 @@ __global__ void __launch_bounds__(384, 1)
         // keys past the row's last visible one count as -inf; whole warps of
         // fully visible rows (every tile off the causal diagonal) skip the selects
         if constexpr (kMod != 0) {
+          const bool cut = __any_sync(0xffffffffu, cnt < 32 * nch || from > 0);
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
-          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          if constexpr (kMod != kScored) {
+            const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+            int form = kCapNear;
+            if constexpr ((kMod & kModCap) != 0) {
+              if (cut) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < nch)
-              score_run<kMod, false, 32, -1>(reinterpret_cast<float(&)[32]>(sr[k]), nullptr, sc,
-                                             (float)(ahead - 1 - 32 * k), abs_needed);
-          if (__any_sync(0xffffffffu, cnt < 32 * nch || from > 0)) {
+                for (int k = 0; k < 4; ++k)
+                  score_fill(reinterpret_cast<float(&)[32]>(sr[k]), from - 32 * k, cnt - 32 * k, 0.f);
+              }
+              float am = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < nch) am = fmaxf(am, score_abs_max(reinterpret_cast<float(&)[32]>(sr[k])));
+              form = cap_form(am, sc);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
+              if (k < nch)
+                score_run<kMod, -1>(reinterpret_cast<float(&)[32]>(sr[k]), sc, form, (float)(ahead - 1 - 32 * k),
+                                    abs_needed);
+          }
+          if (cut) {
 #pragma unroll
-              for (int n = 0; n < 32; ++n)
-                if (32 * k + n >= cnt || 32 * k + n < from) sr[k][n] = __float_as_uint(-INFINITY);
+            for (int k = 0; k < 4; ++k)
+              score_fill(reinterpret_cast<float(&)[32]>(sr[k]), from - 32 * k, cnt - 32 * k, -INFINITY);
           }
         } else if (__any_sync(0xffffffffu, cnt < 32 * nch)) {
 #pragma unroll
@@ -432,53 +446,60 @@ __global__ void __launch_bounds__(384, 1)
             for (int n = 0; n < 32; ++n)
               if (32 * k + n >= cnt) sr[k][n] = __float_as_uint(-INFINITY);
         }
-        // row maximum: per chunk four independent partial maxima of 8 values
-        float mloc = -INFINITY;
+        if constexpr ((kMod & kModBounded) == 0) {  // bounded scores take a maximum of 0 throughout
+          // row maximum: per chunk four independent partial maxima of 8 values
+          float mloc = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < nch) {
-            float pm[4];
+          for (int k = 0; k < 4; ++k) {
+            if (k < nch) {
+              float pm[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t* v = &sr[k][8 * i];
-              pm[i] = fmax3(fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])),
-                            fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5])),
-                            fmaxf(__uint_as_float(v[6]), __uint_as_float(v[7])));
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t* v = &sr[k][8 * i];
+                pm[i] = fmax3(fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])),
+                              fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5])),
+                              fmaxf(__uint_as_float(v[6]), __uint_as_float(v[7])));
+              }
+              mloc = fmax3(mloc, fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
             }
-            mloc = fmax3(mloc, fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
           }
-        }
-        const float mt = kMod != 0 ? mloc : mloc * sl2;
-        // lazy rescale: move the running max only when it grows by > 8 (log2 units)
-        const bool upd = mt > m + 8.0f;
-        const float alpha = upd ? ex2(m - mt) : 1.0f;
-        const bool need_o = upd && (m != -INFINITY) && (jl > 0);
-        if (upd) {
-          l *= alpha;
-          m = mt;
-        }
-        if (__any_sync(0xffffffffu, need_o)) {
-          // O holds the previous tile's PV: this tile's QK^T was issued only
-          // after it completed.  The wait on its s_free phase is exact (the
-          // next phase needs this warpgroup's P) and returns at once; it
-          // orders the TMEM accesses below after that PV.
-          if (!mbar_wait(&sb.s_free, (g - 1) & 1u, &s_abort)) {
-            ok = false;
-            return;
+          float mt;
+          if constexpr (kMod == 0 || kMod == kScored) {
+            mt = mloc * sl2;
+          } else {
+            mt = mloc;  // in log2 units already
           }
-          tc_fence_after();
-          const float f = need_o ? alpha : 1.0f;
+          // lazy rescale: move the running max only when it grows by > 8 (log2 units)
+          const bool upd = mt > m + 8.0f;
+          const float alpha = upd ? ex2(m - mt) : 1.0f;
+          const bool need_o = upd && (m != -INFINITY) && (jl > 0);
+          if (upd) {
+            l *= alpha;
+            m = mt;
+          }
+          if (__any_sync(0xffffffffu, need_o)) {
+            // O holds the previous tile's PV: this tile's QK^T was issued only
+            // after it completed.  The wait on its s_free phase is exact (the
+            // next phase needs this warpgroup's P) and returns at once; it
+            // orders the TMEM accesses below after that PV.
+            if (!mbar_wait(&sb.s_free, (g - 1) & 1u, &s_abort)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after();
+            const float f = need_o ? alpha : 1.0f;
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld32(o_col + 32 * k, o);
-            tmem_ld_wait(o);
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[32];
+              tmem_ld32(o_col + 32 * k, o);
+              tmem_ld_wait(o);
 #pragma unroll
-            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-            tmem_st32(o_col + 32 * k, o);
+              for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+              tmem_st32(o_col + 32 * k, o);
+            }
           }
         }
-        const float mm = (m == -INFINITY) ? 0.f : m;
+        const float mm = (kMod & kModBounded) != 0 || m == -INFINITY ? 0.f : m;
         // P = 2^(S scale_log2 - m): the scale-and-shift as packed pair FMAs,
         // the row sum in four packed accumulators (short dependency chains);
         // packed P of key columns [32 k, 32 k + 32) goes to TMEM columns
@@ -490,11 +511,12 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-              float x0, x1;
-              if constexpr (kMod != 0)  // already in log2 units
-                fadd2(x0, x1, __uint_as_float(sr[k][2 * n]), __uint_as_float(sr[k][2 * n + 1]), -mm, -mm);
-              else
-                ffma2(x0, x1, __uint_as_float(sr[k][2 * n]), __uint_as_float(sr[k][2 * n + 1]), sl2, sl2, -mm, -mm);
+              const float s0 = __uint_as_float(sr[k][2 * n]), s1 = __uint_as_float(sr[k][2 * n + 1]);
+              float x0 = s0, x1 = s1;
+              if constexpr (kMod == 0 || kMod == kScored)
+                ffma2(x0, x1, s0, s1, sl2, sl2, -mm, -mm);
+              else if constexpr ((kMod & kModBounded) == 0)
+                fadd2(x0, x1, s0, s1, -mm, -mm);
               const float p0 = ex2(x0), p1 = ex2(x1);
               const int a = 2 * (n & 3);
               fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);

@@ -5,12 +5,19 @@
 //   y -= slope |i' - j|                         (i' = i + koff: the key position a query sits at)
 // in log2 units (y log2(e)), as the softmax takes them.
 //
-// tanh u = 1 - 2 r, r = 1 / (1 + e^(2u)): one 2^x and one reciprocal, exact to
-// fp32 rounding in absolute terms (softcap 2^-22; the hardware's one-step tanh
-// is off by 2^-11, 0.02 at a cap of 50).  Two scores share a reciprocal:
-// 1/a = b / (ab), 1/b = a / (ab), with the exponents held to 2^60 so that ab
-// stays finite (tanh is 1 to the last bit long before).  The derivative is
-// 1 - tanh^2 = 4 r (1 - r).
+// tanh, chosen per warp and run of scores by the largest |x| of the run:
+//   s times a polynomial in s^2, a relative minimax fit of tanh(u) / u derived
+//     by exchange on the interval: three terms for |x| <= softcap / 4 (relative
+//     error 4.0e-7), five for |x| <= 0.75 softcap (5.7e-7);
+//   else 1 - 2 r, r = 1 / (1 + e^(2u)): one 2^x and one reciprocal, shared by
+//     two scores (1/a = b / (ab), 1/b = a / (ab), with exponents held to 2^60
+//     so that ab stays finite; tanh is 1 to the last bit long before).
+// All are exact to fp32 rounding in absolute terms (about softcap 2^-21; the
+// hardware's one-step tanh is off by 2^-11, 0.02 at a cap of 50).  What a run
+// costs, from a loop of the softmax's steps with two warps per scheduler, in
+// cycles per 32 scores: no cap 4.8, three terms 7.0, five 9.6, the reciprocal
+// 13.1 -- the softmax's 2^x alone is 4 of them, so the polynomials, which take
+// only multiply-adds, run beside it.
 //
 // The bias is linear in j on either side of i', so a row that sees only keys
 // up to its own position (every causal row without a prefix) takes one fused
@@ -28,8 +35,78 @@ THD_DEV float rcp(float x) {
   return y;
 }
 
-// r = 1 / (1 + 2^(c s)) of two scores
-THD_DEV void cap_pair(float& r0, float& r1, float s0, float s1, float c) {
+struct ScoreConsts {
+  float sl2;       // softmax_scale log2(e)
+  float cap_a;     // softcap log2(e)
+  float cap_c;     // 2 log2(e) softmax_scale / softcap
+  float cap_n[3], cap_near;  // tanh = s (n0 + n1 s^2 + ..) while |s| <= cap_near; kScaled: times cap_a
+  float cap_f[5], cap_far;
+  float slope;  // the head's slope log2(e)
+};
+template <int kMod, bool kScaled, class P>
+THD_DEV ScoreConsts score_consts(const P& p, int h) {
+  ScoreConsts k;
+  k.sl2 = p.scale_log2;
+  k.cap_a = p.mods.cap_a;
+  k.cap_c = p.mods.cap_c;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) k.cap_n[i] = p.mods.cap_n[i] * (kScaled ? k.cap_a : 1.f);
+#pragma unroll
+  for (int i = 0; i < 5; ++i) k.cap_f[i] = p.mods.cap_f[i] * (kScaled ? k.cap_a : 1.f);
+  k.cap_near = p.mods.cap_near;
+  k.cap_far = p.mods.cap_far;
+  k.slope = 0.f;
+  if constexpr ((kMod & kModDist) != 0) k.slope = p.mods.slopes[h] * 1.4426950408889634f;
+  return k;
+}
+
+// The largest |s| of a thread's scores.
+template <int N>
+THD_DEV float score_abs_max(const float (&s)[N]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < N; n += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], fabsf(s[n + 2 * i]), fabsf(s[n + 2 * i + 1]));
+  return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+
+// The scores outside [from, to) become v.  Runs with masked columns set those
+// to 0 before the largest |s| is taken: a masked score, or a column that no
+// product wrote, must not choose the form (results stay reproducible).
+template <int N>
+THD_DEV void score_fill(float (&s)[N], int from, int to, float v) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (n < from || n >= to) s[n] = v;
+}
+
+// Which form of tanh the warp's run takes, by the largest |s| of each thread
+// (a NaN among the scores may pass for small: it stays a NaN in every form).
+constexpr int kCapNear = 0, kCapFar = 1, kCapWide = 2;
+THD_DEV int cap_form(float abs_max, const ScoreConsts& k) {
+  if (__all_sync(0xffffffffu, abs_max <= k.cap_near)) return kCapNear;
+  return __all_sync(0xffffffffu, abs_max <= k.cap_far) ? kCapFar : kCapWide;
+}
+
+// The polynomial's value at two scores: tanh = s times it.
+template <int kForm>
+THD_DEV void cap_poly(float& q0, float& q1, float s0, float s1, const ScoreConsts& k) {
+  float w0, w1;
+  fmul2(w0, w1, s0, s1, s0, s1);
+  if constexpr (kForm == kCapNear) {
+    ffma2(q0, q1, w0, w1, k.cap_n[2], k.cap_n[2], k.cap_n[1], k.cap_n[1]);
+    ffma2(q0, q1, w0, w1, q0, q1, k.cap_n[0], k.cap_n[0]);
+  } else {
+    ffma2(q0, q1, w0, w1, k.cap_f[4], k.cap_f[4], k.cap_f[3], k.cap_f[3]);
+    ffma2(q0, q1, w0, w1, q0, q1, k.cap_f[2], k.cap_f[2]);
+    ffma2(q0, q1, w0, w1, q0, q1, k.cap_f[1], k.cap_f[1]);
+    ffma2(q0, q1, w0, w1, q0, q1, k.cap_f[0], k.cap_f[0]);
+  }
+}
+
+// r = 1 / (1 + 2^(c s)) of two scores: tanh = 1 - 2 r.
+THD_DEV void cap_wide(float& r0, float& r1, float s0, float s1, float c) {
   float x0, x1, a0, a1;
   fmul2(x0, x1, s0, s1, c, c);
   fadd2(a0, a1, ex2(fminf(x0, 60.f)), ex2(fminf(x1, 60.f)), 1.f, 1.f);
@@ -37,70 +114,107 @@ THD_DEV void cap_pair(float& r0, float& r1, float s0, float s1, float c) {
   fmul2(r0, r1, q, q, a1, a0);
 }
 
-struct ScoreConsts {
-  float sl2;    // softmax_scale log2(e)
-  float cap_a;  // softcap log2(e)
-  float cap_c;
-  float slope;  // the head's slope log2(e)
-};
-template <int kMod, class P>
-THD_DEV ScoreConsts score_consts(const P& p, int h) {
-  ScoreConsts k;
-  k.sl2 = p.scale_log2;
-  k.cap_a = p.mods.cap_a;
-  k.cap_c = p.mods.cap_c;
-  k.slope = 0.f;
-  if constexpr ((kMod & kModDist) != 0) k.slope = p.mods.slopes[h] * 1.4426950408889634f;
-  return k;
-}
-
-// One thread's N scores (N even), in place: s[n] becomes y log2(e).  d0 = i' - j
-// of the first one and dir = -1 (the scores run along j) or +1 (along i'), so
-// score n sits at distance |d0 + dir n|; `abs_needed` (uniform over the warp):
-// some visible score has i' < j.  With kGrad, w[n] = 1 - tanh^2.
-template <int kMod, bool kGrad, int N, int kDir>
-THD_DEV void score_run(float (&s)[N], float* w, const ScoreConsts& k, float d0, bool abs_needed) {
-  constexpr bool kCap = (kMod & kModCap) != 0, kDist = (kMod & kModDist) != 0;
-  const float base = kDist ? -k.slope * d0 : 0.f;   // bias of score 0, linear side
-  const float step = kDist ? -k.slope * kDir : 0.f;  // and what each score adds
-  if (kDist && abs_needed) {
-#pragma unroll
-    for (int n = 0; n < N; n += 2) {
-      float b0 = -k.slope * fabsf(d0 + kDir * n), b1 = -k.slope * fabsf(d0 + kDir * (n + 1));
-      if constexpr (kCap) {
-        float r0, r1;
-        cap_pair(r0, r1, s[n], s[n + 1], k.cap_c);
-        if constexpr (kGrad) {
-          w[n] = 4.f * r0 * (1.f - r0);
-          w[n + 1] = 4.f * r1 * (1.f - r1);
-        }
-        ffma2(s[n], s[n + 1], r0, r1, -2.f * k.cap_a, -2.f * k.cap_a, b0 + k.cap_a, b1 + k.cap_a);
-      } else {
-        ffma2(s[n], s[n + 1], s[n], s[n + 1], k.sl2, k.sl2, b0, b1);
-      }
-    }
-    return;
+// A run's bias: score n has b(n) = -slope |d0 + dir n|, dir = -1 where the
+// scores run along j and +1 along i'.  kAbs: some score sits past its own
+// position; else b(n) = base + step n.
+template <int kDir, bool kAbs>
+struct BiasRun {
+  float d0, slope, base, step;
+  THD_DEV BiasRun(float d0_, float slope_, float top) : d0(d0_), slope(slope_) {
+    base = kAbs ? top : top - slope_ * d0_;
+    step = -slope_ * kDir;
   }
-  const float top = kCap ? base + k.cap_a : base;
+  THD_DEV void at(int n, float& b0, float& b1) const {
+    if constexpr (kAbs) {
+      b0 = fmaf(-slope, fabsf(d0 + kDir * n), base);
+      b1 = fmaf(-slope, fabsf(d0 + kDir * (n + 1)), base);
+    } else {
+      ffma2(b0, b1, step, step, (float)n, (float)(n + 1), base, base);
+    }
+  }
+};
+
+// One thread's N scores, in place: s[n] becomes a s[n] + b(n) + top.
+template <int kDir, bool kAbs, int N>
+THD_DEV void bias_run(float (&s)[N], float a, float d0, float slope, float top) {
+  const BiasRun<kDir, kAbs> b(d0, slope, top);
 #pragma unroll
   for (int n = 0; n < N; n += 2) {
-    float b0 = top, b1 = top;
-    if constexpr (kDist) ffma2(b0, b1, step, step, (float)n, (float)(n + 1), top, top);
-    if constexpr (kCap) {
-      float r0, r1;
-      cap_pair(r0, r1, s[n], s[n + 1], k.cap_c);
-      if constexpr (kGrad) {
-        float t0, t1;
-        fmul2(t0, t1, r0, r1, 4.f, 4.f);
-        ffma2(w[n], w[n + 1], -t0, -t1, r0, r1, t0, t1);
-      }
-      ffma2(s[n], s[n + 1], r0, r1, -2.f * k.cap_a, -2.f * k.cap_a, b0, b1);
-    } else if constexpr (kDist) {
-      ffma2(s[n], s[n + 1], s[n], s[n + 1], k.sl2, k.sl2, b0, b1);
+    float b0, b1;
+    b.at(n, b0, b1);
+    ffma2(s[n], s[n + 1], s[n], s[n + 1], a, a, b0, b1);
+  }
+}
+
+// Scores times the polynomial, plus the linear side's bias.
+template <int kForm, int kDir, bool kDist, int N>
+THD_DEV void poly_run(float (&s)[N], const ScoreConsts& k, float d0) {
+  const BiasRun<kDir, false> b(d0, k.slope, 0.f);
+#pragma unroll
+  for (int n = 0; n < N; n += 2) {
+    float q0, q1;
+    cap_poly<kForm>(q0, q1, s[n], s[n + 1], k);
+    if constexpr (kDist) {
+      float b0, b1;
+      b.at(n, b0, b1);
+      ffma2(s[n], s[n + 1], s[n], s[n + 1], q0, q1, b0, b1);
     } else {
-      fmul2(s[n], s[n + 1], s[n], s[n + 1], k.sl2, k.sl2);
+      fmul2(s[n], s[n + 1], s[n], s[n + 1], q0, q1);
     }
   }
+}
+// top (1 - 2 r)
+template <int N>
+THD_DEV void wide_run(float (&s)[N], const ScoreConsts& k, float top) {
+#pragma unroll
+  for (int n = 0; n < N; n += 2) {
+    float r0, r1;
+    cap_wide(r0, r1, s[n], s[n + 1], k.cap_c);
+    ffma2(s[n], s[n + 1], r0, r1, -2.f * top, -2.f * top, top, top);
+  }
+}
+
+// Forward: one thread's N scores become y log2(e), in place (coefficients
+// scaled by cap_a).  d0 and abs_needed as in BiasRun (abs_needed uniform over
+// the warp).
+template <int kMod, int kDir, int N>
+THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, int form, float d0, bool abs_needed) {
+  constexpr bool kCap = (kMod & kModCap) != 0, kDist = (kMod & kModDist) != 0;
+  if constexpr (kCap) {
+    if (kDist && !abs_needed && form != kCapWide) {  // cap and bias in one go
+      if (form == kCapNear)
+        poly_run<kCapNear, kDir, true>(s, k, d0);
+      else
+        poly_run<kCapFar, kDir, true>(s, k, d0);
+      return;
+    }
+    if (form == kCapNear)
+      poly_run<kCapNear, kDir, false>(s, k, 0.f);
+    else if (form == kCapFar)
+      poly_run<kCapFar, kDir, false>(s, k, 0.f);
+    else
+      wide_run(s, k, k.cap_a);
+  }
+  if constexpr (kDist) {
+    const float a = kCap ? 1.f : k.sl2;
+    if (abs_needed)
+      bias_run<kDir, true>(s, a, d0, k.slope, 0.f);
+    else
+      bias_run<kDir, false>(s, a, d0, k.slope, 0.f);
+  }
+}
+
+// Backward: one thread's N scores become tanh, in place (coefficients
+// unscaled).
+template <int N>
+THD_DEV void tanh_run(float (&s)[N], const ScoreConsts& k) {
+  const int form = cap_form(score_abs_max(s), k);
+  if (form == kCapNear)
+    poly_run<kCapNear, 1, false>(s, k, 0.f);
+  else if (form == kCapFar)
+    poly_run<kCapFar, 1, false>(s, k, 0.f);
+  else
+    wide_run(s, k, 1.f);
 }
 
 }  // namespace thd
