@@ -53,6 +53,10 @@ struct BwdCfg {
   static_assert(256 * kComputeRegs + 128 * kOtherRegs <= 384 * 168, "register split above the launch budget");
 };
 
+// Whether the kernel runs 384 threads with a register split: entry-major, and
+// with scores whose function needs the registers.
+__host__ __device__ constexpr bool bwd_split(bool grouped, int mod) { return !grouped || (mod & ~kScored) != 0; }
+
 struct BwdItem {
   SeqGeom g;
   int b, c, jk, hk;
@@ -126,10 +130,11 @@ __device__ inline void drain_wait_b(uint64_t* bar, uint32_t parity) {
 }
 
 template <int D, bool kGrouped, int kMod>
-__global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
+__global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
     bwd_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = BwdCfg<D>;
+  constexpr bool kSplit = bwd_split(kGrouped, kMod);
   constexpr int S = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem + C::kOffK;
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
     // The compute warps hold a step's P (64 values) and S^T / dP^T chunks per
     // thread: they get 200 registers, warps 8-11 (producer, issuers, idle) 96;
     // 256 x 200 + 128 x 96 fits the 384 x 168 the CTA is launched with.
-    if constexpr (!kGrouped) regs_lower<C::kOtherRegs>();
+    if constexpr (kSplit) regs_lower<C::kOtherRegs>();
     if (warp == 8) {
       // ------------------------------------------------------------ producer (whole warp)
       int stage = 0;
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
       __syncwarp();
     }
   } else {
-    if constexpr (!kGrouped) regs_raise<C::kComputeRegs>();
+    if constexpr (kSplit) regs_raise<C::kComputeRegs>();
     // ------------------------------------------------------------ compute warps
     const int half = warp >> 2;     // which half of the columns this thread owns
     const int row = tid & 127;      // its key row (TMEM lane) / query row when draining dQ
@@ -478,6 +483,7 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
     // the epilogue stores whole 32-byte sectors (the API asks for 16)
     const bool v8_ok = ((reinterpret_cast<uintptr_t>(p.dk) | reinterpret_cast<uintptr_t>(p.dv)) & 31u) == 0;
     uint32_t su = 0, n_done = 0;
+    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w;
@@ -533,89 +539,130 @@ __global__ void __launch_bounds__(kGrouped ? 352 : 384, 1)
         // columns outside [n_lo, n_hi) -- causal, or past the valid rows -- get
         // S = -inf, hence P = 0 and dS = 0); packed P^T goes back over S^T
         float pv[2][32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int kk = 2 * half + i;
-          if (kk < nch) {
-            uint32_t sr[32];
+        if constexpr (kMod != 0) {
+          // P in place over the scores and, for dS, P (1 - tanh^2); then 0 in the
+          // columns that do not see this key, whatever stood there
+          constexpr bool kCap = (kMod & kModCap) != 0;
+          uint32_t pk[2][16];
+          // chunk kk of S^T, with the cap's masked columns at 0; true if any is masked
+          auto load = [&](float(&y)[32], int kk) {
+            uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
             tmem_ld32(acol + 32 * kk, sr);
             tmem_ld_wait(sr);
             const bool cut = __any_sync(0xffffffffu, n_lo > 32 * kk || n_hi < 32 * kk + 32);
-            uint32_t pk[16];
-            if constexpr (kMod != 0) {
-              // P in place over the scores and, for dS, P (1 - tanh^2); then 0
-              // in the columns that do not see this key, whatever stood there
-              constexpr bool kCap = (kMod & kModCap) != 0;
-              float(&y)[32] = reinterpret_cast<float(&)[32]>(sr);
-              if constexpr (kCap) {
-                if (cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-                tanh_run(y, sc);
+            if (kCap && cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+            return cut;
+          };
+          auto measure = [&]() {
+            float am = 0.f, y[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (2 * half + i < nch) {
+                load(y, 2 * half + i);
+                am = fmaxf(am, score_abs_max(y));
               }
-              const float a = kCap ? sc.cap_a : sl2;
-              auto write_p = [&](auto bias) {
+            }
+            return cap_form(am, sc);
+          };
+          auto run = [&](auto form) {
+            float am = 0.f;
 #pragma unroll
-                for (int q4 = 0; q4 < 8; ++q4) {
-                  const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
-                  const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                  for (int e = 0; e < 4; e += 2) {
-                    const int n = 4 * q4 + e;
-                    float x0, x1, b0 = -l[e], b1 = -l[e + 1];
-                    if constexpr ((kMod & kModDist) != 0) {
-                      float c0, c1;
-                      bias.at(n, c0, c1);
-                      fadd2(b0, b1, b0, b1, c0, c1);
-                    }
-                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
-                    x0 = ex2(x0);
-                    x1 = ex2(x1);
-                    if constexpr (kCap) {
-                      float w0, w1;
-                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
-                      fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
-                    } else {
-                      pv[i][n] = x0, pv[i][n + 1] = x1;
-                    }
-                    y[n] = x0, y[n + 1] = x1;
-                  }
+            for (int i = 0; i < 2; ++i) {
+              const int kk = 2 * half + i;
+              if (kk < nch) {
+                float y[32];
+                const bool cut = load(y, kk);
+                if constexpr (kCap) {
+                  am = fmaxf(am, score_abs_max(y));
+                  cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f);
                 }
-              };
-              if ((kMod & kModDist) != 0 && abs_needed)
-                write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
-              else
-                write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
+                const float a = kCap ? sc.cap_a : sl2;
+                auto write_p = [&](auto bias) {
+#pragma unroll
+                  for (int q4 = 0; q4 < 8; ++q4) {
+                    const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
+                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                      const int n = 4 * q4 + e;
+                      float x0, x1, b0 = -l[e], b1 = -l[e + 1];
+                      if constexpr ((kMod & kModDist) != 0) {
+                        float c0, c1;
+                        bias.at(n, c0, c1);
+                        fadd2(b0, b1, b0, b1, c0, c1);
+                      }
+                      ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                      x0 = ex2(x0);
+                      x1 = ex2(x1);
+                      if constexpr (kCap) {
+                        float w0, w1;
+                        ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                        fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
+                      } else {
+                        pv[i][n] = x0, pv[i][n + 1] = x1;
+                      }
+                      y[n] = x0, y[n + 1] = x1;
+                    }
+                  }
+                };
+                if ((kMod & kModDist) != 0 && abs_needed)
+                  write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
+                else
+                  write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
+                if (cut) {
+                  score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+                  score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+                }
+#pragma unroll
+                for (int n = 0; n < 16; ++n) pk[i][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+                // over columns already read, where plain P^T goes (below)
+                if (!kCap) tmem_st16(acol + 64 * half + 16 * i, pk[i]);
+              }
+            }
+            return kCap ? cap_form(am, sc) : kCapNear;
+          };
+          if constexpr (kCap) {
+            cap_with_hint(hint, measure, run);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (2 * half + i < nch) tmem_st16(acol + 64 * half + 16 * i, pk[i]);
+          } else {
+            run(CapForm<kCapNear>{});
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int kk = 2 * half + i;
+            if (kk < nch) {
+              uint32_t sr[32];
+              tmem_ld32(acol + 32 * kk, sr);
+              tmem_ld_wait(sr);
+              const bool cut = __any_sync(0xffffffffu, n_lo > 32 * kk || n_hi < 32 * kk + 32);
+              uint32_t pk[16];
               if (cut) {
-                score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-                score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int n = 32 * kk + e;
+                  if (n < n_lo || n >= n_hi) sr[e] = __float_as_uint(-INFINITY);
+                }
               }
 #pragma unroll
-              for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+              for (int q4 = 0; q4 < 8; ++q4) {
+                const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
+                float x0, x1, x2, x3;
+                ffma2(x0, x1, __uint_as_float(sr[4 * q4]), __uint_as_float(sr[4 * q4 + 1]), sl2, sl2, -l4.x, -l4.y);
+                ffma2(x2, x3, __uint_as_float(sr[4 * q4 + 2]), __uint_as_float(sr[4 * q4 + 3]), sl2, sl2, -l4.z, -l4.w);
+                pv[i][4 * q4] = ex2(x0);
+                pv[i][4 * q4 + 1] = ex2(x1);
+                pv[i][4 * q4 + 2] = ex2(x2);
+                pv[i][4 * q4 + 3] = ex2(x3);
+                pk[2 * q4] = pack_bf16x2(pv[i][4 * q4], pv[i][4 * q4 + 1]);
+                pk[2 * q4 + 1] = pack_bf16x2(pv[i][4 * q4 + 2], pv[i][4 * q4 + 3]);
+              }
+              // packed P^T stays inside this warpgroup's own S^T columns (the other
+              // warpgroup may still be reading its half): chunk kk -> 64 (kk/2) + 16 (kk%2)
               tmem_st16(acol + 64 * (kk >> 1) + 16 * (kk & 1), pk);
-              continue;
             }
-            if (cut) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int n = 32 * kk + e;
-                if (n < n_lo || n >= n_hi) sr[e] = __float_as_uint(-INFINITY);
-              }
-            }
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-              const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
-              float x0, x1, x2, x3;
-              ffma2(x0, x1, __uint_as_float(sr[4 * q4]), __uint_as_float(sr[4 * q4 + 1]), sl2, sl2, -l4.x, -l4.y);
-              ffma2(x2, x3, __uint_as_float(sr[4 * q4 + 2]), __uint_as_float(sr[4 * q4 + 3]), sl2, sl2, -l4.z, -l4.w);
-              pv[i][4 * q4] = ex2(x0);
-              pv[i][4 * q4 + 1] = ex2(x1);
-              pv[i][4 * q4 + 2] = ex2(x2);
-              pv[i][4 * q4 + 3] = ex2(x3);
-              pk[2 * q4] = pack_bf16x2(pv[i][4 * q4], pv[i][4 * q4 + 1]);
-              pk[2 * q4 + 1] = pack_bf16x2(pv[i][4 * q4 + 2], pv[i][4 * q4 + 3]);
-            }
-            // packed P^T stays inside this warpgroup's own S^T columns (the other
-            // warpgroup may still be reading its half): chunk kk -> 64 (kk/2) + 16 (kk%2)
-            tmem_st16(acol + 64 * (kk >> 1) + 16 * (kk & 1), pk);
           }
         }
         // ---- dS = P (dP^T - Delta), once dP^T is in TMEM; the buffer is
@@ -747,7 +794,7 @@ static cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const
   cudaError_t e = cudaFuncSetAttribute(bwd_kernel<D, kGrouped, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   prof_before(THD_KERNEL_BWD, st);
-  bwd_kernel<D, kGrouped, kMod><<<grid, kGrouped ? 352 : 384, C::kSmem, st>>>(p, tq, tdo, tk, tv);
+  bwd_kernel<D, kGrouped, kMod><<<grid, bwd_split(kGrouped, kMod) ? 384 : 352, C::kSmem, st>>>(p, tq, tdo, tk, tv);
   count_launch();
   e = cudaGetLastError();
   prof_after(THD_KERNEL_BWD, st);

@@ -63,6 +63,8 @@ template <int D, bool kGrouped, int kMod>
 __global__ void __launch_bounds__(384, 1)
     dq_kernel(const DqParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = DqCfg<D>;
+  // the register split also carries the longer dS of capped scores
+  constexpr bool kSplit = !kGrouped || (kMod & kModCap) != 0;
   constexpr int KS = C::kKStages, VS = C::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(384, 1)
   if (p.test_stall) {
     mbar_wait(&bar_drain, 0, &s_abort);
   } else if (warp >= 8) {
-    if constexpr (!kGrouped) regs_lower<C::kOtherRegs>();
+    if constexpr (kSplit) regs_lower<C::kOtherRegs>();
     if (warp == 8) {
       // ------------------------------------------------------------ Q, dO and K producer (whole warp)
       int ks = 0;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     }
   } else {
-    if constexpr (!kGrouped) regs_raise<C::kComputeRegs>();
+    if constexpr (kSplit) regs_raise<C::kComputeRegs>();
     // ------------------------------------------------------------ dS + epilogue
     // Thread (half, row) owns query row `row` (its TMEM lane) and key columns
     // [64 half, 64 half + 64) of every tile, plus head-dim columns
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(384, 1)
     // dQ rows start at multiples of 128 bytes: 32-byte stores when dQ is 32-byte aligned
     const bool dq_v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
     uint32_t g = 0, n_item = 0;
+    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w;
@@ -459,69 +462,109 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_dp_free);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const int ch = 2 * half + kk;  // this thread's 32-column chunk
-          if (ch < nch) {
-            uint32_t sr[32];
+        if constexpr (kMod != 0) {
+          // dS = P (dP - Delta) (1 - tanh^2), in place over the scores; then 0 on
+          // the keys this row may not see, whatever stood there
+          constexpr bool kCap = (kMod & kModCap) != 0;
+          uint32_t pk[2][16];
+          // chunk ch of S, with the cap's masked columns at 0; true if any is masked
+          auto load = [&](float(&y)[32], int ch) {
+            uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
             tmem_ld32(scol + 32 * ch, sr);
             tmem_ld_wait(sr);
-            uint32_t pk[16];
-            if constexpr (kMod != 0) {
-              // dS = P (dP - Delta) (1 - tanh^2), in place over the scores; then
-              // 0 on the keys this row may not see, whatever stood there
-              constexpr bool kCap = (kMod & kModCap) != 0;
-              float(&y)[32] = reinterpret_cast<float(&)[32]>(sr);
-              const bool cut = __any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch);
-              if constexpr (kCap) {
-                if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
-                tanh_run(y, sc);
+            const bool cut = __any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch);
+            if (kCap && cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+            return cut;
+          };
+          auto measure = [&]() {
+            float am = 0.f, y[32];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              if (2 * half + kk < nch) {
+                load(y, 2 * half + kk);
+                am = fmaxf(am, score_abs_max(y));
               }
-              const float a = kCap ? sc.cap_a : sl2;
-              auto write_ds = [&](auto bias) {
+            }
+            return cap_form(am, sc);
+          };
+          auto run = [&](auto form) {
+            float am = 0.f;
 #pragma unroll
-                for (int n = 0; n < 32; n += 2) {
-                  float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
-                  if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
-                  ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
-                  fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
-                  if constexpr (kCap) {
-                    float w0, w1;
-                    ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
-                    fmul2(t0, t1, t0, t1, w0, w1);
-                  }
-                  fmul2(y[n], y[n + 1], ex2(x0), ex2(x1), t0, t1);
+            for (int kk = 0; kk < 2; ++kk) {
+              const int ch = 2 * half + kk;  // this thread's 32-column chunk
+              if (ch < nch) {
+                float y[32];
+                const bool cut = load(y, ch);
+                if constexpr (kCap) {
+                  am = fmaxf(am, score_abs_max(y));
+                  cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f);
                 }
-              };
-              const float d0 = (float)(ahead - 1 - 32 * ch);
-              if ((kMod & kModDist) != 0 && abs_needed)
-                write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
-              else
-                write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
-              if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+                const float a = kCap ? sc.cap_a : sl2;
+                auto write_ds = [&](auto bias) {
 #pragma unroll
-              for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+                  for (int n = 0; n < 32; n += 2) {
+                    float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
+                    if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
+                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                    fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
+                    if constexpr (kCap) {
+                      float w0, w1;
+                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                      fmul2(t0, t1, t0, t1, w0, w1);
+                    }
+                    fmul2(y[n], y[n + 1], ex2(x0), ex2(x1), t0, t1);
+                  }
+                };
+                const float d0 = (float)(ahead - 1 - 32 * ch);
+                if ((kMod & kModDist) != 0 && abs_needed)
+                  write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
+                else
+                  write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
+                if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+                // over columns already read, where plain dS goes (below)
+                if (!kCap) tmem_st16(scol + 64 * half + 16 * kk, pk[kk]);
+              }
+            }
+            return kCap ? cap_form(am, sc) : kCapNear;
+          };
+          if constexpr (kCap) {
+            cap_with_hint(hint, measure, run);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              if (2 * half + kk < nch) tmem_st16(scol + 64 * half + 16 * kk, pk[kk]);
+          } else {
+            run(CapForm<kCapNear>{});
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const int ch = 2 * half + kk;  // this thread's 32-column chunk
+            if (ch < nch) {
+              uint32_t sr[32];
+              tmem_ld32(scol + 32 * ch, sr);
+              tmem_ld_wait(sr);
+              // keys this row may not see get S = -inf: P = 0 and dS = 0
+              if (__any_sync(0xffffffffu, cnt < 32 * ch + 32)) {
+#pragma unroll
+                for (int n = 0; n < 32; ++n)
+                  if (32 * ch + n >= cnt) sr[n] = __float_as_uint(-INFINITY);
+              }
+              uint32_t pk[16];
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                float x0, x1, t0, t1, g0, g1;
+                ffma2(x0, x1, __uint_as_float(sr[2 * n]), __uint_as_float(sr[2 * n + 1]), sl2, sl2, -lse2, -lse2);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                fadd2(t0, t1, __uint_as_float(dr[kk][2 * n]), __uint_as_float(dr[kk][2 * n + 1]), -dlt, -dlt);
+                fmul2(g0, g1, p0, p1, t0, t1);
+                pk[n] = pack_bf16x2(g0, g1);
+              }
+              // packed dS stays inside this half's own S columns (the other
+              // warpgroup may still be reading its half): chunk ch -> 64 (ch/2) + 16 (ch%2)
               tmem_st16(scol + 64 * (ch >> 1) + 16 * (ch & 1), pk);
-              continue;
             }
-            // keys this row may not see get S = -inf: P = 0 and dS = 0
-            if (__any_sync(0xffffffffu, cnt < 32 * ch + 32)) {
-#pragma unroll
-              for (int n = 0; n < 32; ++n)
-                if (32 * ch + n >= cnt) sr[n] = __float_as_uint(-INFINITY);
-            }
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              float x0, x1, t0, t1, g0, g1;
-              ffma2(x0, x1, __uint_as_float(sr[2 * n]), __uint_as_float(sr[2 * n + 1]), sl2, sl2, -lse2, -lse2);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              fadd2(t0, t1, __uint_as_float(dr[kk][2 * n]), __uint_as_float(dr[kk][2 * n + 1]), -dlt, -dlt);
-              fmul2(g0, g1, p0, p1, t0, t1);
-              pk[n] = pack_bf16x2(g0, g1);
-            }
-            // packed dS stays inside this half's own S columns (the other
-            // warpgroup may still be reading its half): chunk ch -> 64 (ch/2) + 16 (ch%2)
-            tmem_st16(scol + 64 * (ch >> 1) + 16 * (ch & 1), pk);
           }
         }
         tmem_st_wait();

@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(384, 1)
     // O rows start at multiples of 128 bytes: 32-byte stores when O is 32-byte aligned
     const bool o_v8 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     uint32_t g = 0;
+    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w = 0;
@@ -402,12 +403,15 @@ __global__ void __launch_bounds__(384, 1)
         const int ncols = q_tile_ncols<kMod>(it, p, c, j);  // the N this tile's QK^T computed
         const int nch = ceil_div(ncols, 32);          // 32-column chunks holding S
         uint32_t sr[4][32];
+        auto load = [&]() {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < nch) tmem_ld32(s_col + 32 * k, sr[k]);
+          for (int k = 0; k < 4; ++k)
+            if (k < nch) tmem_ld32(s_col + 32 * k, sr[k]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < nch) tmem_ld_wait(sr[k]);
+          for (int k = 0; k < 4; ++k)
+            if (k < nch) tmem_ld_wait(sr[k]);
+        };
+        if constexpr ((kMod & kModCap) == 0) load();
         // keys past the row's last visible one count as -inf; whole warps of
         // fully visible rows (every tile off the causal diagonal) skip the selects
         if constexpr (kMod != 0) {
@@ -415,24 +419,35 @@ __global__ void __launch_bounds__(384, 1)
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
           if constexpr (kMod != kScored) {
             const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
-            int form = kCapNear;
-            if constexpr ((kMod & kModCap) != 0) {
-              if (cut) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  score_fill(reinterpret_cast<float(&)[32]>(sr[k]), from - 32 * k, cnt - 32 * k, 0.f);
-              }
-              float am = 0.f;
+            auto score = [&](auto form) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (k < nch) am = fmaxf(am, score_abs_max(reinterpret_cast<float(&)[32]>(sr[k])));
-              form = cap_form(am, sc);
-            }
+                if (k < nch)
+                  score_run<kMod, decltype(form)::value, -1>(reinterpret_cast<float(&)[32]>(sr[k]), sc,
+                                                             (float)(ahead - 1 - 32 * k), abs_needed);
+            };
+            if constexpr ((kMod & kModCap) != 0) {
+              auto load_max = [&]() {
+                load();
+                float am = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < nch)
-                score_run<kMod, -1>(reinterpret_cast<float(&)[32]>(sr[k]), sc, form, (float)(ahead - 1 - 32 * k),
-                                    abs_needed);
+                for (int k = 0; k < 4; ++k) {
+                  float(&y)[32] = reinterpret_cast<float(&)[32]>(sr[k]);
+                  if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, 0.f);
+                  if (k < nch) am = fmaxf(am, score_abs_max(y));
+                }
+                return am;
+              };
+              cap_with_hint(
+                  hint, [&]() { return cap_form(load_max(), sc); },
+                  [&](auto form) {
+                    const float am = load_max();
+                    score(form);
+                    return cap_form(am, sc);
+                  });
+            } else {
+              score(CapForm<kCapNear>{});
+            }
           }
           if (cut) {
 #pragma unroll

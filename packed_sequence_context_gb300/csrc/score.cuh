@@ -5,7 +5,8 @@
 //   y -= slope |i' - j|                         (i' = i + koff: the key position a query sits at)
 // in log2 units (y log2(e)), as the softmax takes them.
 //
-// tanh, chosen per warp and run of scores by the largest |x| of the run:
+// tanh, chosen per warp and run of scores by the largest |x| of the run (see
+// cap_form):
 //   s times a polynomial in s^2, a relative minimax fit of tanh(u) / u derived
 //     by exchange on the interval: three terms for |x| <= softcap / 4 (relative
 //     error 4.0e-7), five for |x| <= 0.75 softcap (5.7e-7);
@@ -74,19 +75,45 @@ THD_DEV float score_abs_max(const float (&s)[N]) {
 // The scores outside [from, to) become v.  Runs with masked columns set those
 // to 0 before the largest |s| is taken: a masked score, or a column that no
 // product wrote, must not choose the form (results stay reproducible).
+// Called under a condition that is uniform over the warp; the barrier keeps
+// the compiler from turning that branch into selects on every run (measured:
+// five of a forward tile's eleven instructions per score).
 template <int N>
 THD_DEV void score_fill(float (&s)[N], int from, int to, float v) {
+  __syncwarp();
+  const int lo = from < 0 ? 0 : (from > N ? N : from), hi = to > N ? N : to;
+  const uint32_t n_seen = hi > lo ? (uint32_t)(hi - lo) : 0u;
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    if (n < from || n >= to) s[n] = v;
+    if ((uint32_t)(n - lo) >= n_seen) s[n] = v;
 }
 
 // Which form of tanh the warp's run takes, by the largest |s| of each thread
 // (a NaN among the scores may pass for small: it stays a NaN in every form).
+// The near form is computed while the maximum is taken, instead of after a
+// decision, and again from TMEM in another form if the scores call for that; a
+// warp whose last run was not near measures first.  The result depends on the
+// run's scores alone.  (The three forms in a loop over "the form to try next"
+// made the compiler move every score between registers: 5850 instead of 3560
+// instructions in a forward tile.)
 constexpr int kCapNear = 0, kCapFar = 1, kCapWide = 2;
+template <int kForm>
+struct CapForm {
+  static constexpr int value = kForm;
+};
 THD_DEV int cap_form(float abs_max, const ScoreConsts& k) {
   if (__all_sync(0xffffffffu, abs_max <= k.cap_near)) return kCapNear;
   return __all_sync(0xffffffffu, abs_max <= k.cap_far) ? kCapFar : kCapWide;
+}
+// run(CapForm<f>) loads the scores, computes in form f and returns the form the
+// scores call for; measure() does only that.
+template <typename M, typename F>
+THD_DEV void cap_with_hint(int& hint, M&& measure, F&& run) {
+  int f = hint == kCapNear ? kCapNear : measure();
+  if (f == kCapNear) f = run(CapForm<kCapNear>{});
+  hint = f;
+  if (f == kCapFar) run(CapForm<kCapFar>{});
+  if (f == kCapWide) run(CapForm<kCapWide>{});
 }
 
 // The polynomial's value at two scores: tanh = s times it.
@@ -146,54 +173,40 @@ THD_DEV void bias_run(float (&s)[N], float a, float d0, float slope, float top) 
   }
 }
 
-// Scores times the polynomial, plus the linear side's bias.
+// One thread's N scores become top tanh + bias, in place (polynomials: top is in
+// the coefficients).  Linear side of the bias.
 template <int kForm, int kDir, bool kDist, int N>
-THD_DEV void poly_run(float (&s)[N], const ScoreConsts& k, float d0) {
-  const BiasRun<kDir, false> b(d0, k.slope, 0.f);
+THD_DEV void cap_run(float (&s)[N], const ScoreConsts& k, float top, float d0) {
+  const BiasRun<kDir, false> b(d0, k.slope, kForm == kCapWide ? top : 0.f);
 #pragma unroll
   for (int n = 0; n < N; n += 2) {
-    float q0, q1;
-    cap_poly<kForm>(q0, q1, s[n], s[n + 1], k);
-    if constexpr (kDist) {
-      float b0, b1;
-      b.at(n, b0, b1);
-      ffma2(s[n], s[n + 1], s[n], s[n + 1], q0, q1, b0, b1);
+    float q0, q1, b0 = kForm == kCapWide ? top : 0.f, b1 = b0;
+    if constexpr (kDist) b.at(n, b0, b1);
+    if constexpr (kForm == kCapWide) {
+      cap_wide(q0, q1, s[n], s[n + 1], k.cap_c);
+      ffma2(s[n], s[n + 1], q0, q1, -2.f * top, -2.f * top, b0, b1);
     } else {
-      fmul2(s[n], s[n + 1], s[n], s[n + 1], q0, q1);
+      cap_poly<kForm>(q0, q1, s[n], s[n + 1], k);
+      if constexpr (kDist)
+        ffma2(s[n], s[n + 1], s[n], s[n + 1], q0, q1, b0, b1);
+      else
+        fmul2(s[n], s[n + 1], s[n], s[n + 1], q0, q1);
     }
-  }
-}
-// top (1 - 2 r)
-template <int N>
-THD_DEV void wide_run(float (&s)[N], const ScoreConsts& k, float top) {
-#pragma unroll
-  for (int n = 0; n < N; n += 2) {
-    float r0, r1;
-    cap_wide(r0, r1, s[n], s[n + 1], k.cap_c);
-    ffma2(s[n], s[n + 1], r0, r1, -2.f * top, -2.f * top, top, top);
   }
 }
 
 // Forward: one thread's N scores become y log2(e), in place (coefficients
 // scaled by cap_a).  d0 and abs_needed as in BiasRun (abs_needed uniform over
 // the warp).
-template <int kMod, int kDir, int N>
-THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, int form, float d0, bool abs_needed) {
+template <int kMod, int kForm, int kDir, int N>
+THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, float d0, bool abs_needed) {
   constexpr bool kCap = (kMod & kModCap) != 0, kDist = (kMod & kModDist) != 0;
   if constexpr (kCap) {
-    if (kDist && !abs_needed && form != kCapWide) {  // cap and bias in one go
-      if (form == kCapNear)
-        poly_run<kCapNear, kDir, true>(s, k, d0);
-      else
-        poly_run<kCapFar, kDir, true>(s, k, d0);
+    if (kDist && !abs_needed) {  // cap and bias in one go
+      cap_run<kForm, kDir, true>(s, k, k.cap_a, d0);
       return;
     }
-    if (form == kCapNear)
-      poly_run<kCapNear, kDir, false>(s, k, 0.f);
-    else if (form == kCapFar)
-      poly_run<kCapFar, kDir, false>(s, k, 0.f);
-    else
-      wide_run(s, k, k.cap_a);
+    cap_run<kForm, kDir, false>(s, k, k.cap_a, 0.f);
   }
   if constexpr (kDist) {
     const float a = kCap ? 1.f : k.sl2;
@@ -202,19 +215,6 @@ THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, int form, float d0, 
     else
       bias_run<kDir, false>(s, a, d0, k.slope, 0.f);
   }
-}
-
-// Backward: one thread's N scores become tanh, in place (coefficients
-// unscaled).
-template <int N>
-THD_DEV void tanh_run(float (&s)[N], const ScoreConsts& k) {
-  const int form = cap_form(score_abs_max(s), k);
-  if (form == kCapNear)
-    poly_run<kCapNear, 1, false>(s, k, 0.f);
-  else if (form == kCapFar)
-    poly_run<kCapFar, 1, false>(s, k, 0.f);
-  else
-    wide_run(s, k, 1.f);
 }
 
 }  // namespace thd
