@@ -42,7 +42,7 @@
 
 namespace thd {
 
-template <int D>
+template <int D, int kMod>
 struct DqCfg {
   static constexpr int kKStages = 3;
   static constexpr int kVStages = 2;
@@ -51,18 +51,30 @@ struct DqCfg {
   static constexpr int kSmem = 1024 + 2 * kQBytes + (kKStages + kVStages) * kKVBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDP = 256, kColDQ = 384;
-  static constexpr int kThreads = 384;
+  // dS warpgroups: two, each with half of the columns of a tile; four with a
+  // quarter each where a tanh cap makes dS long enough for its latencies to
+  // show (two warps per scheduler, in step, left it idle half of the time)
+  static constexpr int kGroups = (kMod & kModCap) != 0 ? 4 : 2;
+  static constexpr int kWarps = 4 * kGroups;  // dS warps; the four others follow
+  static constexpr int kThreads = 32 * kWarps + 128;
+  // where packed dS of key columns 16 ks.. sits in the S buffer: inside the S
+  // columns of the warpgroup that writes it (another may still be reading its own)
+  __host__ __device__ static constexpr uint32_t ds_col(int ks) {
+    return kGroups == 2 ? 64 * (ks >> 2) + 8 * (ks & 3) : 32 * (ks >> 1) + 8 * (ks & 1);
+  }
   // register split (setmaxnreg) for the instantiation shorter sequences take:
   // dQ +2-3% on batches of 0.1-8K-token sequences, -0.9% on one long sequence
-  static constexpr uint32_t kComputeRegs = 192;  // per thread, warps 0-7
-  static constexpr uint32_t kOtherRegs = 112;    // per thread, warps 8-11
-  static_assert(256 * kComputeRegs + 128 * kOtherRegs <= 384 * 168, "register split above the launch budget");
+  static constexpr uint32_t kLaunchRegs = kGroups == 2 ? 168 : 96;   // per thread, what 65,536 allow
+  static constexpr uint32_t kComputeRegs = kGroups == 2 ? 192 : 104;  // per thread, dS warps
+  static constexpr uint32_t kOtherRegs = kGroups == 2 ? 112 : 64;     // per thread, the others
+  static_assert(32 * kWarps * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+                "register split above the launch budget");
 };
 
 template <int D, bool kGrouped, int kMod>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     dq_kernel(const DqParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, kMod>;
   // the register split also carries the longer dS of capped scores
   constexpr bool kSplit = !kGrouped || (kMod & kModCap) != 0;
   constexpr int KS = C::kKStages, VS = C::kVStages;
@@ -90,6 +102,7 @@ __global__ void __launch_bounds__(384, 1)
   __shared__ ItemRing ring;  // items handed out to this CTA, in claim order
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int role = warp - C::kWarps;  // of the four warps after the dS warps: 0 Q, dO, K; 1 S, dQ; 2 V; 3 dP
   if (*p.dev_status != 0) return;  // metadata rejected: outputs untouched
   const int n_entries = p.counters[0];
   const int n_items = n_entries * p.Hq;
@@ -105,24 +118,24 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar_s_full[s], 1);
-      mbar_init(&bar_ds_ready[s], 8);  // one arrival per dS warp
+      mbar_init(&bar_ds_ready[s], C::kWarps);  // one arrival per dS warp
     }
     mbar_init(&bar_dp_full, 1);
-    mbar_init(&bar_dp_free, 8);  // one arrival per dS warp
+    mbar_init(&bar_dp_free, C::kWarps);  // one arrival per dS warp
     mbar_init(&bar_q_full, 32);
     mbar_init(&bar_q_empty, 2);  // the S issuer's last read of Q and the dP issuer's last read of dO
     mbar_init(&bar_dq_done, 1);
     mbar_init(&bar_drain, 1);
     mbar_init(&bar_drain2, 1);
-    item_ring_init(&ring, 3 + 8);  // warps 9, 10, 11 (one thread each) and the 8 dS warps
+    item_ring_init(&ring, 3 + C::kWarps);  // warps 9, 10, 11 (one thread each) and the dS warps
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (role == 1) {
     tmem_alloc(&s_tmem, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (role == 0 && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -138,9 +151,9 @@ __global__ void __launch_bounds__(384, 1)
   // role runs, so nothing ever commits to it.
   if (p.test_stall) {
     mbar_wait(&bar_drain, 0, &s_abort);
-  } else if (warp >= 8) {
+  } else if (role >= 0) {
     if constexpr (kSplit) regs_lower<C::kOtherRegs>();
-    if (warp == 8) {
+    if (role == 0) {
       // ------------------------------------------------------------ Q, dO and K producer (whole warp)
       int ks = 0;
       uint32_t kph = 0, n_fill = 0, q_iter = 0;
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (role == 2) {
       // ------------------------------------------------------------ value producer
       if (lane == 0) {
         int vs = 0;
@@ -242,7 +255,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (role == 1) {
       // ------------------------------------------------------------ S = Q K^T and dQ += dS K issuer
       // Two issuing threads, as in the forward: a barrier wait in one does not
       // leave the tensor pipe idle while the other has products to issue.
@@ -266,9 +279,8 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
           const int kslot = (int)(gg % KS);
           const uint64_t kd = kmn + (uint64_t)((kslot * C::kKVBytes) >> 4);
-          // packed dS of key columns 16 kk.. sits at column 64 (kk/4) + 8 (kk%4)
           for (int kk = 0; kk < ncols / 16; ++kk)
-            mma_ts(tmem + C::kColDQ, tmem + b * 128u + 64 * (kk >> 2) + 8 * (kk & 3),
+            mma_ts(tmem + C::kColDQ, tmem + b * 128u + C::ds_col(kk),
                    kd + (uint64_t)(kk * (2048 >> 4)), idesc_dq, (first && kk == 0) ? 0u : 1u);
           tc_commit(&bar_k_empty[kslot]);  // the K slot's last reader
           return true;
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(384, 1)
         drain_wait(&bar_drain, 0);
       }
       __syncwarp();
-    } else if (warp == 11) {
+    } else if (role == 3) {
       // ------------------------------------------------------------ dP = dO V^T issuer
       // Per tile g: once the dS warps have read dP of tile g-1 into registers
       // (dp_free: early in their work on g-1), dP of tile g -- so it is ready
@@ -386,13 +398,14 @@ __global__ void __launch_bounds__(384, 1)
   } else {
     if constexpr (kSplit) regs_raise<C::kComputeRegs>();
     // ------------------------------------------------------------ dS + epilogue
-    // Thread (half, row) owns query row `row` (its TMEM lane) and key columns
-    // [64 half, 64 half + 64) of every tile, plus head-dim columns
-    // [D/2 half, D/2 half + D/2) of dQ.
-    const int half = warp >> 2;
+    // Thread (part, row) owns query row `row` (its TMEM lane) and the 32-column
+    // chunks [kCh part, kCh part + kCh) of every tile, plus as many 32-column
+    // chunks of dQ.
+    constexpr int kCh = 4 / C::kGroups;
+    const int part = warp >> 2;
     const int row = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    constexpr int DH = D / 2;
+    constexpr int kChO = D / 32 >= C::kGroups ? D / 32 / C::kGroups : 1;  // chunks of dQ (parts past D have none)
     const float sl2 = p.scale_log2;
     // dQ rows start at multiples of 128 bytes: 32-byte stores when dQ is 32-byte aligned
     const bool dq_v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
@@ -450,15 +463,15 @@ __global__ void __launch_bounds__(384, 1)
         const int nch = ceil_div(q_tile_ncols<kMod>(it, p, c, j), 32);
         const uint32_t scol = tmem + lane_base + b * 128u;
         const uint32_t pcol = tmem + lane_base + C::kColDP;
-        // dP of this thread's two chunks first, so the buffer can take the
+        // dP of this thread's chunks first, so the buffer can take the
         // next tile's dP while dS is computed
-        uint32_t dr[2][32];
+        uint32_t dr[kCh][32];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          if (2 * half + kk < nch) tmem_ld32(pcol + 32 * (2 * half + kk), dr[kk]);
+        for (int kk = 0; kk < kCh; ++kk)
+          if (kCh * part + kk < nch) tmem_ld32(pcol + 32 * (kCh * part + kk), dr[kk]);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          if (2 * half + kk < nch) tmem_ld_wait(dr[kk]);
+        for (int kk = 0; kk < kCh; ++kk)
+          if (kCh * part + kk < nch) tmem_ld_wait(dr[kk]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_dp_free);
@@ -466,7 +479,7 @@ __global__ void __launch_bounds__(384, 1)
           // dS = P (dP - Delta) (1 - tanh^2), in place over the scores; then 0 on
           // the keys this row may not see, whatever stood there
           constexpr bool kCap = (kMod & kModCap) != 0;
-          uint32_t pk[2][16];
+          uint32_t pk[kCh][16];
           // chunk ch of S, with the cap's masked columns at 0; true if any is masked
           auto load = [&](float(&y)[32], int ch) {
             uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
@@ -479,9 +492,9 @@ __global__ void __launch_bounds__(384, 1)
           auto measure = [&]() {
             float am = 0.f, y[32];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              if (2 * half + kk < nch) {
-                load(y, 2 * half + kk);
+            for (int kk = 0; kk < kCh; ++kk) {
+              if (kCh * part + kk < nch) {
+                load(y, kCh * part + kk);
                 am = fmaxf(am, score_abs_max(y));
               }
             }
@@ -490,8 +503,8 @@ __global__ void __launch_bounds__(384, 1)
           auto run = [&](auto form) {
             float am = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const int ch = 2 * half + kk;  // this thread's 32-column chunk
+            for (int kk = 0; kk < kCh; ++kk) {
+              const int ch = kCh * part + kk;  // this thread's 32-column chunk
               if (ch < nch) {
                 float y[32];
                 const bool cut = load(y, ch);
@@ -523,8 +536,8 @@ __global__ void __launch_bounds__(384, 1)
                 if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
 #pragma unroll
                 for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
-                // over columns already read, where plain dS goes (below)
-                if (!kCap) tmem_st16(scol + 64 * half + 16 * kk, pk[kk]);
+                // over columns already read
+                if (!kCap) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
               }
             }
             return kCap ? cap_form(am, sc) : kCapNear;
@@ -532,15 +545,15 @@ __global__ void __launch_bounds__(384, 1)
           if constexpr (kCap) {
             cap_with_hint(hint, measure, run);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              if (2 * half + kk < nch) tmem_st16(scol + 64 * half + 16 * kk, pk[kk]);
+            for (int kk = 0; kk < kCh; ++kk)
+              if (kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
           } else {
             run(CapForm<kCapNear>{});
           }
         } else {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            const int ch = 2 * half + kk;  // this thread's 32-column chunk
+          for (int kk = 0; kk < kCh; ++kk) {
+            const int ch = kCh * part + kk;  // this thread's 32-column chunk
             if (ch < nch) {
               uint32_t sr[32];
               tmem_ld32(scol + 32 * ch, sr);
@@ -561,9 +574,7 @@ __global__ void __launch_bounds__(384, 1)
                 fmul2(g0, g1, p0, p1, t0, t1);
                 pk[n] = pack_bf16x2(g0, g1);
               }
-              // packed dS stays inside this half's own S columns (the other
-              // warpgroup may still be reading its half): chunk ch -> 64 (ch/2) + 16 (ch%2)
-              tmem_st16(scol + 64 * (ch >> 1) + 16 * (ch & 1), pk);
+              tmem_st16(scol + C::ds_col(2 * ch), pk);
             }
           }
         }
@@ -582,17 +593,17 @@ __global__ void __launch_bounds__(384, 1)
         ++n_item;
       }
 #pragma unroll 1
-      for (int k = 0; k < DH / 32; ++k) {
+      for (int k = kChO * part; k < kChO * (part + 1) && k < D / 32; ++k) {
         uint32_t o[32];
         if (jl > 0) {
-          tmem_ld32(tmem + lane_base + C::kColDQ + half * DH + 32 * k, o);
+          tmem_ld32(tmem + lane_base + C::kColDQ + 32 * k, o);
           tmem_ld_wait(o);
         } else {
 #pragma unroll
           for (int n = 0; n < 32; ++n) o[n] = 0u;
         }
         if (in_rank)
-          store32_bf16(p.dq + (grow * p.Hq + it.h) * D + half * DH + 32 * k, o, valid ? p.scale : 0.f, dq_v8);
+          store32_bf16(p.dq + (grow * p.Hq + it.h) * D + 32 * k, o, valid ? p.scale : 0.f, dq_v8);
       }
       tc_fence_before();
     }
@@ -601,14 +612,14 @@ __global__ void __launch_bounds__(384, 1)
       const int Tend = p.eff[(p.B + 1) + p.B];
       const int64_t nvec = (p.dq_rows - Tend) * (int64_t)p.Hq * (D / 8);
       const int64_t base = (int64_t)Tend * p.Hq * D;
-      for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < nvec; i += (int64_t)gridDim.x * 256)
+      for (int64_t i = (int64_t)blockIdx.x * 32 * C::kWarps + tid; i < nvec; i += (int64_t)gridDim.x * 32 * C::kWarps)
         reinterpret_cast<uint4*>(p.dq + base)[i] = make_uint4(0, 0, 0, 0);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (role == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(384, 1)
 template <int D, bool kGrouped, int kMod>
 static cudaError_t launch_dq_t(const DqParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                                cudaStream_t st) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, kMod>;
   cudaError_t ea = cudaFuncSetAttribute(dq_kernel<D, kGrouped, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (ea != cudaSuccess) return ea;
   prof_before(THD_KERNEL_BWD_DQ, st);
