@@ -543,91 +543,75 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
           // P in place over the scores and, for dS, P (1 - tanh^2); then 0 in the
           // columns that do not see this key, whatever stood there
           constexpr bool kCap = (kMod & kModCap) != 0;
-          uint32_t pk[2][16];
-          // chunk kk of S^T, with the cap's masked columns at 0; true if any is masked
-          auto load = [&](float(&y)[32], int kk) {
-            uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
-            tmem_ld32(acol + 32 * kk, sr);
-            tmem_ld_wait(sr);
-            const bool cut = __any_sync(0xffffffffu, n_lo > 32 * kk || n_hi < 32 * kk + 32);
-            if (kCap && cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-            return cut;
-          };
-          auto measure = [&]() {
-            float am = 0.f, y[32];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (2 * half + i < nch) {
-                load(y, 2 * half + i);
-                am = fmaxf(am, score_abs_max(y));
+          for (int i = 0; i < 2; ++i) {
+            const int kk = 2 * half + i;
+            if (kk < nch) {
+              const bool cut = __any_sync(0xffffffffu, n_lo > 32 * kk || n_hi < 32 * kk + 32);
+              float y[32];
+              auto load = [&]() {
+                tmem_ld32(acol + 32 * kk, reinterpret_cast<uint32_t(&)[32]>(y));
+                tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(y));
+                if (kCap && cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+              };
+              if constexpr (kCap) {
+                cap_with_hint(
+                    hint,
+                    [&]() {
+                      load();
+                      return cap_form(score_abs_max(y), sc);
+                    },
+                    [&](auto form) {
+                      load();
+                      const float am = score_abs_max(y);
+                      cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f);
+                      return cap_form(am, sc);
+                    });
+              } else {
+                load();
               }
-            }
-            return cap_form(am, sc);
-          };
-          auto run = [&](auto form) {
-            float am = 0.f;
+              const float a = kCap ? sc.cap_a : sl2;
+              auto write_p = [&](auto bias) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int kk = 2 * half + i;
-              if (kk < nch) {
-                float y[32];
-                const bool cut = load(y, kk);
-                if constexpr (kCap) {
-                  am = fmaxf(am, score_abs_max(y));
-                  cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f);
-                }
-                const float a = kCap ? sc.cap_a : sl2;
-                auto write_p = [&](auto bias) {
+                for (int q4 = 0; q4 < 8; ++q4) {
+                  const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
+                  const float l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-                  for (int q4 = 0; q4 < 8; ++q4) {
-                    const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
-                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                      const int n = 4 * q4 + e;
-                      float x0, x1, b0 = -l[e], b1 = -l[e + 1];
-                      if constexpr ((kMod & kModDist) != 0) {
-                        float c0, c1;
-                        bias.at(n, c0, c1);
-                        fadd2(b0, b1, b0, b1, c0, c1);
-                      }
-                      ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
-                      x0 = ex2(x0);
-                      x1 = ex2(x1);
-                      if constexpr (kCap) {
-                        float w0, w1;
-                        ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
-                        fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
-                      } else {
-                        pv[i][n] = x0, pv[i][n + 1] = x1;
-                      }
-                      y[n] = x0, y[n + 1] = x1;
+                  for (int e = 0; e < 4; e += 2) {
+                    const int n = 4 * q4 + e;
+                    float x0, x1, b0 = -l[e], b1 = -l[e + 1];
+                    if constexpr ((kMod & kModDist) != 0) {
+                      float c0, c1;
+                      bias.at(n, c0, c1);
+                      fadd2(b0, b1, b0, b1, c0, c1);
                     }
+                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                    x0 = ex2(x0);
+                    x1 = ex2(x1);
+                    if constexpr (kCap) {
+                      float w0, w1;
+                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                      fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
+                    } else {
+                      pv[i][n] = x0, pv[i][n + 1] = x1;
+                    }
+                    y[n] = x0, y[n + 1] = x1;
                   }
-                };
-                if ((kMod & kModDist) != 0 && abs_needed)
-                  write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
-                else
-                  write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
-                if (cut) {
-                  score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-                  score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
                 }
-#pragma unroll
-                for (int n = 0; n < 16; ++n) pk[i][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
-                // over columns already read, where plain P^T goes (below)
-                if (!kCap) tmem_st16(acol + 64 * half + 16 * i, pk[i]);
+              };
+              if ((kMod & kModDist) != 0 && abs_needed)
+                write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
+              else
+                write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
+              if (cut) {
+                score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
+                score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
               }
-            }
-            return kCap ? cap_form(am, sc) : kCapNear;
-          };
-          if constexpr (kCap) {
-            cap_with_hint(hint, measure, run);
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (2 * half + i < nch) tmem_st16(acol + 64 * half + 16 * i, pk[i]);
-          } else {
-            run(CapForm<kCapNear>{});
+              for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+              tmem_st16(acol + 64 * half + 16 * i, pk);  // over columns already read
+            }
           }
         } else {
 #pragma unroll
