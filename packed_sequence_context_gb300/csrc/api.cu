@@ -181,7 +181,7 @@ struct ScoreArgs {
   const int32_t* prefix;
   bool any() const { return softcap > 0.f || slopes || doc_q || prefix; }
   int mod() const { return kScored | (softcap > 0.f ? kModCap : 0) | (slopes ? kModDist : 0); }
-  int fwd_mod() const { return mod() | (softcap > 0.f && !slopes && kLog2e * softcap <= kBoundedCap ? kModBounded : 0); }
+  int fwd_mod() const { return mod() | (softcap > 0.f && kLog2e * softcap <= kBoundedCap ? kModBounded : 0); }
 };
 
 static int check_score(const ScoreArgs& a, float scale) {
@@ -308,7 +308,11 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   const bool grouped = long_sequences(B, T_kv);
   fp.group_kv = locality_group(Hkv, (size_t)T_kv * D * 2 * 2, grouped);
   const int forced = test_fwd_kernel();
-  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : grouped;
+  // Bounded scores: that kernel's tiles in turn are ahead from sequences of
+  // about 1024 tokens on (32 x 512: 119 us against 109; 16 x 1024: 142 against
+  // 150; 8 x 2048: 193 against 226; 1 x 32768: 3.34 ms against 5.09).
+  const bool bounded = score && (score->fwd_mod() & kModBounded);
+  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : bounded ? T_kv >= 1024 * (int64_t)B : grouped;
   fp.dev_status = dev_status;
   fp.B = B;
   fp.Hq = Hq;

@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
                     [&](auto form) {
                       load();
                       const float am = score_abs_max(y);
-                      cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f);
+                      cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f, 0.f);
                       return cap_form(am, sc);
                     });
               } else {

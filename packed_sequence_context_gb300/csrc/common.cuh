@@ -26,8 +26,9 @@ __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 // with kScored set, each query sees the keys of one interval (causal, prefix
 // and document masks together); kModCap and kModDist add the tanh cap and the
 // distance bias.
-// kModBounded (forward, with the cap alone): |y| <= softcap, small enough that
-// 2^y needs no running maximum.
+// kModBounded (forward, with a cap of at most kBoundedCap): a row's largest y is
+// within that of its largest bias, so 2^(y - largest bias) needs no running
+// maximum.
 constexpr int kScored = 1, kModCap = 2, kModDist = 4, kModBounded = 8;
 constexpr float kBoundedCap = 80.f;  // softcap log2(e) at most this: 2^-80 <= P <= 2^80
 

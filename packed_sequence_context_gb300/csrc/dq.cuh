@@ -510,7 +510,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                 const bool cut = load(y, ch);
                 if constexpr (kCap) {
                   am = fmaxf(am, score_abs_max(y));
-                  cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f);
+                  cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f, 0.f);
                 }
                 const float a = kCap ? sc.cap_a : sl2;
                 auto write_ds = [&](auto bias) {

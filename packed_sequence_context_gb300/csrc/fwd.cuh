@@ -33,9 +33,10 @@
 // accumulators are not ordered among themselves, so a buffer is reused for a
 // later QK^T only after the PV that read its P has completed (s_free).
 //
-// Bounded scores (kModBounded: a cap that holds every |y| to 80 or less in log2
-// units): 2^y overflows nowhere, so the running maximum stays 0, O is never
-// rescaled, and the tiles of an item depend on each other only through sums.
+// Bounded scores (kModBounded: a cap of at most 80 in log2 units): with the
+// largest bias of the row's keys, known from the mask, for a maximum, P lies
+// below 2^80 and the sum above 2^-80, so there is no running maximum, O is
+// never rescaled, and an item's tiles depend on each other only through sums.
 // The two softmax warpgroups then take whole tiles in turn instead of half of
 // every tile: each scheduler holds one warp of either, in different phases of
 // their tiles, so the TMEM loads and barriers of one run beside the other's
@@ -417,7 +418,9 @@ __global__ void __launch_bounds__(384, 1)
         sc = score_consts<kMod, true>(p, it.h);
       }
       // ---- key tiles
-      float m = kTurns ? 0.f : -INFINITY, l = 0.f;  // running max (log2 units, shared value) and this half's sum
+      float m = -INFINITY, l = 0.f;  // running max (log2 units, shared value) and this half's sum
+      if constexpr (kTurns)  // bounded scores: their largest bias, throughout
+        m = (kMod & kModDist) != 0 ? largest_bias(sc.slope, pos + it.g.koff, sees.x, sees.y) : 0.f;
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
         if (!ok) return;
@@ -455,6 +458,8 @@ __global__ void __launch_bounds__(384, 1)
           // cap of 128 scores each would not fit the instruction cache); packed P
           // goes over columns already read (chunk k -> column 64 (k/2) + 16 (k%2))
           const uint32_t tcol = tmem + lane_base + sb * 128u;
+          const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
+          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
 #pragma unroll 1
           for (int k = 0; k < nch; ++k) {
             const bool cut = __any_sync(0xffffffffu, cnt < 32 * k + 32 || from > 32 * k);
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(384, 1)
                   float y[32];
                   load(y);
                   const float am = score_abs_max(y);
-                  score_run<kMod, decltype(form)::value, -1>(y, sc, 0.f, false);
+                  score_run<kMod, decltype(form)::value, -1>(y, sc, (float)(ahead - 1 - 32 * k), abs_needed, -m);
                   if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, -INFINITY);
 #pragma unroll
                   for (int i = 0; i < 4; ++i) sa[i] = 0.f;
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int kk = 0; kk < 2; ++kk)
                 if (k0 + kk < nch)
                   score_run<kMod, decltype(form)::value, -1>(reinterpret_cast<float(&)[32]>(sr[kk]), sc,
-                                                             (float)(ahead - 1 - 32 * (k0 + kk)), abs_needed);
+                                                             (float)(ahead - 1 - 32 * (k0 + kk)), abs_needed, 0.f);
             };
             if constexpr ((kMod & kModCap) != 0) {
               auto load_max = [&]() {

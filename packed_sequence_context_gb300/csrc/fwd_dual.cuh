@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(384, 1)
         sc = score_consts<kMod, true>(p, it.h);
       }
       // ---- key tiles
-      float m = (kMod & kModBounded) != 0 ? 0.f : -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
+      float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
+      if constexpr ((kMod & kModBounded) != 0)  // bounded scores: their largest bias, throughout (see fwd.cuh)
+        m = (kMod & kModDist) != 0 ? largest_bias(sc.slope, pos + it.g.koff, sees.x, sees.y) : 0.f;
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
         if (!ok) return;
@@ -424,7 +426,8 @@ __global__ void __launch_bounds__(384, 1)
               for (int k = 0; k < 4; ++k)
                 if (k < nch)
                   score_run<kMod, decltype(form)::value, -1>(reinterpret_cast<float(&)[32]>(sr[k]), sc,
-                                                             (float)(ahead - 1 - 32 * k), abs_needed);
+                                                             (float)(ahead - 1 - 32 * k), abs_needed,
+                                                             (kMod & kModBounded) != 0 ? -m : 0.f);
             };
             if constexpr ((kMod & kModCap) != 0) {
               auto load_max = [&]() {
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int n = 0; n < 32; ++n)
               if (32 * k + n >= cnt) sr[k][n] = __float_as_uint(-INFINITY);
         }
-        if constexpr ((kMod & kModBounded) == 0) {  // bounded scores take a maximum of 0 throughout
+        if constexpr ((kMod & kModBounded) == 0) {
           // row maximum: per chunk four independent partial maxima of 8 values
           float mloc = -INFINITY;
 #pragma unroll

@@ -173,18 +173,20 @@ THD_DEV void bias_run(float (&s)[N], float a, float d0, float slope, float top) 
   }
 }
 
-// One thread's N scores become top tanh + bias, in place (polynomials: top is in
-// the coefficients).  Linear side of the bias.
+// One thread's N scores become scale tanh + bias + top, in place (polynomials:
+// scale is in the coefficients; without a bias top is 0).  Linear side of the
+// bias.
 template <int kForm, int kDir, bool kDist, int N>
-THD_DEV void cap_run(float (&s)[N], const ScoreConsts& k, float top, float d0) {
-  const BiasRun<kDir, false> b(d0, k.slope, kForm == kCapWide ? top : 0.f);
+THD_DEV void cap_run(float (&s)[N], const ScoreConsts& k, float scale, float d0, float top) {
+  if (kForm == kCapWide) top += scale;
+  const BiasRun<kDir, false> b(d0, k.slope, top);
 #pragma unroll
   for (int n = 0; n < N; n += 2) {
-    float q0, q1, b0 = kForm == kCapWide ? top : 0.f, b1 = b0;
+    float q0, q1, b0 = top, b1 = top;
     if constexpr (kDist) b.at(n, b0, b1);
     if constexpr (kForm == kCapWide) {
       cap_wide(q0, q1, s[n], s[n + 1], k.cap_c);
-      ffma2(s[n], s[n + 1], q0, q1, -2.f * top, -2.f * top, b0, b1);
+      ffma2(s[n], s[n + 1], q0, q1, -2.f * scale, -2.f * scale, b0, b1);
     } else {
       cap_poly<kForm>(q0, q1, s[n], s[n + 1], k);
       if constexpr (kDist)
@@ -195,26 +197,35 @@ THD_DEV void cap_run(float (&s)[N], const ScoreConsts& k, float top, float d0) {
   }
 }
 
-// Forward: one thread's N scores become y log2(e), in place (coefficients
-// scaled by cap_a).  d0 and abs_needed as in BiasRun (abs_needed uniform over
-// the warp).
+// Forward: one thread's N scores become y log2(e) + top, in place (coefficients
+// scaled by cap_a; without a bias top is 0).  d0 and abs_needed as in BiasRun
+// (abs_needed uniform over the warp).
 template <int kMod, int kForm, int kDir, int N>
-THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, float d0, bool abs_needed) {
+THD_DEV void score_run(float (&s)[N], const ScoreConsts& k, float d0, bool abs_needed, float top) {
   constexpr bool kCap = (kMod & kModCap) != 0, kDist = (kMod & kModDist) != 0;
   if constexpr (kCap) {
     if (kDist && !abs_needed) {  // cap and bias in one go
-      cap_run<kForm, kDir, true>(s, k, k.cap_a, d0);
+      cap_run<kForm, kDir, true>(s, k, k.cap_a, d0, top);
       return;
     }
-    cap_run<kForm, kDir, false>(s, k, k.cap_a, 0.f);
+    cap_run<kForm, kDir, false>(s, k, k.cap_a, 0.f, 0.f);
   }
   if constexpr (kDist) {
     const float a = kCap ? 1.f : k.sl2;
     if (abs_needed)
-      bias_run<kDir, true>(s, a, d0, k.slope, 0.f);
+      bias_run<kDir, true>(s, a, d0, k.slope, top);
     else
-      bias_run<kDir, false>(s, a, d0, k.slope, 0.f);
+      bias_run<kDir, false>(s, a, d0, k.slope, top);
   }
+}
+
+// The largest bias (log2 units) a query at key position `at` gets from the keys
+// [lo, hi) it sees: of the nearest, or with a negative slope of the farthest.
+THD_DEV float largest_bias(float slope, int at, int lo, int hi) {
+  if (hi <= lo) return 0.f;
+  const int below = at - lo, above = hi - 1 - at;  // distances to the two ends, where those lie
+  const int d = slope >= 0.f ? imax(imax(-below, -above), 0) : imax(below, above);
+  return -slope * (float)d;
 }
 
 }  // namespace thd

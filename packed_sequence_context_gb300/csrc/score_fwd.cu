@@ -13,6 +13,8 @@ static cudaError_t launch_d(const FwdParams& p, const CUtensorMap& tk, const CUt
     case kScored | kModCap | kModBounded:
       return launch_fwd_t<D, false, true, kScored | kModCap | kModBounded>(p, tk, tv, grid, st);
     case kScored | kModDist: return launch_fwd_t<D, false, true, kScored | kModDist>(p, tk, tv, grid, st);
+    case kScored | kModCap | kModDist | kModBounded:
+      return launch_fwd_t<D, false, true, kScored | kModCap | kModDist | kModBounded>(p, tk, tv, grid, st);
     default: return launch_fwd_t<D, false, true, kScored | kModCap | kModDist>(p, tk, tv, grid, st);
   }
 }

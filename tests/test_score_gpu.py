@@ -119,12 +119,22 @@ CASES = {
                    {"cap": 15.0, "bias": True, "docs": 120, "prefix": [200, 3, 30, 384]}),
     "single tokens": ([1, 1, 2, 1], [130, 1, 300, 777], 2, 1, 4, 2, 64, 2, {"cap": 30.0, "bias": True}),
     "many short": ([0, 5, 64, 1, 33, 0, 2, 17] * 8, None, 4, 2, 2, 1, 64, 1, {"cap": 6.0, "docs": 9}),
+    # caps past what needs no running maximum (55), scores in every form of tanh
+    "large cap": ([300, 513], None, 8, 2, 4, 2, 128, 1, {"cap": 90.0}),
+    "large cap bias": ([513, 70], None, 8, 2, 4, 2, 64, 1, {"cap": 70.0, "bias": True, "prefix": [60, 70]}),
+    "three forms": ([640], None, 8, 2, 2, 2, 64, 1, {"cap": 10.0, "std": 4.0}),
+    "three forms bias": ([640], None, 8, 2, 2, 2, 128, 0, {"cap": 10.0, "std": 4.0, "bias": True}),
+    "growing bias": ([300, 200], None, 8, 2, 3, 1, 64, 1, {"cap": 9.0, "slopes": [-0.02, 0.0, 0.3]}),
+    "growing bias both sides": ([100, 257], [300, 257], 16, 2, 3, 1, 128, 2,
+                                {"cap": 9.0, "slopes": [-0.05, 0.01, -0.3], "docs": 40, "prefix": [90, 100]}),
+    "far keys only": ([80, 40], [300, 200], 8, 2, 2, 2, 64, 0, {"cap": 20.0, "slopes": [3.0, 0.5], "docs": 30}),
     "mask only": ([300, 200], None, 8, 2, 2, 2, 128, 1, {"prefix": [100, 50]}),
 }
 
 
 def _make(name, std=2.0):
     lq, lk, unit, cp, Hq, Hkv, D, causal, mods = CASES[name]
+    std = mods.get("std", std)
     lk = lq if lk is None else lk
     seed = sum(map(ord, name))
     c = inputs.make_cross(lq, lk, pad_to=unit, Hq=Hq, Hkv=Hkv, D=D, cp_size=cp, seed=seed)
@@ -133,6 +143,8 @@ def _make(name, std=2.0):
     m = {"softcap": mods.get("cap", 0.0), "slopes": None, "doc_q": None, "doc_k": None, "prefix": None}
     if mods.get("bias"):
         m["slopes"] = (2.0 ** (-6.0 * (np.arange(Hq) + 1) / Hq)).astype(np.float32)
+    if "slopes" in mods:
+        m["slopes"] = np.array(mods["slopes"], np.float32)
     if "docs" in mods:
         m["doc_k"] = _docs(rng, lk, c["cu_kv_pad"], mods["docs"])
         m["doc_q"] = m["doc_k"] if list(lq) == list(lk) else _docs(rng, lq, c["cu_q_pad"], mods["docs"])
