@@ -399,6 +399,7 @@ static int bwd_common(const void* q, const void* k, const void* v, const void* o
   dp.dout = static_cast<const uint16_t*>(dout);
   dp.lse2 = lse2;
   dp.delta = delta;
+  dp.delta_out = delta;
   dp.dq = static_cast<uint16_t*>(dq);
   dp.eff = pp.eff;
   dp.items = pp.items_q;

@@ -445,6 +445,7 @@ struct DqParams {
   const uint16_t* dout;
   const float* lse2;   // [Hq][T_q], lse * log2(e)
   const float* delta;  // [Hq][T_q]: Delta = rowsum(dO * O)
+  float* delta_out;    // scored: the same buffer, for the corrected Delta
   uint16_t* dq;       // bf16 [dq_rows][Hq][D]
   const int32_t* eff;
   const int4* items;  // the query-tile schedule

@@ -20,6 +20,16 @@
 //   dQ += dS K   (A = dS from TMEM, B = the K tile read MN-major)
 // and dQ * scale is written as bf16 at the end of the item.
 //
+// Scored attention, Delta: rowsum(dO O) comes from O in bf16, an error of up to
+// 2^-9 |dO| |O| that dS = P (dP - Delta) takes over whole where few keys share
+// a row's weight (measured against fp64 on rows of 8 to 500 keys: dQ and dK off
+// by 3 to 6e-3, with an exact Delta by 2.4e-3).  The row sum of P (dP - Delta),
+// which is 0 for the exact Delta, corrects it: every item adds it up and leaves
+// the exact Delta for the dK/dV kernel, and an item of at most kTwiceKeys keys
+// walks them twice, the first time for Delta alone (more would cost more than
+// they give: their rows have more keys, dQ is off by 3 to 4e-3 at most, and
+// the walk takes two thirds of dQ's time again).
+//
 // CTA layout (384 threads, one CTA per SM, persistent over the schedule):
 //   warps 0-7  dS in two warpgroups (thread = query row, half of the key
 //              columns) and the dQ epilogue (half of the head dimension)
@@ -71,6 +81,13 @@ struct DqCfg {
                 "register split above the launch budget");
 };
 
+// How often an item walks its key tiles (see above).
+constexpr int kTwiceKeys = 256;
+template <int kMod>
+__device__ inline int dq_passes(const QItem& it) {
+  return kMod != 0 && it.k_hi - it.k_lo <= kTwiceKeys ? 2 : 1;
+}
+
 template <int D, bool kGrouped, int kMod>
 __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     dq_kernel(const DqParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
@@ -95,6 +112,8 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
   __shared__ __align__(8) uint64_t bar_q_full;
   __shared__ __align__(8) uint64_t bar_q_empty;
   __shared__ __align__(8) uint64_t bar_dq_done;
+  __shared__ __align__(8) uint64_t bar_eps[4];  // scored: the dS warps of one quarter of the rows
+  __shared__ float s_eps[kMod != 0 ? C::kGroups - 1 : 1][kMod != 0 ? kTile : 1];
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(8) uint64_t bar_drain2;
   __shared__ uint32_t s_tmem;
@@ -125,6 +144,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     mbar_init(&bar_q_full, 32);
     mbar_init(&bar_q_empty, 2);  // the S issuer's last read of Q and the dP issuer's last read of dO
     mbar_init(&bar_dq_done, 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&bar_eps[s], C::kGroups);
     mbar_init(&bar_drain, 1);
     mbar_init(&bar_drain2, 1);
     item_ring_init(&ring, 3 + C::kWarps);  // warps 9, 10, 11 (one thread each) and the dS warps
@@ -193,25 +213,28 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         fence_proxy_async_smem();
         mbar_arrive(&bar_q_full);
         ++q_iter;
-        for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
-          if (!ok) return;
-          if (!mbar_wait(&bar_k_empty[ks], kph ^ 1u, &s_abort)) {
-            ok = false;
-            return;
-          }
-          if (lane == 0) {
-            const int row = it.g.kv_off + c * it.g.cbkv + j * kTile;
-            mbar_arrive_expect_tx(&bar_k_full[ks], C::kKVBytes);
+        const int passes = dq_passes<kMod>(it);
+        for (int pass = 0; pass < passes; ++pass) {
+          for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+            if (!ok) return;
+            if (!mbar_wait(&bar_k_empty[ks], kph ^ 1u, &s_abort)) {
+              ok = false;
+              return;
+            }
+            if (lane == 0) {
+              const int row = it.g.kv_off + c * it.g.cbkv + j * kTile;
+              mbar_arrive_expect_tx(&bar_k_full[ks], C::kKVBytes);
 #pragma unroll
-            for (int hb = 0; hb < D / 64; ++hb)
-              tma_load_3d(smem_u32(sK + ks * C::kKVBytes + hb * 16384), &tmK, &bar_k_full[ks], hb * 64, it.kvh, row);
-          }
-          ++n_fill;
-          if (++ks == KS) {
-            ks = 0;
-            kph ^= 1u;
-          }
-        });
+              for (int hb = 0; hb < D / 64; ++hb)
+                tma_load_3d(smem_u32(sK + ks * C::kKVBytes + hb * 16384), &tmK, &bar_k_full[ks], hb * 64, it.kvh, row);
+            }
+            ++n_fill;
+            if (++ks == KS) {
+              ks = 0;
+              kph ^= 1u;
+            }
+          });
+        }
         w = __shfl_sync(0xffffffffu, wnext, 0);
       }
       if (lane == 0) {
@@ -231,23 +254,26 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
           int w;
           if (!item_take_one(&ring, kit, w, &s_abort) || w >= n_items) break;
           const QItem it = q_item<kGrouped, kMod>(p, n_entries, w);
-          for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
-            if (!ok) return;
-            if (!mbar_wait(&bar_v_empty[vs], vph ^ 1u, &s_abort)) {
-              ok = false;
-              return;
-            }
-            const int row = it.g.kv_off + c * it.g.cbkv + j * kTile;
-            mbar_arrive_expect_tx(&bar_v_full[vs], C::kKVBytes);
+          const int passes = dq_passes<kMod>(it);
+          for (int pass = 0; pass < passes; ++pass) {
+            for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+              if (!ok) return;
+              if (!mbar_wait(&bar_v_empty[vs], vph ^ 1u, &s_abort)) {
+                ok = false;
+                return;
+              }
+              const int row = it.g.kv_off + c * it.g.cbkv + j * kTile;
+              mbar_arrive_expect_tx(&bar_v_full[vs], C::kKVBytes);
 #pragma unroll
-            for (int hb = 0; hb < D / 64; ++hb)
-              tma_load_3d(smem_u32(sV + vs * C::kKVBytes + hb * 16384), &tmV, &bar_v_full[vs], hb * 64, it.kvh, row);
-            ++n_fill;
-            if (++vs == VS) {
-              vs = 0;
-              vph ^= 1u;
-            }
-          });
+              for (int hb = 0; hb < D / 64; ++hb)
+                tma_load_3d(smem_u32(sV + vs * C::kKVBytes + hb * 16384), &tmV, &bar_v_full[vs], hb * 64, it.kvh, row);
+              ++n_fill;
+              if (++vs == VS) {
+                vs = 0;
+                vph ^= 1u;
+              }
+            });
+          }
         }
         for (int s = 0; s < VS; ++s) {
           const uint32_t fills = n_fill > (uint32_t)s ? (n_fill - 1 - s) / VS + 1 : 0;
@@ -273,15 +299,17 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         uint32_t kph = 0, g = 0, q_iter = 0;
         bool ok = true;
         // issue dQ += dS K for tile gg (its dS in S buffer gg % 2, its K in ring slot gg % KS)
-        auto issue_dq = [&](uint32_t gg, int ncols, bool first) -> bool {
+        // (a pass for Delta alone has none: its S is read, and the slot is free)
+        auto issue_dq = [&](uint32_t gg, int ncols, bool first, bool delta_pass) -> bool {
           const uint32_t b = gg & 1u;
           if (!mbar_wait(&bar_ds_ready[b], (gg >> 1) & 1u, &s_abort)) return false;
           tc_fence_after();
           const int kslot = (int)(gg % KS);
           const uint64_t kd = kmn + (uint64_t)((kslot * C::kKVBytes) >> 4);
-          for (int kk = 0; kk < ncols / 16; ++kk)
-            mma_ts(tmem + C::kColDQ, tmem + b * 128u + C::ds_col(kk),
-                   kd + (uint64_t)(kk * (2048 >> 4)), idesc_dq, (first && kk == 0) ? 0u : 1u);
+          if (!delta_pass)
+            for (int kk = 0; kk < ncols / 16; ++kk)
+              mma_ts(tmem + C::kColDQ, tmem + b * 128u + C::ds_col(kk), kd + (uint64_t)(kk * (2048 >> 4)), idesc_dq,
+                     (first && kk == 0) ? 0u : 1u);
           tc_commit(&bar_k_empty[kslot]);  // the K slot's last reader
           return true;
         };
@@ -298,39 +326,43 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             tc_commit(&bar_q_empty);
             continue;
           }
-          int j = 0, prev_cols = 0;
-          for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
-            if (!ok) return;
-            const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
-            const uint32_t b = g & 1u;
-            if (!mbar_wait(&bar_k_full[ks], kph, &s_abort)) {
-              ok = false;
-              return;
-            }
-            tc_fence_after();
-            const uint32_t idesc_s = idesc_bf16(128, ncols, false, false);
-            const uint64_t kd = kdesc + (uint64_t)((ks * C::kKVBytes) >> 4);
+          const int passes = dq_passes<kMod>(it);
+          for (int pass = 0; ok && pass < passes; ++pass) {
+            const bool last = pass + 1 == passes;
+            int j = 0, prev_cols = 0;
+            for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
+              if (!ok) return;
+              const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
+              const uint32_t b = g & 1u;
+              if (!mbar_wait(&bar_k_full[ks], kph, &s_abort)) {
+                ok = false;
+                return;
+              }
+              tc_fence_after();
+              const uint32_t idesc_s = idesc_bf16(128, ncols, false, false);
+              const uint64_t kd = kdesc + (uint64_t)((ks * C::kKVBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + b * 128u, qdesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(&bar_s_full[b]);
-            if (j == n - 1) tc_commit(&bar_q_empty);  // the item's last read of Q
-            if (++ks == KS) {
-              ks = 0;
-              kph ^= 1u;
-            }
-            if (j > 0 && !issue_dq(g - 1, prev_cols, j == 1)) {
-              ok = false;
-              return;
-            }
-            prev_cols = ncols;
-            ++g;
-            ++j;
-          });
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + b * 128u, qdesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&bar_s_full[b]);
+              if (last && j == n - 1) tc_commit(&bar_q_empty);  // the item's last read of Q
+              if (++ks == KS) {
+                ks = 0;
+                kph ^= 1u;
+              }
+              if (j > 0 && !issue_dq(g - 1, prev_cols, j == 1, !last)) {
+                ok = false;
+                return;
+              }
+              prev_cols = ncols;
+              ++g;
+              ++j;
+            });
+            if (ok && !issue_dq(g - 1, prev_cols, n == 1, !last)) ok = false;
+          }
           if (!ok) break;
-          if (!issue_dq(g - 1, prev_cols, n == 1)) break;
           tc_commit(&bar_dq_done);
         }
         tc_commit(&bar_drain);
@@ -361,34 +393,38 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             tc_commit(&bar_q_empty);
             continue;
           }
-          int j = 0;
-          for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
-            if (!ok) return;
-            const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
-            // the dP buffer is free once the dS warps have read tile g-1's dP
-            if ((g > 0 && !mbar_wait(&bar_dp_free, (g - 1) & 1u, &s_abort)) ||
-                !mbar_wait(&bar_v_full[vs], vph, &s_abort)) {
-              ok = false;
-              return;
-            }
-            tc_fence_after();
-            const uint32_t idesc_p = idesc_bf16(128, ncols, false, false);
-            const uint64_t vd = vdesc + (uint64_t)((vs * C::kKVBytes) >> 4);
+          const int passes = dq_passes<kMod>(it);
+          for (int pass = 0; ok && pass < passes; ++pass) {
+            const bool last = pass + 1 == passes;
+            int j = 0;
+            for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
+              if (!ok) return;
+              const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
+              // the dP buffer is free once the dS warps have read tile g-1's dP
+              if ((g > 0 && !mbar_wait(&bar_dp_free, (g - 1) & 1u, &s_abort)) ||
+                  !mbar_wait(&bar_v_full[vs], vph, &s_abort)) {
+                ok = false;
+                return;
+              }
+              tc_fence_after();
+              const uint32_t idesc_p = idesc_bf16(128, ncols, false, false);
+              const uint64_t vd = vdesc + (uint64_t)((vs * C::kKVBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              mma_ss(tmem + C::kColDP, dodesc + off, vd + off, idesc_p, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(&bar_dp_full);
-            tc_commit(&bar_v_empty[vs]);
-            if (j == n - 1) tc_commit(&bar_q_empty);  // the item's last read of dO
-            if (++vs == VS) {
-              vs = 0;
-              vph ^= 1u;
-            }
-            ++g;
-            ++j;
-          });
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + C::kColDP, dodesc + off, vd + off, idesc_p, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&bar_dp_full);
+              tc_commit(&bar_v_empty[vs]);
+              if (last && j == n - 1) tc_commit(&bar_q_empty);  // the item's last read of dO
+              if (++vs == VS) {
+                vs = 0;
+                vph ^= 1u;
+              }
+              ++g;
+              ++j;
+            });
+          }
         }
         tc_commit(&bar_drain2);
         drain_wait(&bar_drain2, 0);
@@ -409,7 +445,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     const float sl2 = p.scale_log2;
     // dQ rows start at multiples of 128 bytes: 32-byte stores when dQ is 32-byte aligned
     const bool dq_v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
-    uint32_t g = 0, n_item = 0;
+    uint32_t g = 0, n_item = 0, n_eps = 0;
     int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
@@ -427,7 +463,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
       const int64_t grow = (int64_t)it.g.q_off + pos;
       // this row's lse (log2 units) and Delta; rows without a valid query mask
       // every key, so their values never matter
-      const float dlt = valid ? p.delta[(int64_t)it.h * p.T_q + grow] : 0.f;
+      float dlt = valid ? p.delta[(int64_t)it.h * p.T_q + grow] : 0.f;
       const float lse2 = valid ? p.lse2[(int64_t)it.h * p.T_q + grow] : 0.f;
       // scored: the keys this row sees, and its score function
       int2 sees = make_int2(0, 0);
@@ -437,155 +473,201 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         sc = score_consts<kMod, false>(p, it.h);
       }
       int jl = 0;
-      for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
-        if (!ok) return;
-        const uint32_t b = g & 1u;
-        if (!mbar_wait(&bar_s_full[b], (g >> 1) & 1u, &s_abort) || !mbar_wait(&bar_dp_full, g & 1u, &s_abort)) {
-          ok = false;
-          return;
-        }
-        tc_fence_after();
-        const int j0 = c * it.g.cbkv + j * kTile;
-        int cnt = 0, from = 0;  // the row sees columns [from, cnt)
-        if (valid) {
-          cnt = imin(kTile, (c + 1) * it.g.cbkv - j0);
-          if constexpr (kMod != 0) {
-            cnt = imin(cnt, sees.y - j0);
-            from = sees.x - j0;
-          } else {
-            cnt = imin(cnt, it.g.Lkv - j0);
-            if (p.causal) cnt = imin(cnt, pos + it.g.koff - j0 + 1);
+      const int passes = dq_passes<kMod>(it);
+      for (int pass = 0; ok && pass < passes; ++pass) {
+        const bool last = pass + 1 == passes;
+        float eps = 0.f;  // this thread's part of the row sum of P (dP - Delta)
+        for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+          if (!ok) return;
+          const uint32_t b = g & 1u;
+          if (!mbar_wait(&bar_s_full[b], (g >> 1) & 1u, &s_abort) || !mbar_wait(&bar_dp_full, g & 1u, &s_abort)) {
+            ok = false;
+            return;
           }
-          cnt = imax(cnt, 0);
-        }
-        const int ahead = pos + it.g.koff - j0 + 1;  // scored: columns up to the row's own position
-        const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
-        const int nch = ceil_div(q_tile_ncols<kMod>(it, p, c, j), 32);
-        const uint32_t scol = tmem + lane_base + b * 128u;
-        const uint32_t pcol = tmem + lane_base + C::kColDP;
-        // dP of this thread's chunks first, so the buffer can take the
-        // next tile's dP while dS is computed
-        uint32_t dr[kCh][32];
-#pragma unroll
-        for (int kk = 0; kk < kCh; ++kk)
-          if (kCh * part + kk < nch) tmem_ld32(pcol + 32 * (kCh * part + kk), dr[kk]);
-#pragma unroll
-        for (int kk = 0; kk < kCh; ++kk)
-          if (kCh * part + kk < nch) tmem_ld_wait(dr[kk]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_dp_free);
-        if constexpr (kMod != 0) {
-          // dS = P (dP - Delta) (1 - tanh^2), in place over the scores; then 0 on
-          // the keys this row may not see, whatever stood there
-          constexpr bool kCap = (kMod & kModCap) != 0;
-          uint32_t pk[kCh][16];
-          // chunk ch of S, with the cap's masked columns at 0; true if any is masked
-          auto load = [&](float(&y)[32], int ch) {
-            uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
-            tmem_ld32(scol + 32 * ch, sr);
-            tmem_ld_wait(sr);
-            const bool cut = __any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch);
-            if (kCap && cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
-            return cut;
-          };
-          auto measure = [&]() {
-            float am = 0.f, y[32];
-#pragma unroll
-            for (int kk = 0; kk < kCh; ++kk) {
-              if (kCh * part + kk < nch) {
-                load(y, kCh * part + kk);
-                am = fmaxf(am, score_abs_max(y));
-              }
+          tc_fence_after();
+          const int j0 = c * it.g.cbkv + j * kTile;
+          int cnt = 0, from = 0;  // the row sees columns [from, cnt)
+          if (valid) {
+            cnt = imin(kTile, (c + 1) * it.g.cbkv - j0);
+            if constexpr (kMod != 0) {
+              cnt = imin(cnt, sees.y - j0);
+              from = sees.x - j0;
+            } else {
+              cnt = imin(cnt, it.g.Lkv - j0);
+              if (p.causal) cnt = imin(cnt, pos + it.g.koff - j0 + 1);
             }
-            return cap_form(am, sc);
-          };
-          auto run = [&](auto form) {
-            float am = 0.f;
+            cnt = imax(cnt, 0);
+          }
+          const int ahead = pos + it.g.koff - j0 + 1;  // scored: columns up to the row's own position
+          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          const int nch = ceil_div(q_tile_ncols<kMod>(it, p, c, j), 32);
+          const uint32_t scol = tmem + lane_base + b * 128u;
+          const uint32_t pcol = tmem + lane_base + C::kColDP;
+          // dP of this thread's chunks first, so the buffer can take the
+          // next tile's dP while dS is computed
+          uint32_t dr[kCh][32];
+#pragma unroll
+          for (int kk = 0; kk < kCh; ++kk)
+            if (kCh * part + kk < nch) tmem_ld32(pcol + 32 * (kCh * part + kk), dr[kk]);
+#pragma unroll
+          for (int kk = 0; kk < kCh; ++kk)
+            if (kCh * part + kk < nch) tmem_ld_wait(dr[kk]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_dp_free);
+          if constexpr (kMod != 0) {
+            // dS = P (dP - Delta) (1 - tanh^2), in place over the scores, and the row
+            // sum of P (dP - Delta); on the keys this row may not see P = 2^-inf = 0
+            // against dP = 0, and dS is set to 0, whatever stood there
+            constexpr bool kCap = (kMod & kModCap) != 0;
+            uint32_t pk[kCh][16];
+            // chunk ch of S, with the cap's masked columns at 0; true if any is masked
+            auto load = [&](float(&y)[32], int ch) {
+              uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
+              tmem_ld32(scol + 32 * ch, sr);
+              tmem_ld_wait(sr);
+              const bool cut = __any_sync(0xffffffffu, cnt < 32 * ch + 32 || from > 32 * ch);
+              if (kCap && cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+              return cut;
+            };
+            auto measure = [&]() {
+              float am = 0.f, y[32];
+#pragma unroll
+              for (int kk = 0; kk < kCh; ++kk) {
+                if (kCh * part + kk < nch) {
+                  load(y, kCh * part + kk);
+                  am = fmaxf(am, score_abs_max(y));
+                }
+              }
+              return cap_form(am, sc);
+            };
+            float es[2];
+            auto run = [&](auto form) {
+              float am = 0.f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) es[i] = 0.f;
+#pragma unroll
+              for (int kk = 0; kk < kCh; ++kk) {
+                const int ch = kCh * part + kk;  // this thread's 32-column chunk
+                if (ch < nch) {
+                  float y[32];
+                  const bool cut = load(y, ch);
+                  if constexpr (kCap) {
+                    am = fmaxf(am, score_abs_max(y));
+                    cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f, 0.f);
+                  }
+                  if (cut) {
+                    score_fill(y, from - 32 * ch, cnt - 32 * ch, -INFINITY);
+                    score_fill(reinterpret_cast<float(&)[32]>(dr[kk]), from - 32 * ch, cnt - 32 * ch, 0.f);
+                  }
+                  const float a = kCap ? sc.cap_a : sl2;
+                  auto write_ds = [&](auto bias) {
+#pragma unroll
+                    for (int n = 0; n < 32; n += 2) {
+                      float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
+                      if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
+                      ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                      fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
+                      fmul2(t0, t1, ex2(x0), ex2(x1), t0, t1);
+                      fadd2(es[0], es[1], es[0], es[1], t0, t1);
+                      if constexpr (kCap) {
+                        float w0, w1;
+                        ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                        fmul2(y[n], y[n + 1], t0, t1, w0, w1);
+                      } else {
+                        y[n] = t0, y[n + 1] = t1;
+                      }
+                    }
+                  };
+                  const float d0 = (float)(ahead - 1 - 32 * ch);
+                  if ((kMod & kModDist) != 0 && abs_needed)
+                    write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
+                  else
+                    write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
+                  if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+#pragma unroll
+                  for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
+                  // over columns already read
+                  if (!kCap && last) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
+                }
+              }
+              return kCap ? cap_form(am, sc) : kCapNear;
+            };
+            if constexpr (kCap) {
+              cap_with_hint(hint, measure, run);
+#pragma unroll
+              for (int kk = 0; kk < kCh; ++kk)
+                if (last && kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
+            } else {
+              run(CapForm<kCapNear>{});
+            }
+            eps += es[0] + es[1];
+          } else {
 #pragma unroll
             for (int kk = 0; kk < kCh; ++kk) {
               const int ch = kCh * part + kk;  // this thread's 32-column chunk
               if (ch < nch) {
-                float y[32];
-                const bool cut = load(y, ch);
-                if constexpr (kCap) {
-                  am = fmaxf(am, score_abs_max(y));
-                  cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f, 0.f);
+                uint32_t sr[32];
+                tmem_ld32(scol + 32 * ch, sr);
+                tmem_ld_wait(sr);
+                // keys this row may not see get S = -inf: P = 0 and dS = 0
+                if (__any_sync(0xffffffffu, cnt < 32 * ch + 32)) {
+#pragma unroll
+                  for (int n = 0; n < 32; ++n)
+                    if (32 * ch + n >= cnt) sr[n] = __float_as_uint(-INFINITY);
                 }
-                const float a = kCap ? sc.cap_a : sl2;
-                auto write_ds = [&](auto bias) {
+                uint32_t pk[16];
 #pragma unroll
-                  for (int n = 0; n < 32; n += 2) {
-                    float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
-                    if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
-                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
-                    fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
-                    if constexpr (kCap) {
-                      float w0, w1;
-                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
-                      fmul2(t0, t1, t0, t1, w0, w1);
-                    }
-                    fmul2(y[n], y[n + 1], ex2(x0), ex2(x1), t0, t1);
-                  }
-                };
-                const float d0 = (float)(ahead - 1 - 32 * ch);
-                if ((kMod & kModDist) != 0 && abs_needed)
-                  write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
-                else
-                  write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
-                if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
-#pragma unroll
-                for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
-                // over columns already read
-                if (!kCap) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
+                for (int n = 0; n < 16; ++n) {
+                  float x0, x1, t0, t1, g0, g1;
+                  ffma2(x0, x1, __uint_as_float(sr[2 * n]), __uint_as_float(sr[2 * n + 1]), sl2, sl2, -lse2, -lse2);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  fadd2(t0, t1, __uint_as_float(dr[kk][2 * n]), __uint_as_float(dr[kk][2 * n + 1]), -dlt, -dlt);
+                  fmul2(g0, g1, p0, p1, t0, t1);
+                  pk[n] = pack_bf16x2(g0, g1);
+                }
+                tmem_st16(scol + C::ds_col(2 * ch), pk);
               }
             }
-            return kCap ? cap_form(am, sc) : kCapNear;
-          };
-          if constexpr (kCap) {
-            cap_with_hint(hint, measure, run);
-#pragma unroll
-            for (int kk = 0; kk < kCh; ++kk)
-              if (kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
-          } else {
-            run(CapForm<kCapNear>{});
           }
-        } else {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();  // every lane's dS is in TMEM and dP was read: one arrival speaks for the warp
+          if (lane == 0) mbar_arrive(&bar_ds_ready[b]);  // dS of tile g is in TMEM
+          ++g;
+          ++jl;
+        });
+        if constexpr (kMod != 0) {
+          // the row's warpgroups add their parts up, in a fixed order: the last
+          // exchange's sum has been read; the parts are there; the sum is there
+          if (ok && jl > 0) {
+            uint64_t* bar = &bar_eps[warp & 3];
+            auto sync = [&]() {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar);
+              ok = ok && mbar_wait(bar, n_eps++ & 1u, &s_abort);
+            };
+            sync();
+            if (part > 0) s_eps[part - 1][row] = eps;
+            sync();
+            if (part == 0) {
 #pragma unroll
-          for (int kk = 0; kk < kCh; ++kk) {
-            const int ch = kCh * part + kk;  // this thread's 32-column chunk
-            if (ch < nch) {
-              uint32_t sr[32];
-              tmem_ld32(scol + 32 * ch, sr);
-              tmem_ld_wait(sr);
-              // keys this row may not see get S = -inf: P = 0 and dS = 0
-              if (__any_sync(0xffffffffu, cnt < 32 * ch + 32)) {
-#pragma unroll
-                for (int n = 0; n < 32; ++n)
-                  if (32 * ch + n >= cnt) sr[n] = __float_as_uint(-INFINITY);
-              }
-              uint32_t pk[16];
-#pragma unroll
-              for (int n = 0; n < 16; ++n) {
-                float x0, x1, t0, t1, g0, g1;
-                ffma2(x0, x1, __uint_as_float(sr[2 * n]), __uint_as_float(sr[2 * n + 1]), sl2, sl2, -lse2, -lse2);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                fadd2(t0, t1, __uint_as_float(dr[kk][2 * n]), __uint_as_float(dr[kk][2 * n + 1]), -dlt, -dlt);
-                fmul2(g0, g1, p0, p1, t0, t1);
-                pk[n] = pack_bf16x2(g0, g1);
-              }
-              tmem_st16(scol + C::ds_col(2 * ch), pk);
+              for (int i = 1; i < C::kGroups; ++i) eps += s_eps[i - 1][row];
+              s_eps[0][row] = eps;
             }
+            sync();
+            dlt += s_eps[0][row];
           }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();  // every lane's dS is in TMEM and dP was read: one arrival speaks for the warp
-        if (lane == 0) mbar_arrive(&bar_ds_ready[b]);  // dS of tile g is in TMEM
-        ++g;
-        ++jl;
-      });
-      if (!ok) break;
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if constexpr (kMod != 0) {
+        // the exact Delta, for the dK/dV kernel (every warpgroup has read the old one)
+        if (jl > 0 && valid && part == 0) p.delta_out[(int64_t)it.h * p.T_q + grow] = dlt;
+      }
       // ---- epilogue: dQ * scale as bf16; zero on rows without a valid query
       if (jl > 0) {
         if (!mbar_wait(&bar_dq_done, n_item & 1u, &s_abort)) break;
