@@ -9,9 +9,7 @@
 // eight columns of a row 16 bits each: counter (column / 8, row, offset),
 // key = seed; column 8 g + 2 w + h takes half h of word w.  Sixteen bits set
 // the drop probability in steps of 2^-16 (the scale goes by the rounded
-// probability, so the mean is exact) at half the generator's work of 32: a
-// call is about 90 instructions, and at 32 bits an element the bf16 backward
-// (4 bytes an element) would be bound by them instead of by HBM.
+// probability, so the mean is exact) at half the generator's work of 32.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -22,8 +20,8 @@ namespace thd {
 constexpr int kDropThreads = 256;
 constexpr int kDropBatch = 4;  // groups of eight columns a thread has in flight
 
-// Bit e of the result: column 8 g + e of the row is kept.
-__device__ inline uint32_t keep_mask(uint32_t g, uint32_t row, uint64_t offset, uint64_t seed, uint32_t drop) {
+// The four words of columns 8 g .. 8 g + 7 of a row.
+__device__ inline uint4 draw(uint32_t g, uint32_t row, uint64_t offset, uint64_t seed) {
   uint32_t c0 = g, c1 = row, c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
@@ -36,12 +34,18 @@ __device__ inline uint32_t keep_mask(uint32_t g, uint32_t row, uint64_t offset, 
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  const uint32_t w[4] = {c0, c1, c2, c3};
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// Bit e of the result: column 8 g + e is kept (16 bits at least `drop`; the
+// comparisons are of the words against drop << 16, the low halves shifted up).
+__device__ inline uint32_t keep_mask(const uint4& v, uint32_t drop16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    m |= ((w[k] & 0xffffu) >= drop ? 1u : 0u) << (2 * k);
-    m |= ((w[k] >> 16) >= drop ? 1u : 0u) << (2 * k + 1);
+    m |= (w[k] << 16 >= drop16 ? 1u : 0u) << (2 * k);
+    m |= (w[k] >= drop16 ? 1u : 0u) << (2 * k + 1);
   }
   return m;
 }
@@ -92,49 +96,48 @@ struct Vec8<float> {
 };
 
 // C a multiple of 8 and 16-byte aligned tensors: a thread moves groups of
-// eight columns with 16-byte accesses, kDropBatch of them in flight.
+// eight columns with 16-byte accesses, kDropBatch of them in flight while it
+// draws their bits.
 template <typename E, bool kResidual>
 __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const DropoutParams p) {
-  const uint64_t seed = p.rng[0], offset = p.rng[1];
-  const uint32_t G = (uint32_t)(p.C / 8);
-  const int64_t total = p.T * (int64_t)G;
-  const int64_t base = (int64_t)blockIdx.x * (kDropThreads * kDropBatch);
-  const int64_t row0 = base / G;
-  const uint32_t rem0 = (uint32_t)(base - row0 * G);
+  const int64_t total = p.T * (int64_t)p.G;
+  const int64_t base = (int64_t)blockIdx.x * (kDropThreads * kDropBatch) + threadIdx.x;
   Vec8<E> x[kDropBatch], r[kDropBatch];
-  uint32_t keep[kDropBatch];
 #pragma unroll
   for (int k = 0; k < kDropBatch; ++k) {
-    const uint32_t i = k * kDropThreads + threadIdx.x;
-    if (base + i < total) {
-      x[k].load(static_cast<const E*>(p.x) + 8 * (base + i));
-      if (kResidual) r[k].load(static_cast<const E*>(p.residual) + 8 * (base + i));
+    const int64_t i = base + k * kDropThreads;
+    if (i < total) {
+      x[k].load(static_cast<const E*>(p.x) + 8 * i);
+      if (kResidual) r[k].load(static_cast<const E*>(p.residual) + 8 * i);
     }
   }
+  const uint64_t seed = p.rng[0], offset = p.rng[1];
+  const uint32_t drop16 = p.drop << 16;
+  int64_t row = base / p.G;
+  uint32_t g = (uint32_t)(base - row * p.G);
 #pragma unroll
   for (int k = 0; k < kDropBatch; ++k) {
-    const uint32_t i = k * kDropThreads + threadIdx.x;
-    if (base + i < total) {
-      const uint32_t at = rem0 + i, dr = at / G;
-      const int64_t row = row0 + dr;
-      const uint32_t id = p.row_ids ? (uint32_t)p.row_ids[row] : (uint32_t)row;
-      keep[k] = keep_mask(at - dr * G, id, offset, seed, p.drop);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kDropBatch; ++k) {
-    const uint32_t i = k * kDropThreads + threadIdx.x;
-    if (base + i < total) {
-      float f[8], g[8];
+    const int64_t i = base + k * kDropThreads;
+    if (i < total) {
+      const uint4 w4 = draw(g, p.row_ids ? (uint32_t)p.row_ids[row] : (uint32_t)row, offset, seed);
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      float f[8], h[8];
       x[k].get(f);
-      if (kResidual) r[k].get(g);
+      if (kResidual) r[k].get(h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f[e] = (keep[k] >> e) & 1u ? f[e] * p.scale : 0.f;
-        if (kResidual) f[e] += g[e];
+        const bool keep = (e & 1 ? w[e / 2] : w[e / 2] << 16) >= drop16;  // the half against drop
+        f[e] = keep ? f[e] * p.scale : 0.f;
+        if (kResidual) f[e] += h[e];
       }
       x[k].set(f);
-      x[k].store(static_cast<E*>(p.out) + 8 * (base + i));
+      x[k].store(static_cast<E*>(p.out) + 8 * i);
+    }
+    row += p.step_rows;  // kDropThreads groups on
+    g += p.step_groups;
+    if (g >= p.G) {
+      g -= p.G;
+      ++row;
     }
   }
 }
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
     }
   }
   const uint32_t id = p.row_ids ? (uint32_t)p.row_ids[row] : (uint32_t)row;
-  const uint32_t mine = keep_mask((uint32_t)(c0 / 8) + lane, id, offset, seed, p.drop);
+  const uint32_t mine = keep_mask(draw((uint32_t)(c0 / 8) + lane, id, offset, seed), p.drop << 16);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t m = __shfl_sync(0xffffffffu, mine, 4 * k + (lane >> 3));
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
 }
 
 template <typename E, bool kResidual>
-static cudaError_t launch_dropout_t(const DropoutParams& p, cudaStream_t st) {
+static cudaError_t launch_dropout_t(DropoutParams p, cudaStream_t st) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out) |
                       reinterpret_cast<uintptr_t>(p.residual);
   const bool vec = p.C % 8 == 0 && (a & 15u) == 0;
@@ -188,6 +191,11 @@ static cudaError_t launch_dropout_t(const DropoutParams& p, cudaStream_t st) {
   const int per_block = vec ? kDropThreads * kDropBatch : kDropThreads;
   const int64_t grid = (work + per_block - 1) / per_block;
   if (grid >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  if (vec) {
+    p.G = (uint32_t)(p.C / 8);
+    p.step_rows = kDropThreads / p.G;
+    p.step_groups = kDropThreads % p.G;
+  }
   prof_before(THD_KERNEL_DROPOUT, st);
   if (vec)
     dropout_vec_kernel<E, kResidual><<<(unsigned)grid, kDropThreads, 0, st>>>(p);

@@ -16,6 +16,7 @@ struct DropoutParams {
   int64_t T, C;
   uint32_t drop;  // drop where the 16 random bits are below this
   float scale;    // 65536 / (65536 - drop)
+  uint32_t G, step_rows, step_groups;  // vector path: C / 8; kDropThreads groups on, in rows and groups
 };
 
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, cudaStream_t st);

@@ -16,9 +16,12 @@
 // What bounds it: HBM.  Every element is read and written once; a token's
 // cosines and sines are computed once and shared by all of its heads (40 heads
 // of 128 elements cost 64 sincos).  A block takes a few tokens with all their
-// heads: first one thread per (token, pair) leaves cos and sin in shared
-// memory, then a thread keeps one (token, 8 pairs) in registers and walks the
-// heads, kRopeBatch heads' 16-byte loads in flight at once.
+// heads: a thread keeps one (token, 8 pairs) and walks the heads, the loads of
+// its first ones in flight while one thread per (token, pair) leaves cos and
+// sin in shared memory.  Measured on one GB300, inputs larger than L2: 131,072
+// tokens of 32 + 8 heads of 128, bf16, 394 us (6816 GB/s, the rate of a plain
+// copy); with the loads after the angles, and both as floats (122 registers, two
+// blocks per SM instead of three), 675 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -27,8 +30,8 @@
 namespace thd {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;     // heads a thread has in flight
 constexpr int kRopeMinTokens = 4;  // tokens per block, at least
+constexpr int kRopeHeads = 4;      // heads a thread walks, at least, where a token has as many
 
 // cos and sin of the angle of pair i at token t
 __device__ inline float2 rope_cos_sin(const RopeParams& p, int64_t t, int i) {
@@ -40,102 +43,133 @@ __device__ inline float2 rope_cos_sin(const RopeParams& p, int64_t t, int i) {
   return make_float2(c, p.inverse ? -s : s);
 }
 
-// Eight consecutive elements.
-__device__ inline void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive elements, as loaded.
+template <typename E>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 v;
+  __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
   }
-}
-__device__ inline void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ inline void store8(uint16_t* p, const float (&v)[8]) {
-  uint32_t w[4];
+  __device__ void set(const float (&f)[8]) {
+    uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ inline void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
 
 // 16-byte vectors: D a multiple of 8, rot of 16 (halves) or 8 (adjacent
 // pairs), every row 16-byte aligned.  A unit is what one thread moves of a
 // head: 8 pairs from two vectors (halves), 4 pairs from one (adjacent), or one
-// vector past rot that is copied.
+// vector past rot that is copied.  Query and key heads are one list.
 template <typename E, bool kAdjacent>
-__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_constant__ RopeParams p, int units,
-                                                                int slots, int tokens) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_vec_kernel(const __grid_constant__ RopeParams p, int units,
+                                                                   int slots, int tokens) {
   extern __shared__ float2 s_cs[];  // [tokens][rot / 2]
   const int half = p.rot / 2, tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * tokens;
   const int nt = (int)(p.T - t0 < tokens ? p.T - t0 : tokens);
-  for (int i = tid; i < nt * half; i += kRopeThreads) {
-    const int tl = i / half;
-    s_cs[i] = rope_cos_sin(p, t0 + tl, i - tl * half);
-  }
-  __syncthreads();
   const int group = tid / units, u = tid - group * units;
   const int tl = group / slots, slot = group - tl * slots;  // `slots` heads of a token side by side
-  if (tl >= nt) return;
-  const int64_t t = t0 + tl;
+  const bool works = tl < nt;
+  const int64_t t = t0 + (works ? tl : 0);
   const int rot_units = kAdjacent ? p.rot / 8 : p.rot / 16;
   const bool rotates = u < rot_units;
   const int c0 = rotates ? 8 * u : p.rot + 8 * (u - rot_units);
+  const int heads = works ? p.x[0].H + p.x[1].H : 0;
+  const E* in[2];
+  E* out[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {  // key heads follow the queries'
+    const int64_t first = w == 0 ? 0 : -(int64_t)p.x[0].H * p.D;
+    in[w] = static_cast<const E*>(p.x[w].in) + t * p.x[w].in_stride + first + c0;
+    out[w] = static_cast<E*>(p.x[w].out) + t * p.x[w].out_stride + first + c0;
+  }
+  constexpr int kBatch = sizeof(E) == 2 ? 4 : 2;  // heads in flight: 32 registers of loads
+  Raw8<E> a[kBatch], b[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h0 + k * slots;
+      if (h < heads) {
+        const E* src = (h < p.x[0].H ? in[0] : in[1]) + (int64_t)h * p.D;
+        a[k].load(src);
+        if (!kAdjacent && rotates) b[k].load(src + half);
+      }
+    }
+  };
+  load(slot);  // in flight while the angles are made
+  for (int i = tid; i < nt * half; i += kRopeThreads) {
+    const int il = i / half;
+    s_cs[i] = rope_cos_sin(p, t0 + il, i - il * half);
+  }
+  __syncthreads();
   constexpr int kPairs = kAdjacent ? 4 : 8;
   float2 cs[kPairs];
-  if (rotates) {
 #pragma unroll
-    for (int k = 0; k < kPairs; ++k) cs[k] = s_cs[tl * half + kPairs * u + k];
-  }
+  for (int k = 0; k < kPairs; ++k) cs[k] = rotates && works ? s_cs[tl * half + kPairs * u + k] : make_float2(1.f, 0.f);
+  for (int h0 = slot; h0 < heads; h0 += slots * kBatch) {
+    if (h0 != slot) load(h0);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const RopeTensor& x = p.x[w];
-    const E* in = static_cast<const E*>(x.in) + t * x.in_stride + c0;
-    E* out = static_cast<E*>(x.out) + t * x.out_stride + c0;
-    for (int h0 = slot; h0 < x.H; h0 += slots * kRopeBatch) {
-      float a[kRopeBatch][8], b[kRopeBatch][8];
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h0 + k * slots;
+      if (h >= heads) break;
+      E* dst = (h < p.x[0].H ? out[0] : out[1]) + (int64_t)h * p.D;
+      if (rotates) {
+        float x[8], y[8];
+        a[k].get(x);
+        if constexpr (kAdjacent) {
 #pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
-        const int h = h0 + k * slots;
-        if (h < x.H) {
-          load8(in + h * p.D, a[k]);
-          if (!kAdjacent && rotates) load8(in + h * p.D + half, b[k]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
-        const int h = h0 + k * slots;
-        if (h >= x.H) break;
-        if (rotates) {
-          if constexpr (kAdjacent) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float r = a[k][2 * e], i = a[k][2 * e + 1];
-              a[k][2 * e] = r * cs[e].x - i * cs[e].y;
-              a[k][2 * e + 1] = i * cs[e].x + r * cs[e].y;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float r = a[k][e], i = b[k][e];
-              a[k][e] = r * cs[e].x - i * cs[e].y;
-              b[k][e] = i * cs[e].x + r * cs[e].y;
-            }
-            store8(out + h * p.D + half, b[k]);
+          for (int e = 0; e < 4; ++e) {
+            const float r = x[2 * e], i = x[2 * e + 1];
+            x[2 * e] = r * cs[e].x - i * cs[e].y;
+            x[2 * e + 1] = i * cs[e].x + r * cs[e].y;
           }
+        } else {
+          b[k].get(y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float r = x[e], i = y[e];
+            x[e] = r * cs[e].x - i * cs[e].y;
+            y[e] = i * cs[e].x + r * cs[e].y;
+          }
+          b[k].set(y);
+          b[k].store(dst + half);
         }
-        store8(out + h * p.D, a[k]);
+        a[k].set(x);
       }
+      a[k].store(dst);
     }
   }
 }
@@ -189,7 +223,7 @@ static bool vec_ok(const RopeTensor& x, int esize) {
 
 template <typename E, bool kAdjacent>
 static cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t st) {
-  const int heads = p.x[0].H > p.x[1].H ? p.x[0].H : p.x[1].H;
+  const int heads = p.x[0].H + p.x[1].H;
   const bool vec = p.D % 8 == 0 && p.rot % (kAdjacent ? 8 : 16) == 0 && vec_ok(p.x[0], sizeof(E)) &&
                    vec_ok(p.x[1], sizeof(E));
   prof_before(THD_KERNEL_ROPE, st);
@@ -197,7 +231,8 @@ static cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t st) {
     const int units = (kAdjacent ? p.rot / 8 : p.rot / 16) + (p.D - p.rot) / 8;
     const int groups = kRopeThreads / units;
     int slots = groups / kRopeMinTokens;
-    slots = slots < 1 ? 1 : (slots > heads ? heads : slots);
+    if (slots > (heads + kRopeHeads - 1) / kRopeHeads) slots = (heads + kRopeHeads - 1) / kRopeHeads;
+    if (slots < 1) slots = 1;
     const int tokens = groups / slots;
     const size_t smem = sizeof(float2) * (size_t)tokens * (p.rot / 2);
     rope_vec_kernel<E, kAdjacent><<<(unsigned)((p.T + tokens - 1) / tokens), kRopeThreads, smem, st>>>(
