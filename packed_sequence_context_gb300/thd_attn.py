@@ -143,10 +143,17 @@ def _h(a):
     return a.ctypes.data
 
 
+_RAW_STREAM = None
+
+
 def _s(stream):
     if stream is None:
+        global _RAW_STREAM
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _RAW_STREAM is None:  # the handle without a Stream object around it (0.1 us instead of 3), where torch has it
+            _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        return _RAW_STREAM(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -344,18 +351,20 @@ def _need(where: str, ok: bool):
 
 def _dtype(where: str, t) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return THD_DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return THD_DTYPE_FP32
     raise ThdError(where, THD_ERR_UNSUPPORTED)
 
 
-def _current(where: str, t):
-    """The tensor must be on the current CUDA device: that is where the
-    library launches."""
+def _current(where: str, t) -> int:
+    """The tensor's device index; it must be the current CUDA device, where
+    the library launches."""
     import torch
-    _need(where, t.is_cuda and t.device.index == torch.cuda.current_device())
+    dev = t.get_device()  # -1 on the CPU
+    _need(where, dev >= 0 and dev == torch.cuda.current_device())
+    return dev
 
 
 def _workspace(nbytes, device):
@@ -454,19 +463,28 @@ def _score_checks(w, q, k, v, more, offsets, dist_slopes, doc_q, doc_kv, prefix_
     """What the library cannot see of a scored call: types, shapes, layout and
     device of its tensors.  `more`: (tensor, shape, dtype) triples."""
     import torch
-    _current(w, q)
+    dev = _current(w, q)
     _need(w, q.dim() == 3 and k.dim() == 3)
-    (T_q, Hq, D), (T_kv, Hkv, _) = q.shape, k.shape
+    qs, ks = q.shape, k.shape
     B = offsets[0].numel() - 1
-    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    triples = [(q, (T_q, Hq, D), bf16), (k, (T_kv, Hkv, D), bf16), (v, (T_kv, Hkv, D), bf16),
-               (dist_slopes, (Hq,), f32), (doc_q, (T_q,), i32), (doc_kv, (T_kv,), i32), (prefix_len, (B,), i32)]
-    triples += [(c, (B + 1,), i32) for c in offsets] + more
-    dev = q.device
-    for t, shape, dtype in triples:
+    bf16, i32 = torch.bfloat16, torch.int32
+    triples = [(q, qs, bf16), (k, (ks[0], ks[1], qs[2]), bf16), (v, ks, bf16), *more]
+    for t in offsets:
         if t is not None:
-            _need(w, t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous())
-    return B, T_q, T_kv, Hq, Hkv, D
+            triples.append((t, (B + 1,), i32))
+    if dist_slopes is not None:
+        triples.append((dist_slopes, (qs[1],), torch.float32))
+    if doc_q is not None:
+        triples.append((doc_q, (qs[0],), i32))
+    if doc_kv is not None:
+        triples.append((doc_kv, (ks[0],), i32))
+    if prefix_len is not None:
+        triples.append((prefix_len, (B,), i32))
+    for t, shape, dtype in triples:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                                  and t.is_contiguous()):
+            _need(w, False)
+    return B, qs[0], ks[0], qs[1], ks[1], qs[2]
 
 
 def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None, cu_seqlens_kv_padded=None, *,
@@ -478,8 +496,8 @@ def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=Non
     (prefix_len int32 [B]).  Returns (o, lse, dev_status)."""
     import torch
     w = "thd_attn_score_fwd"
-    more = [(out, q.shape, torch.bfloat16), (lse, (q.shape[1], q.shape[0]), torch.float32),
-            (dev_status, (1,), torch.int32)]
+    more = [] if out is None and lse is None and dev_status is None else \
+        [(out, q.shape, torch.bfloat16), (lse, (q.shape[1], q.shape[0]), torch.float32), (dev_status, (1,), torch.int32)]
     B, T_q, T_kv, Hq, Hkv, D = _score_checks(
         w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
         doc_q, doc_kv, prefix_len)
@@ -636,12 +654,13 @@ def attn_bwd_a2a(q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_padded, *, cp_siz
     return dq, dk, dv, st
 
 
-def _rope_rows(t, H, D):
-    """Rows of [H, D] whose heads are contiguous: their stride in elements, or
-    None.  A dimension of size 1 may carry any stride."""
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
-        return None
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), H * D)
+def _rope_rows(where, like, t, T, H, D):
+    """The stride, in elements, of rows of [H, D] whose heads are contiguous.
+    A dimension of size 1 may carry any stride."""
+    _need(where, t.shape == (T, H, D) and t.dtype is like.dtype and t.get_device() == like.get_device())
+    s0, s1, s2 = t.stride()
+    _need(where, (s2 == 1 or D == 1) and (s1 == D or H == 1))
+    return s0 if T > 1 else max(s0, H * D)
 
 
 def rope(q, k, positions, inv_freq, axis_of=None, *, adjacent=False, inverse=False, q_out=None, k_out=None,
@@ -657,30 +676,31 @@ def rope(q, k, positions, inv_freq, axis_of=None, *, adjacent=False, inverse=Fal
     import torch
     w = "thd_rope"
     T, Hq, D = q.shape
-    _current(w, q)
+    dev = _current(w, q)
     dt = _dtype(w, q)
     inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
     axis = np.zeros(inv.size, np.uint8) if axis_of is None else np.ascontiguousarray(axis_of, dtype=np.uint8)
     n_axes = positions.shape[0] if positions.dim() == 2 else 1
-    _need(w, inv.ndim == 1 and axis.shape == inv.shape and positions.dtype == torch.int32 and
-          positions.is_contiguous() and positions.shape[-1] == T and positions.device == q.device)
-    qo = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    Hkv, ko = 0, None
+    _need(w, inv.ndim == 1 and axis.shape == inv.shape and positions.dtype is torch.int32 and
+          positions.shape[-1] == T and positions.get_device() == dev and positions.is_contiguous())
+    s_q, s_qo = _rope_rows(w, q, q, T, Hq, D), Hq * D
+    if q_out is None:
+        q_out = q.new_empty((T, Hq, D))
+    else:
+        s_qo = _rope_rows(w, q, q_out, T, Hq, D)
+    Hkv = s_k = s_ko = 0
     if k is not None:
-        _need(w, k.dim() == 3 and k.shape[0] == T and k.shape[2] == D)
         Hkv = k.shape[1]
-        ko = torch.empty((T, Hkv, D), dtype=k.dtype, device=k.device) if k_out is None else k_out
-    strides = []
-    for t, H in ((q, Hq), (k, Hkv), (qo, Hq), (ko, Hkv)):
-        s = 0
-        if t is not None:
-            _need(w, t.shape == (T, H, D) and t.dtype == q.dtype and t.device == q.device)
-            s = _rope_rows(t, H, D)
-            _need(w, s is not None)
-        strides.append(s)
-    _check(w, thd_rope(q, k, qo, ko, *strides, T, Hq, Hkv, D, 2 * inv.size, positions, n_axes, inv, axis,
-                       int(adjacent), int(inverse), dt, stream))
-    return qo, ko
+        s_k, s_ko = _rope_rows(w, q, k, T, Hkv, D), Hkv * D
+        if k_out is None:
+            k_out = k.new_empty((T, Hkv, D))
+        else:
+            s_ko = _rope_rows(w, q, k_out, T, Hkv, D)
+    else:
+        _need(w, k_out is None)
+    _check(w, thd_rope(q, k, q_out, k_out, s_q, s_k, s_qo, s_ko, T, Hq, Hkv, D, 2 * inv.size, positions, n_axes, inv,
+                       axis, int(adjacent), int(inverse), dt, stream))
+    return q_out, k_out
 
 
 def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None):
@@ -691,17 +711,22 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
     x.  out may be x or residual.  Returns out."""
     import torch
     w = "thd_dropout_add"
-    _current(w, x)
+    dev = _current(w, x)
     dt = _dtype(w, x)
-    C = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    C = shape[-1]
     T = x.numel() // C if C else 0
-    o = torch.empty_like(x) if out is None else out
-    for t in (x, residual, o):
-        _need(w, t is None or (t.shape == x.shape and t.dtype == x.dtype and t.device == x.device and
-                               t.is_contiguous()))
-    _need(w, rng.device == x.device and rng.numel() == 2 and rng.is_contiguous() and
-          rng.dtype in (torch.int64, torch.uint64))
-    _need(w, row_ids is None or (row_ids.dtype == torch.int32 and row_ids.numel() == T and row_ids.is_contiguous()
-                                 and row_ids.device == x.device))
-    _check(w, thd_dropout_add(x, residual, o, T, C, row_ids, p, rng, dt, stream))
-    return o
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(w, out.shape == shape and out.dtype is dtype and out.get_device() == dev and out.is_contiguous())
+    if residual is not None:
+        _need(w, residual.shape == shape and residual.dtype is dtype and residual.get_device() == dev and
+              residual.is_contiguous())
+    if row_ids is not None:
+        _need(w, row_ids.dtype is torch.int32 and row_ids.numel() == T and row_ids.get_device() == dev and
+              row_ids.is_contiguous())
+    _need(w, x.is_contiguous() and rng.get_device() == dev and rng.numel() == 2 and rng.is_contiguous() and
+          (rng.dtype is torch.int64 or rng.dtype is torch.uint64))
+    _check(w, thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dt, stream))
+    return out
