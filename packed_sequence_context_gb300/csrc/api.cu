@@ -215,12 +215,12 @@ static ScoreMods score_mods(const ScoreArgs& a, float scale, int causal, char* w
   if (a.softcap > 0.f) {
     m.cap_a = (float)(kLog2e * a.softcap);
     m.cap_c = (float)(2.0 * kLog2e * scale / a.softcap);
-    // tanh(u) / u = sum c_k u^(2k), to 4.0e-7 of its value on |u| <= 0.25 and
+    // tanh(u) / u = sum c_k u^(2k), to 7.8e-7 of its value on |u| <= 0.28 and
     // to 5.7e-7 on |u| <= 0.75, in s = u / c
-    constexpr double near_c[3] = {0.999999604345, -0.333219082252, 0.128416134328};
+    constexpr double near_c[3] = {0.999999226834, -0.333155230175, 0.127209170193};
     constexpr double far_c[5] = {0.999999434924, -0.33328251533, 0.132589832236, -0.0500563027154, 0.0129296324108};
     const double c = (double)scale / a.softcap;
-    m.cap_near = cap_polynomial(near_c, 3, 0.25, c, a.softcap, m.cap_n);
+    m.cap_near = cap_polynomial(near_c, 3, 0.28, c, a.softcap, m.cap_n);
     m.cap_far = cap_polynomial(far_c, 5, 0.75, c, a.softcap, m.cap_f);
   }
   m.slopes = a.slopes;

@@ -483,7 +483,6 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
     // the epilogue stores whole 32-byte sectors (the API asks for 16)
     const bool v8_ok = ((reinterpret_cast<uintptr_t>(p.dk) | reinterpret_cast<uintptr_t>(p.dv)) & 31u) == 0;
     uint32_t su = 0, n_done = 0;
-    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w;
@@ -499,6 +498,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
       const bool valid_kv = in_chunk && j_pos < it.g.Lkv;
       // scored: the queries that see this key
       int2 seen = make_int2(0, 0);
+      int cap = kCapNear;  // the item's form of tanh so far (see cap_form)
       if constexpr (kMod != 0) {
         if (valid_kv) seen = key_seen_by(p, p.mods, it.g, it.b, j_pos);
       }
@@ -555,18 +555,12 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
                 if (kCap && cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
               };
               if constexpr (kCap) {
-                cap_with_hint(
-                    hint,
-                    [&]() {
-                      load();
-                      return cap_form(score_abs_max(y), sc);
-                    },
-                    [&](auto form) {
-                      load();
-                      const float am = score_abs_max(y);
-                      cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f, 0.f);
-                      return cap_form(am, sc);
-                    });
+                cap_in_form(cap, [&](auto form) {
+                  load();
+                  const float am = score_abs_max(y);
+                  cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f, 0.f);
+                  return cap_form(am, sc);
+                });
               } else {
                 load();
               }

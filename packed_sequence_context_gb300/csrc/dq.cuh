@@ -446,7 +446,6 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     // dQ rows start at multiples of 128 bytes: 32-byte stores when dQ is 32-byte aligned
     const bool dq_v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
     uint32_t g = 0, n_item = 0, n_eps = 0;
-    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w;
@@ -467,6 +466,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
       const float lse2 = valid ? p.lse2[(int64_t)it.h * p.T_q + grow] : 0.f;
       // scored: the keys this row sees, and its score function
       int2 sees = make_int2(0, 0);
+      int cap = kCapNear;  // the item's form of tanh so far (see cap_form)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
@@ -530,17 +530,6 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               if (kCap && cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
               return cut;
             };
-            auto measure = [&]() {
-              float am = 0.f, y[32];
-#pragma unroll
-              for (int kk = 0; kk < kCh; ++kk) {
-                if (kCh * part + kk < nch) {
-                  load(y, kCh * part + kk);
-                  am = fmaxf(am, score_abs_max(y));
-                }
-              }
-              return cap_form(am, sc);
-            };
             float es[2];
             auto run = [&](auto form) {
               float am = 0.f;
@@ -594,7 +583,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               return kCap ? cap_form(am, sc) : kCapNear;
             };
             if constexpr (kCap) {
-              cap_with_hint(hint, measure, run);
+              cap_in_form(cap, run);
 #pragma unroll
               for (int kk = 0; kk < kCh; ++kk)
                 if (last && kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);

@@ -393,7 +393,6 @@ __global__ void __launch_bounds__(384, 1)
     // O rows start at multiples of 128 bytes: 32-byte stores when O is 32-byte aligned
     const bool o_v8 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     uint32_t g = 0, n_item = 0, n_done = 0;
-    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w = (int)(blockIdx.x + kit * gridDim.x);
@@ -412,6 +411,7 @@ __global__ void __launch_bounds__(384, 1)
       const int64_t grow = (int64_t)it.g.q_off + pos;
       // scored: the keys this row sees, and its score function
       int2 sees = make_int2(0, 0);
+      int cap = kCapNear;  // the item's form of tanh so far (see cap_form)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
@@ -471,30 +471,23 @@ __global__ void __launch_bounds__(384, 1)
               tmem_ld_wait(sr);
               if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, 0.f);
             };
-            cap_with_hint(
-                hint,
-                [&]() {
-                  float y[32];
-                  load(y);
-                  return cap_form(score_abs_max(y), sc);
-                },
-                [&](auto form) {
-                  float y[32];
-                  load(y);
-                  const float am = score_abs_max(y);
-                  score_run<kMod, decltype(form)::value, -1>(y, sc, (float)(ahead - 1 - 32 * k), abs_needed, -m);
-                  if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, -INFINITY);
+            cap_in_form(cap, [&](auto form) {
+              float y[32];
+              load(y);
+              const float am = score_abs_max(y);
+              score_run<kMod, decltype(form)::value, -1>(y, sc, (float)(ahead - 1 - 32 * k), abs_needed, -m);
+              if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, -INFINITY);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) sa[i] = 0.f;
+              for (int i = 0; i < 4; ++i) sa[i] = 0.f;
 #pragma unroll
-                  for (int n = 0; n < 16; ++n) {
-                    const float p0 = ex2(y[2 * n]), p1 = ex2(y[2 * n + 1]);
-                    const int a = 2 * (n & 1);
-                    fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);
-                    pk[n] = pack_bf16x2(p0, p1);
-                  }
-                  return cap_form(am, sc);
-                });
+              for (int n = 0; n < 16; ++n) {
+                const float p0 = ex2(y[2 * n]), p1 = ex2(y[2 * n + 1]);
+                const int a = 2 * (n & 1);
+                fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);
+                pk[n] = pack_bf16x2(p0, p1);
+              }
+              return cap_form(am, sc);
+            });
             tmem_st16(tcol + 64 * (k >> 1) + 16 * (k & 1), pk);
             l += (sa[0] + sa[1]) + (sa[2] + sa[3]);
           }
@@ -545,13 +538,11 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 return am;
               };
-              cap_with_hint(
-                  hint, [&]() { return cap_form(load_max(), sc); },
-                  [&](auto form) {
-                    const float am = load_max();
-                    score(form);
-                    return cap_form(am, sc);
-                  });
+              cap_in_form(cap, [&](auto form) {
+                const float am = load_max();
+                score(form);
+                return cap_form(am, sc);
+              });
             } else {
               score(CapForm<kCapNear>{});
             }

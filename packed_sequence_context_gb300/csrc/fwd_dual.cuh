@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(384, 1)
     // O rows start at multiples of 128 bytes: 32-byte stores when O is 32-byte aligned
     const bool o_v8 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     uint32_t g = 0;
-    int hint = kCapNear;  // the form of the warp's last run of scores (see cap_form)
     bool ok = true;
     for (uint32_t kit = 0; ok; ++kit) {
       int w = 0;
@@ -372,6 +371,7 @@ __global__ void __launch_bounds__(384, 1)
       const int64_t grow = (int64_t)it.g.q_off + pos;
       // scored: the keys this row sees, and its score function
       int2 sees = make_int2(0, 0);
+      int cap = kCapNear;  // the item's form of tanh so far (see cap_form)
       ScoreConsts sc;
       if constexpr (kMod != 0) {
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
@@ -441,13 +441,11 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 return am;
               };
-              cap_with_hint(
-                  hint, [&]() { return cap_form(load_max(), sc); },
-                  [&](auto form) {
-                    const float am = load_max();
-                    score(form);
-                    return cap_form(am, sc);
-                  });
+              cap_in_form(cap, [&](auto form) {
+                const float am = load_max();
+                score(form);
+                return cap_form(am, sc);
+              });
             } else {
               score(CapForm<kCapNear>{});
             }

@@ -8,8 +8,8 @@
 // tanh, chosen per warp and run of scores by the largest |x| of the run (see
 // cap_form):
 //   s times a polynomial in s^2, a relative minimax fit of tanh(u) / u derived
-//     by exchange on the interval: three terms for |x| <= softcap / 4 (relative
-//     error 4.0e-7), five for |x| <= 0.75 softcap (5.7e-7);
+//     by exchange on the interval: three terms for |x| <= 0.28 softcap (relative
+//     error 7.8e-7), five for |x| <= 0.75 softcap (5.7e-7);
 //   else 1 - 2 r, r = 1 / (1 + e^(2u)): one 2^x and one reciprocal, shared by
 //     two scores (1/a = b / (ab), 1/b = a / (ab), with exponents held to 2^60
 //     so that ab stays finite; tanh is 1 to the last bit long before).
@@ -88,14 +88,14 @@ THD_DEV void score_fill(float (&s)[N], int from, int to, float v) {
     if ((uint32_t)(n - lo) >= n_seen) s[n] = v;
 }
 
-// Which form of tanh the warp's run takes, by the largest |s| of each thread
-// (a NaN among the scores may pass for small: it stays a NaN in every form).
-// The near form is computed while the maximum is taken, instead of after a
-// decision, and again from TMEM in another form if the scores call for that; a
-// warp whose last run was not near measures first.  The result depends on the
-// run's scores alone.  (The three forms in a loop over "the form to try next"
-// made the compiler move every score between registers: 5850 instead of 3560
-// instructions in a forward tile.)
+// Which form of tanh the warp's run takes: the first whose range holds the
+// largest |s| of every thread (a NaN among the scores may pass for small: it
+// stays a NaN in every form), and none below that of the warp's earlier runs in
+// the same work item.  A run is computed in the item's form while the maximum
+// is taken, instead of after a decision, and again from TMEM if the scores call
+// for a wider one; the result depends on the item's scores alone.  (The three
+// forms in a loop over "the form to try next" made the compiler move every
+// score between registers: 5850 instead of 3560 instructions in a forward tile.)
 constexpr int kCapNear = 0, kCapFar = 1, kCapWide = 2;
 template <int kForm>
 struct CapForm {
@@ -106,14 +106,19 @@ THD_DEV int cap_form(float abs_max, const ScoreConsts& k) {
   return __all_sync(0xffffffffu, abs_max <= k.cap_far) ? kCapFar : kCapWide;
 }
 // run(CapForm<f>) loads the scores, computes in form f and returns the form the
-// scores call for; measure() does only that.
-template <typename M, typename F>
-THD_DEV void cap_with_hint(int& hint, M&& measure, F&& run) {
-  int f = hint == kCapNear ? kCapNear : measure();
-  if (f == kCapNear) f = run(CapForm<kCapNear>{});
-  hint = f;
-  if (f == kCapFar) run(CapForm<kCapFar>{});
-  if (f == kCapWide) run(CapForm<kCapWide>{});
+// scores call for.
+template <typename F>
+THD_DEV void cap_in_form(int& form, F&& run) {
+  bool done = false;
+  if (form == kCapNear) {
+    form = run(CapForm<kCapNear>{});
+    done = form == kCapNear;
+  }
+  if (!done && form == kCapFar) {
+    done = run(CapForm<kCapFar>{}) != kCapWide;
+    if (!done) form = kCapWide;
+  }
+  if (!done) run(CapForm<kCapWide>{});
 }
 
 // The polynomial's value at two scores: tanh = s times it.
