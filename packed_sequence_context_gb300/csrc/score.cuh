@@ -40,20 +40,20 @@ struct ScoreConsts {
   float sl2;       // softmax_scale log2(e)
   float cap_a;     // softcap log2(e)
   float cap_c;     // 2 log2(e) softmax_scale / softcap
-  float cap_n[3], cap_near;  // tanh = s (n0 + n1 s^2 + ..) while |s| <= cap_near; kScaled: times cap_a
+  float cap_n[3], cap_near;  // tanh = s (n0 + n1 s^2 + ..) while |s| <= cap_near; kForward: times cap_a
   float cap_f[5], cap_far;
   float slope;  // the head's slope log2(e)
 };
-template <int kMod, bool kScaled, class P>
+template <int kMod, bool kForward, class P>
 THD_DEV ScoreConsts score_consts(const P& p, int h) {
   ScoreConsts k;
   k.sl2 = p.scale_log2;
   k.cap_a = p.mods.cap_a;
   k.cap_c = p.mods.cap_c;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) k.cap_n[i] = p.mods.cap_n[i] * (kScaled ? k.cap_a : 1.f);
+  for (int i = 0; i < 3; ++i) k.cap_n[i] = p.mods.cap_n[i] * (kForward ? k.cap_a : 1.f);
 #pragma unroll
-  for (int i = 0; i < 5; ++i) k.cap_f[i] = p.mods.cap_f[i] * (kScaled ? k.cap_a : 1.f);
+  for (int i = 0; i < 5; ++i) k.cap_f[i] = p.mods.cap_f[i] * (kForward ? k.cap_a : 1.f);
   k.cap_near = p.mods.cap_near;
   k.cap_far = p.mods.cap_far;
   k.slope = 0.f;
@@ -75,12 +75,8 @@ THD_DEV float score_abs_max(const float (&s)[N]) {
 // The scores outside [from, to) become v.  Runs with masked columns set those
 // to 0 before the largest |s| is taken: a masked score, or a column that no
 // product wrote, must not choose the form (results stay reproducible).
-// Called under a condition that is uniform over the warp; the barrier keeps
-// the compiler from turning that branch into selects on every run (measured:
-// five of a forward tile's eleven instructions per score).
 template <int N>
 THD_DEV void score_fill(float (&s)[N], int from, int to, float v) {
-  __syncwarp();
   const int lo = from < 0 ? 0 : (from > N ? N : from), hi = to > N ? N : to;
   const uint32_t n_seen = hi > lo ? (uint32_t)(hi - lo) : 0u;
 #pragma unroll

@@ -90,6 +90,25 @@ def test_matches_oracle(thd_lib, dtype, residual, rows, C, p):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 2, 7, 9, 255, 256, 257, 511, 513, 1111])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_odd_rows_in_bf16(thd_lib, C, shift):
+    """Rows that start on odd elements (pairs straddle the groups of eight and
+    the rows have elements without a partner), and tensors off the 4-byte grid;
+    what lies around the output stays."""
+    rows = 9
+    rng = np.random.default_rng(C)
+    base = torch.from_numpy(rng.standard_normal((2, rows * C + 2))).bfloat16().cuda()
+    x, res = (base[i].clone()[shift:shift + rows * C].view(rows, C) for i in range(2))
+    out = torch.full((rows * C + 2,), 9.0, dtype=torch.bfloat16, device="cuda")
+    for r in (None, res):
+        T.dropout_add(x, _state(21, 22), 0.4, residual=r, out=out[shift:shift + rows * C].view(rows, C))
+        torch.cuda.synchronize()
+        _check(out[shift:shift + rows * C].view(rows, C), x, r, np.arange(rows), 0.4, 21, 22)
+        assert bool((out[:shift] == 9.0).all()) and bool((out[shift + rows * C:] == 9.0).all())
+
+
+@pytest.mark.gpu
 def test_off_the_grid_tensors_give_the_same_bits(thd_lib):
     """C a multiple of 8 but tensors off the 16-byte grid take the one-element
     path: the same bits; in place over x and over the residual as well."""
