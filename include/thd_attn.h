@@ -299,7 +299,8 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
  *     it changes nothing);
  *   documents: query and key have the same number, doc_q[row] == doc_kv[row].
  * A query that sees no key gets o = 0, lse = -inf (and zero gradients).
- *   softcap: >= 0, finite; 0: no cap.
+ *   softcap: 0 (no cap), or positive with softmax_scale / softcap between
+ *     2^-40 and 2^40.
  *   dist_slopes: device fp32 [Hq] or NULL, finite (constants: no gradient).
  *   doc_q [T_q], doc_kv [T_kv]: device int32 document number of every row, or
  *     both NULL.  They may be one array.  Inside a sequence the numbers of

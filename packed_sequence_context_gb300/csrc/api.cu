@@ -186,8 +186,9 @@ struct ScoreArgs {
 
 static int check_score(const ScoreArgs& a, float scale) {
   if (!(a.softcap >= 0.f) || !std::isfinite(a.softcap)) return THD_ERR_INVALID_ARG;
-  // 2 log2(e) scale / softcap has to be a finite float
-  if (a.softcap > 0.f && !std::isfinite((float)(2.0 * kLog2e * scale / a.softcap))) return THD_ERR_INVALID_ARG;
+  // powers of scale / softcap have to be floats (see cap_polynomial)
+  const double c = a.softcap > 0.f ? (double)scale / a.softcap : 1.0;
+  if (!(c >= 0x1p-40 && c <= 0x1p40)) return THD_ERR_INVALID_ARG;
   if ((a.doc_q == nullptr) != (a.doc_kv == nullptr)) return THD_ERR_INVALID_ARG;
   if (!aligned(a.slopes, 4) || !aligned(a.doc_q, 4) || !aligned(a.doc_kv, 4) || !aligned(a.prefix, 4))
     return THD_ERR_INVALID_ARG;
@@ -195,18 +196,27 @@ static int check_score(const ScoreArgs& a, float scale) {
 }
 
 // Coefficients of tanh(c s) = s (b0 + b1 s^2 + ..) from those in u = c s, and
-// the largest |s| they hold for: 0 when a power of c, alone or times the cap,
-// is no normal float.
+// the largest |s| they hold for.  Where a power of c, alone or times the cap,
+// passes a float's normal range: above it none is used (all 0, for |s| = 0
+// alone); below it the terms from there on are 0, and |u| stays where the
+// first of them is less than 1e-7.
 static float cap_polynomial(const double* ck, int n, double u_max, double c, double softcap, float* b) {
   double pw = c;
-  bool ok = true;
+  for (int i = 0; i < n; ++i) b[i] = 0.f;
   for (int i = 0; i < n; ++i, pw *= c * c) {
     const double v = std::fabs(ck[i] * pw), a = v * kLog2e * softcap;
+    if (v < 1e-37 || a < 1e-37) {
+      if (i == 0) return 0.f;
+      u_max = std::fmin(u_max, std::pow(1e-7 / std::fabs(ck[i]), 0.5 / i));
+      break;
+    }
+    if (v > 1e37 || a > 1e37) {
+      for (int k = 0; k < i; ++k) b[k] = 0.f;
+      return 0.f;
+    }
     b[i] = (float)(ck[i] * pw);
-    ok = ok && v > 1e-37 && v < 1e37 && a > 1e-37 && a < 1e37;
   }
-  const double lim = u_max / c;
-  return ok && lim * lim > 1e-37 && lim * lim < 1e37 ? (float)lim : 0.f;
+  return (float)(u_max / c);
 }
 
 static ScoreMods score_mods(const ScoreArgs& a, float scale, int causal, char* ws, const WsLayout& L, bool bwd) {

@@ -285,6 +285,12 @@ THD_DEV float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Minimum that keeps a NaN (fminf drops it).
+THD_DEV float fmin_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // Packed fp32 pair arithmetic (sm_100+): (d0, d1) = (a0 b0 + c0, a1 b1 + c1)
 // and (d0, d1) = (a0 + b0, a1 + b1), each one instruction for two lanes' worth.
 THD_DEV void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {

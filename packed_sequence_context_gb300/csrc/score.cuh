@@ -137,7 +137,7 @@ THD_DEV void cap_poly(float& q0, float& q1, float s0, float s1, const ScoreConst
 THD_DEV void cap_wide(float& r0, float& r1, float s0, float s1, float c) {
   float x0, x1, a0, a1;
   fmul2(x0, x1, s0, s1, c, c);
-  fadd2(a0, a1, ex2(fminf(x0, 60.f)), ex2(fminf(x1, 60.f)), 1.f, 1.f);
+  fadd2(a0, a1, ex2(fmin_nan(x0, 60.f)), ex2(fmin_nan(x1, 60.f)), 1.f, 1.f);
   const float q = rcp(a0 * a1);
   fmul2(r0, r1, q, q, a1, a0);
 }

@@ -459,12 +459,13 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_pa
     return dq, dk, dv, st
 
 
-def _score_checks(w, q, k, v, more, offsets, dist_slopes, doc_q, doc_kv, prefix_len):
+def _score_checks(w, q, k, v, more, offsets, dist_slopes, doc_q, doc_kv, prefix_len, workspace):
     """What the library cannot see of a scored call: types, shapes, layout and
     device of its tensors.  `more`: (tensor, shape, dtype) triples."""
     import torch
     dev = _current(w, q)
-    _need(w, q.dim() == 3 and k.dim() == 3)
+    _need(w, q.dim() == 3 and k.dim() == 3 and
+          (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
     qs, ks = q.shape, k.shape
     B = offsets[0].numel() - 1
     bf16, i32 = torch.bfloat16, torch.int32
@@ -500,7 +501,7 @@ def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=Non
         [(out, q.shape, torch.bfloat16), (lse, (q.shape[1], q.shape[0]), torch.float32), (dev_status, (1,), torch.int32)]
     B, T_q, T_kv, Hq, Hkv, D = _score_checks(
         w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
-        doc_q, doc_kv, prefix_len)
+        doc_q, doc_kv, prefix_len, workspace)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     o = torch.empty_like(q) if out is None else out
     l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
@@ -531,7 +532,7 @@ def attn_score_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
             (dq, qs, bf16), (dk, ks, bf16), (dv, ks, bf16), (dev_status, (1,), torch.int32)]
     B, T_q, T_kv, Hq, Hkv, D = _score_checks(
         w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
-        doc_q, doc_kv, prefix_len)
+        doc_q, doc_kv, prefix_len, workspace)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     dq = torch.empty(qs, dtype=bf16, device=q.device) if dq is None else dq
     dk = torch.empty(ks, dtype=bf16, device=q.device) if dk is None else dk

@@ -37,7 +37,7 @@ def _bwd(**kw):
 
 @pytest.mark.parametrize("kw", [
     {"q": None}, {"st": None}, {"q": 18}, {"cap": -1.0}, {"cap": float("inf")}, {"cap": float("nan")},
-    {"cap": 1e-44}, {"dq": 16}, {"dk": 16}, {"slopes": 18}, {"dq": 18, "dk": 16}, {"prefix": 17}, {"scale": 0.0},
+    {"cap": 1e-44}, {"cap": 1.5e11}, {"cap": 1e-14}, {"dq": 16}, {"dk": 16}, {"slopes": 18}, {"dq": 18, "dk": 16}, {"prefix": 17}, {"scale": 0.0},
     {"causal": 3}, {"pad": 2}, {"Hq": 3}, {"cp": 0}])
 @pytest.mark.parametrize("call", [_fwd, _bwd])
 def test_refuses_bad_arguments(thd_lib, call, kw):
@@ -291,6 +291,80 @@ def test_saturated_scores(thd_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [3.0e6, 1.0e9])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_cap_far_above_the_scores_changes_nothing(thd_lib, kernel, cap):
+    """|x| / cap is below 1e-4: tanh departs from its argument by 1e-9 of it,
+    and its polynomial's first coefficient by 7.8e-7 -- inside the uncapped
+    bounds, whose D 2^-24 sum |q||k| is at least 3.8e-6 |x|."""
+    c, m, cp, causal, scale = _make("cap")
+    ref = _ref(c, {**m, "softcap": 0.0}, causal, scale)
+    d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
+    kw["softcap"] = cap
+    T.thd_test_select_fwd_kernel(kernel)
+    try:
+        o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        T.check_status(st)
+    finally:
+        T.thd_test_select_fwd_kernel(0)
+    _close("o", o, ref)
+    _close("lse", lse, ref)
+    grads = T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw)
+    T.check_status(grads[3])
+    for n, g in zip(("dq", "dk", "dv"), grads):
+        _close(n, g, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_tiny_cap_and_queries_of_zero(thd_lib, kernel):
+    """Coefficients past fp32 are not used, not even against scores of 0."""
+    c, m, cp, causal, scale = _make("cap")
+    m["softcap"] = 1e-9
+    c["q"][::2] = 0
+    ref = _ref(c, m, causal, scale)
+    d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
+    T.thd_test_select_fwd_kernel(kernel)
+    try:
+        o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        T.check_status(st)
+    finally:
+        T.thd_test_select_fwd_kernel(0)
+    _close("o", o, ref)
+    _close("lse", lse, ref)
+    d["q"].zero_()
+    grads = T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw)
+    assert all(torch.isfinite(g.float()).all() for g in grads[:3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("std", [0.1, 1.0, 100.0])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_nan_key_shows_in_the_rows_that_see_it(thd_lib, kernel, std):
+    """In every form of tanh; rows before it and other heads' keys keep their
+    numbers.  (A NaN on a row with a valid token is the caller's; it must not
+    turn into plausible numbers.)"""
+    c, m, cp, causal, scale = _make("cap", std=std)
+    d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
+    want, _, _ = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+    at = 70  # a position of the second sequence
+    row = int(c["cu_kv_pad"][1]) + at
+    d["k"][row, 0, 5] = float("nan")
+    T.thd_test_select_fwd_kernel(kernel)
+    try:
+        o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        T.check_status(st)
+    finally:
+        T.thd_test_select_fwd_kernel(0)
+    see = slice(row, int(c["cu_q_pad"][1]) + 128)
+    assert torch.isnan(o[see, 0].float()).all()
+    other = o.clone()
+    other[see, 0] = 0
+    assert torch.isfinite(other.float()).all()
+    assert float((other[:, 1].float() - want[:, 1].float()).abs().max()) <= 4 * 2.0 ** -8 * float(d["v"].float().abs().max())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kernel", KERNELS)
 def test_decreasing_documents_are_refused_on_the_device(thd_lib, kernel):
     """Status 108, outputs untouched; numbers may fall between sequences and on
@@ -383,7 +457,8 @@ def test_helper_refuses_wrong_tensors(thd_lib):
     for bad in ({"doc_q": kw["doc_q"].long()}, {"doc_q": kw["doc_q"][:-1]}, {"doc_kv": None},
                 {"dist_slopes": kw["dist_slopes"].double()}, {"dist_slopes": kw["dist_slopes"][:2]},
                 {"prefix_len": kw["prefix_len"][:2]}, {"prefix_len": kw["prefix_len"].cpu()},
-                {"softcap": -1.0}, {"out": d["q"].float()}, {"causal": 5}):
+                {"softcap": -1.0}, {"out": d["q"].float()}, {"causal": 5},
+                {"workspace": torch.empty(1 << 24, dtype=torch.uint8)}):
         with pytest.raises(T.ThdError):
             T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **{**kw, **bad})
     for q, k, v in ((d["q"].float(), d["k"], d["v"]), (d["q"], d["k"][:-1], d["v"]),
