@@ -187,6 +187,20 @@ def test_a_captured_graph_draws_anew_when_its_state_advances(thd_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [32768, 32767])
+def test_elements_past_32_bits(thd_lib, C):
+    """70,001 rows, 2.3e9 elements: the last rows are what they are alone."""
+    rows, n = 70001, 5
+    rng = torch.tensor([11, 13], dtype=torch.int64, device="cuda")
+    x = torch.zeros(rows, C, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = torch.randn(n, C, device="cuda").bfloat16()
+    ids = torch.arange(rows, dtype=torch.int32, device="cuda")
+    want = T.dropout_add(x[-n:].clone(), rng, 0.3, row_ids=ids[-n:].clone())
+    out = T.dropout_add(x, rng, 0.3, out=x)
+    assert torch.equal(out[-n:], want) and not out[:-n].any()
+
+
+@pytest.mark.gpu
 def test_helper_refuses_wrong_tensors(thd_lib):
     x = torch.zeros(8, 16, device="cuda", dtype=torch.bfloat16)
     rng, ids = _state(1, 2), torch.zeros(8, device="cuda", dtype=torch.int32)

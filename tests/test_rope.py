@@ -199,6 +199,20 @@ def test_captured_in_a_graph_on_another_stream(thd_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,rot", [(128, 128), (125, 62)])
+def test_elements_past_32_bits(thd_lib, D, rot):
+    """700,001 rows of 32 heads, in place: the last rows are what they are alone."""
+    rows, H, n = 700001, 32, 5
+    freq = 10000.0 ** (-np.arange(rot // 2) / (rot // 2))
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    q = torch.zeros(rows, H, D, dtype=torch.bfloat16, device="cuda")
+    q[-n:] = torch.randn(n, H, D, device="cuda").bfloat16()
+    want, _ = T.rope(q[-n:].clone(), None, pos[-n:].clone(), freq)
+    T.rope(q, None, pos, freq, q_out=q)
+    assert torch.equal(q[-n:], want) and not q[:-n].any()
+
+
+@pytest.mark.gpu
 def test_helper_refuses_wrong_tensors(thd_lib):
     inv, axis = _table(64, [32])
     q = torch.zeros(4, 2, 64, device="cuda", dtype=torch.bfloat16)

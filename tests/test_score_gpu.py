@@ -450,6 +450,74 @@ def test_two_streams_at_once(thd_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fwd,kernel", [(KERNELS[0], T.THD_KERNEL_FWD), (KERNELS[1], T.THD_KERNEL_FWD),
+                                        (KERNELS[0], T.THD_KERNEL_BWD_DQ), (KERNELS[0], T.THD_KERNEL_BWD)])
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+def test_waits_end(thd_lib, cap, fwd, kernel):
+    """The bounded wait of the scored kernels (their block sizes differ with a
+    cap) runs out, the call reports it, its outputs stay as they were, and the
+    next call is right."""
+    c, m, cp, causal, scale = _make("bias all")
+    m["softcap"] = cap
+    d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
+    T.thd_test_select_fwd_kernel(fwd)
+    try:
+        o, lse, _ = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        outs = [torch.full_like(d[x], 7.0) for x in ("q", "k", "v")]
+        assert T.thd_test_arm_stall(kernel) == T.THD_OK
+        if kernel == T.THD_KERNEL_FWD:
+            _, _, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw, out=outs[0])
+            assert torch.all(outs[0] == 7.0)
+        else:
+            g = dict(zip(("dq", "dk", "dv"), outs))
+            st = T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw, **g)[3]
+            assert torch.all(outs[1] == 7.0) and torch.all(outs[2] == 7.0)
+            assert bool(torch.all(outs[0] == 7.0)) == (kernel == T.THD_KERNEL_BWD_DQ)
+        assert int(st.item()) == T.THD_ERR_TIMEOUT
+        o2, lse2, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        T.check_status(st)
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    finally:
+        T.thd_test_arm_stall(0)
+        T.thd_test_select_fwd_kernel(0)
+
+
+@pytest.mark.gpu
+def test_elements_past_32_bits(thd_lib):
+    """614,400 rows of 32 heads of 128, 2.5e9 elements: the last sequence, in a
+    batch of 1200, gives what it gives alone, bit for bit (the forward kernel
+    named, since the choice goes by the whole batch)."""
+    B, L, Hq, Hkv, D = 1200, 512, 32, 2, 128
+    n = B * L
+    g = torch.Generator().manual_seed(3)
+    kw = {"softcap": 30.0, "cp_size": 2, "dist_slopes": torch.full((Hq,), 0.01, device="cuda")}
+    docs = torch.zeros(n, dtype=torch.int32, device="cuda")
+    docs[-200:] = 1
+    cu = torch.arange(0, n + 1, L, dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    last = {x: torch.randn(L, h, D, generator=g).bfloat16().cuda()
+            for x, h in (("q", Hq), ("k", Hkv), ("v", Hkv), ("do", Hq))}
+    d = {x: torch.zeros(n, *t.shape[1:], dtype=torch.bfloat16, device="cuda") for x, t in last.items()}
+    for x, t in last.items():
+        d[x][-L:] = t
+    T.thd_test_select_fwd_kernel(T.THD_FWD_KERNEL_DUAL)
+    try:
+        o1, l1, st = T.attn_score_fwd(*(last[x] for x in "qkv"), one, one, doc_q=docs[-L:], doc_kv=docs[-L:], **kw)
+        T.check_status(st)
+        o, lse, st = T.attn_score_fwd(*(d[x] for x in "qkv"), cu, cu, doc_q=docs, doc_kv=docs, **kw)
+        T.check_status(st)
+    finally:
+        T.thd_test_select_fwd_kernel(0)
+    assert torch.equal(o[-L:], o1) and torch.equal(lse[:, -L:], l1)
+    g1 = T.attn_score_bwd(*(last[x] for x in "qkv"), o1, l1, last["do"], one, one, doc_q=docs[-L:],
+                          doc_kv=docs[-L:], **kw)
+    ga = T.attn_score_bwd(*(d[x] for x in "qkv"), o, lse, d["do"], cu, cu, doc_q=docs, doc_kv=docs, **kw)
+    T.check_status(ga[3])
+    for a, b in zip(ga[:3], g1[:3]):
+        assert torch.equal(a[-L:], b)
+
+
+@pytest.mark.gpu
 def test_helper_refuses_wrong_tensors(thd_lib):
     c, m, cp, causal, scale = _make("everything")
     d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
