@@ -318,11 +318,15 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   const bool grouped = long_sequences(B, T_kv);
   fp.group_kv = locality_group(Hkv, (size_t)T_kv * D * 2 * 2, grouped);
   const int forced = test_fwd_kernel();
-  // Bounded scores: that kernel's tiles in turn are ahead from sequences of
-  // about 1024 tokens on (32 x 512: 119 us against 109; 16 x 1024: 142 against
-  // 150; 8 x 2048: 193 against 226; 1 x 32768: 3.34 ms against 5.09).
-  const bool bounded = score && (score->fwd_mod() & kModBounded);
-  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : bounded ? T_kv >= 1024 * (int64_t)B : grouped;
+  // Scored: the mean length from which the kernel for long sequences is ahead,
+  // single against two items in flight, us on 32,768 tokens of 16 + 4 heads of
+  // 128 (64: the same to a factor of two in length):
+  //   bounded cap     1024: 273 / 258   2048: 363 / 396   8192: 918 / 1220
+  //   masks, bias     2048: 430 / 412   4096: 684 / 707   8192: 1183 / 1323
+  //   cap, unbounded  4096: 774 / 795 (with a bias 903 / 880)   8192: 1372 / 1466
+  const int mod = score ? score->fwd_mod() : 0;
+  const int64_t from = mod & kModBounded ? 2048 : mod & kModCap ? 8192 : 4096;
+  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : score ? T_kv >= from * B : grouped;
   fp.dev_status = dev_status;
   fp.B = B;
   fp.Hq = Hq;
@@ -341,8 +345,8 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   const bool part32 = step >= 0 && part_fp32;
   if (score) {
     fp.mods = mods;
-    return cuda_status(single ? launch_score_fwd(fp, tk, tv, D, score->fwd_mod(), grid, st)
-                              : launch_score_fwd_dual(fp, tk, tv, D, score->fwd_mod(), grid, st));
+    return cuda_status(single ? launch_score_fwd(fp, tk, tv, D, mod, grid, st)
+                              : launch_score_fwd_dual(fp, tk, tv, D, mod, grid, st));
   }
   return cuda_status(single ? launch_fwd(fp, tk, tv, D, part32, grouped, grid, st)
                             : launch_fwd_dual(fp, tk, tv, D, part32, grid, st));

@@ -41,6 +41,18 @@
 // TMEM (512 columns): S of stream x in [128x, 128x + 128), P written back over
 // its first 64 columns as packed bf16 (PV reads it from TMEM as the A
 // operand); O of stream x in [256 + 128x, 256 + 128x + D).
+//
+// Scores with a cap or a bias go chunk by chunk of 32 columns in a loop that is
+// not unrolled, instead of the whole row in registers: 128 scores times the
+// cap's forms in straight-line code hold 128 registers and no longer fit the
+// instruction cache.  Bounded scores (see fwd.cuh) need one walk over the
+// chunks; others take two, the first leaving the scores in TMEM in log2 units
+// and their maximum.  Measured, the whole row against chunks: cap 50, a packed
+// batch of 256 to 4096 tokens, 16 + 16 heads of 128, 703 against 379 us; on
+// 32,768 tokens of 16 + 4 heads of 128 in sequences of 128 and of 2048, without
+// a bound (cap 90) 184 / 143 and 477 / 457 us, bias alone 150 / 130 and
+// 412 / 409.  Masks alone keep the whole row (sequences of 2048: 350 against
+// 354 us, of 8192 1061 against 1122).
 #pragma once
 
 #include "common.cuh"
@@ -93,6 +105,8 @@ __global__ void __launch_bounds__(384, 1)
     fwd_dual_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = FwdDualCfg<D>;
   constexpr int KS = C::kKStages, VS = C::kVStages;
+  constexpr bool kBounded = (kMod & kModBounded) != 0;
+  constexpr bool kChunks = (kMod & (kModCap | kModDist)) != 0;  // a score function: chunk by chunk (see above)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) FwdStreamBars bars[2];
@@ -379,7 +393,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       // ---- key tiles
       float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
-      if constexpr ((kMod & kModBounded) != 0)  // bounded scores: their largest bias, throughout (see fwd.cuh)
+      if constexpr (kBounded)  // bounded scores: their largest bias, throughout (see fwd.cuh)
         m = (kMod & kModDist) != 0 ? largest_bias(sc.slope, pos + it.g.koff, sees.x, sees.y) : 0.f;
       int jl = 0;
       for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
@@ -404,87 +418,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         const int ncols = q_tile_ncols<kMod>(it, p, c, j);  // the N this tile's QK^T computed
         const int nch = ceil_div(ncols, 32);          // 32-column chunks holding S
-        uint32_t sr[4][32];
-        auto load = [&]() {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < nch) tmem_ld32(s_col + 32 * k, sr[k]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < nch) tmem_ld_wait(sr[k]);
-        };
-        if constexpr ((kMod & kModCap) == 0) load();
-        // keys past the row's last visible one count as -inf; whole warps of
-        // fully visible rows (every tile off the causal diagonal) skip the selects
-        if constexpr (kMod != 0) {
-          const bool cut = __any_sync(0xffffffffu, cnt < 32 * nch || from > 0);
-          const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
-          if constexpr (kMod != kScored) {
-            const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
-            auto score = [&](auto form) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < nch)
-                  score_run<kMod, decltype(form)::value, -1>(reinterpret_cast<float(&)[32]>(sr[k]), sc,
-                                                             (float)(ahead - 1 - 32 * k), abs_needed,
-                                                             (kMod & kModBounded) != 0 ? -m : 0.f);
-            };
-            if constexpr ((kMod & kModCap) != 0) {
-              auto load_max = [&]() {
-                load();
-                float am = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  float(&y)[32] = reinterpret_cast<float(&)[32]>(sr[k]);
-                  if (cut) score_fill(y, from - 32 * k, cnt - 32 * k, 0.f);
-                  if (k < nch) am = fmaxf(am, score_abs_max(y));
-                }
-                return am;
-              };
-              cap_in_form(cap, [&](auto form) {
-                const float am = load_max();
-                score(form);
-                return cap_form(am, sc);
-              });
-            } else {
-              score(CapForm<kCapNear>{});
-            }
-          }
-          if (cut) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              score_fill(reinterpret_cast<float(&)[32]>(sr[k]), from - 32 * k, cnt - 32 * k, -INFINITY);
-          }
-        } else if (__any_sync(0xffffffffu, cnt < 32 * nch)) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int n = 0; n < 32; ++n)
-              if (32 * k + n >= cnt) sr[k][n] = __float_as_uint(-INFINITY);
-        }
-        if constexpr ((kMod & kModBounded) == 0) {
-          // row maximum: per chunk four independent partial maxima of 8 values
-          float mloc = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k < nch) {
-              float pm[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t* v = &sr[k][8 * i];
-                pm[i] = fmax3(fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])),
-                              fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5])),
-                              fmaxf(__uint_as_float(v[6]), __uint_as_float(v[7])));
-              }
-              mloc = fmax3(mloc, fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-            }
-          }
-          float mt;
-          if constexpr (kMod == 0 || kMod == kScored) {
-            mt = mloc * sl2;
-          } else {
-            mt = mloc;  // in log2 units already
-          }
+        // the row's maximum so far, given the tile's (log2 units); false: a wait ran out
+        auto raise_max = [&](float mt) -> bool {
           // lazy rescale: move the running max only when it grows by > 8 (log2 units)
           const bool upd = mt > m + 8.0f;
           const float alpha = upd ? ex2(m - mt) : 1.0f;
@@ -498,10 +433,7 @@ __global__ void __launch_bounds__(384, 1)
             // after it completed.  The wait on its s_free phase is exact (the
             // next phase needs this warpgroup's P) and returns at once; it
             // orders the TMEM accesses below after that PV.
-            if (!mbar_wait(&sb.s_free, (g - 1) & 1u, &s_abort)) {
-              ok = false;
-              return;
-            }
+            if (!mbar_wait(&sb.s_free, (g - 1) & 1u, &s_abort)) return false;
             tc_fence_after();
             const float f = need_o ? alpha : 1.0f;
 #pragma unroll 1
@@ -514,8 +446,147 @@ __global__ void __launch_bounds__(384, 1)
               tmem_st32(o_col + 32 * k, o);
             }
           }
+          return true;
+        };
+        if constexpr (kChunks) {
+          // the row's chunks of 32 scores one at a time; packed P of chunk k goes
+          // to columns [16 k, 16 k + 16), all of which this thread has read
+          const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
+          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          auto cut = [&](int k) { return __any_sync(0xffffffffu, cnt < 32 * k + 32 || from > 32 * k); };
+          // y = chunk k's scores + top in log2 units, -inf on masked keys; then(y)
+          auto scores = [&](int k, float top, auto then) {
+            const bool c_cut = cut(k);
+            auto run = [&](auto form) {
+              float y[32];
+              uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
+              tmem_ld32(s_col + 32 * k, sr);
+              tmem_ld_wait(sr);
+              float am = 0.f;
+              if constexpr ((kMod & kModCap) != 0) {
+                if (c_cut) score_fill(y, from - 32 * k, cnt - 32 * k, 0.f);
+                am = score_abs_max(y);
+              }
+              score_run<kMod, decltype(form)::value, -1>(y, sc, (float)(ahead - 1 - 32 * k), abs_needed, top);
+              if (c_cut) score_fill(y, from - 32 * k, cnt - 32 * k, -INFINITY);
+              then(y);
+              return (kMod & kModCap) != 0 ? cap_form(am, sc) : kCapNear;
+            };
+            if constexpr ((kMod & kModCap) != 0)
+              cap_in_form(cap, run);
+            else
+              run(CapForm<kCapNear>{});
+          };
+          float sa[4];
+          uint32_t pk[16];
+          auto exps = [&](const float(&y)[32], float mm) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sa[i] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              float x0 = y[2 * n], x1 = y[2 * n + 1];
+              if constexpr (!kBounded) fadd2(x0, x1, x0, x1, -mm, -mm);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              const int a = 2 * (n & 1);
+              fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);
+              pk[n] = pack_bf16x2(p0, p1);
+            }
+          };
+          if constexpr (kBounded) {
+#pragma unroll 1
+            for (int k = 0; k < nch; ++k) {
+              scores(k, -m, [&](const float(&y)[32]) { exps(y, 0.f); });
+              tmem_st16(s_col + 16 * k, pk);
+              l += (sa[0] + sa[1]) + (sa[2] + sa[3]);
+            }
+          } else {
+            // first the scores, back in place, and their maximum
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int k = 0; k < nch; ++k) {
+              float z[32], mc;
+              scores(k, 0.f, [&](const float(&y)[32]) {
+                float pm[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float* v = &y[8 * i];
+                  pm[i] = fmax3(fmax3(v[0], v[1], v[2]), fmax3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+                }
+                mc = fmax3(fmaxf(pm[0], pm[1]), pm[2], pm[3]);
+#pragma unroll
+                for (int n = 0; n < 32; ++n) z[n] = y[n];
+              });
+              mt = fmaxf(mt, mc);
+              tmem_st32(s_col + 32 * k, reinterpret_cast<uint32_t(&)[32]>(z));
+            }
+            tmem_st_wait();
+            if (!raise_max(mt)) {
+              ok = false;
+              return;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+            for (int k = 0; k < nch; ++k) {
+              float y[32];
+              uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
+              tmem_ld32(s_col + 32 * k, sr);
+              tmem_ld_wait(sr);
+              exps(y, mm);
+              tmem_st16(s_col + 16 * k, pk);
+              l += (sa[0] + sa[1]) + (sa[2] + sa[3]);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();  // every lane's P is in TMEM: one arrival speaks for the warp
+          if (lane == 0) mbar_arrive(&sb.p_ready);
+          ++g;
+          ++jl;
+          return;
         }
-        const float mm = (kMod & kModBounded) != 0 || m == -INFINITY ? 0.f : m;
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nch) tmem_ld32(s_col + 32 * k, sr[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nch) tmem_ld_wait(sr[k]);
+        // keys past the row's last visible one count as -inf; whole warps of
+        // fully visible rows (every tile off the causal diagonal) skip the selects
+        if constexpr (kMod != 0) {
+          if (__any_sync(0xffffffffu, cnt < 32 * nch || from > 0)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              score_fill(reinterpret_cast<float(&)[32]>(sr[k]), from - 32 * k, cnt - 32 * k, -INFINITY);
+          }
+        } else if (__any_sync(0xffffffffu, cnt < 32 * nch)) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+              if (32 * k + n >= cnt) sr[k][n] = __float_as_uint(-INFINITY);
+        }
+        // row maximum: per chunk four independent partial maxima of 8 values
+        float mloc = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < nch) {
+            float pm[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* v = &sr[k][8 * i];
+              pm[i] = fmax3(fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])),
+                            fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5])),
+                            fmaxf(__uint_as_float(v[6]), __uint_as_float(v[7])));
+            }
+            mloc = fmax3(mloc, fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+          }
+        }
+        if (!raise_max(mloc * sl2)) {
+          ok = false;
+          return;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
         // P = 2^(S scale_log2 - m): the scale-and-shift as packed pair FMAs,
         // the row sum in four packed accumulators (short dependency chains);
         // packed P of key columns [32 k, 32 k + 32) goes to TMEM columns
@@ -528,11 +599,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
               const float s0 = __uint_as_float(sr[k][2 * n]), s1 = __uint_as_float(sr[k][2 * n + 1]);
-              float x0 = s0, x1 = s1;
-              if constexpr (kMod == 0 || kMod == kScored)
-                ffma2(x0, x1, s0, s1, sl2, sl2, -mm, -mm);
-              else if constexpr ((kMod & kModBounded) == 0)
-                fadd2(x0, x1, s0, s1, -mm, -mm);
+              float x0, x1;
+              ffma2(x0, x1, s0, s1, sl2, sl2, -mm, -mm);
               const float p0 = ex2(x0), p1 = ex2(x1);
               const int a = 2 * (n & 3);
               fadd2(sa[a], sa[a + 1], sa[a], sa[a + 1], p0, p1);
