@@ -86,7 +86,7 @@ def _kernel_traffic(kernel: str, workload: str):
         return None
     cs = os.path.join(ROOT, "packed_sequence_context_gb300", "csrc")
     h = hashlib.sha256()
-    src = {"fwd_dual_kernel": "fwd_dual.cu"}.get(kernel, kernel.split("_")[0] + ".cu")
+    src = {"fwd_dual_kernel": "fwd_dual.cuh"}.get(kernel, kernel.split("_")[0] + ".cuh")
     for name in (src, "common.cuh", "ptx.cuh", "sched.cuh"):
         with open(os.path.join(cs, name), "rb") as f:
             h.update(f.read())

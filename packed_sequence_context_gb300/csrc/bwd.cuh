@@ -9,7 +9,7 @@
 // step i, and dK/dV travel back around the ring to their owner.  Here the
 // owner keeps its key tile in shared memory and visits, in ring order, the
 // query tiles of every rank that sees it; dK/dV accumulate in TMEM (no
-// travel).  dQ is the query-stationary pass of dq.cu.
+// travel).  dQ is the query-stationary pass of dq.cuh.
 //
 // One work item = (sequence b, key chunk c, key tile jk within the chunk, kv
 // head hk).  For each query tile (chunk qc, tile jq) that sees it and each
@@ -25,7 +25,17 @@
 // entry-major instantiation (shorter sequences) runs 384 threads: warp 11,
 // idle, completes the fourth warpgroup so that setmaxnreg can move registers
 // to the compute warps (dK/dV +5% on batches of 0.1-8K-token sequences); the
-// grouped one (long sequences, where that measured -1%) runs 352.
+// grouped one (long sequences, where that measured -1%) runs 352, but for
+// scores with a cap or a bias, which need the registers.
+//
+// Scored attention: with t = tanh(x / softcap), dx = P (dP - Delta) (1 - t^2).
+// The scores' function is evaluated chunk by chunk (32 query columns) while P
+// is made; P (1 - t^2) stays in registers until dP^T is there.  32,768 tokens,
+// 16 + 4 heads of 128: plain 7.05 ms (1249 TFLOPS of the four products), masks
+// 7.3, bias 7.7, cap 50 8.3 (1060), cap and bias 9.9; cap 6670 instructions a
+// 128 x 128 tile against 4150, tensor pipe 50% busy: the compute warps' steps
+// (P, then dS) set the pace.  Not kept, slower: packing P early to free
+// registers (8.3 -> 8.9 ms), 1 - t^2 as a polynomial of its own.
 #pragma once
 
 #include "common.cuh"

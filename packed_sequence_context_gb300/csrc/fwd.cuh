@@ -40,7 +40,10 @@
 // The two softmax warpgroups then take whole tiles in turn instead of half of
 // every tile: each scheduler holds one warp of either, in different phases of
 // their tiles, so the TMEM loads and barriers of one run beside the other's
-// arithmetic, and a row needs no exchange per tile.
+// arithmetic, and a row needs no exchange per tile.  32,768 tokens, 16 + 4 heads
+// of 128: cap 50 3.1 ms (1402 TFLOPS, plain 3.3 ms), cap and bias 3.7 (with a
+// running maximum and half a tile each 4.4 and 5.7); bias alone 4.2, masks
+// alone 3.3.
 #pragma once
 
 #include "common.cuh"
@@ -61,7 +64,7 @@ struct FwdCfg {
   static constexpr int kSBufs = 3;          // S/P buffers of 128 columns
   static constexpr uint32_t kColO = 384;
   static constexpr int kThreads = 384;
-  // tiles in turn: a thread holds a whole row's packed P; per thread, warps 0-7 and 8-11
+  // tiles in turn: registers per thread, warps 0-7 and 8-11
   static constexpr uint32_t kSoftmaxRegs = 200, kOtherRegs = 96;
   static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split above the launch budget");
 };

@@ -10,7 +10,7 @@
 // 2cp-1-r.
 //
 // Work items, the ring walk and the on-chip LSE merge are those of the
-// single-item forward kernel (fwd.cu): item = (rank r, sequence b, query
+// single-item forward kernel (fwd.cuh): item = (rank r, sequence b, query
 // head h, rank-local 128-row query tile t), walking ring steps i = 0..cp-1
 // (KV of rank s = (r-i) mod cp: chunks s then 2cp-1-s) and the key tiles any
 // query of the tile may see; one-step mode writes step `step_lo`'s partial.
