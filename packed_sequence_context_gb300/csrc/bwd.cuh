@@ -18,24 +18,28 @@
 //   P^T  = exp(S^T scale - lse)          dS^T = P^T (dP^T - Delta)
 //   dV  += P^T dO     dK  += dS^T Q       (A = P^T / dS^T from TMEM, packed bf16
 //                                          over the S^T they were computed from)
-// CTA: warps 0-7 compute in two warpgroups -- a thread owns one key row (its
-// TMEM lane) and half of the query columns for P/dS, and half of the head
-// dimension when writing dK/dV; warp 8 TMA producer (+ lse/Delta staging);
-// warp 9 TMEM allocator and S^T issuer; warp 10 dV/dK/dP^T issuer.  The
-// entry-major instantiation (shorter sequences) runs 384 threads: warp 11,
-// idle, completes the fourth warpgroup so that setmaxnreg can move registers
-// to the compute warps (dK/dV +5% on batches of 0.1-8K-token sequences); the
-// grouped one (long sequences, where that measured -1%) runs 352, but for
-// scores with a cap or a bias, which need the registers.
+// CTA: the compute warps, then up to four warps with a role each.
+//   compute  two warpgroups, with a tanh cap four: a thread owns one key row (its
+//            TMEM lane) and a half (quarter) of the query columns for P/dS, and
+//            as much of the head dimension when writing dK/dV
+//   role 0   TMA producer (+ lse/Delta staging)
+//   role 1   TMEM allocator and S^T issuer
+//   role 2   dV/dK/dP^T issuer
+//   role 3   none: it completes the last warpgroup, so that setmaxnreg can move
+//            registers to the compute warps (384 threads instead of 352: dK/dV +5%
+//            on batches of 0.1-8K-token sequences).  Plain attention on long
+//            sequences, where that measured -1%, runs without it.
 //
 // Scored attention: with t = tanh(x / softcap), dx = P (dP - Delta) (1 - t^2).
-// The scores' function is evaluated chunk by chunk (32 query columns) while P
-// is made; P (1 - t^2) stays in registers until dP^T is there.  32,768 tokens,
-// 16 + 4 heads of 128: plain 7.05 ms (1249 TFLOPS of the four products), masks
-// 7.3, bias 7.7, cap 50 8.3 (1060), cap and bias 9.9; cap 6670 instructions a
-// 128 x 128 tile against 4150, tensor pipe 50% busy: the compute warps' steps
-// (P, then dS) set the pace.  Not kept, slower: packing P early to free
-// registers (8.3 -> 8.9 ms), 1 - t^2 as a polynomial of its own.
+// The scores' function is evaluated while P is made; P (1 - t^2) stays in
+// registers until dP^T is there.  A cap doubles the compute warps' work per step
+// and their latencies set the pace (two warps a scheduler issued in 41% of the
+// cycles), hence four warpgroups there: 32,768 tokens, 16 + 4 heads of 128, cap
+// 50 8.3 -> 8.15 ms, cap and bias 9.9 -> 8.7, every run in the wide form of tanh
+// 9.2 -> 8.6; sequences of 256 100 -> 87 us.  A bias alone gains nothing by them
+// (7.7 ms); masks alone 7.3, plain 7.05 (1249 TFLOPS of the four products).
+// Not kept, slower: 112 registers for the compute warps and 32 for the others
+// (8.8 ms), 1 - t^2 as a polynomial of its own.
 #pragma once
 
 #include "common.cuh"
@@ -45,7 +49,7 @@
 
 namespace thd {
 
-template <int D>
+template <int D, int kMod>
 struct BwdCfg {
   static constexpr int kStages = 2;
   static constexpr int kTileBytes = kTile * D * 2;  // one [128, D] bf16 tile
@@ -58,14 +62,27 @@ struct BwdCfg {
   static constexpr int kSmem = kOffRing + 256;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDV = 0, kColDK = D, kColX = 2 * D, kColY = 2 * D + 128;
-  static constexpr uint32_t kComputeRegs = 200;  // per thread, warps 0-7
-  static constexpr uint32_t kOtherRegs = 96;     // per thread, warps 8-11
-  static_assert(256 * kComputeRegs + 128 * kOtherRegs <= 384 * 168, "register split above the launch budget");
+  // compute warpgroups: two, each with half of the columns of a step; four with
+  // a quarter each where a tanh cap makes P and dS long
+  static constexpr int kGroups = (kMod & kModCap) != 0 ? 4 : 2;
+  static constexpr int kWarps = 4 * kGroups;  // compute warps; the four others follow
+  static constexpr int kThreads = 32 * kWarps + 128;
+  // where packed P^T of query columns 16 ks.. sits in the S^T buffer, and dS^T
+  // beside it: inside the S^T columns of the warpgroup that writes them
+  __host__ __device__ static constexpr uint32_t p_col(int ks) {
+    return kGroups == 2 ? 64 * (ks >> 2) + 8 * (ks & 3) : 32 * (ks >> 1) + 8 * (ks & 1);
+  }
+  static constexpr uint32_t kDsOff = kGroups == 2 ? 32 : 16;
+  static constexpr uint32_t kLaunchRegs = kGroups == 2 ? 168 : 96;   // per thread, what 65,536 allow
+  static constexpr uint32_t kComputeRegs = kGroups == 2 ? 200 : 104;  // per thread, compute warps
+  static constexpr uint32_t kOtherRegs = kGroups == 2 ? 96 : 64;      // per thread, the others
+  static_assert(32 * kWarps * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+                "register split above the launch budget");
 };
 
-// Whether the kernel runs 384 threads with a register split: entry-major, and
-// with scores whose function needs the registers.
-__host__ __device__ constexpr bool bwd_split(bool grouped, int mod) { return !grouped || (mod & ~kScored) != 0; }
+// Whether the kernel runs a complete last warpgroup with a register split:
+// entry-major, and with scores whose function needs the registers.
+__host__ __device__ constexpr bool bwd_split(bool grouped, int mod) { return !grouped || mod != 0; }
 
 struct BwdItem {
   SeqGeom g;
@@ -140,10 +157,10 @@ __device__ inline void drain_wait_b(uint64_t* bar, uint32_t parity) {
 }
 
 template <int D, bool kGrouped, int kMod>
-__global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
+__global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::kThreads : 352), 1)
     bwd_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
-  using C = BwdCfg<D>;
+  using C = BwdCfg<D, kMod>;
   constexpr bool kSplit = bwd_split(kGrouped, kMod);
   constexpr int S = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -169,6 +186,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
   ItemRing* ring = reinterpret_cast<ItemRing*>(smem + C::kOffRing);  // items of this CTA, in claim order
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int role = warp - C::kWarps;  // of the warps after the compute warps: 0 loads; 1 S^T; 2 dV, dK, dP^T; 3 none
   if (*p.dev_status != 0) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need a 1024-byte aligned base
     if (tid == 0) atomicCAS(p.dev_status, 0, THD_ERR_UNSUPPORTED);
@@ -179,7 +197,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
 
   if (tid == 0) {
     mbar_init(bar_kv_full, 1);
-    mbar_init(bar_kv_empty, 2);  // warp 9 saw the tile arrive; warp 10: its last reader completed
+    mbar_init(bar_kv_empty, 2);  // role 1 saw the tile arrive; role 2: its last reader completed
     for (int s = 0; s < S; ++s) {
       mbar_init(&bar_qdo_full[s], 33);  // 32 cp.async arrivals + the TMA expect-tx arrival
       mbar_init(&bar_qdo_empty[s], 1);
@@ -187,21 +205,21 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
       mbar_init(&bar_do_empty[s], 1);
     }
     mbar_init(bar_st_full, 1);
-    mbar_init(bar_p_ready, 8);  // one arrival per compute warp
+    mbar_init(bar_p_ready, C::kWarps);  // one arrival per compute warp
     mbar_init(bar_dk_done, 1);
-    mbar_init(bar_y_free, 8);  // one arrival per compute warp
+    mbar_init(bar_y_free, C::kWarps);  // one arrival per compute warp
     mbar_init(bar_dp_full, 1);
     mbar_init(bar_drain2, 1);
     mbar_init(bar_drain, 1);
-    item_ring_init(ring, 2 + 8);  // warps 9, 10 (one thread each) and the 8 compute warps
+    item_ring_init(ring, 2 + C::kWarps);  // the two issuers (one thread each) and the compute warps
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (role == 1) {
     tmem_alloc(s_tmem, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (role == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmDO);
     tma_prefetch_desc(&tmK);
@@ -219,12 +237,11 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
   // role runs, so nothing ever commits to it.
   if (p.test_stall) {
     mbar_wait(bar_drain, 0, s_abort);
-  } else if (warp >= 8) {
-    // The compute warps hold a step's P (64 values) and S^T / dP^T chunks per
-    // thread: they get 200 registers, warps 8-11 (producer, issuers, idle) 96;
-    // 256 x 200 + 128 x 96 fits the 384 x 168 the CTA is launched with.
+  } else if (role >= 0) {
+    // The compute warps hold a step's P (64 values a thread, or 32) and S^T /
+    // dP^T chunks: they get the registers of the other four (see BwdCfg).
     if constexpr (kSplit) regs_lower<C::kOtherRegs>();
-    if (warp == 8) {
+    if (role == 0) {
       // ------------------------------------------------------------ producer (whole warp)
       int stage = 0;
       uint32_t ph = 0, kv_iter = 0, n_fill = 0;
@@ -316,15 +333,15 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (role == 1) {
       // ------------------------------------------------------------ S^T issuer
       // The two 128-column TMEM buffers T0, T1 swap roles every step: step s
       // puts S^T(s) (then P^T(s)) in T[s % 2] and dP^T(s) in T[(s + 1) % 2].
       // Two issuing threads, as in the forward (a barrier wait in one does not
       // idle the tensor pipe while the other has products to issue):
-      //   warp 9:  S^T(s), as soon as the compute warps hold dP^T(s-1), which sat
+      //   role 1:  S^T(s), as soon as the compute warps hold dP^T(s-1), which sat
       //            in the same buffer, in registers (y_free)
-      //   warp 10: once the compute warps have written P^T(s-1) and dS(s-1),
+      //   role 2:  once the compute warps have written P^T(s-1) and dS(s-1),
       //            dV(s-1) and dK(s-1); then dP^T(s) into the buffer P^T(s-1)
       //            leaves once dV(s-1) has read it.
       // The compute warps of step s compute P from S^T(s) while dV/dK(s-1) run
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
           if (!mbar_wait(bar_kv_full, kv_iter & 1u, s_abort)) break;
           ++kv_iter;
           // this thread has seen the tile's phase: the tile may be refilled once
-          // warp 10 also releases it, and never before this wait (which would
+          // role 2 also releases it, and never before this wait (which would
           // leave this wait two phases behind when the item has no step)
           mbar_arrive(bar_kv_empty);
           for_each_q_step<kMod>(it, p, [&](int qc, int jq, int) {
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
         drain_wait_b(bar_drain, 0);
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (role == 2) {
       // ------------------------------------------------------------ dV, dK and dP^T issuer
       if (lane == 0) {
         constexpr uint32_t idesc_kv = idesc_bf16(128, D, false, true);  // dV, dK (B MN-major)
@@ -405,13 +422,13 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
           // dK += dS^T Q  (dS^T packed bf16 beside P^T: K-step ks at column
           // 64 (ks/4) + 32 + 8 (ks%4); K = the valid query rows)
           for (int ks = 0; ks < pv_n16; ++ks)
-            mma_ts(tmem + C::kColDK, pcol + 64 * (ks >> 2) + 32 + 8 * (ks & 3), sdesc_sw128(qb + ks * 2048, 16384, 1024),
+            mma_ts(tmem + C::kColDK, pcol + C::p_col(ks) + C::kDsOff, sdesc_sw128(qb + ks * 2048, 16384, 1024),
                    idesc_kv, (pv_first && ks == 0) ? 0u : 1u);
           tc_commit(&bar_qdo_empty[pv_stage]);
           // dV += P^T dO  (P^T packed bf16: query columns 16 ks.. of K-step ks sit
           // at column 64 (ks/4) + 8 (ks%4))
           for (int ks = 0; ks < pv_n16; ++ks)
-            mma_ts(tmem + C::kColDV, pcol + 64 * (ks >> 2) + 8 * (ks & 3), sdesc_sw128(dob + ks * 2048, 16384, 1024),
+            mma_ts(tmem + C::kColDV, pcol + C::p_col(ks), sdesc_sw128(dob + ks * 2048, 16384, 1024),
                    idesc_kv, (pv_first && ks == 0) ? 0u : 1u);
           tc_commit(&bar_do_empty[pv_stage]);
           // the item's last step: dk_done completes once per item, when every
@@ -485,7 +502,8 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
   } else {
     if constexpr (kSplit) regs_raise<C::kComputeRegs>();
     // ------------------------------------------------------------ compute warps
-    const int half = warp >> 2;     // which half of the columns this thread owns
+    constexpr int kCh = 4 / C::kGroups;  // 32-column chunks of a step a thread owns
+    const int half = warp >> 2;          // its warpgroup: chunks [kCh half, kCh half + kCh)
     const int row = tid & 127;      // its key row (TMEM lane) / query row when draining dQ
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float sl2 = p.scale_log2;
@@ -548,14 +566,14 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
         // ---- P = 2^(S^T scale log2(e) - lse) for this thread's chunks (query
         // columns outside [n_lo, n_hi) -- causal, or past the valid rows -- get
         // S = -inf, hence P = 0 and dS = 0); packed P^T goes back over S^T
-        float pv[2][32];
+        float pv[kCh][32];
         if constexpr (kMod != 0) {
           // P in place over the scores and, for dS, P (1 - tanh^2); then 0 in the
           // columns that do not see this key, whatever stood there
           constexpr bool kCap = (kMod & kModCap) != 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int kk = 2 * half + i;
+          for (int i = 0; i < kCh; ++i) {
+            const int kk = kCh * half + i;
             if (kk < nch) {
               const bool cut = __any_sync(0xffffffffu, n_lo > 32 * kk || n_hi < 32 * kk + 32);
               float y[32];
@@ -575,7 +593,10 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
                 load();
               }
               const float a = kCap ? sc.cap_a : sl2;
-              auto write_p = [&](auto bias) {
+              uint32_t pk[16];
+              const int lo = n_lo - 32 * kk;
+              const uint32_t n_seen = n_hi > n_lo ? (uint32_t)(n_hi - n_lo) : 0u;
+              auto write_p = [&](auto bias, auto with_cut) {
 #pragma unroll
                 for (int q4 = 0; q4 < 8; ++q4) {
                   const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
@@ -592,6 +613,10 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
                     ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
                     x0 = ex2(x0);
                     x1 = ex2(x1);
+                    if constexpr (decltype(with_cut)::value != 0) {
+                      if ((uint32_t)(n - lo) >= n_seen) x0 = 0.f;
+                      if ((uint32_t)(n + 1 - lo) >= n_seen) x1 = 0.f;
+                    }
                     if constexpr (kCap) {
                       float w0, w1;
                       ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
@@ -599,22 +624,21 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
                     } else {
                       pv[i][n] = x0, pv[i][n + 1] = x1;
                     }
-                    y[n] = x0, y[n + 1] = x1;
+                    pk[n / 2] = pack_bf16x2(x0, x1);
                   }
                 }
               };
-              if ((kMod & kModDist) != 0 && abs_needed)
-                write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f));
+              auto write = [&](auto with_cut) {
+                if ((kMod & kModDist) != 0 && abs_needed)
+                  write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f), with_cut);
+                else
+                  write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f), with_cut);
+              };
+              if (cut)
+                write(CapForm<1>{});
               else
-                write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f));
-              if (cut) {
-                score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-                score_fill(pv[i], n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
-              }
-              uint32_t pk[16];
-#pragma unroll
-              for (int n = 0; n < 16; ++n) pk[n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
-              tmem_st16(acol + 64 * half + 16 * i, pk);  // over columns already read
+                write(CapForm<0>{});
+              tmem_st16(acol + C::p_col(2 * kk), pk);  // over columns already read
             }
           }
         } else {
@@ -660,19 +684,19 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
           return;
         }
         tc_fence_after();
-        if (2 * half >= nch) {
+        if (kCh * half >= nch) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_y_free);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int kk = 2 * half + i;
+        for (int i = 0; i < kCh; ++i) {
+          const int kk = kCh * half + i;
           if (kk < nch) {
             uint32_t dr[32];
             tmem_ld32(bcol + 32 * kk, dr);
             tmem_ld_wait(dr);
-            if (kk + 1 >= imin(nch, 2 * half + 2)) {  // this warp's last dP^T chunk is in registers
+            if (kk + 1 >= imin(nch, kCh * half + kCh)) {  // this warp's last dP^T chunk is in registers
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar_y_free);
@@ -689,9 +713,8 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
               dk[2 * q4] = pack_bf16x2(g0, g1);
               dk[2 * q4 + 1] = pack_bf16x2(g2, g3);
             }
-            // packed dS^T beside P^T, in the S^T columns this thread has read:
-            // chunk kk -> 64 (kk/2) + 32 + 16 (kk%2)
-            tmem_st16(acol + 64 * (kk >> 1) + 32 + 16 * (kk & 1), dk);
+            // packed dS^T beside P^T, in the S^T columns this thread has read
+            tmem_st16(acol + C::p_col(2 * kk) + C::kDsOff, dk);
           }
         }
         tmem_st_wait();
@@ -709,6 +732,29 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
         ++n_done;
         tc_fence_after();
       }
+if constexpr (C::kGroups == 4) {
+        // dK, then dV: a quarter's registers do not hold both
+        constexpr int kChO = D / 32 >= C::kGroups ? D / 32 / C::kGroups : 1;  // warpgroups past D have none
+#pragma unroll 1
+        for (int u = 0; u < 2 * kChO; ++u) {
+          const int kk = kChO * half + (u >> 1);
+          if (kk >= D / 32) break;
+          const bool is_v = (u & 1) != 0;
+          uint32_t o[32];
+          if (nsteps > 0) {
+            tmem_ld32(tmem + lane_base + (is_v ? C::kColDV : C::kColDK) + 32 * kk, o);
+            tmem_ld_wait(o);
+          } else {
+#pragma unroll
+            for (int n = 0; n < 32; ++n) o[n] = 0u;
+          }
+          if (in_chunk) {
+            const int64_t grow = (int64_t)it.g.kv_off + j_pos;
+            store32_bf16((is_v ? p.dv : p.dk) + (grow * p.Hkv + it.hk) * D + 32 * kk, o,
+                         !valid_kv ? 0.f : is_v ? 1.f : p.scale, v8_ok);
+          }
+        }
+      } else {
 #pragma unroll 1
       for (int kk = half * (D / 64); kk < (half + 1) * (D / 64); ++kk) {
         uint32_t a[32], bq[32];
@@ -752,6 +798,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
           }
         }
       }
+      }
       tc_fence_before();
     }
     // ---- dK/dV rows past the last sequence: zero
@@ -759,7 +806,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
       const int Tend = p.eff[3 * (p.B + 1) + p.B];
       const int64_t nvec = (p.dkv_rows - Tend) * (int64_t)p.Hkv * (D / 8);
       const int64_t base = (int64_t)Tend * p.Hkv * D;
-      for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < nvec; i += (int64_t)gridDim.x * 256) {
+      for (int64_t i = (int64_t)blockIdx.x * 32 * C::kWarps + tid; i < nvec; i += (int64_t)gridDim.x * 32 * C::kWarps) {
         reinterpret_cast<uint4*>(p.dk + base)[i] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4*>(p.dv + base)[i] = make_uint4(0, 0, 0, 0);
       }
@@ -768,7 +815,7 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (role == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -778,11 +825,11 @@ __global__ void __launch_bounds__(bwd_split(kGrouped, kMod) ? 384 : 352, 1)
 template <int D, bool kGrouped, int kMod>
 static cudaError_t launch_bwd_t(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tdo,
                                 const CUtensorMap& tk, const CUtensorMap& tv, int grid, cudaStream_t st) {
-  using C = BwdCfg<D>;
+  using C = BwdCfg<D, kMod>;
   cudaError_t e = cudaFuncSetAttribute(bwd_kernel<D, kGrouped, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   prof_before(THD_KERNEL_BWD, st);
-  bwd_kernel<D, kGrouped, kMod><<<grid, bwd_split(kGrouped, kMod) ? 384 : 352, C::kSmem, st>>>(p, tq, tdo, tk, tv);
+  bwd_kernel<D, kGrouped, kMod><<<grid, bwd_split(kGrouped, kMod) ? C::kThreads : 352, C::kSmem, st>>>(p, tq, tdo, tk, tv);
   count_launch();
   e = cudaGetLastError();
   prof_after(THD_KERNEL_BWD, st);
