@@ -19,7 +19,7 @@
 //   dV  += P^T dO     dK  += dS^T Q       (A = P^T / dS^T from TMEM, packed bf16
 //                                          over the S^T they were computed from)
 // CTA: the compute warps, then up to four warps with a role each.
-//   compute  two warpgroups, with a tanh cap four: a thread owns one key row (its
+//   compute  two warpgroups, four for scored attention: a thread owns one key row (its
 //            TMEM lane) and a half (quarter) of the query columns for P/dS, and
 //            as much of the head dimension when writing dK/dV
 //   role 0   TMA producer (+ lse/Delta staging)
@@ -34,12 +34,13 @@
 // The scores' function is evaluated while P is made; P (1 - t^2) stays in
 // registers until dP^T is there.  A cap doubles the compute warps' work per step
 // and their latencies set the pace (two warps a scheduler issued in 41% of the
-// cycles), hence four warpgroups there: 32,768 tokens, 16 + 4 heads of 128, cap
-// 50 8.3 -> 8.15 ms, cap and bias 9.9 -> 8.7, every run in the wide form of tanh
-// 9.2 -> 8.6; sequences of 256 100 -> 87 us.  A bias alone gains nothing by them
-// (7.7 ms); masks alone 7.3, plain 7.05 (1249 TFLOPS of the four products).
-// Not kept, slower: 112 registers for the compute warps and 32 for the others
-// (8.8 ms), 1 - t^2 as a polynomial of its own.
+// cycles), hence four warpgroups.  Measured, two against four: 32,768 tokens, 16
+// + 4 heads of 128, cap 50 8.3 / 8.15 ms, cap and bias 9.9 / 8.7, every run in
+// the wide form of tanh 9.2 / 8.6, bias alone 7.7 / 7.8, masks alone 7.3 / 7.35
+// (plain 7.05: 1249 TFLOPS of the four products); cap on sequences of 256 100 /
+// 87 us; on padded batches bias 474 / 434 us, masks 281 / 242.  Not kept,
+// slower: 112 registers for the compute warps and 32 for the others (8.8 ms),
+// 1 - t^2 as a polynomial of its own.
 #pragma once
 
 #include "common.cuh"
@@ -63,8 +64,8 @@ struct BwdCfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDV = 0, kColDK = D, kColX = 2 * D, kColY = 2 * D + 128;
   // compute warpgroups: two, each with half of the columns of a step; four with
-  // a quarter each where a tanh cap makes P and dS long
-  static constexpr int kGroups = (kMod & kModCap) != 0 ? 4 : 2;
+  // a quarter each for scored attention, whose P and dS take longer
+  static constexpr int kGroups = kMod != 0 ? 4 : 2;
   static constexpr int kWarps = 4 * kGroups;  // compute warps; the four others follow
   static constexpr int kThreads = 32 * kWarps + 128;
   // where packed P^T of query columns 16 ks.. sits in the S^T buffer, and dS^T

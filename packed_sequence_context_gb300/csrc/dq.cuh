@@ -32,7 +32,7 @@
 //
 // CTA layout (one CTA per SM, persistent over the schedule): the dS warps, then
 // four warps with a role each.
-//   dS warps  two warpgroups (384 threads in all), with a tanh cap four (640):
+//   dS warps  two warpgroups (384 threads in all), with a cap or a bias four (640):
 //             thread = query row, a half (quarter) of the key columns; and the
 //             dQ epilogue (as much of the head dimension)
 //   role 0    producer: gathers the item's Q and dO rows (cp.async) and
@@ -47,11 +47,13 @@
 // order).
 //
 // 32,768 tokens, 16 + 4 heads of 128: plain 3.7 ms (1783 TFLOPS of the three
-// products), masks 3.85, bias 4.15, cap 50 5.0 (1320), cap and bias 5.6; the row
-// sum of P (dP - Delta) is 4% of that (without it, two warpgroups against four:
-// cap 5.1 / 4.6, cap and bias 6.2 / 5.2).  With a cap the
-// tensor pipe is 56% busy and the schedulers issue in 64% of the cycles.
-// Sequences of 256 (keys walked twice): masks 152 us, plain 99.
+// products), masks 3.8, bias 4.1, cap 50 5.0 (1320), cap and bias 5.6; the row
+// sum of P (dP - Delta) is 4% of that.  Two warpgroups against four: cap 5.1 /
+// 4.6, cap and bias 6.2 / 5.2 (both before the row sum); bias alone, padded
+// batch of 128 to 1600, 520 / 486 us, sequences of 256 164 / 170; masks alone,
+// 32,768 tokens, 3.8 / 4.0 ms.  With a cap the tensor pipe is 55% busy and the
+// schedulers issue in 64% of the cycles.  Sequences of 256 (keys walked twice):
+// masks 152 us, plain 99.
 #pragma once
 
 #include "common.cuh"
@@ -71,9 +73,9 @@ struct DqCfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDP = 256, kColDQ = 384;
   // dS warpgroups: two, each with half of the columns of a tile; four with a
-  // quarter each where a tanh cap makes dS long enough for its latencies to
-  // show (two warps per scheduler, in step, left it idle half of the time)
-  static constexpr int kGroups = (kMod & kModCap) != 0 ? 4 : 2;
+  // quarter each where a cap or a bias makes dS long enough for its latencies
+  // to show (two warps per scheduler, in step, left it idle half of the time)
+  static constexpr int kGroups = (kMod & (kModCap | kModDist)) != 0 ? 4 : 2;
   static constexpr int kWarps = 4 * kGroups;  // dS warps; the four others follow
   static constexpr int kThreads = 32 * kWarps + 128;
   // where packed dS of key columns 16 ks.. sits in the S buffer: inside the S
@@ -101,8 +103,8 @@ template <int D, bool kGrouped, int kMod>
 __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
     dq_kernel(const DqParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = DqCfg<D, kMod>;
-  // the register split also carries the longer dS of capped scores
-  constexpr bool kSplit = !kGrouped || (kMod & kModCap) != 0;
+  // the register split also carries the longer dS of a score function
+  constexpr bool kSplit = !kGrouped || C::kGroups == 4;
   constexpr int KS = C::kKStages, VS = C::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
