@@ -148,10 +148,14 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
       }
     }
   };
+  // a thread's first entry stays in registers between the two passes
+  int4 first = make_int4(0, 0, 0, 0);
+  int2 first_range = make_int2(0, 0);
   for (int w = tid; w < total; w += nt) {
     int b, x, y, cost;
-    int2 range;
+    int2 range = make_int2(0, 0);
     entry(w, b, x, y, cost, range);
+    if (w == tid) first = make_int4(b, x, y, cost), first_range = range;
     atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
   }
   __syncthreads();
@@ -175,9 +179,12 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   }
   __syncthreads();
   for (int w = tid; w < total; w += nt) {
-    int b, x, y, cost;
-    int2 range = make_int2(0, 0);
-    entry(w, b, x, y, cost, range);
+    int b = first.x, x = first.y, y = first.z, cost = first.w;
+    int2 range = first_range;
+    if (w != tid) {
+      range = make_int2(0, 0);
+      entry(w, b, x, y, cost, range);
+    }
     const int pos = atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
     items[pos] = make_int4(b, x, y, cost);
     if (ranges) ranges[pos] = range;
