@@ -95,6 +95,7 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_KERNEL_ROPE 10
 #define THD_KERNEL_DROPOUT 11
 #define THD_KERNEL_DOCS 12
+#define THD_KERNEL_BWD_JOIN 13
 
 /* mask modes (the `causal` argument of the attention entry points) */
 #define THD_CAUSAL_NONE 0
@@ -329,6 +330,9 @@ THD_API int thd_attn_score_fwd(const void* q, const void* k, const void* v, void
  *     dx = P (dP - Delta) (1 - tanh^2(x / softcap)).
  * Arguments as thd_attn_bwd, with the modifications the forward was given;
  * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible.
+ * Delta is corrected by the row sum of P (dP - Delta) where O's rounding to
+ * bf16 would show.  Launches: planner, preprocess, dQ and dK/dV; with documents
+ * two more; with few key tiles to go round, one that joins dK/dV's parts.
  */
 THD_API int thd_attn_score_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                const void* dout, void* dq, void* dk, void* dv, int64_t dq_rows, int64_t dkv_rows,

@@ -273,7 +273,7 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
     if (rc) return rc;
     if (!score->any()) score = nullptr;
   }
-  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp, false, score != nullptr, score && score->doc_q);
+  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp, false, score != nullptr, score && score->doc_q);
   rc = check_ws(ws, ws_bytes, L.total);
   if (rc) return rc;
   char* w = static_cast<char*>(ws);
@@ -374,7 +374,7 @@ static int bwd_common(const void* q, const void* k, const void* v, const void* o
     if (rc) return rc;
     if (!score->any()) score = nullptr;
   }
-  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, D, cp_size, true, score != nullptr, score && score->doc_q);
+  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, true, score != nullptr, score && score->doc_q);
   rc = check_ws(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   char* w = static_cast<char*>(workspace);
@@ -466,12 +466,20 @@ static int bwd_common(const void* q, const void* k, const void* v, const void* o
   bp.scale = softmax_scale;
   bp.scale_log2 = softmax_scale * 1.4426950408889634f;
   bp.test_stall = take_test_stall(THD_KERNEL_BWD) ? 1 : 0;
-  const int64_t bound = (int64_t)L.item_cap * Hkv;
+  const int64_t bound = (int64_t)L.item_cap * Hkv * L.parts;
   const int grid = (int)(bound < num_sms() ? (bound > 0 ? bound : 1) : num_sms());
+  if (!score) return cuda_status(launch_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, grid, st));
   bp.mods = pp.mods;
   bp.mods.ranges = pp.ranges;
-  return cuda_status(score ? launch_score_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, score->mod(), grid, st)
-                           : launch_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, grid, st));
+  bp.parts = L.parts;
+  bp.part = reinterpret_cast<float*>(w + L.part);
+  bp.T_kv = T_kv;
+  if (L.parts == 1)
+    return cuda_status(launch_score_bwd(bp, tq, tdo, tk, tv, D, grouped_kv, score->mod(), grid, st));
+  rc = cuda_status(launch_score_bwd_parts(bp, tq, tdo, tk, tv, D, score->mod(), grid, st));
+  if (rc) return rc;
+  return cuda_status(launch_bwd_join(bp.part, L.parts, bp.dk, bp.dv, softmax_scale, pp.eff, B, T_kv, Hkv, D,
+                                     dev_status, st));
 }
 
 // ------------------------------------------------------------------ A2A / hierarchical
@@ -529,7 +537,7 @@ static A2aWs a2a_ws_layout(int B, int64_t T, int Hq, int Hkv, int D, int cp, int
     if (i < n) off = align_up(off + sizes[i], 256);
   }
   w.attn = off;
-  w.total = off + ws_layout(B, T, T, Hq, D, cp / a2a, bwd).total;
+  w.total = off + ws_layout(B, T, T, Hq, Hkv, D, cp / a2a, bwd).total;
   return w;
 }
 
@@ -584,7 +592,7 @@ int thd_version(void) { return 100; }
 
 size_t thd_workspace_size(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp_size, int for_bwd) {
   if (check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp_size, -1) != THD_OK) return 0;
-  return ws_layout(B, T_q, T_kv, Hq, D, cp_size, for_bwd != 0).total;
+  return ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, for_bwd != 0).total;
 }
 
 int thd_cp_partition(const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded, int B, int cp_size,
@@ -666,7 +674,7 @@ int thd_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
 size_t thd_score_workspace_size(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp_size, int has_docs,
                                 int for_bwd) {
   if (check_sizes(B, T_q, T_kv, Hq, Hkv, D, cp_size, -1) != THD_OK) return 0;
-  return ws_layout(B, T_q, T_kv, Hq, D, cp_size, for_bwd != 0, true, has_docs != 0).total;
+  return ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, for_bwd != 0, true, has_docs != 0).total;
 }
 
 int thd_attn_score_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,

@@ -90,6 +90,7 @@ struct BwdItem {
   int b, c, jk, hk;
   int kv_first, kv_last;  // valid key positions of the tile (first > last: none)
   int q_lo, q_hi;         // scored: the queries that may see the tile
+  int part;               // kModParts: which of the walk's steps are the item's (every p.parts-th)
 };
 
 // Work item w -> (schedule entry, kv head).  Items are ordered by groups of
@@ -100,6 +101,10 @@ template <bool kGrouped, int kMod>
 __device__ inline BwdItem bwd_item(const BwdParams& p, int n_entries, int w) {
   BwdItem it;
   int x;  // schedule entry
+  if constexpr ((kMod & kModParts) != 0) {
+    it.part = w & (p.parts - 1);
+    w >>= 31 - __clz(p.parts);
+  }
   if constexpr (kGrouped) {
     const int per = n_entries * p.group_kv;  // items per group
     const int grp = w / per, rem = w - grp * per;
@@ -132,6 +137,7 @@ __device__ inline void for_each_q_step(const BwdItem& it, const BwdParams& p, F&
   const int G = p.Hq / p.Hkv;
   const int s = chunk_owner(it.c, p.cp);
   const int nq = ceil_div(it.g.cbq, kTile);
+  int n_step = 0;
   for (int i = 0; i < p.cp; ++i) {
     const int r = (s + i) % p.cp;
     for (int e = 0; e < 2; ++e) {
@@ -139,7 +145,8 @@ __device__ inline void for_each_q_step(const BwdItem& it, const BwdParams& p, F&
       if constexpr (kMod != 0) {
         const int2 n = chunk_tiles_in(qc, it.g.cbq, it.q_lo, it.q_hi);
         for (int jq = n.x; jq < n.y; ++jq)
-          for (int hh = 0; hh < G; ++hh) f(qc, jq, it.hk * G + hh);
+          for (int hh = 0; hh < G; ++hh)
+            if ((kMod & kModParts) == 0 || (n_step++ & (p.parts - 1)) == it.part) f(qc, jq, it.hk * G + hh);
         continue;
       }
       for (int jq = 0; jq < nq; ++jq) {
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
     return;
   }
   const int n_entries = p.counters[0];
-  const int n_items = n_entries * p.Hkv;
+  const int n_items = n_entries * p.Hkv * ((kMod & kModParts) != 0 ? p.parts : 1);
 
   if (tid == 0) {
     mbar_init(bar_kv_full, 1);
@@ -751,8 +758,12 @@ if constexpr (C::kGroups == 4) {
           }
           if (in_chunk) {
             const int64_t grow = (int64_t)it.g.kv_off + j_pos;
-            store32_bf16((is_v ? p.dv : p.dk) + (grow * p.Hkv + it.hk) * D + 32 * kk, o,
-                         !valid_kv ? 0.f : is_v ? 1.f : p.scale, v8_ok);
+            if constexpr ((kMod & kModParts) != 0)
+              store32_f32(p.part + (((is_v ? p.parts : 0) + it.part) * p.T_kv + grow) * p.Hkv * D + it.hk * D + 32 * kk,
+                          o, valid_kv ? 1.f : 0.f, (reinterpret_cast<uintptr_t>(p.part) & 31u) == 0);
+            else
+              store32_bf16((is_v ? p.dv : p.dk) + (grow * p.Hkv + it.hk) * D + 32 * kk, o,
+                           !valid_kv ? 0.f : is_v ? 1.f : p.scale, v8_ok);
           }
         }
       } else {

@@ -29,7 +29,8 @@ __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 // kModBounded (forward, with a cap of at most kBoundedCap): a row's largest y is
 // within that of its largest bias, so 2^(y - largest bias) needs no running
 // maximum.
-constexpr int kScored = 1, kModCap = 2, kModDist = 4, kModBounded = 8;
+// kModParts (dK/dV): a key tile's walk is shared among bwd_parts work items.
+constexpr int kScored = 1, kModCap = 2, kModDist = 4, kModBounded = 8, kModParts = 16;
 constexpr float kBoundedCap = 80.f;  // softcap log2(e) at most this: 2^-80 <= P <= 2^80
 
 struct ScoreMods {
@@ -67,6 +68,8 @@ struct WsLayout {
   size_t doc_err = 0;   // int32
   size_t rows_q = 0;    // int2 [T_q], with documents
   size_t rows_kv = 0;   // int2 [T_kv], with documents, backward
+  size_t part = 0;      // fp32 [2 parts][T_kv][Hkv][D], dK and dV of a key tile's parts (bwd_parts > 1)
+  int parts = 1;
   size_t total = 0;
   int item_cap = 0;
   int item_cap_q = 0;
@@ -74,8 +77,24 @@ struct WsLayout {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int D, int cp, bool bwd, bool scored = false,
-                          bool docs = false) {
+// Scored dK/dV: how many work items share a key tile's walk over its queries
+// (each takes every bwd_parts-th step and leaves fp32 dK, dV that a last kernel
+// adds up).  A causal sequence's first key tiles see twice the mean number of
+// queries, so the SMs need a few items each before the longest no longer sets
+// the time: with fewer than three an SM, two or four share a tile, as long as
+// each keeps 16 steps.  Measured, one against more: 32,768 tokens of 4 + 1
+// heads of 128 (256 key tiles, two parts) 2.84 / PLACE1 ms, 16,384 of 8 + 2 heads
+// of 64 in documents of about 2000 300 / PLACE2 us.
+constexpr int kBwdSms = 152;
+inline int bwd_parts(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv) {
+  const int64_t items = (T_kv / kTile + 1) * Hkv, steps = (T_q / (B > 0 ? B : 1) / kTile + 1) * (Hq / Hkv);
+  int parts = 1;
+  while (parts < 4 && items * parts < 3 * kBwdSms && steps / (2 * parts) >= 16) parts *= 2;
+  return parts;
+}
+
+inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp, bool bwd,
+                          bool scored = false, bool docs = false) {
   WsLayout w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -102,14 +121,17 @@ inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int D, int c
   }
   if (scored) {
     w.ranges = take(sizeof(int32_t) * 2 * (size_t)w.item_cap);
-    if (bwd) w.ranges_q = take(sizeof(int32_t) * 2 * (size_t)w.item_cap_q);
+    if (bwd) {
+      w.ranges_q = take(sizeof(int32_t) * 2 * (size_t)w.item_cap_q);
+      w.parts = bwd_parts(B, T_q, T_kv, Hq, Hkv);
+      if (w.parts > 1) w.part = take(sizeof(float) * 2 * (size_t)w.parts * (size_t)T_kv * Hkv * D);
+    }
   }
   if (docs) {
     w.doc_err = take(sizeof(int32_t));
     w.rows_q = take(sizeof(int32_t) * 2 * (size_t)T_q);
     if (bwd) w.rows_kv = take(sizeof(int32_t) * 2 * (size_t)T_kv);
   }
-  (void)D;
   w.total = off;
   return w;
 }
@@ -438,6 +460,9 @@ struct BwdParams {
   float scale, scale_log2;
   int test_stall;  // test hook: every thread waits for a barrier nothing completes
   ScoreMods mods;  // scored attention
+  float* part;     // scored, parts > 1: fp32 [2 parts][T_kv][Hkv][D], dK's parts, then dV's
+  int parts;       // scored: work items that share a key tile's walk
+  int64_t T_kv;
 };
 
 struct DqParams {
@@ -478,6 +503,11 @@ cudaError_t launch_score_fwd_dual(const FwdParams& p, const CUtensorMap& tk, con
                                   int grid, cudaStream_t st);
 cudaError_t launch_score_bwd(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                              const CUtensorMap& tv, int D, bool grouped, int mod, int grid, cudaStream_t st);
+cudaError_t launch_bwd_join(const float* part, int parts, uint16_t* dk, uint16_t* dv, float scale, const int32_t* eff,
+                            int B, int64_t T_kv, int Hkv, int D, const int32_t* dev_status, cudaStream_t st);
+cudaError_t launch_score_bwd_parts(const BwdParams& p, const CUtensorMap& tq, const CUtensorMap& tdo,
+                                   const CUtensorMap& tk, const CUtensorMap& tv, int D, int mod, int grid,
+                                   cudaStream_t st);
 cudaError_t launch_score_dq(const DqParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D, bool grouped,
                             int mod, int grid, cudaStream_t st);
 cudaError_t launch_docs(const int32_t* doc_q, const int32_t* doc_kv, const int32_t* eff, int B, int64_t T_q,

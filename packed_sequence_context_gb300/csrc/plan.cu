@@ -392,6 +392,48 @@ cudaError_t launch_docs(const int32_t* doc_q, const int32_t* doc_kv, const int32
   return e;
 }
 
+// ------------------------------------------------------------------ dK/dV parts
+// Scored dK/dV whose key tiles were shared: the sum of the parts in their order,
+// one thread for eight elements of both.  Bound by HBM (and less: the parts
+// were written just before and fit in L2 where they are few).
+__global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__ part, int parts, uint16_t* dk,
+                                                       uint16_t* dv, float scale, const int32_t* __restrict__ eff,
+                                                       int B, int64_t T_kv, int HD, const int32_t* dev_status) {
+  if (*dev_status != 0) return;
+  const int64_t n = (int64_t)eff[3 * (B + 1) + B] * HD, all = T_kv * HD;  // the sequences' rows: the rest is zeroed already
+  for (int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < 2 * n; i += 8 * (int64_t)gridDim.x * 256) {
+    const bool is_v = i >= n;
+    const int64_t at = is_v ? i - n : i;
+    const float* src = part + (is_v ? parts * all : 0) + at;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < parts; ++k) {
+      const float4 a = *reinterpret_cast<const float4*>(src + k * all);
+      const float4 b = *reinterpret_cast<const float4*>(src + k * all + 4);
+      s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w, s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    }
+    const float f = is_v ? 1.f : scale;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(s[2 * k] * f, s[2 * k + 1] * f);
+      o[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>((is_v ? dv : dk) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+cudaError_t launch_bwd_join(const float* part, int parts, uint16_t* dk, uint16_t* dv, float scale, const int32_t* eff,
+                            int B, int64_t T_kv, int Hkv, int D, const int32_t* dev_status, cudaStream_t st) {
+  const int64_t want = (T_kv * Hkv * D / 8 * 2 + 255) / 256;
+  const int grid = (int)(want < 1 ? 1 : (want < 16LL * num_sms() ? want : 16LL * num_sms()));
+  prof_before(THD_KERNEL_BWD_JOIN, st);
+  bwd_join_kernel<<<grid, 256, 0, st>>>(part, parts, dk, dv, scale, eff, B, T_kv, Hkv * D, dev_status);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  prof_after(THD_KERNEL_BWD_JOIN, st);
+  return e;
+}
+
 // ------------------------------------------------------------------ LSE merge
 // (o_acc, lse_acc) <- merge with (o_part, lse_part).  A block owns a tile of
 // tt consecutive tokens with all H heads: that tile's O rows are one

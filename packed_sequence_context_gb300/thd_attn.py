@@ -47,6 +47,7 @@ THD_KERNEL_A2A = 9
 THD_KERNEL_ROPE = 10
 THD_KERNEL_DROPOUT = 11
 THD_KERNEL_DOCS = 12
+THD_KERNEL_BWD_JOIN = 13
 
 THD_FWD_KERNEL_SINGLE = 1
 THD_FWD_KERNEL_DUAL = 2

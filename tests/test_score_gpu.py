@@ -513,8 +513,40 @@ def test_elements_past_32_bits(thd_lib):
                           doc_kv=docs[-L:], **kw)
     ga = T.attn_score_bwd(*(d[x] for x in "qkv"), o, lse, d["do"], cu, cu, doc_q=docs, doc_kv=docs, **kw)
     T.check_status(ga[3])
-    for a, b in zip(ga[:3], g1[:3]):
-        assert torch.equal(a[-L:], b)
+    assert torch.equal(ga[0][-L:], g1[0])
+    # dK, dV: a key tile's walk may be shared among work items when there are few of them, so the fp32 sums differ in
+    # order (64 x 2^-24 of the terms) and each is rounded to bf16 (2^-8)
+    for a, b in zip(ga[1:3], g1[1:3]):
+        assert float((a[-L:].float() - b.float()).norm()) <= (2 * 2.0 ** -8 + 2.0 ** -14) * float(b.float().norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,lengths", [(8, 1, 64, [2100, 900]), (4, 1, 128, [4000, 60]), (1, 1, 64, [4133])])
+def test_shared_key_tiles(thd_lib, Hq, Hkv, D, lengths):
+    """Few key tiles, each walked by several work items: the gradients, every
+    score modification on, against the oracle; repeats are bit-identical; rows
+    past the last sequence are zero."""
+    c = inputs.make_cross(lengths, lengths, pad_to=8, Hq=Hq, Hkv=Hkv, D=D, cp_size=4, seed=9)
+    rng = np.random.default_rng(10)
+    m = {"softcap": 20.0, "slopes": (2.0 ** -(np.arange(Hq) + 3.0)).astype(np.float32), "prefix": None,
+         "doc_k": _docs(rng, lengths, c["cu_kv_pad"], 1500)}
+    m["doc_q"] = m["doc_k"]
+    scale = D ** -0.5
+    ref = _ref(c, m, 1, scale)
+    d = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}
+    off, kw = _offsets(c), _kw(m, 4, 1, scale)
+    o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+    T.check_status(st)
+    T.thd_profile_enable(T.THD_KERNEL_BWD_JOIN, 4)
+    runs = [T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw, dkv_rows=d["k"].shape[0] + 5)
+            for _ in range(2)]
+    assert len(T.thd_profile_read()) == 2
+    T.thd_profile_enable(0, 0)
+    for n, a, b in zip(("dq", "dk", "dv"), *runs):
+        assert torch.equal(a, b)
+        _close(n, a[:d["q" if n == "dq" else "k"].shape[0]], ref)
+        if n != "dq":
+            assert not a[-5:].any()
 
 
 @pytest.mark.gpu
