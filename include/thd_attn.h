@@ -346,7 +346,9 @@ THD_API int thd_attn_score_bwd(const void* q, const void* k, const void* v, cons
 /*
  * Bytes of workspace thd_attn_score_fwd (for_bwd = 0) or thd_attn_score_bwd
  * (for_bwd = 1) needs; has_docs: document numbers are given.  Returns 0 for
- * invalid sizes.
+ * invalid sizes.  The backward of a call with few key tiles asks for more, to
+ * share them among the SMs; what a call with more tokens asks for serves it too
+ * (it then shares them less).
  */
 THD_API size_t thd_score_workspace_size(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp_size,
                                         int has_docs, int for_bwd);

@@ -374,7 +374,10 @@ static int bwd_common(const void* q, const void* k, const void* v, const void* o
     if (rc) return rc;
     if (!score->any()) score = nullptr;
   }
-  const WsLayout L = ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, true, score != nullptr, score && score->doc_q);
+  WsLayout L = ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, true, score != nullptr, score && score->doc_q);
+  // a workspace sized for more tokens, whose key tiles are not shared, serves too
+  while (L.parts > 1 && workspace_bytes < L.total)
+    L = ws_layout(B, T_q, T_kv, Hq, Hkv, D, cp_size, true, true, score->doc_q, L.parts / 2);
   rc = check_ws(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   char* w = static_cast<char*>(workspace);

@@ -79,22 +79,33 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Scored dK/dV: how many work items share a key tile's walk over its queries
 // (each takes every bwd_parts-th step and leaves fp32 dK, dV that a last kernel
-// adds up).  A causal sequence's first key tiles see twice the mean number of
-// queries, so the SMs need a few items each before the longest no longer sets
-// the time: with fewer than three an SM, two or four share a tile, as long as
-// each keeps 16 steps.  Measured, one against more: 32,768 tokens of 4 + 1
-// heads of 128 (256 key tiles, two parts) 2.84 / PLACE1 ms, 16,384 of 8 + 2 heads
-// of 64 in documents of about 2000 300 / PLACE2 us.
-constexpr int kBwdSms = 152;
-inline int bwd_parts(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv) {
-  const int64_t items = (T_kv / kTile + 1) * Hkv, steps = (T_q / (B > 0 ? B : 1) / kTile + 1) * (Hq / Hkv);
-  int parts = 1;
-  while (parts < 4 && items * parts < 3 * kBwdSms && steps / (2 * parts) >= 16) parts *= 2;
-  return parts;
+// adds up).  An SM works on one item, and a causal sequence's first key tile
+// sees twice the mean number of queries: unshared, the pass takes the longest
+// walk or, if that is more, the mean walk times items / SMs.  Sharing divides
+// the first and costs the join (8 us) and the parts' way to memory and back; of
+// 1, 2, .. 16 the rule takes what that makes least, at 2 us a step (a query tile
+// of one head), as long as every part keeps 12 steps.  Backward measured, cap
+// 50, heads of 128, one item a tile against the rule's, us: 32,768 tokens of
+// 4 + 1 heads 3775 / 3437, 8192 of 16 + 4 1055 / 982, 4096 of 8 + 2 369 / 237,
+// 4096 of 32 + 1 2323 / 711; 4096 of 8 + 8, which it leaves alone, 202 (two
+// parts 239).
+constexpr double kBwdSms = 152;
+inline int bwd_parts(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D) {
+  const double items = (double)(T_kv / kTile + 1) * Hkv;
+  const double steps = (double)(T_q / (B > 0 ? B : 1) / kTile + 1) * (Hq / Hkv);
+  const double shared = items * steps / (2 * kBwdSms);  // all SMs at work
+  int best = 1;
+  double least = 2 * (steps > shared ? steps : shared);
+  for (int parts = 2; parts <= 16 && steps / parts >= 12; parts *= 2) {
+    const double walk = steps / parts > shared ? steps / parts : shared;
+    const double t = 2 * walk + 8 + items * parts * kTile * D * 16 / 5e6;
+    if (t < least) best = parts, least = t;
+  }
+  return best;
 }
 
 inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D, int cp, bool bwd,
-                          bool scored = false, bool docs = false) {
+                          bool scored = false, bool docs = false, int most_parts = 16) {
   WsLayout w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -123,7 +134,8 @@ inline WsLayout ws_layout(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int
     w.ranges = take(sizeof(int32_t) * 2 * (size_t)w.item_cap);
     if (bwd) {
       w.ranges_q = take(sizeof(int32_t) * 2 * (size_t)w.item_cap_q);
-      w.parts = bwd_parts(B, T_q, T_kv, Hq, Hkv);
+      w.parts = bwd_parts(B, T_q, T_kv, Hq, Hkv, D);
+      if (w.parts > most_parts) w.parts = most_parts;
       if (w.parts > 1) w.part = take(sizeof(float) * 2 * (size_t)w.parts * (size_t)T_kv * Hkv * D);
     }
   }

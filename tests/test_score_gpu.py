@@ -547,6 +547,14 @@ def test_shared_key_tiles(thd_lib, Hq, Hkv, D, lengths):
         _close(n, a[:d["q" if n == "dq" else "k"].shape[0]], ref)
         if n != "dq":
             assert not a[-5:].any()
+    # a workspace short of the shared tiles' room: shared less, or not at all
+    t = d["q"].shape[0]
+    for n in (T.thd_score_workspace_size(len(lengths), t, t, Hq, Hkv, D, 4, 1, 1) - 256, 300000):
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        less = T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw, workspace=ws)
+        T.check_status(less[3])
+        for x, g in zip(("dq", "dk", "dv"), less):
+            _close(x, g, ref)
 
 
 @pytest.mark.gpu
