@@ -67,8 +67,8 @@ constexpr int kPlanSmemSeqs = 1024;
 // longest-first (counting sort on the number of tiles visited).  `eff` and
 // `toff` are where the planner reads the effective metadata and the tile
 // offsets (shared memory when they fit); `tile_off` receives the offsets in
-// the workspace.  Returns false when the schedule exceeds its capacity.
-__device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* toff, int mode, int32_t* tile_off,
+// the workspace.
+__device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* toff, int mode, int32_t* tile_off,
                               int32_t* counters, int4* items, int2* ranges, int item_cap, int* s_warp,
                               int* s_hist) {
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -96,8 +96,11 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   }
   const int total = carry;
   if (total > item_cap) {
-    if (tid == 0) *p.dev_status = THD_DEV_ERR_CAPACITY;
-    return false;
+    if (tid == 0) {
+      *p.dev_status = THD_DEV_ERR_CAPACITY;
+      counters[0] = counters[1] = 0;
+    }
+    return;
   }
   for (int i = tid; i < kCostBins; i += nt) s_hist[i] = 0;
   __syncthreads();
@@ -193,7 +196,6 @@ __device__ bool plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
     counters[0] = total;
     counters[1] = 0;  // the attention kernel's dynamic hand-out counter
   }
-  return true;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
@@ -306,19 +308,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
   }
   if (p.mode == 0) return;
   const int32_t* effr = meta_in_smem ? s_meta : eff;
-  if (!plan_schedule(p, effr, meta_in_smem ? s_meta + 4 * (B + 1) : p.tile_off, p.mode == 3 ? 2 : p.mode,
-                     p.tile_off, p.counters, p.items, p.ranges, p.item_cap, s_warp, s_hist))
-    return;
-  if (p.mode == 3) {
-    __syncthreads();  // s_hist and the staged tile offsets are reused
-    plan_schedule(p, effr, meta_in_smem ? s_meta + 4 * (B + 1) : p.tile_off_q, 1, p.tile_off_q, p.counters_q,
-                  p.items_q, p.ranges_q, p.item_cap_q, s_warp, s_hist);
-  }
+  // mode 3: two blocks, one schedule each (metadata and status: both write the
+  // same values; that a schedule exceeds its capacity, the one thing that would
+  // differ, cannot happen to metadata that passed the checks above)
+  const bool q_too = p.mode == 3 && blockIdx.x == 1;
+  int32_t* tile_off = q_too ? p.tile_off_q : p.tile_off;
+  plan_schedule(p, effr, meta_in_smem ? s_meta + 4 * (B + 1) : tile_off, q_too ? 1 : p.mode == 3 ? 2 : p.mode, tile_off,
+                q_too ? p.counters_q : p.counters, q_too ? p.items_q : p.items, q_too ? p.ranges_q : p.ranges,
+                q_too ? p.item_cap_q : p.item_cap, s_warp, s_hist);
 }
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t st) {
   prof_before(p.mode == 0 ? THD_KERNEL_PARTITION : THD_KERNEL_PLAN, st);
-  plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+  plan_kernel<<<p.mode == 3 ? 2 : 1, kPlanThreads, 0, st>>>(p);
   count_launch();
   cudaError_t e = cudaGetLastError();
   prof_after(p.mode == 0 ? THD_KERNEL_PARTITION : THD_KERNEL_PLAN, st);
@@ -330,25 +332,27 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t st) {
 // number, and each key row's queries, as intervals of positions (see
 // query_sees).  Numbers do not decrease inside a sequence, so both ends are
 // binary searches over the other side's numbers; a decrease is reported.
-// One thread per row; bound by the latency of about 2 log2(L) dependent
-// loads that hit in L2: 8.7 us for 16,384 + 16,384 rows.
-__device__ inline int first_not_below(const int32_t* a, int n, int x) {  // first i with a[i] >= x
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] < x) lo = mid + 1;
-    else hi = mid;
+// One thread per row; bound by the latency of about log2(L) dependent loads
+// that hit in L2: 7.1 us for 16,384 + 16,384 rows (8.7 with one search after
+// the other).
+//
+// [first i with a[i] >= x, first i with a[i] > x): both searches step together,
+// their loads in flight side by side.
+__device__ inline int2 rows_of(const int32_t* a, int n, int x) {
+  int lo0 = 0, hi0 = n, lo1 = 0, hi1 = n;
+  while (lo0 < hi0 || lo1 < hi1) {
+    const int m0 = (lo0 + hi0) >> 1, m1 = (lo1 + hi1) >> 1;
+    const int v0 = lo0 < hi0 ? a[m0] : 0, v1 = lo1 < hi1 ? a[m1] : 0;
+    if (lo0 < hi0) {
+      if (v0 < x) lo0 = m0 + 1;
+      else hi0 = m0;
+    }
+    if (lo1 < hi1) {
+      if (v1 <= x) lo1 = m1 + 1;
+      else hi1 = m1;
+    }
   }
-  return lo;
-}
-__device__ inline int first_above(const int32_t* a, int n, int x) {  // first i with a[i] > x
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
+  return make_int2(lo0, lo1);
 }
 
 __global__ void __launch_bounds__(256) docs_kernel(const int32_t* __restrict__ doc_q,
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(256) docs_kernel(const int32_t* __restrict__ d
     if (!rows) continue;
     const int32_t* other = query ? doc_kv + pad_kv[b] : doc_q + pad_q[b];
     const int n = query ? cu_kv[b + 1] - cu_kv[b] : cu_q[b + 1] - cu_q[b];
-    rows[t] = make_int2(first_not_below(other, n, id), first_above(other, n, id));
+    rows[t] = rows_of(other, n, id);
   }
 }
 
