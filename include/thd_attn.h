@@ -308,6 +308,10 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
  *     its valid rows must not decrease (else THD_DEV_ERR_DOC_ORDER); rows
  *     without a valid token are not looked at.
  *   prefix_len: device int32 [B] or NULL.
+ * cp_size: padded lengths have to be divisible by 2 cp_size as in
+ *   thd_attn_fwd.  Otherwise it changes nothing: with every rank's rows in the
+ *   one buffer each sequence is walked as a whole, not by the ranks' chunks,
+ *   and the outputs are those of any cp_size, bit for bit.
  * Key tiles that no query of a tile sees are skipped, whatever mask hides
  * them.  With none of the four given the call is thd_attn_fwd.  Every row
  * with a valid token must hold finite q, k, v: a masked key's score counts

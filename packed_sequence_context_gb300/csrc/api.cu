@@ -320,12 +320,13 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   const int forced = test_fwd_kernel();
   // Scored: the mean length from which the kernel for long sequences is ahead,
   // single against two items in flight, us on 32,768 tokens of 16 + 4 heads of
-  // 128 (64: the same to a factor of two in length):
-  //   bounded cap     1024: 273 / 258   2048: 363 / 396   8192: 918 / 1220
-  //   masks, bias     2048: 430 / 412   4096: 684 / 707   8192: 1183 / 1323
-  //   cap, unbounded  4096: 774 / 795 (with a bias 903 / 880)   8192: 1372 / 1466
+  // 128 (of 64: the same but for a factor of two in length at most):
+  //   masks             1024: 213 / 215   2048: 307 / 328   8192: 871 / 1009
+  //   bias              1024: 243 / 244   2048: 359 / 394   8192: 1074 / 1321
+  //   cap, bounded      1024: 237 / 234   2048: 328 / 367   8192: 880 / 1173
+  //   cap, unbounded    2048: 437 / 438   4096: 725 / 776   8192: 1308 / 1473
   const int mod = score ? score->fwd_mod() : 0;
-  const int64_t from = mod & kModBounded ? 2048 : mod & kModCap ? 8192 : 4096;
+  const int64_t from = (mod & (kModCap | kModBounded)) == kModCap ? 4096 : 1536;
   const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : score ? T_kv >= from * B : grouped;
   fp.dev_status = dev_status;
   fp.B = B;

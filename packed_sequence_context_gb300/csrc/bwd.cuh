@@ -119,7 +119,7 @@ __device__ inline BwdItem bwd_item(const BwdParams& p, int n_entries, int w) {
   it.b = e.x;
   it.c = e.y;
   it.jk = e.z;
-  it.g = seq_geom(p.eff, p.B, it.b, p.cp, p.causal);
+  it.g = seq_geom(p.eff, p.B, it.b, p.cp, p.causal, kMod != 0);
   bwd_kv_range(it.g, it.c, it.jk, it.kv_first, it.kv_last);
   if constexpr (kMod != 0) {
     const int2 q = p.mods.ranges[x];
@@ -135,20 +135,20 @@ template <int kMod, typename F>
 __device__ inline void for_each_q_step(const BwdItem& it, const BwdParams& p, F&& f) {
   if (it.kv_first > it.kv_last) return;
   const int G = p.Hq / p.Hkv;
+  if constexpr (kMod != 0) {  // the sequence's tiles in order, as chunk 0
+    const int2 n = tiles_in(it.q_lo, it.q_hi);
+    int n_step = 0;
+    for (int jq = n.x; jq < n.y; ++jq)
+      for (int hh = 0; hh < G; ++hh)
+        if ((kMod & kModParts) == 0 || (n_step++ & (p.parts - 1)) == it.part) f(0, jq, it.hk * G + hh);
+    return;
+  }
   const int s = chunk_owner(it.c, p.cp);
   const int nq = ceil_div(it.g.cbq, kTile);
-  int n_step = 0;
   for (int i = 0; i < p.cp; ++i) {
     const int r = (s + i) % p.cp;
     for (int e = 0; e < 2; ++e) {
       const int qc = e == 0 ? r : 2 * p.cp - 1 - r;
-      if constexpr (kMod != 0) {
-        const int2 n = chunk_tiles_in(qc, it.g.cbq, it.q_lo, it.q_hi);
-        for (int jq = n.x; jq < n.y; ++jq)
-          for (int hh = 0; hh < G; ++hh)
-            if ((kMod & kModParts) == 0 || (n_step++ & (p.parts - 1)) == it.part) f(qc, jq, it.hk * G + hh);
-        continue;
-      }
       for (int jq = 0; jq < nq; ++jq) {
         if (!bwd_q_tile_visits(it.g, qc, jq, it.kv_first, it.kv_last, p.causal != 0)) continue;
         for (int hh = 0; hh < G; ++hh) f(qc, jq, it.hk * G + hh);

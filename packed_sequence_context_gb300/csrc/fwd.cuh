@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int rr = 0; rr < 4; ++rr) {
           const int row = lane + 32 * rr;
           const int prow = it.t * kTile + row;
-          const bool in_rank = prow < 2 * it.g.cbq;
+          const bool in_rank = prow < rank_rows<kMod>(it.g);
           const int pos = in_rank ? local_to_pos(prow, it.r, it.g.cbq, p.cp) : 0;
           const bool valid = in_rank && pos < it.g.Lq;
           const uint16_t* src = valid ? p.q + (((int64_t)it.g.q_off + pos) * p.Hq + it.h) * D : p.q;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(384, 1)
       if (w >= n_items) break;
       const FwdItem it = q_item<kDyn, kMod>(p, n_entries, w);
       const int prow = it.t * kTile + row;
-      const bool in_rank = prow < 2 * it.g.cbq;
+      const bool in_rank = prow < rank_rows<kMod>(it.g);
       const int pos = in_rank ? local_to_pos(prow, it.r, it.g.cbq, p.cp) : 0;
       const bool valid = in_rank && pos < it.g.Lq;
       const int64_t grow = (int64_t)it.g.q_off + pos;

@@ -79,8 +79,11 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
     const int b = base + tid;
     int n = 0;
     if (b < B) {
-      SeqGeom g = seq_geom(eff, B, b, cp, p.causal);
-      n = mode == 1 ? cp * ceil_div(2 * g.cbq, kTile) : 2 * cp * ceil_div(g.cbkv, kTile);
+      SeqGeom g = seq_geom(eff, B, b, cp, p.causal, ranges != nullptr);
+      if (ranges)
+        n = ceil_div(mode == 1 ? g.cbq : g.cbkv, kTile);
+      else
+        n = mode == 1 ? cp * ceil_div(2 * g.cbq, kTile) : 2 * cp * ceil_div(g.cbkv, kTile);
     }
     int tot;
     const int ex = block_exclusive_scan(n, s_warp, tot);
@@ -110,45 +113,31 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
     b = upper_index(toff, B, w);
     // skip empty sequences that share the same offset
     while (b < B && toff[b + 1] <= w) ++b;
-    SeqGeom g = seq_geom(eff, B, b, cp, p.causal);
+    SeqGeom g = seq_geom(eff, B, b, cp, p.causal, ranges != nullptr);
     const int rem = w - toff[b];
-    if (mode == 1) {
+    if (ranges) {
+      x = 0;
+      y = rem;
+      const int2 rows = tile_rows(mode == 1 ? g.Lq : g.Lkv, rem);
+      if (rows.x <= rows.y && mode == 1) {
+        range.x = query_sees(p, p.mods, g, b, rows.x).x;
+        range.y = query_sees(p, p.mods, g, b, rows.y).y;
+      } else if (rows.x <= rows.y) {
+        range.x = key_seen_by(p, p.mods, g, b, rows.x).x;
+        range.y = key_seen_by(p, p.mods, g, b, rows.y).y;
+      }
+      const int2 n = tiles_in(range.x, range.y);
+      cost = n.y - n.x;
+    } else if (mode == 1) {
       const int per_r = ceil_div(2 * g.cbq, kTile);
       x = rem / per_r;
       y = rem % per_r;
-      if (ranges) {
-        const int qmax = fwd_tile_qmax(g, x, y, cp);
-        cost = 0;
-        if (qmax >= 0) {
-          range.x = query_sees(p, p.mods, g, b, fwd_tile_qmin(g, x, y, cp)).x;
-          range.y = query_sees(p, p.mods, g, b, qmax).y;
-          for (int c = 0; c < 2 * cp; ++c) {
-            const int2 n = chunk_tiles_in(c, g.cbkv, range.x, range.y);
-            cost += n.y - n.x;
-          }
-        }
-      } else {
-        cost = fwd_item_tiles(g, x, y, cp, p.causal != 0, p.step_lo, p.step_hi);
-      }
+      cost = fwd_item_tiles(g, x, y, cp, p.causal != 0, p.step_lo, p.step_hi);
     } else {
       const int per_c = ceil_div(g.cbkv, kTile);
       x = rem / per_c;
       y = rem % per_c;
-      if (ranges) {
-        int kf, kl;
-        bwd_kv_range(g, x, y, kf, kl);
-        cost = 0;
-        if (kf <= kl) {
-          range.x = key_seen_by(p, p.mods, g, b, kf).x;
-          range.y = key_seen_by(p, p.mods, g, b, kl).y;
-          for (int c = 0; c < 2 * cp; ++c) {
-            const int2 n = chunk_tiles_in(c, g.cbq, range.x, range.y);
-            cost += n.y - n.x;
-          }
-        }
-      } else {
-        cost = bwd_item_qtiles(g, x, y, cp, p.causal != 0);
-      }
+      cost = bwd_item_qtiles(g, x, y, cp, p.causal != 0);
     }
   };
   // a thread's first entry stays in registers between the two passes

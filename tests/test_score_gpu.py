@@ -230,6 +230,22 @@ def test_without_modifications_it_is_plain_attention(thd_lib, causal):
 
 
 @pytest.mark.gpu
+def test_the_ring_size_changes_no_bit(thd_lib):
+    """Padded lengths every ring size divides: the same outputs and gradients."""
+    c, m, _, causal, scale = _make("everything")   # padded to multiples of 24
+    d, off = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c)
+    want = None
+    for cp in (1, 2, 3, 4, 6, 12):
+        kw = _kw(m, cp, causal, scale)
+        o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+        T.check_status(st)
+        g = T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **kw)
+        T.check_status(g[3])
+        want = want or (o, lse, *g[:3])
+        assert all(torch.equal(a, b) for a, b in zip(want, (o, lse, *g[:3])))
+
+
+@pytest.mark.gpu
 def test_documents_equal_separate_sequences(thd_lib):
     """Documents inside one sequence give what the same rows give as sequences
     of their own (on lengths that cp_size = 1 can split), bit for bit in dQ's

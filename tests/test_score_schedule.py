@@ -1,10 +1,10 @@
 """CPU test of scored attention's work decomposition: a host program built
 with nvcc runs the __host__ __device__ geometry the kernels and the planner
-use (query_sees, key_seen_by, fwd_tile_qmin / qmax, chunk_tiles_in) on random
-ragged metadata with documents and prefixes.  Against the masks' definition:
-the two intervals describe the same visible pairs, every visible pair lies in
-a visited tile of both walks, visited tiles lie inside their chunk, and a tile
-is visited only inside its item's range."""
+use (query_sees, key_seen_by, tile_rows, tiles_in) on random ragged metadata
+with documents and prefixes.  Against the masks' definition: the two intervals
+describe the same visible pairs, every visible pair lies in a visited tile of
+both walks, visited tiles lie inside the sequence, and a tile is visited only
+inside its item's range."""
 
 import os
 import shutil
@@ -38,7 +38,7 @@ int main() {
     for (int i = 0; docs && i < Lkv; ++i) if (scanf("%d %d", &rk[i].x, &rk[i].y) != 2) return 1;
     SeqGeom g;
     g.q_off = g.kv_off = 0;
-    g.Lq = Lq, g.Lkv = Lkv, g.cbq = Pq / (2 * cp), g.cbkv = Pkv / (2 * cp);
+    g.Lq = Lq, g.Lkv = Lkv, g.cbq = Pq, g.cbkv = Pkv;
     g.koff = p.causal == 2 ? Lkv - Lq : 0;
     ScoreMods m{};
     m.rows_q = docs ? rq.data() : nullptr;
@@ -47,31 +47,27 @@ int main() {
     printf("C %d\n", n);
     for (int i = 0; i < Lq; ++i) { const int2 s = query_sees(p, m, g, 0, i); printf("q %d %d\n", s.x, s.y); }
     for (int j = 0; j < Lkv; ++j) { const int2 s = key_seen_by(p, m, g, 0, j); printf("k %d %d\n", s.x, s.y); }
-    for (int r = 0; r < cp; ++r)
-      for (int t = 0; t < ceil_div(2 * g.cbq, kTile); ++t) {
-        const int qmax = fwd_tile_qmax(g, r, t, cp);
-        if (qmax < 0) continue;
-        const int lo = query_sees(p, m, g, 0, fwd_tile_qmin(g, r, t, cp)).x, hi = query_sees(p, m, g, 0, qmax).y;
-        printf("F %d %d %d %d", r, t, lo, hi);
-        for (int c = 0; c < 2 * cp; ++c) {
-          const int2 n = chunk_tiles_in(c, g.cbkv, lo, hi);
-          for (int j = n.x; j < n.y; ++j) printf(" %d:%d", c, j);
-        }
-        printf("\n");
-      }
-    for (int c = 0; c < 2 * cp; ++c)
-      for (int jk = 0; jk < ceil_div(g.cbkv, kTile); ++jk) {
-        int kf, kl;
-        bwd_kv_range(g, c, jk, kf, kl);
-        if (kf > kl) continue;
-        const int lo = key_seen_by(p, m, g, 0, kf).x, hi = key_seen_by(p, m, g, 0, kl).y;
-        printf("K %d %d %d %d", c, jk, lo, hi);
-        for (int q = 0; q < 2 * cp; ++q) {
-          const int2 n = chunk_tiles_in(q, g.cbq, lo, hi);
-          for (int j = n.x; j < n.y; ++j) printf(" %d:%d", q, j);
-        }
-        printf("\n");
-      }
+    for (int t = 0; t < ceil_div(g.cbq, kTile); ++t) {
+      const int2 rows = tile_rows(Lq, t);
+      if (rows.x > rows.y) continue;
+      const int lo = query_sees(p, m, g, 0, rows.x).x, hi = query_sees(p, m, g, 0, rows.y).y;
+      printf("F %d %d %d", t, lo, hi);
+      const int2 n = tiles_in(lo, hi);
+      for (int j = n.x; j < n.y; ++j) printf(" %d", j);
+      printf("\n");
+    }
+    for (int t = 0; t < ceil_div(g.cbkv, kTile); ++t) {
+      const int2 rows = tile_rows(Lkv, t);
+      int kf, kl;
+      bwd_kv_range(g, 0, t, kf, kl);
+      if (kf != rows.x || kl != rows.y) return 2;
+      if (kf > kl) continue;
+      const int lo = key_seen_by(p, m, g, 0, kf).x, hi = key_seen_by(p, m, g, 0, kl).y;
+      printf("K %d %d %d", t, lo, hi);
+      const int2 n = tiles_in(lo, hi);
+      for (int j = n.x; j < n.y; ++j) printf(" %d", j);
+      printf("\n");
+    }
   }
   return 0;
 }
@@ -139,25 +135,20 @@ def test_intervals_and_walks_cover_the_masks(walker):
         assert np.array_equal((j[None] >= q[:, :1]) & (j[None] < q[:, 1:]), see)
         assert np.array_equal(((i[None] >= k[:, :1]) & (i[None] < k[:, 1:])).T, see)
         assert np.all((0 <= q) & (q <= lk)) and np.all((0 <= k) & (k <= lq))
-        cbq, cbk = pq // (2 * cp), pk // (2 * cp)
         done = np.zeros_like(see, dtype=int)
         done_k = np.zeros_like(done)
         for ln in lines:
-            if ln[0] == "F":
-                rank, t, lo, hi = map(int, ln[1:5])
-                p = np.arange(t * TILE, min((t + 1) * TILE, 2 * cbq))
-                rows = np.where(p < cbq, rank * cbq + p, (2 * cp - 1 - rank) * cbq + p - cbq)
-                rows = rows[rows < lq]
-                for c, jt in (map(int, x.split(":")) for x in ln[5:]):
-                    a, z = c * cbk + jt * TILE, min(c * cbk + min((jt + 1) * TILE, cbk), hi)
-                    assert 0 <= jt * TILE < cbk and a < z <= lk and z > lo
+            if ln[0] not in "FK":
+                continue
+            t, lo, hi = map(int, ln[1:4])
+            own, other = (lq, lk) if ln[0] == "F" else (lk, lq)
+            rows = np.arange(t * TILE, min((t + 1) * TILE, own))
+            for jt in map(int, ln[4:]):
+                a, z = jt * TILE, min((jt + 1) * TILE, other)
+                assert 0 <= a < z and z > lo and a < hi
+                if ln[0] == "F":
                     done[np.ix_(rows, np.arange(a, z))] += 1
-            elif ln[0] == "K":
-                c, jk, lo, hi = map(int, ln[1:5])
-                keys = np.arange(c * cbk + jk * TILE, min(c * cbk + min((jk + 1) * TILE, cbk), lk))
-                for qc, jq in (map(int, x.split(":")) for x in ln[5:]):
-                    a, z = qc * cbq + jq * TILE, min(qc * cbq + min((jq + 1) * TILE, cbq), lq)
-                    assert 0 <= jq * TILE < cbq and a < z and z > lo and a < hi
-                    done_k[np.ix_(np.arange(a, z), keys)] += 1
+                else:
+                    done_k[np.ix_(np.arange(a, z), rows)] += 1
         assert np.all(done[see] == 1) and np.all(done <= 1)
         assert np.all(done_k[see] == 1) and np.all(done_k <= 1)
