@@ -34,8 +34,8 @@
 // The scores' function is evaluated while P is made; P (1 - t^2) stays in
 // registers until dP^T is there.  A cap doubles the compute warps' work per step
 // and their latencies set the pace (two warps a scheduler issued in 41% of the
-// cycles), hence four warpgroups.  Measured, two against four: 32,768 tokens, 16
-// + 4 heads of 128, cap 50 8.3 / 8.15 ms, cap and bias 9.9 / 8.7, every run in
+// cycles), hence four warpgroups.  Measured, two against four, before sequences were
+// walked as a whole: 32,768 tokens, 16 + 4 heads of 128, cap 50 8.3 / 8.15 ms, cap and bias 9.9 / 8.7, every run in
 // the wide form of tanh 9.2 / 8.6, bias alone 7.7 / 7.8, masks alone 7.3 / 7.35
 // (plain 7.05: 1249 TFLOPS of the four products); cap on sequences of 256 100 /
 // 87 us; on padded batches bias 474 / 434 us, masks 281 / 242.  Not kept,

@@ -86,9 +86,8 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // 1, 2, .. 16 the rule takes what that makes least, at 2 us a step (a query tile
 // of one head), as long as every part keeps 12 steps.  Backward measured, cap
 // 50, heads of 128, one item a tile against the rule's, us: 32,768 tokens of
-// 4 + 1 heads 3775 / 3437, 8192 of 16 + 4 1055 / 982, 4096 of 8 + 2 369 / 237,
-// 4096 of 32 + 1 2323 / 711; 4096 of 8 + 8, which it leaves alone, 202 (two
-// parts 239).
+// 4 + 1 heads 4161 / 3308, 8192 of 16 + 4 1120 / 922, 4096 of 8 + 2 359 / 209,
+// 4096 of 32 + 1 2278 / 647; 4096 of 8 + 8 it leaves alone, 207 (two parts 239).
 constexpr double kBwdSms = 152;
 inline int bwd_parts(int B, int64_t T_q, int64_t T_kv, int Hq, int Hkv, int D) {
   const double items = (double)(T_kv / kTile + 1) * Hkv;

@@ -46,14 +46,14 @@
 // its dS, by the same thread (the tensor pipe runs one thread's MMAs in issue
 // order).
 //
-// 32,768 tokens, 16 + 4 heads of 128: plain 3.7 ms (1783 TFLOPS of the three
-// products), masks 3.8, bias 4.1, cap 50 5.0 (1320), cap and bias 5.6; the row
-// sum of P (dP - Delta) is 4% of that.  Two warpgroups against four: cap 5.1 /
-// 4.6, cap and bias 6.2 / 5.2 (both before the row sum); bias alone, padded
-// batch of 128 to 1600, 520 / 486 us, sequences of 256 164 / 170; masks alone,
-// 32,768 tokens, 3.8 / 4.0 ms.  With a cap the tensor pipe is 55% busy and the
-// schedulers issue in 64% of the cycles.  Sequences of 256 (keys walked twice):
-// masks 152 us, plain 99.
+// 32,768 tokens, 16 + 4 heads of 128: plain 3.7 ms (1785 TFLOPS of the three
+// products), masks 3.7, bias 4.0, cap 50 4.75 (1385), cap and bias 5.3; the row
+// sum of P (dP - Delta) is 4% of that.  Two warpgroups against four (before the
+// row sum, and before sequences were walked as a whole): cap 5.1 / 4.6, cap and
+// bias 6.2 / 5.2; bias alone, padded batch of 154 to 1409, 520 / 486 us,
+// sequences of 256 164 / 170; masks alone, 32,768 tokens, 3.8 / 4.0 ms.  With a
+// cap the tensor pipe is 59% busy and the schedulers issue in 65% of the cycles.
+// Sequences of 256 (keys walked twice): masks 131 us, plain 99.
 #pragma once
 
 #include "common.cuh"

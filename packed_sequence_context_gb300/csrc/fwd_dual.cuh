@@ -47,8 +47,8 @@
 // cap's forms in straight-line code hold 128 registers and no longer fit the
 // instruction cache.  Bounded scores (see fwd.cuh) need one walk over the
 // chunks; others take two, the first leaving the scores in TMEM in log2 units
-// and their maximum.  Measured, the whole row against chunks: cap 50, a packed
-// batch of 256 to 4096 tokens, 16 + 16 heads of 128, 703 against 379 us; on
+// and their maximum.  Measured, the whole row against chunks (before sequences
+// were walked as a whole): cap 50, a packed batch of 256 to 4096 tokens, 16 + 16 heads of 128, 703 against 379 us; on
 // 32,768 tokens of 16 + 4 heads of 128 in sequences of 128 and of 2048, without
 // a bound (cap 90) 184 / 143 and 477 / 457 us, bias alone 150 / 130 and
 // 412 / 409.  Masks alone keep the whole row (sequences of 2048: 350 against
