@@ -128,6 +128,10 @@ CASES = {
     "growing bias both sides": ([100, 257], [300, 257], 16, 2, 3, 1, 128, 2,
                                 {"cap": 9.0, "slopes": [-0.05, 0.01, -0.3], "docs": 40, "prefix": [90, 100]}),
     "far keys only": ([80, 40], [300, 200], 8, 2, 2, 2, 64, 0, {"cap": 20.0, "slopes": [3.0, 0.5], "docs": 30}),
+    # many query heads to a key head: the key tiles are shared among work items
+    "no keys": ([900, 64], [0, 64], 8, 2, 32, 1, 64, 2, {"cap": 9.0, "bias": True}),
+    "no queries": ([0, 700], [300, 700], 8, 2, 32, 1, 64, 2, {"cap": 9.0, "prefix": [9, 80]}),
+    "padded much": ([3, 129, 700], None, 512, 2, 24, 1, 128, 1, {"bias": True, "docs": 300}),
     "mask only": ([300, 200], None, 8, 2, 2, 2, 128, 1, {"prefix": [100, 50]}),
 }
 
@@ -571,6 +575,40 @@ def test_shared_key_tiles(thd_lib, Hq, Hkv, D, lengths):
         T.check_status(less[3])
         for x, g in zip(("dq", "dk", "dv"), less):
             _close(x, g, ref)
+
+
+@pytest.mark.gpu
+def test_backwards_on_two_streams_and_in_a_graph(thd_lib):
+    """Shared key tiles: two backward calls in flight, and a captured one, give
+    what one alone gives; a refused batch leaves the gradients as they were."""
+    c, m, cp, causal, scale = _make("padded much")
+    d, off, kw = {x: _gpu(c[x]) for x in ("q", "k", "v", "do")}, _offsets(c), _kw(m, cp, causal, scale)
+    o, lse, st = T.attn_score_fwd(d["q"], d["k"], d["v"], *off, **kw)
+    T.check_status(st)
+    call = lambda **more: T.attn_score_bwd(d["q"], d["k"], d["v"], o, lse, d["do"], *off, **{**kw, **more})  # noqa: E731
+    T.thd_profile_enable(T.THD_KERNEL_BWD_JOIN, 4)
+    want = call()
+    assert len(T.thd_profile_read()) == 1
+    T.thd_profile_enable(0, 0)
+    torch.cuda.synchronize()
+    got = []
+    for s in [torch.cuda.Stream() for _ in range(2)]:
+        with torch.cuda.stream(s):
+            got += [call() for _ in range(3)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.append(call())
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for g in got:
+        assert int(g[3].item()) == 0 and all(torch.equal(a, b) for a, b in zip(g[:3], want[:3]))
+    bad = kw["doc_q"].clone()
+    bad[int(c["cu_q_pad"][2]) + 5] = -99
+    outs = {x: torch.full_like(d[y], 7.0) for x, y in (("dq", "q"), ("dk", "k"), ("dv", "v"))}
+    st = call(doc_q=bad, **outs)[3]
+    assert int(st.item()) == T.THD_DEV_ERR_DOC_ORDER and all(torch.all(x == 7.0) for x in outs.values())
 
 
 @pytest.mark.gpu
