@@ -325,9 +325,14 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   //   bias              1024: 243 / 244   2048: 359 / 394   8192: 1074 / 1321
   //   cap, bounded      1024: 237 / 234   2048: 328 / 367   8192: 880 / 1173
   //   cap, unbounded    2048: 437 / 438   4096: 725 / 776   8192: 1308 / 1473
+  // With fewer items than the two streams of every SM the second one idles:
+  // single below two items an SM (128 items of 4096 tokens, cap: 41 / 73; of 512
+  // 17 / 19), and from 1024 tokens below four (512 of 1024 41 / 45, of 512 37 / 31).
   const int mod = score ? score->fwd_mod() : 0;
-  const int64_t from = (mod & (kModCap | kModBounded)) == kModCap ? 4096 : 1536;
-  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : score ? T_kv >= from * B : grouped;
+  const int64_t items = T_q / kTile * Hq;
+  const int64_t from = items < 4LL * num_sms() ? 1024 : (mod & (kModCap | kModBounded)) == kModCap ? 4096 : 1536;
+  const bool scored_single = items < 2LL * num_sms() || T_kv >= from * B;
+  const bool single = forced ? forced == THD_FWD_KERNEL_SINGLE : score ? scored_single : grouped;
   fp.dev_status = dev_status;
   fp.B = B;
   fp.Hq = Hq;
