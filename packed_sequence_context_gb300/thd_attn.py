@@ -8,11 +8,17 @@ fallback: if the library is missing, ``lib()`` raises.
 
 The lower-case helpers at the end (``attn_fwd``, ``attn_bwd``, ...) allocate
 outputs, workspace and the device status word with torch and call the
-``thd_*`` functions -- allocation and marshalling only.
+``thd_*`` functions -- allocation and marshalling only.  With ``stream=`` (a
+torch stream, or a cudaStream_t as an int) they allocate from that stream's
+memory, where the kernels run, and keep what they were given and what they
+return until both streams are done with it; ordering the two streams is the
+caller's.  A raw handle's stream may end before the tensors do, so there the
+caller also keeps the inputs until the work is done.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -145,6 +151,7 @@ def _h(a):
 
 
 _RAW_STREAM = None
+_HERE = contextlib.nullcontext()
 
 
 def _s(stream):
@@ -368,6 +375,43 @@ def _current(where: str, t) -> int:
     return dev
 
 
+def _aside(stream):
+    """The torch stream of a call that does not run on the current one, else
+    None.  0 and 1 are the legacy default stream."""
+    if stream is None:
+        return None
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return None if stream == torch.cuda.current_stream() else stream
+
+
+def _alloc_on(side):
+    """Where the buffers of a call are made: a block of the current stream's
+    memory would be free for the current stream's next tensor once the helper
+    drops it, and may still be in use by what that stream ran before."""
+    import torch
+    return _HERE if side is None else torch.cuda.stream(side)
+
+
+def _keep(side, stream, given, made):
+    """After a launch on another stream: the memory of what the call was given
+    (unless by a raw handle) and of what it returns stays until both streams
+    are done with it."""
+    if side is None:
+        return
+    import torch
+    cur = torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream):
+        for t in given:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(side)
+    for t in made:
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(cur)
+
+
 def _workspace(nbytes, device):
     import torch
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -383,14 +427,18 @@ def attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None, cu_
     T_kv, Hkv, _ = k.shape
     B = cu_seqlens_q.numel() - 1
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    nbytes = thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0)
-    ws = _workspace(nbytes, q.device) if workspace is None else workspace
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
+        st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        nbytes = thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0)
+        ws = _workspace(nbytes, q.device) if workspace is None else workspace
     _check("thd_attn_fwd", thd_attn_fwd(q, k, v, o, l, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
                                         cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal), scale,
                                         cp_size, pad_between_seqs, ws, ws.numel(), st, stream))
+    _keep(side, stream, (q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, out, lse,
+                         dev_status, workspace), (o, l, st))
     return o, l, st
 
 
@@ -403,14 +451,18 @@ def attn_fwd_step(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None
     T_kv, Hkv, _ = k.shape
     B = cu_seqlens_q.numel() - 1
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty((T_q, Hq, D), dtype=torch.float32, device=q.device) if out is None else out
-    l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    st = torch.zeros(1, dtype=torch.int32, device=q.device)
-    ws = _workspace(thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0), q.device)
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty((T_q, Hq, D), dtype=torch.float32, device=q.device) if out is None else out
+        l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
+        st = torch.zeros(1, dtype=torch.int32, device=q.device)
+        ws = _workspace(thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0), q.device)
     _check("thd_attn_fwd_step", thd_attn_fwd_step(q, k, v, o, l, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
                                                   cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal),
                                                   scale, cp_size, pad_between_seqs, step, ws, ws.numel(), st,
                                                   stream))
+    _keep(side, stream, (q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, out, lse),
+          (o, l, st))
     return o, l, st
 
 
@@ -423,15 +475,19 @@ def attn_fwd_step_bf16(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded
     T_kv, Hkv, _ = k.shape
     B = cu_seqlens_q.numel() - 1
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty((T_q, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    ws = _workspace(thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0), q.device) if workspace is None \
-        else workspace
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty((T_q, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+        l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
+        st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        ws = _workspace(thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 0), q.device) if workspace is None \
+            else workspace
     _check("thd_attn_fwd_step_bf16", thd_attn_fwd_step_bf16(q, k, v, o, l, cu_seqlens_q, cu_seqlens_kv,
                                                             cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv,
                                                             Hq, Hkv, D, int(causal), scale, cp_size,
                                                             pad_between_seqs, step, ws, ws.numel(), st, stream))
+    _keep(side, stream, (q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, out, lse,
+                         dev_status, workspace), (o, l, st))
     return o, l, st
 
 
@@ -447,16 +503,21 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_pa
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     dq_rows = T_q if dq_rows is None else dq_rows
     dkv_rows = T_kv if dkv_rows is None else dkv_rows
-    dq = torch.empty((dq_rows, Hq, D), dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty((dkv_rows, Hkv, D), dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty((dkv_rows, Hkv, D), dtype=q.dtype, device=q.device) if dv is None else dv
-    st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    nbytes = thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 1)
-    ws = _workspace(nbytes, q.device) if workspace is None else workspace
+    given = (q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, dq, dk, dv,
+             dev_status, workspace)
+    side = _aside(stream)
+    with _alloc_on(side):
+        dq = torch.empty((dq_rows, Hq, D), dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty((dkv_rows, Hkv, D), dtype=q.dtype, device=q.device) if dk is None else dk
+        dv = torch.empty((dkv_rows, Hkv, D), dtype=q.dtype, device=q.device) if dv is None else dv
+        st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        nbytes = thd_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, 1)
+        ws = _workspace(nbytes, q.device) if workspace is None else workspace
     _check("thd_attn_bwd", thd_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q,
                                         cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq,
                                         Hkv, D, int(causal), scale, cp_size, pad_between_seqs, ws, ws.numel(), st,
                                         stream))
+    _keep(side, stream, given, (dq, dk, dv, st))
     return dq, dk, dv, st
 
 
@@ -504,16 +565,20 @@ def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=Non
         w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
         doc_q, doc_kv, prefix_len, workspace)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    if workspace is None:
-        workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, int(doc_q is not None), 0),
-                               q.device)
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((Hq, T_q), dtype=torch.float32, device=q.device) if lse is None else lse
+        st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        if workspace is None:
+            workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size,
+                                                            int(doc_q is not None), 0), q.device)
     _check(w, thd_attn_score_fwd(q, k, v, o, l, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
                                  cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal), scale, cp_size,
                                  pad_between_seqs, softcap, dist_slopes, doc_q, doc_kv, prefix_len, workspace,
                                  workspace.numel(), st, stream))
+    _keep(side, stream, (q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, dist_slopes,
+                         doc_q, doc_kv, prefix_len, out, lse, dev_status, workspace), (o, l, st))
     return o, l, st
 
 
@@ -535,17 +600,22 @@ def attn_score_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
         w, q, k, v, more, (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded), dist_slopes,
         doc_q, doc_kv, prefix_len, workspace)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    dq = torch.empty(qs, dtype=bf16, device=q.device) if dq is None else dq
-    dk = torch.empty(ks, dtype=bf16, device=q.device) if dk is None else dk
-    dv = torch.empty(ks, dtype=bf16, device=q.device) if dv is None else dv
-    st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    if workspace is None:
-        workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size, int(doc_q is not None), 1),
-                               q.device)
+    given = (q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, dist_slopes,
+             doc_q, doc_kv, prefix_len, dq, dk, dv, dev_status, workspace)
+    side = _aside(stream)
+    with _alloc_on(side):
+        dq = torch.empty(qs, dtype=bf16, device=q.device) if dq is None else dq
+        dk = torch.empty(ks, dtype=bf16, device=q.device) if dk is None else dk
+        dv = torch.empty(ks, dtype=bf16, device=q.device) if dv is None else dv
+        st = torch.empty(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        if workspace is None:
+            workspace = _workspace(thd_score_workspace_size(B, T_q, T_kv, Hq, Hkv, D, cp_size,
+                                                            int(doc_q is not None), 1), q.device)
     _check(w, thd_attn_score_bwd(q, k, v, o, lse, dout, dq, dk, dv, dq_rows, dkv_rows, cu_seqlens_q, cu_seqlens_kv,
                                  cu_seqlens_q_padded, cu_seqlens_kv_padded, B, T_q, T_kv, Hq, Hkv, D, int(causal),
                                  scale, cp_size, pad_between_seqs, softcap, dist_slopes, doc_q, doc_kv, prefix_len,
                                  workspace, workspace.numel(), st, stream))
+    _keep(side, stream, given, (dq, dk, dv, st))
     return dq, dk, dv, st
 
 
@@ -558,16 +628,19 @@ def cp_partition(cu_seqlens, cu_seqlens_padded=None, *, cp_size, pad_between_seq
     B = cu_seqlens.numel() - 1
     dev = cu_seqlens.device
     cap = int(token_map_capacity) if token_map_capacity is not None else 0
-    out = {
-        "cu_rank": torch.empty((cp_size, B + 1), dtype=torch.int32, device=dev),
-        "cu_rank_padded": torch.empty((cp_size, B + 1), dtype=torch.int32, device=dev),
-        "cu_rank_half": torch.empty((cp_size, 2, B + 1), dtype=torch.int32, device=dev),
-        "token_map": torch.empty(max(cap, 1), dtype=torch.int32, device=dev),
-    }
-    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    side = _aside(stream)
+    with _alloc_on(side):
+        out = {
+            "cu_rank": torch.empty((cp_size, B + 1), dtype=torch.int32, device=dev),
+            "cu_rank_padded": torch.empty((cp_size, B + 1), dtype=torch.int32, device=dev),
+            "cu_rank_half": torch.empty((cp_size, 2, B + 1), dtype=torch.int32, device=dev),
+            "token_map": torch.empty(max(cap, 1), dtype=torch.int32, device=dev),
+        }
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
     _check("thd_cp_partition", thd_cp_partition(cu_seqlens, cu_seqlens_padded, B, cp_size, pad_between_seqs,
                                                 out["cu_rank"], out["cu_rank_padded"], out["cu_rank_half"],
                                                 out["token_map"] if cap else None, cap, st, stream))
+    _keep(side, stream, (cu_seqlens, cu_seqlens_padded), (*out.values(), st))
     return out, st
 
 
@@ -575,12 +648,14 @@ def lse_merge(o_acc, lse_acc, o_part, lse_part, stream=None):
     """In-place merge of (o_part, lse_part) into (o_acc, lse_acc)."""
     T, H, D = o_acc.shape
     _check("thd_lse_merge", thd_lse_merge(o_acc, lse_acc, o_part, lse_part, T, H, D, stream))
+    _keep(_aside(stream), stream, (o_acc, lse_acc, o_part, lse_part), ())
 
 
 def lse_merge_bf16(o_acc, lse_acc, o_part, lse_part, stream=None):
     """In-place merge of a bf16 partial (o_part, lse_part) into the fp32 (o_acc, lse_acc)."""
     T, H, D = o_acc.shape
     _check("thd_lse_merge_bf16", thd_lse_merge_bf16(o_acc, lse_acc, o_part, lse_part, T, H, D, stream))
+    _keep(_aside(stream), stream, (o_acc, lse_acc, o_part, lse_part), ())
 
 
 def grad_tail_zero(dq, dk, dv, cu_seqlens_q_padded, cu_seqlens_kv_padded, host_knows_no_tail=False, stream=None):
@@ -590,6 +665,7 @@ def grad_tail_zero(dq, dk, dv, cu_seqlens_q_padded, cu_seqlens_kv_padded, host_k
     _check("thd_grad_tail_zero", thd_grad_tail_zero(dq, dk, dv, dq.shape[0], dk.shape[0], Hq, Hkv, D,
                                                     cu_seqlens_q_padded, cu_seqlens_kv_padded, B,
                                                     int(host_knows_no_tail), stream))
+    _keep(_aside(stream), stream, (dq, dk, dv, cu_seqlens_q_padded, cu_seqlens_kv_padded), ())
 
 
 def cp_a2a(src, cu_seqlens_padded, *, cp_size, a2a_size, direction, out=None, dev_status=None, stream=None):
@@ -606,10 +682,13 @@ def cp_a2a(src, cu_seqlens_padded, *, cp_size, a2a_size, direction, out=None, de
         H = a * Hg
         shape = (cp_size, T // cp_size, H, D)
     B = cu_seqlens_padded.numel() - 1
-    dst = torch.empty(shape, dtype=src.dtype, device=src.device) if out is None else out
-    st = torch.zeros(1, dtype=torch.int32, device=src.device) if dev_status is None else dev_status
+    side = _aside(stream)
+    with _alloc_on(side):
+        dst = torch.empty(shape, dtype=src.dtype, device=src.device) if out is None else out
+        st = torch.zeros(1, dtype=torch.int32, device=src.device) if dev_status is None else dev_status
     _check("thd_cp_a2a", thd_cp_a2a(src, dst, cu_seqlens_padded, B, T, H, D, cp_size, a2a_size, direction, st,
                                     stream))
+    _keep(side, stream, (src, cu_seqlens_padded, out, dev_status), (dst, st))
     return dst, st
 
 
@@ -624,13 +703,16 @@ def attn_fwd_a2a(q, k, v, cu_seqlens, cu_seqlens_padded, *, cp_size, a2a_size, c
     T = cp * rows_r
     B = cu_seqlens.numel() - 1
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    nbytes = thd_a2a_workspace_size(B, T, Hq, Hkv, D, cp_size, a2a_size, 0)
-    ws = _workspace(nbytes, q.device) if workspace is None else workspace
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
+        st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        nbytes = thd_a2a_workspace_size(B, T, Hq, Hkv, D, cp_size, a2a_size, 0)
+        ws = _workspace(nbytes, q.device) if workspace is None else workspace
     _check("thd_attn_fwd_a2a", thd_attn_fwd_a2a(q, k, v, o, l, cu_seqlens, cu_seqlens_padded, B, T, Hq, Hkv, D,
                                                 int(causal), scale, cp_size, a2a_size, ws, ws.numel(), st, stream))
+    _keep(side, stream, (q, k, v, cu_seqlens, cu_seqlens_padded, out, lse, dev_status, workspace), (o, l, st))
     return o, l, st
 
 
@@ -644,15 +726,19 @@ def attn_bwd_a2a(q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_padded, *, cp_siz
     T = cp * rows_r
     B = cu_seqlens.numel() - 1
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
-    nbytes = thd_a2a_workspace_size(B, T, Hq, Hkv, D, cp_size, a2a_size, 1)
-    ws = _workspace(nbytes, q.device) if workspace is None else workspace
+    given = (q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_padded, dq, dk, dv, dev_status, workspace)
+    side = _aside(stream)
+    with _alloc_on(side):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        st = torch.zeros(1, dtype=torch.int32, device=q.device) if dev_status is None else dev_status
+        nbytes = thd_a2a_workspace_size(B, T, Hq, Hkv, D, cp_size, a2a_size, 1)
+        ws = _workspace(nbytes, q.device) if workspace is None else workspace
     _check("thd_attn_bwd_a2a", thd_attn_bwd_a2a(q, k, v, o, lse, dout, dq, dk, dv, cu_seqlens, cu_seqlens_padded, B,
                                                 T, Hq, Hkv, D, int(causal), scale, cp_size, a2a_size, ws, ws.numel(),
                                                 st, stream))
+    _keep(side, stream, given, (dq, dk, dv, st))
     return dq, dk, dv, st
 
 
@@ -685,23 +771,27 @@ def rope(q, k, positions, inv_freq, axis_of=None, *, adjacent=False, inverse=Fal
     n_axes = positions.shape[0] if positions.dim() == 2 else 1
     _need(w, inv.ndim == 1 and axis.shape == inv.shape and positions.dtype is torch.int32 and
           positions.shape[-1] == T and positions.get_device() == dev and positions.is_contiguous())
+    given = (q, k, positions, q_out, k_out)
     s_q, s_qo = _rope_rows(w, q, q, T, Hq, D), Hq * D
-    if q_out is None:
-        q_out = q.new_empty((T, Hq, D))
-    else:
+    if q_out is not None:
         s_qo = _rope_rows(w, q, q_out, T, Hq, D)
     Hkv = s_k = s_ko = 0
     if k is not None:
         Hkv = k.shape[1]
         s_k, s_ko = _rope_rows(w, q, k, T, Hkv, D), Hkv * D
-        if k_out is None:
-            k_out = k.new_empty((T, Hkv, D))
-        else:
+        if k_out is not None:
             s_ko = _rope_rows(w, q, k_out, T, Hkv, D)
     else:
         _need(w, k_out is None)
+    side = _aside(stream)
+    with _alloc_on(side):
+        if q_out is None:
+            q_out = q.new_empty((T, Hq, D))
+        if k is not None and k_out is None:
+            k_out = k.new_empty((T, Hkv, D))
     _check(w, thd_rope(q, k, q_out, k_out, s_q, s_k, s_qo, s_ko, T, Hq, Hkv, D, 2 * inv.size, positions, n_axes, inv,
                        axis, int(adjacent), int(inverse), dt, stream))
+    _keep(side, stream, given, (q_out, k_out))
     return q_out, k_out
 
 
@@ -718,9 +808,8 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
     shape, dtype = x.shape, x.dtype
     C = shape[-1]
     T = x.numel() // C if C else 0
-    if out is None:
-        out = torch.empty_like(x)
-    else:
+    given = (x, rng, residual, row_ids, out)
+    if out is not None:
         _need(w, out.shape == shape and out.dtype is dtype and out.get_device() == dev and out.is_contiguous())
     if residual is not None:
         _need(w, residual.shape == shape and residual.dtype is dtype and residual.get_device() == dev and
@@ -730,5 +819,10 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
               row_ids.is_contiguous())
     _need(w, x.is_contiguous() and rng.get_device() == dev and rng.numel() == 2 and rng.is_contiguous() and
           (rng.dtype is torch.int64 or rng.dtype is torch.uint64))
+    side = _aside(stream)
+    if out is None:
+        with _alloc_on(side):
+            out = torch.empty_like(x)
     _check(w, thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dt, stream))
+    _keep(side, stream, given, (out,))
     return out
