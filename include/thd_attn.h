@@ -334,8 +334,11 @@ THD_API int thd_attn_score_fwd(const void* q, const void* k, const void* v, void
  *     dx = P (dP - Delta) (1 - tanh^2(x / softcap)).
  * Arguments as thd_attn_bwd, with the modifications the forward was given;
  * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible.
- * Delta is corrected by the row sum of P (dP - Delta) where O's rounding to
- * bf16 would show.  Launches: planner, preprocess, dQ and dK/dV; with documents
+ * Delta, off by O's rounding to bf16, is corrected by the row sum of
+ * P (dP - Delta): for dK always, for dQ in rows that see at most 128 keys and in
+ * heads with |dist_slopes[h]| >= 0.375.  Elsewhere dQ is as exact as plain
+ * attention's: 2.4e-3 relative where the scores spread a row's weight, 3 to 4e-3
+ * where they gather it on a few keys.  Launches: planner, preprocess, dQ and dK/dV; with documents
  * two more; with few key tiles to go round, one that joins dK/dV's parts.
  */
 THD_API int thd_attn_score_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,

@@ -282,6 +282,20 @@ __host__ __device__ inline int2 key_seen_by(const P& p, const ScoreMods& mods, c
   return make_int2(lo, imax(lo, hi));
 }
 
+// The keys [x, y) of the rows first .. last of a query tile that see few keys: a
+// row that sees 1 to 128 has its interval inside, rows that see more may.  The
+// first row's document counts unless that row sees more than kFewKeys, the last
+// row's unless that one does (inside a document a row sees at least as many keys
+// as the one before, at most one more under a causal mask), those between always.
+constexpr int kFewKeys = 256;
+template <class P>
+__host__ __device__ inline int2 few_keys(const P& p, const ScoreMods& mods, const SeqGeom& g, int b, int first,
+                                         int last) {
+  const int2 a = query_sees(p, mods, g, b, first), z = query_sees(p, mods, g, b, last);
+  const int a_end = mods.rows_q ? mods.rows_q[(int64_t)g.q_off + first].y : g.Lkv;
+  return make_int2(a.y - a.x <= kFewKeys ? a.x : a_end, z.y - z.x <= kFewKeys ? z.y : z.x);
+}
+
 // First and last valid position of tile t of a sequence of L (first > last: none).
 __host__ __device__ inline int2 tile_rows(int L, int t) { return make_int2(t * kTile, imin((t + 1) * kTile, L) - 1); }
 
@@ -301,7 +315,8 @@ __host__ __device__ inline int rank_rows(const SeqGeom& g) {
 struct QItem {
   SeqGeom g;
   int b, r, t, h, kvh, qmax;
-  int k_lo, k_hi;  // scored: the keys the tile's queries may see
+  int k_lo, k_hi;      // scored: the keys the tile's queries may see
+  int few_lo, few_hi;  // scored: the keys of a walk for Delta (see few_keys)
 };
 
 // Work item w -> (schedule entry, query head).  Items are ordered by groups
@@ -330,7 +345,7 @@ __device__ inline QItem q_item(const P& p, int n_entries, int w) {
   }
   const int4 e = p.items[x];
   it.b = e.x;
-  it.r = e.y;
+  it.r = kMod != 0 ? 0 : e.y;
   it.t = e.z;
   it.kvh = it.h / (p.Hq / p.Hkv);
   it.g = seq_geom(p.eff, p.B, it.b, p.cp, p.causal, kMod != 0);
@@ -338,6 +353,8 @@ __device__ inline QItem q_item(const P& p, int n_entries, int w) {
     const int2 k = p.mods.ranges[x];
     it.k_lo = k.x;
     it.k_hi = k.y;
+    it.few_lo = e.y;
+    it.few_hi = e.w;
   } else {
     it.qmax = fwd_tile_qmax(it.g, it.r, it.t, p.cp);
   }
@@ -346,13 +363,13 @@ __device__ inline QItem q_item(const P& p, int n_entries, int w) {
 
 // Calls f(c, j) for every key tile the item visits, in ring order: step i
 // holds the KV of rank s = (r - i) mod cp, chunks s then 2cp-1-s.  Scored: the
-// sequence's tiles as chunk 0, the last first: under a causal mask and a bias
-// the nearest keys hold the maximum, which then hardly moves (32,768 tokens,
-// bias alone 4.6 -> 4.1 ms).
+// sequence's tiles as chunk 0 (those that hold one of `keys`), the last first:
+// under a causal mask and a bias the nearest keys hold the maximum, which then
+// hardly moves (32,768 tokens, bias alone 4.6 -> 4.1 ms).
 template <int kMod, class P, typename F>
-__device__ inline void for_each_kv_tile(const QItem& it, const P& p, F&& f) {
+__device__ inline void for_each_kv_tile(const QItem& it, const P& p, int2 keys, F&& f) {
   if constexpr (kMod != 0) {
-    const int2 n = tiles_in(it.k_lo, it.k_hi);
+    const int2 n = tiles_in(keys.x, keys.y);
     for (int j = n.y; j-- > n.x;) f(0, j);
     return;
   }
@@ -364,6 +381,11 @@ __device__ inline void for_each_kv_tile(const QItem& it, const P& p, F&& f) {
       for (int j = 0; j < n; ++j) f(c, j);
     }
   }
+}
+
+template <int kMod, class P, typename F>
+__device__ inline void for_each_kv_tile(const QItem& it, const P& p, F&& f) {
+  for_each_kv_tile<kMod>(it, p, kMod != 0 ? make_int2(it.k_lo, it.k_hi) : make_int2(0, 0), f);
 }
 
 // Columns (keys) of tile (c, j) any query of the item may see, rounded up to

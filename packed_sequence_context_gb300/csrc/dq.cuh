@@ -21,14 +21,27 @@
 // and dQ * scale is written as bf16 at the end of the item.
 //
 // Scored attention, Delta: rowsum(dO O) comes from O in bf16, an error of up to
-// 2^-9 |dO| |O| that dS = P (dP - Delta) takes over whole where few keys share
-// a row's weight (measured against fp64 on rows of 8 to 500 keys: dQ and dK off
-// by 3 to 6e-3, with an exact Delta by 2.4e-3).  The row sum of P (dP - Delta),
-// which is 0 for the exact Delta, corrects it: every item adds it up and leaves
-// the exact Delta for the dK/dV kernel, and an item of at most kTwiceKeys keys
-// walks them twice, the first time for Delta alone (more would cost more than
-// they give: their rows have more keys, dQ is off by 3 to 4e-3 at most, and
-// the walk takes two thirds of dQ's time again).
+// 2^-9 |dO| |O| that dS = P (dP - Delta) takes over whole; it shows in rows whose
+// weight lies on a few keys, most where dP - Delta itself is nearly 0.  The row
+// sum of P (dP - Delta), which is 0 for the exact Delta, corrects it: every item
+// adds it up and leaves the exact Delta for the dK/dV kernel.  For dQ itself an
+// item walks the keys of rows that see few of them a first time, for Delta alone:
+// those of short walks and of documents that begin or end inside its tile
+// (few_keys), or all of its keys where the head's slope is at least kSteepSlope
+// either way.
+// Others keep Delta from O, as plain attention does for every row: a walk for
+// Delta takes two thirds of dQ's time again, and how far the scores themselves
+// gather a row's weight is only known after it.  From kSteepSlope on Delta's
+// error outgrows that of dS's own rounding.  Emulated against fp64, 512 rows
+// behind 512 keys, D = 128: relative error of dQ, and of its worst row, with Delta
+// from O (corrected it is 2.4e-3 and 0.4% in every line):
+//   no bias 2.4e-3, 0.4%; slope 1/32 2.5e-3, 1.7%; 1/8 3.0e-3, 4%; 1/4 3.0e-3,
+//   7%; 3/8 3.3e-3, 6%; 0.7 4.0e-3, 40%; 2 6.0e-3, 8 times the row's norm
+//   documents of 512 rows 2.6e-3, 1%; 64 3.0e-3, 8%; 8 3.9e-3, the row's norm
+//   scores of standard deviation 3 under a cap 3.1e-3, 58%; 6 4.2e-3, 3 times
+// (the worst rows' gradients are nearly 0: their weight lies on one key).
+// What the walk for steep slopes costs: 12 padded sequences of 154 to 1409, 5 of
+// 32 heads, dQ 268 -> 289 us; 16,384 tokens in documents, 1 of 8 heads, 190 -> 223.
 //
 // CTA layout (one CTA per SM, persistent over the schedule): the dS warps, then
 // four warps with a role each.
@@ -92,11 +105,19 @@ struct DqCfg {
                 "register split above the launch budget");
 };
 
-// How often an item walks its key tiles (see above).
-constexpr int kTwiceKeys = 256;
+// An item's walks over its keys: the first one's, and whether it is the last (the
+// one that makes dQ, over all of them; else it is for Delta alone, see above).
+constexpr float kSteepSlope = 0.375f;
+__device__ inline int2 all_keys(const QItem& it) { return make_int2(it.k_lo, it.k_hi); }
 template <int kMod>
-__device__ inline int dq_passes(const QItem& it) {
-  return kMod != 0 && it.k_hi - it.k_lo <= kTwiceKeys ? 2 : 1;
+__device__ inline int2 first_keys(const DqParams& p, const QItem& it, bool& last) {
+  last = true;
+  if constexpr (kMod == 0) return make_int2(0, 0);
+  int2 k = make_int2(it.few_lo, it.few_hi);
+  if constexpr ((kMod & kModDist) != 0)
+    if (fabsf(p.mods.slopes[it.h]) >= kSteepSlope) k = all_keys(it);
+  last = k.x >= k.y;
+  return last ? all_keys(it) : k;
 }
 
 template <int D, bool kGrouped, int kMod>
@@ -224,9 +245,9 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         fence_proxy_async_smem();
         mbar_arrive(&bar_q_full);
         ++q_iter;
-        const int passes = dq_passes<kMod>(it);
-        for (int pass = 0; pass < passes; ++pass) {
-          for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+        bool last;
+        for (int2 keys = first_keys<kMod>(p, it, last);; keys = all_keys(it), last = true) {
+          for_each_kv_tile<kMod>(it, p, keys, [&](int c, int j) {
             if (!ok) return;
             if (!mbar_wait(&bar_k_empty[ks], kph ^ 1u, &s_abort)) {
               ok = false;
@@ -245,6 +266,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               kph ^= 1u;
             }
           });
+          if (last) break;
         }
         w = __shfl_sync(0xffffffffu, wnext, 0);
       }
@@ -265,9 +287,9 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
           int w;
           if (!item_take_one(&ring, kit, w, &s_abort) || w >= n_items) break;
           const QItem it = q_item<kGrouped, kMod>(p, n_entries, w);
-          const int passes = dq_passes<kMod>(it);
-          for (int pass = 0; pass < passes; ++pass) {
-            for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+          bool last;
+          for (int2 keys = first_keys<kMod>(p, it, last);; keys = all_keys(it), last = true) {
+            for_each_kv_tile<kMod>(it, p, keys, [&](int c, int j) {
               if (!ok) return;
               if (!mbar_wait(&bar_v_empty[vs], vph ^ 1u, &s_abort)) {
                 ok = false;
@@ -284,6 +306,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                 vph ^= 1u;
               }
             });
+            if (last) break;
           }
         }
         for (int s = 0; s < VS; ++s) {
@@ -337,11 +360,10 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             tc_commit(&bar_q_empty);
             continue;
           }
-          const int passes = dq_passes<kMod>(it);
-          for (int pass = 0; ok && pass < passes; ++pass) {
-            const bool last = pass + 1 == passes;
+          bool last;
+          for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
             int j = 0, prev_cols = 0;
-            for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
+            for_each_kv_tile<kMod>(it, p, keys, [&](int c, int jt) {
               if (!ok) return;
               const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
               const uint32_t b = g & 1u;
@@ -372,6 +394,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               ++j;
             });
             if (ok && !issue_dq(g - 1, prev_cols, n == 1, !last)) ok = false;
+            if (last) break;
           }
           if (!ok) break;
           tc_commit(&bar_dq_done);
@@ -404,11 +427,10 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             tc_commit(&bar_q_empty);
             continue;
           }
-          const int passes = dq_passes<kMod>(it);
-          for (int pass = 0; ok && pass < passes; ++pass) {
-            const bool last = pass + 1 == passes;
+          bool last;
+          for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
             int j = 0;
-            for_each_kv_tile<kMod>(it, p, [&](int c, int jt) {
+            for_each_kv_tile<kMod>(it, p, keys, [&](int c, int jt) {
               if (!ok) return;
               const int ncols = q_tile_ncols<kMod>(it, p, c, jt);
               // the dP buffer is free once the dS warps have read tile g-1's dP
@@ -435,6 +457,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               ++g;
               ++j;
             });
+            if (last) break;
           }
         }
         tc_commit(&bar_drain2);
@@ -484,11 +507,12 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         sc = score_consts<kMod, false>(p, it.h);
       }
       int jl = 0;
-      const int passes = dq_passes<kMod>(it);
-      for (int pass = 0; ok && pass < passes; ++pass) {
-        const bool last = pass + 1 == passes;
+      bool last;
+      for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
+        // a sum over part of the row's keys says nothing: such a row sees none here
+        if (kMod != 0 && !last && (sees.x < keys.x || sees.y > keys.y)) sees = make_int2(0, 0);
         float eps = 0.f;  // this thread's part of the row sum of P (dP - Delta)
-        for_each_kv_tile<kMod>(it, p, [&](int c, int j) {
+        for_each_kv_tile<kMod>(it, p, keys, [&](int c, int j) {
           if (!ok) return;
           const uint32_t b = g & 1u;
           if (!mbar_wait(&bar_s_full[b], (g >> 1) & 1u, &s_abort) || !mbar_wait(&bar_dp_full, g & 1u, &s_abort)) {
@@ -659,6 +683,8 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             dlt += s_eps[0][row];
           }
         }
+        if (last) break;
+        if (kMod != 0 && valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
       }
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;

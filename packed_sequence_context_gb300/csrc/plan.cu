@@ -63,7 +63,9 @@ __device__ inline void set_err(int* s_err, int code) { atomicMin(s_err, code); }
 constexpr int kPlanSmemSeqs = 1024;
 
 // a3: one schedule.  Query-tile entries are rank-local query tiles (b, r, t);
-// key-tile entries are chunk-aligned key tiles (b, c, jk).  Both are ordered
+// key-tile entries are chunk-aligned key tiles (b, c, jk); scored, both are tiles
+// of the whole sequence, c = 0, and a query tile's entry holds the keys that its
+// walk for Delta covers (see few_keys) in the places of r and of the cost.  Both are ordered
 // longest-first (counting sort on the number of tiles visited).  `eff` and
 // `toff` are where the planner reads the effective metadata and the tile
 // offsets (shared memory when they fit); `tile_off` receives the offsets in
@@ -109,7 +111,7 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   __syncthreads();
   // a scored schedule also leaves each entry's range of keys (queries), and
   // its cost is the number of tiles in it
-  auto entry = [&](int w, int& b, int& x, int& y, int& cost, int2& range) {
+  auto entry = [&](int w, int& b, int& x, int& y, int& cost, int2& range, int& few_hi) {
     b = upper_index(toff, B, w);
     // skip empty sequences that share the same offset
     while (b < B && toff[b + 1] <= w) ++b;
@@ -122,6 +124,9 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
       if (rows.x <= rows.y && mode == 1) {
         range.x = query_sees(p, p.mods, g, b, rows.x).x;
         range.y = query_sees(p, p.mods, g, b, rows.y).y;
+        const int2 few = few_keys(p, p.mods, g, b, rows.x, rows.y);
+        x = few.x;
+        few_hi = few.y;
       } else if (rows.x <= rows.y) {
         range.x = key_seen_by(p, p.mods, g, b, rows.x).x;
         range.y = key_seen_by(p, p.mods, g, b, rows.y).y;
@@ -143,11 +148,13 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   // a thread's first entry stays in registers between the two passes
   int4 first = make_int4(0, 0, 0, 0);
   int2 first_range = make_int2(0, 0);
+  int first_few_hi = 0;
+  const bool scored_q = ranges && mode == 1;
   for (int w = tid; w < total; w += nt) {
-    int b, x, y, cost;
+    int b, x, y, cost, few_hi = 0;
     int2 range = make_int2(0, 0);
-    entry(w, b, x, y, cost, range);
-    if (w == tid) first = make_int4(b, x, y, cost), first_range = range;
+    entry(w, b, x, y, cost, range, few_hi);
+    if (w == tid) first = make_int4(b, x, y, cost), first_range = range, first_few_hi = few_hi;
     atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
   }
   __syncthreads();
@@ -171,14 +178,15 @@ __device__ void plan_schedule(const PlanParams& p, const int32_t* eff, int32_t* 
   }
   __syncthreads();
   for (int w = tid; w < total; w += nt) {
-    int b = first.x, x = first.y, y = first.z, cost = first.w;
+    int b = first.x, x = first.y, y = first.z, cost = first.w, few_hi = first_few_hi;
     int2 range = first_range;
     if (w != tid) {
       range = make_int2(0, 0);
-      entry(w, b, x, y, cost, range);
+      few_hi = 0;
+      entry(w, b, x, y, cost, range, few_hi);
     }
     const int pos = atomicAdd(&s_hist[kCostBins - 1 - imin(cost, kCostBins - 1)], 1);
-    items[pos] = make_int4(b, x, y, cost);
+    items[pos] = make_int4(b, x, y, scored_q ? few_hi : cost);
     if (ranges) ranges[pos] = range;
   }
   if (tid == 0) {
