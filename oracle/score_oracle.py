@@ -13,9 +13,9 @@ conversion to log2 units and back (2^-22 |y|).
   P = e^(y - lse): relative (u + dl + dlse), u for its own rounding to bf16
   O:  sum of that over P |v|, and its rounding u |O|
   Delta = rowsum(dO O): sum |dO| tol(O), O being stored in bf16
-  dS: relative (u + dl + dlse) and P w (tol(Delta) + D 2^-24 sum |dO||v|)
-      and, under a cap, P |dP - Delta| 2^-19: tanh off by 2^-20 (see the cap)
-      is 1 - tanh^2 off by twice that, which counts where it is nearly 0
+  dS: relative (u + dl + dlse) and P w (tol(Delta) + D 2^-24 sum |dO||v|); w =
+      1 - tanh^2 is off relatively by 2^-12 (a rounded tanh's 2^-22 against the
+      1.3e-3 it is at x / softcap = 4) and 2 / softcap times the error of x
   dQ, dK, dV: those errors through the product, and the result's rounding."""
 
 from __future__ import annotations
@@ -98,7 +98,8 @@ def score(q, k, v, cu_q, cu_k, pad_q, pad_k, *, causal, scale, softcap=0.0, slop
             es = (U + dl + tl[:, None] + 2.0 ** -20) * np.abs(dS) * 1.01
             es = es + P * (td[:, None] + D * 2.0 ** -23 * (np.abs(dO) @ np.abs(V).T)) * (w + 2.0 ** -20) * 1.02
             if softcap:
-                es = es + 2.0 ** -19 * P * np.abs(dP - delta[:, None])
+                dx = scale * D * 2.0 ** -24 * (np.abs(Q) @ np.abs(K).T)
+                es = es + (2.0 ** -12 + 2 / softcap * dx) * np.abs(dS)
             out["dq"][rq, h] = scale * dS @ K
             out["tol_dq"][rq, h] = scale * es @ np.abs(K)
             out["dk"][rk, h // G] += scale * dS.T @ Q

@@ -232,6 +232,7 @@ static ScoreMods score_mods(const ScoreArgs& a, float scale, int causal, char* w
     const double c = (double)scale / a.softcap;
     m.cap_near = cap_polynomial(near_c, 3, 0.28, c, a.softcap, m.cap_n);
     m.cap_far = cap_polynomial(far_c, 5, 0.75, c, a.softcap, m.cap_f);
+    m.cap_sat = (float)(4.0 / c);
   }
   m.slopes = a.slopes;
   if (a.doc_q) {

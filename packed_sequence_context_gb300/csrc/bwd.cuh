@@ -591,11 +591,14 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
                 if (kCap && cut) score_fill(y, n_lo - 32 * kk, n_hi - 32 * kk, 0.f);
               };
               if constexpr (kCap) {
-                cap_in_form(cap, [&](auto form) {
+                cap_in_form_sat(cap, [&](auto form) {
                   load();
                   const float am = score_abs_max(y);
-                  cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f, 0.f);
-                  return cap_form(am, sc);
+                  if constexpr (decltype(form)::value == kCapSat)
+                    cap_sat_run(y, sc.cap_c);
+                  else
+                    cap_run<decltype(form)::value, 1, false>(y, sc, 1.f, 0.f, 0.f);
+                  return cap_form_sat(am, sc);
                 });
               } else {
                 load();
@@ -604,7 +607,8 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
               uint32_t pk[16];
               const int lo = n_lo - 32 * kk;
               const uint32_t n_seen = n_hi > n_lo ? (uint32_t)(n_hi - n_lo) : 0u;
-              auto write_p = [&](auto bias, auto with_cut) {
+              auto write_p = [&](auto bias, auto with_cut, auto sat) {
+                constexpr bool kSat = decltype(sat)::value != 0;
 #pragma unroll
                 for (int q4 = 0; q4 < 8; ++q4) {
                   const float4 l4 = lds128f(lse_s + 4 * (32 * kk + 4 * q4));  // lse in log2 units
@@ -618,7 +622,9 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
                       bias.at(n, c0, c1);
                       fadd2(b0, b1, b0, b1, c0, c1);
                     }
-                    ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                    float h0, h1;  // the score, or its tanh
+                    cap_tanh<kSat>(h0, h1, y[n], y[n + 1]);
+                    ffma2(x0, x1, h0, h1, a, a, b0, b1);
                     x0 = ex2(x0);
                     x1 = ex2(x1);
                     if constexpr (decltype(with_cut)::value != 0) {
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
                     }
                     if constexpr (kCap) {
                       float w0, w1;
-                      ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                      cap_slope<kSat>(w0, w1, y[n], y[n + 1], h0, h1);
                       fmul2(pv[i][n], pv[i][n + 1], w0, w1, x0, x1);
                     } else {
                       pv[i][n] = x0, pv[i][n + 1] = x1;
@@ -637,12 +643,16 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
                 }
               };
               auto write = [&](auto with_cut) {
-                if ((kMod & kModDist) != 0 && abs_needed)
-                  write_p(BiasRun<1, true>((float)(d0 + 32 * kk), sc.slope, 0.f), with_cut);
-                else
-                  write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f), with_cut);
+                write_p(BiasRun<1, false>((float)(d0 + 32 * kk), sc.slope, 0.f), with_cut, CapForm<0>{});
               };
-              if (cut)
+              const BiasRun<1, true> both_sides((float)(d0 + 32 * kk), sc.slope, 0.f);
+              if (kCap && cap == kCapSat)  // the form this run was made in
+                write_p(both_sides, CapForm<1>{}, CapForm<kCap>{});
+              else if ((kMod & kModDist) != 0 && !kCap && abs_needed && !cut)
+                write_p(both_sides, CapForm<0>{}, CapForm<0>{});
+              else if ((kMod & kModDist) != 0 && abs_needed)  // under a cap always with the cut (see cap_sat_run)
+                write_p(both_sides, CapForm<1>{}, CapForm<0>{});
+              else if (cut)
                 write(CapForm<1>{});
               else
                 write(CapForm<0>{});

@@ -40,6 +40,7 @@ struct ScoreMods {
   // |s| <= cap_near, five while |s| <= cap_far (0: never)
   float cap_n[3], cap_near;
   float cap_f[5], cap_far;
+  float cap_sat;          // |s| past which dK/dV takes 1 - tanh^2 apart from tanh
   const float* slopes;    // [Hq], or null
   const int2* rows_q;     // per query row: the keys [x, y) of its document, or null
   const int2* rows_kv;    // per key row: the queries [x, y) of its document, or null

@@ -576,27 +576,37 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                 if (ch < nch) {
                   float y[32];
                   const bool cut = load(y, ch);
+                  constexpr int kForm = decltype(form)::value;
+                  constexpr bool kWide = kCap && kForm == kCapWide;
                   if constexpr (kCap) {
                     am = fmaxf(am, score_abs_max(y));
-                    cap_run<decltype(form)::value, -1, false>(y, sc, 1.f, 0.f, 0.f);
+                    if constexpr (!kWide) cap_run<kForm, -1, false>(y, sc, 1.f, 0.f, 0.f);
                   }
+                  // wide: tanh = -1 there instead of P = 0, and dP - Delta = 0
                   if (cut) {
                     score_fill(y, from - 32 * ch, cnt - 32 * ch, -INFINITY);
-                    score_fill(reinterpret_cast<float(&)[32]>(dr[kk]), from - 32 * ch, cnt - 32 * ch, 0.f);
+                    score_fill(reinterpret_cast<float(&)[32]>(dr[kk]), from - 32 * ch, cnt - 32 * ch, kWide ? dlt : 0.f);
                   }
                   const float a = kCap ? sc.cap_a : sl2;
+                  const float top = kWide ? a - lse2 : -lse2;
                   auto write_ds = [&](auto bias) {
 #pragma unroll
                     for (int n = 0; n < 32; n += 2) {
-                      float x0, x1, t0, t1, b0 = -lse2, b1 = -lse2;
+                      float x0, x1, t0, t1, w0, w1, b0 = top, b1 = top;
                       if constexpr ((kMod & kModDist) != 0) bias.at(n, b0, b1);
-                      ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                      if constexpr (kWide) {
+                        cap_wide_grad(x0, x1, w0, w1, y[n], y[n + 1], sc.cap_c);
+                        ffma2(x0, x1, x0, x1, -a, -a, b0, b1);
+                        // a masked key's bias may be far above the row's lse
+                        if constexpr ((kMod & kModDist) != 0) x0 = fmin_nan(x0, 127.f), x1 = fmin_nan(x1, 127.f);
+                      } else {
+                        ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
+                      }
                       fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
                       fmul2(t0, t1, ex2(x0), ex2(x1), t0, t1);
                       fadd2(es[0], es[1], es[0], es[1], t0, t1);
                       if constexpr (kCap) {
-                        float w0, w1;
-                        ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
+                        if constexpr (!kWide) ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
                         fmul2(y[n], y[n + 1], t0, t1, w0, w1);
                       } else {
                         y[n] = t0, y[n + 1] = t1;
@@ -605,9 +615,9 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                   };
                   const float d0 = (float)(ahead - 1 - 32 * ch);
                   if ((kMod & kModDist) != 0 && abs_needed)
-                    write_ds(BiasRun<-1, true>(d0, sc.slope, -lse2));
+                    write_ds(BiasRun<-1, true>(d0, sc.slope, top));
                   else
-                    write_ds(BiasRun<-1, false>(d0, sc.slope, -lse2));
+                    write_ds(BiasRun<-1, false>(d0, sc.slope, top));
                   if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
 #pragma unroll
                   for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);

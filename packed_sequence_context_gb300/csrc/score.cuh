@@ -42,6 +42,7 @@ struct ScoreConsts {
   float cap_c;     // 2 log2(e) softmax_scale / softcap
   float cap_n[3], cap_near;  // tanh = s (n0 + n1 s^2 + ..) while |s| <= cap_near; kForward: times cap_a
   float cap_f[5], cap_far;
+  float cap_sat;
   float slope;  // the head's slope log2(e)
 };
 template <int kMod, bool kForward, class P>
@@ -56,6 +57,7 @@ THD_DEV ScoreConsts score_consts(const P& p, int h) {
   for (int i = 0; i < 5; ++i) k.cap_f[i] = p.mods.cap_f[i] * (kForward ? k.cap_a : 1.f);
   k.cap_near = p.mods.cap_near;
   k.cap_far = p.mods.cap_far;
+  k.cap_sat = p.mods.cap_sat;
   k.slope = 0.f;
   if constexpr ((kMod & kModDist) != 0) k.slope = p.mods.slopes[h] * 1.4426950408889634f;
   return k;
@@ -117,6 +119,32 @@ THD_DEV void cap_in_form(int& form, F&& run) {
   if (!done) run(CapForm<kCapWide>{});
 }
 
+// dK/dV has a form more, for scores past cap_sat (see cap_sat_run).
+constexpr int kCapSat = 3;
+THD_DEV int cap_form_sat(float abs_max, const ScoreConsts& k) {
+  if (__all_sync(0xffffffffu, abs_max <= k.cap_near)) return kCapNear;
+  if (__all_sync(0xffffffffu, abs_max <= k.cap_far)) return kCapFar;
+  return __any_sync(0xffffffffu, abs_max > k.cap_sat) ? kCapSat : kCapWide;
+}
+template <typename F>
+THD_DEV void cap_in_form_sat(int& form, F&& run) {
+  bool done = false;
+  if (form == kCapNear) {
+    form = run(CapForm<kCapNear>{});
+    done = form == kCapNear;
+  }
+  if (!done && form == kCapFar) {
+    const int f = run(CapForm<kCapFar>{});
+    done = f <= kCapFar;
+    if (!done) form = f;
+  }
+  if (!done && form == kCapWide) {
+    done = run(CapForm<kCapWide>{}) != kCapSat;
+    if (!done) form = kCapSat;
+  }
+  if (!done) run(CapForm<kCapSat>{});
+}
+
 // The polynomial's value at two scores: tanh = s times it.
 template <int kForm>
 THD_DEV void cap_poly(float& q0, float& q1, float s0, float s1, const ScoreConsts& k) {
@@ -140,6 +168,61 @@ THD_DEV void cap_wide(float& r0, float& r1, float s0, float s1, float c) {
   fadd2(a0, a1, ex2(fmin_nan(x0, 60.f)), ex2(fmin_nan(x1, 60.f)), 1.f, 1.f);
   const float q = rcp(a0 * a1);
   fmul2(r0, r1, q, q, a1, a0);
+}
+
+// dQ's wide form, of two scores: R = 2 / (1 + e), e = 2^(c s), gives tanh = 1 - R
+// and w = 1 - tanh^2 = e R^2, as many instructions as 1 - tanh^2 from tanh, and w
+// keeps its relative precision however near to 1 |tanh| is.  From a rounded tanh
+// it is off by up to 2^-22 / w: 2e-4 at x / cap = 4, 3% at 7, 20% at 8, and twice
+// that at -7 and -8.
+THD_DEV void cap_wide_grad(float& r0, float& r1, float& w0, float& w1, float s0, float s1, float c) {
+  float x0, x1, a0, a1;
+  fmul2(x0, x1, s0, s1, c, c);
+  const float e0 = ex2(fmin_nan(x0, 60.f)), e1 = ex2(fmin_nan(x1, 60.f));
+  ffma2(a0, a1, e0, e1, 0.5f, 0.5f, 0.5f, 0.5f);
+  const float q = rcp(a0 * a1);
+  fmul2(r0, r1, q, q, a1, a0);
+  fmul2(w0, w1, e0, e1, r0, r1);
+  fmul2(w0, w1, w0, w1, r0, r1);
+}
+
+// dK/dV's form for saturated scores.  It makes P and 1 - tanh^2 in a pass of their
+// own, from one value a score, and has no register left for R and e there: that
+// took 9.1 instead of 8.5 ms (32,768 tokens, 16 + 4 heads of 128, cap 50) whatever
+// the form.  Here the value is u = sign(s) (1 - |tanh|) = sign(s) 2 z / (1 + z),
+// z = 2^(-c |s|); with S = sign(u), tanh = S - u and 1 - tanh^2 = u (S + tanh).  It
+// takes more instructions than the wide form (every score past 4: 8.5 -> 10.2 ms),
+// hence only from x / cap = 4 on (cap_sat), where that is off by 2e-4.  A fifth copy
+// of that pass (with a cap and a bias both sides of it, cut or not) took 10.4
+// instead of 8.7 ms, so under a cap the bias of both sides always has the cut.
+template <int N>
+THD_DEV void cap_sat_run(float (&s)[N], float c) {
+#pragma unroll
+  for (int n = 0; n < N; n += 2) {
+    const float z0 = ex2(-c * fabsf(s[n])), z1 = ex2(-c * fabsf(s[n + 1]));
+    float a0, a1, r0, r1;
+    ffma2(a0, a1, z0, z1, 0.5f, 0.5f, 0.5f, 0.5f);
+    const float q = rcp(a0 * a1);  // z <= 1: no limit on the exponents
+    fmul2(r0, r1, q, q, a1, a0);
+    fmul2(r0, r1, r0, r1, z0, z1);
+    s[n] = copysignf(r0, s[n]);
+    s[n + 1] = copysignf(r1, s[n + 1]);
+  }
+}
+// tanh and 1 - tanh^2 of two scores, from tanh or (kSat) from u.
+template <bool kSat>
+THD_DEV void cap_tanh(float& t0, float& t1, float s0, float s1) {
+  t0 = s0, t1 = s1;
+  if constexpr (kSat) fadd2(t0, t1, copysignf(1.f, s0), copysignf(1.f, s1), -s0, -s1);
+}
+template <bool kSat>
+THD_DEV void cap_slope(float& w0, float& w1, float s0, float s1, float t0, float t1) {
+  if constexpr (kSat) {
+    fadd2(w0, w1, copysignf(1.f, s0), copysignf(1.f, s1), t0, t1);
+    fmul2(w0, w1, w0, w1, s0, s1);
+  } else {
+    ffma2(w0, w1, -t0, -t1, t0, t1, 1.f, 1.f);
+  }
 }
 
 // A run's bias: score n has b(n) = -slope |d0 + dir n|, dir = -1 where the

@@ -33,6 +33,9 @@ CASES = {
     "documents in wide tiles": ([1200], 2, 1, 128, 1, {"docs": [700, 3, 290, 5]}),
     "documents both ways": ([900], 2, 2, 64, 0, {"docs": [300, 6, 280], "cap": 15.0}),
     "near the cap": ([500], 2, 1, 64, 1, {"cap": 6.0, "std": 5.0}),
+    # every score at 5.5 to 8.5 times the cap, of either sign
+    "saturated": ([300], 2, 2, 64, 1, {"cap": 5.0, "saturated": 0.5}),
+    "saturated below": ([300], 2, 1, 128, 1, {"cap": 5.0, "saturated": 1.0, "slopes": [0.01, -0.02]}),
     "gathered scores": ([800], 2, 2, 128, 1, {"cap": 50.0, "std": 6.0}),
 }
 
@@ -42,6 +45,13 @@ def _make(name):
     seed = 1000 + sum(map(ord, name))
     c = inputs.make_cross(lengths, lengths, pad_to=4, Hq=Hq, Hkv=Hkv, D=D, cp_size=2, seed=seed)
     c["q"] = (c["q"].float() * mods.get("std", 1.5)).bfloat16()
+    if "saturated" in mods:   # the scores lie on the first element: 5 x 7, spread by the other elements' share of them
+        rng = np.random.default_rng(seed)
+        n, hk = c["k"].shape[0], Hkv
+        c["q"] *= 0.3
+        c["q"][:, :, 0] = 16.0
+        sign = torch.from_numpy(np.where(rng.random((n, hk)) < mods["saturated"], -1.0, 1.0))
+        c["k"][:, :, 0] = (sign * (35.0 + 5.0 * torch.from_numpy(rng.uniform(-1, 1, (n, hk)))) * D ** 0.5 / 16).bfloat16()
     m = {"softcap": mods.get("cap", 0.0), "slopes": None, "doc_q": None, "doc_k": None, "prefix": None}
     if "slopes" in mods:
         m["slopes"] = np.array(mods["slopes"], np.float32)
@@ -92,6 +102,8 @@ def _rounded(c, m, causal, scale, mistake=None):
             if mistake == "dK with Delta from O":
                 delta_k = (dO * O).sum(-1)
             w = 1 - (0.98 if mistake == "0.98 tanh^2" else 1.0) * t * t
+            if mistake == "1 - tanh^2 of a rounded tanh":
+                w = 1 - t.astype(np.float32).astype(np.float64) ** 2
             if mistake == "a key too many":   # every row's first masked key
                 first = np.where(see.any(1), see.argmax(1) - 1, -1)
                 for i in np.flatnonzero(first >= 0):
@@ -133,6 +145,8 @@ def test_the_models_values_are_the_oracles():
     ("documents in wide tiles", "Delta from O everywhere", ("dq",)),
     ("steep", "dK with Delta from O", ("dk",)), ("documents of few", "dK with Delta from O", ("dk",)),
     ("near the cap", "0.98 tanh^2", ("dq", "dk")),
+    ("saturated", "1 - tanh^2 of a rounded tanh", ("dq", "dk")),
+    ("saturated below", "1 - tanh^2 of a rounded tanh", ("dq", "dk")),
     ("documents in wide tiles", "a key too many", ("dv",)), ("gentle", "scale 1% off", ("dq", "dk"))])
 def test_planted_mistakes_break_them(name, mistake, shows):
     c, m, causal, scale = _make(name)
