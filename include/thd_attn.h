@@ -495,8 +495,8 @@ THD_API int thd_attn_bwd_a2a(const void* q, const void* k, const void* v, const 
  *     (a, b) -> (a cos - b sin, b cos + a sin).
  * Elements past rot_dim are copied.  inverse = 1 turns by -angle: the
  * gradient of the inputs from the gradient of the outputs.  Angles are exact
- * to 2^-24 turns at any 32-bit position; products and sums are fp32, rounded
- * once.
+ * to 2^-24 turns at any 32-bit position for |inv_freq| up to 2^40 (past that
+ * the error grows with it); products and sums are fp32, rounded once.
  *   q_in, q_out: rows of [Hq, D]; k_in, k_out: rows of [Hkv, D] (NULL with
  *     Hkv = 0: queries alone).  `..._stride`: elements between rows, at least
  *     H * D (larger for a slice of a fused projection's output, as input or

@@ -890,10 +890,7 @@ int thd_rope(const void* q_in, const void* k_in, void* q_out, void* k_out, int64
   std::memset(&p, 0, sizeof(p));
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!std::isfinite(inv_freq[i]) || axis_of[i] >= n_axes) return THD_ERR_INVALID_ARG;
-    // turns per position: whole turns drop out at whole positions
-    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double frac = turns - std::floor(turns);              // in [0, 1]
-    p.turn[i] = (uint64_t)std::ldexp(frac, 63) << 1;            // 2^64 wraps to 0
+    p.turn[i] = rope_turn(inv_freq[i]);
     p.axis[i] = axis_of[i];
   }
   p.x[0] = RopeTensor{q_in, q_out, q_in_stride, q_out_stride, Hq};

@@ -7,10 +7,10 @@
 // and the elements past rot_dim are copied.
 //
 // The angle is reduced exactly, without floating point: the host gives f_i as
-// F_i = f_i / (2 pi) in turns, a 64-bit binary fraction, and position * F_i
-// modulo 2^64 is the fraction of a turn whatever the position (a 32-bit
-// product would be off by position * 2^-33 turns; this one by position * 2^-55,
-// the rounding of f_i itself).  Its top 32 bits, as a signed number of half
+// F_i = f_i / (2 pi) in turns, a 64-bit binary fraction (rope_turn), and
+// position * F_i modulo 2^64 is the fraction of a turn whatever the position (a
+// 32-bit product would be off by position * 2^-33 turns; this one by
+// position * 2^-64).  Its top 32 bits, as a signed number of half
 // turns, go to sincospif.
 //
 // What bounds it: HBM.  Every element is read and written once; a token's
