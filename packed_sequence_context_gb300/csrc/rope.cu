@@ -10,8 +10,9 @@
 // F_i = f_i / (2 pi) in turns, a 64-bit binary fraction (rope_turn), and
 // position * F_i modulo 2^64 is the fraction of a turn whatever the position (a
 // 32-bit product would be off by position * 2^-33 turns; this one by
-// position * 2^-64).  Its top 32 bits, as a signed number of half
-// turns, go to sincospif.
+// position * 2^-64).  Its quarter turns are taken off as integers too, and what
+// is left, at most 1/8 turn either way, goes to sincospif: 24 bits of it round
+// the angle by 2^-27 turns, of the whole fraction they would by 2^-25.
 //
 // What bounds it: HBM.  Every element is read and written once; a token's
 // cosines and sines are computed once and shared by all of its heads (40 heads
@@ -36,11 +37,14 @@ constexpr int kRopeHeads = 4;      // heads a thread walks, at least, where a to
 // cos and sin of the angle of pair i at token t
 __device__ inline float2 rope_cos_sin(const RopeParams& p, int64_t t, int i) {
   const int64_t pos = p.pos[(int64_t)p.axis[i] * p.T + t];
-  const uint64_t frac = (uint64_t)pos * p.turn[i] + 0x80000000ull;  // rounded to 32 bits
-  const float half_turns = (float)(int32_t)(frac >> 32) * 0x1p-31f;
+  const uint64_t frac = (uint64_t)pos * p.turn[i];
+  const uint32_t quarters = (uint32_t)((frac + (1ull << 61)) >> 62);  // the nearest, mod 4
+  const float half_turns = (float)(int64_t)(frac - ((uint64_t)quarters << 62)) * 0x1p-63f;  // within +-1/4 of it
   float s, c;
   sincospif(half_turns, &s, &c);
-  return make_float2(c, p.inverse ? -s : s);
+  const float x = quarters & 1 ? -s : c, y = quarters & 1 ? c : s;
+  const float cs = quarters & 2 ? -x : x, sn = quarters & 2 ? -y : y;
+  return make_float2(cs, p.inverse ? -sn : sn);
 }
 
 // Eight consecutive elements, as loaded.

@@ -3,10 +3,12 @@ both sides of 1: the host's part (turns per position as a 64-bit fraction,
 rope_turn) on the CPU against 100-digit arithmetic, and sines and cosines on the
 GPU against the exactly reduced angle.
 
-GPU tolerance, fp32, on inputs (1, 0) and (0, 1): the angle is rounded to a
-24-bit float of half turns, 2^-26 turns, after one to 2^-33 turns; sine and
-cosine are off by two units in the last place, 2^-23 at most, and the result by
-one rounding, 2^-24: below 2 pi (2^-26 + 2^-33) + 3 2^-24 < 2^-21."""
+GPU tolerance, fp32, on inputs (1, 0) and (0, 1): the angle lies within 1/8 turn
+of a quarter and is rounded to 24 bits there, 2^-27 turns at most, and the turns
+per position are off by 2^-64 at positions up to 2^31, 2^-33 turns.  Sine and
+cosine, of at most pi / 4 either way and so with half a unit of at most 2^-25,
+are off by two units in the last place, 2^-23, and the result by one rounding,
+2^-25: below 2 pi (2^-27 + 2^-33) + 2^-23 + 2^-25 = 2.0e-7 < 2^-22."""
 
 import os
 import shutil
@@ -94,4 +96,4 @@ def test_sines_at_any_position(thd_lib, inverse):
             a = 2 * np.pi * float(frac if frac < Fraction(1, 2) else frac - 1) * (-1 if inverse else 1)
             want = [np.cos(a), np.sin(a), -np.sin(a), np.cos(a)]
             have = [y[t, 0, i], y[t, 0, len(fs) + i], y[t, 1, i], y[t, 1, len(fs) + i]]
-            assert np.abs(np.subtract(have, want)).max() <= 2.0 ** -21, (p, f)
+            assert np.abs(np.subtract(have, want)).max() <= 2.0 ** -22, (p, f)
