@@ -302,7 +302,9 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
  * A query that sees no key gets o = 0, lse = -inf (and zero gradients).
  *   softcap: 0 (no cap), or positive with softmax_scale / softcap between
  *     2^-40 and 2^40.
- *   dist_slopes: device fp32 [Hq] or NULL, finite (constants: no gradient).
+ *   dist_slopes: device fp32 [Hq] or NULL (constants: no gradient), of either
+ *     sign; slope times distance must stay below 2^100.  Scores are fp32: a key's
+ *     y, and a row's lse, are exact to 2^-22 of their size.
  *   doc_q [T_q], doc_kv [T_kv]: device int32 document number of every row, or
  *     both NULL.  They may be one array.  Inside a sequence the numbers of
  *     its valid rows must not decrease (else THD_DEV_ERR_DOC_ORDER); rows

@@ -555,11 +555,11 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
         } else {
           if (p.causal) n_lo = imin(imax(j_pos - it.g.koff - q0, 0), kTile);
         }
-        // scored: d = i' - j of query column 0; a visible column with i' < j
-        const int d0 = q0 + it.g.koff - j_pos;
-        const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, n_lo < n_hi && d0 + n_lo < 0);
         ScoreConsts sc;
         if constexpr (kMod != 0) sc = score_consts<kMod, false>(p, h);
+        // scored: d = i' - j of query column 0; a visible column with i' < j
+        const int d0 = q0 + it.g.koff - j_pos;
+        const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, n_lo < n_hi && (d0 + n_lo < 0 || fabsf(sc.slope) > kSteepBias));
         // the cp.async writes of lse/Delta are visible to the threads that
         // observe the stage barrier's phase, so observe it here (it cannot have
         // moved on: the stage is refilled only after this step's p_ready)

@@ -617,7 +617,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                   if ((kMod & kModDist) != 0 && abs_needed)
                     write_ds(BiasRun<-1, true>(d0, sc.slope, top));
                   else
-                    write_ds(BiasRun<-1, false>(d0, sc.slope, top));
+                    write_ds(BiasRun<-1, false, true>(d0, sc.slope, top));
                   if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
 #pragma unroll
                   for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(384, 1)
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
         sc = score_consts<kMod, true>(p, it.h);
       }
+      const int linear = (kMod & kModDist) != 0 ? linear_to(sc, pos + it.g.koff) : 0;
       // ---- key tiles
       float m = -INFINITY, l = 0.f;  // running max (log2 units, shared value) and this half's sum
       if constexpr (kTurns)  // bounded scores: their largest bias, throughout
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(384, 1)
           // goes over columns already read (chunk k -> column 64 (k/2) + 16 (k%2))
           const uint32_t tcol = tmem + lane_base + sb * 128u;
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
-          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt + j0 - 1 > linear);
 #pragma unroll 1
           for (int k = 0; k < nch; ++k) {
             const bool cut = __any_sync(0xffffffffu, cnt < 32 * k + 32 || from > 32 * k);
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(384, 1)
           const bool cut = __any_sync(0xffffffffu, cnt - 32 * k0 < nvalid || from > 32 * k0);
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
           if constexpr (kMod != kScored) {
-            const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+            const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt + j0 - 1 > linear);
             auto score = [&](auto form) {
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk)

@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(384, 1)
         if (valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
         sc = score_consts<kMod, true>(p, it.h);
       }
+      const int linear = (kMod & kModDist) != 0 ? linear_to(sc, pos + it.g.koff) : 0;
       // ---- key tiles
       float m = -INFINITY, l = 0.f;  // running max (log2 units) and sum of the row
       if constexpr (kBounded)  // bounded scores: their largest bias, throughout (see fwd.cuh)
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(384, 1)
           // the row's chunks of 32 scores one at a time; packed P of chunk k goes
           // to columns [16 k, 16 k + 16), all of which this thread has read
           const int ahead = pos + it.g.koff - j0 + 1;  // columns up to the row's own position
-          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt > ahead);
+          const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, cnt > 0 && cnt + j0 - 1 > linear);
           auto cut = [&](int k) { return __any_sync(0xffffffffu, cnt < 32 * k + 32 || from > 32 * k); };
           // y = chunk k's scores + top in log2 units, -inf on masked keys; then(y)
           auto scores = [&](int k, float top, auto then) {

@@ -22,8 +22,14 @@
 //
 // The bias is linear in j on either side of i', so a row that sees only keys
 // up to its own position (every causal row without a prefix) takes one fused
-// multiply-add for it; other rows take the absolute value.
+// multiply-add for it; other rows take the absolute value.  base + step n leaves
+// near keys the rounding of the base, 2^-19 of the slope in a run of 32, so heads
+// with a steep slope take the absolute value too, and dQ, where that choice took
+// 5% of the kernel (cap and bias, 5.94 -> 6.24 ms), forms the distance first
+// (kExact: one more addition for two scores, 6.03 ms).
 #pragma once
+
+#include <climits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -227,23 +233,32 @@ THD_DEV void cap_slope(float& w0, float& w1, float s0, float s1, float t0, float
 
 // A run's bias: score n has b(n) = -slope |d0 + dir n|, dir = -1 where the
 // scores run along j and +1 along i'.  kAbs: some score sits past its own
-// position; else b(n) = base + step n.
-template <int kDir, bool kAbs>
+// position; else b(n) = base + step n, or with kExact top - slope (d0 + dir n).
+template <int kDir, bool kAbs, bool kExact = false>
 struct BiasRun {
   float d0, slope, base, step;
   THD_DEV BiasRun(float d0_, float slope_, float top) : d0(d0_), slope(slope_) {
-    base = kAbs ? top : top - slope_ * d0_;
+    base = kAbs || kExact ? top : top - slope_ * d0_;
     step = -slope_ * kDir;
   }
   THD_DEV void at(int n, float& b0, float& b1) const {
     if constexpr (kAbs) {
       b0 = fmaf(-slope, fabsf(d0 + kDir * n), base);
       b1 = fmaf(-slope, fabsf(d0 + kDir * (n + 1)), base);
+    } else if constexpr (kExact) {
+      float t0, t1;
+      fadd2(t0, t1, (float)(kDir * n), (float)(kDir * (n + 1)), d0, d0);
+      ffma2(b0, b1, t0, t1, -slope, -slope, base, base);
     } else {
       ffma2(b0, b1, step, step, (float)n, (float)(n + 1), base, base);
     }
   }
 };
+
+// A row at key position `at` takes the linear side for tiles whose keys it sees up
+// to this position: its own, or with a steep slope (log2 units) none.
+constexpr float kSteepBias = 4.f;
+THD_DEV int linear_to(const ScoreConsts& k, int at) { return fabsf(k.slope) > kSteepBias ? INT_MIN / 2 : at; }
 
 // One thread's N scores, in place: s[n] becomes a s[n] + b(n) + top.
 template <int kDir, bool kAbs, int N>

@@ -36,6 +36,10 @@ CASES = {
     # every score at 5.5 to 8.5 times the cap, of either sign
     "saturated": ([300], 2, 2, 64, 1, {"cap": 5.0, "saturated": 0.5}),
     "saturated below": ([300], 2, 1, 128, 1, {"cap": 5.0, "saturated": 1.0, "slopes": [0.01, -0.02]}),
+    # the row's own key or its neighbour has all of the weight, at a bias of 0 beside biases of 1e2 to 1e7
+    "very steep": ([500, 37], 4, 2, 64, 1, {"slopes": [40.0, 300.0, 3.0e4, 1.0e6]}),
+    "very steep cap": ([500, 37], 3, 3, 128, 1, {"slopes": [40.0, 3.0e4, 1.0e6], "cap": 20.0}),
+    "very steep both ways": ([300], 2, 1, 64, 0, {"slopes": [100.0, 1.0e5], "cap": 9.0}),
     "gathered scores": ([800], 2, 2, 128, 1, {"cap": 50.0, "std": 6.0}),
 }
 
@@ -159,6 +163,40 @@ def test_planted_mistakes_break_them(name, mistake, shows):
 
 
 # ------------------------------------------------------------------ GPU
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [T.THD_FWD_KERNEL_SINGLE, T.THD_FWD_KERNEL_DUAL])
+@pytest.mark.parametrize("name", [n for n in CASES if n.startswith("very steep")])
+def test_lse_beside_far_larger_biases(thd_lib, name, kernel):
+    """A row's lse against its scores' errors in score_oracle weighted by P: the
+    biases of keys without weight count nothing."""
+    c, m, causal, scale = _make(name)
+    (q, k, v, cu, _, pad, _), _ = _args(c)
+    g = lambda x: None if x is None else torch.from_numpy(x).cuda()  # noqa: E731
+    off = [g(c[n]) for n in ("cu_q", "cu_kv", "cu_q_pad", "cu_kv_pad")]
+    T.thd_test_select_fwd_kernel(kernel)
+    try:
+        _, lse, st = T.attn_score_fwd(c["q"].cuda(), c["k"].cuda(), c["v"].cuda(), *off, softcap=m["softcap"],
+                                      dist_slopes=g(m["slopes"]), cp_size=2, causal=causal, softmax_scale=scale)
+        T.check_status(st)
+    finally:
+        T.thd_test_select_fwd_kernel(0)
+    q, k, D, G = q.astype(np.float64), k.astype(np.float64), q.shape[2], q.shape[1] // k.shape[1]
+    for b in range(len(cu) - 1):
+        rows = slice(int(pad[b]), int(pad[b] + cu[b + 1] - cu[b]))
+        n = rows.stop - rows.start
+        see, at = so.visible(n, n, causal, None, None, None)
+        for h in range(q.shape[1]):
+            Q, K = q[rows, h], k[rows, h // G]
+            x = scale * Q @ K.T
+            bias = float(m["slopes"][h]) * np.abs(at[:, None] - np.arange(n))
+            y = (m["softcap"] * np.tanh(x / m["softcap"]) if m["softcap"] else x) - bias
+            P, want = so._softmax_rows(np.where(see, y, -np.inf))
+            dl = scale * D * 2.0 ** -24 * (np.abs(Q) @ np.abs(K).T) + m["softcap"] * 2.0 ** -20
+            dl = dl + 2.0 ** -22 * (bias + np.abs(y))
+            tol = (P * dl).sum(1) + 2.0 ** -20 + 2.0 ** -22 * np.abs(want)
+            assert np.all(np.abs(lse[h, rows].double().cpu().numpy() - want) <= tol)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", list(CASES))
 def test_gradients_row_by_row(thd_lib, name):
