@@ -763,12 +763,18 @@ def rope(q, k, positions, inv_freq, axis_of=None, *, adjacent=False, inverse=Fal
     import numpy as np
     import torch
     w = "thd_rope"
+    _need(w, q.dim() == 3 and (k is None or k.dim() == 3) and positions.dim() in (1, 2))
     T, Hq, D = q.shape
     dev = _current(w, q)
     dt = _dtype(w, q)
     inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    axis = np.zeros(inv.size, np.uint8) if axis_of is None else np.ascontiguousarray(axis_of, dtype=np.uint8)
     n_axes = positions.shape[0] if positions.dim() == 2 else 1
+    axis = np.zeros(inv.size, np.uint8) if axis_of is None else np.ascontiguousarray(axis_of)
+    if axis.dtype != np.uint8:  # numbers that a byte would change into others
+        _need(w, axis.dtype.kind in "iufb" and axis.size > 0 and 0 <= axis.min() and axis.max() < n_axes)
+        byte = axis.astype(np.uint8)
+        _need(w, np.array_equal(byte, axis))
+        axis = byte
     _need(w, inv.ndim == 1 and axis.shape == inv.shape and positions.dtype is torch.int32 and
           positions.shape[-1] == T and positions.get_device() == dev and positions.is_contiguous())
     given = (q, k, positions, q_out, k_out)
@@ -805,6 +811,7 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
     w = "thd_dropout_add"
     dev = _current(w, x)
     dt = _dtype(w, x)
+    _need(w, x.dim() >= 1)
     shape, dtype = x.shape, x.dtype
     C = shape[-1]
     T = x.numel() // C if C else 0
