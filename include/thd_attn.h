@@ -301,7 +301,7 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
  *   documents: query and key have the same number, doc_q[row] == doc_kv[row].
  * A query that sees no key gets o = 0, lse = -inf (and zero gradients).
  *   softcap: 0 (no cap), or positive with softmax_scale / softcap between
- *     2^-40 and 2^40.
+ *     2^-40 and 2^40; it and softmax_scale at most 2.3e38.
  *   dist_slopes: device fp32 [Hq] or NULL (constants: no gradient), of either
  *     sign; slope times distance must stay below 2^100.  Scores are fp32: a key's
  *     y, and a row's lse, are exact to 2^-22 of their size.

@@ -189,6 +189,8 @@ static int check_score(const ScoreArgs& a, float scale) {
   // powers of scale / softcap have to be floats (see cap_polynomial)
   const double c = a.softcap > 0.f ? (double)scale / a.softcap : 1.0;
   if (!(c >= 0x1p-40 && c <= 0x1p40)) return THD_ERR_INVALID_ARG;
+  // the kernels take both in log2 units
+  if (!std::isfinite((float)(kLog2e * scale)) || !std::isfinite((float)(kLog2e * a.softcap))) return THD_ERR_INVALID_ARG;
   if ((a.doc_q == nullptr) != (a.doc_kv == nullptr)) return THD_ERR_INVALID_ARG;
   if (!aligned(a.slopes, 4) || !aligned(a.doc_q, 4) || !aligned(a.doc_kv, 4) || !aligned(a.prefix, 4))
     return THD_ERR_INVALID_ARG;
