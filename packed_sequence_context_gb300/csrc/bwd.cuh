@@ -750,7 +750,7 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
         ++n_done;
         tc_fence_after();
       }
-if constexpr (C::kGroups == 4) {
+      if constexpr (C::kGroups == 4) {
         // dK, then dV: a quarter's registers do not hold both
         constexpr int kChO = D / 32 >= C::kGroups ? D / 32 / C::kGroups : 1;  // warpgroups past D have none
 #pragma unroll 1
@@ -778,48 +778,48 @@ if constexpr (C::kGroups == 4) {
         }
       } else {
 #pragma unroll 1
-      for (int kk = half * (D / 64); kk < (half + 1) * (D / 64); ++kk) {
-        uint32_t a[32], bq[32];
-        if (nsteps > 0) {
-          tmem_ld32(tmem + lane_base + C::kColDK + 32 * kk, a);
-          tmem_ld32(tmem + lane_base + C::kColDV + 32 * kk, bq);
-          tmem_ld_wait(a);
-          tmem_ld_wait(bq);
-        } else {
-#pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            a[n] = 0u;
-            bq[n] = 0u;
-          }
-        }
-        if (in_chunk) {
-          const float fk = valid_kv ? p.scale : 0.f;
-          const float fv = valid_kv ? 1.f : 0.f;
-          const int64_t grow = (int64_t)it.g.kv_off + j_pos;
-          uint16_t* dkp = p.dk + (grow * p.Hkv + it.hk) * D + 32 * kk;
-          uint16_t* dvp = p.dv + (grow * p.Hkv + it.hk) * D + 32 * kk;
-          uint32_t x[16], y[16];  // the 32 columns of dK and of dV, packed bf16
-#pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            x[n] = pack_bf16x2(__uint_as_float(a[2 * n]) * fk, __uint_as_float(a[2 * n + 1]) * fk);
-            y[n] = pack_bf16x2(__uint_as_float(bq[2 * n]) * fv, __uint_as_float(bq[2 * n + 1]) * fv);
-          }
-          if (v8_ok) {
-            // two 32-byte stores per tensor: each writes one whole sector of the row
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              st_global_v8(dkp + 16 * h2, *reinterpret_cast<const uint32_t(*)[8]>(x + 8 * h2));
-              st_global_v8(dvp + 16 * h2, *reinterpret_cast<const uint32_t(*)[8]>(y + 8 * h2));
-            }
+        for (int kk = half * (D / 64); kk < (half + 1) * (D / 64); ++kk) {
+          uint32_t a[32], bq[32];
+          if (nsteps > 0) {
+            tmem_ld32(tmem + lane_base + C::kColDK + 32 * kk, a);
+            tmem_ld32(tmem + lane_base + C::kColDV + 32 * kk, bq);
+            tmem_ld_wait(a);
+            tmem_ld_wait(bq);
           } else {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              reinterpret_cast<uint4*>(dkp)[n] = make_uint4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
-              reinterpret_cast<uint4*>(dvp)[n] = make_uint4(y[4 * n], y[4 * n + 1], y[4 * n + 2], y[4 * n + 3]);
+            for (int n = 0; n < 32; ++n) {
+              a[n] = 0u;
+              bq[n] = 0u;
+            }
+          }
+          if (in_chunk) {
+            const float fk = valid_kv ? p.scale : 0.f;
+            const float fv = valid_kv ? 1.f : 0.f;
+            const int64_t grow = (int64_t)it.g.kv_off + j_pos;
+            uint16_t* dkp = p.dk + (grow * p.Hkv + it.hk) * D + 32 * kk;
+            uint16_t* dvp = p.dv + (grow * p.Hkv + it.hk) * D + 32 * kk;
+            uint32_t x[16], y[16];  // the 32 columns of dK and of dV, packed bf16
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              x[n] = pack_bf16x2(__uint_as_float(a[2 * n]) * fk, __uint_as_float(a[2 * n + 1]) * fk);
+              y[n] = pack_bf16x2(__uint_as_float(bq[2 * n]) * fv, __uint_as_float(bq[2 * n + 1]) * fv);
+            }
+            if (v8_ok) {
+              // two 32-byte stores per tensor: each writes one whole sector of the row
+#pragma unroll
+              for (int h2 = 0; h2 < 2; ++h2) {
+                st_global_v8(dkp + 16 * h2, *reinterpret_cast<const uint32_t(*)[8]>(x + 8 * h2));
+                st_global_v8(dvp + 16 * h2, *reinterpret_cast<const uint32_t(*)[8]>(y + 8 * h2));
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                reinterpret_cast<uint4*>(dkp)[n] = make_uint4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
+                reinterpret_cast<uint4*>(dvp)[n] = make_uint4(y[4 * n], y[4 * n + 1], y[4 * n + 2], y[4 * n + 3]);
+              }
             }
           }
         }
-      }
       }
       tc_fence_before();
     }

@@ -16,10 +16,9 @@
 // with a residual 153 us (99%), without one (2/3 of the bytes to as much of the
 // generator) 119 us (85%), fp32 with one 292 us (104%); rows of 1,111 columns,
 // off every alignment, fp32 91% and bf16 with a residual 67%.
-#include <cuda_bf16.h>
-
 #include "common.cuh"
 #include "dropout.cuh"
+#include "vec8.cuh"
 
 namespace thd {
 
@@ -55,51 +54,6 @@ __device__ inline uint32_t keep_mask(const uint4& v, uint32_t drop16) {
   }
   return m;
 }
-
-template <typename E>
-struct Vec8;  // eight elements in 16-byte pieces
-template <>
-struct Vec8<uint16_t> {
-  uint4 v;
-  __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-  __device__ void set(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-  __device__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
 
 // C a multiple of 8 and 16-byte aligned tensors: a thread moves groups of
 // eight columns with 16-byte accesses, kDropBatch of them in flight while it
@@ -153,11 +107,6 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
 // mask of one group of eight, and the elements move one to a lane (coalesced
 // whatever the row's alignment), their mask byte fetched from the lane that
 // drew it.
-__device__ inline float to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ inline float to_f32(float v) { return v; }
-__device__ inline void put(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-__device__ inline void put(float* p, float v) { *p = v; }
-
 template <typename E, bool kResidual>
 __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const DropoutParams p) {
   const uint64_t seed = p.rng[0], offset = p.rng[1];

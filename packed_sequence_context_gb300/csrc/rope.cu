@@ -23,10 +23,9 @@
 // tokens of 32 + 8 heads of 128, bf16, 394 us (6816 GB/s, the rate of a plain
 // copy); with the loads after the angles, and both as floats (122 registers, two
 // blocks per SM instead of three), 675 us.
-#include <cuda_bf16.h>
-
 #include "common.cuh"
 #include "rope.cuh"
+#include "vec8.cuh"
 
 namespace thd {
 
@@ -46,52 +45,6 @@ __device__ inline float2 rope_cos_sin(const RopeParams& p, int64_t t, int i) {
   const float cs = quarters & 2 ? -x : x, sn = quarters & 2 ? -y : y;
   return make_float2(cs, p.inverse ? -sn : sn);
 }
-
-// Eight consecutive elements, as loaded.
-template <typename E>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-  uint4 v;
-  __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-  __device__ void set(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-  __device__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
 
 // 16-byte vectors: D a multiple of 8, rot of 16 (halves) or 8 (adjacent
 // pairs), every row 16-byte aligned.  A unit is what one thread moves of a
@@ -121,7 +74,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_vec_kernel(const __grid_
     out[w] = static_cast<E*>(p.x[w].out) + t * p.x[w].out_stride + first + c0;
   }
   constexpr int kBatch = sizeof(E) == 2 ? 4 : 2;  // heads in flight: 32 registers of loads
-  Raw8<E> a[kBatch], b[kBatch];
+  Vec8<E> a[kBatch], b[kBatch];
   auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -180,11 +133,6 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_vec_kernel(const __grid_
 
 // Any head size, rotated size and alignment: one thread per pair (or copied
 // element) of a token's heads, with the same cos and sin table.
-__device__ inline float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ inline float load1(const float* p) { return *p; }
-__device__ inline void store1(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-__device__ inline void store1(float* p, float v) { *p = v; }
-
 template <typename E, bool kAdjacent>
 __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 s_cs[kRopeMinTokens * kRopeMaxPairs];
@@ -211,9 +159,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const __grid_
         }
         const int64_t ia = base + (kAdjacent ? 2 * j : j), ib = base + (kAdjacent ? 2 * j + 1 : j + half);
         const float2 cs = s_cs[tl * half + j];
-        const float a = load1(in + ia), b = load1(in + ib);
-        store1(out + ia, a * cs.x - b * cs.y);
-        store1(out + ib, b * cs.x + a * cs.y);
+        const float a = to_f32(in[ia]), b = to_f32(in[ib]);
+        put(out + ia, a * cs.x - b * cs.y);
+        put(out + ib, b * cs.x + a * cs.y);
       }
     }
   }
