@@ -316,8 +316,12 @@ THD_API int thd_attn_bwd(const void* q, const void* k, const void* v, const void
  *   and the outputs are those of any cp_size, bit for bit.
  * Key tiles that no query of a tile sees are skipped, whatever mask hides
  * them.  With none of the four given the call is thd_attn_fwd.  Every row
- * with a valid token must hold finite q, k, v: a masked key's score counts
- * nothing, but its row of v is multiplied by 0.
+ * with a valid token must hold finite q, k, v, and so must up to 15 rows behind
+ * a sequence's last one, pad rows, the next sequence's, or rows behind the last
+ * (the backward: of dO too): a masked key's score counts nothing, but its row
+ * of v is multiplied by 0.  With a softcap of at most 55.4, P is formed without a
+ * running maximum, between 2^-80 and 2^80: elements of v have to be 0 or between
+ * 2^-40 and 2^30 in magnitude, or they may be lost or overflow.
  * Other arguments as thd_attn_fwd; the workspace is larger:
  * thd_score_workspace_size(.., has_docs = doc_q != NULL, 0).
  * Launches: planner and forward; with documents two more (checks, extents).
@@ -335,7 +339,8 @@ THD_API int thd_attn_score_fwd(const void* q, const void* k, const void* v, void
  * P = exp(y - lse), dP = dO v^T, Delta = rowsum(dO * O):
  *     dx = P (dP - Delta) (1 - tanh^2(x / softcap)).
  * Arguments as thd_attn_bwd, with the modifications the forward was given;
- * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible.
+ * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible for a
+ * workspace of the same size (a smaller one adds dK and dV up in other parts).
  * Delta, off by O's rounding to bf16, is corrected by the row sum of
  * P (dP - Delta): for dK always, for dQ in rows that see at most 128 keys and in
  * heads with |dist_slopes[h]| >= 0.375.  Elsewhere dQ is as exact as plain

@@ -190,7 +190,8 @@ static int check_score(const ScoreArgs& a, float scale) {
   const double c = a.softcap > 0.f ? (double)scale / a.softcap : 1.0;
   if (!(c >= 0x1p-40 && c <= 0x1p40)) return THD_ERR_INVALID_ARG;
   // the kernels take both in log2 units
-  if (!std::isfinite((float)(kLog2e * scale)) || !std::isfinite((float)(kLog2e * a.softcap))) return THD_ERR_INVALID_ARG;
+  if (!std::isfinite((float)(kLog2e * scale)) || !std::isfinite((float)(kLog2e * a.softcap)))
+    return THD_ERR_INVALID_ARG;
   if ((a.doc_q == nullptr) != (a.doc_kv == nullptr)) return THD_ERR_INVALID_ARG;
   if (!aligned(a.slopes, 4) || !aligned(a.doc_q, 4) || !aligned(a.doc_kv, 4) || !aligned(a.prefix, 4))
     return THD_ERR_INVALID_ARG;
@@ -328,6 +329,8 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   //   bias              1024: 243 / 244   2048: 359 / 394   8192: 1074 / 1321
   //   cap, bounded      1024: 237 / 234   2048: 328 / 367   8192: 880 / 1173
   //   cap, unbounded    2048: 437 / 438   4096: 725 / 776   8192: 1308 / 1473
+  // (by the sequences' mean length, the only one the host knows: documents cut
+  // walks shorter than that says, here, in the item orders and in bwd_parts)
   // With fewer items than the two streams of every SM the second one idles:
   // single below two items an SM (128 items of 4096 tokens, cap: 41 / 73; of 512
   // 17 / 19), and from 1024 tokens below four (512 of 1024 41 / 45, of 512 37 / 31).

@@ -34,7 +34,9 @@
 // The scores' function is evaluated while P is made; P (1 - t^2) stays in
 // registers until dP^T is there.  A cap doubles the compute warps' work per step
 // and their latencies set the pace (two warps a scheduler issued in 41% of the
-// cycles), hence four warpgroups.  Measured, two against four, before sequences were
+// cycles), hence four warpgroups.  32,768 tokens, 16 + 4 heads of 128, ms: plain 7.4
+// (1192 TFLOPS of the four products), masks 7.3, bias 7.8, cap 50 8.7, cap and bias
+// 8.9, every score saturated 10.5.  Measured, two against four, before sequences were
 // walked as a whole: 32,768 tokens, 16 + 4 heads of 128, cap 50 8.3 / 8.15 ms, cap and bias 9.9 / 8.7, every run in
 // the wide form of tanh 9.2 / 8.6, bias alone 7.7 / 7.8, masks alone 7.3 / 7.35
 // (plain 7.05: 1249 TFLOPS of the four products); cap on sequences of 256 100 /
@@ -559,7 +561,8 @@ __global__ void __launch_bounds__((bwd_split(kGrouped, kMod) ? BwdCfg<D, kMod>::
         if constexpr (kMod != 0) sc = score_consts<kMod, false>(p, h);
         // scored: d = i' - j of query column 0; a visible column with i' < j
         const int d0 = q0 + it.g.koff - j_pos;
-        const bool abs_needed = (kMod & kModDist) != 0 && __any_sync(0xffffffffu, n_lo < n_hi && (d0 + n_lo < 0 || fabsf(sc.slope) > kSteepBias));
+        const bool abs_needed = (kMod & kModDist) != 0 &&
+                                __any_sync(0xffffffffu, n_lo < n_hi && (d0 + n_lo < 0 || fabsf(sc.slope) > kSteepBias));
         // the cp.async writes of lse/Delta are visible to the threads that
         // observe the stage barrier's phase, so observe it here (it cannot have
         // moved on: the stage is refilled only after this step's p_ready)

@@ -253,10 +253,10 @@ __host__ __device__ inline int fwd_item_tiles(const SeqGeom& g, int r, int t, in
 // [128 t, 128 t + 128) of it, not of a rank's chunks.  Outputs do not depend on
 // that beyond rounding (every rank's rows lie in the one buffer, and scored
 // attention has no single ring step to expose), while chunks of a few dozen
-// rows leave most of a tile empty: a packed batch of 8 sequences of 488 to 3792,
-// 16 heads of 128, cap 50, walked by four ranks' chunks took 384 us, as a whole
-// 263; 12 padded sequences of 154 to 1409 with a bias, forward and backward,
-// 1310 and 764; one sequence of 28 113 and 36.
+// rows leave most of a tile empty.  By four ranks' chunks and as a whole, us, when
+// that changed: a packed batch of 8 sequences of 488 to 3792, 16 heads of 128, cap
+// 50, 384 and 238; 12 padded sequences of 154 to 1409 with a bias, forward and
+// backward, 1310 and 750; one sequence of 28 113 and 36.
 template <class P>
 __host__ __device__ inline int2 query_sees(const P& p, const ScoreMods& mods, const SeqGeom& g, int b, int pos) {
   int lo = 0, hi = g.Lkv;

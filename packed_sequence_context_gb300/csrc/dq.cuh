@@ -59,14 +59,16 @@
 // its dS, by the same thread (the tensor pipe runs one thread's MMAs in issue
 // order).
 //
-// 32,768 tokens, 16 + 4 heads of 128: plain 3.7 ms (1785 TFLOPS of the three
-// products), masks 3.7, bias 4.0, cap 50 4.75 (1385), cap and bias 5.3; the row
-// sum of P (dP - Delta) is 4% of that.  Two warpgroups against four (before the
+// 32,768 tokens, 16 + 4 heads of 128: plain 3.8 ms (1727 TFLOPS of the three
+// products), masks 3.75, cap 50 4.9 (1336), every score saturated 5.8; with the two
+// walks of 2 of the 16 heads, bias 4.4, cap and bias 6.05.  The row sum of
+// P (dP - Delta) is 4% of that.  Two warpgroups against four (before the
 // row sum, and before sequences were walked as a whole): cap 5.1 / 4.6, cap and
 // bias 6.2 / 5.2; bias alone, padded batch of 154 to 1409, 520 / 486 us,
 // sequences of 256 164 / 170; masks alone, 32,768 tokens, 3.8 / 4.0 ms.  With a
 // cap the tensor pipe is 59% busy and the schedulers issue in 65% of the cycles.
-// Sequences of 256 (keys walked twice): masks 131 us, plain 99.
+// 32,768 tokens in sequences of 256 (keys walked twice): masks 260 us, cap 317; of
+// 512 246 and 320.
 #pragma once
 
 #include "common.cuh"
@@ -585,7 +587,8 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                   // wide: tanh = -1 there instead of P = 0, and dP - Delta = 0
                   if (cut) {
                     score_fill(y, from - 32 * ch, cnt - 32 * ch, -INFINITY);
-                    score_fill(reinterpret_cast<float(&)[32]>(dr[kk]), from - 32 * ch, cnt - 32 * ch, kWide ? dlt : 0.f);
+                    score_fill(reinterpret_cast<float(&)[32]>(dr[kk]), from - 32 * ch, cnt - 32 * ch,
+                               kWide ? dlt : 0.f);
                   }
                   const float a = kCap ? sc.cap_a : sl2;
                   const float top = kWide ? a - lse2 : -lse2;

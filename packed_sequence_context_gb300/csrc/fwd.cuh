@@ -41,7 +41,7 @@
 // every tile: each scheduler holds one warp of either, in different phases of
 // their tiles, so the TMEM loads and barriers of one run beside the other's
 // arithmetic, and a row needs no exchange per tile.  32,768 tokens, 16 + 4 heads
-// of 128: cap 50 3.1 ms (1410 TFLOPS, plain 3.3 ms), cap and bias 3.8 (with a
+// of 128: cap 50 3.15 ms (1396 TFLOPS, plain 3.43 ms), cap and bias 3.8 (with a
 // running maximum and half a tile each 4.4 and 5.7); bias alone 4.0, masks
 // alone 3.2.
 #pragma once

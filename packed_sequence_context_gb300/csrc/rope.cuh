@@ -41,8 +41,8 @@ inline uint64_t rope_turn(double f) {
   const double p = product;
   double e = std::fma(a, hi, -p) + a * lo;
   e -= std::rint(e);  // whole turns drop out at whole positions
-  const double s = std::ldexp(p - std::floor(p), 64), whole = std::floor(s);  // both exact, s < 2^64
-  const double rest = (s - whole) + std::ldexp(e, 64);                        // |rest| <= 2^63 + 1
+  const double s = (p - std::floor(p)) * 0x1p64, whole = std::floor(s);  // both exact, s < 2^64
+  const double rest = (s - whole) + e * 0x1p64;                        // |rest| <= 2^63 + 1
   const uint64_t r = (uint64_t)std::rint(std::fabs(rest));
   const uint64_t turn = (uint64_t)whole + (rest < 0 ? 0 - r : r);
   return f < 0 ? 0 - turn : turn;

@@ -391,8 +391,10 @@ def _alloc_on(side):
     """Where the buffers of a call are made: a block of the current stream's
     memory would be free for the current stream's next tensor once the helper
     drops it, and may still be in use by what that stream ran before."""
+    if side is None:
+        return _HERE
     import torch
-    return _HERE if side is None else torch.cuda.stream(side)
+    return torch.cuda.stream(side)
 
 
 def _keep(side, stream, given, made):
