@@ -59,7 +59,7 @@
 // its dS, by the same thread (the tensor pipe runs one thread's MMAs in issue
 // order).
 //
-// 32,768 tokens, 16 + 4 heads of 128: plain 3.8 ms (1727 TFLOPS of the three
+// 32,768 tokens, 16 + 4 heads of 128: plain 3.8 ms (1741 TFLOPS of the three
 // products), masks 3.75, cap 50 4.9 (1336), every score saturated 5.8; with the two
 // walks of 2 of the 16 heads, bias 4.4, cap and bias 6.05.  The row sum of
 // P (dP - Delta) is 4% of that.  Two warpgroups against four (before the
@@ -699,7 +699,8 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         if (last) break;
         if (kMod != 0 && valid) sees = query_sees(p, p.mods, it.g, it.b, pos);
       }
-      if (!__all_sync(0xffffffffu, ok)) {
+      // (scored: the exchange above leaves each lane its own answer)
+      if (kMod != 0 ? !__all_sync(0xffffffffu, ok) : !ok) {
         ok = false;
         break;
       }
