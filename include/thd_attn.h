@@ -342,8 +342,9 @@ THD_API int thd_attn_score_fwd(const void* q, const void* k, const void* v, void
  * workspace thd_score_workspace_size(.., has_docs, 1).  Bit-reproducible for a
  * workspace of the same size (a smaller one adds dK and dV up in other parts).
  * Delta, off by O's rounding to bf16, is corrected by the row sum of
- * P (dP - Delta): for dK always, for dQ in rows that see at most 128 keys and in
- * heads with |dist_slopes[h]| >= 0.375.  Elsewhere dQ is as exact as plain
+ * P (dP - Delta): for dK always, for dQ with heads of 64 always, with heads of 128
+ * in rows that see at most 128 keys and in heads with |dist_slopes[h]| >= 0.375.
+ * Elsewhere dQ is as exact as plain
  * attention's: 2.4e-3 relative where the scores spread a row's weight, 3 to 4e-3
  * where they gather it on a few keys.  Launches: planner, preprocess, dQ and dK/dV; with documents
  * two more; with few key tiles to go round, one that joins dK/dV's parts.

@@ -16,6 +16,9 @@ dS = P (dP - Delta) w with w = 1 - tanh^2.  Where Delta = rowsum(dO O) is taken
 from O in bf16 instead of being corrected, Delta's mean square is
 sum_d dO^2 (mean square of O) and all of a row's dS share it:
   dQ_i gains c^2 that (sum_j P w K_j)^2.
+With heads of 64 dQ is made with Delta from O and corrected in every row, by
+how far Delta was off times sum_j P w K_j: both carry that into a rounding,
+  dQ_i gains c^2 2 R^2 that sum_j P^2 w^2 K^2.
 Errors of fp32: P is off relatively by that of the scores, taken as in
 score_oracle at a quarter (they are sums of many roundings, there at their
 worst), and dP - Delta by D 2^-24 sum |dO||V| / 4.
@@ -36,8 +39,8 @@ ROW, HEAD = 3.0, 1.25
 
 
 def delta_corrected(see, slope, doc_q, doc_k, tile=128, few=256, steep=0.375):
-    """[lq] bool: which rows' dQ is to have the corrected Delta.  All of them
-    with a steep slope; else those whose keys lie inside the few keys of their
+    """[lq] bool: which rows' dQ is to have the corrected Delta where the head's
+    size is not 64.  All of them with a steep slope; else those whose keys lie inside the few keys of their
     tile of rows: from the first row's first key, or the end of its document if
     that row sees many, to the last row's last key, or the start of its
     document."""
@@ -96,8 +99,13 @@ def model(q, k, v, cu_q, cu_k, pad_q, pad_k, *, causal, scale, softcap=0.0, slop
             out["o"][rq, h], out["ms_o"][rq, h] = O, ms_o
             out["dq"][rq, h] = scale * dS @ K
             ms = scale ** 2 * s2 @ K ** 2 + (R * out["dq"][rq, h]) ** 2
-            shared = (dO ** 2 * ms_o).sum(-1) * ~delta_corrected(see, slope, *docs)
-            out["ms_dq"][rq, h] = ms + scale ** 2 * shared[:, None] * ((P * w) @ K) ** 2
+            that = (dO ** 2 * ms_o).sum(-1)[:, None]
+            if D == 64:
+                ms = ms + scale ** 2 * 2 * R ** 2 * that * ((P * w) ** 2 @ K ** 2)
+            else:
+                that = that * ~delta_corrected(see, slope, *docs)[:, None]
+                ms = ms + scale ** 2 * that * ((P * w) @ K) ** 2
+            out["ms_dq"][rq, h] = ms
             out["dk"][rk, h // G] += scale * dS.T @ Q
             out["ms_dk"][rk, h // G] += scale ** 2 * s2.T @ Q ** 2
             out["dv"][rk, h // G] += P.T @ dO

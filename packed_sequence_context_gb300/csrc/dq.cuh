@@ -23,8 +23,12 @@
 // Scored attention, Delta: rowsum(dO O) comes from O in bf16, an error of up to
 // 2^-9 |dO| |O| that dS = P (dP - Delta) takes over whole; it shows in rows whose
 // weight lies on a few keys, most where dP - Delta itself is nearly 0.  The row
-// sum of P (dP - Delta), which is 0 for the exact Delta, corrects it: every item
-// adds it up and leaves the exact Delta for the dK/dV kernel.  For dQ itself an
+// sum off of P (dP - Delta), which is 0 for the exact Delta, corrects it: every
+// item adds it up and leaves the exact Delta for the dK/dV kernel.  For dQ itself:
+// heads of 64 leave room in TMEM for M = sum of P (1 - tanh^2) K, one product more
+// a tile, and dQ - off M is exact in every row (32,768 tokens of 16 + 4 heads:
+// masks 3.2 -> 4.15 ms, bias 4.0 -> 4.95, cap 4.55 -> 5.0, and without the walks
+// below cap and bias 5.9 -> 5.6).  Heads of 128 leave none; there an
 // item walks the keys of rows that see few of them a first time, for Delta alone:
 // those of short walks and of documents that begin or end inside its tile
 // (few_keys), or all of its keys where the head's slope is at least kSteepSlope
@@ -41,7 +45,7 @@
 //   scores of standard deviation 3 under a cap 3.1e-3, 58%; 6 4.2e-3, 3 times
 // (the worst rows' gradients are nearly 0: their weight lies on one key).
 // What the walk for steep slopes costs: 12 padded sequences of 154 to 1409, 5 of
-// 32 heads, dQ 268 -> 289 us; 16,384 tokens in documents, 1 of 8 heads, 190 -> 223.
+// 32 heads, dQ 268 -> 291 us.
 //
 // CTA layout (one CTA per SM, persistent over the schedule): the dS warps, then
 // four warps with a role each.
@@ -87,6 +91,9 @@ struct DqCfg {
   static constexpr int kSmem = 1024 + 2 * kQBytes + (kKStages + kVStages) * kKVBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDP = 256, kColDQ = 384;
+  // scored, where TMEM has room for it: M = sum of P (1 - tanh^2) K beside dQ
+  static constexpr bool kMass = kMod != 0 && D == 64;
+  static constexpr uint32_t kColM = kColDQ + D;
   // dS warpgroups: two, each with half of the columns of a tile; four with a
   // quarter each where a cap or a bias makes dS long enough for its latencies
   // to show (two warps per scheduler, in step, left it idle half of the time)
@@ -98,6 +105,7 @@ struct DqCfg {
   __host__ __device__ static constexpr uint32_t ds_col(int ks) {
     return kGroups == 2 ? 64 * (ks >> 2) + 8 * (ks & 3) : 32 * (ks >> 1) + 8 * (ks & 1);
   }
+  static constexpr uint32_t kMassOff = kGroups == 2 ? 32 : 16;  // packed P (1 - tanh^2) beside it
   // register split (setmaxnreg) for the instantiation shorter sequences take:
   // dQ +2-3% on batches of 0.1-8K-token sequences, -0.9% on one long sequence
   static constexpr uint32_t kLaunchRegs = kGroups == 2 ? 168 : 96;   // per thread, what 65,536 allow
@@ -111,10 +119,11 @@ struct DqCfg {
 // one that makes dQ, over all of them; else it is for Delta alone, see above).
 constexpr float kSteepSlope = 0.375f;
 __device__ inline int2 all_keys(const QItem& it) { return make_int2(it.k_lo, it.k_hi); }
-template <int kMod>
+template <int D, int kMod>
 __device__ inline int2 first_keys(const DqParams& p, const QItem& it, bool& last) {
   last = true;
   if constexpr (kMod == 0) return make_int2(0, 0);
+  if constexpr (DqCfg<D, kMod>::kMass) return all_keys(it);
   int2 k = make_int2(it.few_lo, it.few_hi);
   if constexpr ((kMod & kModDist) != 0)
     if (fabsf(p.mods.slopes[it.h]) >= kSteepSlope) k = all_keys(it);
@@ -248,7 +257,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         mbar_arrive(&bar_q_full);
         ++q_iter;
         bool last;
-        for (int2 keys = first_keys<kMod>(p, it, last);; keys = all_keys(it), last = true) {
+        for (int2 keys = first_keys<D, kMod>(p, it, last);; keys = all_keys(it), last = true) {
           for_each_kv_tile<kMod>(it, p, keys, [&](int c, int j) {
             if (!ok) return;
             if (!mbar_wait(&bar_k_empty[ks], kph ^ 1u, &s_abort)) {
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
           if (!item_take_one(&ring, kit, w, &s_abort) || w >= n_items) break;
           const QItem it = q_item<kGrouped, kMod>(p, n_entries, w);
           bool last;
-          for (int2 keys = first_keys<kMod>(p, it, last);; keys = all_keys(it), last = true) {
+          for (int2 keys = first_keys<D, kMod>(p, it, last);; keys = all_keys(it), last = true) {
             for_each_kv_tile<kMod>(it, p, keys, [&](int c, int j) {
               if (!ok) return;
               if (!mbar_wait(&bar_v_empty[vs], vph ^ 1u, &s_abort)) {
@@ -346,6 +355,10 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             for (int kk = 0; kk < ncols / 16; ++kk)
               mma_ts(tmem + C::kColDQ, tmem + b * 128u + C::ds_col(kk), kd + (uint64_t)(kk * (2048 >> 4)), idesc_dq,
                      (first && kk == 0) ? 0u : 1u);
+          if constexpr (C::kMass)
+            for (int kk = 0; kk < ncols / 16; ++kk)
+              mma_ts(tmem + C::kColM, tmem + b * 128u + C::ds_col(kk) + C::kMassOff, kd + (uint64_t)(kk * (2048 >> 4)),
+                     idesc_dq, (first && kk == 0) ? 0u : 1u);
           tc_commit(&bar_k_empty[kslot]);  // the K slot's last reader
           return true;
         };
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             continue;
           }
           bool last;
-          for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
+          for (int2 keys = first_keys<D, kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
             int j = 0, prev_cols = 0;
             for_each_kv_tile<kMod>(it, p, keys, [&](int c, int jt) {
               if (!ok) return;
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             continue;
           }
           bool last;
-          for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
+          for (int2 keys = first_keys<D, kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
             int j = 0;
             for_each_kv_tile<kMod>(it, p, keys, [&](int c, int jt) {
               if (!ok) return;
@@ -509,8 +522,9 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         sc = score_consts<kMod, false>(p, it.h);
       }
       int jl = 0;
+      float off = 0.f;  // how far Delta was off in the walk that made dQ
       bool last;
-      for (int2 keys = first_keys<kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
+      for (int2 keys = first_keys<D, kMod>(p, it, last); ok; keys = all_keys(it), last = true) {
         // a sum over part of the row's keys says nothing: such a row sees none here
         if (kMod != 0 && !last && (sees.x < keys.x || sees.y > keys.y)) sees = make_int2(0, 0);
         float eps = 0.f;  // this thread's part of the row sum of P (dP - Delta)
@@ -557,7 +571,10 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
             // sum of P (dP - Delta); on the keys this row may not see P = 2^-inf = 0
             // against dP = 0, and dS is set to 0, whatever stood there
             constexpr bool kCap = (kMod & kModCap) != 0;
-            uint32_t pk[kCh][16];
+            // one chunk a thread, and two results of it: the form is settled before
+            // they are made, and they go to TMEM as they are made
+            constexpr bool kNow = C::kMass && kCh == 1;
+            uint32_t pk[kCh][16], pm[C::kMass ? kCh : 1][16];
             // chunk ch of S, with the cap's masked columns at 0; true if any is masked
             auto load = [&](float(&y)[32], int ch) {
               uint32_t(&sr)[32] = reinterpret_cast<uint32_t(&)[32]>(y);
@@ -582,6 +599,10 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                   constexpr bool kWide = kCap && kForm == kCapWide;
                   if constexpr (kCap) {
                     am = fmaxf(am, score_abs_max(y));
+                    if constexpr (kNow) {
+                      const int f = cap_form(am, sc);
+                      if (f > kForm) return f;
+                    }
                     if constexpr (!kWide) cap_run<kForm, -1, false>(y, sc, 1.f, 0.f, 0.f);
                   }
                   // wide: tanh = -1 there instead of P = 0, and dP - Delta = 0
@@ -606,14 +627,17 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                         ffma2(x0, x1, y[n], y[n + 1], a, a, b0, b1);
                       }
                       fadd2(t0, t1, __uint_as_float(dr[kk][n]), __uint_as_float(dr[kk][n + 1]), -dlt, -dlt);
-                      fmul2(t0, t1, ex2(x0), ex2(x1), t0, t1);
+                      x0 = ex2(x0), x1 = ex2(x1);
+                      fmul2(t0, t1, x0, x1, t0, t1);
                       fadd2(es[0], es[1], es[0], es[1], t0, t1);
                       if constexpr (kCap) {
                         if constexpr (!kWide) ffma2(w0, w1, -y[n], -y[n + 1], y[n], y[n + 1], 1.f, 1.f);
                         fmul2(y[n], y[n + 1], t0, t1, w0, w1);
+                        if constexpr (C::kMass) fmul2(x0, x1, x0, x1, w0, w1);
                       } else {
                         y[n] = t0, y[n + 1] = t1;
                       }
+                      if constexpr (C::kMass) pm[kk][n / 2] = pack_bf16x2(x0, x1);
                     }
                   };
                   const float d0 = (float)(ahead - 1 - 32 * ch);
@@ -621,22 +645,32 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
                     write_ds(BiasRun<-1, true>(d0, sc.slope, top));
                   else
                     write_ds(BiasRun<-1, false, true>(d0, sc.slope, top));
-                  if (cut) score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+                  if (cut) {
+                    score_fill(y, from - 32 * ch, cnt - 32 * ch, 0.f);
+                    if constexpr (C::kMass) score_mask(pm[kk], from - 32 * ch, cnt - 32 * ch);
+                  }
 #pragma unroll
                   for (int n = 0; n < 16; ++n) pk[kk][n] = pack_bf16x2(y[2 * n], y[2 * n + 1]);
                   // over columns already read
-                  if (!kCap && last) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
+                  if constexpr (kNow)
+                    if (C::kMass) tmem_st16(scol + C::ds_col(2 * ch) + C::kMassOff, pm[kk]);
+                  if ((!kCap || kNow) && last) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
                 }
               }
-              return kCap ? cap_form(am, sc) : kCapNear;
+              return kCap && !kNow ? cap_form(am, sc) : decltype(form)::value;
             };
             if constexpr (kCap) {
               cap_in_form(cap, run);
 #pragma unroll
               for (int kk = 0; kk < kCh; ++kk)
-                if (last && kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
+                if (!kNow && last && kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)), pk[kk]);
             } else {
               run(CapForm<kCapNear>{});
+            }
+            if constexpr (C::kMass && !kNow) {  // over columns that every chunk of this thread has been read from
+#pragma unroll
+              for (int kk = 0; kk < kCh; ++kk)
+                if (kCh * part + kk < nch) tmem_st16(scol + C::ds_col(2 * (kCh * part + kk)) + C::kMassOff, pm[kk]);
             }
             eps += es[0] + es[1];
           } else {
@@ -693,7 +727,8 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
               s_eps[0][row] = eps;
             }
             sync();
-            dlt += s_eps[0][row];
+            off = s_eps[0][row];
+            dlt += off;
           }
         }
         if (last) break;
@@ -720,6 +755,14 @@ __global__ void __launch_bounds__((DqCfg<D, kMod>::kThreads), 1)
         if (jl > 0) {
           tmem_ld32(tmem + lane_base + C::kColDQ + 32 * k, o);
           tmem_ld_wait(o);
+          if constexpr (C::kMass) {  // dS = P (dP - Delta) w was made with Delta - off
+            uint32_t m[32];
+            tmem_ld32(tmem + lane_base + C::kColM + 32 * k, m);
+            tmem_ld_wait(m);
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+              o[n] = __float_as_uint(fmaf(-off, __uint_as_float(m[n]), __uint_as_float(o[n])));
+          }
         } else {
 #pragma unroll
           for (int n = 0; n < 32; ++n) o[n] = 0u;

@@ -92,6 +92,15 @@ THD_DEV void score_fill(float (&s)[N], int from, int to, float v) {
     if ((uint32_t)(n - lo) >= n_seen) s[n] = v;
 }
 
+// The same for 32 bf16 numbers in pairs, which become 0.
+THD_DEV void score_mask(uint32_t (&s)[16], int from, int to) {
+  const int lo = from < 0 ? 0 : from, hi = to > 32 ? 32 : to;
+  const uint32_t n_seen = hi > lo ? (uint32_t)(hi - lo) : 0u;
+#pragma unroll
+  for (int n = 0; n < 32; n += 2)
+    s[n / 2] &= ((uint32_t)(n - lo) < n_seen ? 0xffffu : 0u) | ((uint32_t)(n + 1 - lo) < n_seen ? 0xffff0000u : 0u);
+}
+
 // Which form of tanh the warp's run takes: the first whose range holds the
 // largest |s| of every thread (a NaN among the scores may pass for small: it
 // stays a NaN in every form), and none below that of the warp's earlier runs in
