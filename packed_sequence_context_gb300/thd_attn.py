@@ -528,8 +528,7 @@ def _score_checks(w, q, k, v, more, offsets, dist_slopes, doc_q, doc_kv, prefix_
     device of its tensors.  `more`: (tensor, shape, dtype) triples."""
     import torch
     dev = _current(w, q)
-    _need(w, q.dim() == 3 and k.dim() == 3 and
-          (workspace is None or workspace.get_device() == dev and workspace.is_contiguous()))
+    _need(w, workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
     qs, ks = q.shape, k.shape
     B = offsets[0].numel() - 1
     bf16, i32 = torch.bfloat16, torch.int32
@@ -561,6 +560,7 @@ def attn_score_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=Non
     (prefix_len int32 [B]).  Returns (o, lse, dev_status)."""
     import torch
     w = "thd_attn_score_fwd"
+    _need(w, q.dim() == 3 and k.dim() == 3)
     more = [] if out is None and lse is None and dev_status is None else \
         [(out, q.shape, torch.bfloat16), (lse, (q.shape[1], q.shape[0]), torch.float32), (dev_status, (1,), torch.int32)]
     B, T_q, T_kv, Hq, Hkv, D = _score_checks(
@@ -592,6 +592,7 @@ def attn_score_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     rows as in attn_bwd.  Returns (dq, dk, dv, dev_status)."""
     import torch
     w = "thd_attn_score_bwd"
+    _need(w, q.dim() == 3 and k.dim() == 3)
     bf16 = torch.bfloat16
     dq_rows = q.shape[0] if dq_rows is None else dq_rows
     dkv_rows = k.shape[0] if dkv_rows is None else dkv_rows

@@ -60,3 +60,22 @@ def test_dropout_of_a_number(lib):
     with pytest.raises(T.ThdError) as e:
         T.dropout_add(torch.tensor(1.0), torch.zeros(2, dtype=torch.int64), 0.5)
     assert e.value.code == T.THD_ERR_INVALID_ARG and not lib.calls
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "o", "dout", "lse"])
+@pytest.mark.parametrize("shape", [(), (8,), (8, 64), (1, 8, 2, 64)])
+@pytest.mark.parametrize("bwd", [False, True])
+def test_scored_attention_of_other_dimensions(lib, bwd, name, shape):
+    t = {"q": (8, 2, 64), "k": (8, 1, 64), "v": (8, 1, 64), "o": (8, 2, 64), "dout": (8, 2, 64), "lse": (2, 8)}
+    if name == "lse" and len(shape) == 2:
+        shape = (8, 2)
+    t[name] = shape
+    t = {n: torch.zeros(s, dtype=torch.float32 if n == "lse" else torch.bfloat16) for n, s in t.items()}
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    with pytest.raises(T.ThdError) as e:
+        if bwd:
+            T.attn_score_bwd(*(t[n] for n in ("q", "k", "v", "o", "lse", "dout")), cu, cu, softcap=5.0)
+        else:
+            T.attn_score_fwd(t["q"], t["k"], t["v"], cu, cu, softcap=5.0, out=t["o"], lse=t["lse"],
+                             dev_status=None if name != "dout" else torch.zeros(2, dtype=torch.int32))
+    assert e.value.code == T.THD_ERR_INVALID_ARG and not lib.calls
