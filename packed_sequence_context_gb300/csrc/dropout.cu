@@ -15,7 +15,8 @@
 // GB300, inputs larger than L2, of the rate of a plain copy: 41,888 x 4,096 bf16
 // with a residual 153 us (99%), without one (2/3 of the bytes to as much of the
 // generator) 119 us (85%), fp32 with one 292 us (104%); rows of 1,111 columns,
-// off every alignment, fp32 91% and bf16 with a residual 67%.
+// off every alignment, fp32 91% and bf16 with a residual 67% (its elements move one
+// to a lane, 64 bytes a warp's access).
 #include "common.cuh"
 #include "dropout.cuh"
 #include "vec8.cuh"
