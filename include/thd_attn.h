@@ -81,6 +81,8 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_DEV_ERR_CAUSAL_LENGTHS 106 /* top-left causal with q and kv lengths differing */
 #define THD_DEV_ERR_CAPACITY 107       /* internal schedule capacity exceeded */
 #define THD_DEV_ERR_DOC_ORDER 108      /* document numbers decrease inside a sequence */
+#define THD_DEV_ERR_PAGE 109           /* the block table names a page outside the cache */
+#define THD_DEV_ERR_KV_LEN 110         /* a cached length below 0 or the new rows, or past the block table */
 
 /* Kernel identifiers for the profiling hook. */
 #define THD_KERNEL_PLAN 1
@@ -96,15 +98,20 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_KERNEL_DROPOUT 11
 #define THD_KERNEL_DOCS 12
 #define THD_KERNEL_BWD_JOIN 13
+#define THD_KERNEL_DECODE 14
+#define THD_KERNEL_DECODE_JOIN 15
+#define THD_KERNEL_CACHE_APPEND 16
+#define THD_KERNEL_CACHE_EVICT 17
 
 /* mask modes (the `causal` argument of the attention entry points) */
 #define THD_CAUSAL_NONE 0
 #define THD_CAUSAL_TOP_LEFT 1
 #define THD_CAUSAL_BOTTOM_RIGHT 2
 
-/* element types of the row-wise operators */
+/* element types of the row-wise operators and of a key-value cache */
 #define THD_DTYPE_BF16 0
 #define THD_DTYPE_FP32 1
+#define THD_DTYPE_E4M3 2 /* a cache's keys and values, with an exponent for each row */
 
 /* thd_cp_a2a directions */
 #define THD_A2A_TO_GROUPS 0 /* shards -> per-member head groups (the all-to-all in front of attention) */
@@ -546,6 +553,128 @@ THD_API int thd_rope(const void* q_in, const void* k_in, void* q_out, void* k_ou
  */
 THD_API int thd_dropout_add(const void* x, const void* residual, void* out, int64_t T, int64_t C,
                             const int32_t* row_ids, double p, const uint64_t* rng, int dtype, thd_stream_t stream);
+
+/*
+ * ---- a paged key-value cache: what fills it, reads it and keeps it small ----
+ *
+ * A cache holds the keys and values of sequences in pages of page_size slots.
+ * Sequence b's slot j is slot j % page_size of page block_table[b][j /
+ * page_size]; its kv_len[b] first slots are held.  Entries of the table behind
+ * those are not read.  The slots' order means nothing to attention: what a
+ * slot's token was numbered is kept, where it matters, in `pos`.
+ *   k, v: [num_pages][page_size][Hkv][D] in any order of the first three
+ *     dimensions (kv_stride: elements from page to page, slot to slot and head
+ *     to head, the same for both; rows contiguous).  16-byte aligned, strides a
+ *     multiple of 16 bytes.  D 64 or 128.
+ *   dtype THD_DTYPE_BF16, or THD_DTYPE_E4M3 with k_exp, v_exp: a uint8 for each
+ *     slot and head (exp_stride, as kv_stride): the row stands for its e4m3
+ *     numbers times 2^(exp - 127); 255: not a number.
+ *   `weight` (fp32) and `pos` (int32) of the calls below are such arrays, a
+ *     number for each slot and head, with weight_stride and pos_stride.
+ *   num_pages < 2^31; max_pages * page_size <= 2^30; Hq / Hkv <= 512.
+ *   A page may stand in several sequences' rows of the table while it is only
+ *     read; what a call writes (append, evict, weights) lies in pages of one
+ *     sequence, once.
+ * The struct is read before a call returns; its pointers are device pointers.
+ *
+ * Device status of these calls: STICKY.  *dev_status is only ever raised, to
+ * the largest code met; its owner zeroes it (once, before the first call, and
+ * reads it when it likes: a captured graph of many steps keeps one word).  A
+ * call that raises it neither reads nor writes outside the cache; what it writes
+ * for the sequences concerned is unspecified.
+ */
+typedef struct thd_kv_cache {
+  void* k;
+  void* v;
+  uint8_t* k_exp; /* NULL for THD_DTYPE_BF16 */
+  uint8_t* v_exp;
+  const int32_t* block_table; /* [B] rows of max_pages entries, table_stride entries apart */
+  const int32_t* kv_len;      /* [B] */
+  int64_t num_pages;
+  int64_t table_stride;
+  int64_t kv_stride[3]; /* page, slot, head: elements */
+  int64_t exp_stride[3];
+  int64_t weight_stride[3];
+  int64_t pos_stride[3];
+  int32_t page_size, max_pages, B, Hkv, D, dtype;
+} thd_kv_cache;
+
+/*
+ * thd_cache_append -- the new rows of packed sequences into their caches, one
+ * launch.  Sequence b's rows are [cu_seqlens[b], cu_seqlens[b+1]) of k and v,
+ * m_b of them, and go to its slots [kv_len[b] - m_b, kv_len[b]): kv_len counts
+ * them already, as for the attention that follows.  cu_seqlens NULL: one row a
+ * sequence, T == B.  Rows behind cu_seqlens[B] are left out.
+ *   k, v: bf16 rows of [Hkv, D], k_stride and v_stride elements apart (a
+ *     slice of a fused projection's output), 16-byte aligned, strides too.
+ *   e4m3: per row and head, with x the largest magnitude, the exponent is the
+ *     smallest e with x <= 448 * 2^(e - 127), at least 67 (127 for a row of
+ *     zeros); stored is the row times 2^(127 - e), rounded to nearest even.  A
+ *     row with an infinity or NaN is stored as 255.
+ *   weight, pos: NULL, or set for the new slots: 0, and the token's number
+ *     tokens_seen[b] - m_b + i (tokens_seen NULL: kv_len).
+ */
+THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, int64_t k_stride,
+                             int64_t v_stride, int64_t T, const int32_t* cu_seqlens, float* weight, int32_t* pos,
+                             const int32_t* tokens_seen, int32_t* dev_status, thd_stream_t stream);
+
+/*
+ * thd_attn_decode -- attention of one new token of each sequence over its
+ * cache (which holds the token's own key and value: append first).  For
+ * query head h of sequence b, over its visible slots j, kv_start[b] <= j <
+ * kv_len[b] (kv_start NULL: 0, else clamped to [0, kv_len[b]]: the first slot
+ * of the token's document):
+ *     x_j = softmax_scale q . k_j,  y_j = softcap tanh(x_j / softcap) (softcap 0: x_j)
+ *           - dist_slopes[h] (tokens_seen[b] - 1 - pos_j)
+ *     lse = log sum_j exp(y_j),  p_j = exp(y_j - lse),  o = sum_j p_j v_j
+ * as thd_attn_score_fwd gives a sequence's last row.  No visible slot: o = 0,
+ * lse = -inf.  Rows of several ranks' caches merge by thd_lse_merge.
+ *   q: bf16 rows of [Hq, D], q_stride (even) elements apart, 4-byte aligned.
+ *   o: bf16 [B, Hq, D], 16-byte aligned; lse: fp32 [Hq, B].
+ *   dist_slopes fp32 [Hq] or NULL.  pos NULL: a slot's token has the slot's
+ *     number; tokens_seen NULL: kv_len.  Both are read with dist_slopes only.
+ *   weight_out NULL, or: weight_out = weight_in + the sum of p_j over the kv
+ *     head's query heads, for the visible slots (weight_out may be weight_in,
+ *     else they do not overlap).
+ *   Lengths are read on the device: a captured graph serves growing ones.
+ * Bit-reproducible on one kind of GPU.  Launches: 2 (1 for tables of at most 64
+ * slots and no weights).  Workspace: thd_decode_workspace_size.
+ */
+THD_API int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, void* o, float* lse, int Hq,
+                            float softmax_scale, float softcap, const float* dist_slopes, const int32_t* kv_start,
+                            const int32_t* pos, const int32_t* tokens_seen, const float* weight_in,
+                            float* weight_out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            thd_stream_t stream);
+
+/*
+ * Bytes of workspace thd_attn_decode needs; capacity: max_pages * page_size
+ * (it counts with weights alone: 4 bytes a slot and query head).  Returns 0
+ * for invalid sizes.
+ */
+THD_API size_t thd_decode_workspace_size(int B, int Hq, int Hkv, int D, int64_t capacity, int has_weights);
+
+/*
+ * thd_cache_evict -- shrinks caches to `budget` slots, kv head by kv head, one
+ * launch.  Of a sequence's n = kv_len[b] > budget slots the budget with the
+ * largest weight stay, ties going to the lower slot; slots whose token is
+ * among the first `sinks` (pos < sinks) or the last `recent` (pos >=
+ * tokens_seen[b] - recent) count as +infinity, NaN as less than all.  Kept
+ * slots in front of the budget stay where they are; the i-th kept slot behind
+ * it moves into the i-th evicted slot in front of it: keys, values, exponents,
+ * weight and pos.  Slots behind the budget are left as they were.
+ *   new_len: int32 [B] = min(n, budget); not kv_len itself.
+ *   weight_out, pos_out: may be weight_in, pos_in (then only moved numbers are
+ *     written), else they get those of all slots below new_len.
+ *   0 < budget; sinks, recent >= 0.
+ * Workspace: thd_evict_workspace_size.
+ */
+THD_API int thd_cache_evict(const thd_kv_cache* cache, const float* weight_in, float* weight_out,
+                            const int32_t* pos_in, int32_t* pos_out, const int32_t* tokens_seen, int budget, int sinks,
+                            int recent, int32_t* new_len, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, thd_stream_t stream);
+
+/* Bytes of workspace thd_cache_evict needs; 0 for invalid sizes. */
+THD_API size_t thd_evict_workspace_size(int B, int Hkv, int64_t capacity, int budget);
 
 /*
  * Profiling hook (not needed for normal use): while enabled for `kernel_id`

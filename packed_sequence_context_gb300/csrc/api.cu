@@ -10,6 +10,7 @@
 #include <cudaTypedefs.h>
 
 #include "a2a.cuh"
+#include "cache.cuh"
 #include "common.cuh"
 #include "dropout.cuh"
 #include "rope.cuh"
@@ -598,6 +599,8 @@ const char* thd_status_string(int s) {
     case THD_DEV_ERR_EXCEEDS_BUF: return "sequences exceed the buffer rows";
     case THD_DEV_ERR_CAUSAL_LENGTHS: return "top-left causal attention needs equal q/kv lengths per sequence";
     case THD_DEV_ERR_DOC_ORDER: return "document numbers decrease inside a sequence";
+    case THD_DEV_ERR_PAGE: return "block table names a page outside the cache";
+    case THD_DEV_ERR_KV_LEN: return "cached length outside the block table, or below the new rows";
     case THD_DEV_ERR_CAPACITY: return "internal schedule capacity exceeded";
     default: return "unknown status";
   }
@@ -934,6 +937,196 @@ int thd_dropout_add(const void* x, const void* residual, void* out, int64_t T, i
   d.drop = (uint32_t)drop;
   d.scale = (float)(65536.0 / (65536.0 - drop));
   return cuda_status(launch_dropout(d, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The cache a call was given, as the kernels see it; what can be wrong with it
+// without reading device memory.
+static SlotStrides slot_strides(const int64_t (&s)[3], int64_t bytes) {
+  return SlotStrides{s[0] * bytes, s[1] * bytes, s[2] * bytes};
+}
+
+static int check_cache(const thd_kv_cache* c, CacheView* v) {
+  if (!c) return THD_ERR_INVALID_ARG;
+  if (c->B < 1 || c->B >= (1 << 24) || c->Hkv < 1 || c->Hkv > (1 << 20) || c->page_size < 1 || c->max_pages < 1 ||
+      c->num_pages < 1 || c->num_pages >= ((int64_t)1 << 31) || (c->B > 1 && c->table_stride < c->max_pages))
+    return THD_ERR_INVALID_ARG;
+  if (c->D != 64 && c->D != 128) return THD_ERR_UNSUPPORTED;
+  if (c->dtype != THD_DTYPE_BF16 && c->dtype != THD_DTYPE_E4M3) return THD_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30)) return THD_ERR_UNSUPPORTED;
+  const bool e4m3 = c->dtype == THD_DTYPE_E4M3;
+  if (!c->k || !c->v || !c->block_table || !c->kv_len || e4m3 != (c->k_exp != nullptr) || e4m3 != (c->v_exp != nullptr))
+    return THD_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->block_table, 4) || !aligned(c->kv_len, 4))
+    return THD_ERR_INVALID_ARG;
+  const int64_t esize = e4m3 ? 1 : 2;
+  for (int i = 0; i < 3; ++i)
+    if (c->kv_stride[i] < 0 || c->kv_stride[i] * esize % 16 != 0 || c->exp_stride[i] < 0 || c->weight_stride[i] < 0 ||
+        c->pos_stride[i] < 0)
+      return THD_ERR_INVALID_ARG;
+  v->k = static_cast<uint8_t*>(c->k);
+  v->v = static_cast<uint8_t*>(c->v);
+  v->k_exp = c->k_exp;
+  v->v_exp = c->v_exp;
+  v->row = slot_strides(c->kv_stride, esize);
+  v->exp = slot_strides(c->exp_stride, 1);
+  v->table = c->block_table;
+  v->table_stride = c->table_stride;
+  v->kv_len = c->kv_len;
+  v->num_pages = c->num_pages;
+  v->capacity = (int64_t)c->max_pages * c->page_size;
+  v->page_size = c->page_size;
+  v->B = c->B;
+  v->Hkv = c->Hkv;
+  v->D = c->D;
+  return THD_OK;
+}
+
+int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                     int64_t T, const int32_t* cu_seqlens, float* weight, int32_t* pos, const int32_t* tokens_seen,
+                     int32_t* dev_status, thd_stream_t stream) {
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int rc = check_cache(cache, &p.c);
+  if (rc != THD_OK) return rc;
+  if (T < 0 || T >= ((int64_t)1 << 31) || (!cu_seqlens && T != cache->B)) return THD_ERR_INVALID_ARG;
+  if (T == 0) return THD_OK;
+  const int64_t row = (int64_t)cache->Hkv * cache->D;
+  if (!k || !v || !dev_status || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || !aligned(weight, 4) ||
+      !aligned(pos, 4) || !aligned(tokens_seen, 4) || !aligned(dev_status, 4))
+    return THD_ERR_INVALID_ARG;
+  if (T > 1 && (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)) return THD_ERR_INVALID_ARG;
+  p.in[0] = static_cast<const uint16_t*>(k);
+  p.in[1] = static_cast<const uint16_t*>(v);
+  p.in_stride[0] = k_stride;
+  p.in_stride[1] = v_stride;
+  p.T = T;
+  p.cu = cu_seqlens;
+  p.weight = weight;
+  p.weight_at = slot_strides(cache->weight_stride, 1);
+  p.pos = pos;
+  p.pos_at = slot_strides(cache->pos_stride, 1);
+  p.seen = tokens_seen;
+  p.status = dev_status;
+  return cuda_status(launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Workspace of a decode: [units][part][part_ml][lse2][scores].
+struct DecodeWs {
+  size_t units, part, part_ml, lse2, scores, total;
+};
+static DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int64_t capacity, bool weights) {
+  const size_t heads = (size_t)decode_heads(Hq / Hkv);
+  DecodeWs w;
+  w.units = 0;
+  w.part = align_up(sizeof(int64_t) * ((size_t)B + 1), 256);
+  w.part_ml = align_up(w.part + sizeof(float) * 2 * kDecodeMaxGrid * heads * D, 256);
+  w.lse2 = align_up(w.part_ml + sizeof(float) * 2 * kDecodeMaxGrid * heads * 3, 256);
+  w.scores = align_up(w.lse2 + (weights ? sizeof(float) * (size_t)B * Hq : 0), 256);
+  w.total = align_up(w.scores + (weights ? sizeof(float) * (size_t)B * Hq * (size_t)capacity : 0), 256);
+  return w;
+}
+
+size_t thd_decode_workspace_size(int B, int Hq, int Hkv, int D, int64_t capacity, int has_weights) {
+  if (B < 1 || B >= (1 << 24) || Hq < 1 || Hkv < 1 || Hkv > (1 << 20) || Hq % Hkv != 0 || Hq / Hkv > kDecodeMaxGroup ||
+      (D != 64 && D != 128) || capacity < 1 || capacity > ((int64_t)1 << 30))
+    return 0;
+  return decode_ws(B, Hq, Hkv, D, capacity, has_weights != 0).total;
+}
+
+int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, void* o, float* lse, int Hq,
+                    float softmax_scale, float softcap, const float* dist_slopes, const int32_t* kv_start,
+                    const int32_t* pos, const int32_t* tokens_seen, const float* weight_in, float* weight_out,
+                    void* workspace, size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream) {
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  int rc = check_cache(cache, &p.c);
+  if (rc != THD_OK) return rc;
+  const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
+  if (Hq < 1 || Hq % Hkv != 0) return THD_ERR_INVALID_ARG;
+  if (Hq / Hkv > kDecodeMaxGroup) return THD_ERR_UNSUPPORTED;
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
+    return THD_ERR_INVALID_ARG;
+  // the kernel's factors: a scale or cap that is none as a float is refused
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f) || !std::isfinite(softcap * 1.4426950408889634f) ||
+      (softcap > 0.f && !(std::isfinite(softmax_scale / softcap) && softmax_scale / softcap > 0.f)))
+    return THD_ERR_INVALID_ARG;
+  if (!q || !o || !lse || !dev_status || !aligned(q, 4) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(dist_slopes, 4) || !aligned(kv_start, 4) || !aligned(pos, 4) || !aligned(tokens_seen, 4) ||
+      !aligned(weight_in, 4) || !aligned(weight_out, 4) || !aligned(dev_status, 4) ||
+      (weight_in == nullptr) != (weight_out == nullptr))
+    return THD_ERR_INVALID_ARG;
+  if (B > 1 && (q_stride < (int64_t)Hq * D || q_stride % 2 != 0)) return THD_ERR_INVALID_ARG;
+  const DecodeWs w = decode_ws(B, Hq, Hkv, D, p.c.capacity, weight_out != nullptr);
+  rc = check_ws(workspace, workspace_bytes, w.total);
+  if (rc != THD_OK) return rc;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.G = Hq / Hkv;
+  p.blocks = (p.G + decode_heads(p.G) - 1) / decode_heads(p.G);
+  p.scale = softmax_scale;
+  p.cap = softcap;
+  p.slopes = dist_slopes;
+  p.start = kv_start;
+  p.pos = dist_slopes ? pos : nullptr;
+  p.pos_at = slot_strides(cache->pos_stride, 1);
+  p.seen = tokens_seen;
+  p.weight_in = weight_in;
+  p.weight_out = weight_out;
+  p.weight_at = slot_strides(cache->weight_stride, 1);
+  p.status = dev_status;
+  char* const ws = static_cast<char*>(workspace);
+  p.units = reinterpret_cast<int64_t*>(ws + w.units);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  p.scores = reinterpret_cast<float*>(ws + w.scores);
+  return cuda_status(launch_decode(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Moves of an item: no more than the slots in front of the budget, or behind it.
+static int64_t evict_room(int64_t capacity, int budget) {
+  const int64_t behind = capacity - budget;
+  return behind < 0 ? 0 : behind < budget ? behind : budget;
+}
+
+size_t thd_evict_workspace_size(int B, int Hkv, int64_t capacity, int budget) {
+  if (B < 1 || B >= (1 << 24) || Hkv < 1 || Hkv > (1 << 20) || capacity < 1 || capacity > ((int64_t)1 << 30) || budget < 1)
+    return 0;
+  return align_up(sizeof(int32_t) * 2 * (size_t)B * Hkv * (size_t)evict_room(capacity, budget), 256) + 256;
+}
+
+int thd_cache_evict(const thd_kv_cache* cache, const float* weight_in, float* weight_out, const int32_t* pos_in,
+                    int32_t* pos_out, const int32_t* tokens_seen, int budget, int sinks, int recent, int32_t* new_len,
+                    void* workspace, size_t workspace_bytes, int32_t* dev_status, thd_stream_t stream) {
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  int rc = check_cache(cache, &p.c);
+  if (rc != THD_OK) return rc;
+  if (budget < 1 || sinks < 0 || recent < 0) return THD_ERR_INVALID_ARG;
+  if (!weight_in || !weight_out || !pos_in || !pos_out || !tokens_seen || !new_len || !dev_status ||
+      !aligned(weight_in, 4) || !aligned(weight_out, 4) || !aligned(pos_in, 4) || !aligned(pos_out, 4) ||
+      !aligned(tokens_seen, 4) || !aligned(new_len, 4) || !aligned(dev_status, 4) || new_len == cache->kv_len)
+    return THD_ERR_INVALID_ARG;
+  rc = check_ws(workspace, workspace_bytes, thd_evict_workspace_size(cache->B, cache->Hkv, p.c.capacity, budget));
+  if (rc != THD_OK) return rc;
+  p.weight_in = weight_in;
+  p.weight_out = weight_out;
+  p.weight_at = slot_strides(cache->weight_stride, 1);
+  p.pos_in = pos_in;
+  p.pos_out = pos_out;
+  p.pos_at = slot_strides(cache->pos_stride, 1);
+  p.seen = tokens_seen;
+  p.new_len = new_len;
+  p.status = dev_status;
+  p.moves = static_cast<int32_t*>(workspace);
+  p.room = evict_room(p.c.capacity, budget);
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  return cuda_status(launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int thd_profile_enable(int kernel_id, int max_records) {

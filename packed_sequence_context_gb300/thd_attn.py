@@ -40,6 +40,8 @@ THD_DEV_ERR_EXCEEDS_BUF = 105
 THD_DEV_ERR_CAUSAL_LENGTHS = 106
 THD_DEV_ERR_CAPACITY = 107
 THD_DEV_ERR_DOC_ORDER = 108
+THD_DEV_ERR_PAGE = 109
+THD_DEV_ERR_KV_LEN = 110
 
 THD_KERNEL_PLAN = 1
 THD_KERNEL_FWD = 2
@@ -54,6 +56,10 @@ THD_KERNEL_ROPE = 10
 THD_KERNEL_DROPOUT = 11
 THD_KERNEL_DOCS = 12
 THD_KERNEL_BWD_JOIN = 13
+THD_KERNEL_DECODE = 14
+THD_KERNEL_DECODE_JOIN = 15
+THD_KERNEL_CACHE_APPEND = 16
+THD_KERNEL_CACHE_EVICT = 17
 
 THD_FWD_KERNEL_SINGLE = 1
 THD_FWD_KERNEL_DUAL = 2
@@ -64,6 +70,7 @@ THD_CAUSAL_BOTTOM_RIGHT = 2
 
 THD_DTYPE_BF16 = 0
 THD_DTYPE_FP32 = 1
+THD_DTYPE_E4M3 = 2
 
 THD_A2A_TO_GROUPS = 0
 THD_A2A_TO_SHARDS = 1
@@ -74,6 +81,18 @@ _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 _f64 = ctypes.c_double
 _sz = ctypes.c_size_t
+
+
+class KvCache(ctypes.Structure):
+    """thd_kv_cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_exp", _vp), ("v_exp", _vp), ("block_table", _vp), ("kv_len", _vp),
+                ("num_pages", _i64), ("table_stride", _i64), ("kv_stride", _i64 * 3), ("exp_stride", _i64 * 3),
+                ("weight_stride", _i64 * 3), ("pos_stride", _i64 * 3), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+_kvp = ctypes.POINTER(KvCache)
 
 # name -> (restype, argtypes); mirrors include/thd_attn.h
 SIGNATURES = {
@@ -109,6 +128,12 @@ SIGNATURES = {
     "thd_rope": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
                         _vp, _i32, _i32, _i32, _vp]),
     "thd_dropout_add": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _f64, _vp, _i32, _vp]),
+    "thd_cache_append": (_i32, [_kvp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "thd_attn_decode": (_i32, [_kvp, _vp, _i64, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
+                               _vp]),
+    "thd_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i64, _i32]),
+    "thd_cache_evict": (_i32, [_kvp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp, _vp]),
+    "thd_evict_workspace_size": (_sz, [_i32, _i32, _i64, _i32]),
     "thd_profile_enable": (_i32, [_i32, _i32]),
     "thd_profile_read": (_i32, [_vp, _i32, _vp]),
     "thd_launch_count": (ctypes.c_uint64, []),
@@ -303,6 +328,33 @@ def thd_rope(q_in, k_in, q_out, k_out, q_in_stride, k_in_stride, q_out_stride, k
 
 def thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dtype, stream=None) -> int:
     return lib().thd_dropout_add(_p(x), _p(residual), _p(out), T, C, _p(row_ids), p, _p(rng), dtype, _s(stream))
+
+
+def thd_cache_append(cache, k, v, k_stride, v_stride, T, cu_seqlens, weight, pos, tokens_seen, dev_status,
+                     stream=None) -> int:
+    return lib().thd_cache_append(cache, _p(k), _p(v), k_stride, v_stride, T, _p(cu_seqlens), _p(weight), _p(pos),
+                                  _p(tokens_seen), _p(dev_status), _s(stream))
+
+
+def thd_attn_decode(cache, q, q_stride, o, lse, Hq, softmax_scale, softcap, dist_slopes, kv_start, pos, tokens_seen,
+                    weight_in, weight_out, workspace, workspace_bytes, dev_status, stream=None) -> int:
+    return lib().thd_attn_decode(cache, _p(q), q_stride, _p(o), _p(lse), Hq, softmax_scale, softcap, _p(dist_slopes),
+                                 _p(kv_start), _p(pos), _p(tokens_seen), _p(weight_in), _p(weight_out), _p(workspace),
+                                 workspace_bytes, _p(dev_status), _s(stream))
+
+
+def thd_decode_workspace_size(B, Hq, Hkv, D, capacity, has_weights) -> int:
+    return lib().thd_decode_workspace_size(B, Hq, Hkv, D, capacity, has_weights)
+
+
+def thd_cache_evict(cache, weight_in, weight_out, pos_in, pos_out, tokens_seen, budget, sinks, recent, new_len, workspace,
+                    workspace_bytes, dev_status, stream=None) -> int:
+    return lib().thd_cache_evict(cache, _p(weight_in), _p(weight_out), _p(pos_in), _p(pos_out), _p(tokens_seen), budget,
+                                 sinks, recent, _p(new_len), _p(workspace), workspace_bytes, _p(dev_status), _s(stream))
+
+
+def thd_evict_workspace_size(B, Hkv, capacity, budget) -> int:
+    return lib().thd_evict_workspace_size(B, Hkv, capacity, budget)
 
 
 def thd_profile_enable(kernel_id: int, max_records: int) -> int:
@@ -836,3 +888,155 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
     _check(w, thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dt, stream))
     _keep(side, stream, given, (out,))
     return out
+
+
+def _slot_array(where, t, dtype, pages, slots, heads, dev):
+    """Strides of an array [pages, slots, heads] in any order of its dimensions."""
+    _need(where, t.dtype is dtype and t.shape == (pages, slots, heads) and t.get_device() == dev)
+    return t.stride()
+
+
+def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, pos):
+    """The cache of a call as thd_kv_cache; weight, pos: lists of arrays with
+    the same strides (or of None)."""
+    import torch
+    dev = _current(where, k_cache)
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    _need(where, len(shape) == 4 and v_cache.shape == shape and v_cache.stride() == strides and
+          v_cache.dtype is dtype and v_cache.get_device() == dev and strides[3] == 1)
+    pages, slots, heads, D = shape
+    e4m3 = dtype is torch.float8_e4m3fn
+    if not e4m3 and dtype is not torch.bfloat16:
+        raise ThdError(where, THD_ERR_UNSUPPORTED)
+    _need(where, block_table.dim() == 2 and block_table.dtype is torch.int32 and block_table.get_device() == dev)
+    B, max_pages = block_table.shape
+    ts0, ts1 = block_table.stride()
+    _need(where, (ts1 == 1 or max_pages <= 1) and (B <= 1 or ts0 >= max_pages))
+    _need(where, kv_len.dtype is torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous() and
+          kv_len.get_device() == dev)
+    c = KvCache(k=k_cache.data_ptr(), v=v_cache.data_ptr(), block_table=block_table.data_ptr(), kv_len=kv_len.data_ptr(),
+                num_pages=pages, table_stride=ts0, page_size=slots, max_pages=max_pages, B=B, Hkv=heads, D=D,
+                dtype=THD_DTYPE_E4M3 if e4m3 else THD_DTYPE_BF16)
+    c.kv_stride[:] = strides[:3]
+    _need(where, (k_exp is not None) == e4m3 and (v_exp is not None) == e4m3)
+    if e4m3:
+        c.exp_stride[:] = _slot_array(where, k_exp, torch.uint8, pages, slots, heads, dev)
+        _need(where, _slot_array(where, v_exp, torch.uint8, pages, slots, heads, dev) == k_exp.stride())
+        c.k_exp, c.v_exp = k_exp.data_ptr(), v_exp.data_ptr()
+    for arrays, dt, to in ((weight, torch.float32, c.weight_stride), (pos, torch.int32, c.pos_stride)):
+        first = None
+        for t in arrays:
+            if t is not None:
+                s = _slot_array(where, t, dt, pages, slots, heads, dev)
+                _need(where, first is None or first == s)
+                first = s
+        if first is not None:
+            to[:] = first
+    return c, dev
+
+
+def _numbers(where, dev, *pairs):
+    """Contiguous arrays of a call: (tensor or None, shape, dtype)."""
+    for t, shape, dtype in pairs:
+        if t is not None:
+            _need(where, t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev)
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None, k_exp=None, v_exp=None, weight=None,
+                 pos=None, tokens_seen=None, dev_status=None, stream=None):
+    """New rows k, v [T, Hkv, D] bf16 (slices of a fused projection may be
+    given) into the caches [num_pages, page_size, Hkv, D] (bf16 or
+    float8_e4m3fn with uint8 exponents k_exp, v_exp [num_pages, page_size,
+    Hkv]; any order of the first three dimensions in memory) at the pages of
+    block_table int32 [B, max_pages]: sequence b's rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] (None: one row each) become its slots up to kv_len[b],
+    which counts them.  weight fp32 and pos int32 (arrays like the exponents)
+    are set for the new slots: 0, and the tokens' numbers up to tokens_seen[b]
+    (None: kv_len).  Returns dev_status, which is only ever raised: pass one
+    word to many calls, zeroed once."""
+    import torch
+    w = "thd_cache_append"
+    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight,), (pos,))
+    _need(w, k.dim() == 3 and k.dtype is torch.bfloat16 and k.get_device() == dev)
+    T = k.shape[0]
+    s_k, s_v = _rope_rows(w, k, k, T, c.Hkv, c.D), _rope_rows(w, k, v, T, c.Hkv, c.D)
+    i32 = torch.int32
+    _numbers(w, dev, (cu_seqlens, (c.B + 1,), i32), (tokens_seen, (c.B,), i32), (dev_status, (1,), i32))
+    side = _aside(stream)
+    with _alloc_on(side):
+        st = torch.zeros(1, dtype=i32, device=k.device) if dev_status is None else dev_status
+    _check(w, thd_cache_append(c, k, v, s_k, s_v, T, cu_seqlens, weight, pos, tokens_seen, st, stream))
+    _keep(side, stream, (k, v, k_cache, v_cache, block_table, kv_len, cu_seqlens, k_exp, v_exp, weight, pos, tokens_seen,
+                         dev_status), (st,))
+    return st
+
+
+def attn_decode(q, k_cache, v_cache, block_table, kv_len, *, k_exp=None, v_exp=None, softmax_scale=None, softcap=0.0,
+                dist_slopes=None, kv_start=None, pos=None, tokens_seen=None, weight=None, weight_out=None, out=None,
+                lse=None, dev_status=None, workspace=None, stream=None):
+    """Attention of one new token a sequence, q [B, Hq, D] bf16 (rows may be
+    slices of a fused projection), over a cache as cache_append's; softcap and
+    dist_slopes as attn_score_fwd's (distances by pos and tokens_seen, or by
+    slots and kv_len), kv_start int32 [B] the first visible slot.  weight: the
+    tokens' attention weights are added to it (into weight_out, if given).
+    Returns (o [B, Hq, D], lse [Hq, B], dev_status)."""
+    import torch
+    w = "thd_attn_decode"
+    if weight_out is None:
+        weight_out = weight
+    _need(w, weight is not None or weight_out is None)
+    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight, weight_out), (pos,))
+    _need(w, q.dim() == 3 and q.dtype is torch.bfloat16 and q.get_device() == dev)
+    B, Hq, D = c.B, q.shape[1], c.D
+    s_q = _rope_rows(w, q, q, B, Hq, D)
+    f32, i32 = torch.float32, torch.int32
+    _numbers(w, dev, (dist_slopes, (Hq,), f32), (kv_start, (B,), i32), (tokens_seen, (B,), i32),
+             (out, (B, Hq, D), torch.bfloat16), (lse, (Hq, B), f32), (dev_status, (1,), i32))
+    _need(w, workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    given = (q, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, dist_slopes, kv_start, pos, tokens_seen, weight,
+             weight_out, out, lse, dev_status, workspace)
+    side = _aside(stream)
+    with _alloc_on(side):
+        o = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+        l = torch.empty((Hq, B), dtype=f32, device=q.device) if lse is None else lse
+        st = torch.zeros(1, dtype=i32, device=q.device) if dev_status is None else dev_status
+        if workspace is None:
+            workspace = _workspace(thd_decode_workspace_size(B, Hq, c.Hkv, D, c.max_pages * c.page_size,
+                                                             int(weight is not None)), q.device)
+    _check(w, thd_attn_decode(c, q, s_q, o, l, Hq, scale, softcap, dist_slopes, kv_start, pos, tokens_seen, weight,
+                              weight_out, workspace, workspace.numel() * workspace.element_size(), st, stream))
+    _keep(side, stream, given, (o, l, st))
+    return o, l, st
+
+
+def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen, *, budget, sinks=0, recent=0,
+                k_exp=None, v_exp=None, weight_out=None, pos_out=None, new_len=None, dev_status=None, workspace=None,
+                stream=None):
+    """Shrinks caches as cache_append's to `budget` slots a sequence and kv
+    head: the largest weights stay, with the first `sinks` and the last
+    `recent` tokens (by pos and tokens_seen).  Slots move in place; weight and
+    pos too, unless weight_out, pos_out take them.  Returns (new_len int32 [B],
+    dev_status)."""
+    import torch
+    w = "thd_cache_evict"
+    weight_out = weight if weight_out is None else weight_out
+    pos_out = pos if pos_out is None else pos_out
+    _need(w, weight is not None and pos is not None)
+    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight, weight_out), (pos, pos_out))
+    i32 = torch.int32
+    _need(w, tokens_seen is not None)
+    _numbers(w, dev, (tokens_seen, (c.B,), i32), (new_len, (c.B,), i32), (dev_status, (1,), i32))
+    _need(w, workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+    given = (k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen, k_exp, v_exp, weight_out, pos_out, new_len,
+             dev_status, workspace)
+    side = _aside(stream)
+    with _alloc_on(side):
+        n = torch.empty(c.B, dtype=i32, device=k_cache.device) if new_len is None else new_len
+        st = torch.zeros(1, dtype=i32, device=k_cache.device) if dev_status is None else dev_status
+        if workspace is None:
+            workspace = _workspace(thd_evict_workspace_size(c.B, c.Hkv, c.max_pages * c.page_size, budget), k_cache.device)
+    _check(w, thd_cache_evict(c, weight, weight_out, pos, pos_out, tokens_seen, budget, sinks, recent, n, workspace,
+                              workspace.numel() * workspace.element_size(), st, stream))
+    _keep(side, stream, given, (n, st))
+    return n, st
