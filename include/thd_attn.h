@@ -102,6 +102,7 @@ typedef struct CUstream_st* thd_stream_t; /* identical to cudaStream_t */
 #define THD_KERNEL_DECODE_JOIN 15
 #define THD_KERNEL_CACHE_APPEND 16
 #define THD_KERNEL_CACHE_EVICT 17
+#define THD_KERNEL_DECODE_WEIGHTS 18
 
 /* mask modes (the `causal` argument of the attention entry points) */
 #define THD_CAUSAL_NONE 0
@@ -638,7 +639,7 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  *     else they do not overlap).
  *   Lengths are read on the device: a captured graph serves growing ones.
  * Bit-reproducible on one kind of GPU.  Launches: 2 (1 for tables of at most 64
- * slots and no weights).  Workspace: thd_decode_workspace_size.
+ * slots), with weights one more.  Workspace: thd_decode_workspace_size.
  */
 THD_API int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, void* o, float* lse, int Hq,
                             float softmax_scale, float softcap, const float* dist_slopes, const int32_t* kv_start,

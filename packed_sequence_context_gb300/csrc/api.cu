@@ -974,7 +974,7 @@ static int check_cache(const thd_kv_cache* c, CacheView* v) {
   v->kv_len = c->kv_len;
   v->num_pages = c->num_pages;
   v->capacity = (int64_t)c->max_pages * c->page_size;
-  v->page_size = c->page_size;
+  v->page = divisor((uint32_t)c->page_size);
   v->B = c->B;
   v->Hkv = c->Hkv;
   v->D = c->D;
@@ -1010,15 +1010,16 @@ int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, in
   return cuda_status(launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Workspace of a decode: [units][part][part_ml][lse2][scores].
+// Workspace of a decode: [units][joins][part][part_ml][lse2][scores].
 struct DecodeWs {
-  size_t units, part, part_ml, lse2, scores, total;
+  size_t units, joins, part, part_ml, lse2, scores, total;
 };
 static DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int64_t capacity, bool weights) {
   const size_t heads = (size_t)decode_heads(Hq / Hkv);
   DecodeWs w;
   w.units = 0;
-  w.part = align_up(sizeof(int64_t) * ((size_t)B + 1), 256);
+  w.joins = align_up(sizeof(int64_t) * ((size_t)B + 1), 256);
+  w.part = align_up(w.joins + sizeof(DecodeJoin) * kDecodeMaxGrid, 256);
   w.part_ml = align_up(w.part + sizeof(float) * 2 * kDecodeMaxGrid * heads * D, 256);
   w.lse2 = align_up(w.part_ml + sizeof(float) * 2 * kDecodeMaxGrid * heads * 3, 256);
   w.scores = align_up(w.lse2 + (weights ? sizeof(float) * (size_t)B * Hq : 0), 256);
@@ -1079,6 +1080,7 @@ int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, 
   p.status = dev_status;
   char* const ws = static_cast<char*>(workspace);
   p.units = reinterpret_cast<int64_t*>(ws + w.units);
+  p.joins = reinterpret_cast<DecodeJoin*>(ws + w.joins);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   p.lse2 = reinterpret_cast<float*>(ws + w.lse2);

@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (n > c.capacity || j < 0) {
         raise(p.status, THD_DEV_ERR_KV_LEN);
       } else {
-        page = page_of(c, b, (uint32_t)j / (uint32_t)c.page_size);
+        const Place at_j = place_of(c, (int)j);
+        page = page_of(c, b, at_j.page);
         if (page < 0) raise(p.status, THD_DEV_ERR_PAGE);
-        slot = (uint32_t)j % (uint32_t)c.page_size;
+        slot = (int)at_j.slot;
         pos = (int)((p.seen ? (int64_t)p.seen[b] : n) - back);
       }
     }
@@ -191,16 +192,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     if (bad) raise(p.status, THD_DEV_ERR_KV_LEN);
     p.new_len[b] = n < p.budget ? n : p.budget;
   }
-  const uint32_t ps = (uint32_t)c.page_size;
   const int chunk = (n + p.share - 1) / p.share;
   const int lo = rank * chunk < n ? rank * chunk : n, hi = lo + chunk < n ? lo + chunk : n;
   const bool copy_w = p.weight_out != p.weight_in, copy_p = p.pos_out != p.pos_in;
 
   // weight and position of a slot to the outputs' slot of the same number
   auto carry = [&](int i) {
-    const int page = page_of(c, b, (uint32_t)i / ps);
+    const Place x = place_of(c, i);
+    const int page = page_of(c, b, x.page);
     if (page < 0) return;
-    const int64_t w = at(p.weight_at, page, (uint32_t)i % ps, g), q = at(p.pos_at, page, (uint32_t)i % ps, g);
+    const int64_t w = at(p.weight_at, page, x.slot, g), q = at(p.pos_at, page, x.slot, g);
     if (copy_w) p.weight_out[w] = p.weight_in[w];
     if (copy_p) p.pos_out[q] = p.pos_in[q];
   };
@@ -212,13 +213,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
 
   const int seen = p.seen[b];
   auto read_key = [&](int i) -> uint32_t {
-    const int page = page_of(c, b, (uint32_t)i / ps);
+    const Place x = place_of(c, i);
+    const int page = page_of(c, b, x.page);
     if (page < 0) {
       raise(p.status, THD_DEV_ERR_PAGE);
       return 0u;
     }
-    const int pos = p.pos_in[at(p.pos_at, page, (uint32_t)i % ps, g)];
-    return order_of(p.weight_in[at(p.weight_at, page, (uint32_t)i % ps, g)],
+    const int pos = p.pos_in[at(p.pos_at, page, x.slot, g)];
+    return order_of(p.weight_in[at(p.weight_at, page, x.slot, g)],
                     pos < p.sinks || (int64_t)pos >= (int64_t)seen - p.recent);
   };
   {
@@ -364,9 +366,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       const uint32_t i = i0 + u * stride;
       pf[u] = pt[u] = -1;
       if (i < total) {
-        const uint32_t f = (uint32_t)of[i], t = (uint32_t)to[i];
-        pf[u] = page_of(c, b, f / ps), sf[u] = f % ps;
-        pt[u] = page_of(c, b, t / ps), st[u] = t % ps;
+        const Place f = place_of(c, of[i]), t = place_of(c, to[i]);
+        pf[u] = page_of(c, b, f.page), sf[u] = f.slot;
+        pt[u] = page_of(c, b, t.page), st[u] = t.slot;
         if (pt[u] < 0) pf[u] = -1;
       }
       if (pf[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(rows + at(c.row, pf[u], sf[u], g));

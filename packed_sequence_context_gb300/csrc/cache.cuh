@@ -15,6 +15,19 @@ struct SlotStrides {
   int64_t page, slot, head;
 };
 
+// Division by the page size without a division: for 0 <= x <= 2^30 and
+// 1 <= d <= 2^30, x / d = x mul >> shift with mul = ceil(2^shift / d), shift =
+// 30 + ceil(log2 d) (mul d exceeds 2^shift by less than d, x times which stays
+// below 2^shift).
+struct Divisor {
+  uint32_t d, mul, shift;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t log = 0;
+  while ((1u << log) < d) ++log;
+  return Divisor{d, (uint32_t)((((uint64_t)1 << (30 + log)) + d - 1) / d), 30 + log};
+}
+
 struct CacheView {
   uint8_t* k;
   uint8_t* v;
@@ -27,7 +40,8 @@ struct CacheView {
   const int32_t* kv_len;
   int64_t num_pages;
   int64_t capacity;  // slots a sequence's row of the table names: max_pages * page_size
-  int page_size, B, Hkv, D;
+  Divisor page;      // slots of one
+  int B, Hkv, D;
 };
 
 struct AppendParams {
@@ -43,6 +57,13 @@ struct AppendParams {
   const int32_t* seen;  // null: kv_len
   int32_t* status;
   int tokens;  // a block
+};
+
+// An item that several blocks shared, as its last block leaves it for the join:
+// query heads h .. h + heads - 1 of sequence b, parts of `count` blocks from
+// `first` on.  count 0: none.
+struct DecodeJoin {
+  int b, h, heads, first, count;
 };
 
 struct DecodeParams {
@@ -66,7 +87,8 @@ struct DecodeParams {
   int64_t* units;   // [B + 1] units in front of each sequence
   float* part;      // [2 grid][heads of an item][D]
   float* part_ml;   // [2 grid][heads of an item][3]
-  float* lse2;      // [B][Hq], items that one block computed alone (with weights)
+  DecodeJoin* joins;  // [grid]
+  float* lse2;      // [B][Hq] in base 2, with weights
   float* scores;    // [B][Hkv][capacity][G], with weights
   int grid;
 };
@@ -107,6 +129,14 @@ __device__ inline int slots_of(const CacheView& c, int b, bool& bad) {
   const int n = c.kv_len[b];
   bad = n < 0 || n > c.capacity;
   return bad ? 0 : n;
+}
+
+struct Place {
+  uint32_t page, slot;
+};
+__device__ inline Place place_of(const CacheView& c, int j) {
+  const uint32_t q = (uint32_t)(((uint64_t)(uint32_t)j * c.page.mul) >> c.page.shift);
+  return Place{q, (uint32_t)j - q * c.page.d};
 }
 
 // The page of a sequence's slot, or -1 where the table names none of the cache.

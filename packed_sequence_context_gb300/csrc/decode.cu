@@ -33,6 +33,7 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 3;
 constexpr int kDecTile = 8192;  // bytes of a stage: a tile's keys, then its values
 constexpr int kUnit = 64;       // slots
+constexpr int kLead = 2;        // units that an item's beginning and end cost
 constexpr int kMinUnits = 2;    // of a block, while there are few
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -65,11 +66,28 @@ THD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+THD_DEV void mma16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two numbers as e4m3 (lo in the low byte), and what that rounding left of them.
+THD_DEV uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t y;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
+  return y;
+}
 // Two e4m3 numbers (low half) as two fp16, exactly.
 THD_DEV uint32_t e4m3x2(uint32_t x) {
   uint32_t y;
   asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
   return y;
+}
+// 32 times what that rounding left of them (exact: at most 8 times 32), again as e4m3.
+THD_DEV uint32_t rest_of(float lo, float hi, uint32_t rounded) {
+  const uint32_t h = e4m3x2(rounded);
+  const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(32.f)));
+  return to_e4m3x2(fmaf(lo, 32.f, -f.x), fmaf(hi, 32.f, -f.y));
 }
 template <bool kHalf>
 THD_DEV uint32_t pack2(float lo, float hi) {
@@ -104,6 +122,12 @@ THD_DEV Range range_of(const DecodeParams& p, int b) {
   return r;
 }
 THD_DEV int units_of(const Range& r) { return (r.n - r.s + kUnit - 1) / kUnit; }
+// What an item counts in the cut: its units, and kLead in front of them for its
+// beginning and end (queries, first loads, the join of the warps).
+THD_DEV int cost_of(const Range& r) {
+  const int n = units_of(r);
+  return n > 0 ? n + kLead : 0;
+}
 
 // Blocks that share `total` units, and what the c-th of them takes: [c total /
 // blocks, (c + 1) total / blocks).
@@ -121,10 +145,13 @@ struct DecShape {
   static constexpr int kSub = kKeys / 16;
   static constexpr int kPieces = kRow / 16;
   static constexpr int kHeads = 8 * NT;
+  // next to e4m3 values, probabilities as two e4m3 numbers each, where the two
+  // sums' registers allow it (else as fp16, the values converted)
+  static constexpr bool kPv8 = kFp8 && NT * D <= 128;
   static constexpr int kPitch = D + 4;                 // floats of a head's row in the join of the warps
   // shared memory, bytes
   static constexpr int kRing = kDecStages * kDecTile;  // a warp's
-  static constexpr int kMeta = kDecStages * kKeys * 8; // a warp's: exponents and positions
+  static constexpr int kMeta = kDecStages * kKeys * 12; // a warp's: the rows' scales, positions
   static constexpr int kQ = D * kHeads * 2;
   static constexpr size_t kSmem = (size_t)kDecWarps * (kRing + kMeta) + kQ + sizeof(float) * (kHeads * (2 + 3 * kDecWarps));
   static_assert(kHeads * kPitch * 4 <= kRing, "a warp's partial fits its ring");
@@ -159,7 +186,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
   const int b_lo = tid * per < c.B ? tid * per : c.B, b_hi = b_lo + per < c.B ? b_lo + per : c.B;
   {
     int64_t sum = 0;
-    for (int b = b_lo; b < b_hi; ++b) sum += units_of(range_of(p, b));
+    for (int b = b_lo; b < b_hi; ++b) sum += cost_of(range_of(p, b));
     s_seg[tid + 1] = sum;
     if (tid == 0) s_seg[0] = 0;
     __syncthreads();
@@ -194,19 +221,20 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
     int64_t at_b = s_seg[tid];
     for (int b = b_lo; b < b_hi; ++b) {
       p.units[b] = at_b;
-      at_b += units_of(range_of(p, b));
+      at_b += cost_of(range_of(p, b));
     }
     if (tid == kDecThreads - 1) p.units[c.B] = s_seg[kDecThreads];
   }
   const int HG = c.Hkv * p.blocks;  // items of a sequence
   const int64_t total = s_seg[kDecThreads] * HG;
   const int64_t blocks = blocks_for(total, (int)gridDim.x);
+  if (tid == 0) p.joins[blockIdx.x].count = 0;
   if (blockIdx.x >= blocks) return;
   int64_t u = blockIdx.x * total / blocks;
   const int64_t u_end = (blockIdx.x + 1) * total / blocks;
 
   // the first item
-  int b, item = 0, i0 = 0;
+  int b, item = 0, ic = 0;  // ic: where in the item's cost
   {
     const int64_t ub = u / HG;
     int seg = 0;
@@ -215,24 +243,37 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
     b = seg * per;
     int64_t before = s_seg[seg];
     for (; b < c.B; ++b) {
-      const int n = units_of(range_of(p, b));
+      const int n = cost_of(range_of(p, b));
       if (ub < before + n) {
         const int64_t r = u - before * HG;
         item = (int)(r / n);
-        i0 = (int)(r % n);
+        ic = (int)(r % n);
         break;
       }
       before += n;
     }
   }
 
-  const uint32_t ps = (uint32_t)c.page_size;
+  const int64_t v_minus_k = c.v - c.k;
   const uint32_t ring_a = smem_u32(ring);
   while (u < u_end && b < c.B) {
     const Range rg = range_of(p, b);
-    const int units = units_of(rg);
-    const int64_t take64 = u_end - u;
-    const int take = take64 < units - i0 ? (int)take64 : units - i0;
+    const int units = units_of(rg), cost = units + kLead;
+    const int step = u_end - u < cost - ic ? (int)(u_end - u) : cost - ic;
+    const int i0 = ic > kLead ? ic - kLead : 0, take = ic + step - kLead - i0;  // the first unit, how many
+    auto advance = [&]() {
+      u += step;
+      ic = 0;
+      if (u < u_end && ++item == HG) {
+        item = 0;
+        do ++b;
+        while (b < c.B && units_of(range_of(p, b)) == 0);
+      }
+    };
+    if (take <= 0) {  // of this item nothing but a part of what it counts in front
+      advance();
+      continue;
+    }
     const int g = item / p.blocks, h0 = (item % p.blocks) * S::kHeads;  // kv head; first query head of its group
     const int heads = p.G - h0 < S::kHeads ? p.G - h0 : S::kHeads;
     const int k0 = rg.s + i0 * kUnit;
@@ -243,13 +284,15 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
     // ---- a tile's copies
     constexpr int kRpl = S::kKeys > 32 ? S::kKeys / 32 : 1;  // rows a lane finds the place of
     int pid[kRpl];
-    uint32_t pend[kRpl];  // exponents on their way to shared memory
+    // exponents on their way to shared memory: loaded when a tile's copies are
+    // issued, looked at a tile later (combining them sooner would wait for them)
+    uint32_t pend_k[kRpl], pend_v[kRpl];
     int pend_stage = -1;
     auto fetch_pid = [&](int t) {
 #pragma unroll
       for (int r = 0; r < kRpl; ++r) {
         const int row = lane + 32 * r, j = k0 + t * S::kKeys + row;
-        pid[r] = row < S::kKeys && j < k1 ? c.table[b * c.table_stride + (uint32_t)j / ps] : 0;
+        pid[r] = row < S::kKeys && j < k1 ? c.table[b * c.table_stride + place_of(c, j).page] : 0;
       }
     };
     auto flush = [&]() {
@@ -257,45 +300,74 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
 #pragma unroll
         for (int r = 0; r < kRpl; ++r)
           if (lane + 32 * r < S::kKeys)
-            reinterpret_cast<uint32_t*>(meta)[pend_stage * 2 * S::kKeys + lane + 32 * r] = pend[r];
+            reinterpret_cast<float2*>(meta + pend_stage * 12 * S::kKeys)[lane + 32 * r] =
+                make_float2(scale_of(pend_k[r]), pend_v[r] == 255u ? NAN : (float)((int)pend_v[r] - 127));
       }
       pend_stage = -1;
     };
     auto issue = [&](int t, int stage) {
+      const int j0 = k0 + t * S::kKeys;
+      const uint32_t dst = ring_a + stage * kDecTile, meta_a = smem_u32(meta) + stage * 12 * S::kKeys;
+      constexpr int kRowsPer = 32 / S::kPieces;  // rows of one warp-wide copy
+      const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
+      pend_stage = stage;
+      const Place first = place_of(c, j0);
+      const int page0 = __shfl_sync(0xffffffffu, pid[0], 0);
+      if (first.slot + S::kKeys <= c.page.d && j0 + S::kKeys <= k1 && page0 >= 0 && page0 < c.num_pages) {
+        // the whole tile in one page
+        const uint8_t* from = c.k + at(c.row, page0, first.slot + row0, g) + 16 * piece;
+        const int64_t step = kRowsPer * c.row.slot;
+#pragma unroll
+        for (int i = 0; i < S::kKeys / kRowsPer; ++i) {
+          const uint32_t a = dst + swz<S::kPieces>(i * kRowsPer + row0, piece);
+          cp_async_16(a, from, 16);
+          cp_async_16(a + kDecTile / 2, from + v_minus_k, 16);
+          from += step;
+        }
+#pragma unroll
+        for (int r = 0; r < kRpl; ++r) {
+          const int row = lane + 32 * r;
+          if (row < S::kKeys) {
+            if (kFp8) {
+              const int64_t e = at(c.exp, page0, first.slot + row, g);
+              pend_k[r] = c.k_exp[e];
+              pend_v[r] = c.v_exp[e];
+            }
+            if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, page0, first.slot + row, g));
+          }
+        }
+        return;
+      }
       int64_t off[kRpl];
 #pragma unroll
       for (int r = 0; r < kRpl; ++r) {
-        const int row = lane + 32 * r, j = k0 + t * S::kKeys + row;
+        const int row = lane + 32 * r, j = j0 + row;
         off[r] = -1;
-        pend[r] = 127u | 127u << 8;
+        pend_k[r] = pend_v[r] = 127u;
         if (row < S::kKeys && j < k1) {
-          const uint32_t slot = (uint32_t)j % ps;
+          const uint32_t slot = place_of(c, j).slot;
           if (pid[r] < 0 || pid[r] >= c.num_pages) {
             raise(p.status, THD_DEV_ERR_PAGE);
           } else {
             off[r] = at(c.row, pid[r], slot, g);
             if (kFp8) {
               const int64_t e = at(c.exp, pid[r], slot, g);
-              pend[r] = (uint32_t)c.k_exp[e] | (uint32_t)c.v_exp[e] << 8;
+              pend_k[r] = c.k_exp[e];
+              pend_v[r] = c.v_exp[e];
             }
-            if (p.pos)
-              cp_async_4(smem_u32(meta) + (stage * 2 * S::kKeys + S::kKeys + row) * 4, p.pos + at(p.pos_at, pid[r], slot, g));
+            if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, pid[r], slot, g));
           }
         }
       }
-      const uint32_t dst = ring_a + stage * kDecTile;
-      constexpr int kRowsPer = 32 / S::kPieces;  // rows of one warp-wide copy
-      const int piece = lane % S::kPieces;
 #pragma unroll
       for (int i = 0; i < S::kKeys / kRowsPer; ++i) {
-        const int row = i * kRowsPer + lane / S::kPieces;
+        const int row = i * kRowsPer + row0;
         const int64_t o = __shfl_sync(0xffffffffu, off[kRpl > 1 ? (i * kRowsPer) / 32 : 0], row & 31);
         const uint32_t a = dst + swz<S::kPieces>(row, piece);
-        const int64_t from = o < 0 ? 0 : o + 16 * piece;
-        cp_async_16(a, c.k + from, o < 0 ? 0 : 16);
-        cp_async_16(a + kDecTile / 2, c.v + from, o < 0 ? 0 : 16);
+        const uint8_t* const from = c.k + (o < 0 ? 0 : o + 16 * piece);
+        cp_async_16(a, from, o < 0 ? 0 : 16);
+        cp_async_16(a + kDecTile / 2, from + v_minus_k, o < 0 ? 0 : 16);
       }
-      pend_stage = stage;
     };
 
     // ---- the first copies, then the queries, which all warps share
@@ -318,8 +390,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         w[k] = n < heads ? reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + (int64_t)(g * p.G + h0 + n) * D)[lane + 32 * k] : 0u;
       float mul = 1.f;
       if (kFp8) {
-        // fp16 queries: the largest of a head is brought to [2^14, 2^15) by a
-        // power of two, so elements down to 2^-28 of it keep bf16's precision
+        // two e4m3 numbers for each element, the second 32 times what the first's
+        // rounding left: the largest of a head is brought to [128, 256) by a
+        // power of two, then bf16's eight bits are kept whole down to 2^-15 of
+        // it, and what is smaller to 2^-22 of it
         uint32_t big = 0;
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) big = __vmaxu2(big, w[k] & 0x7fff7fffu);
@@ -327,23 +401,27 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         big = __reduce_max_sync(0xffffffffu, big);
         int e = (int)(big >> 7);                  // exponent field of the largest
         e = e == 0 ? 1 : e;
-        const int up = 127 + 14 - e;              // 2^up times the head; in two steps, each a normal number
+        const int up = 127 + 7 - e;               // 2^up times the head; in two steps, each a normal number
         const float m1 = __uint_as_float((uint32_t)(127 + up / 2) << 23);
         const float m2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
         mul = (1.f / m1) * (1.f / m2);
+        if (e == 255) mul = NAN;                  // an infinity or NaN among the elements
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           const float lo = __uint_as_float(w[k] << 16) * m1 * m2, hi = __uint_as_float(w[k] & 0xffff0000u) * m1 * m2;
-          w[k] = pack2<true>(lo, hi);
+          const uint32_t first = to_e4m3x2(lo, hi);
+          const int d = 2 * (lane + 32 * k), kp = d >> 5, in = d & 31;
+          uint8_t* const to = s_q + ((kp * NT + (n >> 3)) * 32 + (n & 7) * 4 + ((in & 15) >> 2)) * 16 + (in >> 4) * 4 + (in & 3);
+          *reinterpret_cast<uint16_t*>(to) = (uint16_t)first;
+          *reinterpret_cast<uint16_t*>(to + 8) = (uint16_t)rest_of(lo, hi, first);
         }
-      }
+      } else {
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k) {
-        const int d = 2 * (lane + 32 * k), ks = d >> 4, in = d & 15;
-        // fragment order of the matrix instruction's second operand; the e4m3
-        // form counts the elements of a step as its keys' bytes arrive
-        const int reg = kFp8 ? (in & 3) >> 1 : in >> 3, quad = kFp8 ? in >> 2 : (in & 7) >> 1;
-        *reinterpret_cast<uint32_t*>(s_q + ((((ks * NT + (n >> 3)) * 32 + (n & 7) * 4 + quad) * 2 + reg) * 4)) = w[k];
+        for (int k = 0; k < kPairs; ++k) {
+          const int d = 2 * (lane + 32 * k), ks = d >> 4, in = d & 15;
+          // fragment order of the matrix instruction's second operand
+          *reinterpret_cast<uint32_t*>(s_q + ((((ks * NT + (n >> 3)) * 32 + (n & 7) * 4 + ((in & 7) >> 1)) * 2 + (in >> 3)) * 4)) = w[k];
+        }
       }
       if (lane == 0) {
         s_hs[n] = mul * (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e);
@@ -359,24 +437,27 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
 
     // ---- tiles: running maximum (base 2) m and sum l of each head, O^T
     // mo: the maximum of score + log2 of the value's scale, what O is relative to
-    float m[NT][2], mo[NT][2], l[NT][2], o[D / 16][NT][4];
+    // o2: the sum over the probabilities' second numbers, 32 times as large
+    // base: m, or 0 while there is none
+    float m[NT][2], mo[NT][2], l[NT][2], base[NT][2], up[NT][2], o[D / 16][NT][4], o2[S::kPv8 ? D / 16 : 1][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = mo[nt][e] = -INFINITY, l[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) m[nt][e] = mo[nt][e] = -INFINITY, l[nt][e] = base[nt][e] = up[nt][e] = 0.f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[d][nt][e] = o2[S::kPv8 ? d : 0][nt][e] = 0.f;
 
     int stage = 0;
     for (int t = warp; t < tiles; t += kDecWarps) {
       cp_wait<kDecStages - 2>();
       __syncwarp();
       const uint32_t kt = ring_a + stage * kDecTile, vt = kt + kDecTile / 2;
-      const uint32_t* const mt = reinterpret_cast<const uint32_t*>(meta) + stage * 2 * S::kKeys;
+      const float2* const scales = reinterpret_cast<const float2*>(meta + stage * 12 * S::kKeys);
+      const uint32_t* const numbers = reinterpret_cast<const uint32_t*>(meta + stage * 12 * S::kKeys + 8 * S::kKeys);
       float s[S::kSub][NT][4];
 #pragma unroll
       for (int sub = 0; sub < S::kSub; ++sub)
@@ -387,149 +468,228 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
       // lanes' rows and pieces of the four 8x8 matrices of a load: rows 0-7 and
       // 8-15 of the first 16 bytes, then of the second
       const int lrow = lane & 15, lpc = lane >> 4;
-#pragma unroll
-      for (int kp = 0; kp < S::kPieces / 2; ++kp) {
-        constexpr int kSteps = kFp8 ? 2 : 1;  // steps of 16 elements in 32 bytes
-        uint2 bq[kSteps][NT];
-#pragma unroll
-        for (int x = 0; x < kSteps; ++x)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            bq[x][nt] = *reinterpret_cast<const uint2*>(s_q + (((kp * kSteps + x) * NT + nt) * 32 + lane) * 8);
+      if (kFp8) {
 #pragma unroll
         for (int sub = 0; sub < S::kSub; ++sub) {
-          uint32_t r[4];
-          ldsm4(r, kt + swz<S::kPieces>(sub * 16 + lrow, 2 * kp + lpc));
-          if (kFp8) {
-            const uint32_t a0[4] = {e4m3x2(r[0]), e4m3x2(r[1]), e4m3x2(r[0] >> 16), e4m3x2(r[1] >> 16)};
-            const uint32_t a1[4] = {e4m3x2(r[2]), e4m3x2(r[3]), e4m3x2(r[2] >> 16), e4m3x2(r[3] >> 16)};
+          float rest[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rest[nt][e] = 0.f;
+#pragma unroll
+          for (int kp = 0; kp < S::kPieces / 2; ++kp) {
+            uint32_t r[4];
+            ldsm4(r, kt + swz<S::kPieces>(sub * 16 + lrow, 2 * kp + lpc));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816<true>(s[sub][nt], a0, bq[0][nt].x, bq[0][nt].y);
-              mma16816<true>(s[sub][nt], a1, bq[kSteps - 1][nt].x, bq[kSteps - 1][nt].y);
+              const uint4 bq = *reinterpret_cast<const uint4*>(s_q + ((kp * NT + nt) * 32 + lane) * 16);
+              mma16832(s[sub][nt], r, bq.x, bq.y);
+              mma16832(rest[nt], r, bq.z, bq.w);
             }
-          } else {
+          }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[sub][nt], r, bq[0][nt].x, bq[0][nt].y);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[sub][nt][e] = fmaf(rest[nt][e], 1.f / 32, s[sub][nt][e]);
+        }
+      } else {
+#pragma unroll
+        for (int kp = 0; kp < S::kPieces / 2; ++kp) {
+          uint2 bq[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) bq[nt] = *reinterpret_cast<const uint2*>(s_q + ((kp * NT + nt) * 32 + lane) * 8);
+#pragma unroll
+          for (int sub = 0; sub < S::kSub; ++sub) {
+            uint32_t r[4];
+            ldsm4(r, kt + swz<S::kPieces>(sub * 16 + lrow, 2 * kp + lpc));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[sub][nt], r, bq[nt].x, bq[nt].y);
           }
         }
       }
       // scores in base 2
       const int j0 = k0 + t * S::kKeys;
       float lv[S::kSub][2];  // log2 of the values' scales
-      float mx[NT][2], mxo[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mx[nt][e] = mxo[nt][e] = -INFINITY;
 #pragma unroll
       for (int sub = 0; sub < S::kSub; ++sub)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int row = sub * 16 + half * 8 + gid, j = j0 + row;
-          const bool ok = j < k1;
-          float ksc = 1.f, far = 0.f;
+          float2 sc;
           if (kFp8) {
-            const uint32_t e = mt[row];
-            ksc = scale_of(e & 0xffu);
-            lv[sub][half] = (e >> 8) == 255u ? NAN : (float)((int)(e >> 8) - 127);
+            sc = scales[sub * 16 + half * 8 + gid];
+            lv[sub][half] = sc.y;
           }
-          if (p.slopes) far = (float)(int)((uint32_t)seen - 1u - (p.pos ? mt[S::kKeys + row] : (uint32_t)j));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              y[e] = s[sub][nt][2 * half + e] * hs[nt][e];
-              if (kFp8) y[e] *= ksc;
-              if (p.cap > 0.f) y[e] = p.cap * kLog2e * tanhf(y[e]);
-              if (p.slopes) y[e] = fmaf(-sl[nt][e], far, y[e]);
-              y[e] = ok ? y[e] : -INFINITY;
-              s[sub][nt][2 * half + e] = y[e];
-              mx[nt][e] = fmaxf(mx[nt][e], y[e]);
-              if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], y[e] + lv[sub][half]);
-            }
-            if (p.weight_out && j < k1) {
-              float* const to = p.scores + (((int64_t)b * c.Hkv + g) * c.capacity + j) * p.G + h0 + nt * 8 + 2 * t4;
-              if (nt * 8 + 2 * t4 < heads) to[0] = y[0];
-              if (nt * 8 + 2 * t4 + 1 < heads) to[1] = y[1];
-            }
+            float &y0 = s[sub][nt][2 * half], &y1 = s[sub][nt][2 * half + 1];
+            if (kFp8) fmul2(y0, y1, y0, y1, sc.x, sc.x);
+            fmul2(y0, y1, y0, y1, hs[nt][0], hs[nt][1]);
           }
         }
-      bool moved = false;
-      float al[NT][2], alo[NT][2];
+      if (p.cap > 0.f) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int sub = 0; sub < S::kSub; ++sub)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-            if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], __shfl_xor_sync(0xffffffffu, mxo[nt][e], d));
-          }
-          const float m2 = fmaxf(m[nt][e], mx[nt][e]);
-          moved |= m2 > m[nt][e];
-          al[nt][e] = m2 > m[nt][e] ? ex2(m[nt][e] - m2) : 1.f;
-          m[nt][e] = m2;
-          if (kFp8) {
-            const float o2 = fmaxf(mo[nt][e], mxo[nt][e]);
-            moved |= o2 > mo[nt][e];
-            alo[nt][e] = o2 > mo[nt][e] ? ex2(mo[nt][e] - o2) : 1.f;
-            mo[nt][e] = o2;
-          } else {
-            alo[nt][e] = al[nt][e];
-            mo[nt][e] = m2;
-          }
-        }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          l[nt][0] *= al[nt][0];
-          l[nt][1] *= al[nt][1];
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            o[d][nt][0] *= alo[nt][0];
-            o[d][nt][1] *= alo[nt][1];
-            o[d][nt][2] *= alo[nt][0];
-            o[d][nt][3] *= alo[nt][1];
-          }
-        }
+            for (int e = 0; e < 4; ++e) s[sub][nt][e] = p.cap * kLog2e * tanhf(s[sub][nt][e]);
       }
-      // probabilities: summed in fp32, rounded to 16 bits (bf16 next to bf16
-      // values, fp16 next to e4m3) for the product, as the packed kernels do
-      uint32_t pb[S::kSub][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float base[2], baseo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          base[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-          baseo[e] = mo[nt][e] == -INFINITY ? 0.f : mo[nt][e];
-        }
+      if (p.slopes) {
 #pragma unroll
         for (int sub = 0; sub < S::kSub; ++sub)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            float w[2];
+            const int row = sub * 16 + half * 8 + gid;
+            const float far = (float)(int)((uint32_t)seen - 1u - (p.pos ? numbers[row] : (uint32_t)(j0 + row)));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y = s[sub][nt][2 * half + e];
-              w[e] = ex2(y - base[e]);
-              l[nt][e] += w[e];
-              if (kFp8) w[e] = ex2(y + lv[sub][half] - baseo[e]);
-            }
-            pb[sub][nt][half] = movm_t(pack2<kFp8>(w[0], w[1]));
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) s[sub][nt][2 * half + e] = fmaf(-sl[nt][e], far, s[sub][nt][2 * half + e]);
           }
+      }
+      if (j0 + S::kKeys > k1) {  // slots behind the last
+#pragma unroll
+        for (int sub = 0; sub < S::kSub; ++sub)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            if (j0 + sub * 16 + half * 8 + gid >= k1) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) s[sub][nt][2 * half] = s[sub][nt][2 * half + 1] = -INFINITY;
+            }
+      }
+      if (p.weight_out) {
+#pragma unroll
+        for (int sub = 0; sub < S::kSub; ++sub)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int j = j0 + sub * 16 + half * 8 + gid;
+            if (j < k1) {
+              float* const to = p.scores + (((int64_t)b * c.Hkv + g) * c.capacity + j) * p.G + h0 + 2 * t4;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (nt * 8 + 2 * t4 + e < heads) to[nt * 8 + e] = s[sub][nt][2 * half + e];
+            }
+          }
+      }
+      // The maximum moves only when a score passes it by more than kSlack: until
+      // then the lanes need not know one another's scores.  (Probabilities then
+      // reach 2^kSlack: any bf16 or fp32 does, 256 * 1.7 is an e4m3 number, 256 an fp16.)
+      constexpr float kSlack = S::kPv8 ? 0.75f : 8.f;
+      float mx[NT][2], mxo[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = mxo[nt][e] = -INFINITY;
+#pragma unroll
+          for (int sub = 0; sub < S::kSub; ++sub) {
+            mx[nt][e] = fmax3(mx[nt][e], s[sub][nt][e], s[sub][nt][2 + e]);
+            if (kFp8) mxo[nt][e] = fmax3(mxo[nt][e], s[sub][nt][e] + lv[sub][0], s[sub][nt][2 + e] + lv[sub][1]);
+          }
+          moved |= mx[nt][e] > m[nt][e] + kSlack;
+          if (kFp8) moved |= mxo[nt][e] > mo[nt][e] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2], alo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+              if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], __shfl_xor_sync(0xffffffffu, mxo[nt][e], d));
+            }
+            const float m2 = fmaxf(m[nt][e], mx[nt][e]);
+            al[e] = m2 > m[nt][e] ? ex2(m[nt][e] - m2) : 1.f;
+            m[nt][e] = m2;
+            base[nt][e] = m2 == -INFINITY ? 0.f : m2;
+            alo[e] = al[e];
+            if (kFp8) {
+              const float o2m = fmaxf(mo[nt][e], mxo[nt][e]);
+              alo[e] = o2m > mo[nt][e] ? ex2(mo[nt][e] - o2m) : 1.f;
+              mo[nt][e] = o2m;
+              // from a probability times the value's scale to what the product takes
+              up[nt][e] = ex2(base[nt][e] - (o2m == -INFINITY ? 0.f : o2m) + (S::kPv8 ? 8.f : 0.f));
+            }
+            l[nt][e] *= al[e];
+          }
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            fmul2(o[d][nt][0], o[d][nt][1], o[d][nt][0], o[d][nt][1], alo[0], alo[1]);
+            fmul2(o[d][nt][2], o[d][nt][3], o[d][nt][2], o[d][nt][3], alo[0], alo[1]);
+            if (S::kPv8) {
+              float(&x)[4] = o2[S::kPv8 ? d : 0][nt];
+              fmul2(x[0], x[1], x[0], x[1], alo[0], alo[1]);
+              fmul2(x[2], x[3], x[2], x[3], alo[0], alo[1]);
+            }
+          }
+        }
+      }
+      // probabilities: summed in fp32, and for the product rounded as bf16 next
+      // to bf16 values (2^-8, as the packed kernels do), next to e4m3 ones as
+      // fp16 (2^-11) or as two e4m3 numbers (2^-8, and 2^-23 of the largest)
+      uint32_t pb[S::kSub][NT][2];
+#pragma unroll
+      for (int sub = 0; sub < S::kSub; ++sub) {
+        float vs[2];
+        if (kFp8) vs[0] = ex2(lv[sub][0]), vs[1] = ex2(lv[sub][1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[2][2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float y0, y1;
+            fadd2(y0, y1, s[sub][nt][2 * half], s[sub][nt][2 * half + 1], -base[nt][0], -base[nt][1]);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], y0, y1);
+            if (kFp8) {
+              fmul2(y0, y1, y0, y1, vs[half], vs[half]);
+              fmul2(y0, y1, y0, y1, up[nt][0], up[nt][1]);
+            }
+            w[half][0] = y0;
+            w[half][1] = y1;
+          }
+          if (S::kPv8) {
+            // a register has a head's slots gid and gid + 8 side by side
+            const uint32_t a0 = to_e4m3x2(w[0][0], w[1][0]), a1 = to_e4m3x2(w[0][1], w[1][1]);
+            pb[sub][nt][0] = movm_t(a0 | a1 << 16);
+            pb[sub][nt][1] = movm_t(rest_of(w[0][0], w[1][0], a0) | rest_of(w[0][1], w[1][1], a1) << 16);
+          } else {
+            pb[sub][nt][0] = movm_t(pack2<kFp8>(w[0][0], w[0][1]));
+            pb[sub][nt][1] = movm_t(pack2<kFp8>(w[1][0], w[1][1]));
+          }
+        }
       }
       // O^T += V^T P^T
 #pragma unroll
       for (int dp = 0; dp < S::kPieces / 2; ++dp)
 #pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub) {
+        for (int sub = 0; sub < S::kSub; sub += S::kPv8 ? 2 : 1) {
           uint32_t r[4];
-          if (kFp8) {
+          if (S::kPv8) {
             // matrices: slots 0-7 and 8-15 of 16 elements, then of the next 16;
-            // a register has elements 2 gid and 2 gid + 1 of two slots
+            // a register has elements 2 gid and 2 gid + 1 of two slots; a step
+            // of 32 slots counts them as the probabilities' registers do
+            uint32_t r2[4];
+            ldsm4t(r, vt + swz<S::kPieces>(sub * 16 + lrow, 2 * dp + lpc));
+            ldsm4t(r2, vt + swz<S::kPieces>(sub * 16 + 16 + lrow, 2 * dp + lpc));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t a[4] = {__byte_perm(r[2 * x], r[2 * x + 1], 0x6240), __byte_perm(r[2 * x], r[2 * x + 1], 0x7351),
+                                     __byte_perm(r2[2 * x], r2[2 * x + 1], 0x6240), __byte_perm(r2[2 * x], r2[2 * x + 1], 0x7351)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                constexpr int kNext = S::kPv8 ? 1 : 0;
+                mma16832(o[(S::kPv8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][0], pb[sub + kNext][nt][0]);
+                mma16832(o2[(S::kPv8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][1], pb[sub + kNext][nt][1]);
+              }
+            }
+          } else if (kFp8) {
             ldsm4t(r, vt + swz<S::kPieces>(sub * 16 + lrow, 2 * dp + lpc));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -569,7 +729,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
         if (gid == 0) {
           float* const to = s_ml + warp * 3 * S::kHeads + nt * 8 + 2 * t4 + e;
-          to[0] = mo[nt][e];
+          to[0] = kFp8 ? mo[nt][e] : m[nt][e];
           to[S::kHeads] = m[nt][e];
           to[2 * S::kHeads] = l[nt][e];
         }
@@ -584,18 +744,26 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 3 * S::kHeads + nt * 8 + 2 * t4 + e]);
-        f[e] = top == -INFINITY ? 1.f : ex2(mo[nt][e] - top);
+        f[e] = top == -INFINITY ? 1.f : ex2((kFp8 ? mo[nt][e] : m[nt][e]) - top);
+        if (S::kPv8) f[e] *= 1.f / 256;
       }
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int at_d = d * 16 + (kFp8 ? 2 * gid + (e >> 1) : gid + 8 * (e >> 1));
-          mine[(nt * 8 + 2 * t4 + (e & 1)) * S::kPitch + at_d] = o[d][nt][e] * f[e & 1];
+          mine[(nt * 8 + 2 * t4 + (e & 1)) * S::kPitch + at_d] =
+              (S::kPv8 ? fmaf(o2[S::kPv8 ? d : 0][nt][e], 1.f / 32, o[d][nt][e]) : o[d][nt][e]) * f[e & 1];
         }
     }
     __syncthreads();
     const bool whole = take == units;
+    if (tid == 0 && !whole && i0 + take == units) {
+      // the item's last block names its parts: the first block's is in that
+      // one's second slot, the others' in their first
+      const int64_t first = owner_of(u - ic + kLead, total, blocks);
+      p.joins[blockIdx.x] = DecodeJoin{b, g * p.G + h0, heads, (int)first, (int)(blockIdx.x - first) + 1};
+    }
     const int64_t slot = 2 * (int64_t)blockIdx.x + (i0 > 0 ? 0 : 1);
     for (int i = tid; i < heads * (D / 4); i += kDecThreads) {
       const int n = i / (D / 4), d = 4 * (i % (D / 4));
@@ -636,144 +804,159 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         }
       }
     }
-    // on to the next item
-    u += take;
-    i0 = 0;
-    if (u < u_end && ++item == HG) {
-      item = 0;
-      do ++b;
-      while (b < c.B && units_of(range_of(p, b)) == 0);
-    }
+    advance();
     __syncthreads();  // the rings are read
   }
 }
 
 // ------------------------------------------------------------------ the join
-// The parts of the items that several blocks shared, a block for each (sequence,
-// query head); behind them, blocks that turn the scores into weights.
-constexpr int kJoinThreads = 256;
-
-THD_DEV float joined_lse2(const DecodeParams& p, int64_t u0, int64_t u1, int64_t total, int64_t blocks, int kheads, int n,
-                          int lane) {
-  const int64_t c0 = owner_of(u0, total, blocks), c1 = owner_of(u1 - 1, total, blocks);
-  float top = -INFINITY;
-  for (int64_t x = c0 + lane; x <= c1; x += 32)
-    top = fmaxf(top, p.part_ml[((2 * x + (x * total / blocks > u0 ? 0 : 1)) * kheads + n) * 3 + 1]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int64_t x = c0 + lane; x <= c1; x += 32) {
-    const float* ml = p.part_ml + ((2 * x + (x * total / blocks > u0 ? 0 : 1)) * kheads + n) * 3;
-    sum += ml[2] * ex2(ml[1] - base);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return base + log2f(sum);
-}
+// The parts of an item that several blocks shared: a block of 128 threads for
+// each (block that ended one, head), four parts at a time, a head's row across
+// the lanes.  The sums run over the parts in order, four interleaved.
+constexpr int kJoinThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams p, int kheads, int weight_blocks) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams p, int kheads) {
   constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
   __shared__ float4 s_x[kJoinThreads];
+  __shared__ float s_ml[kDecodeMaxGrid][3], s_top[kJoinThreads / 32][2], s_sum[kParts];
+  const int tid = threadIdx.x, n = blockIdx.y;
+  grid_dep_launch();
+  grid_dep_wait();
+  const DecodeJoin j = p.joins[blockIdx.x];
+  if (j.count == 0 || n >= j.heads) return;
+  // part k's row
+  auto row_of = [&](int k) { return (2 * (int64_t)(j.first + k) + (k == 0 ? 1 : 0)) * kheads + n; };
+  float topo = -INFINITY, top = -INFINITY;
+  for (int k = tid; k < j.count; k += kJoinThreads) {
+    const float* ml = p.part_ml + row_of(k) * 3;
+    s_ml[k][0] = ml[0], s_ml[k][1] = ml[1], s_ml[k][2] = ml[2];
+    topo = fmaxf(topo, ml[0]);
+    top = fmaxf(top, ml[1]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, d));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  if ((tid & 31) == 0) s_top[tid >> 5][0] = topo, s_top[tid >> 5][1] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) topo = fmaxf(topo, s_top[w][0]), top = fmaxf(top, s_top[w][1]);
+  const float base = top == -INFINITY ? 0.f : top, baseo = topo == -INFINITY ? 0.f : topo;
+  const int lane = tid % kLanes, mine = tid / kLanes;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = mine; k < j.count; k += kParts) {
+    const float4 y = *reinterpret_cast<const float4*>(p.part + row_of(k) * D + 4 * lane);
+    const float f = ex2(s_ml[k][0] - baseo);
+    sum += s_ml[k][2] * ex2(s_ml[k][1] - base);
+    acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
+  }
+  s_x[tid] = acc;
+  if (lane == 0) s_sum[mine] = sum;
+  __syncthreads();
+  if (tid < kLanes) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float4 y = s_x[k * kLanes + tid];
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      z += s_sum[k];
+    }
+    const float f = z == 0.f ? 0.f : ex2(baseo - base) / z;
+    uint2 y;
+    y.x = pack2<false>(x.x * f, x.y * f);
+    y.y = pack2<false>(x.z * f, x.w * f);
+    const int64_t row = (int64_t)j.b * p.Hq + j.h + n;
+    *reinterpret_cast<uint2*>(p.o + row * D + 4 * tid) = y;
+    if (tid == 0) {
+      const float lse2 = base + log2f(z);
+      p.lse[(int64_t)(j.h + n) * p.c.B + j.b] = lse2 * kLn2;
+      if (p.weight_out) p.lse2[row] = lse2;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the weights
+// From the scores and the finished log-sum-exps: a block takes a contiguous run
+// of the units of (sequence, kv head) pairs, a thread up to four slots at a time.
+// 4 G + 8 bytes a slot and kv head, the scores mostly from L2.
+constexpr int kWeightThreads = 256;
+
+__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const DecodeParams p) {
   __shared__ float s_lse[kDecodeMaxGroup];
   const CacheView& c = p.c;
   const int tid = threadIdx.x;
   grid_dep_wait();
-  const int HG = c.Hkv * p.blocks;
-  const int64_t total = p.units[c.B] * HG;
-  if (total == 0) return;
-  const int64_t blocks = blocks_for(total, p.grid);
-  const int64_t joins = (int64_t)c.B * p.Hq;
-  if (blockIdx.x < joins) {
-    const int b = (int)(blockIdx.x / p.Hq), h = (int)(blockIdx.x % p.Hq);
-    const int g = h / p.G, n = (h % p.G) % kheads, item = g * p.blocks + (h % p.G) / kheads;
-    const int64_t units = p.units[b + 1] - p.units[b];
-    const int64_t u0 = p.units[b] * HG + item * units, u1 = u0 + units;
-    if (units == 0) return;
-    const int64_t c0 = owner_of(u0, total, blocks), c1 = owner_of(u1 - 1, total, blocks);
-    if (c0 == c1) return;  // one block's: written
-    const int lane = tid % kLanes, mine = tid / kLanes;
-    float topo = -INFINITY, top = -INFINITY;
-    for (int64_t x = c0; x <= c1; ++x) {
-      const float* ml = p.part_ml + ((2 * x + (x * total / blocks > u0 ? 0 : 1)) * kheads + n) * 3;
-      topo = fmaxf(topo, ml[0]);
-      top = fmaxf(top, ml[1]);
-    }
-    const float base = top == -INFINITY ? 0.f : top, baseo = topo == -INFINITY ? 0.f : topo;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int64_t x = c0 + mine; x <= c1; x += kParts) {
-      const int64_t slot = (2 * x + (x * total / blocks > u0 ? 0 : 1)) * kheads + n;
-      const float* ml = p.part_ml + slot * 3;
-      const float4 y = *reinterpret_cast<const float4*>(p.part + slot * D + 4 * lane);
-      const float f = ex2(ml[0] - baseo);
-      sum += ml[2] * ex2(ml[1] - base);
-      acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
-    }
-    __shared__ float s_sum[kParts];
-    s_x[tid] = acc;
-    if (lane == 0) s_sum[mine] = sum;
-    __syncthreads();
-    if (tid < kLanes) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float s = 0.f;
-      for (int k = 0; k < kParts; ++k) {
-        const float4 y = s_x[k * kLanes + tid];
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-        s += s_sum[k];
-      }
-      const float f = s == 0.f ? 0.f : ex2(baseo - base) / s;
-      uint2 y;
-      y.x = pack2<false>(x.x * f, x.y * f);
-      y.y = pack2<false>(x.z * f, x.w * f);
-      *reinterpret_cast<uint2*>(p.o + ((int64_t)b * p.Hq + h) * D + 4 * tid) = y;
-      if (tid == 0) p.lse[(int64_t)h * c.B + b] = (base + log2f(s)) * kLn2;
-    }
-    return;
-  }
-  // weights: the units of (sequence, kv head) pairs, cut evenly
-  const int64_t w = blockIdx.x - joins, all = p.units[c.B] * c.Hkv;
-  int64_t u = w * all / weight_blocks;
-  const int64_t u_end = (w + 1) * all / weight_blocks;
+  const int64_t all = p.units[c.B] * c.Hkv;
+  int64_t u = blockIdx.x * all / gridDim.x;
+  const int64_t u_end = (blockIdx.x + 1) * all / gridDim.x;
   while (u < u_end) {
     const int64_t ub = u / c.Hkv;
-    int lo = 0, hi = c.B - 1;  // the sequence: the last with units in front of it <= ub, and units of its own
+    int lo = 0, hi = c.B - 1;  // the sequence: the last with no more than ub in front of it
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.units[mid] <= ub) lo = mid; else hi = mid - 1;
     }
     const int b = lo;
-    const int64_t units = p.units[b + 1] - p.units[b], r = u - p.units[b] * c.Hkv;
-    const int g = (int)(r / units);
-    const int64_t i0 = r % units;
-    const int64_t take = u_end - u < units - i0 ? u_end - u : units - i0;
-    for (int n = tid >> 5; n < p.G; n += kJoinThreads / 32) {
-      const int item = g * p.blocks + n / kheads;
-      const int64_t v0 = p.units[b] * HG + item * units;
-      float z;
-      if (owner_of(v0, total, blocks) == owner_of(v0 + units - 1, total, blocks))
-        z = p.lse2[(int64_t)b * p.Hq + g * p.G + n];
-      else
-        z = joined_lse2(p, v0, v0 + units, total, blocks, kheads, n % kheads, tid & 31);
-      if ((tid & 31) == 0) s_lse[n] = z == -INFINITY ? INFINITY : z;
+    const int64_t cost = p.units[b + 1] - p.units[b], r = u - p.units[b] * c.Hkv;
+    const int g = (int)(r / cost);
+    const int64_t ic = r - g * cost;
+    const int64_t take = u_end - u < cost - ic ? u_end - u : cost - ic;
+    u += take;
+    if (ic + take <= kLead) continue;
+    for (int n = tid; n < p.G; n += kWeightThreads) {
+      const float z = p.lse2[(int64_t)b * p.Hq + g * p.G + n];
+      s_lse[n] = z == -INFINITY ? INFINITY : z;
     }
     __syncthreads();
     const Range rg = range_of(p, b);
-    const int k0 = rg.s + (int)i0 * kUnit;
-    const int k1 = rg.n - k0 < take * kUnit ? rg.n : k0 + (int)take * kUnit;
-    for (int j = k0 + tid; j < k1; j += kJoinThreads) {
-      const int page = page_of(c, b, (uint32_t)j / (uint32_t)c.page_size);
-      if (page < 0) continue;
-      const float* s = p.scores + (((int64_t)b * c.Hkv + g) * c.capacity + j) * p.G;
-      float x = 0.f;
-      for (int n = 0; n < p.G; ++n) x += ex2(s[n] - s_lse[n]);
-      const int64_t a = at(p.weight_at, page, (uint32_t)j % (uint32_t)c.page_size, g);
-      p.weight_out[a] = p.weight_in[a] + x;
+    const int k0 = rg.s + (int)(ic > kLead ? ic - kLead : 0) * kUnit;
+    const int64_t k_end = rg.s + (ic + take - kLead) * kUnit;
+    const int k1 = k_end < rg.n ? (int)k_end : rg.n;
+    const float* const scores = p.scores + ((int64_t)b * c.Hkv + g) * c.capacity * p.G;
+    for (int j0 = k0; j0 < k1; j0 += 4 * kWeightThreads) {
+      int64_t a[4];
+      float w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + x * kWeightThreads + tid;
+        a[x] = -1;
+        if (j < k1) {
+          const Place to = place_of(c, j);
+          const int page = page_of(c, b, to.page);
+          if (page >= 0) a[x] = at(p.weight_at, page, to.slot, g);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        w[x] = a[x] < 0 ? 0.f : p.weight_in[a[x]];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + x * kWeightThreads + tid;
+        if (a[x] < 0) continue;
+        const float* const s = scores + (int64_t)j * p.G;
+        float sum = 0.f;
+        if (p.G % 4 == 0) {
+#pragma unroll 4
+          for (int n = 0; n < p.G; n += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(s + n);
+            sum += ex2(y.x - s_lse[n]) + ex2(y.y - s_lse[n + 1]) + (ex2(y.z - s_lse[n + 2]) + ex2(y.w - s_lse[n + 3]));
+          }
+        } else {
+          for (int n = 0; n < p.G; ++n) sum += ex2(s[n] - s_lse[n]);
+        }
+        w[x] += sum;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (a[x] >= 0) p.weight_out[a[x]] = w[x];
     }
     __syncthreads();
-    u += take;
   }
 }
 
@@ -807,25 +990,31 @@ cudaError_t launch_decode(DecodeParams p, cudaStream_t st) {
   p.grid = (int)grid;
   cudaError_t e = p.c.k_exp ? launch_decode_d<true>(p, heads, st) : launch_decode_d<false>(p, heads, st);
   if (e != cudaSuccess) return e;
-  // an item of one unit is one block's, and without weights nothing is left to do
-  if (p.c.capacity <= kUnit && !p.weight_out) return cudaSuccess;
-  const int wb = p.weight_out ? 4 * num_sms() : 0;
-  const int64_t joins = (int64_t)p.c.B * p.Hq;
-  if (joins + wb >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(joins + wb));
-  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  prof_before(THD_KERNEL_DECODE_JOIN, st);
-  e = p.c.D == 64 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p, heads, wb)
-                  : cudaLaunchKernelEx(&cfg, decode_join_kernel<128>, p, heads, wb);
-  count_launch();
-  prof_after(THD_KERNEL_DECODE_JOIN, st);
+  if (p.c.capacity > kUnit) {  // an item of one unit is one block's
+    cfg.gridDim = dim3((unsigned)p.grid, (unsigned)heads);
+    cfg.blockDim = dim3(kJoinThreads);
+    prof_before(THD_KERNEL_DECODE_JOIN, st);
+    e = p.c.D == 64 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p, heads)
+                    : cudaLaunchKernelEx(&cfg, decode_join_kernel<128>, p, heads);
+    count_launch();
+    prof_after(THD_KERNEL_DECODE_JOIN, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.weight_out) {
+    cfg.gridDim = dim3((unsigned)(8 * num_sms()));
+    cfg.blockDim = dim3(kWeightThreads);
+    prof_before(THD_KERNEL_DECODE_WEIGHTS, st);
+    e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, p);
+    count_launch();
+    prof_after(THD_KERNEL_DECODE_WEIGHTS, st);
+  }
   return e;
 }
 

@@ -60,6 +60,7 @@ THD_KERNEL_DECODE = 14
 THD_KERNEL_DECODE_JOIN = 15
 THD_KERNEL_CACHE_APPEND = 16
 THD_KERNEL_CACHE_EVICT = 17
+THD_KERNEL_DECODE_WEIGHTS = 18
 
 THD_FWD_KERNEL_SINGLE = 1
 THD_FWD_KERNEL_DUAL = 2
