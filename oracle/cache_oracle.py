@@ -79,10 +79,10 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
       the bias's magnitude;
     * exp2 to 2^-22, sums in fp32 (n 2^-24, by halves and by tiles: 2^-18 here
       for up to 64 x 1024 slots);
-    * next to e4m3 keys, queries as two e4m3 numbers: off by at most 2^-22 of a
-      head's largest element (far smaller elements; 0 for the others);
-    * probabilities rounded to bf16, or next to e4m3 values to fp16 or two e4m3
-      numbers (2^-8, and 2^-23 of the largest), the output to bf16 (2^-8).
+    * next to e4m3 keys, queries as fp16, off by at most 2^-39 of a head's
+      largest element (elements far below it; 0 for the others);
+    * probabilities rounded to bf16 (2^-8), or next to e4m3 values to fp16 (2^-11,
+      and 2^-32 of the largest), the output to bf16 (2^-8).
     """
     q = np.asarray(q, np.float64)
     B, Hq, D = q.shape
@@ -92,7 +92,7 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
     tol_o, tol_lse = np.full((B, Hq, D), 1e-30), np.zeros((Hq, B))
     w = None if weight is None else np.asarray(weight, np.float64).copy()
     tol_w = None if weight is None else np.zeros(w.shape)
-    half = 2.0 ** -8
+    half = 2.0 ** -11 if e4m3 else 2.0 ** -8
     for b in range(B):
         s0 = 0 if start is None else min(max(int(start[b]), 0), int(kv_len[b]))
         p, at = (x[s0:] for x in slots(table[b], int(kv_len[b]), page))
@@ -109,7 +109,7 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
             y = softcap * np.tanh(x / softcap) if softcap else x
             err = 2.0 ** -24 * (D + 12) * size + 2.0 ** -21 * (softcap + np.abs(y))
             if e4m3:
-                err = err + 2.0 ** -22 * scale * np.abs(q[b, h]).max() * np.abs(k).sum(1)
+                err = err + 2.0 ** -39 * scale * np.abs(q[b, h]).max() * np.abs(k).sum(1)
             if slopes is not None:
                 num = np.asarray(pos[p, at, g], np.float64) if pos is not None else np.arange(s0, int(kv_len[b]))
                 far = float(slopes[h]) * ((int(seen[b]) if seen is not None else int(kv_len[b])) - 1 - num)
@@ -125,12 +125,12 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
             o[b, h], lse[h, b] = pr @ v, m + np.log(z)
             tol_lse[h, b] = dz + 2.0 ** -22 * abs(lse[h, b]) + 2.0 ** -22 * abs(m)
             size = np.abs(v)
-            # each weight: rounded, off by its score, by the sum; e4m3 below its normal numbers (2^-23 of the largest
+            # each weight: rounded, off by its score, by the sum; fp16 below its normal numbers (2^-32 of the largest
             # product of weight and value scale)
             tol_o[b, h] += ((pr * (half + rel + dz))[:, None] * size).sum(0) + 2.0 ** -8 * np.abs(o[b, h])
             if e4m3:
                 top = float((pr * 2.0 ** (np.asarray(cache["v_exp"][p, at, g], np.float64) - 127)).max())
-                tol_o[b, h] += 2.0 ** -23 * top * np.abs(np.asarray(cache["v"][p, at, g], np.float64)).sum(0)
+                tol_o[b, h] += 2.0 ** -32 * top * np.abs(np.asarray(cache["v"][p, at, g], np.float64)).sum(0)
             if w is not None:
                 w[p, at, g] += pr
                 tol_w[p, at, g] += pr * (rel + dz + 2.0 ** -20) + 1e-30

@@ -4,6 +4,12 @@
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
+#ifndef MPDL
+#define MPDL 0
+#endif
+#ifndef APDL
+#define APDL 1
+#endif
 #include "vec8.cuh"
 
 namespace thd {
@@ -36,6 +42,8 @@ __device__ inline int row_exponent(uint32_t big) {
 template <bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   __shared__ int s_page[kAppendTokens], s_slot[kAppendTokens], s_pos[kAppendTokens];
+  follow();
+  depend();
   const CacheView& c = p.c;
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
   const int count = (int)(p.T - t0 < p.tokens ? p.T - t0 : p.tokens);
@@ -141,12 +149,8 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
   p.tokens = (int)(n > kAppendTokens ? kAppendTokens : n);
   const int64_t grid = (a.T + p.tokens - 1) / p.tokens;
   prof_before(THD_KERNEL_CACHE_APPEND, st);
-  if (a.c.k_exp)
-    append_kernel<true><<<(unsigned)grid, kAppendThreads, 0, st>>>(p);
-  else
-    append_kernel<false><<<(unsigned)grid, kAppendThreads, 0, st>>>(p);
-  count_launch();
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_following(a.c.k_exp ? append_kernel<true> : append_kernel<false>, dim3((unsigned)grid),
+                                         kAppendThreads, 0, st, APDL, (const AppendParams)p);
   prof_after(THD_KERNEL_CACHE_APPEND, st);
   return e;
 }
@@ -407,6 +411,7 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(sizeof(uint32_t) * kEvictMaxHeld));
   if (e != cudaSuccess) return e;
+  prof_before(THD_KERNEL_CACHE_EVICT, st);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)share;
@@ -418,7 +423,6 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  prof_before(THD_KERNEL_CACHE_EVICT, st);
   e = cudaLaunchKernelEx(&cfg, evict_kernel, p);
   count_launch();
   prof_after(THD_KERNEL_CACHE_EVICT, st);

@@ -119,7 +119,31 @@ constexpr int kDecodeMaxGrid = 1024;   // blocks of a decode launch (the workspa
 constexpr int kDecodeMaxGroup = 512;   // query heads of a kv head
 int decode_heads(int G);               // query heads of a work item
 
+// Launches a kernel that may start while the one in front of it in the stream
+// ends: its blocks begin with depend(), which waits for that kernel's end and
+// the writes of it, and with follow(), which lets the next such kernel start.
+// What this hides is the launch, a microsecond or two of each.
+template <typename... A>
+cudaError_t launch_following(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, int pdl, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  count_launch();
+  return e;
+}
+
 #ifdef __CUDACC__
+__device__ inline void follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ inline void depend() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The status word of the cache's operators is sticky: the largest code since
 // its owner zeroed it (whatever the order of the blocks).
 __device__ inline void raise(int32_t* status, int code) { atomicMax(status, code); }

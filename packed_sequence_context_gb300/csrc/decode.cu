@@ -24,18 +24,29 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#ifndef MPDL
+#define MPDL 0
+#endif
+#ifndef APDL
+#define APDL 1
+#endif
 #include "ptx.cuh"
 
 namespace thd {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecStages = 3;
+#ifndef BP8
+#define BP8 3
+#define BPB 2
+#endif
 constexpr int kDecTile = 8192;  // bytes of a stage: a tile's keys, then its values
 constexpr int kUnit = 64;       // slots
 constexpr int kLead = 2;        // units that an item's beginning and end cost
 constexpr int kMinUnits = 2;    // of a block, while there are few
 
+constexpr float kSlack = 8.f;   // see the running maximum
+constexpr float kRaise = 7.f;   // fp16 probabilities are 2^7 times as large: 2^15 at most, 2^-31 at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -50,6 +61,11 @@ THD_DEV void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
+// A 16-byte asynchronous copy, and one that fills with zeros (reading nothing) unless `on`.
+THD_DEV void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+THD_DEV void cp16_if(uint32_t dst, const void* src, bool on) { cp_async_16(dst, src, on ? 16 : 0); }
 THD_DEV uint32_t movm_t(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -66,28 +82,11 @@ THD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-THD_DEV void mma16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Two numbers as e4m3 (lo in the low byte), and what that rounding left of them.
-THD_DEV uint32_t to_e4m3x2(float lo, float hi) {
-  uint16_t y;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
-  return y;
-}
 // Two e4m3 numbers (low half) as two fp16, exactly.
 THD_DEV uint32_t e4m3x2(uint32_t x) {
   uint32_t y;
   asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
   return y;
-}
-// 32 times what that rounding left of them (exact: at most 8 times 32), again as e4m3.
-THD_DEV uint32_t rest_of(float lo, float hi, uint32_t rounded) {
-  const uint32_t h = e4m3x2(rounded);
-  const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(32.f)));
-  return to_e4m3x2(fmaf(lo, 32.f, -f.x), fmaf(hi, 32.f, -f.y));
 }
 template <bool kHalf>
 THD_DEV uint32_t pack2(float lo, float hi) {
@@ -101,8 +100,6 @@ THD_DEV uint32_t pack2(float lo, float hi) {
 THD_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 THD_DEV void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
-THD_DEV void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-THD_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 2^(e - 127) of a stored exponent; 255: NaN.
 THD_DEV float scale_of(uint32_t e) {
@@ -138,6 +135,15 @@ THD_DEV int64_t blocks_for(int64_t total, int grid) {
 THD_DEV int64_t owner_of(int64_t unit, int64_t total, int64_t blocks) { return ((unit + 1) * blocks - 1) / total; }
 
 // ------------------------------------------------------------------ the walk
+// What a block works on at a time: slots [k0, k1) of a sequence, for query heads
+// h0 .. of kv head g.
+struct Segment {
+  int b, g, h0, k0, k1;
+  int i0;      // units of the item in front of it
+  bool last;   // the item ends with it
+  int64_t at;  // where the item's cost begins in the cut
+};
+
 template <bool kFp8, int D, int NT>
 struct DecShape {
   static constexpr int kRow = D * (kFp8 ? 1 : 2);      // bytes
@@ -145,35 +151,40 @@ struct DecShape {
   static constexpr int kSub = kKeys / 16;
   static constexpr int kPieces = kRow / 16;
   static constexpr int kHeads = 8 * NT;
-  // next to e4m3 values, probabilities as two e4m3 numbers each, where the two
-  // sums' registers allow it (else as fp16, the values converted)
-  static constexpr bool kPv8 = kFp8 && NT * D <= 128;
-  static constexpr int kPitch = D + 4;                 // floats of a head's row in the join of the warps
+  static constexpr int kStages = 2;
+  static constexpr int kPerSm = NT > 1 ? 2 : kFp8 ? BP8 : BPB;   // blocks
+  // slots worked on at a time, in sixteens: more of them overlap better, fewer
+  // leave the registers to the heads
+  static constexpr int kStep = NT == 1 ? kSub : NT == 2 && kSub > 1 ? 2 : 1;
+  // whether a warp's part of O fits one stage, so that the other may be filled meanwhile
+  static constexpr bool kAhead = kHeads * D * 4 <= kDecTile;
   // shared memory, bytes
-  static constexpr int kRing = kDecStages * kDecTile;  // a warp's
-  static constexpr int kMeta = kDecStages * kKeys * 12; // a warp's: the rows' scales, positions
+  static constexpr int kRing = kStages * kDecTile;  // a warp's
+  static constexpr int kMeta = kStages * kKeys * 12; // a warp's: the rows' scales, positions
   static constexpr int kQ = D * kHeads * 2;
   static constexpr size_t kSmem = (size_t)kDecWarps * (kRing + kMeta) + kQ + sizeof(float) * (kHeads * (2 + 3 * kDecWarps));
-  static_assert(kHeads * kPitch * 4 <= kRing, "a warp's partial fits its ring");
+  static_assert(kHeads * D * 4 <= kRing, "a warp's partial fits its ring");
 };
 
-// Byte offset of 16-byte piece c of row r in a tile's keys or values: pieces
-// are permuted so that eight rows' equal pieces lie in eight different bank
-// groups.
+// A tile's keys or values: row r's 16-byte piece c lies at piece c ^ x(r) of the
+// row, x(r) = r mod 8 (rows of 64 bytes: r / 2 mod 4), so that eight rows' equal
+// pieces lie in eight different bank groups.  Where a lane's row is fixed but for
+// multiples of 8, or its piece but for even numbers, what varies is an exclusive
+// or of address bits 4 to 7 and a constant.
 template <int kPieces>
 THD_DEV uint32_t swz(int r, int c) {
-  if (kPieces >= 8) return (uint32_t)(r * kPieces * 16 + ((c ^ (r & 7)) << 4));
-  return (uint32_t)(r * kPieces * 16 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * kPieces * 16 + ((c ^ (kPieces >= 8 ? r & 7 : (r >> 1) & 3)) << 4));
 }
 
 template <bool kFp8, int D, int NT>
-__global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) decode_kernel(const DecodeParams p) {
   using S = DecShape<kFp8, D, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_seg[kDecThreads + 1];
+  __shared__ int s_at[kDecWarps];  // where a warp's part of O lies in its ring
   const CacheView& c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
-  grid_dep_launch();
+  follow();
   uint8_t* const ring = smem + warp * S::kRing;
   uint8_t* const meta = smem + kDecWarps * S::kRing + warp * S::kMeta;
   uint8_t* const s_q = smem + kDecWarps * (S::kRing + S::kMeta);
@@ -181,6 +192,14 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
   float* const s_sl = s_hs + S::kHeads;
   float* const s_ml = s_sl + S::kHeads;                       // [kDecWarps][3][kHeads]
 
+  depend();
+  // the block table on its way to L2 while the lengths come: a line a thread
+  {
+    const int64_t bytes = (c.B - 1) * c.table_stride * 4 + c.capacity / c.page.d * 4;
+    const int64_t line = ((int64_t)blockIdx.x * kDecThreads + tid) * 128;
+    if (line < bytes)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(c.table) + line));
+  }
   // units in front of each sequence; rows without a visible slot; bad lengths
   const int per = (c.B + kDecThreads - 1) / kDecThreads;
   const int b_lo = tid * per < c.B ? tid * per : c.B, b_hi = b_lo + per < c.B ? b_lo + per : c.B;
@@ -254,14 +273,21 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
     }
   }
 
-  const int64_t v_minus_k = c.v - c.k;
-  const uint32_t ring_a = smem_u32(ring);
-  while (u < u_end && b < c.B) {
-    const Range rg = range_of(p, b);
-    const int units = units_of(rg), cost = units + kLead;
-    const int step = u_end - u < cost - ic ? (int)(u_end - u) : cost - ic;
-    const int i0 = ic > kLead ? ic - kLead : 0, take = ic + step - kLead - i0;  // the first unit, how many
-    auto advance = [&]() {
+  // the next run of an item's units in this block's share
+  auto next = [&](Segment& x) {
+    while (u < u_end && b < c.B) {
+      const Range rg = range_of(p, b);
+      const int units = units_of(rg), cost = units + kLead;
+      const int step = u_end - u < cost - ic ? (int)(u_end - u) : cost - ic;
+      x.b = b;
+      x.g = item / p.blocks;
+      x.h0 = (item % p.blocks) * S::kHeads;
+      x.i0 = ic > kLead ? ic - kLead : 0;
+      const int take = ic + step - kLead - x.i0;  // 0 or less: nothing but a part of what the item counts in front
+      x.last = x.i0 + take == units;
+      x.k0 = rg.s + x.i0 * kUnit;
+      x.k1 = rg.n - x.k0 < take * kUnit ? rg.n : x.k0 + take * kUnit;
+      x.at = u - ic;
       u += step;
       ic = 0;
       if (u < u_end && ++item == HG) {
@@ -269,131 +295,146 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         do ++b;
         while (b < c.B && units_of(range_of(p, b)) == 0);
       }
-    };
-    if (take <= 0) {  // of this item nothing but a part of what it counts in front
-      advance();
-      continue;
+      if (take > 0) return true;
     }
-    const int g = item / p.blocks, h0 = (item % p.blocks) * S::kHeads;  // kv head; first query head of its group
-    const int heads = p.G - h0 < S::kHeads ? p.G - h0 : S::kHeads;
-    const int k0 = rg.s + i0 * kUnit;
-    const int k1 = rg.n - k0 < take * kUnit ? rg.n : k0 + take * kUnit;
-    const int tiles = (k1 - k0 + S::kKeys - 1) / S::kKeys;
-    const int seen = p.slopes ? (p.seen ? p.seen[b] : rg.n) : 0;
+    return false;
+  };
 
-    // ---- a tile's copies
-    constexpr int kRpl = S::kKeys > 32 ? S::kKeys / 32 : 1;  // rows a lane finds the place of
-    int pid[kRpl];
-    // exponents on their way to shared memory: loaded when a tile's copies are
-    // issued, looked at a tile later (combining them sooner would wait for them)
-    uint32_t pend_k[kRpl], pend_v[kRpl];
-    int pend_stage = -1;
-    auto fetch_pid = [&](int t) {
+  const int64_t v_minus_k = c.v - c.k;
+  const uint32_t ring_a = smem_u32(ring);
+
+  // ---- a tile's copies
+  constexpr int kRpl = S::kKeys > 32 ? S::kKeys / 32 : 1;  // rows a lane finds the place of
+  int pid[kRpl], pid_after[kRpl];  // pages of the rows of the next tile to issue, and of the one after it
+  // exponents on their way to shared memory: loaded when a tile's copies are
+  // issued, looked at a tile later (combining them sooner would wait for them)
+  uint32_t pend_k[kRpl], pend_v[kRpl];
+  int pend_stage = -1;
+  auto fetch_pid = [&](const Segment& x, int t) {
 #pragma unroll
-      for (int r = 0; r < kRpl; ++r) {
-        const int row = lane + 32 * r, j = k0 + t * S::kKeys + row;
-        pid[r] = row < S::kKeys && j < k1 ? c.table[b * c.table_stride + place_of(c, j).page] : 0;
-      }
-    };
-    auto flush = [&]() {
-      if (kFp8 && pend_stage >= 0) {
+    for (int r = 0; r < kRpl; ++r) {
+      const int row = lane + 32 * r, j = x.k0 + t * S::kKeys + row;
+      pid[r] = pid_after[r];
+      pid_after[r] = row < S::kKeys && j < x.k1 ? c.table[x.b * c.table_stride + place_of(c, j).page] : 0;
+    }
+  };
+  auto flush = [&]() {
+    if (kFp8 && pend_stage >= 0) {
 #pragma unroll
-        for (int r = 0; r < kRpl; ++r)
-          if (lane + 32 * r < S::kKeys)
-            reinterpret_cast<float2*>(meta + pend_stage * 12 * S::kKeys)[lane + 32 * r] =
-                make_float2(scale_of(pend_k[r]), pend_v[r] == 255u ? NAN : (float)((int)pend_v[r] - 127));
-      }
-      pend_stage = -1;
-    };
-    auto issue = [&](int t, int stage) {
-      const int j0 = k0 + t * S::kKeys;
-      const uint32_t dst = ring_a + stage * kDecTile, meta_a = smem_u32(meta) + stage * 12 * S::kKeys;
-      constexpr int kRowsPer = 32 / S::kPieces;  // rows of one warp-wide copy
-      const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
-      pend_stage = stage;
-      const Place first = place_of(c, j0);
-      const int page0 = __shfl_sync(0xffffffffu, pid[0], 0);
-      if (first.slot + S::kKeys <= c.page.d && j0 + S::kKeys <= k1 && page0 >= 0 && page0 < c.num_pages) {
-        // the whole tile in one page
-        const uint8_t* from = c.k + at(c.row, page0, first.slot + row0, g) + 16 * piece;
-        const int64_t step = kRowsPer * c.row.slot;
-#pragma unroll
-        for (int i = 0; i < S::kKeys / kRowsPer; ++i) {
-          const uint32_t a = dst + swz<S::kPieces>(i * kRowsPer + row0, piece);
-          cp_async_16(a, from, 16);
-          cp_async_16(a + kDecTile / 2, from + v_minus_k, 16);
-          from += step;
-        }
-#pragma unroll
-        for (int r = 0; r < kRpl; ++r) {
-          const int row = lane + 32 * r;
-          if (row < S::kKeys) {
-            if (kFp8) {
-              const int64_t e = at(c.exp, page0, first.slot + row, g);
-              pend_k[r] = c.k_exp[e];
-              pend_v[r] = c.v_exp[e];
-            }
-            if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, page0, first.slot + row, g));
-          }
-        }
-        return;
-      }
-      int64_t off[kRpl];
-#pragma unroll
-      for (int r = 0; r < kRpl; ++r) {
-        const int row = lane + 32 * r, j = j0 + row;
-        off[r] = -1;
-        pend_k[r] = pend_v[r] = 127u;
-        if (row < S::kKeys && j < k1) {
-          const uint32_t slot = place_of(c, j).slot;
-          if (pid[r] < 0 || pid[r] >= c.num_pages) {
-            raise(p.status, THD_DEV_ERR_PAGE);
-          } else {
-            off[r] = at(c.row, pid[r], slot, g);
-            if (kFp8) {
-              const int64_t e = at(c.exp, pid[r], slot, g);
-              pend_k[r] = c.k_exp[e];
-              pend_v[r] = c.v_exp[e];
-            }
-            if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, pid[r], slot, g));
-          }
-        }
-      }
+      for (int r = 0; r < kRpl; ++r)
+        if (lane + 32 * r < S::kKeys)
+          reinterpret_cast<float2*>(meta + pend_stage * 12 * S::kKeys)[lane + 32 * r] =
+              make_float2(scale_of(pend_k[r]), pend_v[r] == 255u ? NAN : (float)((int)pend_v[r] - 127));
+    }
+    pend_stage = -1;
+  };
+  auto issue = [&](const Segment& x, int t, int stage) {
+    const int j0 = x.k0 + t * S::kKeys, k1 = x.k1, g = x.g;
+    const uint32_t slot0 = place_of(c, j0).slot;
+    constexpr int kRowsPer = 32 / S::kPieces;  // rows of one warp-wide copy: 512 bytes
+    const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
+    const uint32_t dst = ring_a + stage * kDecTile + swz<S::kPieces>(row0, piece), meta_a = smem_u32(meta) + stage * 12 * S::kKeys;
+    // of the i-th copy: row i kRowsPer + row0
+    auto at_row = [&](int i) { return dst ^ (S::kPieces >= 8 ? ((i * kRowsPer) & 7) << 4 : 0); };
+    pend_stage = stage;
+    const int page0 = __shfl_sync(0xffffffffu, pid[0], 0);
+    if (slot0 + S::kKeys <= c.page.d && j0 + S::kKeys <= k1 && page0 >= 0 && page0 < c.num_pages) {
+      // the whole tile in one page
+      const uint8_t* from = c.k + at(c.row, page0, slot0 + row0, g) + 16 * piece;
+      const uint8_t* from_v = from + v_minus_k;
+      const int64_t step = kRowsPer * c.row.slot;
 #pragma unroll
       for (int i = 0; i < S::kKeys / kRowsPer; ++i) {
-        const int row = i * kRowsPer + row0;
-        const int64_t o = __shfl_sync(0xffffffffu, off[kRpl > 1 ? (i * kRowsPer) / 32 : 0], row & 31);
-        const uint32_t a = dst + swz<S::kPieces>(row, piece);
-        const uint8_t* const from = c.k + (o < 0 ? 0 : o + 16 * piece);
-        cp_async_16(a, from, o < 0 ? 0 : 16);
-        cp_async_16(a + kDecTile / 2, from + v_minus_k, o < 0 ? 0 : 16);
+        cp16(at_row(i) + i * 512, from);
+        cp16(at_row(i) + i * 512 + kDecTile / 2, from_v);
+        from += step;
+        from_v += step;
       }
-    };
-
-    // ---- the first copies, then the queries, which all warps share
-    fetch_pid(warp);
 #pragma unroll
-    for (int s = 0; s < kDecStages - 1; ++s) {
-      const int t = warp + s * kDecWarps;
-      flush();
-      if (t < tiles) {
-        issue(t, s);
-        fetch_pid(t + kDecWarps);
+      for (int r = 0; r < kRpl; ++r) {
+        const int row = lane + 32 * r;
+        if (row < S::kKeys) {
+          if (kFp8) {
+            const int64_t e = at(c.exp, page0, slot0 + row, g);
+            pend_k[r] = c.k_exp[e];
+            pend_v[r] = c.v_exp[e];
+          }
+          if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, page0, slot0 + row, g));
+        }
       }
-      cp_commit();
+      return;
     }
-    for (int n = warp; n < S::kHeads; n += kDecWarps) {
-      constexpr int kPairs = D / 64;  // of a lane
-      uint32_t w[kPairs];
+    int64_t off[kRpl];
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k)
-        w[k] = n < heads ? reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + (int64_t)(g * p.G + h0 + n) * D)[lane + 32 * k] : 0u;
+    for (int r = 0; r < kRpl; ++r) {
+      const int row = lane + 32 * r, j = j0 + row;
+      off[r] = -1;
+      pend_k[r] = pend_v[r] = 127u;
+      if (row < S::kKeys && j < k1) {
+        const uint32_t slot = place_of(c, j).slot;
+        if (pid[r] < 0 || pid[r] >= c.num_pages) {
+          raise(p.status, THD_DEV_ERR_PAGE);
+        } else {
+          off[r] = at(c.row, pid[r], slot, g);
+          if (kFp8) {
+            const int64_t e = at(c.exp, pid[r], slot, g);
+            pend_k[r] = c.k_exp[e];
+            pend_v[r] = c.v_exp[e];
+          }
+          if (p.pos) cp_async_4(meta_a + S::kKeys * 8 + row * 4, p.pos + at(p.pos_at, pid[r], slot, g));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::kKeys / kRowsPer; ++i) {
+      const int row = i * kRowsPer + row0;
+      const int64_t o = __shfl_sync(0xffffffffu, off[kRpl > 1 ? (i * kRowsPer) / 32 : 0], row & 31);
+      const uint8_t* const from = c.k + (o < 0 ? 0 : o + 16 * piece);
+      cp16_if(at_row(i) + i * 512, from, o >= 0);
+      cp16_if(at_row(i) + i * 512 + kDecTile / 2, from + v_minus_k, o >= 0);
+    }
+  };
+
+  // ---- an item's queries: a warp takes every kDecWarps-th head
+  constexpr int kPairs = D / 64, kQHeads = S::kHeads / kDecWarps;  // of a lane, of a warp
+  uint32_t q_next[kQHeads][kPairs];
+  auto fetch_q = [&](const Segment& x) {
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i) {
+      const int n = warp + i * kDecWarps;
+      const uint32_t* const row = reinterpret_cast<const uint32_t*>(p.q + x.b * p.q_stride + (int64_t)(x.g * p.G + x.h0 + n) * D);
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) q_next[i][k] = x.h0 + n < p.G ? row[lane + 32 * k] : 0u;
+    }
+  };
+
+  Segment cur;
+  if (!next(cur)) return;
+  fetch_q(cur);
+  fetch_pid(cur, warp);
+  fetch_pid(cur, warp + kDecWarps);
+#pragma unroll
+  for (int x = 0; x < S::kStages; ++x) {
+    const int t = warp + x * kDecWarps;
+    flush();
+    if (cur.k0 + t * S::kKeys < cur.k1) issue(cur, t, x);
+    fetch_pid(cur, t + 2 * kDecWarps);
+    cp_commit();
+  }
+  int stage = 0;
+  for (;;) {
+    const int b = cur.b, g = cur.g, h0 = cur.h0, k0 = cur.k0, k1 = cur.k1;
+    const int heads = p.G - h0 < S::kHeads ? p.G - h0 : S::kHeads;
+    const int tiles = (k1 - k0 + S::kKeys - 1) / S::kKeys;
+    const int seen = p.slopes ? (p.seen ? p.seen[b] : c.kv_len[b]) : 0;
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i) {
+      const int n = warp + i * kDecWarps;
+      uint32_t(&w)[kPairs] = q_next[i];
       float mul = 1.f;
       if (kFp8) {
-        // two e4m3 numbers for each element, the second 32 times what the first's
-        // rounding left: the largest of a head is brought to [128, 256) by a
-        // power of two, then bf16's eight bits are kept whole down to 2^-15 of
-        // it, and what is smaller to 2^-22 of it
+        // fp16 queries: the largest of a head is brought to [2^14, 2^15) by a
+        // power of two, so elements down to 2^-28 of it keep bf16's precision
         uint32_t big = 0;
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) big = __vmaxu2(big, w[k] & 0x7fff7fffu);
@@ -401,7 +442,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         big = __reduce_max_sync(0xffffffffu, big);
         int e = (int)(big >> 7);                  // exponent field of the largest
         e = e == 0 ? 1 : e;
-        const int up = 127 + 7 - e;               // 2^up times the head; in two steps, each a normal number
+        const int up = 127 + 14 - e;              // 2^up times the head; in two steps, each a normal number
         const float m1 = __uint_as_float((uint32_t)(127 + up / 2) << 23);
         const float m2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
         mul = (1.f / m1) * (1.f / m2);
@@ -409,23 +450,20 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           const float lo = __uint_as_float(w[k] << 16) * m1 * m2, hi = __uint_as_float(w[k] & 0xffff0000u) * m1 * m2;
-          const uint32_t first = to_e4m3x2(lo, hi);
-          const int d = 2 * (lane + 32 * k), kp = d >> 5, in = d & 31;
-          uint8_t* const to = s_q + ((kp * NT + (n >> 3)) * 32 + (n & 7) * 4 + ((in & 15) >> 2)) * 16 + (in >> 4) * 4 + (in & 3);
-          *reinterpret_cast<uint16_t*>(to) = (uint16_t)first;
-          *reinterpret_cast<uint16_t*>(to + 8) = (uint16_t)rest_of(lo, hi, first);
+          w[k] = pack2<true>(lo, hi);
         }
-      } else {
+      }
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-          const int d = 2 * (lane + 32 * k), ks = d >> 4, in = d & 15;
-          // fragment order of the matrix instruction's second operand
-          *reinterpret_cast<uint32_t*>(s_q + ((((ks * NT + (n >> 3)) * 32 + (n & 7) * 4 + ((in & 7) >> 1)) * 2 + (in >> 3)) * 4)) = w[k];
-        }
+      for (int k = 0; k < kPairs; ++k) {
+        const int d = 2 * (lane + 32 * k), ks = d >> 4, in = d & 15;
+        // fragment order of the matrix instruction's second operand; next to
+        // e4m3 keys a step's elements are counted as the keys' bytes arrive
+        const int reg = kFp8 ? (in & 3) >> 1 : in >> 3, quad = kFp8 ? in >> 2 : (in & 7) >> 1;
+        *reinterpret_cast<uint32_t*>(s_q + ((((ks * NT + (n >> 3)) * 32 + (n & 7) * 4 + quad) * 2 + reg) * 4)) = w[k];
       }
       if (lane == 0) {
         s_hs[n] = mul * (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e);
-        s_sl[n] = p.slopes && n < heads ? p.slopes[g * p.G + h0 + n] * kLog2e : 0.f;
+        s_sl[n] = p.slopes && n < heads ? p.slopes[cur.g * p.G + cur.h0 + n] * kLog2e : 0.f;
       }
     }
     __syncthreads();
@@ -437,288 +475,257 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
 
     // ---- tiles: running maximum (base 2) m and sum l of each head, O^T
     // mo: the maximum of score + log2 of the value's scale, what O is relative to
-    // o2: the sum over the probabilities' second numbers, 32 times as large
-    // base: m, or 0 while there is none
-    float m[NT][2], mo[NT][2], l[NT][2], base[NT][2], up[NT][2], o[D / 16][NT][4], o2[S::kPv8 ? D / 16 : 1][NT][4];
+    // nbase: -m, or 0 while there is none; up: from a probability times its value's
+    // scale to what the product takes
+    float m[NT][2], mo[NT][2], l[NT][2], nbase[NT][2], up[NT][2], o[D / 16][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = mo[nt][e] = -INFINITY, l[nt][e] = base[nt][e] = up[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) m[nt][e] = mo[nt][e] = -INFINITY, l[nt][e] = nbase[nt][e] = up[nt][e] = 0.f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][nt][e] = o2[S::kPv8 ? d : 0][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
 
-    int stage = 0;
     for (int t = warp; t < tiles; t += kDecWarps) {
-      cp_wait<kDecStages - 2>();
+      cp_wait<S::kStages - 1>();
       __syncwarp();
-      const uint32_t kt = ring_a + stage * kDecTile, vt = kt + kDecTile / 2;
-      const float2* const scales = reinterpret_cast<const float2*>(meta + stage * 12 * S::kKeys);
-      const uint32_t* const numbers = reinterpret_cast<const uint32_t*>(meta + stage * 12 * S::kKeys + 8 * S::kKeys);
-      float s[S::kSub][NT][4];
+#pragma unroll 1
+      for (int r0 = 0; r0 < S::kKeys && k0 + t * S::kKeys + r0 < k1; r0 += 16 * S::kStep) {  // rows of the tile at a time
+        const float2* const scales = reinterpret_cast<const float2*>(meta + stage * 12 * S::kKeys) + r0;
+        const uint32_t* const numbers = reinterpret_cast<const uint32_t*>(meta + stage * 12 * S::kKeys + 8 * S::kKeys) + r0;
+        float s[S::kStep][NT][4];
 #pragma unroll
-      for (int sub = 0; sub < S::kSub; ++sub)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[sub][nt][e] = 0.f;
-      // lanes' rows and pieces of the four 8x8 matrices of a load: rows 0-7 and
-      // 8-15 of the first 16 bytes, then of the second
-      const int lrow = lane & 15, lpc = lane >> 4;
-      if (kFp8) {
-#pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub) {
-          float rest[NT][4];
+        for (int sub = 0; sub < S::kStep; ++sub)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rest[nt][e] = 0.f;
-#pragma unroll
-          for (int kp = 0; kp < S::kPieces / 2; ++kp) {
-            uint32_t r[4];
-            ldsm4(r, kt + swz<S::kPieces>(sub * 16 + lrow, 2 * kp + lpc));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint4 bq = *reinterpret_cast<const uint4*>(s_q + ((kp * NT + nt) * 32 + lane) * 16);
-              mma16832(s[sub][nt], r, bq.x, bq.y);
-              mma16832(rest[nt], r, bq.z, bq.w);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[sub][nt][e] = fmaf(rest[nt][e], 1.f / 32, s[sub][nt][e]);
-        }
-      } else {
+            for (int e = 0; e < 4; ++e) s[sub][nt][e] = 0.f;
+        // lanes' rows and pieces of a load's four 8x8 matrices: rows 0-7 and 8-15
+        // of the first 16 bytes, then of the second; of bf16 values, which are
+        // loaded transposed, the two pieces of rows 0-7, then of rows 8-15
+        constexpr int kSubBytes = 16 * S::kRow;
+        const uint32_t tile_a = ring_a + stage * kDecTile + r0 * S::kRow;
+        const uint32_t kt = tile_a + swz<S::kPieces>(lane & 15, lane >> 4);
+        const uint32_t vt = kFp8 ? kt : tile_a + swz<S::kPieces>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+        constexpr int kSteps = kFp8 ? 2 : 1;  // steps of 16 elements in 32 bytes
 #pragma unroll
         for (int kp = 0; kp < S::kPieces / 2; ++kp) {
-          uint2 bq[NT];
+          uint2 bq[kSteps][NT];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) bq[nt] = *reinterpret_cast<const uint2*>(s_q + ((kp * NT + nt) * 32 + lane) * 8);
+          for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-          for (int sub = 0; sub < S::kSub; ++sub) {
+            for (int nt = 0; nt < NT; ++nt)
+              bq[x][nt] = *reinterpret_cast<const uint2*>(s_q + (((kp * kSteps + x) * NT + nt) * 32 + lane) * 8);
+#pragma unroll
+          for (int sub = 0; sub < S::kStep; ++sub) {
             uint32_t r[4];
-            ldsm4(r, kt + swz<S::kPieces>(sub * 16 + lrow, 2 * kp + lpc));
+            ldsm4(r, (kt ^ (kp << 5)) + sub * kSubBytes);
+            if (kFp8) {
+              const uint32_t a0[4] = {e4m3x2(r[0]), e4m3x2(r[1]), e4m3x2(r[0] >> 16), e4m3x2(r[1] >> 16)};
+              const uint32_t a1[4] = {e4m3x2(r[2]), e4m3x2(r[3]), e4m3x2(r[2] >> 16), e4m3x2(r[3] >> 16)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[sub][nt], r, bq[nt].x, bq[nt].y);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816<true>(s[sub][nt], a0, bq[0][nt].x, bq[0][nt].y);
+                mma16816<true>(s[sub][nt], a1, bq[kSteps - 1][nt].x, bq[kSteps - 1][nt].y);
+              }
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[sub][nt], r, bq[0][nt].x, bq[0][nt].y);
+            }
           }
         }
-      }
-      // scores in base 2
-      const int j0 = k0 + t * S::kKeys;
-      float lv[S::kSub][2];  // log2 of the values' scales
+        // scores in base 2
+        const int j0 = k0 + t * S::kKeys + r0;
+        float lv[S::kStep][2];  // log2 of the values' scales
 #pragma unroll
-      for (int sub = 0; sub < S::kSub; ++sub)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float2 sc;
-          if (kFp8) {
-            sc = scales[sub * 16 + half * 8 + gid];
-            lv[sub][half] = sc.y;
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float &y0 = s[sub][nt][2 * half], &y1 = s[sub][nt][2 * half + 1];
-            if (kFp8) fmul2(y0, y1, y0, y1, sc.x, sc.x);
-            fmul2(y0, y1, y0, y1, hs[nt][0], hs[nt][1]);
-          }
-        }
-      if (p.cap > 0.f) {
-#pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[sub][nt][e] = p.cap * kLog2e * tanhf(s[sub][nt][e]);
-      }
-      if (p.slopes) {
-#pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub)
+        for (int sub = 0; sub < S::kStep; ++sub)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int row = sub * 16 + half * 8 + gid;
-            const float far = (float)(int)((uint32_t)seen - 1u - (p.pos ? numbers[row] : (uint32_t)(j0 + row)));
+            float2 sc;
+            if (kFp8) {
+              sc = scales[sub * 16 + half * 8 + gid];
+              lv[sub][half] = sc.y;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float &y0 = s[sub][nt][2 * half], &y1 = s[sub][nt][2 * half + 1];
+              if (kFp8) fmul2(y0, y1, y0, y1, sc.x, sc.x);
+              fmul2(y0, y1, y0, y1, hs[nt][0], hs[nt][1]);
+            }
+          }
+        if (p.cap > 0.f) {
+#pragma unroll
+          for (int sub = 0; sub < S::kStep; ++sub)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) s[sub][nt][2 * half + e] = fmaf(-sl[nt][e], far, s[sub][nt][2 * half + e]);
-          }
-      }
-      if (j0 + S::kKeys > k1) {  // slots behind the last
+              for (int e = 0; e < 4; ++e) s[sub][nt][e] = p.cap * kLog2e * tanhf(s[sub][nt][e]);
+        }
+        if (p.slopes) {
 #pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub)
+          for (int sub = 0; sub < S::kStep; ++sub)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if (j0 + sub * 16 + half * 8 + gid >= k1) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) s[sub][nt][2 * half] = s[sub][nt][2 * half + 1] = -INFINITY;
-            }
-      }
-      if (p.weight_out) {
-#pragma unroll
-        for (int sub = 0; sub < S::kSub; ++sub)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int j = j0 + sub * 16 + half * 8 + gid;
-            if (j < k1) {
-              float* const to = p.scores + (((int64_t)b * c.Hkv + g) * c.capacity + j) * p.G + h0 + 2 * t4;
+            for (int half = 0; half < 2; ++half) {
+              const int row = sub * 16 + half * 8 + gid;
+              const float far = (float)(int)((uint32_t)seen - 1u - (p.pos ? numbers[row] : (uint32_t)(j0 + row)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (nt * 8 + 2 * t4 + e < heads) to[nt * 8 + e] = s[sub][nt][2 * half + e];
+                for (int e = 0; e < 2; ++e) s[sub][nt][2 * half + e] = fmaf(-sl[nt][e], far, s[sub][nt][2 * half + e]);
             }
-          }
-      }
-      // The maximum moves only when a score passes it by more than kSlack: until
-      // then the lanes need not know one another's scores.  (Probabilities then
-      // reach 2^kSlack: any bf16 or fp32 does, 256 * 1.7 is an e4m3 number, 256 an fp16.)
-      constexpr float kSlack = S::kPv8 ? 0.75f : 8.f;
-      float mx[NT][2], mxo[NT][2];
-      bool moved = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = mxo[nt][e] = -INFINITY;
-#pragma unroll
-          for (int sub = 0; sub < S::kSub; ++sub) {
-            mx[nt][e] = fmax3(mx[nt][e], s[sub][nt][e], s[sub][nt][2 + e]);
-            if (kFp8) mxo[nt][e] = fmax3(mxo[nt][e], s[sub][nt][e] + lv[sub][0], s[sub][nt][2 + e] + lv[sub][1]);
-          }
-          moved |= mx[nt][e] > m[nt][e] + kSlack;
-          if (kFp8) moved |= mxo[nt][e] > mo[nt][e] + kSlack;
         }
-      if (__any_sync(0xffffffffu, moved)) {
+        if (j0 + 16 * S::kStep > k1) {  // slots behind the last
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float al[2], alo[2];
+          for (int sub = 0; sub < S::kStep; ++sub)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (j0 + sub * 16 + half * 8 + gid >= k1) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[sub][nt][2 * half] = s[sub][nt][2 * half + 1] = -INFINITY;
+              }
+        }
+        if (p.weight_out) {
+#pragma unroll
+          for (int sub = 0; sub < S::kStep; ++sub)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int j = j0 + sub * 16 + half * 8 + gid;
+              if (j < k1) {
+                float* const to = p.scores + (((int64_t)b * c.Hkv + g) * c.capacity + j) * p.G + h0 + 2 * t4;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (nt * 8 + 2 * t4 + e < heads) to[nt * 8 + e] = s[sub][nt][2 * half + e];
+              }
+            }
+        }
+        // The maximum moves only when a score passes it by more than kSlack: until
+        // then the lanes need not know one another's scores.  Probabilities then
+        // reach 2^8, which any bf16, fp16 or fp32 sum takes.
+        float mx[NT][2], mxo[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            mx[nt][e] = mxo[nt][e] = -INFINITY;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-              if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], __shfl_xor_sync(0xffffffffu, mxo[nt][e], d));
+            for (int sub = 0; sub < S::kStep; ++sub) {
+              mx[nt][e] = fmax3(mx[nt][e], s[sub][nt][e], s[sub][nt][2 + e]);
+              if (kFp8) mxo[nt][e] = fmax3(mxo[nt][e], s[sub][nt][e] + lv[sub][0], s[sub][nt][2 + e] + lv[sub][1]);
             }
-            const float m2 = fmaxf(m[nt][e], mx[nt][e]);
-            al[e] = m2 > m[nt][e] ? ex2(m[nt][e] - m2) : 1.f;
-            m[nt][e] = m2;
-            base[nt][e] = m2 == -INFINITY ? 0.f : m2;
-            alo[e] = al[e];
-            if (kFp8) {
-              const float o2m = fmaxf(mo[nt][e], mxo[nt][e]);
-              alo[e] = o2m > mo[nt][e] ? ex2(mo[nt][e] - o2m) : 1.f;
-              mo[nt][e] = o2m;
-              // from a probability times the value's scale to what the product takes
-              up[nt][e] = ex2(base[nt][e] - (o2m == -INFINITY ? 0.f : o2m) + (S::kPv8 ? 8.f : 0.f));
-            }
-            l[nt][e] *= al[e];
+            moved |= mx[nt][e] > m[nt][e] + kSlack;
+            if (kFp8) moved |= mxo[nt][e] > mo[nt][e] + kSlack;
           }
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            fmul2(o[d][nt][0], o[d][nt][1], o[d][nt][0], o[d][nt][1], alo[0], alo[1]);
-            fmul2(o[d][nt][2], o[d][nt][3], o[d][nt][2], o[d][nt][3], alo[0], alo[1]);
-            if (S::kPv8) {
-              float(&x)[4] = o2[S::kPv8 ? d : 0][nt];
-              fmul2(x[0], x[1], x[0], x[1], alo[0], alo[1]);
-              fmul2(x[2], x[3], x[2], x[3], alo[0], alo[1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float al[2], alo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) {
+                mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+                if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], __shfl_xor_sync(0xffffffffu, mxo[nt][e], d));
+              }
+              const float m2 = fmaxf(m[nt][e], mx[nt][e]);
+              al[e] = m2 > m[nt][e] ? ex2(m[nt][e] - m2) : 1.f;
+              m[nt][e] = m2;
+              nbase[nt][e] = m2 == -INFINITY ? 0.f : -m2;
+              alo[e] = al[e];
+              if (kFp8) {
+                const float o2m = fmaxf(mo[nt][e], mxo[nt][e]);
+                alo[e] = o2m > mo[nt][e] ? ex2(mo[nt][e] - o2m) : 1.f;
+                mo[nt][e] = o2m;
+                up[nt][e] = ex2(kRaise - nbase[nt][e] - (o2m == -INFINITY ? 0.f : o2m));
+              }
+              l[nt][e] *= al[e];
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              fmul2(o[d][nt][0], o[d][nt][1], o[d][nt][0], o[d][nt][1], alo[0], alo[1]);
+              fmul2(o[d][nt][2], o[d][nt][3], o[d][nt][2], o[d][nt][3], alo[0], alo[1]);
             }
           }
         }
-      }
-      // probabilities: summed in fp32, and for the product rounded as bf16 next
-      // to bf16 values (2^-8, as the packed kernels do), next to e4m3 ones as
-      // fp16 (2^-11) or as two e4m3 numbers (2^-8, and 2^-23 of the largest)
-      uint32_t pb[S::kSub][NT][2];
+          // probabilities: summed in fp32, and for the product rounded to bf16 next
+        // to bf16 values (2^-8, as the packed kernels do), to fp16 next to e4m3
+        // ones (2^-11, and 2^-32 of the largest)
+        uint32_t pb[S::kStep][NT][2];
 #pragma unroll
-      for (int sub = 0; sub < S::kSub; ++sub) {
-        float vs[2];
-        if (kFp8) vs[0] = ex2(lv[sub][0]), vs[1] = ex2(lv[sub][1]);
+        for (int sub = 0; sub < S::kStep; ++sub) {
+          float vs[2];
+          if (kFp8) vs[0] = ex2(lv[sub][0]), vs[1] = ex2(lv[sub][1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[2][2];
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[2][2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float y0, y1;
-            fadd2(y0, y1, s[sub][nt][2 * half], s[sub][nt][2 * half + 1], -base[nt][0], -base[nt][1]);
-            y0 = ex2(y0);
-            y1 = ex2(y1);
-            fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], y0, y1);
-            if (kFp8) {
-              fmul2(y0, y1, y0, y1, vs[half], vs[half]);
-              fmul2(y0, y1, y0, y1, up[nt][0], up[nt][1]);
+            for (int half = 0; half < 2; ++half) {
+              float y0, y1;
+              fadd2(y0, y1, s[sub][nt][2 * half], s[sub][nt][2 * half + 1], nbase[nt][0], nbase[nt][1]);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], y0, y1);
+              if (kFp8) {
+                fmul2(y0, y1, y0, y1, vs[half], vs[half]);
+                fmul2(y0, y1, y0, y1, up[nt][0], up[nt][1]);
+              }
+              w[half][0] = y0;
+              w[half][1] = y1;
             }
-            w[half][0] = y0;
-            w[half][1] = y1;
-          }
-          if (S::kPv8) {
-            // a register has a head's slots gid and gid + 8 side by side
-            const uint32_t a0 = to_e4m3x2(w[0][0], w[1][0]), a1 = to_e4m3x2(w[0][1], w[1][1]);
-            pb[sub][nt][0] = movm_t(a0 | a1 << 16);
-            pb[sub][nt][1] = movm_t(rest_of(w[0][0], w[1][0], a0) | rest_of(w[0][1], w[1][1], a1) << 16);
-          } else {
             pb[sub][nt][0] = movm_t(pack2<kFp8>(w[0][0], w[0][1]));
             pb[sub][nt][1] = movm_t(pack2<kFp8>(w[1][0], w[1][1]));
           }
         }
-      }
-      // O^T += V^T P^T
+        // O^T += V^T P^T
 #pragma unroll
-      for (int dp = 0; dp < S::kPieces / 2; ++dp)
+        for (int dp = 0; dp < S::kPieces / 2; ++dp)
 #pragma unroll
-        for (int sub = 0; sub < S::kSub; sub += S::kPv8 ? 2 : 1) {
-          uint32_t r[4];
-          if (S::kPv8) {
-            // matrices: slots 0-7 and 8-15 of 16 elements, then of the next 16;
-            // a register has elements 2 gid and 2 gid + 1 of two slots; a step
-            // of 32 slots counts them as the probabilities' registers do
-            uint32_t r2[4];
-            ldsm4t(r, vt + swz<S::kPieces>(sub * 16 + lrow, 2 * dp + lpc));
-            ldsm4t(r2, vt + swz<S::kPieces>(sub * 16 + 16 + lrow, 2 * dp + lpc));
+          for (int sub = 0; sub < S::kStep; ++sub) {
+            uint32_t r[4];
+            if (kFp8) {
+              // matrices: slots 0-7 and 8-15 of 16 elements, then of the next 16;
+              // a register has elements 2 gid and 2 gid + 1 of two slots
+              ldsm4t(r, (vt ^ (dp << 5)) + kDecTile / 2 + sub * kSubBytes);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t a[4] = {__byte_perm(r[2 * x], r[2 * x + 1], 0x6240), __byte_perm(r[2 * x], r[2 * x + 1], 0x7351),
-                                     __byte_perm(r2[2 * x], r2[2 * x + 1], 0x6240), __byte_perm(r2[2 * x], r2[2 * x + 1], 0x7351)};
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t y0 = __byte_perm(r[2 * x], 0, 0x3120), y1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                const uint32_t a[4] = {e4m3x2(y0), e4m3x2(y0 >> 16), e4m3x2(y1), e4m3x2(y1 >> 16)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                constexpr int kNext = S::kPv8 ? 1 : 0;
-                mma16832(o[(S::kPv8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][0], pb[sub + kNext][nt][0]);
-                mma16832(o2[(S::kPv8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][1], pb[sub + kNext][nt][1]);
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<true>(o[(kFp8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][0], pb[sub][nt][1]);
               }
+            } else {
+              ldsm4t(r, (vt ^ (dp << 5)) + kDecTile / 2 + sub * kSubBytes);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[dp][nt], r, pb[sub][nt][0], pb[sub][nt][1]);
             }
-          } else if (kFp8) {
-            ldsm4t(r, vt + swz<S::kPieces>(sub * 16 + lrow, 2 * dp + lpc));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t y0 = __byte_perm(r[2 * x], 0, 0x3120), y1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-              const uint32_t a[4] = {e4m3x2(y0), e4m3x2(y0 >> 16), e4m3x2(y1), e4m3x2(y1 >> 16)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(o[(kFp8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][0], pb[sub][nt][1]);
-            }
-          } else {
-            // matrices: elements 0-7 and 8-15 of slots 0-7, then of slots 8-15
-            ldsm4t(r, vt + swz<S::kPieces>(sub * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * dp + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[dp][nt], r, pb[sub][nt][0], pb[sub][nt][1]);
           }
-        }
+      }
       __syncwarp();  // the stage is read
       flush();
-      const int tn = t + (kDecStages - 1) * kDecWarps;
+      const int tn = t + S::kStages * kDecWarps;
       if (tn < tiles) {
-        int ns = stage + kDecStages - 1;
-        ns = ns >= kDecStages ? ns - kDecStages : ns;
-        issue(tn, ns);
-        fetch_pid(tn + kDecWarps);
+        issue(cur, tn, stage);
+        fetch_pid(cur, tn + 2 * kDecWarps);
       }
       cp_commit();
-      stage = stage + 1 == kDecStages ? 0 : stage + 1;
+      stage ^= 1;
     }
-    cp_wait<0>();
+
+    // ---- what the next item begins with is on its way during this one's end:
+    // its queries, its pages and the warp's first tile, into the stage that is free
+    Segment after;
+    const bool more = next(after);
+    if (more) {
+      fetch_q(after);
+      fetch_pid(after, warp);
+      fetch_pid(after, warp + kDecWarps);
+    }
 
     // ---- the item's end: the warps' sums, then their O, through shared memory
 #pragma unroll
@@ -734,8 +741,17 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
           to[2 * S::kHeads] = l[nt][e];
         }
       }
+    // the warp's part of O goes through the other stage (or both)
+    if (lane == 0) s_at[warp] = S::kAhead ? (stage ^ 1) * kDecTile : 0;
     __syncthreads();
-    float* const mine = reinterpret_cast<float*>(ring);
+    float* const mine = reinterpret_cast<float*>(ring + s_at[warp]);
+    if (S::kAhead) {
+      if (more) {
+        if (after.k0 + warp * S::kKeys < after.k1) issue(after, warp, stage);
+        fetch_pid(after, warp + 2 * kDecWarps);
+      }
+      cp_commit();
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[2];
@@ -745,26 +761,27 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 3 * S::kHeads + nt * 8 + 2 * t4 + e]);
         f[e] = top == -INFINITY ? 1.f : ex2((kFp8 ? mo[nt][e] : m[nt][e]) - top);
-        if (S::kPv8) f[e] *= 1.f / 256;
+        if (kFp8) f[e] *= 1.f / 128;
       }
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int at_d = d * 16 + (kFp8 ? 2 * gid + (e >> 1) : gid + 8 * (e >> 1));
-          mine[(nt * 8 + 2 * t4 + (e & 1)) * S::kPitch + at_d] =
-              (S::kPv8 ? fmaf(o2[S::kPv8 ? d : 0][nt][e], 1.f / 32, o[d][nt][e]) : o[d][nt][e]) * f[e & 1];
+          const int n = nt * 8 + 2 * t4 + (e & 1);
+          mine[n * D + (at_d ^ (n >> 1 & 3) << 3)] =  // eight words apart for the four lanes of a row
+              o[d][nt][e] * f[e & 1];
         }
     }
     __syncthreads();
-    const bool whole = take == units;
-    if (tid == 0 && !whole && i0 + take == units) {
+    const bool whole = cur.i0 == 0 && cur.last;
+    if (tid == 0 && !whole && cur.last) {
       // the item's last block names its parts: the first block's is in that
       // one's second slot, the others' in their first
-      const int64_t first = owner_of(u - ic + kLead, total, blocks);
+      const int64_t first = owner_of(cur.at + kLead, total, blocks);
       p.joins[blockIdx.x] = DecodeJoin{b, g * p.G + h0, heads, (int)first, (int)(blockIdx.x - first) + 1};
     }
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (i0 > 0 ? 0 : 1);
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.i0 > 0 ? 0 : 1);
     for (int i = tid; i < heads * (D / 4); i += kDecThreads) {
       const int n = i / (D / 4), d = 4 * (i % (D / 4));
       float top = -INFINITY, topo = -INFINITY, sum = 0.f;
@@ -781,7 +798,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * S::kRing + (n * S::kPitch + d) * 4);
+        const float4 y = *reinterpret_cast<const float4*>(smem + w * S::kRing + s_at[w] + (n * D + (d ^ (n >> 1 & 3) << 3)) * 4);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
       if (whole) {
@@ -804,8 +821,17 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const DecodeParams 
         }
       }
     }
-    advance();
+    if (!more) return;
     __syncthreads();  // the rings are read
+    cur = after;
+#pragma unroll
+    for (int x = S::kAhead ? 1 : 0; x < S::kStages; ++x) {
+      const int t = warp + x * kDecWarps;
+      flush();
+      if (cur.k0 + t * S::kKeys < cur.k1) issue(cur, t, stage ^ x);
+      fetch_pid(cur, t + 2 * kDecWarps);
+      cp_commit();
+    }
   }
 }
 
@@ -821,12 +847,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   __shared__ float4 s_x[kJoinThreads];
   __shared__ float s_ml[kDecodeMaxGrid][3], s_top[kJoinThreads / 32][2], s_sum[kParts];
   const int tid = threadIdx.x, n = blockIdx.y;
-  grid_dep_launch();
-  grid_dep_wait();
+  follow();
+  depend();
   const DecodeJoin j = p.joins[blockIdx.x];
   if (j.count == 0 || n >= j.heads) return;
   // part k's row
   auto row_of = [&](int k) { return (2 * (int64_t)(j.first + k) + (k == 0 ? 1 : 0)) * kheads + n; };
+  // the first rows are on their way while the maxima are found
+  constexpr int kAhead = 8;
+  const int lane = tid % kLanes, mine = tid / kLanes;
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (mine + i * kParts < j.count)
+      ahead[i] = *reinterpret_cast<const float4*>(p.part + row_of(mine + i * kParts) * D + 4 * lane);
   float topo = -INFINITY, top = -INFINITY;
   for (int k = tid; k < j.count; k += kJoinThreads) {
     const float* ml = p.part_ml + row_of(k) * 3;
@@ -844,16 +878,19 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) topo = fmaxf(topo, s_top[w][0]), top = fmaxf(top, s_top[w][1]);
   const float base = top == -INFINITY ? 0.f : top, baseo = topo == -INFINITY ? 0.f : topo;
-  const int lane = tid % kLanes, mine = tid / kLanes;
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = mine; k < j.count; k += kParts) {
-    const float4 y = *reinterpret_cast<const float4*>(p.part + row_of(k) * D + 4 * lane);
+  auto add = [&](int k, const float4& y) {
     const float f = ex2(s_ml[k][0] - baseo);
     sum += s_ml[k][2] * ex2(s_ml[k][1] - base);
     acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (mine + i * kParts < j.count) add(mine + i * kParts, ahead[i]);
+#pragma unroll 8
+  for (int k = mine + kAhead * kParts; k < j.count; k += kParts)
+    add(k, *reinterpret_cast<const float4*>(p.part + row_of(k) * D + 4 * lane));
   s_x[tid] = acc;
   if (lane == 0) s_sum[mine] = sum;
   __syncthreads();
@@ -890,7 +927,8 @@ __global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const De
   __shared__ float s_lse[kDecodeMaxGroup];
   const CacheView& c = p.c;
   const int tid = threadIdx.x;
-  grid_dep_wait();
+  follow();
+  depend();
   const int64_t all = p.units[c.B] * c.Hkv;
   int64_t u = blockIdx.x * all / gridDim.x;
   const int64_t u_end = (blockIdx.x + 1) * all / gridDim.x;
@@ -962,20 +1000,20 @@ __global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const De
 
 // ------------------------------------------------------------------ launch
 template <bool kFp8, int D, int NT>
-static cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
+static cudaError_t launch_decode_t(DecodeParams& p, cudaStream_t st) {
   using S = DecShape<kFp8, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<kFp8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
+  int grid = S::kPerSm * num_sms();  // one wave
+  p.grid = grid > kDecodeMaxGrid ? kDecodeMaxGrid : grid;
   prof_before(THD_KERNEL_DECODE, st);
-  decode_kernel<kFp8, D, NT><<<p.grid, kDecThreads, S::kSmem, st>>>(p);
-  count_launch();
-  e = cudaGetLastError();
+  e = launch_following(decode_kernel<kFp8, D, NT>, dim3((unsigned)p.grid), kDecThreads, S::kSmem, st, MPDL, (const DecodeParams)p);
   prof_after(THD_KERNEL_DECODE, st);
   return e;
 }
 
 template <bool kFp8>
-static cudaError_t launch_decode_d(const DecodeParams& p, int heads, cudaStream_t st) {
+static cudaError_t launch_decode_d(DecodeParams& p, int heads, cudaStream_t st) {
   if (p.c.D == 64)
     return heads == 8 ? launch_decode_t<kFp8, 64, 1>(p, st)
                       : heads == 16 ? launch_decode_t<kFp8, 64, 2>(p, st) : launch_decode_t<kFp8, 64, 4>(p, st);
@@ -985,34 +1023,18 @@ static cudaError_t launch_decode_d(const DecodeParams& p, int heads, cudaStream_
 
 cudaError_t launch_decode(DecodeParams p, cudaStream_t st) {
   const int heads = decode_heads(p.G);
-  int64_t grid = 2LL * num_sms();  // two blocks an SM, one wave
-  if (grid > kDecodeMaxGrid) grid = kDecodeMaxGrid;
-  p.grid = (int)grid;
   cudaError_t e = p.c.k_exp ? launch_decode_d<true>(p, heads, st) : launch_decode_d<false>(p, heads, st);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (p.c.capacity > kUnit) {  // an item of one unit is one block's
-    cfg.gridDim = dim3((unsigned)p.grid, (unsigned)heads);
-    cfg.blockDim = dim3(kJoinThreads);
     prof_before(THD_KERNEL_DECODE_JOIN, st);
-    e = p.c.D == 64 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p, heads)
-                    : cudaLaunchKernelEx(&cfg, decode_join_kernel<128>, p, heads);
-    count_launch();
+    e = launch_following(p.c.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
+                         dim3((unsigned)p.grid, (unsigned)heads), kJoinThreads, 0, st, 1, (const DecodeParams)p, (int)heads);
     prof_after(THD_KERNEL_DECODE_JOIN, st);
     if (e != cudaSuccess) return e;
   }
   if (p.weight_out) {
-    cfg.gridDim = dim3((unsigned)(8 * num_sms()));
-    cfg.blockDim = dim3(kWeightThreads);
     prof_before(THD_KERNEL_DECODE_WEIGHTS, st);
-    e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, p);
-    count_launch();
+    e = launch_following(decode_weights_kernel, dim3((unsigned)(8 * num_sms())), kWeightThreads, 0, st, 1, (const DecodeParams)p);
     prof_after(THD_KERNEL_DECODE_WEIGHTS, st);
   }
   return e;
