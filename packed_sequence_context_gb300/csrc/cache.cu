@@ -159,18 +159,18 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
 // One cluster of `share` blocks an item (sequence, kv head).  Every block holds
 // its part of the slots' weights in shared memory as integers of the same
 // order (protected slots on top), so they are read once; the budget-th largest
-// is found by its digits (11, 11 and 10 bits, a histogram each, added up over
-// the cluster through distributed shared memory), ties and the slots to move are
-// numbered by ballots and counts, and the cluster's blocks then move rows.  Kept
+// is found by its four 8-bit digits (a histogram each, added up over the cluster
+// through distributed shared memory), ties and the slots to move are numbered by
+// counts and ballots, and the cluster's blocks then move rows.  Kept
 // slots in front of the budget stay where they are and evicted ones there take
 // the kept ones behind it, in order: the fewest bytes that can move, sources
 // (behind) and targets (in front) that never meet, and nothing to wait for
 // between them.
 namespace cg = cooperative_groups;
 
-constexpr int kEvictThreads = 256;
+constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kEvictMaxHeld = 40960;  // keys in a block's shared memory (160 KB)
 
 __device__ inline uint32_t order_of(float w, bool kept) {
@@ -180,11 +180,12 @@ __device__ inline uint32_t order_of(float w, bool kept) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t s_key[];  // [held]
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_scan[kEvictWarps], s_cnt[kEvictWarps][2];
-  __shared__ uint32_t s_digit, s_left, s_sum[3];  // this block's equal slots, holes, movers
+  __shared__ uint32_t s_hist[kBins], s_scan[kBins / 32];
+  __shared__ uint32_t s_digit, s_left;
+  // larger and equal keys in front of the budget and behind it: a warp's, a block's
+  __shared__ uint4 s_cnt[kEvictWarps], s_sum;
   const CacheView& c = p.c;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)(blockIdx.x % p.share), item = (int)(blockIdx.x / p.share);
@@ -229,167 +230,215 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   };
   {
     const int m = hi - lo < p.held ? hi - lo : p.held;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < m; i += kEvictThreads) s_key[i] = read_key(lo + i);
   }
   auto key = [&](int i) { return i - lo < p.held ? s_key[i - lo] : read_key(i); };
 
   // the budget-th largest, digit by digit
   uint32_t prefix = 0, mask = 0, left = (uint32_t)p.budget;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
-    for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = 0;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < kBins) s_hist[tid] = 0;
     __syncthreads();
     for (int i0 = lo; i0 < hi; i0 += kEvictThreads) {
       const int i = i0 + tid;
       const uint32_t k = i < hi ? key(i) : 0u;
       const bool in = i < hi && (k & mask) == prefix;
-      const uint32_t d = (k >> shift) & digits;
-      // a warp of equals (protected slots, tokens nobody looked at) adds once
-      const uint32_t act = __ballot_sync(0xffffffffu, in);
-      if (act) {
-        const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(act) - 1);
-        if (__all_sync(0xffffffffu, !in || d == d0)) {
-          if (lane == 0) atomicAdd(&s_hist[d0], (uint32_t)__popc(act));
-        } else if (in) {
-          atomicAdd(&s_hist[d], 1u);
-        }
-      }
+      const uint32_t d = (k >> shift) & (kBins - 1);
+      if (!__any_sync(0xffffffffu, in)) continue;
+      // equals in a warp add once
+      const uint32_t same = __match_any_sync(0xffffffffu, in ? d : 0xffffffffu);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[d], (uint32_t)__popc(same));
     }
     cluster.sync();
-    uint32_t mine[kBins / kEvictThreads], sum = 0;
-    const int first = kBins - (tid + 1) * (kBins / kEvictThreads);  // thread 0 has the top bins
+    uint32_t mine = 0, inc = 0;
+    const int bin = kBins - 1 - tid;  // thread 0 has the top one
+    if (tid < kBins) {
+#pragma unroll 8
+      for (int r = 0; r < p.share; ++r) mine += cluster.map_shared_rank(s_hist, r)[bin];
+      inc = mine;
 #pragma unroll
-    for (int k = 0; k < kBins / kEvictThreads; ++k) mine[k] = 0;
-    for (int r = 0; r < p.share; ++r) {
-      const uint32_t* h = cluster.map_shared_rank(s_hist, r) + first;
-#pragma unroll
-      for (int k = 0; k < kBins / kEvictThreads; ++k) mine[k] += h[k];
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      if (lane == 31) s_scan[warp] = inc;
     }
-#pragma unroll
-    for (int k = 0; k < kBins / kEvictThreads; ++k) sum += mine[k];
-    uint32_t inc = sum;
+    __syncthreads();
+    if (tid < kBins) {
+      for (int w = 0; w < warp; ++w) inc += s_scan[w];
+      if (inc - mine < left && left <= inc) {
+        s_digit = (uint32_t)bin;
+        s_left = left - (inc - mine);
+      }
+    }
+    cluster.sync();  // also: every block has read the histograms
+    prefix |= s_digit << shift;
+    mask |= (uint32_t)(kBins - 1) << shift;
+    left = s_left;
+  }
+  // Kept: keys above `prefix`, and the first `left` slots equal to it.  Every warp
+  // counts both kinds in its slots, in front of the budget and behind it; which
+  // of the equal ones stay follows from how many there are in front, and with
+  // that how many slots each warp has to give and to take.
+  const int part = ((hi - lo + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;  // a warp's slots
+  const int wlo = lo + warp * part < hi ? lo + warp * part : hi, whi = wlo + part < hi ? wlo + part : hi;
+  {
+    uint4 n4 = make_uint4(0, 0, 0, 0);
+    for (int i = wlo + lane; i < whi; i += 32) {
+      const uint32_t k = key(i);
+      const uint32_t larger = k > prefix ? 1u : 0u, equal = k == prefix ? 1u : 0u, front = i < p.budget ? 1u : 0u;
+      n4.x += larger & front;
+      n4.y += larger & ~front;
+      n4.z += equal & front;
+      n4.w += equal & ~front;
+    }
+    n4.x = __reduce_add_sync(0xffffffffu, n4.x);
+    n4.y = __reduce_add_sync(0xffffffffu, n4.y);
+    n4.z = __reduce_add_sync(0xffffffffu, n4.z);
+    n4.w = __reduce_add_sync(0xffffffffu, n4.w);
+    if (lane == 0) s_cnt[warp] = n4;
+  }
+  __syncthreads();
+  const uint4 of_warp = lane < kEvictWarps ? s_cnt[lane] : make_uint4(0, 0, 0, 0);
+  if (warp == 0) {
+    uint4 n4;
+    n4.x = __reduce_add_sync(0xffffffffu, of_warp.x);
+    n4.y = __reduce_add_sync(0xffffffffu, of_warp.y);
+    n4.z = __reduce_add_sync(0xffffffffu, of_warp.z);
+    n4.w = __reduce_add_sync(0xffffffffu, of_warp.w);
+    if (lane == 0) s_sum = n4;
+  }
+  cluster.sync();
+  // A row of lanes (blocks, or warps), the counts and the first slot of each:
+  // what lies in front of lane `me` (equal ones, evicted slots in front of the
+  // budget, kept ones behind it), given what lies in front of lane 0.
+  uint32_t equal_before = 0, hole_at = 0, mover_at = 0, total = 0;
+  auto number = [&](const uint4& n4, int first, int end, int me) {
+    uint32_t eq = n4.z + n4.w, inc = eq;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += y;
     }
-    if (lane == 31) s_scan[warp] = inc;
-    __syncthreads();
-    uint32_t above = inc - sum;
-    for (int w = 0; w < warp; ++w) above += s_scan[w];
-    if (above < left && left <= above + sum) {
-      uint32_t rest = left - above;
-      int k = kBins / kEvictThreads - 1;
-      for (; k > 0 && rest > mine[k]; --k) rest -= mine[k];
-      s_digit = (uint32_t)(first + k);
-      s_left = rest;
-    }
-    cluster.sync();  // also: every block has read the histograms
-    prefix |= s_digit << shift;
-    mask |= digits << shift;
-    left = s_left;
-  }
-  // kept: keys above `prefix`, and the first `left` slots equal to it
-  const int part = ((hi - lo + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;  // a warp's slots
-  const int wlo = lo + warp * part < hi ? lo + warp * part : hi, whi = wlo + part < hi ? wlo + part : hi;
-  // numbers the warp's slots: f(slot, kept) with the warp converged
-  auto walk = [&](uint32_t equal_before, auto&& f) {
-    for (int i0 = wlo; i0 < whi; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < whi ? key(i) : 0u;
-      const bool eq = i < whi && k == prefix;
-      const uint32_t bal = __ballot_sync(0xffffffffu, eq);
-      const uint32_t before = equal_before + __popc(bal & ((1u << lane) - 1u));
-      f(i, i < whi, i < whi && (k > prefix || (eq && before < left)));
-      equal_before += __popc(bal);
-    }
+    const uint32_t before = equal_before + inc - eq;
+    const uint32_t stay = before >= left ? 0u : left - before < eq ? left - before : eq;
+    const uint32_t stay_front = stay < n4.z ? stay : n4.z;
+    const int front = (end < p.budget ? end : p.budget) - first;
+    const uint32_t holes = (front > 0 ? (uint32_t)front : 0u) - n4.x - stay_front, movers = n4.y + stay - stay_front;
+    total = __reduce_add_sync(0xffffffffu, movers);
+    equal_before = __shfl_sync(0xffffffffu, before, me);
+    hole_at += __reduce_add_sync(0xffffffffu, lane < me ? holes : 0u);
+    mover_at += __reduce_add_sync(0xffffffffu, lane < me ? movers : 0u);
   };
-  uint32_t equal = 0;
-  for (int i = wlo + lane; i < whi; i += 32) equal += key(i) == prefix ? 1u : 0u;
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) s_scan[warp] = equal;
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t s = 0;
-    for (int w = 0; w < kEvictWarps; ++w) s += s_scan[w];
-    s_sum[0] = s;
+  auto clip = [](int x, int most) { return x < most ? x : most; };
+  {
+    const int first = clip((lane < p.share ? lane : 0) * chunk, n);
+    const uint4 of_block = lane < p.share ? *cluster.map_shared_rank(&s_sum, lane) : make_uint4(0, 0, 0, 0);
+    number(of_block, lane < p.share ? first : 0, lane < p.share ? clip(first + chunk, n) : 0, rank);
   }
-  cluster.sync();
-  uint32_t equal_before = 0;
-  for (int r = 0; r < rank; ++r) equal_before += *cluster.map_shared_rank(&s_sum[0], r);
-  for (int w = 0; w < warp; ++w) equal_before += s_scan[w];
-  uint32_t holes = 0, movers = 0;
-  walk(equal_before, [&](int i, bool in, bool keep) {
-    holes += __popc(__ballot_sync(0xffffffffu, in && !keep && i < p.budget));
-    movers += __popc(__ballot_sync(0xffffffffu, keep && i >= p.budget));
-  });
-  if (lane == 0) s_cnt[warp][0] = holes, s_cnt[warp][1] = movers;
-  __syncthreads();
-  if (tid < 2) {
-    uint32_t s = 0;
-    for (int w = 0; w < kEvictWarps; ++w) s += s_cnt[w][tid];
-    s_sum[1 + tid] = s;
+  const uint32_t moves = total;
+  {
+    const int first = clip(lo + (lane < kEvictWarps ? lane : 0) * part, hi);
+    number(of_warp, lane < kEvictWarps ? first : 0, lane < kEvictWarps ? clip(first + part, hi) : 0, warp);
   }
-  cluster.sync();
-  uint32_t hole_at = 0, mover_at = 0, total = 0;
-  for (int r = 0; r < p.share; ++r) {
-    const uint32_t* s = cluster.map_shared_rank(s_sum, r);
-    if (r < rank) hole_at += s[1], mover_at += s[2];
-    total += s[2];
-  }
-  for (int w = 0; w < warp; ++w) hole_at += s_cnt[w][0], mover_at += s_cnt[w][1];
   int32_t* const to = p.moves + (int64_t)item * 2 * p.room;
   int32_t* const of = to + p.room;
-  walk(equal_before, [&](int i, bool in, bool keep) {
+  for (int i0 = wlo; i0 < whi; i0 += 32) {
+    const int i = i0 + lane;
+    const bool in = i < whi;
+    const uint32_t k = in ? key(i) : 0u, under = (1u << lane) - 1u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix);
+    const bool keep = in && (k > prefix || (k == prefix && equal_before + __popc(eq & under) < left));
+    equal_before += __popc(eq);
     const bool hole = in && !keep && i < p.budget, mover = keep && i >= p.budget;
     const uint32_t bh = __ballot_sync(0xffffffffu, hole), bm = __ballot_sync(0xffffffffu, mover);
-    const uint32_t under = (1u << lane) - 1u;
     if (hole) to[hole_at + __popc(bh & under)] = i;
     if (mover) of[mover_at + __popc(bm & under)] = i;
     hole_at += __popc(bh);
     mover_at += __popc(bm);
-    if (keep && i < p.budget && (copy_w || copy_p)) carry(i);
-  });
+    if (in && i < p.budget && (copy_w || copy_p)) {
+      if (i - lo < p.held) s_key[i - lo] = keep ? 1u : 0u;  // the key is needed no more
+      else if (keep) carry(i);
+    }
+  }
   __threadfence();
   cluster.sync();  // the lists; and no block leaves while another reads its counts
 
-  const int row16 = c.D * (c.k_exp ? 1 : 2) / 16;       // 16-byte pieces of a row
-  const int lanes = 2 * row16, per = 32 / lanes;        // keys and values side by side in a warp
+  // A warp takes up to 32 moves: a lane finds a move's places and carries its
+  // numbers, then the lanes copy the rows side by side, keys next to values,
+  // kAtOnce of them in flight.
+  const int row16 = c.D * (c.k_exp ? 1 : 2) / 16;  // 16-byte pieces of a row
+  const int lanes = 2 * row16, per = 32 / lanes;   // of a move; moves of a warp-wide copy
   const int sub = lane / lanes, piece = lane % lanes;
   const bool val = piece >= row16;
   uint8_t* const rows = (val ? c.v : c.k) + (piece - (val ? row16 : 0)) * 16;
-  const uint32_t stride = (uint32_t)(p.share * kEvictWarps * per);
-  for (uint32_t i0 = (uint32_t)((rank * kEvictWarps + warp) * per + sub); i0 < total; i0 += 4 * stride) {
-    uint4 x[4];
-    int pf[4], pt[4];
-    uint32_t sf[4], st[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t i = i0 + u * stride;
-      pf[u] = pt[u] = -1;
-      if (i < total) {
-        const Place f = place_of(c, of[i]), t = place_of(c, to[i]);
-        pf[u] = page_of(c, b, f.page), sf[u] = f.slot;
-        pt[u] = page_of(c, b, t.page), st[u] = t.slot;
-        if (pt[u] < 0) pf[u] = -1;
-      }
-      if (pf[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(rows + at(c.row, pf[u], sf[u], g));
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (pf[u] < 0) continue;
-      *reinterpret_cast<uint4*>(rows + at(c.row, pt[u], st[u], g)) = x[u];
-      if (piece == 0) {
-        p.weight_out[at(p.weight_at, pt[u], st[u], g)] = p.weight_in[at(p.weight_at, pf[u], sf[u], g)];
-        p.pos_out[at(p.pos_at, pt[u], st[u], g)] = p.pos_in[at(p.pos_at, pf[u], sf[u], g)];
+  const uint32_t warps = (uint32_t)(p.share * kEvictWarps);
+  const uint32_t each = moves > 32 * warps ? 32u : (moves + warps - 1) / warps;
+  for (uint32_t m0 = (uint32_t)(rank * kEvictWarps + warp) * each; m0 < moves; m0 += warps * each) {
+    const uint32_t here = moves - m0 < each ? moves - m0 : each;
+    int64_t rf = -1, rt = 0;
+    if ((uint32_t)lane < here) {
+      const Place f = place_of(c, of[m0 + lane]), t = place_of(c, to[m0 + lane]);
+      const int pf = page_of(c, b, f.page), pt = page_of(c, b, t.page);
+      if (pf >= 0 && pt >= 0) {
+        rf = at(c.row, pf, f.slot, g);
+        rt = at(c.row, pt, t.slot, g);
+        const float w = p.weight_in[at(p.weight_at, pf, f.slot, g)];
+        const int number = p.pos_in[at(p.pos_at, pf, f.slot, g)];
         if (c.k_exp) {
-          const int64_t f = at(c.exp, pf[u], sf[u], g), t = at(c.exp, pt[u], st[u], g);
-          c.k_exp[t] = c.k_exp[f];
-          c.v_exp[t] = c.v_exp[f];
+          const int64_t ef = at(c.exp, pf, f.slot, g), et = at(c.exp, pt, t.slot, g);
+          const uint8_t ke = c.k_exp[ef], ve = c.v_exp[ef];
+          c.k_exp[et] = ke;
+          c.v_exp[et] = ve;
+        }
+        p.weight_out[at(p.weight_at, pt, t.slot, g)] = w;
+        p.pos_out[at(p.pos_at, pt, t.slot, g)] = number;
+      }
+    }
+    constexpr int kAtOnce = 4;
+    for (uint32_t m = 0; m < here; m += kAtOnce * per) {
+      uint4 x[kAtOnce];
+      int64_t into[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const uint32_t k = m + u * per + sub;
+        const int64_t from = __shfl_sync(0xffffffffu, rf, k & 31);
+        into[u] = __shfl_sync(0xffffffffu, rt, k & 31);
+        if (k >= here || from < 0) into[u] = -1;
+        if (into[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(rows + from);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (into[u] >= 0) *reinterpret_cast<uint4*>(rows + into[u]) = x[u];
+    }
+  }
+  if (copy_w || copy_p) {  // what stays, to the other arrays
+    const int m = hi - lo < p.held ? hi - lo : p.held, end = p.budget - lo < m ? p.budget - lo : m;
+    for (int i0 = tid; i0 < end; i0 += 4 * kEvictThreads) {
+      int64_t a[4], q[4];
+      float w[4];
+      int number[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kEvictThreads;
+        a[u] = -1;
+        if (i < end && s_key[i]) {
+          const Place x = place_of(c, lo + i);
+          const int page = page_of(c, b, x.page);
+          if (page >= 0) a[u] = at(p.weight_at, page, x.slot, g), q[u] = at(p.pos_at, page, x.slot, g);
         }
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (a[u] >= 0) w[u] = p.weight_in[a[u]], number[u] = p.pos_in[q[u]];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (a[u] >= 0) {
+          if (copy_w) p.weight_out[a[u]] = w[u];
+          if (copy_p) p.pos_out[q[u]] = number[u];
+        }
     }
   }
 }

@@ -42,7 +42,10 @@ constexpr int kDecThreads = 32 * kDecWarps;
 #endif
 constexpr int kDecTile = 8192;  // bytes of a stage: a tile's keys, then its values
 constexpr int kUnit = 64;       // slots
-constexpr int kLead = 2;        // units that an item's beginning and end cost
+#ifndef LEAD
+#define LEAD 3
+#endif
+constexpr int kLead = LEAD;        // units that an item's beginning and end cost
 constexpr int kMinUnits = 2;    // of a block, while there are few
 
 constexpr float kSlack = 8.f;   // see the running maximum
