@@ -1015,13 +1015,13 @@ struct DecodeWs {
   size_t units, joins, part, part_ml, lse2, scores, total;
 };
 static DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int64_t capacity, bool weights) {
-  const size_t heads = (size_t)decode_heads(Hq / Hkv);
+  const size_t heads = (size_t)decode_heads(Hq / Hkv), blocks = (size_t)decode_blocks(B, Hkv, Hq / Hkv, capacity);
   DecodeWs w;
   w.units = 0;
   w.joins = align_up(sizeof(int64_t) * ((size_t)B + 1), 256);
-  w.part = align_up(w.joins + sizeof(DecodeJoin) * kDecodeMaxGrid, 256);
-  w.part_ml = align_up(w.part + sizeof(float) * 2 * kDecodeMaxGrid * heads * D, 256);
-  w.lse2 = align_up(w.part_ml + sizeof(float) * 2 * kDecodeMaxGrid * heads * 3, 256);
+  w.part = align_up(w.joins + sizeof(DecodeJoin) * blocks, 256);
+  w.part_ml = align_up(w.part + sizeof(float) * 2 * blocks * heads * D, 256);
+  w.lse2 = align_up(w.part_ml + sizeof(float) * 2 * blocks * heads * 3, 256);
   w.scores = align_up(w.lse2 + (weights ? sizeof(float) * (size_t)B * Hq : 0), 256);
   w.total = align_up(w.scores + (weights ? sizeof(float) * (size_t)B * Hq * (size_t)capacity : 0), 256);
   return w;

@@ -4,21 +4,18 @@
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
-#ifndef MPDL
-#define MPDL 0
-#endif
-#ifndef APDL
-#define APDL 1
-#endif
 #include "vec8.cuh"
 
 namespace thd {
 
 // ------------------------------------------------------------------ append
 // A block takes `tokens` rows; its first threads find each row's sequence (a
-// binary search of the offsets) and slot, then all threads walk the rows of
-// (token, head, k or v), eight elements a lane.  Bound by HBM: the rows are read
-// and written once, 16 bytes a lane (8 written for e4m3).
+// binary search of the offsets) and where its slot lies, then its warps walk
+// (token, head) pairs, the key's row on some lanes and the value's on others,
+// eight elements a lane, four pairs in flight.  Bound by HBM: the rows are read and
+// written once, 16 bytes a lane (8 written for e4m3).  The search and the page
+// are three to six loads one after the other, so a block takes many rows where
+// there are many.
 //
 // e4m3 with a power of two for each row and head: e is the smallest exponent
 // with max |row| <= 448 * 2^e, so dividing is exact and the only rounding is the
@@ -26,7 +23,7 @@ namespace thd {
 // (a scale of max / 448 would round twice and gain nothing but the last half
 // binade).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 8;  // at most, a block
+constexpr int kAppendTokens = 32;  // at most, a block
 
 // The stored exponent of a row whose largest magnitude (bf16, sign off) is
 // `big`: 448 = 1.75 * 2^8, so 2^(x - 8) serves up to a mantissa of 1.75.  No
@@ -39,11 +36,16 @@ __device__ inline int row_exponent(uint32_t big) {
   return e < 67 ? 67 : e;
 }
 
-template <bool kFp8>
+// Where a block's row goes: byte offset of its slot's rows, element offsets of
+// its numbers; row -1: nowhere.
+struct AppendRow {
+  int64_t row, exp, weight, pos;
+  int number;
+};
+
+template <bool kFp8, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  __shared__ int s_page[kAppendTokens], s_slot[kAppendTokens], s_pos[kAppendTokens];
-  follow();
-  depend();
+  __shared__ AppendRow s_row[kAppendTokens];
   const CacheView& c = p.c;
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
   const int count = (int)(p.T - t0 < p.tokens ? p.T - t0 : p.tokens);
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
   if (threadIdx.x < count) {
     const int64_t t = t0 + threadIdx.x;
-    int page = -1, slot = 0, pos = 0;
+    AppendRow out = {-1, 0, 0, 0, 0};
     int b = (int)t;
     int64_t back = 1;  // rows from this one to its sequence's end
     bool mine = t < c.B;
@@ -75,49 +77,56 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (n > c.capacity || j < 0) {
         raise(p.status, THD_DEV_ERR_KV_LEN);
       } else {
-        const Place at_j = place_of(c, (int)j);
-        page = page_of(c, b, at_j.page);
-        if (page < 0) raise(p.status, THD_DEV_ERR_PAGE);
-        slot = (int)at_j.slot;
-        pos = (int)((p.seen ? (int64_t)p.seen[b] : n) - back);
+        const Place x = place_of(c, (int)j);
+        const int page = page_of(c, b, x.page);
+        if (page < 0) {
+          raise(p.status, THD_DEV_ERR_PAGE);
+        } else {
+          out.row = at(c.row, page, x.slot, 0);
+          out.exp = at(c.exp, page, x.slot, 0);
+          out.weight = at(p.weight_at, page, x.slot, 0);
+          out.pos = at(p.pos_at, page, x.slot, 0);
+        }
+        out.number = (int)((p.seen ? (int64_t)p.seen[b] : n) - back);
       }
     }
-    s_page[threadIdx.x] = page;
-    s_slot[threadIdx.x] = slot;
-    s_pos[threadIdx.x] = pos;
+    s_row[threadIdx.x] = out;
   }
   __syncthreads();
-  const int lanes = c.D / 8;                       // of a row
-  const int rows = count * c.Hkv * 2;              // (token, head, k or v)
-  const int per = kAppendThreads / lanes, lane = threadIdx.x % lanes;
-  const int steps = (rows + per - 1) / per;        // every lane walks alike: the exponent is a shuffle
-  for (int i0 = 0; i0 < steps; i0 += 4) {
-    Vec8<uint16_t> x[4];
-    bool ok[4];
-    int tok[4], g[4], kv[4];
+  constexpr int kLanes = D / 8, kPairs = 32 / (2 * kLanes);  // of a row; a warp's (token, head) pairs at a time
+  constexpr int kAtOnce = 4, kStride = kPairs * kAppendThreads / 32;
+  const int lane = threadIdx.x & 31, piece = lane % kLanes, kv = lane / kLanes & 1;
+  const uint16_t* const in = p.in[kv] + t0 * p.in_stride[kv] + 8 * piece;
+  uint8_t* const cache = (kv ? c.v : c.k) + (kFp8 ? 8 : 16) * piece;
+  const int pairs = count * c.Hkv;
+  // every lane walks alike: the exponent is a shuffle
+  for (int r0 = (threadIdx.x >> 5) * kPairs; r0 < pairs; r0 += kAtOnce * kStride) {
+    Vec8<uint16_t> x[kAtOnce];
+    int tok[kAtOnce], g[kAtOnce];
+    bool ok[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (i0 + u) * per + threadIdx.x / lanes;
-      ok[u] = r < rows;
-      kv[u] = r & 1;
-      g[u] = (r >> 1) % c.Hkv;
-      tok[u] = ok[u] ? (r >> 1) / c.Hkv : 0;
-      ok[u] = ok[u] && s_page[tok[u]] >= 0;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = r0 + u * kStride + lane / (2 * kLanes);
+      tok[u] = r < pairs ? (int)(((uint64_t)(uint32_t)r * p.heads.mul) >> p.heads.shift) : 0;
+      g[u] = r - tok[u] * c.Hkv;
+      ok[u] = r < pairs && s_row[tok[u]].row >= 0;
       x[u].v = make_uint4(0, 0, 0, 0);
-      if (ok[u]) x[u].load(p.in[kv[u]] + (t0 + tok[u]) * p.in_stride[kv[u]] + (int64_t)g[u] * c.D + 8 * lane);
+      if (ok[u]) x[u].load(in + tok[u] * p.in_stride[kv] + g[u] * D);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint8_t* out = (kv[u] ? c.v : c.k);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const AppendRow& to = s_row[tok[u]];
+      uint8_t* const out = cache + to.row + g[u] * c.row.head;
       if (!kFp8) {
-        if (ok[u]) x[u].store(reinterpret_cast<uint16_t*>(out + at(c.row, s_page[tok[u]], s_slot[tok[u]], g[u])) + 8 * lane);
+        if (ok[u]) x[u].store(reinterpret_cast<uint16_t*>(out));
       } else {
         const uint32_t w[4] = {x[u].v.x, x[u].v.y, x[u].v.z, x[u].v.w};
         uint32_t big = 0;  // of both halves: a bf16's order is its bits'
 #pragma unroll
         for (int q = 0; q < 4; ++q) big = __vmaxu2(big, w[q] & 0x7fff7fffu);
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, d));
         big = max(big >> 16, big & 0xffffu);
-        for (int d = lanes / 2; d > 0; d >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
         const int e = row_exponent(big);
         const float inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
         float f[8];
@@ -125,18 +134,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         uint32_t y[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q] * inv, f[4 * q + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-          uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q + 2] * inv, f[4 * q + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q] * inv, f[4 * q + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q + 2] * inv, f[4 * q + 3] * inv), __NV_SATFINITE, __NV_E4M3);
           y[q] = e == 255 ? 0x7f7f7f7fu : lo | hi << 16;
         }
         if (ok[u]) {
-          *reinterpret_cast<uint2*>(out + at(c.row, s_page[tok[u]], s_slot[tok[u]], g[u]) + 8 * lane) = make_uint2(y[0], y[1]);
-          if (lane == 0) (kv[u] ? c.v_exp : c.k_exp)[at(c.exp, s_page[tok[u]], s_slot[tok[u]], g[u])] = (uint8_t)e;
+          *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+          if (piece == 0) (kv ? c.v_exp : c.k_exp)[to.exp + g[u] * c.exp.head] = (uint8_t)e;
         }
       }
-      if (ok[u] && lane == 0 && kv[u] == 0) {
-        if (p.weight) p.weight[at(p.weight_at, s_page[tok[u]], s_slot[tok[u]], g[u])] = 0.f;
-        if (p.pos) p.pos[at(p.pos_at, s_page[tok[u]], s_slot[tok[u]], g[u])] = s_pos[tok[u]];
+      if (ok[u] && piece == 0) {
+        if (kv == 0 && p.weight) p.weight[to.weight + g[u] * p.weight_at.head] = 0.f;
+        if (kv == 1 && p.pos) p.pos[to.pos + g[u] * p.pos_at.head] = to.number;
       }
     }
   }
@@ -145,12 +154,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
   AppendParams p = a;
-  int64_t n = (a.T + 2 * num_sms() - 1) / (2 * num_sms());  // two blocks an SM first
+  const int64_t n = (a.T + 8 * num_sms() - 1) / (8 * num_sms());  // eight blocks an SM first
   p.tokens = (int)(n > kAppendTokens ? kAppendTokens : n);
-  const int64_t grid = (a.T + p.tokens - 1) / p.tokens;
+  p.heads = divisor((uint32_t)a.c.Hkv);
+  const unsigned grid = (unsigned)((a.T + p.tokens - 1) / p.tokens);
   prof_before(THD_KERNEL_CACHE_APPEND, st);
-  const cudaError_t e = launch_following(a.c.k_exp ? append_kernel<true> : append_kernel<false>, dim3((unsigned)grid),
-                                         kAppendThreads, 0, st, APDL, (const AppendParams)p);
+  if (a.c.k_exp && a.c.D == 64) append_kernel<true, 64><<<grid, kAppendThreads, 0, st>>>(p);
+  if (a.c.k_exp && a.c.D == 128) append_kernel<true, 128><<<grid, kAppendThreads, 0, st>>>(p);
+  if (!a.c.k_exp && a.c.D == 64) append_kernel<false, 64><<<grid, kAppendThreads, 0, st>>>(p);
+  if (!a.c.k_exp && a.c.D == 128) append_kernel<false, 128><<<grid, kAppendThreads, 0, st>>>(p);
+  count_launch();
+  const cudaError_t e = cudaGetLastError();
   prof_after(THD_KERNEL_CACHE_APPEND, st);
   return e;
 }
@@ -457,8 +471,8 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t st) {
   p.held = (int)held;
   if (items * share >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
   const size_t smem = sizeof(uint32_t) * (size_t)held;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(uint32_t) * kEvictMaxHeld));
+  static bool allowed[64] = {};
+  cudaError_t e = allow_smem(evict_kernel, sizeof(uint32_t) * kEvictMaxHeld, allowed);
   if (e != cudaSuccess) return e;
   prof_before(THD_KERNEL_CACHE_EVICT, st);
   cudaLaunchAttribute attr[1];

@@ -15,7 +15,7 @@ struct SlotStrides {
   int64_t page, slot, head;
 };
 
-// Division by the page size without a division: for 0 <= x <= 2^30 and
+// Division by a number the host knows, without a division: for 0 <= x <= 2^30 and
 // 1 <= d <= 2^30, x / d = x mul >> shift with mul = ceil(2^shift / d), shift =
 // 30 + ceil(log2 d) (mul d exceeds 2^shift by less than d, x times which stays
 // below 2^shift).
@@ -56,7 +56,8 @@ struct AppendParams {
   SlotStrides pos_at;
   const int32_t* seen;  // null: kv_len
   int32_t* status;
-  int tokens;  // a block
+  int tokens;     // a block
+  Divisor heads;  // Hkv
 };
 
 // An item that several blocks shared, as its last block leaves it for the join:
@@ -115,19 +116,33 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_decode(DecodeParams p, cudaStream_t st);
 cudaError_t launch_evict(EvictParams p, cudaStream_t st);
 
-constexpr int kDecodeMaxGrid = 1024;   // blocks of a decode launch (the workspace holds two parts for each)
+constexpr int kDecodeMaxGrid = 512;    // blocks of a decode launch (the workspace holds two parts for each)
 constexpr int kDecodeMaxGroup = 512;   // query heads of a kv head
 int decode_heads(int G);               // query heads of a work item
+// The most blocks that a decode of these sizes has work for, whatever the lengths.
+int decode_blocks(int B, int Hkv, int G, int64_t capacity);
+
+// A kernel's limit of dynamic shared memory, raised once on each device (`done`:
+// the kernel's own).
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
 
 // Launches a kernel that may start while the one in front of it in the stream
 // ends: its blocks begin with depend(), which waits for that kernel's end and
 // the writes of it, and with follow(), which lets the next such kernel start.
 // What this hides is the launch, a microsecond or two of each.
 template <typename... A>
-cudaError_t launch_following(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, int pdl, A... args) {
+cudaError_t launch_following(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = pdl;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);

@@ -24,28 +24,15 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
-#ifndef MPDL
-#define MPDL 0
-#endif
-#ifndef APDL
-#define APDL 1
-#endif
 #include "ptx.cuh"
 
 namespace thd {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-#ifndef BP8
-#define BP8 3
-#define BPB 2
-#endif
 constexpr int kDecTile = 8192;  // bytes of a stage: a tile's keys, then its values
 constexpr int kUnit = 64;       // slots
-#ifndef LEAD
-#define LEAD 3
-#endif
-constexpr int kLead = LEAD;        // units that an item's beginning and end cost
+constexpr int kLead = 3;        // units that an item's beginning and end cost
 constexpr int kMinUnits = 2;    // of a block, while there are few
 
 constexpr float kSlack = 8.f;   // see the running maximum
@@ -54,6 +41,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 int decode_heads(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : 32; }
+int decode_blocks(int B, int Hkv, int G, int64_t capacity) {
+  const int64_t items = (int64_t)B * Hkv * ((G + decode_heads(G) - 1) / decode_heads(G));
+  const int64_t total = items * ((capacity + kUnit - 1) / kUnit + kLead), n = (total + kMinUnits - 1) / kMinUnits;
+  return n < kDecodeMaxGrid ? (int)n : kDecodeMaxGrid;
+}
 
 // ------------------------------------------------------------------ PTX
 THD_DEV void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -155,7 +147,7 @@ struct DecShape {
   static constexpr int kPieces = kRow / 16;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kStages = 2;
-  static constexpr int kPerSm = NT > 1 ? 2 : kFp8 ? BP8 : BPB;   // blocks
+  static constexpr int kPerSm = kFp8 && NT == 1 ? 3 : 2;  // blocks
   // slots worked on at a time, in sixteens: more of them overlap better, fewer
   // leave the registers to the heads
   static constexpr int kStep = NT == 1 ? kSub : NT == 2 && kSub > 1 ? 2 : 1;
@@ -195,7 +187,6 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
   float* const s_sl = s_hs + S::kHeads;
   float* const s_ml = s_sl + S::kHeads;                       // [kDecWarps][3][kHeads]
 
-  depend();
   // the block table on its way to L2 while the lengths come: a line a thread
   {
     const int64_t bytes = (c.B - 1) * c.table_stride * 4 + c.capacity / c.page.d * 4;
@@ -1005,12 +996,15 @@ __global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const De
 template <bool kFp8, int D, int NT>
 static cudaError_t launch_decode_t(DecodeParams& p, cudaStream_t st) {
   using S = DecShape<kFp8, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<kFp8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  static bool allowed[64] = {};  // of this instantiation
+  cudaError_t e = allow_smem(decode_kernel<kFp8, D, NT>, S::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  int grid = S::kPerSm * num_sms();  // one wave
-  p.grid = grid > kDecodeMaxGrid ? kDecodeMaxGrid : grid;
+  const int wave = S::kPerSm * num_sms(), most = decode_blocks(p.c.B, p.c.Hkv, p.G, p.c.capacity);
+  p.grid = wave < most ? wave : most;
   prof_before(THD_KERNEL_DECODE, st);
-  e = launch_following(decode_kernel<kFp8, D, NT>, dim3((unsigned)p.grid), kDecThreads, S::kSmem, st, MPDL, (const DecodeParams)p);
+  decode_kernel<kFp8, D, NT><<<(unsigned)p.grid, kDecThreads, S::kSmem, st>>>(p);
+  count_launch();
+  e = cudaGetLastError();
   prof_after(THD_KERNEL_DECODE, st);
   return e;
 }
@@ -1031,13 +1025,13 @@ cudaError_t launch_decode(DecodeParams p, cudaStream_t st) {
   if (p.c.capacity > kUnit) {  // an item of one unit is one block's
     prof_before(THD_KERNEL_DECODE_JOIN, st);
     e = launch_following(p.c.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
-                         dim3((unsigned)p.grid, (unsigned)heads), kJoinThreads, 0, st, 1, (const DecodeParams)p, (int)heads);
+                         dim3((unsigned)p.grid, (unsigned)heads), kJoinThreads, 0, st, (const DecodeParams)p, (int)heads);
     prof_after(THD_KERNEL_DECODE_JOIN, st);
     if (e != cudaSuccess) return e;
   }
   if (p.weight_out) {
     prof_before(THD_KERNEL_DECODE_WEIGHTS, st);
-    e = launch_following(decode_weights_kernel, dim3((unsigned)(8 * num_sms())), kWeightThreads, 0, st, 1, (const DecodeParams)p);
+    e = launch_following(decode_weights_kernel, dim3((unsigned)(8 * num_sms())), kWeightThreads, 0, st, (const DecodeParams)p);
     prof_after(THD_KERNEL_DECODE_WEIGHTS, st);
   }
   return e;

@@ -20,8 +20,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libthdattn.so")
@@ -85,7 +87,7 @@ _sz = ctypes.c_size_t
 
 
 class KvCache(ctypes.Structure):
-    """thd_kv_cache."""
+    """thd_kv_cache.  The thd_* functions take one, or its bytes."""
     _fields_ = [("k", _vp), ("v", _vp), ("k_exp", _vp), ("v_exp", _vp), ("block_table", _vp), ("kv_len", _vp),
                 ("num_pages", _i64), ("table_stride", _i64), ("kv_stride", _i64 * 3), ("exp_stride", _i64 * 3),
                 ("weight_stride", _i64 * 3), ("pos_stride", _i64 * 3), ("page_size", ctypes.c_int32),
@@ -93,7 +95,12 @@ class KvCache(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
-_kvp = ctypes.POINTER(KvCache)
+_pack_cache = struct.Struct("=6Q14q6i").pack   # the fields in order, without padding
+
+
+def _c(cache):
+    return cache if cache is None or isinstance(cache, bytes) else ctypes.byref(cache)
+
 
 # name -> (restype, argtypes); mirrors include/thd_attn.h
 SIGNATURES = {
@@ -129,11 +136,11 @@ SIGNATURES = {
     "thd_rope": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
                         _vp, _i32, _i32, _i32, _vp]),
     "thd_dropout_add": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _f64, _vp, _i32, _vp]),
-    "thd_cache_append": (_i32, [_kvp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
-    "thd_attn_decode": (_i32, [_kvp, _vp, _i64, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
+    "thd_cache_append": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "thd_attn_decode": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
                                _vp]),
     "thd_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i64, _i32]),
-    "thd_cache_evict": (_i32, [_kvp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp, _vp]),
+    "thd_cache_evict": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp, _vp]),
     "thd_evict_workspace_size": (_sz, [_i32, _i32, _i64, _i32]),
     "thd_profile_enable": (_i32, [_i32, _i32]),
     "thd_profile_read": (_i32, [_vp, _i32, _vp]),
@@ -162,11 +169,7 @@ def lib() -> ctypes.CDLL:
 
 def _p(x):
     """Device pointer of a tensor (or pass an int / None through)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def _h(a):
@@ -333,13 +336,13 @@ def thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dtype, stream=None)
 
 def thd_cache_append(cache, k, v, k_stride, v_stride, T, cu_seqlens, weight, pos, tokens_seen, dev_status,
                      stream=None) -> int:
-    return lib().thd_cache_append(cache, _p(k), _p(v), k_stride, v_stride, T, _p(cu_seqlens), _p(weight), _p(pos),
+    return lib().thd_cache_append(_c(cache), _p(k), _p(v), k_stride, v_stride, T, _p(cu_seqlens), _p(weight), _p(pos),
                                   _p(tokens_seen), _p(dev_status), _s(stream))
 
 
 def thd_attn_decode(cache, q, q_stride, o, lse, Hq, softmax_scale, softcap, dist_slopes, kv_start, pos, tokens_seen,
                     weight_in, weight_out, workspace, workspace_bytes, dev_status, stream=None) -> int:
-    return lib().thd_attn_decode(cache, _p(q), q_stride, _p(o), _p(lse), Hq, softmax_scale, softcap, _p(dist_slopes),
+    return lib().thd_attn_decode(_c(cache), _p(q), q_stride, _p(o), _p(lse), Hq, softmax_scale, softcap, _p(dist_slopes),
                                  _p(kv_start), _p(pos), _p(tokens_seen), _p(weight_in), _p(weight_out), _p(workspace),
                                  workspace_bytes, _p(dev_status), _s(stream))
 
@@ -350,7 +353,7 @@ def thd_decode_workspace_size(B, Hq, Hkv, D, capacity, has_weights) -> int:
 
 def thd_cache_evict(cache, weight_in, weight_out, pos_in, pos_out, tokens_seen, budget, sinks, recent, new_len, workspace,
                     workspace_bytes, dev_status, stream=None) -> int:
-    return lib().thd_cache_evict(cache, _p(weight_in), _p(weight_out), _p(pos_in), _p(pos_out), _p(tokens_seen), budget,
+    return lib().thd_cache_evict(_c(cache), _p(weight_in), _p(weight_out), _p(pos_in), _p(pos_out), _p(tokens_seen), budget,
                                  sinks, recent, _p(new_len), _p(workspace), workspace_bytes, _p(dev_status), _s(stream))
 
 
@@ -891,56 +894,83 @@ def dropout_add(x, rng, p, *, residual=None, row_ids=None, out=None, stream=None
     return out
 
 
-def _slot_array(where, t, dtype, pages, slots, heads, dev):
-    """Strides of an array [pages, slots, heads] in any order of its dimensions."""
-    _need(where, t.dtype is dtype and t.shape == (pages, slots, heads) and t.get_device() == dev)
-    return t.stride()
+def _row_stride(where, like, t, T, H, D):
+    """_rope_rows, with the contiguous case first."""
+    if t.stride() == (H * D, D, 1) and t.shape == (T, H, D) and t.dtype is like.dtype and \
+            t.get_device() == like.get_device():
+        return H * D
+    return _rope_rows(where, like, t, T, H, D)
 
 
-def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, pos):
-    """The cache of a call as thd_kv_cache; weight, pos: lists of arrays with
-    the same strides (or of None)."""
+def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos, pos_out):
+    """The cache of a call as thd_kv_cache's bytes, its B, Hkv, D and slots of
+    a table's row, and the device."""
     import torch
     dev = _current(where, k_cache)
     shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
-    _need(where, len(shape) == 4 and v_cache.shape == shape and v_cache.stride() == strides and
-          v_cache.dtype is dtype and v_cache.get_device() == dev and strides[3] == 1)
-    pages, slots, heads, D = shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype is not dtype or \
+            v_cache.get_device() != dev or strides[3] != 1:
+        _need(where, False)
     e4m3 = dtype is torch.float8_e4m3fn
     if not e4m3 and dtype is not torch.bfloat16:
         raise ThdError(where, THD_ERR_UNSUPPORTED)
-    _need(where, block_table.dim() == 2 and block_table.dtype is torch.int32 and block_table.get_device() == dev)
+    i32 = torch.int32
+    if block_table.dim() != 2 or block_table.dtype is not i32 or block_table.get_device() != dev:
+        _need(where, False)
     B, max_pages = block_table.shape
     ts0, ts1 = block_table.stride()
-    _need(where, (ts1 == 1 or max_pages <= 1) and (B <= 1 or ts0 >= max_pages))
-    _need(where, kv_len.dtype is torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous() and
-          kv_len.get_device() == dev)
-    c = KvCache(k=k_cache.data_ptr(), v=v_cache.data_ptr(), block_table=block_table.data_ptr(), kv_len=kv_len.data_ptr(),
-                num_pages=pages, table_stride=ts0, page_size=slots, max_pages=max_pages, B=B, Hkv=heads, D=D,
-                dtype=THD_DTYPE_E4M3 if e4m3 else THD_DTYPE_BF16)
-    c.kv_stride[:] = strides[:3]
-    _need(where, (k_exp is not None) == e4m3 and (v_exp is not None) == e4m3)
+    if not (ts1 == 1 or max_pages <= 1) or not (B <= 1 or ts0 >= max_pages) or kv_len.dtype is not i32 or \
+            kv_len.shape != (B,) or not kv_len.is_contiguous() or kv_len.get_device() != dev:
+        _need(where, False)
+    numbers = shape[:3]
+    es, ws, ps = _NO_STRIDES, _NO_STRIDES, _NO_STRIDES
+    ke = ve = 0
+    if (k_exp is not None) != e4m3 or (v_exp is not None) != e4m3:
+        _need(where, False)
     if e4m3:
-        c.exp_stride[:] = _slot_array(where, k_exp, torch.uint8, pages, slots, heads, dev)
-        _need(where, _slot_array(where, v_exp, torch.uint8, pages, slots, heads, dev) == k_exp.stride())
-        c.k_exp, c.v_exp = k_exp.data_ptr(), v_exp.data_ptr()
-    for arrays, dt, to in ((weight, torch.float32, c.weight_stride), (pos, torch.int32, c.pos_stride)):
-        first = None
-        for t in arrays:
-            if t is not None:
-                s = _slot_array(where, t, dt, pages, slots, heads, dev)
-                _need(where, first is None or first == s)
-                first = s
-        if first is not None:
-            to[:] = first
-    return c, dev
+        es = k_exp.stride()
+        for t in (k_exp, v_exp):
+            if t.dtype is not torch.uint8 or t.shape != numbers or t.stride() != es or t.get_device() != dev:
+                _need(where, False)
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    if weight is not None:
+        ws = weight.stride()
+        for t in (weight,) if weight_out is weight or weight_out is None else (weight, weight_out):
+            if t.dtype is not torch.float32 or t.shape != numbers or t.stride() != ws or t.get_device() != dev:
+                _need(where, False)
+    if pos is not None:
+        ps = pos.stride()
+        for t in (pos,) if pos_out is pos or pos_out is None else (pos, pos_out):
+            if t.dtype is not i32 or t.shape != numbers or t.stride() != ps or t.get_device() != dev:
+                _need(where, False)
+    pages, slots, heads, D = shape
+    try:
+        c = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, block_table.data_ptr(), kv_len.data_ptr(), pages,
+                        ts0, strides[0], strides[1], strides[2], *es, *ws, *ps, slots, max_pages, B, heads, D,
+                        THD_DTYPE_E4M3 if e4m3 else THD_DTYPE_BF16)
+    except struct.error:  # a size past the struct's
+        _need(where, False)
+    return c, B, heads, D, max_pages * slots, dev
 
 
-def _numbers(where, dev, *pairs):
+_NO_STRIDES = (0, 0, 0)
+
+
+def _numbers(where, dev, *triples):
     """Contiguous arrays of a call: (tensor or None, shape, dtype)."""
-    for t, shape, dtype in pairs:
-        if t is not None:
-            _need(where, t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev)
+    for t, shape, dtype in triples:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _need(where, False)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(*sizes):
+    return thd_decode_workspace_size(*sizes)
+
+
+@functools.lru_cache(maxsize=256)
+def _evict_bytes(*sizes):
+    return thd_evict_workspace_size(*sizes)
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None, k_exp=None, v_exp=None, weight=None,
@@ -957,18 +987,22 @@ def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None
     word to many calls, zeroed once."""
     import torch
     w = "thd_cache_append"
-    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight,), (pos,))
-    _need(w, k.dim() == 3 and k.dtype is torch.bfloat16 and k.get_device() == dev)
+    c, B, Hkv, D, _, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, None, pos, None)
+    if k.dim() != 3 or k.dtype is not torch.bfloat16 or k.get_device() != dev:
+        _need(w, False)
     T = k.shape[0]
-    s_k, s_v = _rope_rows(w, k, k, T, c.Hkv, c.D), _rope_rows(w, k, v, T, c.Hkv, c.D)
+    s_k, s_v = _row_stride(w, k, k, T, Hkv, D), _row_stride(w, k, v, T, Hkv, D)
     i32 = torch.int32
-    _numbers(w, dev, (cu_seqlens, (c.B + 1,), i32), (tokens_seen, (c.B,), i32), (dev_status, (1,), i32))
+    _numbers(w, dev, (cu_seqlens, (B + 1,), i32), (tokens_seen, (B,), i32), (dev_status, (1,), i32))
     side = _aside(stream)
-    with _alloc_on(side):
-        st = torch.zeros(1, dtype=i32, device=k.device) if dev_status is None else dev_status
+    st = dev_status
+    if st is None:
+        with _alloc_on(side):
+            st = torch.zeros(1, dtype=i32, device=k.device)
     _check(w, thd_cache_append(c, k, v, s_k, s_v, T, cu_seqlens, weight, pos, tokens_seen, st, stream))
-    _keep(side, stream, (k, v, k_cache, v_cache, block_table, kv_len, cu_seqlens, k_exp, v_exp, weight, pos, tokens_seen,
-                         dev_status), (st,))
+    if side is not None:
+        _keep(side, stream, (k, v, k_cache, v_cache, block_table, kv_len, cu_seqlens, k_exp, v_exp, weight, pos, tokens_seen,
+                             dev_status), (st,))
     return st
 
 
@@ -985,29 +1019,39 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_len, *, k_exp=None, v_exp=N
     w = "thd_attn_decode"
     if weight_out is None:
         weight_out = weight
-    _need(w, weight is not None or weight_out is None)
-    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight, weight_out), (pos,))
-    _need(w, q.dim() == 3 and q.dtype is torch.bfloat16 and q.get_device() == dev)
-    B, Hq, D = c.B, q.shape[1], c.D
-    s_q = _rope_rows(w, q, q, B, Hq, D)
+    c, B, Hkv, D, capacity, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos,
+                                         None)
+    if (weight is None) != (weight_out is None) or q.dim() != 3 or q.dtype is not torch.bfloat16 or \
+            q.get_device() != dev or workspace is not None and not (workspace.get_device() == dev and
+                                                                    workspace.is_contiguous()):
+        _need(w, False)
+    Hq = q.shape[1]
+    s_q = _row_stride(w, q, q, B, Hq, D)
     f32, i32 = torch.float32, torch.int32
-    _numbers(w, dev, (dist_slopes, (Hq,), f32), (kv_start, (B,), i32), (tokens_seen, (B,), i32),
-             (out, (B, Hq, D), torch.bfloat16), (lse, (Hq, B), f32), (dev_status, (1,), i32))
-    _need(w, workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+    if dev_status is not None:
+        _numbers(w, dev, (dev_status, (1,), i32))
+    if dist_slopes is not None or kv_start is not None or tokens_seen is not None:
+        _numbers(w, dev, (dist_slopes, (Hq,), f32), (kv_start, (B,), i32), (tokens_seen, (B,), i32))
+    if out is not None or lse is not None:
+        _numbers(w, dev, (out, (B, Hq, D), torch.bfloat16), (lse, (Hq, B), f32))
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    given = (q, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, dist_slopes, kv_start, pos, tokens_seen, weight,
-             weight_out, out, lse, dev_status, workspace)
     side = _aside(stream)
+    given = None if side is None else (q, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, dist_slopes, kv_start, pos,
+                                       tokens_seen, weight, weight_out, out, lse, dev_status, workspace)
+    at = q.device
     with _alloc_on(side):
-        o = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-        l = torch.empty((Hq, B), dtype=f32, device=q.device) if lse is None else lse
-        st = torch.zeros(1, dtype=i32, device=q.device) if dev_status is None else dev_status
+        o = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=at) if out is None else out
+        l = torch.empty((Hq, B), dtype=f32, device=at) if lse is None else lse
+        st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
         if workspace is None:
-            workspace = _workspace(thd_decode_workspace_size(B, Hq, c.Hkv, D, c.max_pages * c.page_size,
-                                                             int(weight is not None)), q.device)
+            size = _decode_bytes(B, Hq, Hkv, D, capacity, weight is not None)
+            workspace = torch.empty(size, dtype=torch.uint8, device=at)
+        else:
+            size = workspace.numel() * workspace.element_size()
     _check(w, thd_attn_decode(c, q, s_q, o, l, Hq, scale, softcap, dist_slopes, kv_start, pos, tokens_seen, weight,
-                              weight_out, workspace, workspace.numel() * workspace.element_size(), st, stream))
-    _keep(side, stream, given, (o, l, st))
+                              weight_out, workspace, size, st, stream))
+    if side is not None:
+        _keep(side, stream, given, (o, l, st))
     return o, l, st
 
 
@@ -1024,20 +1068,26 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
     weight_out = weight if weight_out is None else weight_out
     pos_out = pos if pos_out is None else pos_out
     _need(w, weight is not None and pos is not None)
-    c, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, (weight, weight_out), (pos, pos_out))
+    c, B, Hkv, _, capacity, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos,
+                                         pos_out)
     i32 = torch.int32
-    _need(w, tokens_seen is not None)
-    _numbers(w, dev, (tokens_seen, (c.B,), i32), (new_len, (c.B,), i32), (dev_status, (1,), i32))
-    _need(w, workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
-    given = (k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen, k_exp, v_exp, weight_out, pos_out, new_len,
-             dev_status, workspace)
+    if tokens_seen is None or workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
+        _need(w, False)
+    _numbers(w, dev, (tokens_seen, (B,), i32), (new_len, (B,), i32), (dev_status, (1,), i32))
     side = _aside(stream)
+    given = None if side is None else (k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen, k_exp, v_exp,
+                                       weight_out, pos_out, new_len, dev_status, workspace)
+    at = k_cache.device
     with _alloc_on(side):
-        n = torch.empty(c.B, dtype=i32, device=k_cache.device) if new_len is None else new_len
-        st = torch.zeros(1, dtype=i32, device=k_cache.device) if dev_status is None else dev_status
+        n = torch.empty(B, dtype=i32, device=at) if new_len is None else new_len
+        st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
         if workspace is None:
-            workspace = _workspace(thd_evict_workspace_size(c.B, c.Hkv, c.max_pages * c.page_size, budget), k_cache.device)
+            size = _evict_bytes(B, Hkv, capacity, budget)
+            workspace = torch.empty(size, dtype=torch.uint8, device=at)
+        else:
+            size = workspace.numel() * workspace.element_size()
     _check(w, thd_cache_evict(c, weight, weight_out, pos, pos_out, tokens_seen, budget, sinks, recent, n, workspace,
-                              workspace.numel() * workspace.element_size(), st, stream))
-    _keep(side, stream, given, (n, st))
+                              size, st, stream))
+    if side is not None:
+        _keep(side, stream, given, (n, st))
     return n, st
