@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
+#include "ptx.cuh"
 #include "vec8.cuh"
 
 namespace thd {
@@ -11,9 +12,9 @@ namespace thd {
 // ------------------------------------------------------------------ append
 // A block takes `tokens` rows; its first threads find each row's sequence (a
 // binary search of the offsets) and where its slot lies, then its warps walk
-// (token, head) pairs, the key's row on some lanes and the value's on others,
-// eight elements a lane, four pairs in flight.  Bound by HBM: the rows are read and
-// written once, 16 bytes a lane (8 written for e4m3).  The search and the page
+// (token, head) pairs, the key's row on some lanes and the value's on others, two
+// runs of eight elements a lane, three pairs in flight.  Bound by HBM: the rows are
+// read and written once, 16 bytes a lane (8 written for e4m3).  The search and the page
 // are three to six loads one after the other, so a block takes many rows where
 // there are many.
 //
@@ -93,15 +94,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     s_row[threadIdx.x] = out;
   }
   __syncthreads();
-  constexpr int kLanes = D / 8, kPairs = 32 / (2 * kLanes);  // of a row; a warp's (token, head) pairs at a time
-  constexpr int kAtOnce = 4, kStride = kPairs * kAppendThreads / 32;
+  constexpr int kLanes = D / 16, kPairs = 32 / (2 * kLanes);  // of a row; a warp's (token, head) pairs at a time
+  constexpr int kAtOnce = 3, kStride = kPairs * kAppendThreads / 32;
   const int lane = threadIdx.x & 31, piece = lane % kLanes, kv = lane / kLanes & 1;
-  const uint16_t* const in = p.in[kv] + t0 * p.in_stride[kv] + 8 * piece;
+  const uint16_t* const in = p.in[kv] + t0 * p.in_stride[kv] + 8 * piece;  // and D / 2 elements further
   uint8_t* const cache = (kv ? c.v : c.k) + (kFp8 ? 8 : 16) * piece;
   const int pairs = count * c.Hkv;
   // every lane walks alike: the exponent is a shuffle
   for (int r0 = (threadIdx.x >> 5) * kPairs; r0 < pairs; r0 += kAtOnce * kStride) {
-    Vec8<uint16_t> x[kAtOnce];
+    Vec8<uint16_t> x[kAtOnce][2];
     int tok[kAtOnce], g[kAtOnce];
     bool ok[kAtOnce];
 #pragma unroll
@@ -110,36 +111,46 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       tok[u] = r < pairs ? (int)(((uint64_t)(uint32_t)r * p.heads.mul) >> p.heads.shift) : 0;
       g[u] = r - tok[u] * c.Hkv;
       ok[u] = r < pairs && s_row[tok[u]].row >= 0;
-      x[u].v = make_uint4(0, 0, 0, 0);
-      if (ok[u]) x[u].load(in + tok[u] * p.in_stride[kv] + g[u] * D);
+      x[u][0].v = x[u][1].v = make_uint4(0, 0, 0, 0);
+      if (ok[u]) {
+        const uint16_t* const from = in + tok[u] * p.in_stride[kv] + g[u] * D;
+        x[u][0].load(from);
+        x[u][1].load(from + D / 2);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const AppendRow& to = s_row[tok[u]];
       uint8_t* const out = cache + to.row + g[u] * c.row.head;
       if (!kFp8) {
-        if (ok[u]) x[u].store(reinterpret_cast<uint16_t*>(out));
+        if (ok[u]) {
+          x[u][0].store(reinterpret_cast<uint16_t*>(out));
+          x[u][1].store(reinterpret_cast<uint16_t*>(out) + D / 2);
+        }
       } else {
-        const uint32_t w[4] = {x[u].v.x, x[u].v.y, x[u].v.z, x[u].v.w};
+        const uint32_t w[8] = {x[u][0].v.x, x[u][0].v.y, x[u][0].v.z, x[u][0].v.w, x[u][1].v.x, x[u][1].v.y, x[u][1].v.z, x[u][1].v.w};
         uint32_t big = 0;  // of both halves: a bf16's order is its bits'
 #pragma unroll
-        for (int q = 0; q < 4; ++q) big = __vmaxu2(big, w[q] & 0x7fff7fffu);
+        for (int q = 0; q < 8; ++q) big = __vmaxu2(big, w[q] & 0x7fff7fffu);
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, d));
         big = max(big >> 16, big & 0xffffu);
         const int e = row_exponent(big);
         const float inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-        float f[8];
-        x[u].get(f);
-        uint32_t y[2];
+        uint32_t y[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q] * inv, f[4 * q + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q + 2] * inv, f[4 * q + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-          y[q] = e == 255 ? 0x7f7f7f7fu : lo | hi << 16;
+        for (int q = 0; q < 4; ++q) {
+          float f[4];
+          fmul2(f[0], f[1], __uint_as_float(w[2 * q] << 16), __uint_as_float(w[2 * q] & 0xffff0000u), inv, inv);
+          fmul2(f[2], f[3], __uint_as_float(w[2 * q + 1] << 16), __uint_as_float(w[2 * q + 1] & 0xffff0000u), inv, inv);
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+          y[q] = lo | hi << 16;
         }
+        if (e == 255) y[0] = y[1] = y[2] = y[3] = 0x7f7f7f7fu;
         if (ok[u]) {
           *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+          *reinterpret_cast<uint2*>(out + D / 2) = make_uint2(y[2], y[3]);
           if (piece == 0) (kv ? c.v_exp : c.k_exp)[to.exp + g[u] * c.exp.head] = (uint8_t)e;
         }
       }
