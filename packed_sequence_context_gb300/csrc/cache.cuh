@@ -88,10 +88,11 @@ struct DecodeParams {
   int64_t* units;   // [B + 1] units in front of each sequence
   float* part;      // [2 grid][heads of an item][D]
   float* part_ml;   // [2 grid][heads of an item][3]
-  DecodeJoin* joins;  // [grid]
+  DecodeJoin* joins;  // [items], or of the items that end in a block's share [grid]
   float* lse2;      // [B][Hq] in base 2, with weights
   float* scores;    // [B][Hkv][capacity][G], with weights
   int grid;
+  bool by_item;
 };
 
 struct EvictParams {

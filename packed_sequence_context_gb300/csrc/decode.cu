@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
       for (int i = tid; i < p.Hq * D / 8; i += kDecThreads)
         reinterpret_cast<uint4*>(p.o + (int64_t)b * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
       for (int h = tid; h < p.Hq; h += kDecThreads) p.lse[(int64_t)h * c.B + b] = -INFINITY;
+      if (p.by_item)
+        for (int i = tid; i < c.Hkv * p.blocks; i += kDecThreads) p.joins[b * c.Hkv * p.blocks + i].count = 0;
     }
   }
   if (blockIdx.x == 0) {
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
   const int HG = c.Hkv * p.blocks;  // items of a sequence
   const int64_t total = s_seg[kDecThreads] * HG;
   const int64_t blocks = blocks_for(total, (int)gridDim.x);
-  if (tid == 0) p.joins[blockIdx.x].count = 0;
+  if (tid == 0 && !p.by_item) p.joins[blockIdx.x].count = 0;
   if (blockIdx.x >= blocks) return;
   int64_t u = blockIdx.x * total / blocks;
   const int64_t u_end = (blockIdx.x + 1) * total / blocks;
@@ -769,11 +771,12 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
     }
     __syncthreads();
     const bool whole = cur.i0 == 0 && cur.last;
-    if (tid == 0 && !whole && cur.last) {
+    if (tid == 0 && cur.last && (!whole || p.by_item)) {
       // the item's last block names its parts: the first block's is in that
       // one's second slot, the others' in their first
-      const int64_t first = owner_of(cur.at + kLead, total, blocks);
-      p.joins[blockIdx.x] = DecodeJoin{b, g * p.G + h0, heads, (int)first, (int)(blockIdx.x - first) + 1};
+      const int64_t first = whole ? 0 : owner_of(cur.at + kLead, total, blocks);
+      p.joins[p.by_item ? b * HG + g * p.blocks + h0 / S::kHeads : blockIdx.x] =
+          DecodeJoin{b, g * p.G + h0, heads, (int)first, whole ? 0 : (int)(blockIdx.x - first) + 1};
     }
     const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.i0 > 0 ? 0 : 1);
     for (int i = tid; i < heads * (D / 4); i += kDecThreads) {
@@ -831,7 +834,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
 
 // ------------------------------------------------------------------ the join
 // The parts of an item that several blocks shared: a block of 128 threads for
-// each (block that ended one, head), four parts at a time, a head's row across
+// each (item or block that ended one, head), four parts at a time, a head's row across
 // the lanes.  The sums run over the parts in order, four interleaved.
 constexpr int kJoinThreads = 128;
 
@@ -912,84 +915,66 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
 }
 
 // ------------------------------------------------------------------ the weights
-// From the scores and the finished log-sum-exps: a block takes a contiguous run
-// of the units of (sequence, kv head) pairs, a thread up to four slots at a time.
-// 4 G + 8 bytes a slot and kv head, the scores mostly from L2.
-constexpr int kWeightThreads = 256;
+// From the scores and the finished log-sum-exps, 4 G + 8 bytes a slot and kv head,
+// the scores mostly from L2: `share` blocks for each (sequence, kv head), every
+// one of them runs of 1024 slots, four a thread.  Where the numbers lie and what
+// they were is found while the kernels in front still run.
+constexpr int kWeightThreads = 256, kWeightSlots = 4;
 
-__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const DecodeParams p, int share) {
   __shared__ float s_lse[kDecodeMaxGroup];
   const CacheView& c = p.c;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, pair = (int)(blockIdx.x / share), b = pair / c.Hkv, g = pair % c.Hkv;
   follow();
-  depend();
-  const int64_t all = p.units[c.B] * c.Hkv;
-  int64_t u = blockIdx.x * all / gridDim.x;
-  const int64_t u_end = (blockIdx.x + 1) * all / gridDim.x;
-  while (u < u_end) {
-    const int64_t ub = u / c.Hkv;
-    int lo = 0, hi = c.B - 1;  // the sequence: the last with no more than ub in front of it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.units[mid] <= ub) lo = mid; else hi = mid - 1;
-    }
-    const int b = lo;
-    const int64_t cost = p.units[b + 1] - p.units[b], r = u - p.units[b] * c.Hkv;
-    const int g = (int)(r / cost);
-    const int64_t ic = r - g * cost;
-    const int64_t take = u_end - u < cost - ic ? u_end - u : cost - ic;
-    u += take;
-    if (ic + take <= kLead) continue;
-    for (int n = tid; n < p.G; n += kWeightThreads) {
-      const float z = p.lse2[(int64_t)b * p.Hq + g * p.G + n];
-      s_lse[n] = z == -INFINITY ? INFINITY : z;
-    }
-    __syncthreads();
-    const Range rg = range_of(p, b);
-    const int k0 = rg.s + (int)(ic > kLead ? ic - kLead : 0) * kUnit;
-    const int64_t k_end = rg.s + (ic + take - kLead) * kUnit;
-    const int k1 = k_end < rg.n ? (int)k_end : rg.n;
-    const float* const scores = p.scores + ((int64_t)b * c.Hkv + g) * c.capacity * p.G;
-    for (int j0 = k0; j0 < k1; j0 += 4 * kWeightThreads) {
-      int64_t a[4];
-      float w[4];
+  const Range rg = range_of(p, b);
+  const float* const scores = p.scores + ((int64_t)b * c.Hkv + g) * c.capacity * p.G;
+  constexpr int kRun = kWeightThreads * kWeightSlots;
+  bool waited = false;
+  for (int64_t j0 = rg.s + (int64_t)(blockIdx.x % share) * kRun; j0 < rg.n; j0 += (int64_t)share * kRun) {
+    int64_t a[kWeightSlots];
+    float w[kWeightSlots];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int j = j0 + x * kWeightThreads + tid;
-        a[x] = -1;
-        if (j < k1) {
-          const Place to = place_of(c, j);
-          const int page = page_of(c, b, to.page);
-          if (page >= 0) a[x] = at(p.weight_at, page, to.slot, g);
-        }
+    for (int x = 0; x < kWeightSlots; ++x) {
+      const int64_t j = j0 + x * kWeightThreads + tid;
+      a[x] = -1;
+      if (j < rg.n) {
+        const Place to = place_of(c, (int)j);
+        const int page = page_of(c, b, to.page);
+        if (page >= 0) a[x] = at(p.weight_at, page, to.slot, g);
       }
+    }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        w[x] = a[x] < 0 ? 0.f : p.weight_in[a[x]];
+    for (int x = 0; x < kWeightSlots; ++x) w[x] = a[x] < 0 ? 0.f : p.weight_in[a[x]];
+    if (!waited) {
+      waited = true;
+      depend();
+      for (int n = tid; n < p.G; n += kWeightThreads) {
+        const float z = p.lse2[(int64_t)b * p.Hq + g * p.G + n];
+        s_lse[n] = z == -INFINITY ? INFINITY : z;
       }
+      __syncthreads();
+    }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int j = j0 + x * kWeightThreads + tid;
-        if (a[x] < 0) continue;
-        const float* const s = scores + (int64_t)j * p.G;
-        float sum = 0.f;
-        if (p.G % 4 == 0) {
+    for (int x = 0; x < kWeightSlots; ++x) {
+      if (a[x] < 0) continue;
+      const float* const s = scores + (j0 + x * kWeightThreads + tid) * p.G;
+      float sum = 0.f;
+      if (p.G % 4 == 0) {
 #pragma unroll 4
-          for (int n = 0; n < p.G; n += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(s + n);
-            sum += ex2(y.x - s_lse[n]) + ex2(y.y - s_lse[n + 1]) + (ex2(y.z - s_lse[n + 2]) + ex2(y.w - s_lse[n + 3]));
-          }
-        } else {
-          for (int n = 0; n < p.G; ++n) sum += ex2(s[n] - s_lse[n]);
+        for (int n = 0; n < p.G; n += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(s + n);
+          sum += ex2(y.x - s_lse[n]) + ex2(y.y - s_lse[n + 1]) + (ex2(y.z - s_lse[n + 2]) + ex2(y.w - s_lse[n + 3]));
         }
-        w[x] += sum;
+      } else {
+        for (int n = 0; n < p.G; ++n) sum += ex2(s[n] - s_lse[n]);
       }
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (a[x] >= 0) p.weight_out[a[x]] = w[x];
+      w[x] += sum;
     }
-    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kWeightSlots; ++x)
+      if (a[x] >= 0) p.weight_out[a[x]] = w[x];
   }
+  if (!waited) depend();  // no block of a kernel ends before what it follows: the next one counts on that
 }
 
 // ------------------------------------------------------------------ launch
@@ -1001,6 +986,7 @@ static cudaError_t launch_decode_t(DecodeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int wave = S::kPerSm * num_sms(), most = decode_blocks(p.c.B, p.c.Hkv, p.G, p.c.capacity);
   p.grid = wave < most ? wave : most;
+  p.by_item = (int64_t)p.c.B * p.c.Hkv * p.blocks <= p.grid;
   prof_before(THD_KERNEL_DECODE, st);
   decode_kernel<kFp8, D, NT><<<(unsigned)p.grid, kDecThreads, S::kSmem, st>>>(p);
   count_launch();
@@ -1023,15 +1009,23 @@ cudaError_t launch_decode(DecodeParams p, cudaStream_t st) {
   cudaError_t e = p.c.k_exp ? launch_decode_d<true>(p, heads, st) : launch_decode_d<false>(p, heads, st);
   if (e != cudaSuccess) return e;
   if (p.c.capacity > kUnit) {  // an item of one unit is one block's
+    const int64_t items = (int64_t)p.c.B * p.c.Hkv * p.blocks;
     prof_before(THD_KERNEL_DECODE_JOIN, st);
     e = launch_following(p.c.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
-                         dim3((unsigned)p.grid, (unsigned)heads), kJoinThreads, 0, st, (const DecodeParams)p, (int)heads);
+                         dim3((unsigned)(p.by_item ? items : p.grid), (unsigned)heads), kJoinThreads, 0, st, (const DecodeParams)p,
+                         (int)heads);
     prof_after(THD_KERNEL_DECODE_JOIN, st);
     if (e != cudaSuccess) return e;
   }
   if (p.weight_out) {
+    // as many blocks as eight an SM, or the slots, ask for
+    const int64_t pairs = (int64_t)p.c.B * p.c.Hkv, run = kWeightThreads * kWeightSlots;
+    const int64_t most = (p.c.capacity + run - 1) / run, want = (8LL * num_sms() + pairs - 1) / pairs;
+    const int64_t share = most < want ? most : want;
+    if (pairs * share >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
     prof_before(THD_KERNEL_DECODE_WEIGHTS, st);
-    e = launch_following(decode_weights_kernel, dim3((unsigned)(8 * num_sms())), kWeightThreads, 0, st, (const DecodeParams)p);
+    e = launch_following(decode_weights_kernel, dim3((unsigned)(pairs * share)), kWeightThreads, 0, st, (const DecodeParams)p,
+                         (int)share);
     prof_after(THD_KERNEL_DECODE_WEIGHTS, st);
   }
   return e;
