@@ -77,11 +77,11 @@ THD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 numbers (low half) as two fp16, exactly.
-THD_DEV uint32_t e4m3x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
-  return y;
+// Four e4m3 numbers as two pairs of fp16, exactly.
+THD_DEV void e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 template <bool kHalf>
 THD_DEV uint32_t pack2(float lo, float hi) {
@@ -520,8 +520,11 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
             uint32_t r[4];
             ldsm4(r, (kt ^ (kp << 5)) + sub * kSubBytes);
             if (kFp8) {
-              const uint32_t a0[4] = {e4m3x2(r[0]), e4m3x2(r[1]), e4m3x2(r[0] >> 16), e4m3x2(r[1] >> 16)};
-              const uint32_t a1[4] = {e4m3x2(r[2]), e4m3x2(r[3]), e4m3x2(r[2] >> 16), e4m3x2(r[3] >> 16)};
+              uint32_t a0[4], a1[4];
+              e4m3x4(r[0], a0[0], a0[2]);
+              e4m3x4(r[1], a0[1], a0[3]);
+              e4m3x4(r[2], a1[0], a1[2]);
+              e4m3x4(r[3], a1[1], a1[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma16816<true>(s[sub][nt], a0, bq[0][nt].x, bq[0][nt].y);
@@ -689,8 +692,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
               ldsm4t(r, (vt ^ (dp << 5)) + kDecTile / 2 + sub * kSubBytes);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint32_t y0 = __byte_perm(r[2 * x], 0, 0x3120), y1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-                const uint32_t a[4] = {e4m3x2(y0), e4m3x2(y0 >> 16), e4m3x2(y1), e4m3x2(y1 >> 16)};
+                uint32_t a[4];
+                e4m3x4(__byte_perm(r[2 * x], 0, 0x3120), a[0], a[1]);
+                e4m3x4(__byte_perm(r[2 * x + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma16816<true>(o[(kFp8 ? 2 * dp + x : 0)][nt], a, pb[sub][nt][0], pb[sub][nt][1]);
