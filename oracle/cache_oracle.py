@@ -81,8 +81,9 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
       for up to 64 x 1024 slots);
     * next to e4m3 keys, queries as fp16, off by at most 2^-39 of a head's
       largest element (elements far below it; 0 for the others);
-    * probabilities rounded to bf16 (2^-8), or next to e4m3 values to fp16 (2^-11,
-      and 2^-32 of the largest), the output to bf16 (2^-8).
+    * probabilities rounded to bf16 (2^-8; 2^-16, as two numbers, up to 16 query
+      heads a kv head), or next to e4m3 values to fp16 (2^-11, and 2^-32 of the
+      largest), the output to bf16 (2^-8).
     """
     q = np.asarray(q, np.float64)
     B, Hq, D = q.shape
@@ -92,7 +93,7 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
     tol_o, tol_lse = np.full((B, Hq, D), 1e-30), np.zeros((Hq, B))
     w = None if weight is None else np.asarray(weight, np.float64).copy()
     tol_w = None if weight is None else np.zeros(w.shape)
-    half = 2.0 ** -11 if e4m3 else 2.0 ** -8
+    half = 2.0 ** -11 if e4m3 else 2.0 ** -16 if G <= 16 else 2.0 ** -8
     for b in range(B):
         s0 = 0 if start is None else min(max(int(start[b]), 0), int(kv_len[b]))
         p, at = (x[s0:] for x in slots(table[b], int(kv_len[b]), page))
