@@ -639,7 +639,8 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  *     else they do not overlap).
  *   Lengths are read on the device: a captured graph serves growing ones.
  * Bit-reproducible on one kind of GPU.  Launches: 2 (1 for tables of at most 64
- * slots), with weights one more.  Workspace: thd_decode_workspace_size.
+ * slots), with weights one more.  Workspace: thd_decode_workspace_size; calls that
+ * may run at the same time need one each.
  */
 THD_API int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, void* o, float* lse, int Hq,
                             float softmax_scale, float softcap, const float* dist_slopes, const int32_t* kv_start,
@@ -663,7 +664,7 @@ THD_API size_t thd_decode_workspace_size(int B, int Hq, int Hkv, int D, int64_t 
  * slots in front of the budget stay where they are; the i-th kept slot behind
  * it moves into the i-th evicted slot in front of it: keys, values, exponents,
  * weight and pos.  Slots behind the budget are left as they were.
- *   new_len: int32 [B] = min(n, budget); not kv_len itself.
+ *   new_len: int32 [B] = min(n, budget); neither kv_len nor tokens_seen.
  *   weight_out, pos_out: may be weight_in, pos_in (then only moved numbers are
  *     written), else they get those of all slots below new_len.
  *   0 < budget; sinks, recent >= 0.

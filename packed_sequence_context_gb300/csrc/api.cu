@@ -948,7 +948,8 @@ static SlotStrides slot_strides(const int64_t (&s)[3], int64_t bytes) {
 static int check_cache(const thd_kv_cache* c, CacheView* v) {
   if (!c) return THD_ERR_INVALID_ARG;
   if (c->B < 1 || c->B >= (1 << 24) || c->Hkv < 1 || c->Hkv > (1 << 20) || c->page_size < 1 || c->max_pages < 1 ||
-      c->num_pages < 1 || c->num_pages >= ((int64_t)1 << 31) || (c->B > 1 && c->table_stride < c->max_pages))
+      c->num_pages < 1 || c->num_pages >= ((int64_t)1 << 31) ||
+      (c->B > 1 && c->table_stride != 0 && c->table_stride < c->max_pages))
     return THD_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return THD_ERR_UNSUPPORTED;
   if (c->dtype != THD_DTYPE_BF16 && c->dtype != THD_DTYPE_E4M3) return THD_ERR_UNSUPPORTED;
@@ -1110,7 +1111,8 @@ int thd_cache_evict(const thd_kv_cache* cache, const float* weight_in, float* we
   if (budget < 1 || sinks < 0 || recent < 0) return THD_ERR_INVALID_ARG;
   if (!weight_in || !weight_out || !pos_in || !pos_out || !tokens_seen || !new_len || !dev_status ||
       !aligned(weight_in, 4) || !aligned(weight_out, 4) || !aligned(pos_in, 4) || !aligned(pos_out, 4) ||
-      !aligned(tokens_seen, 4) || !aligned(new_len, 4) || !aligned(dev_status, 4) || new_len == cache->kv_len)
+      !aligned(tokens_seen, 4) || !aligned(new_len, 4) || !aligned(dev_status, 4) || new_len == cache->kv_len ||
+      new_len == tokens_seen)
     return THD_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, thd_evict_workspace_size(cache->B, cache->Hkv, p.c.capacity, budget));
   if (rc != THD_OK) return rc;

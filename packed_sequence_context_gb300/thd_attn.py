@@ -20,7 +20,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import math
 import os
 import struct
@@ -902,14 +901,24 @@ def _row_stride(where, like, t, T, H, D):
     return _rope_rows(where, like, t, T, H, D)
 
 
+def _slot_strides(t):
+    """Strides of the first three dimensions; one of size 1 may carry any."""
+    s = t.stride()
+    if 1 in t.shape:
+        s = tuple(0 if n == 1 else x for n, x in zip(t.shape[:3], s)) + s[3:]
+    return s
+
+
 def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos, pos_out):
     """The cache of a call as thd_kv_cache's bytes, its B, Hkv, D and slots of
     a table's row, and the device."""
     import torch
     dev = _current(where, k_cache)
-    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype is not dtype or \
-            v_cache.get_device() != dev or strides[3] != 1:
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
+        _need(where, False)
+    strides = _slot_strides(k_cache)
+    if _slot_strides(v_cache) != strides or v_cache.dtype is not dtype or v_cache.get_device() != dev or strides[3] != 1:
         _need(where, False)
     e4m3 = dtype is torch.float8_e4m3fn
     if not e4m3 and dtype is not torch.bfloat16:
@@ -919,7 +928,7 @@ def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, w
         _need(where, False)
     B, max_pages = block_table.shape
     ts0, ts1 = block_table.stride()
-    if not (ts1 == 1 or max_pages <= 1) or not (B <= 1 or ts0 >= max_pages) or kv_len.dtype is not i32 or \
+    if not (ts1 == 1 or max_pages <= 1) or not (B <= 1 or ts0 == 0 or ts0 >= max_pages) or kv_len.dtype is not i32 or \
             kv_len.shape != (B,) or not kv_len.is_contiguous() or kv_len.get_device() != dev:
         _need(where, False)
     numbers = shape[:3]
@@ -928,20 +937,20 @@ def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, w
     if (k_exp is not None) != e4m3 or (v_exp is not None) != e4m3:
         _need(where, False)
     if e4m3:
-        es = k_exp.stride()
+        es = _slot_strides(k_exp) if k_exp.dim() == 3 else None
         for t in (k_exp, v_exp):
-            if t.dtype is not torch.uint8 or t.shape != numbers or t.stride() != es or t.get_device() != dev:
+            if t.dtype is not torch.uint8 or t.shape != numbers or _slot_strides(t) != es or t.get_device() != dev:
                 _need(where, False)
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     if weight is not None:
-        ws = weight.stride()
+        ws = _slot_strides(weight) if weight.dim() == 3 else None
         for t in (weight,) if weight_out is weight or weight_out is None else (weight, weight_out):
-            if t.dtype is not torch.float32 or t.shape != numbers or t.stride() != ws or t.get_device() != dev:
+            if t.dtype is not torch.float32 or t.shape != numbers or _slot_strides(t) != ws or t.get_device() != dev:
                 _need(where, False)
     if pos is not None:
-        ps = pos.stride()
+        ps = _slot_strides(pos) if pos.dim() == 3 else None
         for t in (pos,) if pos_out is pos or pos_out is None else (pos, pos_out):
-            if t.dtype is not i32 or t.shape != numbers or t.stride() != ps or t.get_device() != dev:
+            if t.dtype is not i32 or t.shape != numbers or _slot_strides(t) != ps or t.get_device() != dev:
                 _need(where, False)
     pages, slots, heads, D = shape
     try:
@@ -961,16 +970,6 @@ def _numbers(where, dev, *triples):
     for t, shape, dtype in triples:
         if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
             _need(where, False)
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_bytes(*sizes):
-    return thd_decode_workspace_size(*sizes)
-
-
-@functools.lru_cache(maxsize=256)
-def _evict_bytes(*sizes):
-    return thd_evict_workspace_size(*sizes)
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None, k_exp=None, v_exp=None, weight=None,
@@ -1044,7 +1043,7 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_len, *, k_exp=None, v_exp=N
         l = torch.empty((Hq, B), dtype=f32, device=at) if lse is None else lse
         st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
         if workspace is None:
-            size = _decode_bytes(B, Hq, Hkv, D, capacity, weight is not None)
+            size = thd_decode_workspace_size(B, Hq, Hkv, D, capacity, weight is not None)
             workspace = torch.empty(size, dtype=torch.uint8, device=at)
         else:
             size = workspace.numel() * workspace.element_size()
@@ -1082,7 +1081,7 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
         n = torch.empty(B, dtype=i32, device=at) if new_len is None else new_len
         st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
         if workspace is None:
-            size = _evict_bytes(B, Hkv, capacity, budget)
+            size = thd_evict_workspace_size(B, Hkv, capacity, budget)
             workspace = torch.empty(size, dtype=torch.uint8, device=at)
         else:
             size = workspace.numel() * workspace.element_size()

@@ -168,6 +168,54 @@ def test_decode_scores(cap, bias, docs, pos, fp8):
     _decode(c, q, cap=cap, slopes=slopes, start=start, pos=pos, seen=np.array(lens) + (1 << 20) if pos else None, weight=True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_many_short_sequences(fp8):
+    """More sequences than threads and items than blocks, empty ones among them."""
+    lens = np.random.default_rng(3).integers(0, 90, 700)
+    lens[:5] = lens[-3:] = lens[200:210] = 0
+    c = Cache(lens, page=16, Hkv=2, D=64, fp8=fp8, seed=23)
+    q = torch.randn(700, 4, 64, device="cuda").to(torch.bfloat16)
+    _decode(c, q, start=np.random.default_rng(4).integers(-3, 80, 700), weight=True)
+
+
+@pytest.mark.parametrize("fp8,G", [(False, 512), (True, 100), (False, 65)])
+def test_decode_large_groups(fp8, G):
+    c = Cache([700, 0, 65], page=16, Hkv=1, D=64, fp8=fp8, seed=25)
+    q = torch.randn(3, G, 64, device="cuda").to(torch.bfloat16)
+    _decode(c, q, weight=True)
+
+
+def test_decode_one_table_row_for_all():
+    """Beams of one prompt: the same pages, other lengths."""
+    c = Cache([300], page=16, Hkv=2, D=64, seed=27)
+    q = torch.randn(4, 4, 64, device="cuda").to(torch.bfloat16)
+    n = _cuda([300, 17, 0, 250])
+    o, lse, st = T.attn_decode(q, c.k, c.v, c.table.expand(4, -1), n)
+    _status(st)
+    want = T.attn_decode(q, c.k, c.v, c.table.repeat(4, 1), n)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    ref = co.decode(_np(q), c.host(), np.repeat(c.table_np, 4, 0), [300, 17, 0, 250], scale=np.float32(0.125))
+    assert np.all(np.abs(_np(o) - ref["o"]) <= ref["tol_o"])
+
+
+def test_decode_two_streams_at_once():
+    """Calls that overlap, each with its own workspace, next to one another's results."""
+    cs = [Cache([4000, 123], page=16, Hkv=2, D=64, seed=s) for s in (81, 82)]
+    q = torch.randn(2, 8, 64, device="cuda").to(torch.bfloat16)
+    want = [T.attn_decode(q, *c.args()) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            got[i].append(T.attn_decode(q, *cs[i].args(), stream=st))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for o, lse, st in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]) and int(st.item()) == 0
+
+
 def test_decode_slices_and_strides():
     """q out of a fused projection, cache pools that are slices of larger tensors, a table wider than it is used."""
     c = Cache([100, 257], page=16, Hkv=2, D=64, seed=31, wide=40)

@@ -186,3 +186,36 @@ def test_helpers_allocate_from_the_launch_stream(fakes, name):  # noqa: F811
     for t in kw.values():
         if isinstance(t, torch.Tensor):
             assert recorded.get(t.data_ptr()) == {64}
+
+
+def test_the_helpers_bytes_are_the_struct(lib, thd_lib):  # noqa: F811
+    """What the helpers pack is thd_kv_cache, field by field."""
+    import ctypes
+    _, kw = _ok(True)["append"]
+    kw["k_cache"], kw["v_cache"] = (torch.zeros((6, 2, 4, 64), dtype=torch.float8_e4m3fn).transpose(1, 2) for _ in range(2))
+    kw["block_table"] = torch.zeros((3, 9), dtype=torch.int32)[:, 2:4]
+    raw = T._cache("x", *(kw[n] for n in ("k_cache", "v_cache", "block_table", "kv_len", "k_exp", "v_exp", "weight")), None,
+                   kw["pos"], None)[0]
+    assert len(raw) == ctypes.sizeof(T.KvCache)
+    c = T.KvCache.from_buffer_copy(raw)
+    for field, arg in (("k", "k_cache"), ("v", "v_cache"), ("k_exp", "k_exp"), ("v_exp", "v_exp"), ("block_table", "block_table"),
+                       ("kv_len", "kv_len")):
+        assert getattr(c, field) == kw[arg].data_ptr(), field
+    assert (c.num_pages, c.table_stride, c.page_size, c.max_pages, c.B, c.Hkv, c.D, c.dtype) == (6, 9, 4, 2, 3, 2, 64, T.THD_DTYPE_E4M3)
+    assert list(c.kv_stride) == [512, 64, 256] and list(c.exp_stride) == [8, 2, 1] == list(c.weight_stride) == list(c.pos_stride)
+
+
+def test_dimensions_of_size_one_may_carry_any_stride(lib):  # noqa: F811
+    f, kw = _ok(False)["append"]
+    one = lambda dt, *tail: torch.zeros((6, 4, 1, *tail), dtype=dt).as_strided((6, 4, 1, *tail), (256, 64, 3, 1)[:3 + len(tail)])  # noqa: E731
+    kw = {**kw, "k": kw["k"][:, :1].contiguous(), "v": kw["v"][:, :1].contiguous(), "k_cache": one(torch.bfloat16, 64),
+          "v_cache": torch.zeros((6, 4, 1, 64), dtype=torch.bfloat16), "weight": None, "pos": None}
+    f(**kw)
+    c = T.KvCache.from_buffer_copy(lib.calls[-1][1][0])
+    assert list(c.kv_stride) == [256, 64, 0]
+
+
+def test_one_table_row_for_all(lib):  # noqa: F811
+    f, kw = _ok(False)["decode"]
+    f(**{**kw, "block_table": torch.zeros((1, 2), dtype=torch.int32).expand(3, 2)})
+    assert T.KvCache.from_buffer_copy(lib.calls[-1][1][0]).table_stride == 0
