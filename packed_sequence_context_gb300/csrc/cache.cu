@@ -24,7 +24,7 @@ namespace thd {
 // (a scale of max / 448 would round twice and gain nothing but the last half
 // binade).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 32;  // at most, a block
+constexpr int kAppendTokens = 64;  // at most, a block
 
 // The stored exponent of a row whose largest magnitude (bf16, sign off) is
 // `big`: 448 = 1.75 * 2^8, so 2^(x - 8) serves up to a mantissa of 1.75.  No
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
   AppendParams p = a;
-  const int64_t n = (a.T + 8 * num_sms() - 1) / (8 * num_sms());  // eight blocks an SM first
+  const int64_t n = (a.T + 16 * num_sms() - 1) / (16 * num_sms());  // 16 blocks an SM first
   p.tokens = (int)(n > kAppendTokens ? kAppendTokens : n);
   p.heads = divisor((uint32_t)a.c.Hkv);
   const unsigned grid = (unsigned)((a.T + p.tokens - 1) / p.tokens);
@@ -184,8 +184,9 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
 // One cluster of `share` blocks an item (sequence, kv head).  Every block holds
 // its part of the slots' weights in shared memory as integers of the same
 // order (protected slots on top), so they are read once; the budget-th largest
-// is found by its four 8-bit digits (a histogram each, added up over the cluster
-// through distributed shared memory), ties and the slots to move are numbered by
+// is found by its 8-bit digits (a histogram each, added up over the cluster
+// through distributed shared memory; after two of them the candidates are mostly
+// few enough to be compared), ties and the slots to move are numbered by
 // counts and ballots, and the cluster's blocks then move rows.  Kept
 // slots in front of the budget stay where they are and evicted ones there take
 // the kept ones behind it, in order: the fewest bytes that can move, sources
@@ -196,6 +197,7 @@ namespace cg = cooperative_groups;
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 256;
+constexpr int kFew = 1024;             // candidates that are compared with one another
 constexpr int kEvictMaxHeld = 40960;  // keys in a block's shared memory (160 KB)
 
 __device__ inline uint32_t order_of(float w, bool kept) {
@@ -208,7 +210,8 @@ __device__ inline uint32_t order_of(float w, bool kept) {
 __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t s_key[];  // [held]
   __shared__ uint32_t s_hist[kBins], s_scan[kBins / 32];
-  __shared__ uint32_t s_digit, s_left;
+  __shared__ uint32_t s_digit, s_left, s_many, s_mine;
+  __shared__ __align__(16) uint16_t s_few[kFew], s_their[kFew];
   // larger and equal keys in front of the budget and behind it: a warp's, a block's
   __shared__ uint4 s_cnt[kEvictWarps], s_sum;
   const CacheView& c = p.c;
@@ -296,12 +299,62 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
       if (inc - mine < left && left <= inc) {
         s_digit = (uint32_t)bin;
         s_left = left - (inc - mine);
+        s_many = mine;
       }
     }
     cluster.sync();  // also: every block has read the histograms
     prefix |= s_digit << shift;
     mask |= (uint32_t)(kBins - 1) << shift;
     left = s_left;
+    // Half of the key is known.  If few slots share it, every block takes all
+    // their other halves and compares each with each: two rounds of sums over
+    // the cluster less.
+    const uint32_t many = s_many;
+    if (shift != 16 || many > kFew) continue;
+    if (tid == 0) s_mine = 0;
+    __syncthreads();
+    for (int i = lo + tid; i < hi; i += kEvictThreads) {
+      const uint32_t k = key(i);
+      if ((k & mask) == prefix) s_few[atomicAdd(&s_mine, 1u)] = (uint16_t)k;
+    }
+    cluster.sync();
+    uint32_t count = lane < p.share ? *cluster.map_shared_rank(&s_mine, lane) : 0u, first = count;
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, first, d);
+      if (lane >= d) first += y;
+    }
+    first -= count;
+    for (int r = 0; r < p.share; ++r) {
+      const uint32_t n_r = __shfl_sync(0xffffffffu, count, r), at_r = __shfl_sync(0xffffffffu, first, r);
+      const uint16_t* const from = cluster.map_shared_rank(s_few, r);
+      for (uint32_t i = tid; i < n_r; i += kEvictThreads) s_their[at_r + i] = from[i];
+    }
+    const uint32_t whole = (many + 7) & ~7u;  // padded with the smallest; none of those is counted
+    if (many + tid < whole) s_their[many + tid] = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < many; i += kEvictThreads) {
+      const uint32_t me = s_their[i];
+      uint32_t larger = 0, equal = 0;
+      for (uint32_t j = 0; j < whole; j += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(s_their + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          larger += ((w[q] & 0xffffu) > me ? 1u : 0u) + ((w[q] >> 16) > me ? 1u : 0u);
+          equal += ((w[q] & 0xffffu) == me ? 1u : 0u) + ((w[q] >> 16) == me ? 1u : 0u);
+        }
+      }
+      if (me == 0) equal -= whole - many;
+      if (larger < left && left <= larger + equal) {  // so says every thread that has this number
+        s_digit = me;
+        s_left = left - larger;
+      }
+    }
+    __syncthreads();
+    prefix |= s_digit;
+    left = s_left;
+    break;
   }
   // Kept: keys above `prefix`, and the first `left` slots equal to it.  Every warp
   // counts both kinds in its slots, in front of the budget and behind it; which
@@ -441,12 +494,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
   }
   if (copy_w || copy_p) {  // what stays, to the other arrays
     const int m = hi - lo < p.held ? hi - lo : p.held, end = p.budget - lo < m ? p.budget - lo : m;
-    for (int i0 = tid; i0 < end; i0 += 4 * kEvictThreads) {
-      int64_t a[4], q[4];
-      float w[4];
-      int number[4];
+    constexpr int kAtOnce = 4;
+    for (int i0 = tid; i0 < end; i0 += kAtOnce * kEvictThreads) {
+      int64_t a[kAtOnce], q[kAtOnce];
+      float w[kAtOnce];
+      int number[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAtOnce; ++u) {
         const int i = i0 + u * kEvictThreads;
         a[u] = -1;
         if (i < end && s_key[i]) {
@@ -456,10 +510,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
         if (a[u] >= 0) w[u] = p.weight_in[a[u]], number[u] = p.pos_in[q[u]];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
         if (a[u] >= 0) {
           if (copy_w) p.weight_out[a[u]] = w[u];
           if (copy_p) p.pos_out[q[u]] = number[u];
