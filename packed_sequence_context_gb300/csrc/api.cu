@@ -1011,16 +1011,15 @@ int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, in
   return cuda_status(launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Workspace of a decode: [units][joins][part][part_ml][lse2][scores].
+// Workspace of a decode: [joins][part][part_ml][lse2][scores].
 struct DecodeWs {
-  size_t units, joins, part, part_ml, lse2, scores, total;
+  size_t joins, part, part_ml, lse2, scores, total;
 };
 static DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int64_t capacity, bool weights) {
   const size_t heads = (size_t)decode_heads(Hq / Hkv), blocks = (size_t)decode_blocks(B, Hkv, Hq / Hkv, capacity);
   DecodeWs w;
-  w.units = 0;
-  w.joins = align_up(sizeof(int64_t) * ((size_t)B + 1), 256);
-  w.part = align_up(w.joins + sizeof(DecodeJoin) * blocks, 256);
+  w.joins = 0;
+  w.part = align_up(sizeof(DecodeJoin) * blocks, 256);
   w.part_ml = align_up(w.part + sizeof(float) * 2 * blocks * heads * D, 256);
   w.lse2 = align_up(w.part_ml + sizeof(float) * 2 * blocks * heads * 3, 256);
   w.scores = align_up(w.lse2 + (weights ? sizeof(float) * (size_t)B * Hq : 0), 256);
@@ -1080,7 +1079,6 @@ int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, 
   p.weight_at = slot_strides(cache->weight_stride, 1);
   p.status = dev_status;
   char* const ws = static_cast<char*>(workspace);
-  p.units = reinterpret_cast<int64_t*>(ws + w.units);
   p.joins = reinterpret_cast<DecodeJoin*>(ws + w.joins);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);

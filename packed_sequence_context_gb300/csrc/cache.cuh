@@ -85,7 +85,6 @@ struct DecodeParams {
   SlotStrides weight_at;
   int32_t* status;
   // workspace
-  int64_t* units;   // [B + 1] units in front of each sequence
   float* part;      // [2 grid][heads of an item][D]
   float* part_ml;   // [2 grid][heads of an item][3]
   DecodeJoin* joins;  // [items], or of the items that end in a block's share [grid]
