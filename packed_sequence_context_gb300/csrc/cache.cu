@@ -16,7 +16,9 @@ namespace thd {
 // runs of eight elements a lane, three pairs in flight.  Bound by HBM: the rows are
 // read and written once, 16 bytes a lane (8 written for e4m3).  The search and the page
 // are three to six loads one after the other, so a block takes many rows where
-// there are many.
+// there are many (up to 64; 32: 136 us, 64: 130 for 131,072 tokens of 8 heads of
+// 128 to e4m3, 93% of the rate of a plain copy; a packed batch of 14,900 tokens of 16
+// heads as bf16 44 us, 86%).
 //
 // e4m3 with a power of two for each row and head: e is the smallest exponent
 // with max |row| <= 448 * 2^e, so dividing is exact and the only rounding is the
@@ -192,6 +194,11 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
 // the kept ones behind it, in order: the fewest bytes that can move, sources
 // (behind) and targets (in front) that never meet, and nothing to wait for
 // between them.
+//
+// Bound by latency, but for the moves: 4 sequences of 32,768 slots and 8 kv heads cut to
+// 4096 take 56 us, 18 of them the moves at the rate of a plain copy, 7 the keys, 26
+// the selection (four rounds over the cluster of about 4 us each), 5 the numbers
+// that stay when they go to other arrays; 32 sequences of 2000 to 2112 slots 22 us.
 namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 512;
