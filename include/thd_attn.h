@@ -569,7 +569,7 @@ THD_API int thd_dropout_add(const void* x, const void* residual, void* out, int6
  *     multiple of 16 bytes.  D 64 or 128.
  *   dtype THD_DTYPE_BF16, or THD_DTYPE_E4M3 with k_exp, v_exp: a uint8 for each
  *     slot and head (exp_stride, as kv_stride): the row stands for its e4m3
- *     numbers times 2^(exp - 127); 255: not a number.
+ *     numbers times 2^(exp - 127), 15 <= exp; 255: not a number.
  *   `weight` (fp32) and `pos` (int32) of the calls below are such arrays, a
  *     number for each slot and head, with weight_stride and pos_stride.
  *   num_pages < 2^31; max_pages * page_size <= 2^30; Hq / Hkv <= 512.
@@ -631,7 +631,8 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  * as thd_attn_score_fwd gives a sequence's last row.  No visible slot: o = 0,
  * lse = -inf.  Rows of several ranks' caches merge by thd_lse_merge.
  *   q: bf16 rows of [Hq, D], q_stride (even) elements apart, 4-byte aligned.
- *   o: bf16 [B, Hq, D], 16-byte aligned; lse: fp32 [Hq, B].
+ *   o: bf16 [B, Hq, D], 16-byte aligned; lse: fp32 [Hq, B].  Neither overlaps
+ *     an input.
  *   dist_slopes fp32 [Hq] or NULL.  pos NULL: a slot's token has the slot's
  *     number; tokens_seen NULL: kv_len.  Both are read with dist_slopes only.
  *   weight_out NULL, or: weight_out = weight_in + the sum of p_j over the kv

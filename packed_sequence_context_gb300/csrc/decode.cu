@@ -28,10 +28,12 @@
 // Measured on one GB300, heads of 128, of the rate of a plain copy: bf16, 524,288
 // slots of 8 kv heads 303 us (104%), 38 sequences of 8192 with 8, 16 or 32 heads
 // a kv head 186, 186, 190 us (101 to 99%); e4m3, 1,048,576 slots 309 us (103%),
-// 38 sequences with 8, 16, 32 heads 104, 121, 213 us (91, 79, 45%: from 16
+// 38 sequences with 8, 16, 32 heads 104, 115, 171 us (91, 83, 56%: from 16
 // heads on the conversions, softmax and products of a warp's tile take longer than
 // its bytes).  A call begins and ends in about 10 us (lengths, table and first
 // rows are three loads one after the other; the join 2.5 us).
+#include <cfloat>
+
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
@@ -163,13 +165,13 @@ struct DecShape {
   static constexpr int kHeads = 8 * NT;
   // Stages of a warp and blocks of an SM: 8 warps with 16 KB each keep enough
   // bytes in flight for bf16 (a third stage: 301 -> 311 us for 524,288 slots); where
-  // the conversions of e4m3 leave a warp little time to wait, 12 do better (350 -> 329
-  // us for 1,048,576 slots)
+  // the conversions of e4m3 leave a warp little time to wait, 12 do better (8 heads
+  // 350 -> 329 us for 1,048,576 slots, 16 heads 121 -> 115 for 38 x 8192)
   static constexpr int kStages = 2;
-  static constexpr int kPerSm = kFp8 && NT == 1 ? 3 : 2;
+  static constexpr int kPerSm = kFp8 && NT <= 2 ? 3 : 2;
   // slots worked on at a time, in sixteens: more of them overlap better, fewer
-  // leave the registers to the heads (e4m3, 16 heads: 160 us at 16 slots, 143 at 32)
-  static constexpr int kStep = NT == 1 ? kSub : NT == 2 && kSub > 1 ? 2 : 1;
+  // leave the registers to the heads (e4m3, 32 heads: 182 us at 16 slots, 171 at 32)
+  static constexpr int kStep = NT == 1 || kSub < 2 ? kSub : 2;
   // bf16 probabilities as two numbers each (to 2^-16 instead of 2^-8): a second
   // product of every tile, which up to 16 heads' time does not show (at 32 heads 38
   // sequences of 8192 slots take 211 us instead of 190)
@@ -486,21 +488,17 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
       }
     }
     __syncthreads();
-    float hs[NT][2], sl[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) hs[nt][e] = s_hs[nt * 8 + 2 * t4 + e], sl[nt][e] = s_sl[nt * 8 + 2 * t4 + e];
 
-    // ---- tiles: running maximum (base 2) m and sum l of each head, O^T
-    // mo: the maximum of score + log2 of the value's scale, what O is relative to
-    // nbase: -m, or 0 while there is none; up: from a probability times its value's
-    // scale to what the product takes
-    float m[NT][2], mo[NT][2], l[NT][2], nbase[NT][2], up[NT][2], o[D / 16][NT][4];
+    // ---- tiles: running maximum (base 2) and sum of each head, O^T
+    // nm: the maximum, negated; before the first score the largest float, so that
+    // no difference is infinity less infinity
+    // mo: the maximum of score + log2 of the value's scale, what O is relative to;
+    // up: from a probability to what the product takes, but for its value's scale
+    float nm[NT][2], mo[NT][2], l[NT][2], up[NT][2], o[D / 16][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = mo[nt][e] = -INFINITY, l[nt][e] = nbase[nt][e] = up[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) nm[nt][e] = FLT_MAX, mo[nt][e] = -FLT_MAX, l[nt][e] = 0.f, up[nt][e] = 1.f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -562,6 +560,9 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
         // scores in base 2
         const int j0 = k0 + t * S::kKeys + r0;
         float lv[S::kStep][2];  // log2 of the values' scales
+        float2 hs[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) hs[nt] = *reinterpret_cast<const float2*>(s_hs + nt * 8 + 2 * t4);
 #pragma unroll
         for (int sub = 0; sub < S::kStep; ++sub)
 #pragma unroll
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
             for (int nt = 0; nt < NT; ++nt) {
               float &y0 = s[sub][nt][2 * half], &y1 = s[sub][nt][2 * half + 1];
               if (kFp8) fmul2(y0, y1, y0, y1, sc.x, sc.x);
-              fmul2(y0, y1, y0, y1, hs[nt][0], hs[nt][1]);
+              fmul2(y0, y1, y0, y1, hs[nt].x, hs[nt].y);
             }
           }
         if (p.cap > 0.f) {
@@ -594,9 +595,11 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
               const int row = sub * 16 + half * 8 + gid;
               const float far = (float)(int)((uint32_t)seen - 1u - (p.pos ? numbers[row] : (uint32_t)(j0 + row)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) s[sub][nt][2 * half + e] = fmaf(-sl[nt][e], far, s[sub][nt][2 * half + e]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 sl = *reinterpret_cast<const float2*>(s_sl + nt * 8 + 2 * t4);
+                s[sub][nt][2 * half] = fmaf(-sl.x, far, s[sub][nt][2 * half]);
+                s[sub][nt][2 * half + 1] = fmaf(-sl.y, far, s[sub][nt][2 * half + 1]);
+              }
             }
         }
         if (j0 + 16 * S::kStep > k1) {  // slots behind the last
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
               mx[nt][e] = fmax3(mx[nt][e], s[sub][nt][e], s[sub][nt][2 + e]);
               if (kFp8) mxo[nt][e] = fmax3(mxo[nt][e], s[sub][nt][e] + lv[sub][0], s[sub][nt][2 + e] + lv[sub][1]);
             }
-            moved |= mx[nt][e] > m[nt][e] + kSlack;
+            moved |= mx[nt][e] + nm[nt][e] > kSlack;
             if (kFp8) moved |= mxo[nt][e] > mo[nt][e] + kSlack;
           }
         if (__any_sync(0xffffffffu, moved)) {
@@ -654,16 +657,15 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
                 mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
                 if (kFp8) mxo[nt][e] = fmaxf(mxo[nt][e], __shfl_xor_sync(0xffffffffu, mxo[nt][e], d));
               }
-              const float m2 = fmaxf(m[nt][e], mx[nt][e]);
-              al[e] = m2 > m[nt][e] ? ex2(m[nt][e] - m2) : 1.f;
-              m[nt][e] = m2;
-              nbase[nt][e] = m2 == -INFINITY ? 0.f : -m2;
+              const float nm2 = fminf(nm[nt][e], -mx[nt][e]);
+              al[e] = ex2(nm2 - nm[nt][e]);
+              nm[nt][e] = nm2;
               alo[e] = al[e];
               if (kFp8) {
-                const float o2m = fmaxf(mo[nt][e], mxo[nt][e]);
-                alo[e] = o2m > mo[nt][e] ? ex2(mo[nt][e] - o2m) : 1.f;
-                mo[nt][e] = o2m;
-                up[nt][e] = ex2(kRaise - nbase[nt][e] - (o2m == -INFINITY ? 0.f : o2m));
+                const float mo2 = fmaxf(mo[nt][e], mxo[nt][e]);
+                alo[e] = ex2(mo[nt][e] - mo2);
+                mo[nt][e] = mo2;
+                up[nt][e] = ex2(kRaise - nm2 - mo2);
               }
               l[nt][e] *= al[e];
             }
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
             }
           }
         }
-          // probabilities: summed in fp32, and for the product rounded to bf16 next
+        // probabilities: summed in fp32, and for the product rounded to bf16 next
         // to bf16 values (twice, the second time what the first left), to fp16
         // next to e4m3 ones (2^-11, and 2^-32 of the largest)
         uint32_t pb[S::kStep][NT][2], pr[S::kTwo ? S::kStep : 1][NT][2];
@@ -688,13 +690,13 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float y0, y1;
-              fadd2(y0, y1, s[sub][nt][2 * half], s[sub][nt][2 * half + 1], nbase[nt][0], nbase[nt][1]);
+              fadd2(y0, y1, s[sub][nt][2 * half], s[sub][nt][2 * half + 1], nm[nt][0], nm[nt][1]);
               y0 = ex2(y0);
               y1 = ex2(y1);
               fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], y0, y1);
               if (kFp8) {
-                fmul2(y0, y1, y0, y1, vs[half], vs[half]);
                 fmul2(y0, y1, y0, y1, up[nt][0], up[nt][1]);
+                fmul2(y0, y1, y0, y1, vs[half], vs[half]);
               }
               w[half][0] = y0;
               w[half][1] = y1;
@@ -770,8 +772,8 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
         for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
         if (gid == 0) {
           float* const to = s_ml + warp * 3 * S::kHeads + nt * 8 + 2 * t4 + e;
-          to[0] = kFp8 ? mo[nt][e] : m[nt][e];
-          to[S::kHeads] = m[nt][e];
+          to[0] = kFp8 ? mo[nt][e] : -nm[nt][e];
+          to[S::kHeads] = -nm[nt][e];
           to[2 * S::kHeads] = l[nt][e];
         }
       }
@@ -791,10 +793,10 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
       float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
+        float top = -FLT_MAX;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 3 * S::kHeads + nt * 8 + 2 * t4 + e]);
-        f[e] = top == -INFINITY ? 1.f : ex2((kFp8 ? mo[nt][e] : m[nt][e]) - top);
+        f[e] = ex2((kFp8 ? mo[nt][e] : -nm[nt][e]) - top);
         if (kFp8) f[e] *= 1.f / 128;
       }
 #pragma unroll
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
     const int64_t slot = 2 * (int64_t)blockIdx.x + (cur.i0 > 0 ? 0 : 1);
     for (int i = tid; i < heads * (D / 4); i += kDecThreads) {
       const int n = i / (D / 4), d = 4 * (i % (D / 4));
-      float top = -INFINITY, topo = -INFINITY, sum = 0.f;
+      float top = -FLT_MAX, topo = -FLT_MAX, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
         topo = fmaxf(topo, s_ml[w * 3 * S::kHeads + n]);
@@ -827,8 +829,7 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
       }
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
-        const float mw = s_ml[w * 3 * S::kHeads + S::kHeads + n];
-        sum += s_ml[w * 3 * S::kHeads + 2 * S::kHeads + n] * (top == -INFINITY ? 1.f : ex2(mw - top));
+        sum += s_ml[w * 3 * S::kHeads + 2 * S::kHeads + n] * ex2(s_ml[w * 3 * S::kHeads + S::kHeads + n] - top);
       }
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -872,83 +873,85 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
 
 // ------------------------------------------------------------------ the join
 // The parts of an item that several blocks shared: a block of 128 threads for
-// each (item or block that ended one, head), four parts at a time, a head's row across
+// each (item or block that ended one, head or several), four parts at a time, a head's row across
 // the lanes.  The sums run over the parts in order, four interleaved.
 constexpr int kJoinThreads = 128;
 
-template <int D>
+template <int D, bool kSeveral>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams p, int kheads) {
   constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
   __shared__ float4 s_x[kJoinThreads];
   __shared__ float s_ml[kDecodeMaxGrid][3], s_top[kJoinThreads / 32][2], s_sum[kParts];
-  const int tid = threadIdx.x, n = blockIdx.y;
+  const int tid = threadIdx.x;
   follow();
   depend();
   const DecodeJoin j = p.joins[blockIdx.x];
-  if (j.count == 0 || n >= j.heads) return;
-  // part k's row
-  auto row_of = [&](int k) { return (2 * (int64_t)(j.first + k) + (k == 0 ? 1 : 0)) * kheads + n; };
-  // the first rows are on their way while the maxima are found
-  constexpr int kAhead = 8;
-  const int lane = tid % kLanes, mine = tid / kLanes;
-  float4 ahead[kAhead];
+  if (j.count == 0) return;
+  for (int n = blockIdx.y; n < j.heads; n += kSeveral ? (int)gridDim.y : j.heads) {
+    // part k's row
+    auto row_of = [&](int k) { return (2 * (int64_t)(j.first + k) + (k == 0 ? 1 : 0)) * kheads + n; };
+    // the first rows are on their way while the maxima are found
+    constexpr int kAhead = 8;
+    const int lane = tid % kLanes, mine = tid / kLanes;
+    float4 ahead[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (mine + i * kParts < j.count)
-      ahead[i] = *reinterpret_cast<const float4*>(p.part + row_of(mine + i * kParts) * D + 4 * lane);
-  float topo = -INFINITY, top = -INFINITY;
-  for (int k = tid; k < j.count; k += kJoinThreads) {
-    const float* ml = p.part_ml + row_of(k) * 3;
-    s_ml[k][0] = ml[0], s_ml[k][1] = ml[1], s_ml[k][2] = ml[2];
-    topo = fmaxf(topo, ml[0]);
-    top = fmaxf(top, ml[1]);
-  }
+    for (int i = 0; i < kAhead; ++i)
+      if (mine + i * kParts < j.count)
+        ahead[i] = *reinterpret_cast<const float4*>(p.part + row_of(mine + i * kParts) * D + 4 * lane);
+    float topo = -FLT_MAX, top = -FLT_MAX;
+    for (int k = tid; k < j.count; k += kJoinThreads) {
+      const float* ml = p.part_ml + row_of(k) * 3;
+      s_ml[k][0] = ml[0], s_ml[k][1] = ml[1], s_ml[k][2] = ml[2];
+      topo = fmaxf(topo, ml[0]);
+      top = fmaxf(top, ml[1]);
+    }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, d));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  }
-  if ((tid & 31) == 0) s_top[tid >> 5][0] = topo, s_top[tid >> 5][1] = top;
-  __syncthreads();
+    for (int d = 16; d > 0; d >>= 1) {
+      topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, d));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    if ((tid & 31) == 0) s_top[tid >> 5][0] = topo, s_top[tid >> 5][1] = top;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) topo = fmaxf(topo, s_top[w][0]), top = fmaxf(top, s_top[w][1]);
-  const float base = top == -INFINITY ? 0.f : top, baseo = topo == -INFINITY ? 0.f : topo;
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int k, const float4& y) {
-    const float f = ex2(s_ml[k][0] - baseo);
-    sum += s_ml[k][2] * ex2(s_ml[k][1] - base);
-    acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
-  };
+    for (int w = 0; w < kJoinThreads / 32; ++w) topo = fmaxf(topo, s_top[w][0]), top = fmaxf(top, s_top[w][1]);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int k, const float4& y) {
+      const float f = ex2(s_ml[k][0] - topo);
+      sum += s_ml[k][2] * ex2(s_ml[k][1] - top);
+      acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
+    };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (mine + i * kParts < j.count) add(mine + i * kParts, ahead[i]);
+    for (int i = 0; i < kAhead; ++i)
+      if (mine + i * kParts < j.count) add(mine + i * kParts, ahead[i]);
 #pragma unroll 8
-  for (int k = mine + kAhead * kParts; k < j.count; k += kParts)
-    add(k, *reinterpret_cast<const float4*>(p.part + row_of(k) * D + 4 * lane));
-  s_x[tid] = acc;
-  if (lane == 0) s_sum[mine] = sum;
-  __syncthreads();
-  if (tid < kLanes) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float z = 0.f;
+    for (int k = mine + kAhead * kParts; k < j.count; k += kParts)
+      add(k, *reinterpret_cast<const float4*>(p.part + row_of(k) * D + 4 * lane));
+    s_x[tid] = acc;
+    if (lane == 0) s_sum[mine] = sum;
+    __syncthreads();
+    if (tid < kLanes) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float z = 0.f;
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      const float4 y = s_x[k * kLanes + tid];
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      z += s_sum[k];
+      for (int k = 0; k < kParts; ++k) {
+        const float4 y = s_x[k * kLanes + tid];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        z += s_sum[k];
+      }
+      const float f = z == 0.f ? 0.f : ex2(topo - top) / z;
+      uint2 y;
+      y.x = pack2<false>(x.x * f, x.y * f);
+      y.y = pack2<false>(x.z * f, x.w * f);
+      const int64_t row = (int64_t)j.b * p.Hq + j.h + n;
+      *reinterpret_cast<uint2*>(p.o + row * D + 4 * tid) = y;
+      if (tid == 0) {
+        const float lse2 = top + log2f(z);
+        p.lse[(int64_t)(j.h + n) * p.c.B + j.b] = lse2 * kLn2;
+        if (p.weight_out) p.lse2[row] = lse2;
+      }
     }
-    const float f = z == 0.f ? 0.f : ex2(baseo - base) / z;
-    uint2 y;
-    y.x = pack2<false>(x.x * f, x.y * f);
-    y.y = pack2<false>(x.z * f, x.w * f);
-    const int64_t row = (int64_t)j.b * p.Hq + j.h + n;
-    *reinterpret_cast<uint2*>(p.o + row * D + 4 * tid) = y;
-    if (tid == 0) {
-      const float lse2 = base + log2f(z);
-      p.lse[(int64_t)(j.h + n) * p.c.B + j.b] = lse2 * kLn2;
-      if (p.weight_out) p.lse2[row] = lse2;
-    }
+    if (kSeveral) __syncthreads();  // the sums are read
   }
 }
 
@@ -1048,10 +1051,15 @@ cudaError_t launch_decode(DecodeParams p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (p.c.capacity > kUnit) {  // an item of one unit is one block's
     const int64_t items = (int64_t)p.c.B * p.c.Hkv * p.blocks;
+    // a head a block up to 16; of 32, as many blocks as 16 an SM (most find nothing
+    // to do: 304 x 32 of them take 6 us more), each with several heads
+    const int64_t x = p.by_item ? items : p.grid, most = 16LL * num_sms() / x > 8 ? 16LL * num_sms() / x : 8;
+    const bool several = heads > 16 && most < heads;
+    const dim3 grid((unsigned)x, (unsigned)(several ? most : heads));
     prof_before(THD_KERNEL_DECODE_JOIN, st);
-    e = launch_following(p.c.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
-                         dim3((unsigned)(p.by_item ? items : p.grid), (unsigned)heads), kJoinThreads, 0, st, (const DecodeParams)p,
-                         (int)heads);
+    auto* const join = p.c.D == 64 ? (several ? decode_join_kernel<64, true> : decode_join_kernel<64, false>)
+                                   : (several ? decode_join_kernel<128, true> : decode_join_kernel<128, false>);
+    e = launch_following(join, grid, kJoinThreads, 0, st, (const DecodeParams)p, (int)heads);
     prof_after(THD_KERNEL_DECODE_JOIN, st);
     if (e != cudaSuccess) return e;
   }
