@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -335,8 +336,8 @@ def thd_dropout_add(x, residual, out, T, C, row_ids, p, rng, dtype, stream=None)
 
 def thd_cache_append(cache, k, v, k_stride, v_stride, T, cu_seqlens, weight, pos, tokens_seen, dev_status,
                      stream=None) -> int:
-    return lib().thd_cache_append(_c(cache), _p(k), _p(v), k_stride, v_stride, T, _p(cu_seqlens), _p(weight), _p(pos),
-                                  _p(tokens_seen), _p(dev_status), _s(stream))
+    return lib().thd_cache_append(_c(cache), _p(k), _p(v), k_stride, v_stride, T, _p(cu_seqlens),
+                                  _p(weight), _p(pos), _p(tokens_seen), _p(dev_status), _s(stream))
 
 
 def thd_attn_decode(cache, q, q_stride, o, lse, Hq, softmax_scale, softcap, dist_slopes, kv_start, pos, tokens_seen,
@@ -901,12 +902,23 @@ def _row_stride(where, like, t, T, H, D):
     return _rope_rows(where, like, t, T, H, D)
 
 
-def _slot_strides(t):
-    """Strides of the first three dimensions; one of size 1 may carry any."""
-    s = t.stride()
-    if 1 in t.shape:
-        s = tuple(0 if n == 1 else x for n, x in zip(t.shape[:3], s)) + s[3:]
-    return s
+def _same_strides(a, b):
+    """Whether two arrays of one shape lie alike; a dimension of size 1 may
+    carry any stride."""
+    return a.stride() == b.stride() or all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
+def _slot_array(where, t, other, dtype, shape, dev):
+    """Strides of a number for each slot and head; `other` (or None) lies alike."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _need(where, False)
+    if other is not None and other is not t and (other.dtype is not dtype or other.shape != shape or
+                                                 other.get_device() != dev or not _same_strides(t, other)):
+        _need(where, False)
+    return t.stride()
+
+
+_NO_STRIDES = (0, 0, 0)
 
 
 def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos, pos_out):
@@ -914,62 +926,67 @@ def _cache(where, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, w
     a table's row, and the device."""
     import torch
     dev = _current(where, k_cache)
-    shape, dtype = k_cache.shape, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape:
-        _need(where, False)
-    strides = _slot_strides(k_cache)
-    if _slot_strides(v_cache) != strides or v_cache.dtype is not dtype or v_cache.get_device() != dev or strides[3] != 1:
+    shape, dtype, i32 = k_cache.shape, k_cache.dtype, torch.int32
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype or v_cache.get_device() != dev or \
+            not _same_strides(k_cache, v_cache):
         _need(where, False)
     e4m3 = dtype is torch.float8_e4m3fn
     if not e4m3 and dtype is not torch.bfloat16:
         raise ThdError(where, THD_ERR_UNSUPPORTED)
-    i32 = torch.int32
-    if block_table.dim() != 2 or block_table.dtype is not i32 or block_table.get_device() != dev:
+    pages, slots, heads, D = shape
+    s0, s1, s2, s3 = k_cache.stride()
+    if s3 != 1 or block_table.dim() != 2 or block_table.dtype is not i32 or block_table.get_device() != dev:
         _need(where, False)
+    if pages == 1:
+        s0 = 0
+    if slots == 1:
+        s1 = 0
+    if heads == 1:
+        s2 = 0
     B, max_pages = block_table.shape
     ts0, ts1 = block_table.stride()
     if not (ts1 == 1 or max_pages <= 1) or not (B <= 1 or ts0 == 0 or ts0 >= max_pages) or kv_len.dtype is not i32 or \
             kv_len.shape != (B,) or not kv_len.is_contiguous() or kv_len.get_device() != dev:
         _need(where, False)
-    numbers = shape[:3]
-    es, ws, ps = _NO_STRIDES, _NO_STRIDES, _NO_STRIDES
+    numbers = (pages, slots, heads)
+    es = ws = ps = _NO_STRIDES
     ke = ve = 0
-    if (k_exp is not None) != e4m3 or (v_exp is not None) != e4m3:
-        _need(where, False)
     if e4m3:
-        es = _slot_strides(k_exp) if k_exp.dim() == 3 else None
-        for t in (k_exp, v_exp):
-            if t.dtype is not torch.uint8 or t.shape != numbers or _slot_strides(t) != es or t.get_device() != dev:
-                _need(where, False)
+        if k_exp is None or v_exp is None:
+            _need(where, False)
+        es = _slot_array(where, k_exp, v_exp, torch.uint8, numbers, dev)
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    elif k_exp is not None or v_exp is not None:
+        _need(where, False)
     if weight is not None:
-        ws = _slot_strides(weight) if weight.dim() == 3 else None
-        for t in (weight,) if weight_out is weight or weight_out is None else (weight, weight_out):
-            if t.dtype is not torch.float32 or t.shape != numbers or _slot_strides(t) != ws or t.get_device() != dev:
-                _need(where, False)
+        ws = _slot_array(where, weight, weight_out, torch.float32, numbers, dev)
     if pos is not None:
-        ps = _slot_strides(pos) if pos.dim() == 3 else None
-        for t in (pos,) if pos_out is pos or pos_out is None else (pos, pos_out):
-            if t.dtype is not i32 or t.shape != numbers or _slot_strides(t) != ps or t.get_device() != dev:
-                _need(where, False)
-    pages, slots, heads, D = shape
+        ps = _slot_array(where, pos, pos_out, i32, numbers, dev)
     try:
         c = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, block_table.data_ptr(), kv_len.data_ptr(), pages,
-                        ts0, strides[0], strides[1], strides[2], *es, *ws, *ps, slots, max_pages, B, heads, D,
+                        ts0, s0, s1, s2, *es, *ws, *ps, slots, max_pages, B, heads, D,
                         THD_DTYPE_E4M3 if e4m3 else THD_DTYPE_BF16)
     except struct.error:  # a size past the struct's
         _need(where, False)
     return c, B, heads, D, max_pages * slots, dev
 
 
-_NO_STRIDES = (0, 0, 0)
+def _numbers(where, t, n, dtype, dev):
+    """A contiguous array of a call."""
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        _need(where, False)
 
 
-def _numbers(where, dev, *triples):
-    """Contiguous arrays of a call: (tensor or None, shape, dtype)."""
-    for t, shape, dtype in triples:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
-            _need(where, False)
+@functools.lru_cache(maxsize=1024)
+def _sizes(library, name, *sizes):
+    """A workspace's size, which goes by the sizes alone."""
+    return getattr(library, name)(*sizes)
+
+
+def _given_workspace(where, t, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        _need(where, False)
+    return t.numel() * t.element_size()
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None, k_exp=None, v_exp=None, weight=None,
@@ -992,7 +1009,12 @@ def cache_append(k, v, k_cache, v_cache, block_table, kv_len, *, cu_seqlens=None
     T = k.shape[0]
     s_k, s_v = _row_stride(w, k, k, T, Hkv, D), _row_stride(w, k, v, T, Hkv, D)
     i32 = torch.int32
-    _numbers(w, dev, (cu_seqlens, (B + 1,), i32), (tokens_seen, (B,), i32), (dev_status, (1,), i32))
+    if cu_seqlens is not None:
+        _numbers(w, cu_seqlens, B + 1, i32, dev)
+    if tokens_seen is not None:
+        _numbers(w, tokens_seen, B, i32, dev)
+    if dev_status is not None:
+        _numbers(w, dev_status, 1, i32, dev)
     side = _aside(stream)
     st = dev_status
     if st is None:
@@ -1020,33 +1042,35 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_len, *, k_exp=None, v_exp=N
         weight_out = weight
     c, B, Hkv, D, capacity, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos,
                                          None)
-    if (weight is None) != (weight_out is None) or q.dim() != 3 or q.dtype is not torch.bfloat16 or \
-            q.get_device() != dev or workspace is not None and not (workspace.get_device() == dev and
-                                                                    workspace.is_contiguous()):
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if (weight is None) != (weight_out is None) or q.dim() != 3 or q.dtype is not bf16 or q.get_device() != dev:
         _need(w, False)
     Hq = q.shape[1]
     s_q = _row_stride(w, q, q, B, Hq, D)
-    f32, i32 = torch.float32, torch.int32
     if dev_status is not None:
-        _numbers(w, dev, (dev_status, (1,), i32))
-    if dist_slopes is not None or kv_start is not None or tokens_seen is not None:
-        _numbers(w, dev, (dist_slopes, (Hq,), f32), (kv_start, (B,), i32), (tokens_seen, (B,), i32))
-    if out is not None or lse is not None:
-        _numbers(w, dev, (out, (B, Hq, D), torch.bfloat16), (lse, (Hq, B), f32))
+        _numbers(w, dev_status, 1, i32, dev)
+    if dist_slopes is not None:
+        _numbers(w, dist_slopes, Hq, f32, dev)
+    if kv_start is not None:
+        _numbers(w, kv_start, B, i32, dev)
+    if tokens_seen is not None:
+        _numbers(w, tokens_seen, B, i32, dev)
+    for t, n, dtype in ((out, (B, Hq, D), bf16), (lse, (Hq, B), f32)) if out is not None or lse is not None else ():
+        if t is not None and (t.dtype is not dtype or t.shape != n or t.get_device() != dev or not t.is_contiguous()):
+            _need(w, False)
+    size = None if workspace is None else _given_workspace(w, workspace, dev)
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     side = _aside(stream)
     given = None if side is None else (q, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, dist_slopes, kv_start, pos,
                                        tokens_seen, weight, weight_out, out, lse, dev_status, workspace)
     at = q.device
     with _alloc_on(side):
-        o = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=at) if out is None else out
+        o = torch.empty((B, Hq, D), dtype=bf16, device=at) if out is None else out
         l = torch.empty((Hq, B), dtype=f32, device=at) if lse is None else lse
         st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
-        if workspace is None:
-            size = thd_decode_workspace_size(B, Hq, Hkv, D, capacity, weight is not None)
+        if size is None:
+            size = _sizes(lib(), "thd_decode_workspace_size", B, Hq, Hkv, D, capacity, weight is not None)
             workspace = torch.empty(size, dtype=torch.uint8, device=at)
-        else:
-            size = workspace.numel() * workspace.element_size()
     _check(w, thd_attn_decode(c, q, s_q, o, l, Hq, scale, softcap, dist_slopes, kv_start, pos, tokens_seen, weight,
                               weight_out, workspace, size, st, stream))
     if side is not None:
@@ -1070,9 +1094,13 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
     c, B, Hkv, _, capacity, dev = _cache(w, k_cache, v_cache, block_table, kv_len, k_exp, v_exp, weight, weight_out, pos,
                                          pos_out)
     i32 = torch.int32
-    if tokens_seen is None or workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
-        _need(w, False)
-    _numbers(w, dev, (tokens_seen, (B,), i32), (new_len, (B,), i32), (dev_status, (1,), i32))
+    _need(w, tokens_seen is not None)
+    _numbers(w, tokens_seen, B, i32, dev)
+    if new_len is not None:
+        _numbers(w, new_len, B, i32, dev)
+    if dev_status is not None:
+        _numbers(w, dev_status, 1, i32, dev)
+    size = None if workspace is None else _given_workspace(w, workspace, dev)
     side = _aside(stream)
     given = None if side is None else (k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen, k_exp, v_exp,
                                        weight_out, pos_out, new_len, dev_status, workspace)
@@ -1080,11 +1108,9 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
     with _alloc_on(side):
         n = torch.empty(B, dtype=i32, device=at) if new_len is None else new_len
         st = torch.zeros(1, dtype=i32, device=at) if dev_status is None else dev_status
-        if workspace is None:
-            size = thd_evict_workspace_size(B, Hkv, capacity, budget)
+        if size is None:
+            size = _sizes(lib(), "thd_evict_workspace_size", B, Hkv, capacity, budget)
             workspace = torch.empty(size, dtype=torch.uint8, device=at)
-        else:
-            size = workspace.numel() * workspace.element_size()
     _check(w, thd_cache_evict(c, weight, weight_out, pos, pos_out, tokens_seen, budget, sinks, recent, n, workspace,
                               size, st, stream))
     if side is not None:
