@@ -198,7 +198,7 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
 // Bound by latency, but for the moves: 4 sequences of 32,768 slots and 8 kv heads cut to
 // 4096 take 56 us, 18 of them the moves at the rate of a plain copy, 7 the keys, 26
 // the selection (four rounds over the cluster of about 4 us each), 5 the numbers
-// that stay when they go to other arrays; 32 sequences of 2000 to 2112 slots 22 us.
+// that stay when they go to other arrays; 32 sequences of 2000 to 2112 slots 20 us.
 namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 512;
@@ -531,11 +531,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
 
 cudaError_t launch_evict(EvictParams p, cudaStream_t st) {
   const int64_t items = (int64_t)p.c.B * p.c.Hkv;
-  // blocks of an item: until the SMs have two each, while one still has 1024
-  // slots, and as many as it takes to hold the keys
+  // blocks of an item: as many as leave two an SM (one wave), while each still has
+  // 1024 slots, and as many as it takes to hold the keys (64 items of 25,331
+  // slots: 4 blocks each 49 us, 8 in two waves 63)
   int share = 1;
-  while (share < 8 && ((items * share < 2LL * num_sms() && p.c.capacity / share > 1024) ||
-                       p.c.capacity / share > kEvictMaxHeld))
+  while (share < 8 && ((items * share <= num_sms() && p.c.capacity / share > 1024) || p.c.capacity / share > kEvictMaxHeld))
     share *= 2;
   int64_t held = (p.c.capacity + share - 1) / share;
   if (held > kEvictMaxHeld) held = kEvictMaxHeld;
