@@ -240,7 +240,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
   auto carry = [&](int i) {
     const Place x = place_of(c, i);
     const int page = page_of(c, b, x.page);
-    if (page < 0) return;
+    if (page < 0) {
+      raise(p.status, THD_DEV_ERR_PAGE);
+      return;
+    }
     const int64_t w = at(p.weight_at, page, x.slot, g), q = at(p.pos_at, page, x.slot, g);
     if (copy_w) p.weight_out[w] = p.weight_in[w];
     if (copy_p) p.pos_out[q] = p.pos_in[q];
