@@ -83,7 +83,8 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
       largest element (elements far below it; 0 for the others);
     * probabilities rounded to bf16 (2^-8; 2^-16, as two numbers, up to 16 query
       heads a kv head), or next to e4m3 values to fp16 (2^-11, and 2^-32 of the
-      largest), the output to bf16 (2^-8).
+      largest product of probability and scale, rows of zeros left out: those
+      count with the least scale, 2^-112), the output to bf16 (2^-8).
     """
     q = np.asarray(q, np.float64)
     B, Hq, D = q.shape
@@ -130,7 +131,8 @@ def decode(q, cache, table, kv_len, *, scale, softcap=0.0, slopes=None, start=No
             # product of weight and value scale)
             tol_o[b, h] += ((pr * (half + rel + dz))[:, None] * size).sum(0) + 2.0 ** -8 * np.abs(o[b, h])
             if e4m3:
-                top = float((pr * 2.0 ** (np.asarray(cache["v_exp"][p, at, g], np.float64) - 127)).max())
+                size = 2.0 ** (np.asarray(cache["v_exp"][p, at, g], np.float64) - 127)
+                top = float((pr * np.where(np.any(v != 0, 1), size, 2.0 ** -112)).max())
                 tol_o[b, h] += 2.0 ** -32 * top * np.abs(np.asarray(cache["v"][p, at, g], np.float64)).sum(0)
             if w is not None:
                 w[p, at, g] += pr

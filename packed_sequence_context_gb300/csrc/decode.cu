@@ -50,6 +50,7 @@ constexpr int kMinUnits = 2;    // of a block, while there are few
 
 constexpr float kSlack = 8.f;   // see the running maximum
 constexpr float kRaise = 7.f;   // fp16 probabilities are 2^7 times as large: 2^15 at most, 2^-31 at least
+constexpr float kLeastScale = -112.f;  // log2 of the least scale of a row: a stored exponent of 15
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -647,6 +648,50 @@ __global__ void __launch_bounds__(kDecThreads, DecShape<kFp8, D, NT>::kPerSm) de
             if (kFp8) moved |= mxo[nt][e] > mo[nt][e] + kSlack;
           }
         if (__any_sync(0xffffffffu, moved)) {
+          // A row of zeros adds nothing to O whatever its scale says, so it must not
+          // set what O is relative to: rows that would raise that are looked at, and
+          // count as of the least scale if they are zeros.
+          if (kFp8) {
+            bool far = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) far |= mxo[nt][e] > mo[nt][e] + kSlack;
+            if (__any_sync(0xffffffffu, far)) {
+              constexpr int kRows = 16 * S::kStep;
+              uint32_t zeros[(kRows + 31) / 32];
+              bool some = false;
+#pragma unroll
+              for (int k = 0; k < kRows; k += 32) {
+                const uint4* const x =
+                    reinterpret_cast<const uint4*>(ring + stage * kDecTile + kDecTile / 2 + (r0 + k + lane) * S::kRow);
+                bool zero = k + lane < kRows;
+                for (int i = 0; zero && i < S::kPieces; ++i)
+                  zero = ((x[i].x | x[i].y | x[i].z | x[i].w) & 0x7f7f7f7fu) == 0;
+                zeros[k / 32] = __ballot_sync(0xffffffffu, zero);
+                some |= zeros[k / 32] != 0;
+              }
+              if (some) {
+#pragma unroll
+                for (int sub = 0; sub < S::kStep; ++sub)
+#pragma unroll
+                  for (int half = 0; half < 2; ++half) {
+                    const int row = sub * 16 + half * 8 + gid;
+                    // (a row marked as no number stays one)
+                    if ((zeros[sub / 2] >> (row & 31) & 1u) && lv[sub][half] == lv[sub][half]) lv[sub][half] = kLeastScale;
+                  }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    mxo[nt][e] = -INFINITY;
+#pragma unroll
+                    for (int sub = 0; sub < S::kStep; ++sub)
+                      mxo[nt][e] = fmax3(mxo[nt][e], s[sub][nt][e] + lv[sub][0], s[sub][nt][2 + e] + lv[sub][1]);
+                  }
+              }
+            }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float al[2], alo[2];

@@ -1,4 +1,4 @@
-"""Corners of the paged cache: bad pages of sequences that nothing leaves."""
+"""Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits."""
 
 import numpy as np
 import pytest
@@ -49,3 +49,57 @@ def test_evict_reports_a_bad_page_where_nothing_leaves(n, bad):
         p, at = co.slots(c.table_np[b], 20, 16)
         assert same(c.host()["k"][p, at], ref["k"][p, at]) and same(c.host()["v"][p, at], ref["v"][p, at])
         assert same(wo.cpu().numpy()[p, at], rw[p, at]) and same(po.cpu().numpy()[p, at], rp[p, at])
+
+
+# ------------------------------------------------------------------ rows of zeros among 8-bit values
+def _check(c, q, scale, **kw):
+    """attn_decode of an 8-bit cache against the oracle and its bounds."""
+    ref = co.decode(q.double().cpu().numpy(), c.host(), c.table_np, c.lens, scale=np.float32(scale), **kw)
+    o, lse, st = T.attn_decode(q, *c.args(), softmax_scale=scale, **c.exps())
+    _status(st)
+    assert np.all(np.abs(o.double().cpu().numpy() - ref["o"]) <= ref["tol_o"])
+    assert np.all(np.abs(lse.double().cpu().numpy() - ref["lse"]) <= ref["tol_lse"])
+    return o, ref
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 16), (64, 32), (128, 8), (128, 16), (128, 32)])
+@pytest.mark.parametrize("zeros,size,near", [([0], 1e-2, 14.0), ([5, 69], 1e-8, 0.0), (list(range(64)), 1e-3, 9.0),
+                                             ([130], 2.0 ** -50, 3.0), (list(range(0, 150, 2)), 1e-2, 12.0)])
+def test_zero_values_of_a_strong_key_hide_nothing(zeros, size, near, D, G):
+    """Keys that take most of the weight and whose values are zeros, next to small values: what is left of those shows."""
+    n = 150
+    c = Cache([n], page=16, Hkv=1, D=D, fp8=True, seed=7)
+    k = torch.randn(n, 1, D, device="cuda") * 0.1
+    k[zeros] = 1.0                                 # q . k = D for a query of ones
+    v = torch.randn(n, 1, D, device="cuda") * size
+    v[zeros] = 0
+    v[zeros[-1], 0, ::3] = -0.0
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    _status(T.cache_append(k, v, *c.args(), cu_seqlens=_cuda([0, n]), **c.exps()))
+    q = torch.ones(1, G, D, device="cuda", dtype=torch.bfloat16) + torch.randn(1, G, D, device="cuda").to(torch.bfloat16) / 64
+    o, ref = _check(c, q, near / D if near else 1e-6)
+    assert (o.float().abs().amax(-1) > 0).all()    # the rest has e^-14 of the weight at least
+    # whatever scale the rows of zeros carry, as another program may have stored them
+    p, at = co.slots(c.table_np[0], n, 16)
+    for e in (15, 200, 254):
+        c.v_exp[_cuda(p[zeros], torch.int64), _cuda(at[zeros], torch.int64)] = e
+        _check(c, q, near / D if near else 1e-6)
+
+
+def test_zero_values_alone():
+    """Nothing but zeros, also in some warps' and blocks' shares only; one row that is no number stays so."""
+    n = 5000
+    c = Cache([n, 40], page=24, Hkv=2, D=128, fp8=True, seed=8)
+    p, at = co.slots(c.table_np[0], n, 24)
+    zero = slice(700, 4100)
+    c.v.view(torch.uint8)[_cuda(p[zero], torch.int64), _cuda(at[zero], torch.int64)] = 0
+    c.v_exp[_cuda(p[zero], torch.int64), _cuda(at[zero], torch.int64)] = 220
+    p1, at1 = co.slots(c.table_np[1], 40, 24)
+    c.v.view(torch.uint8)[_cuda(p1, torch.int64), _cuda(at1, torch.int64)] = 0x80
+    q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+    o, _ = _check(c, q, 1 / 900)
+    assert not o[1].any()
+    c.v_exp[int(p1[17]), int(at1[17]), 0] = 255    # zeros marked as no numbers
+    o, _, st = T.attn_decode(q, *c.args(), softmax_scale=1 / 900, **c.exps())
+    _status(st)
+    assert torch.isnan(o[1, :4]).all() and not o[1, 4:].any() and not torch.isnan(o[0]).any()
