@@ -641,9 +641,9 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  *   Lengths are read on the device: a captured graph serves growing ones.
  * Sums are fp32.  Probabilities meet bf16 values as two bf16 numbers each (to
  * 2^-16), above 16 query heads a kv head as one (2^-8); e4m3 values as fp16
- * (2^-11) after their row's scale is multiplied in: a row whose probability
- * times scale is under 2^-31 of the largest such product keeps fewer bits, under
- * 2^-39 none (rows of zeros, whatever their scale, do not count as the largest).
+ * (2^-11) after their row's scale is multiplied in, off by at most 2^-32 of the
+ * largest such product (small ones keep fewer bits, below that none; rows of
+ * zeros, whatever their scale, do not count as the largest).
  * Bit-reproducible on one kind of GPU.  Launches: 2 (1 for tables of at most 64
  * slots), with weights one more.  Workspace: thd_decode_workspace_size; calls that
  * may run at the same time need one each.
