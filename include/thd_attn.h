@@ -664,9 +664,11 @@ THD_API size_t thd_decode_workspace_size(int B, int Hq, int Hkv, int D, int64_t 
 /*
  * thd_cache_evict -- shrinks caches to `budget` slots, kv head by kv head, one
  * launch.  Of a sequence's n = kv_len[b] > budget slots the budget with the
- * largest weight stay, ties going to the lower slot; slots whose token is
- * among the first `sinks` (pos < sinks) or the last `recent` (pos >=
- * tokens_seen[b] - recent) count as +infinity, NaN as less than all.  Kept
+ * largest weight stay, ties going to the lower slot; NaN counts as less than
+ * all.  Slots whose token is among the first `sinks` (pos < sinks) or the last
+ * `recent` (pos >= tokens_seen[b] - recent) stay before any weight, +infinity
+ * too; where the budget holds fewer than those, the newest do (the largest pos;
+ * those from tokens_seen[b] - 1 on count alike, and those 2^23 - 2 or more below).  Kept
  * slots in front of the budget stay where they are; the i-th kept slot behind
  * it moves into the i-th evicted slot in front of it: keys, values, exponents,
  * weight and pos.  Slots behind the budget are left as they were.

@@ -154,14 +154,14 @@ def evict(cache, table, kv_len, weight, pos, seen, budget, sinks=0, recent=0):
             if n <= budget:
                 continue
             w = np.asarray(weight[p, at, g], np.float64).copy()
-            w[np.isnan(w)] = -np.inf
             # NaN counts as less than all: below -infinity too
-            nan = np.isnan(np.asarray(weight[p, at, g], np.float64))
-            num = np.asarray(pos[p, at, g], np.int64)
-            safe = (num < sinks) | (num >= int(seen[b]) - recent)
-            w[safe] = np.inf
-            nan &= ~safe
-            order = sorted(range(n), key=lambda j: (nan[j], -w[j], j))
+            nan = np.isnan(w)
+            w[nan] = -np.inf
+            # the protected ones before any weight, the newest first
+            age = int(seen[b]) - 1 - np.asarray(pos[p, at, g], np.int64)
+            safe = (np.asarray(pos[p, at, g], np.int64) < sinks) | (age < recent)
+            age = np.clip(age, 0, (1 << 23) - 2)
+            order = sorted(range(n), key=lambda j: (0, age[j], j) if safe[j] else (1 + nan[j], -w[j], j))
             keep = np.zeros(n, bool)
             keep[order[:budget]] = True
             to = [j for j in range(budget) if not keep[j]]

@@ -207,8 +207,12 @@ constexpr int kBins = 256;
 constexpr int kFew = 1024;             // candidates that are compared with one another
 constexpr int kEvictMaxHeld = 40960;  // keys in a block's shared memory (160 KB)
 
-__device__ inline uint32_t order_of(float w, bool kept) {
-  if (kept) return 0xff800000u;             // as +infinity
+// An integer of the order in which slots stay.  Protected tokens (`age`: how many
+// came after) above every weight, +infinity too, the newest on top: where the
+// budget holds fewer than are protected, the oldest leave first.  Weights end at
+// 0xff800000, which leaves 2^23 - 1 ages apart; those beyond count as one.
+__device__ inline uint32_t order_of(float w, bool kept, int64_t age) {
+  if (kept) return 0xffffffffu - (age < 0 ? 0u : age < 0x7ffffe ? (uint32_t)age : 0x7ffffeu);
   if (!(w == w)) return 0u;                 // NaN: below everything
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -263,8 +267,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
       return 0u;
     }
     const int pos = p.pos_in[at(p.pos_at, page, x.slot, g)];
-    return order_of(p.weight_in[at(p.weight_at, page, x.slot, g)],
-                    pos < p.sinks || (int64_t)pos >= (int64_t)seen - p.recent);
+    const int64_t age = (int64_t)seen - 1 - pos;
+    return order_of(p.weight_in[at(p.weight_at, page, x.slot, g)], pos < p.sinks || age < p.recent, age);
   };
   {
     const int m = hi - lo < p.held ? hi - lo : p.held;

@@ -1082,8 +1082,9 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
                 k_exp=None, v_exp=None, weight_out=None, pos_out=None, new_len=None, dev_status=None, workspace=None,
                 stream=None):
     """Shrinks caches as cache_append's to `budget` slots a sequence and kv
-    head: the largest weights stay, with the first `sinks` and the last
-    `recent` tokens (by pos and tokens_seen).  Slots move in place; weight and
+    head: the first `sinks` and the last `recent` tokens stay (by pos and
+    tokens_seen; the newest of them, where the budget holds fewer), then the
+    largest weights.  Slots move in place; weight and
     pos too, unless weight_out, pos_out take them.  Returns (new_len int32 [B],
     dev_status)."""
     import torch

@@ -1,4 +1,5 @@
-"""Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits."""
+"""Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits;
+more protected tokens than a budget holds."""
 
 import numpy as np
 import pytest
@@ -103,3 +104,55 @@ def test_zero_values_alone():
     o, _, st = T.attn_decode(q, *c.args(), softmax_scale=1 / 900, **c.exps())
     _status(st)
     assert torch.isnan(o[1, :4]).all() and not o[1, 4:].any() and not torch.isnan(o[0]).any()
+
+
+# ------------------------------------------------------------------ more protected tokens than the budget holds
+def _trim(c, w, pos, seen, budget, **kw):
+    """cache_evict in place against the oracle; the kept slots' numbers."""
+    c.weight.copy_(torch.from_numpy(w)), c.pos.copy_(torch.from_numpy(pos))
+    ref, rw, rp, rn = co.evict(c.host(), c.table_np, c.lens, w, pos, seen, budget, kw.get("sinks", 0), kw.get("recent", 0))
+    new, st = T.cache_evict(*c.args(), c.weight, c.pos, _cuda(seen), budget=budget, **kw, **c.exps())
+    _status(st)
+    assert same(c.host()["k"], ref["k"]) and same(c.host()["v"], ref["v"]) and np.array_equal(new.cpu().numpy(), rn)
+    assert same(c.weight.cpu().numpy(), rw) and same(c.pos.cpu().numpy(), rp)
+    return [rp[co.slots(c.table_np[b], int(n), c.page)] for b, n in enumerate(rn)]
+
+
+def _numbered(c, r, seen, mixed):
+    """Every held slot's token, by slot or in no order."""
+    pos = np.full(c.pos.shape, -1, np.int32)
+    for b, n in enumerate(c.lens):
+        p, at = co.slots(c.table_np[b], int(n), c.page)
+        for g in range(c.Hkv):
+            x = seen[b] - n + np.arange(n)
+            pos[p, at, g] = r.permutation(x) if mixed else x
+    return pos
+
+
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("sinks,recent,budget", [(4, 300, 256), (0, 2000, 100), (10, 5, 8), (3, 1, 1), (0, 40, 40), (700, 0, 64),
+                                                 (2 ** 31 - 1, 0, 33), (0, 2 ** 31 - 1, 33)])
+def test_evict_keeps_the_newest(sinks, recent, budget, mixed):
+    c = Cache([700, 41, 5000, 9000], page=16, Hkv=2, D=64, seed=budget)
+    r = np.random.default_rng(budget)
+    seen = c.lens + np.array([0, 3, 100, 1 << 20])
+    pos = _numbered(c, r, seen, mixed)
+    w = r.random(c.weight.shape).astype(np.float32)
+    w[r.random(w.shape) < 0.2] = np.inf            # no weight outranks them
+    left = _trim(c, w, pos, seen, budget, sinks=sinks, recent=recent)
+    for b, p in enumerate(left):
+        if len(p) == budget and recent >= 1:       # the token that was just appended, and all that are protected like it
+            for g in range(2):
+                want = np.arange(seen[b] - min(budget, recent, int(c.lens[b])), seen[b])
+                assert np.isin(want, p[:, g]).all()
+
+
+def test_evict_ages_that_count_alike():
+    """Numbers past tokens_seen, and ages at the end of what is told apart: the lower slots."""
+    c = Cache([900], page=16, Hkv=2, D=64, seed=11)
+    r = np.random.default_rng(12)
+    seen = np.array([1 << 30], np.int32)
+    age = r.choice([-5, -1, 0, 1, 255, 256, 65535, 65536, (1 << 23) - 3, (1 << 23) - 2, (1 << 23) - 1, 1 << 23, 1 << 29], c.pos.shape)
+    pos = (int(seen[0]) - 1 - age).astype(np.int32)
+    for budget in (20, 200, 500, 800):
+        _trim(c, r.random(c.weight.shape).astype(np.float32), pos, seen, budget, recent=2 ** 31 - 1)
