@@ -623,8 +623,7 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  * thd_attn_decode -- attention of one new token of each sequence over its
  * cache (which holds the token's own key and value: append first).  For
  * query head h of sequence b, over its visible slots j, kv_start[b] <= j <
- * kv_len[b] (kv_start NULL: 0, else clamped to [0, kv_len[b]]: the first slot
- * of the token's document):
+ * kv_len[b] (kv_start NULL: 0, else clamped to [0, kv_len[b]]):
  *     x_j = softmax_scale q . k_j,  y_j = softcap tanh(x_j / softcap) (softcap 0: x_j)
  *           - dist_slopes[h] (tokens_seen[b] - 1 - pos_j)
  *     lse = log sum_j exp(y_j),  p_j = exp(y_j - lse),  o = sum_j p_j v_j
@@ -635,6 +634,9 @@ THD_API int thd_cache_append(const thd_kv_cache* cache, const void* k, const voi
  *     an input.
  *   dist_slopes fp32 [Hq] or NULL.  pos NULL: a slot's token has the slot's
  *     number; tokens_seen NULL: kv_len.  Both are read with dist_slopes only.
+ *   kv_start counts slots, not tokens: it is the start of the token's document
+ *     while slots lie in their tokens' order, which is until thd_cache_evict
+ *     moves some.  See there for what to do about documents then.
  *   weight_out NULL, or: weight_out = weight_in + the sum of p_j over the kv
  *     head's query heads, for the visible slots (weight_out may be weight_in,
  *     else they do not overlap).
@@ -676,6 +678,11 @@ THD_API size_t thd_decode_workspace_size(int B, int Hq, int Hkv, int D, int64_t 
  *   weight_out, pos_out: may be weight_in, pos_in (then only moved numbers are
  *     written), else they get those of all slots below new_len.
  *   0 < budget; sinks, recent >= 0.
+ * Documents: slots leave their tokens' order, each kv head its own way, so no
+ * kv_start of thd_attn_decode tells a document's tokens from earlier ones
+ * afterwards.  Tokens that no later one may see are let go first, by a weight of
+ * NaN in their slots (and sinks 0): where kv_len[b] - kv_start[b] >= budget, all
+ * of them leave and the sequence goes on with kv_start 0.
  * Workspace: thd_evict_workspace_size.
  */
 THD_API int thd_cache_evict(const thd_kv_cache* cache, const float* weight_in, float* weight_out,

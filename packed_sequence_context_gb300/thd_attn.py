@@ -1033,7 +1033,8 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_len, *, k_exp=None, v_exp=N
     """Attention of one new token a sequence, q [B, Hq, D] bf16 (rows may be
     slices of a fused projection), over a cache as cache_append's; softcap and
     dist_slopes as attn_score_fwd's (distances by pos and tokens_seen, or by
-    slots and kv_len), kv_start int32 [B] the first visible slot.  weight: the
+    slots and kv_len), kv_start int32 [B] the first visible slot (a document's
+    start while slots lie in order: not after cache_evict).  weight: the
     tokens' attention weights are added to it (into weight_out, if given).
     Returns (o [B, Hq, D], lse [Hq, B], dev_status)."""
     import torch
@@ -1085,8 +1086,10 @@ def cache_evict(k_cache, v_cache, block_table, kv_len, weight, pos, tokens_seen,
     head: the first `sinks` and the last `recent` tokens stay (by pos and
     tokens_seen; the newest of them, where the budget holds fewer), then the
     largest weights.  Slots move in place; weight and
-    pos too, unless weight_out, pos_out take them.  Returns (new_len int32 [B],
-    dev_status)."""
+    pos too, unless weight_out, pos_out take them.  No kv_start of attn_decode
+    means a document after that: give slots that no later token may see a weight
+    of NaN and sinks 0, then they leave first, and all of them where a sequence
+    has `budget` others.  Returns (new_len int32 [B], dev_status)."""
     import torch
     w = "thd_cache_evict"
     weight_out = weight if weight_out is None else weight_out

@@ -1,5 +1,5 @@
 """Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits;
-more protected tokens than a budget holds."""
+more protected tokens than a budget holds; documents and eviction."""
 
 import numpy as np
 import pytest
@@ -156,3 +156,43 @@ def test_evict_ages_that_count_alike():
     pos = (int(seen[0]) - 1 - age).astype(np.int32)
     for budget in (20, 200, 500, 800):
         _trim(c, r.random(c.weight.shape).astype(np.float32), pos, seen, budget, recent=2 ** 31 - 1)
+
+
+# ------------------------------------------------------------------ documents in a cache that is trimmed
+@pytest.mark.parametrize("fp8", [False, True])
+def test_documents_and_eviction(fp8):
+    """What no later token may see leaves first, marked by NaN; then decoding needs no kv_start, and sees what the
+    document's own cache, trimmed alike, would show."""
+    lens, start, budget, recent = np.array([900, 300, 130, 64], np.int32), np.array([400, 0, 66, 0], np.int32), 64, 16
+    c = Cache(lens, page=16, Hkv=2, D=64, fp8=fp8, seed=13)
+    r = np.random.default_rng(14)
+    c.pos.copy_(torch.from_numpy(_numbered(c, r, lens, False)))
+    q = torch.randn(4, 8, 64, device="cuda").to(torch.bfloat16)
+    scale = 1 / 640 if fp8 else 0.125
+    w = c.weight.cpu().numpy()
+    for b in range(4):                             # by the table and the starts, as a program does it
+        p, at = co.slots(c.table_np[b], int(start[b]), 16)
+        w[p, at] = np.nan
+    host, pos = c.host(), c.pos.cpu().numpy()
+    c.weight.copy_(torch.from_numpy(w))
+    new, st = T.cache_evict(*c.args(), c.weight, c.pos, c.kv_len, budget=budget, recent=recent, **c.exps())
+    _status(st)
+    got = c.pos.cpu().numpy()
+    for b in range(4):
+        p, at = co.slots(c.table_np[b], int(new[b]), 16)
+        assert (got[p, at] >= start[b]).all()      # the document's tokens alone
+    o, lse, st = T.attn_decode(q, c.k, c.v, c.table, new, softmax_scale=scale, **c.exps())
+    _status(st)
+    # the document's slots alone, numbered from its first, in pages of one slot
+    for b in range(4):
+        n = int(lens[b] - start[b])
+        p, at = (x[start[b]:] for x in co.slots(c.table_np[b], int(lens[b]), 16))
+        doc = {k: None if x is None else x[p, at][:, None] for k, x in host.items()}
+        table = np.arange(n)[None]
+        doc, dw, dp, m = co.evict(doc, table, [n], w[p, at][:, None], pos[p, at][:, None], [int(lens[b])], budget, 0, recent)
+        ref = co.decode(q[b:b + 1].double().cpu().numpy(), doc, table, m, scale=np.float32(scale))
+        assert np.all(np.abs(o[b:b + 1].double().cpu().numpy() - ref["o"]) <= ref["tol_o"])
+        assert np.all(np.abs(lse[:, b:b + 1].double().cpu().numpy() - ref["lse"]) <= ref["tol_lse"])
+        p2, at2 = co.slots(c.table_np[b], int(new[b]), 16)
+        for g in range(2):
+            assert sorted(got[p2, at2, g]) == sorted(dp[:int(m[0]), 0, g])
