@@ -1,5 +1,6 @@
 """Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits;
-more protected tokens than a budget holds; documents and eviction."""
+more protected tokens than a budget holds; documents and eviction;
+tables much wider than the sequences."""
 
 import numpy as np
 import pytest
@@ -196,3 +197,25 @@ def test_documents_and_eviction(fp8):
         p2, at2 = co.slots(c.table_np[b], int(new[b]), 16)
         for g in range(2):
             assert sorted(got[p2, at2, g]) == sorted(dp[:int(m[0]), 0, g])
+
+
+# ------------------------------------------------------------------ tables for sequences that may come
+@pytest.mark.parametrize("slots,Hkv,lens", [(131072, 16, [2000, 0, 1, 512, 513, 2100] * 3), (1 << 20, 2, [9000, 511, 600]),
+                                            (40000, 4, [700, 3000] * 20)])
+def test_tables_far_wider_than_the_sequences(slots, Hkv, lens):
+    """Grids and shared memory go by the table's width, work by the lengths: results as with a tight table."""
+    wide = Cache(lens, page=16, Hkv=Hkv, D=64, seed=15, wide=slots // 16)
+    r = np.random.default_rng(16)
+    w, pos = r.random(wide.weight.shape).astype(np.float32), _numbered(wide, r, wide.lens, True)
+    wide.weight.copy_(torch.from_numpy(w)), wide.pos.copy_(torch.from_numpy(pos))
+    tight = wide.table[:, :-(-max(lens) // 16)].contiguous()
+    q = torch.randn(len(lens), 2 * Hkv, 64, device="cuda").to(torch.bfloat16)
+    outs = []
+    for table in (tight, wide.table):
+        wo = torch.full_like(wide.weight, -3.0)
+        o, lse, st = T.attn_decode(q, wide.k, wide.v, table, wide.kv_len, weight=wide.weight, weight_out=wo)
+        _status(st)
+        outs.append((o, lse, wo))
+    # (the cut goes by the lengths, and so does the order of sums)
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    _trim(wide, w, pos, wide.lens, 512, sinks=2, recent=100)
