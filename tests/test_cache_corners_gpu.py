@@ -1,6 +1,6 @@
 """Corners of the paged cache: bad pages of sequences that nothing leaves; values of zeros in 8 bits;
 more protected tokens than a budget holds; documents and eviction;
-tables much wider than the sequences."""
+tables much wider than the sequences; weights that lie close together."""
 
 import numpy as np
 import pytest
@@ -219,3 +219,22 @@ def test_tables_far_wider_than_the_sequences(slots, Hkv, lens):
     # (the cut goes by the lengths, and so does the order of sums)
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     _trim(wide, w, pos, wide.lens, 512, sinks=2, recent=100)
+
+
+# ------------------------------------------------------------------ weights that lie close together
+@pytest.mark.parametrize("close", [2, 7, 8, 127, 128, 129, 130, 500, 1024, 1025, 3000])
+def test_evict_close_weights(close):
+    """Around the threshold `close` weights with the same upper half, half of them kept; some equal, spread over the slots."""
+    lens, budget = [9000, 5200], 2048
+    c = Cache(lens, page=16, Hkv=2, D=64, seed=close)
+    r = np.random.default_rng(close)
+    w = np.zeros(c.weight.shape, np.float32)
+    low = np.float32(1.0).view(np.int32)
+    for b, n in enumerate(lens):
+        p, at = co.slots(c.table_np[b], n, 16)
+        for g in range(2):
+            near = (low + r.integers(0, 1 << 16, close) // (1 << (4 * g)) * (1 << (4 * g))).astype(np.int32).view(np.float32)
+            above = budget - close // 2 if close // 2 < budget else 0
+            x = np.concatenate([r.uniform(2, 60, above), near, r.uniform(0.01, 0.9, n - above - close)])
+            w[p, at, g] = r.permutation(x)
+    _trim(c, w, _numbered(c, r, c.lens, True), c.lens, budget)
