@@ -575,7 +575,8 @@ THD_API int thd_dropout_add(const void* x, const void* residual, void* out, int6
  *   num_pages < 2^31; max_pages * page_size <= 2^30; Hq / Hkv <= 512.
  *   A page may stand in several sequences' rows of the table while it is only
  *     read; what a call writes (append, evict, weights) lies in pages of one
- *     sequence, once.
+ *     sequence, once.  Strides of 0 (one number for all heads, say) are for
+ *     arrays that are only read, and for weight and pos of append.
  * The struct is read before a call returns; its pointers are device pointers.
  *
  * Device status of these calls: STICKY.  *dev_status is only ever raised, to

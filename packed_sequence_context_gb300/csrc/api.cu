@@ -982,6 +982,14 @@ static int check_cache(const thd_kv_cache* c, CacheView* v) {
   return THD_OK;
 }
 
+// Whether an array that a call writes has a place of its own for each slot and head.
+static bool apart(const thd_kv_cache* c, const int64_t (&s)[3]) {
+  return (c->num_pages == 1 || s[0] > 0) && (c->page_size == 1 || s[1] > 0) && (c->Hkv == 1 || s[2] > 0);
+}
+static bool rows_apart(const thd_kv_cache* c) {
+  return apart(c, c->kv_stride) && (!c->k_exp || apart(c, c->exp_stride));
+}
+
 int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                      int64_t T, const int32_t* cu_seqlens, float* weight, int32_t* pos, const int32_t* tokens_seen,
                      int32_t* dev_status, thd_stream_t stream) {
@@ -996,6 +1004,7 @@ int thd_cache_append(const thd_kv_cache* cache, const void* k, const void* v, in
       !aligned(pos, 4) || !aligned(tokens_seen, 4) || !aligned(dev_status, 4))
     return THD_ERR_INVALID_ARG;
   if (T > 1 && (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)) return THD_ERR_INVALID_ARG;
+  if (!rows_apart(cache)) return THD_ERR_INVALID_ARG;  // (weight and pos get one number for all heads: those may share it)
   p.in[0] = static_cast<const uint16_t*>(k);
   p.in[1] = static_cast<const uint16_t*>(v);
   p.in_stride[0] = k_stride;
@@ -1060,6 +1069,7 @@ int thd_attn_decode(const thd_kv_cache* cache, const void* q, int64_t q_stride, 
   const DecodeWs w = decode_ws(B, Hq, Hkv, D, p.c.capacity, weight_out != nullptr);
   rc = check_ws(workspace, workspace_bytes, w.total);
   if (rc != THD_OK) return rc;
+  if (weight_out && !apart(cache, cache->weight_stride)) return THD_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_stride;
   p.o = static_cast<uint16_t*>(o);
@@ -1114,6 +1124,8 @@ int thd_cache_evict(const thd_kv_cache* cache, const float* weight_in, float* we
     return THD_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, thd_evict_workspace_size(cache->B, cache->Hkv, p.c.capacity, budget));
   if (rc != THD_OK) return rc;
+  if (!rows_apart(cache) || !apart(cache, cache->weight_stride) || !apart(cache, cache->pos_stride))
+    return THD_ERR_INVALID_ARG;
   p.weight_in = weight_in;
   p.weight_out = weight_out;
   p.weight_at = slot_strides(cache->weight_stride, 1);
