@@ -195,10 +195,13 @@ cudaError_t launch_append(const AppendParams& a, cudaStream_t st) {
 // (behind) and targets (in front) that never meet, and nothing to wait for
 // between them.
 //
-// Bound by latency, but for the moves: 4 sequences of 32,768 slots and 8 kv heads cut to
-// 4096 take 56 us, 18 of them the moves at the rate of a plain copy, 7 the keys, 26
-// the selection (four rounds over the cluster of about 4 us each), 5 the numbers
-// that stay when they go to other arrays; 32 sequences of 2000 to 2112 slots 20 us.
+// Bound by latency, but for the moves.  By the blocks' clocks (at 1.9 GHz), 4
+// sequences of 32,768 slots and 8 kv heads cut to 4096 in clusters of 8: keys 6.7 us,
+// the two digits 5.3 and 4.9 (a walk over the keys and two barriers of the cluster
+// each), candidates 4.0, counts 2.6, lists of moves 2.9, the barrier behind
+// them 1.6, moves at the rate of a plain copy 17.4, the numbers that stay 2.3: 48
+// of 49 us.  32 of 2000 to 2112 slots cut to 2048, a block an item: 2.7, 2.7 and 2.1,
+// 1.8, 1.6, 1.7, 0.7, 1.8, 1.5: 16.5 of 19 us, walks over four keys a thread each.
 namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 512;
@@ -544,9 +547,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
 
 cudaError_t launch_evict(EvictParams p, cudaStream_t st) {
   const int64_t items = (int64_t)p.c.B * p.c.Hkv;
-  // blocks of an item: as many as leave two an SM (one wave), while each still has
-  // 1024 slots, and as many as it takes to hold the keys (64 items of 25,331
-  // slots: 4 blocks each 49 us, 8 in two waves 63)
+  // blocks of an item: as many as leave two an SM, while each still has 1024 slots
+  // (64 items of 25,331 slots: 4 blocks each 49 us, 8 in two waves 63), and as many
+  // as it takes to hold the keys.  Both go by the table's width, the lengths being on
+  // the device: from about 28,000 slots a block on the keys' shared memory leaves
+  // one block an SM, and wide tables of short sequences take several waves (32 of
+  // 2112 slots, 8 kv heads: a table for 2112 slots 19 us, for 131,072 58, for
+  // 1,048,576 111)
   int share = 1;
   while (share < 8 && ((items * share <= num_sms() && p.c.capacity / share > 1024) || p.c.capacity / share > kEvictMaxHeld))
     share *= 2;

@@ -26,11 +26,14 @@
 // item's first copies are under way.
 //
 // Measured on one GB300, heads of 128, of the rate of a plain copy: bf16, 524,288
-// slots of 8 kv heads 303 us (104%), 38 sequences of 8192 with 8, 16 or 32 heads
-// a kv head 186, 186, 190 us (101 to 99%); e4m3, 1,048,576 slots 309 us (103%),
-// 38 sequences with 8, 16, 32 heads 104, 115, 171 us (91, 83, 56%: from 16
+// slots of 8 kv heads 293 us (108%), 38 sequences of 8192 with 8, 16 or 32 heads
+// a kv head 178, 180, 184 us (105, 104, 102%); e4m3, 1,048,576 slots 308 us (103%),
+// 38 sequences with 8, 16, 32 heads 104, 115, 172 us (91, 82, 55%: from 16
 // heads on the conversions, softmax and products of a warp's tile take longer than
-// its bytes).  A call begins and ends in about 10 us (lengths, table and first
+// its bytes, and with 32 two warps a scheduler hide too little of that: it issues
+// in 29% of the cycles, the tensor pipe works in 27%).  Items of one or two units
+// cost a block what long ones do at their beginning and end: 4096 sequences of 16
+// slots 281 us (14%), 1024 of 64 86 (46%), 256 of 128 36 (54%).  A call begins and ends in about 10 us (lengths, table and first
 // rows are three loads one after the other; the join 2.5 us).
 #include <cfloat>
 
